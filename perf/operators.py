@@ -182,19 +182,15 @@ def _prepare_verify(c, g):
     cu = torch.zeros(R + 1, dtype=torch.int32, device=DEV)
     cu[1:] = torch.cumsum(drafts + 1, 0)
     rows = int(cu[-1])
-    nd = rows - R
     target = torch.randn((rows, V), generator=g, device=DEV) * 3.0
-    # the draft model's logits: the target's with some noise
-    is_draft = torch.ones(rows, dtype=torch.bool, device=DEV)
-    is_draft[(cu[1:] - 1).long()] = False
-    draft = target[is_draft]
-    draft = torch.softmax(draft + torch.randn((nd, V), generator=g, device=DEV), 1)
+    # the draft model's logits: the target's with some noise (a draft has the target's row
+    # that it is checked by; the row after a request's last draft has none, and is not read)
+    draft = torch.softmax(target + torch.randn((rows, V), generator=g, device=DEV), 1)
     target = torch.softmax(target, 1)
     # a token from the draft's distribution: the smallest of exponential clocks
-    clock = torch.empty((nd, V), device=DEV).exponential_(generator=g)
-    tok = (draft / clock).argmax(1).to(torch.int32) if nd else torch.zeros(0, dtype=torch.int32, device=DEV)
+    tok = (draft / torch.empty((rows, V), device=DEV).exponential_(generator=g)).argmax(1).to(torch.int32)
     return dict(target=target, draft=draft if c["probs"] else None, tok=tok, cu=cu,
-                u_accept=torch.rand(nd, generator=g, device=DEV), u_sample=torch.rand(R, generator=g, device=DEV),
+                u_accept=torch.rand(rows, generator=g, device=DEV), u_sample=torch.rand(R, generator=g, device=DEV),
                 ctx=_ints(0, 65536, R, g))
 
 
@@ -340,21 +336,17 @@ def _plain_verify(s):
     drafts = cu[1:] - cu[:-1] - 1
     i = torch.arange(n + 1, device=dev)[None, :]
     real = i < drafts[:, None]
-    d = torch.where(real, (cu[:-1] - torch.arange(R, device=dev))[:, None] + i, 0)
-    nothing = s["tok"].numel() == 0
-    tok = torch.zeros_like(d) if nothing else s["tok"].long()[d]
-    p = s["target"].flatten()[torch.where(real, cu[:-1, None] + i, 0) * V + tok].double()
-    q = torch.ones_like(p) if s["draft"] is None or nothing else s["draft"].flatten()[d * V + tok].double()
-    u = torch.zeros_like(p) if nothing else s["u_accept"][d].double()
-    a = torch.cumprod(((u * q < p) & real).long(), 1).sum(1)
+    row = torch.where(real, cu[:-1, None] + i, 0)
+    tok = s["tok"].long()[row]
+    p = s["target"].flatten()[row * V + tok].double()
+    q = torch.ones_like(p) if s["draft"] is None else s["draft"].flatten()[row * V + tok].double()
+    a = torch.cumprod(((s["u_accept"][row].double() * q < p) & real).long(), 1).sum(1)
     w = s["target"][cu[:-1] + a].double()
     bad = (a < drafts)[:, None]  # a rejected draft: its share of the probability is taken off
-    at = d.gather(1, a[:, None])[:, 0]
-    x = tok.gather(1, a[:, None])
-    if s["draft"] is None or nothing:
-        less = torch.where(bad, torch.zeros_like(w).scatter_(1, x, 2.0), 0.0)
+    if s["draft"] is None:
+        less = torch.where(bad, torch.zeros_like(w).scatter_(1, tok.gather(1, a[:, None]), 2.0), 0.0)
     else:
-        less = torch.where(bad, s["draft"][at].double(), 0.0)
+        less = torch.where(bad, s["draft"][cu[:-1] + a].double(), 0.0)
     rest = (w - less).clamp(min=0)
     w = torch.where(rest.sum(1, keepdim=True) > 0, rest, w)
     cum = torch.cumsum(w, 1)
@@ -499,15 +491,15 @@ def _exact_verify(s):
     tokens = np.full((c["req"], c["draft"] + 1), -1, dtype=np.int32)
     num = []
     for r in range(c["req"]):
-        a, n, at = 0, cu[r + 1] - cu[r] - 1, cu[r] - r
+        a, n, at = 0, cu[r + 1] - cu[r] - 1, cu[r]
         while a < n:
             x = tok[at + a]
             q = 1.0 if s["draft"] is None else float(s["draft"][at + a, x])
-            if not ua[at + a] * q < float(s["target"][cu[r] + a, x]):
+            if not ua[at + a] * q < float(s["target"][at + a, x]):
                 break
             tokens[r, a] = x
             a += 1
-        p = s["target"][cu[r] + a].cpu().numpy().astype(np.float64)
+        p = s["target"][at + a].cpu().numpy().astype(np.float64)
         w = p
         if a < n:
             w = p.copy()
