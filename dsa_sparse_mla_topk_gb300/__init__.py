@@ -11,26 +11,28 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
 __all__ = ["DsaError", "load_library", "topk_select", "sparse_mla_fwd", "combine", "sparse_mla_topk",
            "topk_sparse_mla_fwd", "two_kernel_path_supported", "sparse_mla_topk_fused", "fused_path_supported",
            "kv_write",
-           "PrefixCache",
+           "PrefixCache", "BatchLayout", "batch_layout", "qk_norm_rope", "chunk_mla_fwd", "chunk_mla", "verify_draft",
            "kv_tile_count", "kv_tile_size", "pick_num_splits", "status_string", "EXPORTED_SYMBOLS",
-           "DEV_BAD_QPOS", "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_TIMEOUT"]
+           "DEV_BAD_QPOS", "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_TIMEOUT", "DEV_NO_PAGES"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdsa.so")
 
-DEV_BAD_QPOS, DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_TIMEOUT = 1, 2, 4, 8
+DEV_BAD_QPOS, DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_NO_PAGES = 1, 2, 4, 8, 16
 
 # Every symbol include/dsa.h declares.
 EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_topk_workspace_size",
                     "dsa_sparse_mla_fwd", "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_fwd_noalloc",
                     "dsa_sparse_mla_topk_fwd", "dsa_sparse_mla_topk_max_k", "dsa_topk_sparse_mla_fwd",
-                    "dsa_combine", "dsa_kv_write", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
+                    "dsa_combine", "dsa_kv_write", "dsa_batch_layout", "dsa_qk_norm_rope", "dsa_chunk_mla_fwd",
+                    "dsa_verify_draft", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
                     "dsa_prefix_cache_acquire", "dsa_prefix_cache_release", "dsa_prefix_cache_stats",
                     "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits")
 
@@ -85,6 +87,17 @@ def load_library(path: str | None = None):
         lib.dsa_combine.restype = i32
         lib.dsa_kv_write.argtypes = [vp, i32, i32, vp, vp, vp, i32, i32, i32, i64, vp, vp, vp, vp]
         lib.dsa_kv_write.restype = i32
+        lib.dsa_batch_layout.argtypes = [vp, vp, vp, i32, vp, i32, vp, i32, vp, i32, i64, i32, vp, vp, vp, vp, vp, vp,
+                                         vp, vp, vp]
+        lib.dsa_batch_layout.restype = i32
+        lib.dsa_qk_norm_rope.argtypes = [vp, i64, i64, i32, vp, i32, vp, vp, i64, i64, i32, vp, i32, vp, i32, i32, i32,
+                                         i32, vp, vp, i32, f32, i32, vp, vp, vp, i64, vp, vp]
+        lib.dsa_qk_norm_rope.restype = i32
+        lib.dsa_chunk_mla_fwd.argtypes = [vp, vp, vp, i64, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, f32, i32, vp,
+                                          vp, vp, vp, vp, vp]
+        lib.dsa_chunk_mla_fwd.restype = i32
+        lib.dsa_verify_draft.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]
+        lib.dsa_verify_draft.restype = i32
         lib.dsa_prefix_cache_create.argtypes = [i32, i32]
         lib.dsa_prefix_cache_create.restype = vp
         lib.dsa_prefix_cache_destroy.argtypes = [vp]
@@ -458,3 +471,294 @@ def sparse_mla_topk(q, kv, kv_scale, block_table, q_req, q_pos, scores, k: int, 
                             dev_status=dev_status, stream=stream)
     out, lse = combine(op, lp, out=b.get("out"), lse=b.get("lse"), stream=stream)
     return out, lse, idx
+
+
+# ---- the rest of a serving step --------------------------------------------------
+
+
+def _check_all(dev: torch.device, *named):
+    """(tensor or None, name, dtype, ndim) each: as _check, and on ``dev``."""
+    for t, name, dtype, ndim in named:
+        if t is not None:
+            _check(t, name, dtype, ndim)
+            if t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _check_shape(t, name: str, shape: tuple):
+    if t is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+
+
+def _call_on(dev: torch.device, fn: str, stream, *args):
+    """_call with the tensors' device current (its current stream when none is given)."""
+    if dev.index == torch.cuda.current_device():
+        _call(fn, *args, _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            _call(fn, *args, _stream(stream))
+
+
+def _status_arg(dev_status, dev):
+    if dev_status is not None:
+        _check_all(dev, (dev_status, "dev_status", torch.int32, None))
+        if dev_status.numel() < 1:
+            raise ValueError("dev_status needs one element")
+    return _p(dev_status)
+
+
+def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether the spans of memory from the first to the last element overlap."""
+    def span(t):
+        n = 1 + sum((s - 1) * st for s, st in zip(t.shape, t.stride()))
+        return t.data_ptr(), t.data_ptr() + n * t.element_size()
+    if a.numel() == 0 or b.numel() == 0:
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
+class BatchLayout(NamedTuple):
+    """What batch_layout writes (int32 tensors): token ranges cu_q [num_req +
+    1]; request, position and cache slot of every token, -1 padded [capacity];
+    the requests' lengths and pages after the step [num_req]; the count of
+    free-list pages taken [1]."""
+    cu_q: torch.Tensor
+    q_req: torch.Tensor
+    q_pos: torch.Tensor
+    slot: torch.Tensor
+    ctx_len: torch.Tensor
+    pages_held: torch.Tensor
+    free_used: torch.Tensor
+
+
+def batch_layout(ctx_len: torch.Tensor, new_len: torch.Tensor, pages_held: torch.Tensor, block_table: torch.Tensor,
+                 free_pages: torch.Tensor, free_used: torch.Tensor, *, page_size: int, num_pages: int, capacity: int,
+                 out: BatchLayout | None = None, dev_status=None, stream=None) -> BatchLayout:
+    """A step's token ranges, slot map and grown block tables from the
+    requests' lengths (dsa_batch_layout): ``block_table`` gets the new pages in
+    place, everything else is returned.  ``out`` (a BatchLayout of
+    preallocated tensors, not the inputs) is written when given."""
+    dev = ctx_len.device
+    R = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
+    _check_all(dev, (ctx_len, "ctx_len", torch.int32, 1), (new_len, "new_len", torch.int32, 1),
+               (pages_held, "pages_held", torch.int32, 1), (block_table, "block_table", torch.int32, 2),
+               (free_pages, "free_pages", torch.int32, 1), (free_used, "free_used", torch.int32, 1))
+    if new_len.shape[0] != R or pages_held.shape[0] != R or block_table.shape[0] != R or free_used.shape[0] != 1:
+        raise ValueError("inconsistent shapes")
+    if capacity < 0:
+        raise ValueError("capacity must not be negative")
+    if out is None:
+        # one allocation: the token arrays first (each a multiple of 16 bytes apart)
+        cap = (capacity + 3) // 4 * 4
+        buf = torch.empty(3 * cap + 3 * R + 2, dtype=torch.int32, device=dev)
+        t = 3 * cap
+        out = BatchLayout(buf[t:t + R + 1], buf[:capacity], buf[cap:cap + capacity], buf[2 * cap:2 * cap + capacity],
+                          buf[t + R + 1:t + 2 * R + 1], buf[t + 2 * R + 1:t + 3 * R + 1], buf[t + 3 * R + 1:])
+    else:
+        for x, name, n in zip(out, BatchLayout._fields, (R + 1, capacity, capacity, capacity, R, R, 1)):
+            _check_all(dev, (x, "out." + name, torch.int32, 1))
+            _check_shape(x, "out." + name, (n,))
+    _call_on(dev, "dsa_batch_layout", stream, _p(ctx_len), _p(new_len), _p(pages_held), R, _p(block_table),
+             block_table.shape[1], _p(free_pages), free_pages.shape[0], _p(free_used), page_size, num_pages, capacity,
+             _p(out.cu_q), _p(out.q_req), _p(out.q_pos), _p(out.slot), _p(out.ctx_len), _p(out.pages_held),
+             _p(out.free_used), _status_arg(dev_status, dev))
+    return out
+
+
+_ROW_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _rows(x, name: str, dev, dtype, d: int):
+    """Checks rows [tokens, heads, d] whose last dimension is contiguous."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if not x.is_cuda or x.device != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+    if x.dim() != 3 or x.shape[2] != d or (d > 1 and x.stride(2) != 1):
+        raise ValueError(f"{name} must be [tokens, heads, {d}] with a contiguous last dimension")
+
+
+def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor | None,
+                 cos_sin: torch.Tensor | None, *, d_rope: int, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, eps: float = 1e-6, interleaved: bool = True,
+                 q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                 slot: torch.Tensor | None = None, kv: torch.Tensor | None = None,
+                 kv_scale: torch.Tensor | None = None, dev_status=None, stream=None):
+    """Norm of each head's leading ``len(weight)`` values and rotation of its
+    last ``d_rope`` values for query and key rows [tokens, heads, d] (bf16 or
+    fp16, any token and head strides that are multiples of 8), in one pass
+    (dsa_qk_norm_rope).  With ``slot`` / ``kv`` / ``kv_scale`` the single key
+    head goes into the FP8 cache.  Returns (q_out, k_out); a side that is
+    None, or keys that only go into the cache, give None.  Tokens with pos =
+    -1 are left as they were."""
+    some = q if q is not None else k
+    if not isinstance(some, torch.Tensor) or some.dim() != 3:
+        raise ValueError("q or k must be a [tokens, heads, d] tensor")
+    dev, dtype = some.device, some.dtype
+    n, d = some.shape[0], some.shape[2]
+    if dtype not in _ROW_DTYPES:
+        raise TypeError(f"rows must be bfloat16 or float16, got {dtype}")
+    for x, name in ((q, "q"), (k, "k")):
+        if x is not None:
+            _rows(x, name, dev, dtype, d)
+            if x.shape[0] != n:
+                raise ValueError("q and k must have the same number of tokens")
+    cache = slot is not None or kv is not None or kv_scale is not None
+    if cache and (slot is None or kv is None or kv_scale is None or k is None):
+        raise ValueError("the cache write needs k, slot, kv and kv_scale")
+    _check_all(dev, (pos, "pos", torch.int32, 1), (cos_sin, "cos_sin", torch.float32, 2),
+               (q_weight, "q_weight", torch.float32, 1), (k_weight, "k_weight", torch.float32, 1),
+               (slot, "slot", torch.int32, 1), (kv, "kv", torch.uint8, 2), (kv_scale, "kv_scale", torch.float32, 1),
+               (q_out, "q_out", dtype, 3), (k_out, "k_out", dtype, 3))
+    if d_rope and (pos is None or cos_sin is None or cos_sin.shape[1] != d_rope):
+        raise ValueError("a rotation needs pos and cos_sin [max_pos, d_rope]")
+    if pos is not None and pos.shape[0] != n or cache and slot.shape[0] != n:
+        raise ValueError("inconsistent shapes")
+    if cache and (kv.shape[1] != d or kv_scale.shape[0] != kv.shape[0]):
+        raise ValueError("kv must be [slots, d] and kv_scale [slots]")
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=dtype, device=dev)
+    if k is not None and k_out is None and not cache:
+        k_out = torch.empty(k.shape, dtype=dtype, device=dev)
+    for o, name, own in ((q_out, "q_out", q), (k_out, "k_out", k)):
+        if o is None:
+            continue
+        if own is None:
+            raise ValueError(f"{name} without its input")
+        _check_shape(o, name, tuple(own.shape))
+        for x in (q, k):
+            if x is not None and _overlap(o, x) and not (x is own and o.data_ptr() == x.data_ptr() and x.is_contiguous()):
+                raise ValueError(f"{name} overlaps an input (in place needs its own, contiguous)")
+    qs, ks = (x.stride() if x is not None and x.numel() else (0, 0, 1) for x in (q, k))
+    _call_on(dev, "dsa_qk_norm_rope", stream, _p(q), qs[0], qs[1], 0 if q is None else q.shape[1], _p(q_weight),
+             0 if q_weight is None else q_weight.shape[0], _p(q_out), _p(k), ks[0], ks[1],
+             0 if k is None else k.shape[1], _p(k_weight), 0 if k_weight is None else k_weight.shape[0], _p(k_out), n, d,
+             d_rope, _ROW_DTYPES[dtype], _p(pos), _p(cos_sin), 0 if cos_sin is None else cos_sin.shape[0], float(eps),
+             1 if interleaved else 0, _p(slot), _p(kv), _p(kv_scale), kv.shape[0] if cache else 0,
+             _status_arg(dev_status, dev))
+    return q_out, k_out
+
+
+def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_rope: int, page_size: int,
+                  softmax_scale: float, num_splits: int = 1, out=None, lse=None, o_part=None, lse_part=None,
+                  dev_status=None, stream=None):
+    """Attention of each token to all positions 0..q_pos of its request
+    (dsa_chunk_mla_fwd).  num_splits == 1: returns (out bf16, lse fp32).
+    num_splits > 1: returns (o_part fp32 [S, ...], lse_part fp32 [S, ...])."""
+    dev = q.device
+    _check_all(dev, (q, "q", torch.bfloat16, 3), (kv, "kv", torch.uint8, 2), (kv_scale, "kv_scale", torch.float32, 1),
+               (block_table, "block_table", torch.int32, 2), (q_req, "q_req", torch.int32, 1),
+               (q_pos, "q_pos", torch.int32, 1), (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2),
+               (o_part, "o_part", torch.float32, 4), (lse_part, "lse_part", torch.float32, 3))
+    num_q, H, dqk = q.shape
+    if dqk != d_latent + d_rope or kv.shape[1] != dqk or page_size <= 0 or kv.shape[0] % page_size:
+        raise ValueError("q / kv row sizes do not match d_latent + d_rope, or kv is not whole pages")
+    if q_req.shape[0] != num_q or q_pos.shape[0] != num_q or kv_scale.shape[0] != kv.shape[0]:
+        raise ValueError("inconsistent shapes")
+    if num_splits == 1:
+        if out is None:
+            out = torch.empty((num_q, H, d_latent), dtype=torch.bfloat16, device=dev)
+        if lse is None:
+            lse = torch.empty((num_q, H), dtype=torch.float32, device=dev)
+        _check_shape(out, "out", (num_q, H, d_latent))
+        _check_shape(lse, "lse", (num_q, H))
+        ptrs = (_p(out), _p(lse), None, None)
+    else:
+        if o_part is None:
+            o_part = torch.empty((num_splits, num_q, H, d_latent), dtype=torch.float32, device=dev)
+        if lse_part is None:
+            lse_part = torch.empty((num_splits, num_q, H), dtype=torch.float32, device=dev)
+        _check_shape(o_part, "o_part", (num_splits, num_q, H, d_latent))
+        _check_shape(lse_part, "lse_part", (num_splits, num_q, H))
+        ptrs = (None, None, _p(o_part), _p(lse_part))
+    _call_on(dev, "dsa_chunk_mla_fwd", stream, _p(q), _p(kv), _p(kv_scale), kv.shape[0] // page_size, _p(block_table),
+             block_table.shape[0], block_table.shape[1], _p(q_req), _p(q_pos), num_q, H, d_latent, d_rope, page_size,
+             float(softmax_scale), num_splits, *ptrs, _status_arg(dev_status, dev))
+    return (out, lse) if num_splits == 1 else (o_part, lse_part)
+
+
+def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_rope: int, page_size: int,
+              softmax_scale: float, max_ctx: int | None = None, num_splits: int | None = None,
+              buffers: dict | None = None, dev_status=None, stream=None):
+    """The whole pass over every visible position: chunk_mla_fwd, then combine
+    when split.  ``max_ctx`` (default: the block table's width) is about the
+    longest context, from which the number of KV splits is picked when
+    ``num_splits`` is None; the result is right for any value.  ``buffers``
+    (optional) holds preallocated out / lse / o_part / lse_part tensors.
+    Returns (out, lse)."""
+    b = buffers or {}
+    num_q, H, _ = q.shape
+    if num_splits is None:
+        if max_ctx is None:
+            max_ctx = block_table.shape[1] * page_size
+        num_splits = pick_num_splits(num_q, H, d_latent, d_rope, max(1, max_ctx))
+    r = chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
+                      page_size=page_size, softmax_scale=softmax_scale, num_splits=num_splits,
+                      out=b.get("out") if num_splits == 1 else None, lse=b.get("lse") if num_splits == 1 else None,
+                      o_part=b.get("o_part"), lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)
+    if num_splits == 1 or num_q == 0:
+        return r if num_splits == 1 else (torch.empty((0, H, d_latent), dtype=torch.bfloat16, device=q.device),
+                                          torch.empty((0, H), dtype=torch.float32, device=q.device))
+    out, lse = b.get("out"), b.get("lse")
+    dev = q.device
+    if out is None:
+        out = torch.empty((num_q, H, d_latent), dtype=torch.bfloat16, device=dev)
+    if lse is None:
+        lse = torch.empty((num_q, H), dtype=torch.float32, device=dev)
+    _check_all(dev, (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2))
+    _check_shape(out, "out", (num_q, H, d_latent))
+    _check_shape(lse, "lse", (num_q, H))
+    _call_on(dev, "dsa_combine", stream, _p(r[0]), _p(r[1]), num_splits, num_q, H, d_latent, _p(out), _p(lse))
+    return out, lse
+
+
+def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows: torch.Tensor,
+                 u_accept: torch.Tensor, u_sample: torch.Tensor, *, draft_probs: torch.Tensor | None = None,
+                 ctx_len: torch.Tensor | None = None, max_out: int, tokens: torch.Tensor | None = None,
+                 num_out: torch.Tensor | None = None, ctx_out: torch.Tensor | None = None, dev_status=None, stream=None):
+    """Verification of drafted tokens against the target's probabilities from
+    given random numbers (dsa_verify_draft).  Returns (tokens int32 [num_req,
+    max_out], -1 padded; num_out int32 [num_req]; ctx_out = ctx_len + num_out,
+    or None without ctx_len)."""
+    dev = target_probs.device
+    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
+            raise TypeError(f"{name} must be a float32 tensor")
+        if not t.is_cuda or t.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must be [rows, vocab] with contiguous rows")
+    rows, vocab = target_probs.shape
+    _check_all(dev, (draft_tokens, "draft_tokens", torch.int32, 1), (cu_rows, "cu_rows", torch.int32, 1),
+               (u_accept, "u_accept", torch.float32, 1), (u_sample, "u_sample", torch.float32, 1),
+               (ctx_len, "ctx_len", torch.int32, 1), (tokens, "tokens", torch.int32, 2),
+               (num_out, "num_out", torch.int32, 1), (ctx_out, "ctx_out", torch.int32, 1))
+    R = u_sample.shape[0]
+    if cu_rows.shape[0] != R + 1 or draft_tokens.shape[0] != rows or u_accept.shape[0] != rows or \
+            (draft_probs is not None and tuple(draft_probs.shape) != (rows, vocab)):
+        raise ValueError("inconsistent shapes")
+    if max_out < 1:
+        raise ValueError("max_out must be positive")
+    if tokens is None:
+        tokens = torch.empty((R, max_out), dtype=torch.int32, device=dev)
+    if num_out is None:
+        num_out = torch.empty(R, dtype=torch.int32, device=dev)
+    if ctx_len is None:
+        if ctx_out is not None:
+            raise ValueError("ctx_out needs ctx_len")
+    elif ctx_out is None:
+        ctx_out = torch.empty(R, dtype=torch.int32, device=dev)
+    _check_shape(tokens, "tokens", (R, max_out))
+    for t, name in ((num_out, "num_out"), (ctx_len, "ctx_len"), (ctx_out, "ctx_out")):
+        _check_shape(t, name, (R,))
+    ld = target_probs.stride(0) if rows > 1 else vocab
+    ldd = draft_probs.stride(0) if draft_probs is not None and rows > 1 else vocab
+    _call_on(dev, "dsa_verify_draft", stream, _p(target_probs), ld, rows, vocab, _p(draft_probs), ldd, _p(draft_tokens),
+             _p(u_accept), _p(u_sample), _p(cu_rows), R, max_out, _p(ctx_len), _p(tokens), _p(num_out), _p(ctx_out),
+             _status_arg(dev_status, dev))
+    return tokens, num_out, ctx_out

@@ -40,7 +40,7 @@ const char* dsa_status_string(int32_t status) {
   switch (status) {
     case DSA_OK: return "ok";
     case DSA_ERR_INVALID_ARG: return "invalid argument";
-    case DSA_ERR_UNSUPPORTED_SHAPE: return "unsupported (heads, d_latent, d_rope)";
+    case DSA_ERR_UNSUPPORTED_SHAPE: return "unsupported (heads, d_latent, d_rope) or size";
     case DSA_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case DSA_ERR_CUDA: return "CUDA error";
     case DSA_ERR_OUT_OF_PAGES: return "page pool exhausted";
@@ -48,7 +48,7 @@ const char* dsa_status_string(int32_t status) {
   }
 }
 
-int32_t dsa_version(void) { return 100; }
+int32_t dsa_version(void) { return 200; }
 
 int32_t dsa_kv_tile_count(int32_t width, int32_t tile) {
   if (width < 0 || tile <= 0) return -1;
@@ -277,4 +277,163 @@ dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const int32_t
   if (!aligned16(rows) || !aligned16(kv)) return DSA_ERR_INVALID_ARG;
   return from_cuda(dsa::launch_kv_write(rows, n, d_qk, req, pos, block_table, num_req, bt_stride, page_size,
                                         num_pages, kv, kv_scale, dev_status, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Whether [a, a + na) and [b, b + nb) bytes overlap.
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && na > 0 && nb > 0 && x < y + (uint64_t)nb && y < x + (uint64_t)na;
+}
+
+// One side of dsa_qk_norm_rope.
+dsa_status check_norm_side(const void* x, int64_t ts, int64_t hs, int32_t heads, const float* w, int32_t norm_dim,
+                           const void* out, bool out_needed, int32_t num_tokens, int32_t d) {
+  if (heads < 0 || norm_dim < 0 || norm_dim > d || norm_dim % 8 != 0) return DSA_ERR_INVALID_ARG;
+  if (heads == 0 || num_tokens == 0) return DSA_OK;
+  if (!x || !aligned16(x) || ts % 8 != 0 || hs % 8 != 0 || ts < 0 || hs < 0) return DSA_ERR_INVALID_ARG;
+  if (norm_dim > 0 && (!w || !aligned16(w))) return DSA_ERR_INVALID_ARG;
+  if ((!out && out_needed) || !aligned16(out)) return DSA_ERR_INVALID_ARG;
+  if (out == x && ((heads > 1 && hs != d) || (num_tokens > 1 && ts != (int64_t)heads * d))) return DSA_ERR_INVALID_ARG;
+  return DSA_OK;
+}
+
+}  // namespace
+
+dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_len, const int32_t* pages_held, int32_t num_req,
+                            int32_t* block_table, int32_t bt_stride, const int32_t* free_pages, int32_t num_free,
+                            const int32_t* free_used, int32_t page_size, int64_t num_pages, int32_t capacity,
+                            int32_t* cu_q, int32_t* q_req, int32_t* q_pos, int32_t* slot, int32_t* ctx_out,
+                            int32_t* held_out, int32_t* free_used_out, int32_t* dev_status, void* stream) {
+  if (num_req <= 0 || bt_stride <= 0 || num_free < 0 || page_size <= 0 || num_pages <= 0 || capacity < 0)
+    return DSA_ERR_INVALID_ARG;
+  if (num_req > dsa::batch_layout_max_requests() || num_pages > (int64_t)INT32_MAX / page_size)
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!ctx_len || !new_len || !pages_held || !block_table || (num_free > 0 && !free_pages) || !free_used)
+    return DSA_ERR_INVALID_ARG;
+  if (!cu_q || (capacity > 0 && (!q_req || !q_pos || !slot)) || !ctx_out || !held_out || !free_used_out)
+    return DSA_ERR_INVALID_ARG;
+  // every CTA reads the inputs while one writes the new lengths
+  const int64_t nr = 4 * (int64_t)num_req;
+  const void* in[4] = {ctx_len, new_len, pages_held, free_used};
+  const int64_t in_bytes[4] = {nr, nr, nr, 4};
+  const void* out[7] = {cu_q, ctx_out, held_out, free_used_out, q_req, q_pos, slot};
+  const int64_t nt = 4 * (int64_t)capacity, out_bytes[7] = {nr + 4, nr, nr, 4, nt, nt, nt};
+  for (int i = 0; i < 4; ++i)
+    for (int o = 0; o < 7; ++o)
+      if (overlap(in[i], in_bytes[i], out[o], out_bytes[o])) return DSA_ERR_INVALID_ARG;
+  dsa::BatchLayoutArgs a;
+  a.ctx_len = ctx_len;
+  a.new_len = new_len;
+  a.pages_held = pages_held;
+  a.block_table = block_table;
+  a.free_pages = free_pages;
+  a.free_used = free_used;
+  a.num_req = num_req;
+  a.bt_stride = bt_stride;
+  a.page_size = page_size;
+  a.num_free = num_free;
+  a.capacity = capacity;
+  a.num_pages = num_pages;
+  a.cu_q = cu_q;
+  a.q_req = q_req;
+  a.q_pos = q_pos;
+  a.slot = slot;
+  a.ctx_out = ctx_out;
+  a.held_out = held_out;
+  a.free_used_out = free_used_out;
+  a.vec = aligned16(q_req) && aligned16(q_pos) && aligned16(slot);
+  a.dev_status = dev_status;
+  return from_cuda(dsa::launch_batch_layout(a, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_stride, int32_t q_heads,
+                            const float* q_weight, int32_t q_norm_dim, void* q_out, const void* k,
+                            int64_t k_tok_stride, int64_t k_head_stride, int32_t k_heads, const float* k_weight,
+                            int32_t k_norm_dim, void* k_out, int32_t num_tokens, int32_t d, int32_t d_rope,
+                            int32_t dtype, const int32_t* pos, const float* cos_sin, int32_t max_pos, float eps,
+                            int32_t interleaved, const int32_t* slot, uint8_t* kv, float* kv_scale, int64_t num_slots,
+                            int32_t* dev_status, void* stream) {
+  if (num_tokens < 0 || d < 8 || d % 8 != 0 || d > dsa::norm_rope_max_d()) return DSA_ERR_INVALID_ARG;
+  if (d_rope < 0 || d_rope > d || d_rope % 16 != 0 || (interleaved != 0 && interleaved != 1) || !(eps >= 0.f))
+    return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_BF16 && dtype != DSA_FP16) return DSA_ERR_INVALID_ARG;
+  if (q_heads < 0 || k_heads < 0 || q_heads + (int64_t)k_heads > 65536) return DSA_ERR_INVALID_ARG;
+  const bool cache = slot || kv || kv_scale;
+  if (cache && (!slot || !kv || !kv_scale || k_heads != 1 || num_slots <= 0 || !aligned16(kv)))
+    return DSA_ERR_INVALID_ARG;
+  dsa_status st = check_norm_side(q, q_tok_stride, q_head_stride, q_heads, q_weight, q_norm_dim, q_out, true,
+                                  num_tokens, d);
+  if (st != DSA_OK) return st;
+  st = check_norm_side(k, k_tok_stride, k_head_stride, k_heads, k_weight, k_norm_dim, k_out, !cache, num_tokens, d);
+  if (st != DSA_OK) return st;
+  if (num_tokens == 0 || q_heads + k_heads == 0) return DSA_OK;
+  if (d_rope > 0 && (!pos || !cos_sin || !aligned16(cos_sin) || max_pos <= 0)) return DSA_ERR_INVALID_ARG;
+  dsa::NormRopeArgs a;
+  a.q = {q, q_tok_stride, q_head_stride, q_heads, q_norm_dim, q_weight, q_heads > 0 ? q_out : nullptr};
+  a.k = {k, k_tok_stride, k_head_stride, k_heads, k_norm_dim, k_weight, k_heads > 0 ? k_out : nullptr};
+  a.num_tokens = num_tokens;
+  a.d = d;
+  a.d_rope = d_rope;
+  a.dtype = dtype;
+  a.pos = pos;
+  a.cos_sin = cos_sin;
+  a.max_pos = d_rope > 0 ? max_pos : INT32_MAX;
+  a.eps = eps;
+  a.interleaved = interleaved != 0;
+  a.slot = slot;
+  a.kv = cache ? kv : nullptr;
+  a.kv_scale = kv_scale;
+  a.num_slots = num_slots;
+  a.dev_status = dev_status;
+  return from_cuda(dsa::launch_qk_norm_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_scale, int64_t num_pages,
+                             const int32_t* block_table, int32_t num_req, int32_t bt_stride, const int32_t* q_req,
+                             const int32_t* q_pos, int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope,
+                             int32_t page_size, float softmax_scale, int32_t num_splits, void* out, float* lse,
+                             float* o_part, float* lse_part, int32_t* dev_status, void* stream) {
+  dsa::MlaArgs a;
+  // q_pos stands in for idx in the checks; k is unused
+  const dsa_status st = check_mla_args(q, kv, kv_scale, num_pages, block_table, num_req, bt_stride, q_req, q_pos,
+                                       num_q, num_heads, d_latent, d_rope, page_size, 1, softmax_scale, num_splits,
+                                       out, lse, o_part, lse_part, 0, nullptr, 0, dev_status, &a);
+  if (st != DSA_OK || num_q == 0) return st;
+  a.idx = nullptr;
+  return from_cuda(dsa::launch_chunk_simt(a, q_pos, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,
+                            const float* draft_probs, int64_t ld_draft, const int32_t* draft_tokens,
+                            const float* u_accept, const float* u_sample, const int32_t* cu_rows, int32_t num_req,
+                            int32_t max_out, const int32_t* ctx_len, int32_t* tokens, int32_t* num_out,
+                            int32_t* ctx_out, int32_t* dev_status, void* stream) {
+  if (num_rows < 0 || vocab <= 0 || num_req < 0 || max_out <= 0 || ld_target < vocab) return DSA_ERR_INVALID_ARG;
+  if (draft_probs && ld_draft < vocab) return DSA_ERR_INVALID_ARG;
+  if ((ctx_len == nullptr) != (ctx_out == nullptr)) return DSA_ERR_INVALID_ARG;
+  if (num_req > (1 << 24)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (num_req == 0) return DSA_OK;
+  if (!u_sample || !cu_rows || !tokens || !num_out) return DSA_ERR_INVALID_ARG;
+  if (num_rows > 0 && (!target_probs || !draft_tokens || !u_accept)) return DSA_ERR_INVALID_ARG;
+  dsa::VerifyArgs a;
+  a.target = target_probs;
+  a.ld_target = ld_target;
+  a.num_rows = num_rows;
+  a.vocab = vocab;
+  a.draft = draft_probs;
+  a.ld_draft = ld_draft;
+  a.draft_tokens = draft_tokens;
+  a.cu_rows = cu_rows;
+  a.u_accept = u_accept;
+  a.u_sample = u_sample;
+  a.num_req = num_req;
+  a.max_out = max_out;
+  a.ctx_len = ctx_len;
+  a.tokens = tokens;
+  a.num_out = num_out;
+  a.ctx_out = ctx_out;
+  a.dev_status = dev_status;
+  return from_cuda(dsa::launch_verify_draft(a, static_cast<cudaStream_t>(stream)));
 }

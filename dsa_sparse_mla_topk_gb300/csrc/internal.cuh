@@ -87,6 +87,66 @@ cudaError_t launch_kv_write(const void* rows, int32_t n, int32_t d, const int32_
 cudaError_t launch_combine(const float* o_part, const float* lse_part, int32_t num_splits, int32_t num_q,
                            int32_t heads, int32_t d_v, void* out, float* lse, cudaStream_t stream);
 
+// Block tables and slot maps from request lengths (dsa_batch_layout).
+struct BatchLayoutArgs {
+  const int32_t *ctx_len, *new_len, *pages_held;
+  int32_t* block_table;
+  const int32_t* free_pages;
+  const int32_t* free_used;
+  int32_t num_req, bt_stride, page_size, num_free, capacity;
+  int64_t num_pages;
+  int32_t *cu_q, *q_req, *q_pos, *slot, *ctx_out, *held_out, *free_used_out;
+  bool vec;  // the token arrays are 16-byte aligned
+  int32_t* dev_status;
+};
+int batch_layout_max_requests();
+cudaError_t launch_batch_layout(const BatchLayoutArgs& a, cudaStream_t stream);
+
+// Norm and position rotation of query and key rows (dsa_qk_norm_rope).
+struct NormRopeSide {
+  const void* x;                    // [tokens, heads, d] through the strides, or null
+  int64_t tok_stride, head_stride;  // elements
+  int32_t heads, norm_dim;
+  const float* weight;  // [norm_dim]
+  void* out;            // [tokens, heads, d] contiguous, or null
+};
+struct NormRopeArgs {
+  NormRopeSide q, k;
+  int32_t num_tokens, d, d_rope, dtype;
+  const int32_t* pos;
+  const float* cos_sin;
+  int32_t max_pos;
+  float eps;
+  bool interleaved;
+  const int32_t* slot;  // FP8 cache write of the key rows (one key head), or null
+  uint8_t* kv;
+  float* kv_scale;
+  int64_t num_slots;
+  int32_t* dev_status;
+};
+int norm_rope_max_d();
+cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
+
+// Dense attention over positions 0..q_pos[i] (dsa_chunk_mla_fwd).  MlaArgs
+// without idx; k is unused.
+cudaError_t launch_chunk_simt(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream);
+
+// Drafted tokens against the target's probabilities (dsa_verify_draft).
+struct VerifyArgs {
+  const float* target;  // [num_rows, ld_target]
+  int64_t ld_target;
+  int32_t num_rows, vocab;
+  const float* draft;  // [num_rows, ld_draft] or null
+  int64_t ld_draft;
+  const int32_t *draft_tokens, *cu_rows;
+  const float *u_accept, *u_sample;
+  int32_t num_req, max_out;
+  const int32_t* ctx_len;
+  int32_t *tokens, *num_out, *ctx_out;
+  int32_t* dev_status;
+};
+cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream);
+
 // Report a data-dependent error without trapping.
 __device__ __forceinline__ void report(int32_t* status, uint32_t bit) {
   if (status) atomicOr(reinterpret_cast<unsigned int*>(status), bit);

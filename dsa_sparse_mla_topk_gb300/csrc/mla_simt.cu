@@ -50,8 +50,10 @@ struct SimtCfg {
                                        sizeof(float) * H * T + sizeof(float) * 3 * H + sizeof(int64_t) * T;
 };
 
-template <int H, int DL, int DR>
-__global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a) {
+// DENSE: every position 0 .. q_pos[i] instead of the selected ones
+// (dsa_chunk_mla_fwd); a token with q_req = -1 or q_pos = -1 sees nothing.
+template <int H, int DL, int DR, bool DENSE>
+__global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a, const int32_t* __restrict__ q_pos) {
   using C = SimtCfg<H, DL, DR>;
   constexpr int NT = C::NT, T = C::T, DQK = C::DQK;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -79,9 +81,16 @@ __global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a) {
   }
   const int r = a.q_req[i];
   const bool req_ok = (r >= 0 && r < a.num_req);
-  if (!req_ok && tid == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
+  if (!req_ok && (!DENSE || r != -1) && tid == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
 
-  const int ntiles = (a.k + T - 1) / T;
+  int32_t k = a.k;  // entries of this token
+  if constexpr (DENSE) {
+    const int32_t p = q_pos[i];
+    const bool pos_ok = p >= -1 && p <= INT32_MAX - T && p / a.page_size < a.bt_stride;
+    if (!pos_ok && req_ok && tid == 0) report(a.dev_status, DSA_DEV_BAD_QPOS);
+    k = req_ok && pos_ok ? p + 1 : 0;
+  }
+  const int ntiles = (int)(((int64_t)k + T - 1) / T);
   const int t_begin = (int)((int64_t)ntiles * split / S);
   const int t_end = (int)((int64_t)ntiles * (split + 1) / S);
 
@@ -97,14 +106,14 @@ __global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a) {
 #pragma unroll
     for (int d = 0; d < C::DPT; ++d) acc[h][d] = 0.f;
 
-  const int32_t* row_idx = a.idx + (int64_t)i * a.k;
+  const int32_t* row_idx = DENSE ? nullptr : a.idx + (int64_t)i * a.k;
   for (int tile = t_begin; tile < t_end; ++tile) {
     __syncthreads();  // previous tile fully consumed
     if (tid < T) {
       const int e = tile * T + tid;
       int64_t slot = -1;
-      if (e < a.k && req_ok) {
-        const int32_t pos = row_idx[e];
+      if (e < k && req_ok) {
+        const int32_t pos = DENSE ? e : row_idx[e];
         if (pos < -1) {
           report(a.dev_status, DSA_DEV_BAD_INDEX);
         } else if (pos >= 0) {
@@ -242,14 +251,14 @@ __global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a) {
   }
 }
 
-template <int H, int DL, int DR>
-cudaError_t launch_simt_shape(const MlaArgs& a, cudaStream_t stream) {
+template <int H, int DL, int DR, bool DENSE>
+cudaError_t launch_simt_shape(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream) {
   using C = SimtCfg<H, DL, DR>;
-  auto kern = mla_simt_kernel<H, DL, DR>;
+  auto kern = mla_simt_kernel<H, DL, DR, DENSE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem_bytes);
   if (e != cudaSuccess) return e;
   dim3 grid(a.num_q, a.num_splits);
-  kern<<<grid, C::NT, C::smem_bytes, stream>>>(a);
+  kern<<<grid, C::NT, C::smem_bytes, stream>>>(a, q_pos);
   return cudaGetLastError();
 }
 
@@ -257,8 +266,17 @@ cudaError_t launch_simt_shape(const MlaArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_mla_simt(const MlaArgs& a, cudaStream_t stream) {
   if (a.num_q == 0) return cudaSuccess;
-  if (a.heads == 16 && a.d_latent == 64 && a.d_rope == 16) return launch_simt_shape<16, 64, 16>(a, stream);
-  if (a.heads == 64 && a.d_latent == 512 && a.d_rope == 64) return launch_simt_shape<64, 512, 64>(a, stream);
+  if (a.heads == 16 && a.d_latent == 64 && a.d_rope == 16) return launch_simt_shape<16, 64, 16, false>(a, nullptr, stream);
+  if (a.heads == 64 && a.d_latent == 512 && a.d_rope == 64) return launch_simt_shape<64, 512, 64, false>(a, nullptr, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_chunk_simt(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream) {
+  if (a.num_q == 0) return cudaSuccess;
+  if (a.heads == 16 && a.d_latent == 64 && a.d_rope == 16)
+    return launch_simt_shape<16, 64, 16, true>(a, q_pos, stream);
+  if (a.heads == 64 && a.d_latent == 512 && a.d_rope == 64)
+    return launch_simt_shape<64, 512, 64, true>(a, q_pos, stream);
   return cudaErrorInvalidValue;
 }
 

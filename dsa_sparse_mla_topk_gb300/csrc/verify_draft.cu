@@ -1,0 +1,254 @@
+// Drafted tokens verified against the target's probabilities.
+//
+// "Accelerating GLM-5.3-Flash on H200", section 3: a speculative verify step
+// runs the target over a block of drafted tokens.  With the target's
+// probabilities p_i after i drafted tokens, the draft's q_i and uniform
+// numbers u_i, draft x_i is taken while
+//     u_i q_i(x_i) < p_i(x_i)                              (u < p / q)
+// and the first one that is not, at a, is replaced by a token drawn from the
+// rest of the distribution,
+//     w = max(p_a - q_a, 0),   token = min { j : sum_{i <= j} w_i > u sum_i w_i };
+// after the last draft the token comes from p itself (speculative sampling:
+// every output token is then distributed as the target's).  A draft that
+// comes without probabilities is certain: q = 1 at x_i, 0 elsewhere.
+//
+// The token hangs on comparisons of sums of up to a million terms, so the
+// sums are whole numbers: a probability becomes the integer part of p 2^60
+// (exact for p >= 2^-37), p - q and every sum are then exact, whatever the
+// order and the number of CTAs, and u sum w is a 64 x 64 bit product.  An fp32
+// sum would move a border by ~1e-7 at each of V places, which shows in the
+// token about once in a hundred draws at V = 131,072.
+//
+// A thread-block cluster per request.  Every CTA finds a for itself (one lane
+// a draft); the CTAs then sum their parts of the row (each warp one
+// contiguous run, 16-byte loads where the rows allow), exchange the sums over
+// distributed shared memory, and only the warp whose run holds the token
+// reads it again (from L2), 128 values a turn.  Only rows a of p and q are
+// read: HBM-bound for many requests, one round trip after another for few.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace dsa {
+namespace {
+
+constexpr int VD_THREADS = 512;
+constexpr int VD_WARPS = VD_THREADS / 32;
+constexpr int VD_MAX_CLUSTER = 8;
+
+// p in [0, 1] as a multiple of 2^-60 (NaN and negative values: 0)
+__device__ __forceinline__ int64_t fixed60(float p) {
+  return __float2ll_rz(fminf(fmaxf(p, 0.f), 1.f) * 0x1p60f);
+}
+
+struct Row {
+  const float* p;
+  const float* q;   // null: nothing is taken off but `skip`
+  int64_t skip;     // a column of weight 0, or -1
+  int32_t vocab;
+  __device__ __forceinline__ int64_t weight(float pv, float qv, int32_t j) const {
+    const int64_t w = fixed60(pv) - (q ? fixed60(qv) : 0);
+    return j == skip || w < 0 ? 0 : w;
+  }
+};
+
+// Four columns j .. j + 3 (zero past the row's end); vec: 16-byte loads.
+template <bool VEC>
+__device__ __forceinline__ float4 load4(const float* row, int32_t j, int32_t vocab) {
+  if (VEC && j + 4 <= vocab) return *reinterpret_cast<const float4*>(row + j);
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = j + e < vocab ? row[j + e] : 0.f;
+  return make_float4(v[0], v[1], v[2], v[3]);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void weights4(const Row& r, int32_t j, int64_t (&w)[4]) {
+  const float4 p = load4<VEC>(r.p, j, r.vocab);
+  const float4 q = r.q ? load4<VEC>(r.q, j, r.vocab) : make_float4(0.f, 0.f, 0.f, 0.f);
+  w[0] = r.weight(p.x, q.x, j);
+  w[1] = r.weight(p.y, q.y, j + 1);
+  w[2] = r.weight(p.z, q.z, j + 2);
+  w[3] = r.weight(p.w, q.w, j + 3);
+}
+
+__device__ __forceinline__ int64_t warp_sum(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <bool VEC>
+__global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int C = cluster.num_blocks(), rank = cluster.block_rank();
+  const int req = blockIdx.x / C;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int64_t wsum[VD_WARPS];
+  __shared__ int64_t csum[VD_MAX_CLUSTER];  // the CTAs' sums, written by each of them
+  __shared__ int32_t s_take;
+
+  const int32_t row0 = a.cu_rows[req], row1 = a.cu_rows[req + 1];
+  int32_t* out = a.tokens + (int64_t)req * a.max_out;
+  const bool bad = row0 < 0 || row1 < row0 || row1 > a.num_rows;
+  if (bad || row1 == row0) {  // no rows (the same for the whole cluster)
+    if (rank == 0) {
+      if (tid == 0) {
+        if (bad) report(a.dev_status, DSA_DEV_BAD_INDEX);
+        a.num_out[req] = 0;
+        if (a.ctx_out) a.ctx_out[req] = a.ctx_len[req];
+      }
+      for (int e = tid; e < a.max_out; e += VD_THREADS) out[e] = -1;
+    }
+    return;
+  }
+  const int32_t* xs = a.draft_tokens + row0;
+  int32_t n = row1 - row0 - 1;
+  if (n > a.max_out - 1) {  // drafts past the output's width are not looked at
+    n = a.max_out - 1;
+    if (rank == 0 && tid == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
+  }
+
+  // ---- how many drafts are taken: one lane a draft, 32 at a time ----
+  if (warp == 0) {
+    int32_t take = n;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const int i = i0 + lane;
+      bool ok = true;
+      if (i < n) {
+        const int32_t x = xs[i];
+        ok = x >= 0 && x < a.vocab;
+        if (!ok && rank == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
+        if (ok) {
+          const float p = a.target[(int64_t)(row0 + i) * a.ld_target + x];
+          const float q = a.draft ? a.draft[(int64_t)(row0 + i) * a.ld_draft + x] : 1.f;
+          // two 24-bit factors: the product is exact in 64 bits (a NaN rejects)
+          ok = (double)a.u_accept[row0 + i] * (double)q < (double)p;
+        }
+      }
+      const unsigned no = __ballot_sync(0xffffffffu, !ok);
+      if (no) {
+        take = i0 + __ffs(no) - 1;
+        break;
+      }
+    }
+    if (lane == 0) s_take = take;
+  }
+  __syncthreads();
+  const int32_t take = s_take;
+  Row row = {a.target + (int64_t)(row0 + take) * a.ld_target, nullptr, -1, a.vocab};
+  if (take < n) {
+    if (a.draft) row.q = a.draft + (int64_t)(row0 + take) * a.ld_draft;
+    else row.skip = xs[take];
+  }
+
+  // a row without any probability; the warp that finds the token writes it
+  // after the cluster's barrier
+  if (rank == 0 && tid == 0) out[take] = a.vocab - 1;
+
+  // ---- this warp's run of the row: a multiple of 128 columns ----
+  const int nw = C * VD_WARPS;
+  const int32_t run = (int32_t)((((int64_t)a.vocab + nw - 1) / nw + 127) / 128) * 128;
+  const int64_t lo64 = (int64_t)(rank * VD_WARPS + warp) * run;
+  const int32_t lo = (int32_t)min(lo64, (int64_t)a.vocab), hi = (int32_t)min(lo64 + run, (int64_t)a.vocab);
+  int64_t total = 0, before = 0, mine = 0;
+  for (int turn = 0; turn < 2; ++turn) {
+    int64_t s = 0;
+#pragma unroll 4
+    for (int32_t j = lo + 4 * lane; j < hi; j += 128) {
+      int64_t w[4];
+      weights4<VEC>(row, j, w);
+      s += (w[0] + w[1]) + (w[2] + w[3]);
+    }
+    s = warp_sum(s);
+    mine = s;
+    if (lane == 0) wsum[warp] = s;
+    __syncthreads();
+    if (tid < C) {
+      int64_t cta = 0;
+      for (int w = 0; w < VD_WARPS; ++w) cta += wsum[w];
+      *cluster.map_shared_rank(&csum[rank], tid) = cta;
+    }
+    cluster.sync();
+    total = 0, before = 0;
+    for (int c = 0; c < C; ++c) {
+      if (c < rank) before += csum[c];
+      total += csum[c];
+    }
+    for (int w = 0; w < warp; ++w) before += wsum[w];
+    if (total != 0 || (!row.q && row.skip < 0)) break;
+    // nothing is left of the row (p <= q everywhere): the token comes from p
+    row.q = nullptr;
+    row.skip = -1;
+    cluster.sync();  // every CTA has read the sums
+  }
+
+  // ---- the warp whose run holds the token reads it again ----
+  const float u = a.u_sample[req];
+  // u 2^64, u clamped to [0, 1) (NaN: 0); exact for u >= 2^-40
+  const uint64_t u64 = __float2ull_rz(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f) * 0x1p64f);
+  const int64_t t = (int64_t)__umul64hi(u64, (uint64_t)total);  // floor(u sum w): sum_{i <= j} w > t
+  if (before <= t && t < before + mine) {
+    int64_t base = before;
+    for (int32_t j0 = lo; j0 < hi; j0 += 128) {
+      const int32_t j = j0 + 4 * lane;
+      int64_t w[4] = {0, 0, 0, 0};
+      if (j < hi) weights4<VEC>(row, j, w);
+      const int64_t s = (w[0] + w[1]) + (w[2] + w[3]);
+      int64_t inc = s;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+      }
+      const unsigned over = __ballot_sync(0xffffffffu, base + inc > t);
+      if (over) {
+        if (lane == __ffs(over) - 1) {
+          int64_t c = base + inc - s;
+          int e = 0;
+          while (e < 3 && c + w[e] <= t) c += w[e++];
+          out[take] = j + e;
+        }
+        break;
+      }
+      base += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
+  if (rank == 0) {
+    for (int e = tid; e < a.max_out; e += VD_THREADS)
+      if (e != take) out[e] = e < take ? xs[e] : -1;
+    if (tid == 0) {
+      a.num_out[req] = take + 1;
+      if (a.ctx_out) a.ctx_out[req] = a.ctx_len[req] + take + 1;
+    }
+  }
+  // no CTA leaves while another may still write its sum here: all have passed the last cluster.sync
+}
+
+}  // namespace
+
+cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
+  const bool vec = (reinterpret_cast<uintptr_t>(a.target) & 15u) == 0 && a.ld_target % 4 == 0 &&
+                   (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0 && a.ld_draft % 4 == 0));
+  int c = VD_MAX_CLUSTER;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.num_req * c);
+  cfg.blockDim = dim3(VD_THREADS);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<true>, a)
+                            : cudaLaunchKernelEx(&cfg, verify_draft_kernel<false>, a);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace dsa

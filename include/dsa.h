@@ -12,6 +12,13 @@
  * also does the attention call's page lookup); dsa_sparse_mla_topk_fwd runs
  * them as one kernel.  Both give the two calls' results bit for bit.
  *
+ * The rest of a serving step around them:
+ *
+ *   lengths --dsa_batch_layout--> block table, (req, pos, slot) of every token
+ *   q, k rows --dsa_qk_norm_rope--> q, and the key rows in the FP8 cache
+ *   (req, pos) --dsa_chunk_mla_fwd--> (out, lse) over every visible position
+ *   probabilities --dsa_verify_draft--> tokens, the next step's lengths
+ *
  * Sources (page titles):
  *  [LMSYS]  "Accelerating GLM-5.3-Flash on H200: High-Throughput Disaggregated
  *           Serving": section 1 "Architecture and workloads" (an indexer picks
@@ -63,7 +70,7 @@ extern "C" {
 typedef enum {
   DSA_OK = 0,
   DSA_ERR_INVALID_ARG = 1,       /* null pointer, negative size, bad alignment */
-  DSA_ERR_UNSUPPORTED_SHAPE = 2, /* (heads, d_latent, d_rope) not compiled in */
+  DSA_ERR_UNSUPPORTED_SHAPE = 2, /* (heads, d_latent, d_rope) not compiled in, or a size past the call's limit */
   DSA_ERR_WORKSPACE_TOO_SMALL = 3,
   DSA_ERR_CUDA = 4, /* a CUDA runtime call or kernel launch failed */
   DSA_ERR_OUT_OF_PAGES = 5 /* the page pool has no free or evictable page left */
@@ -74,6 +81,7 @@ typedef enum {
 #define DSA_DEV_BAD_INDEX 2u /* idx entry < -1, or its page slot is past the block table row */
 #define DSA_DEV_BAD_PAGE 4u  /* block table entry < 0 or >= num_pages, or q_req out of range */
 #define DSA_DEV_TIMEOUT 8u   /* a bounded wait inside a kernel expired */
+#define DSA_DEV_NO_PAGES 16u /* the free list has too few pages for a request */
 
 /* Static description of a status code (never NULL). */
 DSA_API const char* dsa_status_string(int32_t status);
@@ -300,6 +308,167 @@ DSA_API dsa_status dsa_combine(const float* o_part, const float* lse_part, int32
 DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const int32_t* req, const int32_t* pos,
                                 const int32_t* block_table, int32_t num_req, int32_t bt_stride, int32_t page_size,
                                 int64_t num_pages, uint8_t* kv, float* kv_scale, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_batch_layout -- block tables and slot maps of a step from its requests'
+ * lengths: what dsa_kv_write, dsa_topk_select and the attention calls take as
+ * req, pos and block_table, made on the GPU (no length has to reach the host;
+ * a captured graph stays valid while the lengths change).  [LMSYS] section 2:
+ * KV rows live in a paged pool mapped per request by a block table.
+ *
+ * Request r (0 <= r < num_req) has ctx_len[r] cached positions, pages_held[r]
+ * pages in its block table row, and brings new_len[r] tokens.  With
+ * total = ceil((ctx_len + new_len) / page_size), it needs need =
+ * max(0, total - pages_held) more pages (none when new_len = 0), taken from
+ * the free list in request order: block_table[r, pages_held[r] + x] =
+ * free_pages[*free_used + (needs of the requests before) + x].  The call
+ * writes
+ *   cu_q           int32 [num_req + 1]: request r's tokens are t = cu_q[r] ..
+ *                  cu_q[r + 1] - 1, cu_q the running sum of new_len.
+ *   q_req, q_pos, slot  int32 [capacity]: for each token its request, its
+ *                  position ctx_len[r] + t - cu_q[r] and the cache slot
+ *                  block_table[r, pos / page_size] * page_size + pos % page_size;
+ *                  -1 in all three for every t >= cu_q[num_req].
+ *   ctx_out, held_out  int32 [num_req]: ctx_len + new_len and the pages then held.
+ *   free_used_out  int32 [1]: *free_used plus the pages taken.
+ * ctx_out, held_out and free_used_out must not overlap the inputs (two sets
+ * used in turn): INVALID_ARG otherwise.  Only new entries of block_table are
+ * written.
+ *
+ *   ctx_len, new_len, pages_held  int32 [num_req].
+ *   block_table    int32 [num_req, bt_stride] page ids, updated in place.
+ *   free_pages     int32 [num_free] page ids; free_used int32 [1]: how many of
+ *                  them earlier calls have taken.
+ *   num_req        at most 8,192 (else UNSUPPORTED_SHAPE).
+ * Data errors leave a request as it is (ctx_out = ctx_len, held_out =
+ * pages_held, no pages taken, -1 for its tokens): a negative length sets
+ * DSA_DEV_BAD_QPOS (and the request has no tokens in cu_q); a block table row
+ * that is too short, or a free_used outside the list, DSA_DEV_BAD_INDEX; too
+ * few free pages DSA_DEV_NO_PAGES (a request's needs count against the
+ * requests after it even then).  Tokens past capacity set DSA_DEV_BAD_INDEX:
+ * cu_q stays at the last request that fits.  A page id out of range sets
+ * DSA_DEV_BAD_PAGE and slot = -1.
+ */
+DSA_API dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_len, const int32_t* pages_held,
+                                    int32_t num_req, int32_t* block_table, int32_t bt_stride,
+                                    const int32_t* free_pages, int32_t num_free, const int32_t* free_used,
+                                    int32_t page_size, int64_t num_pages, int32_t capacity, int32_t* cu_q,
+                                    int32_t* q_req, int32_t* q_pos, int32_t* slot, int32_t* ctx_out,
+                                    int32_t* held_out, int32_t* free_used_out, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_qk_norm_rope -- norms of query and key rows for each head, and the
+ * position rotation, in one pass; the key row may go straight into the paged
+ * FP8 cache (the rows the attention calls gather).  [vLLM] "Interpretation":
+ * one latent row serves all heads; [SGLang]: FP8 E4M3 cache.
+ *
+ * For a row x of token t and head h, in fp32:
+ *   y_j = x_j * weight_j / sqrt(mean_{j < norm_dim} x_j^2 + eps)  (j < norm_dim),
+ *   y_j = x_j (j >= norm_dim); then the last d_rope values are rotated by the
+ *   angle of position pos[t]: (y_a, y_b) <- (y_a c - y_b s, y_a s + y_b c) with
+ *   c = cos_sin[pos, i], s = cos_sin[pos, d_rope / 2 + i], for the pairs (a, b)
+ *   = (2i, 2i + 1) of the rotated part (interleaved = 1) or (i, i + d_rope / 2)
+ *   (interleaved = 0).
+ * A row is rounded once, to its own type; in the cache as scale = max |y| /
+ * 448 and byte_j = E4M3(y_j / scale) of the fp32 values (both divisions IEEE
+ * fp32; an all-zero row stores scale 0 and zero bytes).
+ *
+ *   q, k      [num_tokens, heads, d] rows of `dtype` (DSA_BF16, DSA_FP16),
+ *             addressed by token and head strides in elements (multiples of 8;
+ *             16-byte aligned base).  q_heads or k_heads may be 0 (the side is absent).
+ *   q_out, k_out  contiguous [num_tokens, heads, d], 16-byte aligned.  Each may be
+ *             its own input (then contiguous), else must not overlap q or k.  k_out
+ *             may be NULL when the cache is written.
+ *   q_weight, k_weight  fp32 [norm_dim], 16-byte aligned; norm_dim a multiple of 8, at
+ *             most d; 0: no norm (weight may be NULL).
+ *   d         a multiple of 8, at most 1024.  d_rope a multiple of 16, at most
+ *             d, with d - d_rope a multiple of 8; 0: no rotation (cos_sin may be NULL).
+ *   pos       int32 [num_tokens] (NULL allowed when d_rope = 0); -1: a padding
+ *             row, whose outputs are left as they were.
+ *   cos_sin   fp32 [max_pos, d_rope], 16-byte aligned.
+ *   slot, kv, kv_scale  the cache write (all three or none; k_heads must be 1):
+ *             slot int32 [num_tokens] (-1: not cached), kv uint8 [num_slots,
+ *             d] 16-byte aligned, kv_scale fp32 [num_slots].
+ * Data errors: pos outside [-1, max_pos) sets DSA_DEV_BAD_QPOS and the token
+ * is skipped; slot outside [-1, num_slots) sets DSA_DEV_BAD_INDEX and the row
+ * is not cached.  Rows aimed at the same slot leave one of them there,
+ * unspecified which.  Rows with NaN or infinities give unspecified values.
+ */
+#define DSA_BF16 0
+#define DSA_FP16 1
+DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_stride, int32_t q_heads,
+                                    const float* q_weight, int32_t q_norm_dim, void* q_out, const void* k,
+                                    int64_t k_tok_stride, int64_t k_head_stride, int32_t k_heads,
+                                    const float* k_weight, int32_t k_norm_dim, void* k_out, int32_t num_tokens,
+                                    int32_t d, int32_t d_rope, int32_t dtype, const int32_t* pos,
+                                    const float* cos_sin, int32_t max_pos, float eps, int32_t interleaved,
+                                    const int32_t* slot, uint8_t* kv, float* kv_scale, int64_t num_slots,
+                                    int32_t* dev_status, void* stream);
+
+/*
+ * dsa_chunk_mla_fwd -- attention of a chunk of new tokens over the paged FP8
+ * cache: dsa_sparse_mla_fwd without a selection.  Every head of token i
+ * attends to all positions 0..q_pos[i] of request q_req[i] (causal: the
+ * chunk's own rows are in the cache).  For prompts, decode and verify blocks
+ * of contexts no longer than the top-k would be, and for layers without an
+ * indexer.
+ *
+ * Arguments, layouts, outputs and splits are those of dsa_sparse_mla_fwd, with
+ * q_pos (int32 [num_q]) in place of idx and k, and no workspace.  A split takes
+ * a contiguous share of the token's own KV tiles.  A token with q_req = -1
+ * (padding) or q_pos = -1 sees nothing: out = 0 and lse = -inf.  Tokens of one
+ * request next to each other share its rows in L2; any order is correct.
+ * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
+ * and the token sees nothing; q_req outside [-1, num_req) or a page id out of
+ * range sets DSA_DEV_BAD_PAGE; such rows are skipped.
+ */
+DSA_API dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_scale, int64_t num_pages,
+                                     const int32_t* block_table, int32_t num_req, int32_t bt_stride,
+                                     const int32_t* q_req, const int32_t* q_pos, int32_t num_q, int32_t num_heads,
+                                     int32_t d_latent, int32_t d_rope, int32_t page_size, float softmax_scale,
+                                     int32_t num_splits, void* out, float* lse, float* o_part, float* lse_part,
+                                     int32_t* dev_status, void* stream);
+
+/*
+ * dsa_verify_draft -- verification of drafted tokens against the target's
+ * probabilities, from given random numbers.  [LMSYS] section 3: a speculative
+ * verify step runs the target over a block of drafted tokens.
+ *
+ * Request r has the rows t = cu_rows[r] .. cu_rows[r + 1] - 1 of the target's
+ * probabilities and n = rows - 1 drafted tokens; draft i is checked by row t_i =
+ * cu_rows[r] + i: it is taken while u_accept[t_i] * draft_probs[t_i, x_i] <
+ * target_probs[t_i, x_i] (product exact).  At the first draft a that is not taken (a = n if all are)
+ * the last token is drawn: w = max(target_probs[t_a] - draft_probs[t_a], 0)
+ * (target_probs[t_n] after the last draft), token = the lowest j with
+ * sum_{i <= j} w_i > u_sample[r] * sum_i w_i.  Without draft_probs a draft is
+ * certain: 1 at x_i and 0 elsewhere.  If no w is positive, w =
+ * target_probs[t_a].  Weights and sums are whole multiples of 2^-60: exact for
+ * probabilities of 2^-37 or more, and independent of the launch.
+ *
+ *   target_probs  fp32 [num_rows, vocab], row stride ld_target; each row in
+ *                 [0, 1] with a sum below 8 (NaN and negative values count as
+ *                 0, values above 1 as 1; a larger sum gives an unspecified token in range).
+ *   draft_probs   fp32 [num_rows, vocab], row stride ld_draft, or NULL.
+ *   draft_tokens  int32 [num_rows]: x_i of request r at cu_rows[r] + i.
+ *   u_accept      fp32 [num_rows], u_sample fp32 [num_req]: uniform in [0, 1).
+ *                 The entries of a request's last row in draft_probs,
+ *                 draft_tokens and u_accept are not read.
+ *   cu_rows       int32 [num_req + 1] (dsa_batch_layout's cu_q).
+ *   tokens        int32 [num_req, max_out] output: the taken drafts, then the
+ *                 drawn token, then -1.  num_out int32 [num_req] = a + 1.
+ *   ctx_len, ctx_out  int32 [num_req], or both NULL: ctx_out = ctx_len + num_out,
+ *                 the request's cached positions once the rejected rows are
+ *                 dropped (the same buffer is allowed).
+ * A request without rows has num_out = 0 and tokens -1.  Data errors, all
+ * DSA_DEV_BAD_INDEX: cu_rows decreasing or past num_rows (as a request
+ * without rows); a draft outside [0, vocab) (not taken); more rows than
+ * max_out (drafts past max_out - 1 are ignored).
+ */
+DSA_API dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,
+                                    const float* draft_probs, int64_t ld_draft, const int32_t* draft_tokens,
+                                    const float* u_accept, const float* u_sample, const int32_t* cu_rows,
+                                    int32_t num_req, int32_t max_out, const int32_t* ctx_len, int32_t* tokens,
+                                    int32_t* num_out, int32_t* ctx_out, int32_t* dev_status, void* stream);
 
 /*
  * KV-only prefix-sharing page allocator (host side, no GPU involved).

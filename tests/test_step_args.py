@@ -1,0 +1,131 @@
+"""Refusals of the serving step's operators: the C ABI's argument checks (no
+device needed: fake addresses that no check reads) and the binding's."""
+import ctypes
+
+import pytest
+import torch
+
+import dsa_sparse_mla_topk_gb300 as dsa
+from dsa_sparse_mla_topk_gb300 import build as dsa_build
+
+
+@pytest.fixture(scope="module")
+def lib():
+    dsa_build.build()
+    return dsa.load_library()
+
+
+no_device_only = pytest.mark.skipif(torch.cuda.is_available(),
+                                    reason="fake device addresses are only used where no CUDA device is present")
+VP = ctypes.c_void_p
+
+
+def A(i):  # distinct 16-byte aligned addresses, far apart
+    return VP(0x1000000 * (i + 1))
+
+
+MISALIGNED = VP(0x1000004)
+
+
+def _layout(lib, **over):
+    a = dict(ctx=A(0), new=A(1), held=A(2), R=4, bt=A(3), bs=8, free=A(4), nf=16, used=A(5), P=64, np=32, cap=64,
+             cu=A(6), req=A(7), pos=A(8), slot=A(9), co=A(10), ho=A(11), uo=A(12), st=None, s=None)
+    a.update(over)
+    return lib.dsa_batch_layout(*a.values())
+
+
+@no_device_only
+@pytest.mark.parametrize("over,expect", [
+    (dict(R=0), 1), (dict(R=-1), 1), (dict(R=8193), 2), (dict(bs=0), 1), (dict(nf=-1), 1), (dict(P=0), 1),
+    (dict(np=0), 1), (dict(np=1 << 30), 2), (dict(cap=-1), 1),
+    (dict(ctx=None), 1), (dict(new=None), 1), (dict(held=None), 1), (dict(bt=None), 1), (dict(free=None), 1),
+    (dict(used=None), 1), (dict(cu=None), 1), (dict(req=None), 1), (dict(pos=None), 1), (dict(slot=None), 1),
+    (dict(co=None), 1), (dict(ho=None), 1), (dict(uo=None), 1),
+    # outputs over inputs: another CTA may still read them
+    (dict(co=A(0)), 1), (dict(ho=A(2)), 1), (dict(uo=A(5)), 1), (dict(cu=A(1)), 1), (dict(slot=A(0)), 1),
+])
+def test_batch_layout_argument_checks(lib, over, expect):
+    assert _layout(lib, **over) == expect
+
+
+def _norm(lib, **over):
+    a = dict(q=A(0), qt=64 * 576, qh=576, nq=64, qw=A(1), qn=576, qo=A(2), k=A(3), kt=576, kh=576, nk=1, kw=A(4), kn=512,
+             ko=None, T=4, d=576, rope=64, dt=0, pos=A(5), cs=A(6), mp=100, eps=1e-6, il=1, slot=A(7), kv=A(8), sc=A(9),
+             ns=64, st=None, s=None)
+    a.update(over)
+    return lib.dsa_qk_norm_rope(*a.values())
+
+
+@no_device_only
+@pytest.mark.parametrize("over,expect", [
+    (dict(T=-1), 1), (dict(d=0), 1), (dict(d=580), 1), (dict(d=1032), 1), (dict(rope=8), 1), (dict(rope=-16), 1),
+    (dict(rope=592), 1), (dict(dt=2), 1), (dict(il=2), 1), (dict(eps=-1.0), 1), (dict(eps=float("nan")), 1),
+    (dict(nq=-1), 1), (dict(qn=4), 1), (dict(qn=584), 1), (dict(qw=None), 1), (dict(qw=MISALIGNED), 1),
+    (dict(q=None), 1), (dict(q=MISALIGNED), 1), (dict(qt=4), 1), (dict(qh=4), 1), (dict(qt=-8), 1), (dict(qo=None), 1),
+    (dict(qo=MISALIGNED), 1), (dict(qo=A(0), qt=64 * 576 + 8), 1), (dict(k=None), 1),
+    (dict(pos=None), 1), (dict(cs=None), 1), (dict(cs=MISALIGNED), 1), (dict(mp=0), 1),
+    (dict(slot=None), 1), (dict(kv=None), 1), (dict(sc=None), 1), (dict(kv=MISALIGNED), 1), (dict(ns=0), 1),
+    (dict(nk=2, kh=576, kt=1152), 1), (dict(slot=None, kv=None, sc=None), 1),  # no cache and no k_out
+    (dict(T=0), 0), (dict(nq=0, nk=0, slot=None, kv=None, sc=None), 0),
+])
+def test_norm_rope_argument_checks(lib, over, expect):
+    assert _norm(lib, **over) == expect
+
+
+def _chunk(lib, **over):
+    a = dict(q=A(0), kv=A(1), sc=A(2), np=4, bt=A(3), R=1, bs=4, req=A(4), pos=A(5), n=1, H=64, dl=512, dr=64, P=64,
+             scale=0.04, S=1, out=A(6), lse=A(7), op=None, lp=None, st=None, s=None)
+    a.update(over)
+    return lib.dsa_chunk_mla_fwd(*a.values())
+
+
+@no_device_only
+@pytest.mark.parametrize("over,expect", [
+    (dict(H=32), 2), (dict(dl=256), 2), (dict(dr=32), 2), (dict(P=0), 1), (dict(n=-1), 1), (dict(S=0), 1),
+    (dict(S=65), 1), (dict(q=None), 1), (dict(kv=None), 1), (dict(sc=None), 1), (dict(bt=None), 1), (dict(req=None), 1),
+    (dict(pos=None), 1), (dict(out=None), 1), (dict(q=MISALIGNED), 1), (dict(kv=MISALIGNED), 1),
+    (dict(out=MISALIGNED), 1), (dict(scale=float("inf")), 1), (dict(S=4, lp=A(8)), 1),
+    (dict(S=4, op=MISALIGNED, lp=A(8)), 1), (dict(np=0), 1), (dict(np=1 << 26), 2), (dict(R=0), 1), (dict(n=0), 0),
+])
+def test_chunk_argument_checks(lib, over, expect):
+    assert _chunk(lib, **over) == expect
+
+
+def _verify(lib, **over):
+    a = dict(p=A(0), ld=100, rows=8, V=100, q=A(1), ldq=100, tok=A(2), ua=A(3), us=A(4), cu=A(5), R=2, mo=4, ctx=A(6),
+             out=A(7), num=A(8), co=A(9), st=None, s=None)
+    a.update(over)
+    return lib.dsa_verify_draft(*a.values())
+
+
+@no_device_only
+@pytest.mark.parametrize("over,expect", [
+    (dict(rows=-1), 1), (dict(V=0), 1), (dict(R=-1), 1), (dict(mo=0), 1), (dict(ld=99), 1), (dict(ldq=99), 1),
+    (dict(ctx=None), 1), (dict(co=None), 1), (dict(us=None), 1), (dict(cu=None), 1), (dict(out=None), 1),
+    (dict(num=None), 1), (dict(p=None), 1), (dict(tok=None), 1), (dict(ua=None), 1), (dict(R=(1 << 24) + 1), 2),
+    (dict(R=0), 0),
+])
+def test_verify_argument_checks(lib, over, expect):
+    assert _verify(lib, **over) == expect
+
+
+def test_binding_rejects_cpu_tensors_and_types(lib):
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError):
+        dsa.batch_layout(i(2), i(2), i(2), i(2, 4), i(8), i(1), page_size=16, num_pages=8, capacity=4)
+    with pytest.raises(TypeError):
+        dsa.batch_layout(torch.zeros(2), i(2), i(2), i(2, 4), i(8), i(1), page_size=16, num_pages=8, capacity=4)
+    b = torch.zeros(2, 1, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        dsa.qk_norm_rope(b, None, i(2), torch.zeros(4, 16), d_rope=16)
+    with pytest.raises(TypeError):
+        dsa.qk_norm_rope(b.float(), None, i(2), torch.zeros(4, 16), d_rope=16)
+    with pytest.raises(ValueError):
+        dsa.qk_norm_rope(None, None, None, None, d_rope=0)
+    with pytest.raises(ValueError):
+        dsa.chunk_mla(torch.zeros(1, 16, 80, dtype=torch.bfloat16), torch.zeros(16, 80, dtype=torch.uint8),
+                      torch.zeros(16), i(1, 1), i(1), i(1), d_latent=64, d_rope=16, page_size=16, softmax_scale=0.1)
+    with pytest.raises(ValueError):
+        dsa.verify_draft(torch.zeros(2, 8), i(2), i(2), torch.zeros(2), torch.zeros(1), max_out=2)
+    with pytest.raises(TypeError):
+        dsa.verify_draft(torch.zeros(2, 8).double(), i(2), i(2), torch.zeros(2), torch.zeros(1), max_out=2)
