@@ -402,6 +402,8 @@ dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_s
                                        out, lse, o_part, lse_part, 0, nullptr, 0, dev_status, &a);
   if (st != DSA_OK || num_q == 0) return st;
   a.idx = nullptr;
+  if (use_tensor_cores(num_heads, d_latent, d_rope))
+    return from_cuda(dsa::launch_chunk_tc(a, q_pos, static_cast<cudaStream_t>(stream)));
   return from_cuda(dsa::launch_chunk_simt(a, q_pos, static_cast<cudaStream_t>(stream)));
 }
 

@@ -130,6 +130,8 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 // Dense attention over positions 0..q_pos[i] (dsa_chunk_mla_fwd).  MlaArgs
 // without idx; k is unused.
 cudaError_t launch_chunk_simt(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream);
+// The same on the tensor cores, for (64, 512, 64).
+cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream);
 
 // Drafted tokens against the target's probabilities (dsa_verify_draft).
 struct VerifyArgs {

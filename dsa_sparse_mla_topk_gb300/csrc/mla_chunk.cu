@@ -1,0 +1,649 @@
+// Attention of a chunk of new tokens over every visible position of the paged
+// FP8 cache, on the Blackwell tensor cores (tcgen05 + TMEM + TMA).
+//
+// "Accelerating GLM-5.3-Flash on H200", section 3: QK^T, online softmax and
+// the weighted value sum one KV tile at a time, splits merged by a Combine
+// step; "GLM-5.3 Optimizations, Part 2" ("Interpretation"): a latent KV row is
+// shared by all 64 heads.  For token i with request r and position p:
+//   z_j = softmax_scale q . x_j,  x_j = e4m3(kv[slot_j]) s_j,  j = 0 .. p
+//   out = sum_j softmax(z)_j x_j[:512],  lse = ln sum_j exp z_j
+//
+// One CTA = one token x one KV split (the 64 heads are the work that shares a
+// row; the tokens of a request run side by side and share its rows in L2).
+// Bound by the tensor pipe: a 64-row tile is 64 x 64 x (576 + 512) products
+// twice (below), 1,376 cycles of MMAs.  20 warps:
+//  * 3 TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
+//    tiles in flight.  A tile whose positions are all visible comes in boxes
+//    of 64, 32, 16 or 8 rows, the largest that divides the page size (5 to
+//    40 copies; a bad page reads as zeros); the last tile, and page sizes that
+//    are not a multiple of 8, four rows a copy (tile::gather4, 80 copies), rows past the
+//    last position reading as zeros, so that nothing behind it reaches an MMA.
+//  * 1 MMA warp issues kind::f8f6f4 MMAs:
+//        S    = [Q_hi ; Q_lo] K^T          M = 128, N = 64 rows, K = 576
+//        O^T += V^T P_hi^T + V^T P_lo^T    M = 4 x 128 latent dims, N = 64 heads, K = 64 rows
+//    Q's latent part is the A operand in tensor memory, its rope part and K
+//    are in shared memory; V^T is the same tile read MN-major.
+//  * 16 softmax warps turn S into P: lane quadrant q holds heads 16 q .. + 15,
+//    Q_hi rows in lanes 0-15 and Q_lo rows in lanes 16-31; a shuffle adds the
+//    halves, and a thread owns one head and 8 rows of the tile.
+// Q = Q_hi + Q_lo is exact for bf16 (two E4M3 numbers of a token scaled by a
+// power of two).  A weight P' = p s_j 2^E is E4M3 + E5M2: relative error at
+// most 2^-8, and weights down to 2^-22 of the largest are kept, where a second
+// E4M3 number would end at 2^-14: over a long context the many small weights
+// of a flat tail are a share of the result that must not be rounded away.
+// Lazy rescaling: a head's reference maximum moves when a logit passes it by more
+// than 2^2 (p <= 4), E when a row's scale passes its bound; l is summed in fp32
+// from unrounded p.  All waits are bounded.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "internal.cuh"
+#include "mla_tc_common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace dsa {
+namespace {
+
+using namespace sm100;
+
+constexpr int H = 64, DL = 512, DR = 64, DQK = DL + DR;
+constexpr int T = 64;                           // KV rows per tile
+constexpr int NST = 5;                          // KV tiles in flight
+constexpr int NLAT = DL / 128;                  // 128-column latent slices per row
+constexpr int LAT_BYTES = T * 128;              // one latent slice of a tile (128-byte swizzle)
+constexpr int ROPE_OFF = NLAT * LAT_BYTES;      // the rope slice (64-byte swizzle)
+constexpr int STAGE_BYTES = ROPE_OFF + T * DR;  // 36 KB
+constexpr int QM = 2 * H;
+constexpr int QROPE_BYTES = QM * DR;
+constexpr int P_BYTES = H * T;  // P_hi (or P_lo) of a tile: [head][row], K-major, 64-byte swizzle
+constexpr int NPB = 2;
+constexpr int NTMA = 3, WARP_MMA = 3, SM_WARP0 = 4, SM_WARPS = 16;
+constexpr int SM_THREADS = SM_WARPS * 32;
+constexpr int NTHREADS = (SM_WARP0 + SM_WARPS) * 32;
+constexpr float EXCEED_LOG2 = 2.0f;      // p = 2^(z - m) <= 2^2
+constexpr float SCALE_BOUND = 64.0f;     // s_j 2^E < 64: P' < 256
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+// TMEM columns: two S buffers, Q's latent operand, O^T (4 chunks of 64 heads).
+// Q row (= lane) of head h: 32 (h / 16) + h % 16 for Q_hi, 16 more for Q_lo.
+constexpr uint32_t TM_S = 0, TM_Q = 2 * T, TM_O = 256, TM_COLS = 512;
+static_assert(TM_Q + DL / 4 == TM_O, "S, Q and O fill the 512 TMEM columns");
+__device__ constexpr int q_row(int h, int lo) { return 32 * (h >> 4) + (h & 15) + 16 * lo; }
+
+// shared memory (offsets from a 1024-byte aligned base)
+constexpr int OFF_KV = 0;
+constexpr int OFF_QR = OFF_KV + NST * STAGE_BYTES;
+constexpr int OFF_P = OFF_QR + QROPE_BYTES;           // [buffer][hi, lo]
+constexpr int OFF_RED = OFF_P + NPB * 2 * P_BYTES;    // [4 row parts][64 heads] floats
+constexpr int OFF_ALPHA = OFF_RED + 4 * H * 4;        // per-head factor of O, then 1 / l
+constexpr int OFF_ROWF = OFF_ALPHA + H * 4;           // [16 warps][2 tiles][16 rows' logit factors, 16 rows' scales]
+constexpr int OFF_FLAG = OFF_ROWF + SM_WARPS * 2 * 32 * 4;  // rescale flags [4], Q exponent, scales [4]
+constexpr int OFF_BAR = OFF_FLAG + 128;
+constexpr int B_KVF = 0;               // [NST] the tile in stage s has landed
+constexpr int B_KVE = B_KVF + NST;     // [NST] stage s is free
+constexpr int B_SF = B_KVE + NST;      // [2] S buffer b is complete
+constexpr int B_PF = B_SF + 2;         // [2] P buffer b is written (and O rescaled)
+constexpr int B_PVD = B_PF + NPB;      // [2] P V of the tile in P buffer b is done
+constexpr int B_FIN = B_PVD + NPB;     // every MMA is done
+constexpr int B_QREADY = B_FIN + 1;    // Q is converted (and its staging stages are free)
+constexpr int B_QLOAD = B_QREADY + 1;  // raw bf16 Q has landed in the staging stages
+constexpr int NBAR = B_QLOAD + 1;
+constexpr int QSTAGE = NST - 2;
+static_assert(2 * STAGE_BYTES == H * DQK * 2, "bf16 Q fills two KV stages");
+constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;  // with alignment slack
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(OFF_QR % 1024 == 0 && OFF_P % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
+
+struct ChunkMaps {
+  CUtensorMap lat_box, rope_box;  // box_rows rows
+  CUtensorMap lat_row, rope_row;  // one row, for tile::gather4
+};
+
+__global__ void __launch_bounds__(NTHREADS, 1)
+    mla_chunk_kernel(const MlaArgs a, const int32_t* __restrict__ q_pos, const __grid_constant__ ChunkMaps maps,
+                     const int box_rows, const int page_shift) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* red_s = reinterpret_cast<float*>(smem + OFF_RED);
+  float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
+  int* resc_s = reinterpret_cast<int*>(smem + OFF_FLAG);
+  int* qexp_s = resc_s + 4;
+  float* smax_s = reinterpret_cast<float*>(resc_s + 8);  // [4] a tile's row parts' largest scales
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+  auto bar = [&](int b) { return smem_u32(bars + b); };
+  auto wait_warp = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)); };
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the last tokens first: in a causal chunk they see the most
+  const int i = (int)gridDim.x - 1 - (int)blockIdx.x;
+  const int split = blockIdx.y, S = gridDim.y;
+  const int P = a.page_size;
+  const int32_t r = a.q_req[i], last = q_pos[i];
+  const bool req_ok = r >= 0 && r < a.num_req;
+  const bool pos_ok = last >= -1 && last <= INT32_MAX - T && last / P < a.bt_stride;
+  if (tid == 0) {
+    if (!req_ok && r != -1) report(a.dev_status, DSA_DEV_BAD_PAGE);
+    if (req_ok && !pos_ok) report(a.dev_status, DSA_DEV_BAD_QPOS);
+  }
+  const int n = req_ok && pos_ok ? last + 1 : 0;  // visible positions
+  const int ntiles = (n + T - 1) / T;
+  const int t_begin = (int)((int64_t)ntiles * split / S), t_end = (int)((int64_t)ntiles * (split + 1) / S);
+  const int ntl = t_end - t_begin;
+
+  if (ntl == 0) {  // nothing to see: O = 0, lse = -inf
+    for (int e = tid; e < H * DL; e += NTHREADS) {
+      if (S == 1) static_cast<__nv_bfloat16*>(a.out)[(int64_t)i * H * DL + e] = __float2bfloat16_rn(0.f);
+      else a.o_part[((int64_t)split * a.num_q + i) * H * DL + e] = 0.f;
+    }
+    for (int h = tid; h < H; h += NTHREADS) {
+      if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + h] = -INFINITY;
+      else if (a.lse) a.lse[(int64_t)i * H + h] = -INFINITY;
+    }
+    return;
+  }
+
+  // ---------------- setup ----------------
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), TM_COLS);
+    tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < NST; ++s) {
+      mbar_init(bar(B_KVF + s), NTMA);
+      mbar_init(bar(B_KVE + s), 1);
+    }
+    for (int b = 0; b < 2; ++b) mbar_init(bar(B_SF + b), 1);
+    for (int b = 0; b < NPB; ++b) {
+      mbar_init(bar(B_PF + b), SM_WARPS);
+      mbar_init(bar(B_PVD + b), 1);
+    }
+    mbar_init(bar(B_FIN), 1);
+    mbar_init(bar(B_QREADY), SM_WARPS);
+    mbar_init(bar(B_QLOAD), 1);
+    fence_mbarrier_init();
+    tma_prefetch_map(&maps.lat_box);
+    tma_prefetch_map(&maps.rope_box);
+    tma_prefetch_map(&maps.lat_row);
+    tma_prefetch_map(&maps.rope_row);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t kv_base = smem_u32(smem + OFF_KV), qr_base = smem_u32(smem + OFF_QR), p_base = smem_u32(smem + OFF_P);
+  bool ok = true;
+  const int32_t* bt = a.block_table + (int64_t)r * a.bt_stride;
+  // the cache row of a visible position; -1: its page does not exist
+  auto slot_of = [&](int pos) -> int {
+    const int pg = page_shift >= 0 ? pos >> page_shift : pos / P;
+    const int page = __ldg(bt + pg);
+    return page >= 0 && page < a.num_pages ? page * P + (pos - pg * P) : -1;
+  };
+
+  if (warp < NTMA) {
+    // ---------------- TMA warps ----------------
+    if (tid == 0) {  // raw Q into the staging stages
+      mbar_arrive_expect_tx(bar(B_QLOAD), 2 * STAGE_BYTES);
+      tma_bulk_load(kv_base + QSTAGE * STAGE_BYTES, static_cast<const __nv_bfloat16*>(a.q) + (int64_t)i * H * DQK,
+                    2 * STAGE_BYTES, bar(B_QLOAD));
+    }
+    // A tile's copies are numbered group-major, c = 5 g + slice (four latent
+    // slices, then rope), and dealt to the warps in runs, one copy a lane.
+    // Boxes: groups of box_rows rows, y the row of the first; else groups of 4.
+    struct Deal {
+      int g, part;
+      bool has;
+      uint32_t bytes;  // this warp's bytes per tile
+    };
+    auto deal = [&](int rows) {
+      const int nc = (NLAT + 1) * (T / rows);
+      const int c0 = nc * warp / NTMA, c = c0 + lane;
+      Deal d;
+      d.g = c / (NLAT + 1), d.part = c % (NLAT + 1);
+      d.has = lane < nc * (warp + 1) / NTMA - c0;
+      d.bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, d.has && d.part < NLAT)) * 128u * rows +
+                (uint32_t)__popc(__ballot_sync(0xffffffffu, d.has && d.part == NLAT)) * (uint32_t)DR * rows;
+      return d;
+    };
+    const Deal db = deal(box_rows > 0 ? box_rows : 4), dg = deal(4);
+    const int past = (int)(a.num_pages * P);  // a row past the pool: reads as zeros
+    auto boxed = [&](int lt) { return box_rows > 0 && (t_begin + lt + 1) * T <= n; };
+    // the cache rows of this lane's group of tile lt (a box: the first one's, in x)
+    auto rows_of = [&](int lt) -> int4 {
+      int4 v = make_int4(past, past, past, past);
+      if (lt >= ntl) return v;
+      const int base = (t_begin + lt) * T;
+      if (boxed(lt)) {
+        if (db.has) {
+          const int s = slot_of(base + db.g * box_rows);
+          v.x = s >= 0 ? s : past;
+        }
+      } else if (dg.has) {
+        int s[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int pos = base + 4 * dg.g + q;
+          s[q] = pos < n ? slot_of(pos) : -1;
+        }
+        v = make_int4(s[0], s[1], s[2], s[3]);
+      }
+      return v;
+    };
+    int issued = 0;
+    int4 rows_cur = rows_of(0), rows_nxt = rows_of(1);
+    for (int lt = 0; lt < ntl; ++lt) {
+      const int s = lt % NST;
+      const int4 rows_far = rows_of(lt + 2);
+      if (lt >= NST && !wait_warp(B_KVE + s, ((lt - NST) / NST) & 1)) {
+        ok = false;
+        break;
+      }
+      if (lt == QSTAGE && !wait_warp(B_QREADY, 0)) {  // the staging stages hold raw Q until then
+        ok = false;
+        break;
+      }
+      const uint32_t dst = kv_base + s * STAGE_BYTES;
+      const bool bx = boxed(lt);
+      if (lane == 0) mbar_arrive_expect_tx(bar(B_KVF + s), bx ? db.bytes : dg.bytes);
+      __syncwarp();
+      if (bx) {
+        if (db.has) {
+          if (db.part < NLAT)
+            tma_load_2d(dst + db.part * LAT_BYTES + db.g * box_rows * 128, &maps.lat_box, db.part * 128, rows_cur.x,
+                        bar(B_KVF + s));
+          else
+            tma_load_2d(dst + ROPE_OFF + db.g * box_rows * DR, &maps.rope_box, DL, rows_cur.x, bar(B_KVF + s));
+        }
+      } else if (dg.has) {
+        if (dg.part < NLAT)
+          tma_gather4(dst + dg.part * LAT_BYTES + dg.g * 512, &maps.lat_row, dg.part * 128, rows_cur, bar(B_KVF + s));
+        else
+          tma_gather4(dst + ROPE_OFF + dg.g * 256, &maps.rope_row, DL, rows_cur, bar(B_KVF + s));
+      }
+      rows_cur = rows_nxt;
+      rows_nxt = rows_far;
+      issued = lt + 1;
+    }
+    // no copy may land after the CTA is gone
+    for (int lt = issued > NST ? issued - NST : 0; lt < issued; ++lt)
+      if (!wait_warp(B_KVF + lt % NST, (lt / NST) & 1)) ok = false;
+    if (tid < 32 && !wait_warp(B_QLOAD, 0)) ok = false;
+    if (!ok && lane == 0) report(a.dev_status, DSA_DEV_TIMEOUT);
+  } else if (warp == WARP_MMA) {
+    // ---------------- MMA warp ----------------
+    constexpr uint32_t ID_QK = idesc_f16_f32(QM, T, 0, 0, 0);      // kind::f8f6f4: E4M3 x E4M3 -> f32
+    constexpr uint32_t ID_PV_HI = idesc_f16_f32(128, H, 1, 0, 0);
+    constexpr uint32_t ID_PV_LO = ID_PV_HI | (1u << 10);           // B is E5M2
+    const uint64_t a_rope = smem_desc(qr_base, 16, 512, SWIZZLE_64B);
+    auto issue_qk = [&](int lt) {
+      const uint32_t stage = kv_base + (lt % NST) * STAGE_BYTES;
+      const uint64_t b_lat = smem_desc(stage, 16, 1024, SWIZZLE_128B);
+      const uint64_t b_rope = smem_desc(stage + ROPE_OFF, 16, 512, SWIZZLE_64B);
+      const uint32_t d = tmem + TM_S + T * (lt & 1);
+#pragma unroll
+      for (int ka = 0; ka < NLAT; ++ka) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f8_ts_warp(d, tmem + TM_Q + 8 * (4 * ka + kk), b_lat + ((ka * LAT_BYTES + kk * 32) >> 4), ID_QK,
+                         (ka | kk) ? 1u : 0u);
+      }
+#pragma unroll
+      for (int kk = 0; kk < 2; ++kk) mma_f8_ss_warp(d, a_rope + ((kk * 32) >> 4), b_rope + ((kk * 32) >> 4), ID_QK, 1u);
+      mma_commit_warp(bar(B_SF + (lt & 1)));
+    };
+    auto issue_pv = [&](int lt) {
+      const int s = lt % NST, pb = lt % NPB;
+      const uint64_t a0 = smem_desc(kv_base + s * STAGE_BYTES, LAT_BYTES, 1024, SWIZZLE_128B);
+      const uint64_t b0 = smem_desc(p_base + pb * 2 * P_BYTES, 16, 512, SWIZZLE_64B);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll
+        for (int kk = 0; kk < T / 32; ++kk) {
+#pragma unroll
+          for (int c = 0; c < NLAT; ++c)  // consecutive MMAs never share an accumulator
+            mma_f8_ss_warp(tmem + TM_O + 64 * c, a0 + ((c * LAT_BYTES + kk * 32 * 128) >> 4),
+                           b0 + ((w * P_BYTES + kk * 32) >> 4), w ? ID_PV_LO : ID_PV_HI,
+                           (lt > 0 || w > 0 || kk > 0) ? 1u : 0u);
+        }
+      }
+      mma_commit_warp(bar(B_KVE + s));
+      mma_commit_warp(bar(B_PVD + pb));
+    };
+    auto kv_landed = [&](int lt) { return wait_warp(B_KVF + lt % NST, (lt / NST) & 1); };
+    ok = wait_warp(B_QREADY, 0);
+    for (int lt = 0; lt < 2 && lt < ntl && ok; ++lt) {
+      ok = kv_landed(lt);
+      if (ok) {
+        tc_fence_after_sync();
+        issue_qk(lt);
+      }
+    }
+    for (int lt = 0; lt < ntl && ok; ++lt) {
+      ok = wait_warp(B_PF + lt % NPB, (lt / NPB) & 1);
+      if (!ok) break;
+      tc_fence_after_sync();
+      issue_pv(lt);
+      if (lt + 2 < ntl) {  // S buffer lt % 2 has been read
+        ok = kv_landed(lt + 2);
+        if (!ok) break;
+        tc_fence_after_sync();
+        issue_qk(lt + 2);
+      }
+    }
+    __syncwarp();
+    mma_commit_warp(bar(B_FIN));
+    if (!wait_warp(B_FIN, 0)) ok = false;  // every MMA is done before TMEM is released
+    if (!ok && lane == 0) report(a.dev_status, DSA_DEV_TIMEOUT);
+  } else {
+    // ---------------- softmax warps ----------------
+    const int sw = warp - SM_WARP0, st = tid - SM_WARP0 * 32;
+    const int q4 = warp & 3;              // TMEM lane quadrant: heads 16 q4 .. + 15
+    const int part = sw >> 2;             // tile rows 16 part .. + 15; O heads 16 part .. + 15
+    const int hh = 16 * q4 + (lane & 15);  // this thread's head
+    const int up = lane >> 4;             // 0: this lane holds Q_hi logits, 1: Q_lo; rows 16 part + 8 up .. + 7
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * q4) << 16);
+    auto group_sync = [] { named_barrier_sync(2, SM_THREADS); };
+
+    // ---- Q: bf16 -> x 2^qexp -> E4M3 hi and lo, latent part to TMEM, rope part to shared memory ----
+    {
+      constexpr int CH = DQK / 8;  // 16-byte chunks (8 bf16) per head
+      const uint4* qraw = reinterpret_cast<const uint4*>(smem + OFF_KV + QSTAGE * STAGE_BYTES);
+      auto bf_lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+      auto bf_hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+      if (!wait_warp(B_QLOAD, 0)) ok = false;
+      float mx = 0.f;
+#pragma unroll 3
+      for (int e = st; e < H * CH; e += SM_THREADS) {
+        const uint4 v = qraw[e];
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[t])), fabsf(bf_hi(w[t]))));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      if (lane == 0) red_s[sw] = mx;
+      group_sync();
+      if (st == 0) {
+        float m = red_s[0];
+        for (int w = 1; w < SM_WARPS; ++w) m = fmaxf(m, red_s[w]);
+        int e = 0;
+        const bool fin = m > 0.f && m <= 3.0e38f;
+        if (fin) frexpf(m, &e);  // m < 2^e
+        *qexp_s = fin ? 8 - e : 0;
+      }
+      group_sync();
+      const float qs = ldexpf(1.f, *qexp_s);
+      auto split8 = [&](const uint4 v, uint2& hv, uint2& lv) {  // 8 elements as byte quadruples
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          float y0, y1;
+          upk2(mul2(pk2(bf_lo(w[t]), bf_hi(w[t])), pk2(qs, qs)), y0, y1);
+          split_e4m3x2(f32x2_to_f16x2(y0, y1), hi[t], lo[t]);
+        }
+        hv = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
+        lv = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
+      };
+      // Lane u writes row 32 q4 + u: Q_hi (u < 16) or Q_lo of head hh.  The two
+      // lanes of a head split each 32-element block's chunks and swap halves
+      // (loads staggered over the banks).
+      for (int j = part; j < DL / 32; j += 4) {
+        const uint4* src = qraw + hh * CH + 4 * j + 2 * up;
+        const uint4 ra = src[lane & 1], rb = src[(lane & 1) ^ 1];
+        uint2 keep[2], recv[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          uint2 hv, lv;
+          split8((t ^ (lane & 1)) ? rb : ra, hv, lv);
+          keep[t] = up ? lv : hv;
+          const uint2 send = up ? hv : lv;
+          recv[t] = make_uint2(__shfl_xor_sync(0xffffffffu, send.x, 16), __shfl_xor_sync(0xffffffffu, send.y, 16));
+        }
+        const uint2 c0 = up ? recv[0] : keep[0], c1 = up ? recv[1] : keep[1];
+        const uint2 c2 = up ? keep[0] : recv[0], c3 = up ? keep[1] : recv[1];
+        const uint32_t col[8] = {c0.x, c0.y, c1.x, c1.y, c2.x, c2.y, c3.x, c3.y};
+        tmem_st8(t_lane + TM_Q + 8 * j, col);
+      }
+      tmem_wait_st();
+      unsigned char* qr = smem + OFF_QR;
+      for (int e = st; e < H * (DR / 8); e += SM_THREADS) {
+        const int h = e >> 3, c = e & 7;
+        uint2 hv, lv;
+        split8(qraw[h * CH + DL / 8 + c], hv, lv);
+        const int cc = c >> 1, hf = c & 1, rh = q_row(h, 0), rl = q_row(h, 1);
+        *reinterpret_cast<uint2*>(qr + rh * DR + ((cc ^ ((rh >> 1) & 3)) << 4) + hf * 8) = hv;
+        *reinterpret_cast<uint2*>(qr + rl * DR + ((cc ^ ((rl >> 1) & 3)) << 4) + hf * 8) = lv;
+      }
+      // before the TMA warps' copies into the staging stages, and the MMAs
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_QREADY));
+    }
+    const float qk_scale = a.softmax_scale * LOG2E * ldexpf(1.f, -*qexp_s);
+
+    // ---- the tiles ----
+    float m_ref = -INFINITY;      // head hh's reference maximum (log2 domain), the same in its 8 threads
+    uint64_t l2 = pk2(0.f, 0.f);  // head hh's share of l, two running sums
+    int p_exp = 0;                // E, the same in every thread; set at the first row with a scale
+    float p_scale = 1.f;          // 2^E
+    bool p_set = false;
+    float* rowf = reinterpret_cast<float*>(smem + OFF_ROWF) + sw * 2 * 32;
+    // lane's row of tile lt: 16 part + lane % 16
+    auto row_slot = [&](int lt) -> int {
+      const int pos = (t_begin + lt) * T + 16 * part + (lane & 15);
+      if (lt >= ntl || pos >= n) return -1;
+      const int s = slot_of(pos);
+      if (s < 0 && lane < 16 && q4 == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
+      return s;
+    };
+    auto row_scale = [&](int slot) -> float { return slot >= 0 ? __ldg(a.kv_scale + slot) : 0.f; };
+    int slot_c = row_slot(0), slot_n = row_slot(1);
+    float sc_c = row_scale(slot_c);
+    for (int lt = 0; lt < ntl; ++lt) {  // no early exit: every warp reaches every barrier
+      const int sb = lt & 1;
+      const int slot_f = row_slot(lt + 2);
+      const float sc_n = row_scale(slot_n);
+      const unsigned vmask = __ballot_sync(0xffffffffu, slot_c >= 0);  // (twice the same 16 bits)
+      rowf[sb * 32 + lane] = lane < 16 ? sc_c * qk_scale : sc_c;
+      const float smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sc_c))));
+      __syncwarp();
+      const float4* cf4 = reinterpret_cast<const float4*>(rowf + sb * 32 + 8 * up);
+      if (ok && !wait_warp(B_SF + sb, (lt >> 1) & 1)) ok = false;
+      tc_fence_after_sync();
+      float z[8];  // logits of head hh, rows 16 part + 8 up + c, in the log2 domain (invalid: -inf)
+      {
+        float v[16];
+        tmem_ld16(t_lane + TM_S + T * sb + 16 * part, v);
+        tmem_wait_ld();
+        float got[8];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) got[c] = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[8 + c], 16);
+#pragma unroll
+        for (int k4 = 0; k4 < 2; ++k4) {
+          const float4 f = cf4[k4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int c = 4 * k4 + 2 * t;
+            const uint64_t mine = up ? pk2(v[8 + c], v[9 + c]) : pk2(v[c], v[c + 1]);
+            upk2(mul2(add2(mine, pk2(got[c], got[c + 1])), t ? pk2(f.z, f.w) : pk2(f.x, f.y)), z[c], z[c + 1]);
+          }
+        }
+        if (vmask != 0xffffffffu) {
+          const unsigned my_valid = vmask >> (8 * up);
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (!((my_valid >> c) & 1u)) z[c] = -INFINITY;
+        }
+      }
+      float tm = z[0];
+#pragma unroll
+      for (int c = 1; c < 8; ++c) tm = fmaxf(tm, z[c]);
+      // one vote of all softmax threads: does a logit pass its head's
+      // reference, or a row's scale the bound of E?
+      const bool grow = p_set ? smax * p_scale >= SCALE_BOUND : smax > 0.f;
+      if (named_barrier_or(3, SM_THREADS, grow || tm > m_ref + EXCEED_LOG2)) {
+        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
+        if (up == 0) red_s[part * H + hh] = tm;
+        if (q4 == 0 && lane == 0) smax_s[part] = smax;
+        group_sync();
+        const float mt = fmaxf(fmaxf(red_s[hh], red_s[H + hh]), fmaxf(red_s[2 * H + hh], red_s[3 * H + hh]));
+        const float sm = fmaxf(fmaxf(smax_s[0], smax_s[1]), fmaxf(smax_s[2], smax_s[3]));
+        float alpha = 1.f;
+        if (mt > m_ref + EXCEED_LOG2) {
+          alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mt);
+          m_ref = mt;
+        }
+        l2 = mul2(l2, pk2(alpha, alpha));
+        if (sm > 0.f && sm <= 3.0e38f && (!p_set || sm * p_scale >= SCALE_BOUND)) {
+          int e2;
+          frexpf(sm, &e2);         // sm < 2^e2: sm 2^E in [16, 32)
+          const int e = min(5 - e2, 120);  // (2^E stays finite for subnormal scales)
+          if (p_set) alpha *= ldexpf(1.f, e - p_exp);  // O carries 2^E
+          p_exp = e;
+          p_set = true;
+          p_scale = ldexpf(1.f, p_exp);
+        }
+        if (part == 0 && up == 0) alpha_s[hh] = alpha;
+        const unsigned need = __ballot_sync(0xffffffffu, lt > 0 && alpha != 1.f);
+        if (part == 0 && lane == 0) resc_s[q4] = need != 0u;
+        group_sync();
+        if (resc_s[0] | resc_s[1] | resc_s[2] | resc_s[3]) {
+          // O must hold every P V issued so far: the previous tile's
+          if (ok && !wait_warp(B_PVD + (lt - 1) % NPB, ((lt - 1) / NPB) & 1)) ok = false;
+          tc_fence_after_sync();
+          const float* al = alpha_s + 16 * part;
+#pragma unroll 1
+          for (int c = 0; c < NLAT; ++c) {
+            float o[16];
+            const uint32_t addr = t_lane + TM_O + 64 * c + 16 * part;
+            tmem_ld16(addr, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int h = 0; h < 16; ++h) o[h] *= al[h];
+            tmem_st16(addr, o);
+          }
+          tmem_wait_st();
+        }
+      }
+      // weights, folded with the row's scale and 2^E, as E4M3 + E5M2
+      uint32_t phi[4], plo[4];
+      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+      const uint64_t nm2 = pk2(-m_use, -m_use), ps2 = pk2(p_scale, p_scale);
+      const float4* sf4 = reinterpret_cast<const float4*>(rowf + sb * 32 + 16 + 8 * up);
+#pragma unroll
+      for (int k4 = 0; k4 < 2; ++k4) {
+        const float4 f = sf4[k4];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int c = 4 * k4 + 2 * t;
+          float d0, d1;
+          upk2(add2(pk2(z[c], z[c + 1]), nm2), d0, d1);
+          const uint64_t p = pk2(ex2(d0), ex2(d1));
+          l2 = add2(l2, p);
+          float w0, w1;
+          upk2(mul2(p, mul2(t ? pk2(f.z, f.w) : pk2(f.x, f.y), ps2)), w0, w1);
+          split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
+        }
+      }
+      // P buffer lt % 2 was last read by P V(lt - 2), issued before QK^T(lt): the
+      // commit that completed S(lt) tracks it, so the buffer is free
+      {
+        unsigned char* pr = smem + OFF_P + (lt % NPB) * 2 * P_BYTES + hh * T + ((part ^ ((hh >> 1) & 3)) << 4) + 8 * up;
+        *reinterpret_cast<uint2*>(pr) = make_uint2(phi[0] | (phi[1] << 16), phi[2] | (phi[3] << 16));
+        *reinterpret_cast<uint2*>(pr + P_BYTES) = make_uint2(plo[0] | (plo[1] << 16), plo[2] | (plo[3] << 16));
+      }
+      fence_proxy_async_smem();
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_PF + lt % NPB));
+      slot_c = slot_n, slot_n = slot_f;
+      sc_c = sc_n;
+    }
+    // ---------------- epilogue ----------------
+    if (ok && !wait_warp(B_FIN, 0)) ok = false;
+    tc_fence_after_sync();
+    {
+      float la, lb;
+      upk2(l2, la, lb);
+      const float lp = la + lb, lw = lp + __shfl_xor_sync(0xffffffffu, lp, 16);
+      if (up == 0) red_s[part * H + hh] = lw;
+    }
+    group_sync();
+    if (part == 0 && up == 0) {
+      const float l = (red_s[hh] + red_s[H + hh]) + (red_s[2 * H + hh] + red_s[3 * H + hh]);
+      alpha_s[hh] = l > 0.f ? ldexpf(1.f / l, -p_exp) : 0.f;
+      const float lse = l > 0.f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
+      if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
+      else if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
+    }
+    group_sync();
+    if (ok) {
+      // thread (q4, lane) holds latent dim d = 128 c + 32 q4 + lane of heads
+      // 16 part .. + 15: a warp's store covers 32 consecutive d of one head
+      float inv[16];
+#pragma unroll
+      for (int h = 0; h < 16; ++h) inv[h] = alpha_s[16 * part + h];
+#pragma unroll 1
+      for (int c = 0; c < NLAT; ++c) {
+        const int d = 128 * c + 32 * q4 + lane;
+        float o[16];
+        tmem_ld16(t_lane + TM_O + 64 * c + 16 * part, o);
+        tmem_wait_ld();
+        if (S == 1) {
+          __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)i * H + 16 * part) * DL + d;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) ob[h * DL] = __float2bfloat16_rn(o[h] * inv[h]);
+        } else {
+          float* op = a.o_part + (((int64_t)split * a.num_q + i) * H + 16 * part) * DL + d;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) op[h * DL] = o[h] * inv[h];
+        }
+      }
+    } else if (lane == 0) {
+      report(a.dev_status, DSA_DEV_TIMEOUT);
+    }
+  }
+
+  // ---------------- teardown ----------------
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, TM_COLS);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream) {
+  if (a.num_q == 0) return cudaSuccess;
+  // the largest box of rows that never leaves a page (gather4 takes pages that no multiple of 8 fits)
+  int box = T;
+  while (box >= 8 && a.page_size % box != 0) box /= 2;
+  if (box < 8) box = 0;
+  int shift = -1;
+  for (int s = 0; s < 31; ++s)
+    if (a.page_size == (1 << s)) shift = s;
+  ChunkMaps maps;
+  const uint32_t rows = box > 0 ? box : 1;
+  if (!make_kv_map(&maps.lat_box, a, DQK, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_kv_map(&maps.rope_box, a, DQK, DR, rows, CU_TENSOR_MAP_SWIZZLE_64B) ||
+      !make_kv_map(&maps.lat_row, a, DQK, 128, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_kv_map(&maps.rope_row, a, DQK, DR, 1, CU_TENSOR_MAP_SWIZZLE_64B))
+    return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(mla_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  mla_chunk_kernel<<<dim3(a.num_q, a.num_splits), NTHREADS, SMEM_BYTES, stream>>>(a, q_pos, maps, box, shift);
+  return cudaGetLastError();
+}
+
+}  // namespace dsa

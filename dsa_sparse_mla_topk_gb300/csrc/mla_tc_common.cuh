@@ -31,6 +31,18 @@ __device__ __forceinline__ void split_e4m3x2(uint32_t h2, uint32_t& hi, uint32_t
   hi = a;
   lo = b;
 }
+// f16x2 -> hi = E4M3(x) and lo = E5M2(x - hi): 3 significant bits of the
+// residual, down to 2^-17 where E4M3 ends at 2^-10.
+__device__ __forceinline__ void split_e4m3_e5m2x2(uint32_t h2, uint32_t& hi, uint32_t& lo) {
+  unsigned short a, b;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(a) : "r"(h2));
+  uint32_t back;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(back) : "h"(a));
+  const __half2 r = __hsub2(*reinterpret_cast<const __half2*>(&h2), *reinterpret_cast<const __half2*>(&back));
+  asm("cvt.rn.satfinite.e5m2x2.f16x2 %0, %1;" : "=h"(b) : "r"(*reinterpret_cast<const uint32_t*>(&r)));
+  hi = a;
+  lo = b;
+}
 // Two-wide fp32 arithmetic, each lane rounded as its scalar .rn form.
 __device__ __forceinline__ uint64_t pk2(float lo, float hi) {
   uint64_t r;

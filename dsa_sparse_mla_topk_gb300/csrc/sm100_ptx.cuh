@@ -80,6 +80,16 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const void* tmap, int 
       "l"(tmap), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
       : "memory");
 }
+// A box of a 2-D tensor from column x, row y (rows past the tensor read as
+// zeros) into shared memory, swizzled as the tensor map says; completes bytes
+// on `bar`.  x times the element size is a multiple of 16.
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* tmap, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
 // Contiguous bytes global -> shared (16-byte aligned, size a multiple of 16);
 // completes bytes on `bar`.
 __device__ __forceinline__ void tma_bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
