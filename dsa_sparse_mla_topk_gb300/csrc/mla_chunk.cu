@@ -120,12 +120,14 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   auto bar = [&](int b) { return smem_u32(bars + b); };
   auto wait_warp = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar(b), parity)); };
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (the shuffles tell the compiler that a value is the same for the whole
+  // warp: the MMA warp's loop and descriptors then need no vector registers)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // the last tokens first: in a causal chunk they see the most
   const int i = (int)gridDim.x - 1 - (int)blockIdx.x;
   const int split = blockIdx.y, S = gridDim.y;
   const int P = a.page_size;
-  const int32_t r = a.q_req[i], last = q_pos[i];
+  const int32_t r = __shfl_sync(0xffffffffu, a.q_req[i], 0), last = __shfl_sync(0xffffffffu, q_pos[i], 0);
   const bool req_ok = r >= 0 && r < a.num_req;
   const bool pos_ok = last >= -1 && last <= INT32_MAX - T && last / P < a.bt_stride;
   if (tid == 0) {
@@ -281,62 +283,69 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     constexpr uint32_t ID_QK = idesc_f16_f32(QM, T, 0, 0, 0);      // kind::f8f6f4: E4M3 x E4M3 -> f32
     constexpr uint32_t ID_PV_HI = idesc_f16_f32(128, H, 1, 0, 0);
     constexpr uint32_t ID_PV_LO = ID_PV_HI | (1u << 10);           // B is E5M2
+    // the tensor memory of a CTA that holds all 512 columns starts at 0: the
+    // addresses below are then constants and the descriptors warp-uniform
     const uint64_t a_rope = smem_desc(qr_base, 16, 512, SWIZZLE_64B);
-    auto issue_qk = [&](int lt) {
-      const uint32_t stage = kv_base + (lt % NST) * STAGE_BYTES;
-      const uint64_t b_lat = smem_desc(stage, 16, 1024, SWIZZLE_128B);
-      const uint64_t b_rope = smem_desc(stage + ROPE_OFF, 16, 512, SWIZZLE_64B);
-      const uint32_t d = tmem + TM_S + T * (lt & 1);
+    const uint64_t lat0 = smem_desc(kv_base, 16, 1024, SWIZZLE_128B);
+    const uint64_t rope0 = smem_desc(kv_base + ROPE_OFF, 16, 512, SWIZZLE_64B);
+    const uint64_t v0 = smem_desc(kv_base, LAT_BYTES, 1024, SWIZZLE_128B);
+    const uint64_t p0 = smem_desc(p_base, 16, 512, SWIZZLE_64B);
+    auto issue_qk = [&](int stage, int sb) {
+      const uint64_t b_lat = lat0 + (uint32_t)(stage * (STAGE_BYTES >> 4));
+      const uint64_t b_rope = rope0 + (uint32_t)(stage * (STAGE_BYTES >> 4));
+      const uint32_t d = TM_S + T * sb;
 #pragma unroll
       for (int ka = 0; ka < NLAT; ++ka) {
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_f8_ts_warp(d, tmem + TM_Q + 8 * (4 * ka + kk), b_lat + ((ka * LAT_BYTES + kk * 32) >> 4), ID_QK,
+          mma_f8_ts_warp(d, TM_Q + 8 * (4 * ka + kk), b_lat + ((ka * LAT_BYTES + kk * 32) >> 4), ID_QK,
                          (ka | kk) ? 1u : 0u);
       }
 #pragma unroll
       for (int kk = 0; kk < 2; ++kk) mma_f8_ss_warp(d, a_rope + ((kk * 32) >> 4), b_rope + ((kk * 32) >> 4), ID_QK, 1u);
-      mma_commit_warp(bar(B_SF + (lt & 1)));
+      mma_commit_warp(bar(B_SF + sb));
     };
-    auto issue_pv = [&](int lt) {
-      const int s = lt % NST, pb = lt % NPB;
-      const uint64_t a0 = smem_desc(kv_base + s * STAGE_BYTES, LAT_BYTES, 1024, SWIZZLE_128B);
-      const uint64_t b0 = smem_desc(p_base + pb * 2 * P_BYTES, 16, 512, SWIZZLE_64B);
+    auto issue_pv = [&](int stage, int pb, uint32_t acc) {
+      const uint64_t a0 = v0 + (uint32_t)(stage * (STAGE_BYTES >> 4));
+      const uint64_t b0 = p0 + (uint32_t)(pb * ((2 * P_BYTES) >> 4));
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
 #pragma unroll
         for (int kk = 0; kk < T / 32; ++kk) {
 #pragma unroll
           for (int c = 0; c < NLAT; ++c)  // consecutive MMAs never share an accumulator
-            mma_f8_ss_warp(tmem + TM_O + 64 * c, a0 + ((c * LAT_BYTES + kk * 32 * 128) >> 4),
-                           b0 + ((w * P_BYTES + kk * 32) >> 4), w ? ID_PV_LO : ID_PV_HI,
-                           (lt > 0 || w > 0 || kk > 0) ? 1u : 0u);
+            mma_f8_ss_warp(TM_O + 64 * c, a0 + ((c * LAT_BYTES + kk * 32 * 128) >> 4),
+                           b0 + ((w * P_BYTES + kk * 32) >> 4), w ? ID_PV_LO : ID_PV_HI, w > 0 || kk > 0 ? 1u : acc);
         }
       }
-      mma_commit_warp(bar(B_KVE + s));
+      mma_commit_warp(bar(B_KVE + stage));
       mma_commit_warp(bar(B_PVD + pb));
     };
-    auto kv_landed = [&](int lt) { return wait_warp(B_KVF + lt % NST, (lt / NST) & 1); };
-    ok = wait_warp(B_QREADY, 0);
-    for (int lt = 0; lt < 2 && lt < ntl && ok; ++lt) {
-      ok = kv_landed(lt);
-      if (ok) {
-        tc_fence_after_sync();
-        issue_qk(lt);
-      }
-    }
-    for (int lt = 0; lt < ntl && ok; ++lt) {
-      ok = wait_warp(B_PF + lt % NPB, (lt / NPB) & 1);
-      if (!ok) break;
+    // Reductions over the warp leave their result in a uniform register: the
+    // loop's counters and descriptors then need no per-MMA moves.
+    auto wait_u = [&](int b, uint32_t parity) { return __reduce_min_sync(0xffffffffu, (uint32_t)mbar_wait(bar(b), parity)); };
+    const int nt = __reduce_max_sync(0xffffffffu, ntl);
+    uint32_t good = __reduce_min_sync(0xffffffffu, (uint32_t)(tmem == 0)) & wait_u(B_QREADY, 0);
+    for (int lt = 0; lt < 2 && lt < nt && good; ++lt) {
+      good = wait_u(B_KVF + lt, 0);
       tc_fence_after_sync();
-      issue_pv(lt);
-      if (lt + 2 < ntl) {  // S buffer lt % 2 has been read
-        ok = kv_landed(lt + 2);
-        if (!ok) break;
-        tc_fence_after_sync();
-        issue_qk(lt + 2);
-      }
+      if (good) issue_qk(lt, lt);
     }
+    int stage = 0, far = 2, far_phase = 0;  // the stages of tiles lt and lt + 2
+    for (int lt = 0; lt < nt && good; ++lt) {
+      // the tile after next has usually landed long ago: looked at first, so
+      // that nothing but the two MMA groups sits between two waits for P
+      if (lt + 2 < nt) good = wait_u(B_KVF + far, far_phase);
+      good &= wait_u(B_PF + (lt & 1), (lt >> 1) & 1);
+      if (!good) break;
+      tc_fence_after_sync();
+      issue_pv(stage, lt & 1, lt > 0 ? 1u : 0u);
+      if (lt + 2 < nt) issue_qk(far, lt & 1);  // S buffer lt % 2 has been read
+      stage = stage == NST - 1 ? 0 : stage + 1;
+      if (far == NST - 1) far = 0, far_phase ^= 1;
+      else ++far;
+    }
+    ok = good != 0;
     __syncwarp();
     mma_commit_warp(bar(B_FIN));
     if (!wait_warp(B_FIN, 0)) ok = false;  // every MMA is done before TMEM is released
