@@ -11,8 +11,8 @@
 // One CTA = one token x one KV split (the 64 heads are the work that shares a
 // row; the tokens of a request run side by side and share its rows in L2).
 // Bound by the tensor pipe: a 64-row tile is 64 x 64 x (576 + 512) products
-// twice (below), 1,376 cycles of MMAs.  20 warps:
-//  * 3 TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
+// twice (below), 1,376 cycles of MMAs.  Warps:
+//  * 3 (or 7) TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
 //    tiles in flight.  A tile whose positions are all visible comes in boxes
 //    of 64, 32, 16 or 8 rows, the largest that divides the page size (5 to
 //    40 copies; a bad page reads as zeros); the last tile, and page sizes that
@@ -61,9 +61,7 @@ constexpr int QM = 2 * H;
 constexpr int QROPE_BYTES = QM * DR;
 constexpr int P_BYTES = H * T;  // P_hi (or P_lo) of a tile: [head][row], K-major, 64-byte swizzle
 constexpr int NPB = 2;
-constexpr int NTMA = 3, WARP_MMA = 3, SM_WARP0 = 4, SM_WARPS = 16;
-constexpr int SM_THREADS = SM_WARPS * 32;
-constexpr int NTHREADS = (SM_WARP0 + SM_WARPS) * 32;
+constexpr int SM_WARPS = 16, SM_THREADS = SM_WARPS * 32;
 constexpr float EXCEED_LOG2 = 2.0f;      // p = 2^(z - m) <= 2^2
 constexpr float SCALE_BOUND = 64.0f;     // s_j 2^E < 64: P' < 256
 constexpr float LOG2E = 1.4426950408889634f;
@@ -81,8 +79,9 @@ constexpr int OFF_QR = OFF_KV + NST * STAGE_BYTES;
 constexpr int OFF_P = OFF_QR + QROPE_BYTES;           // [buffer][hi, lo]
 constexpr int OFF_RED = OFF_P + NPB * 2 * P_BYTES;    // [4 row parts][64 heads] floats
 constexpr int OFF_ALPHA = OFF_RED + 4 * H * 4;        // per-head factor of O, then 1 / l
-constexpr int OFF_ROWF = OFF_ALPHA + H * 4;           // [16 warps][2 tiles][16 rows' logit factors, 16 rows' scales]
-constexpr int OFF_FLAG = OFF_ROWF + SM_WARPS * 2 * 32 * 4;  // rescale flags [4], Q exponent, scales [4]
+constexpr int OFF_SROW = OFF_ALPHA + H * 4;           // [NST][64] the tiles' row scales
+constexpr int OFF_INFO = OFF_SROW + NST * T * 4;      // [NST][2] valid rows (bits) and largest scale of each 32 rows
+constexpr int OFF_FLAG = OFF_INFO + NST * 2 * 8;      // O flags [4], Q exponent, vote flags [4]
 constexpr int OFF_BAR = OFF_FLAG + 128;
 constexpr int B_KVF = 0;               // [NST] the tile in stage s has landed
 constexpr int B_KVE = B_KVF + NST;     // [NST] stage s is free
@@ -92,7 +91,8 @@ constexpr int B_PVD = B_PF + NPB;      // [2] P V of the tile in P buffer b is d
 constexpr int B_FIN = B_PVD + NPB;     // every MMA is done
 constexpr int B_QREADY = B_FIN + 1;    // Q is converted (and its staging stages are free)
 constexpr int B_QLOAD = B_QREADY + 1;  // raw bf16 Q has landed in the staging stages
-constexpr int NBAR = B_QLOAD + 1;
+constexpr int B_VOTE = B_QLOAD + 1;    // every softmax warp has looked at its logits of the tile
+constexpr int NBAR = B_VOTE + 1;
 constexpr int QSTAGE = NST - 2;
 static_assert(2 * STAGE_BYTES == H * DQK * 2, "bf16 Q fills two KV stages");
 constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
@@ -100,21 +100,40 @@ constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;  // with alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(OFF_QR % 1024 == 0 && OFF_P % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 
+// pos / d for 0 <= pos < 2^31: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d)
+// (< 2^32 or 2^31), floor(pos m / 2^(31 + s)) is exact, as m d - 2^(31 + s) <= 2^s.
+struct FastDiv {
+  uint32_t m;
+  int32_t shift;
+  __device__ __forceinline__ int operator()(int pos) const { return (int)(((uint64_t)(uint32_t)pos * m) >> shift); }
+};
+FastDiv make_fast_div(int32_t d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 struct ChunkMaps {
   CUtensorMap lat_box, rope_box;  // box_rows rows
   CUtensorMap lat_row, rope_row;  // one row, for tile::gather4
 };
 
-__global__ void __launch_bounds__(NTHREADS, 1)
+// NTMA TMA warps (0 .. NTMA - 1), then the MMA warp, then the softmax warps.
+template <int NTMA>
+__global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     mla_chunk_kernel(const MlaArgs a, const int32_t* __restrict__ q_pos, const __grid_constant__ ChunkMaps maps,
-                     const int box_rows, const int page_shift) {
+                     const int box_rows, const FastDiv page_div) {
+  constexpr int WARP_MMA = NTMA, SM_WARP0 = NTMA + 1, NTHREADS = (SM_WARP0 + SM_WARPS) * 32;
+  static_assert(SM_WARP0 % 4 == 0, "a softmax warp's TMEM lanes are those of its warp number modulo 4");
   extern __shared__ unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* red_s = reinterpret_cast<float*>(smem + OFF_RED);
   float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
   int* resc_s = reinterpret_cast<int*>(smem + OFF_FLAG);
   int* qexp_s = resc_s + 4;
-  float* smax_s = reinterpret_cast<float*>(resc_s + 8);  // [4] a tile's row parts' largest scales
+  volatile int* vote_s = resc_s + 8;                     // [4] by tile: some reference or E must move
+  float* srow = reinterpret_cast<float*>(smem + OFF_SROW);
+  uint2* info = reinterpret_cast<uint2*>(smem + OFF_INFO);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
   auto bar = [&](int b) { return smem_u32(bars + b); };
@@ -129,7 +148,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const int P = a.page_size;
   const int32_t r = __shfl_sync(0xffffffffu, a.q_req[i], 0), last = __shfl_sync(0xffffffffu, q_pos[i], 0);
   const bool req_ok = r >= 0 && r < a.num_req;
-  const bool pos_ok = last >= -1 && last <= INT32_MAX - T && last / P < a.bt_stride;
+  const bool pos_ok = last >= -1 && last <= INT32_MAX - T && page_div(max(last, 0)) < a.bt_stride;
   if (tid == 0) {
     if (!req_ok && r != -1) report(a.dev_status, DSA_DEV_BAD_PAGE);
     if (req_ok && !pos_ok) report(a.dev_status, DSA_DEV_BAD_QPOS);
@@ -169,6 +188,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     mbar_init(bar(B_FIN), 1);
     mbar_init(bar(B_QREADY), SM_WARPS);
     mbar_init(bar(B_QLOAD), 1);
+    mbar_init(bar(B_VOTE), SM_WARPS);
+    for (int u = 0; u < 4; ++u) vote_s[u] = 0;
     fence_mbarrier_init();
     tma_prefetch_map(&maps.lat_box);
     tma_prefetch_map(&maps.rope_box);
@@ -182,11 +203,10 @@ __global__ void __launch_bounds__(NTHREADS, 1)
   const uint32_t kv_base = smem_u32(smem + OFF_KV), qr_base = smem_u32(smem + OFF_QR), p_base = smem_u32(smem + OFF_P);
   bool ok = true;
   const int32_t* bt = a.block_table + (int64_t)r * a.bt_stride;
-  // the cache row of a visible position; -1: its page does not exist
-  auto slot_of = [&](int pos) -> int {
-    const int pg = page_shift >= 0 ? pos >> page_shift : pos / P;
-    const int page = __ldg(bt + pg);
-    return page >= 0 && page < a.num_pages ? page * P + (pos - pg * P) : -1;
+  // the page id of a visible position, and the position's cache row (-1: no such page)
+  auto page_of = [&](int pos) -> int { return __ldg(bt + page_div(pos)); };
+  auto slot_in = [&](int page, int pos) -> int {
+    return page >= 0 && page < a.num_pages ? page * P + (pos - page_div(pos) * P) : -1;
   };
 
   if (warp < NTMA) {
@@ -217,32 +237,46 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     const Deal db = deal(box_rows > 0 ? box_rows : 4), dg = deal(4);
     const int past = (int)(a.num_pages * P);  // a row past the pool: reads as zeros
     auto boxed = [&](int lt) { return box_rows > 0 && (t_begin + lt + 1) * T <= n; };
-    // the cache rows of this lane's group of tile lt (a box: the first one's, in x)
-    auto rows_of = [&](int lt) -> int4 {
-      int4 v = make_int4(past, past, past, past);
+    // Everything a tile needs is loaded long before it is used, so that no
+    // round trip to L2 sits in the loop: the page ids of tile lt + 3, then, an
+    // iteration later, the scales behind them.
+    // Page ids of this lane's copy of tile lt (a box: the first row's, in x).
+    auto pages_of = [&](int lt) -> int4 {
+      int4 v = make_int4(-1, -1, -1, -1);
       if (lt >= ntl) return v;
       const int base = (t_begin + lt) * T;
       if (boxed(lt)) {
-        if (db.has) {
-          const int s = slot_of(base + db.g * box_rows);
-          v.x = s >= 0 ? s : past;
-        }
+        if (db.has) v.x = page_of(base + db.g * box_rows);
       } else if (dg.has) {
-        int s[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int pos = base + 4 * dg.g + q;
-          s[q] = pos < n ? slot_of(pos) : -1;
-        }
-        v = make_int4(s[0], s[1], s[2], s[3]);
+        const int pos = base + 4 * dg.g;
+        if (pos < n) v.x = page_of(pos);
+        if (pos + 1 < n) v.y = page_of(pos + 1);
+        if (pos + 2 < n) v.z = page_of(pos + 2);
+        if (pos + 3 < n) v.w = page_of(pos + 3);
       }
       return v;
     };
+    // Warps 0 and 1 also look up the scales of a tile's rows 32 warp + lane.
+    auto row_pos = [&](int lt) { return (t_begin + lt) * T + 32 * warp + lane; };
+    auto row_page = [&](int lt) { return warp < 2 && lt < ntl && row_pos(lt) < n ? page_of(row_pos(lt)) : -1; };
+    auto row_slot = [&](int lt, int page) -> int {
+      if (warp > 1 || lt >= ntl || row_pos(lt) >= n) return -1;
+      const int s = slot_in(page, row_pos(lt));
+      if (s < 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
+      return s;
+    };
+    auto row_scale = [&](int slot) -> float { return slot >= 0 ? __ldg(a.kv_scale + slot) : 0.f; };
     int issued = 0;
-    int4 rows_cur = rows_of(0), rows_nxt = rows_of(1);
+    int4 pg0 = pages_of(0), pg1 = pages_of(1), pg2 = pages_of(2);
+    int rp2 = row_page(2);
+    int slot0 = row_slot(0, row_page(0)), slot1 = row_slot(1, row_page(1));
+    float sc0 = row_scale(slot0), sc1 = row_scale(slot1);
     for (int lt = 0; lt < ntl; ++lt) {
       const int s = lt % NST;
-      const int4 rows_far = rows_of(lt + 2);
+      const int4 pg3 = pages_of(lt + 3);
+      const int rp3 = row_page(lt + 3);
+      const int slot2 = row_slot(lt + 2, rp2);
+      const float sc2 = row_scale(slot2);
       if (lt >= NST && !wait_warp(B_KVE + s, ((lt - NST) / NST) & 1)) {
         ok = false;
         break;
@@ -251,32 +285,45 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         ok = false;
         break;
       }
+      if (warp < 2) {
+        const unsigned valid = __ballot_sync(0xffffffffu, slot0 >= 0);
+        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sc0)));
+        srow[s * T + 32 * warp + lane] = sc0;
+        if (lane == 0) info[s * 2 + warp] = make_uint2(valid, top);
+        __syncwarp();
+      }
       const uint32_t dst = kv_base + s * STAGE_BYTES;
       const bool bx = boxed(lt);
       if (lane == 0) mbar_arrive_expect_tx(bar(B_KVF + s), bx ? db.bytes : dg.bytes);
       __syncwarp();
+      const int base = (t_begin + lt) * T;
       if (bx) {
         if (db.has) {
+          const int row0 = slot_in(pg0.x, base + db.g * box_rows), y = row0 >= 0 ? row0 : past;
           if (db.part < NLAT)
-            tma_load_2d(dst + db.part * LAT_BYTES + db.g * box_rows * 128, &maps.lat_box, db.part * 128, rows_cur.x,
-                        bar(B_KVF + s));
+            tma_load_2d(dst + db.part * LAT_BYTES + db.g * box_rows * 128, &maps.lat_box, db.part * 128, y, bar(B_KVF + s));
           else
-            tma_load_2d(dst + ROPE_OFF + db.g * box_rows * DR, &maps.rope_box, DL, rows_cur.x, bar(B_KVF + s));
+            tma_load_2d(dst + ROPE_OFF + db.g * box_rows * DR, &maps.rope_box, DL, y, bar(B_KVF + s));
         }
-      } else if (dg.has) {
+      } else if (dg.has) {  // (page -1 past the last position: row -1)
+        const int pos = base + 4 * dg.g;
+        const int4 rows = make_int4(slot_in(pg0.x, pos), slot_in(pg0.y, pos + 1), slot_in(pg0.z, pos + 2),
+                                    slot_in(pg0.w, pos + 3));
         if (dg.part < NLAT)
-          tma_gather4(dst + dg.part * LAT_BYTES + dg.g * 512, &maps.lat_row, dg.part * 128, rows_cur, bar(B_KVF + s));
+          tma_gather4(dst + dg.part * LAT_BYTES + dg.g * 512, &maps.lat_row, dg.part * 128, rows, bar(B_KVF + s));
         else
-          tma_gather4(dst + ROPE_OFF + dg.g * 256, &maps.rope_row, DL, rows_cur, bar(B_KVF + s));
+          tma_gather4(dst + ROPE_OFF + dg.g * 256, &maps.rope_row, DL, rows, bar(B_KVF + s));
       }
-      rows_cur = rows_nxt;
-      rows_nxt = rows_far;
+      pg0 = pg1, pg1 = pg2, pg2 = pg3;
+      rp2 = rp3;
+      slot0 = slot1, slot1 = slot2;
+      sc0 = sc1, sc1 = sc2;
       issued = lt + 1;
     }
     // no copy may land after the CTA is gone
     for (int lt = issued > NST ? issued - NST : 0; lt < issued; ++lt)
       if (!wait_warp(B_KVF + lt % NST, (lt / NST) & 1)) ok = false;
-    if (tid < 32 && !wait_warp(B_QLOAD, 0)) ok = false;
+    if (warp == 0 && !wait_warp(B_QLOAD, 0)) ok = false;
     if (!ok && lane == 0) report(a.dev_status, DSA_DEV_TIMEOUT);
   } else if (warp == WARP_MMA) {
     // ---------------- MMA warp ----------------
@@ -388,7 +435,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         *qexp_s = fin ? 8 - e : 0;
       }
       group_sync();
-      const float qs = ldexpf(1.f, *qexp_s);
+      // (a negative softmax scale is Q's sign)
+      const float qs = copysignf(ldexpf(1.f, *qexp_s), a.softmax_scale);
       auto split8 = [&](const uint4 v, uint2& hv, uint2& lv) {  // 8 elements as byte quadruples
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
@@ -437,7 +485,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_QREADY));
     }
-    const float qk_scale = a.softmax_scale * LOG2E * ldexpf(1.f, -*qexp_s);
+    // logit (log2 domain) = (S_hi + S_lo) s_j qk_scale; qk_scale > 0 keeps -inf of a masked row
+    const float qk_scale = fmaxf(fabsf(a.softmax_scale) * LOG2E * ldexpf(1.f, -*qexp_s), 1e-30f);
 
     // ---- the tiles ----
     float m_ref = -INFINITY;      // head hh's reference maximum (log2 domain), the same in its 8 threads
@@ -445,30 +494,16 @@ __global__ void __launch_bounds__(NTHREADS, 1)
     int p_exp = 0;                // E, the same in every thread; set at the first row with a scale
     float p_scale = 1.f;          // 2^E
     bool p_set = false;
-    float* rowf = reinterpret_cast<float*>(smem + OFF_ROWF) + sw * 2 * 32;
-    // lane's row of tile lt: 16 part + lane % 16
-    auto row_slot = [&](int lt) -> int {
-      const int pos = (t_begin + lt) * T + 16 * part + (lane & 15);
-      if (lt >= ntl || pos >= n) return -1;
-      const int s = slot_of(pos);
-      if (s < 0 && lane < 16 && q4 == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
-      return s;
-    };
-    auto row_scale = [&](int slot) -> float { return slot >= 0 ? __ldg(a.kv_scale + slot) : 0.f; };
-    int slot_c = row_slot(0), slot_n = row_slot(1);
-    float sc_c = row_scale(slot_c);
+    const uint64_t qk2 = pk2(qk_scale, qk_scale);
+    int stage = 0, kv_phase = 0;
     for (int lt = 0; lt < ntl; ++lt) {  // no early exit: every warp reaches every barrier
       const int sb = lt & 1;
-      const int slot_f = row_slot(lt + 2);
-      const float sc_n = row_scale(slot_n);
-      const unsigned vmask = __ballot_sync(0xffffffffu, slot_c >= 0);  // (twice the same 16 bits)
-      rowf[sb * 32 + lane] = lane < 16 ? sc_c * qk_scale : sc_c;
-      const float smax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sc_c))));
-      __syncwarp();
-      const float4* cf4 = reinterpret_cast<const float4*>(rowf + sb * 32 + 8 * up);
+      if (ok && !wait_warp(B_KVF + stage, kv_phase)) ok = false;  // (the row scales; landed before S is computed)
+      const float4* s4 = reinterpret_cast<const float4*>(srow + stage * T + 16 * part + 8 * up);
+      const uint2 inf = info[stage * 2 + (part >> 1)];
       if (ok && !wait_warp(B_SF + sb, (lt >> 1) & 1)) ok = false;
       tc_fence_after_sync();
-      float z[8];  // logits of head hh, rows 16 part + 8 up + c, in the log2 domain (invalid: -inf)
+      float z[8];  // (S_hi + S_lo) s_j of head hh, rows 16 part + 8 up + c (invalid: -inf)
       {
         float v[16];
         tmem_ld16(t_lane + TM_S + T * sb + 16 * part, v);
@@ -478,7 +513,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         for (int c = 0; c < 8; ++c) got[c] = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[8 + c], 16);
 #pragma unroll
         for (int k4 = 0; k4 < 2; ++k4) {
-          const float4 f = cf4[k4];
+          const float4 f = s4[k4];
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             const int c = 4 * k4 + 2 * t;
@@ -486,8 +521,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
             upk2(mul2(add2(mine, pk2(got[c], got[c + 1])), t ? pk2(f.z, f.w) : pk2(f.x, f.y)), z[c], z[c + 1]);
           }
         }
-        if (vmask != 0xffffffffu) {
-          const unsigned my_valid = vmask >> (8 * up);
+        if (inf.x != 0xffffffffu) {  // a tile with rows past the last position, or bad pages
+          const unsigned my_valid = inf.x >> (16 * (part & 1) + 8 * up);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             if (!((my_valid >> c) & 1u)) z[c] = -INFINITY;
@@ -496,16 +531,48 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       float tm = z[0];
 #pragma unroll
       for (int c = 1; c < 8; ++c) tm = fmaxf(tm, z[c]);
-      // one vote of all softmax threads: does a logit pass its head's
-      // reference, or a row's scale the bound of E?
+      // Does a logit pass its head's reference, or a scale E's bound?  Every
+      // warp says so and goes on as if none did; the weights are computed again
+      // in the rare tile where some warp's answer was yes.
+      const float smax = __uint_as_float(inf.y);
       const bool grow = p_set ? smax * p_scale >= SCALE_BOUND : smax > 0.f;
-      if (named_barrier_or(3, SM_THREADS, grow || tm > m_ref + EXCEED_LOG2)) {
+      const bool want = __any_sync(0xffffffffu, grow || fmaf(tm, qk_scale, -m_ref) > EXCEED_LOG2);
+      if (lane == 0) {
+        if (want) vote_s[lt & 3] = 1;
+        mbar_arrive(bar(B_VOTE));
+      }
+      uint32_t phi[4], plo[4];
+      uint64_t ln;
+      for (bool again = false;; again = true) {
+        // weights, folded with the row's scale and 2^E, as E4M3 + E5M2
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
+        const uint64_t nm2 = pk2(-m_use, -m_use), ps2 = pk2(p_scale, p_scale);
+        ln = l2;
+#pragma unroll
+        for (int k4 = 0; k4 < 2; ++k4) {
+          const float4 f = s4[k4];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int c = 4 * k4 + 2 * t;
+            float d0, d1;
+            upk2(fma2(pk2(z[c], z[c + 1]), qk2, nm2), d0, d1);
+            const uint64_t p = pk2(ex2(d0), ex2(d1));
+            ln = add2(ln, p);
+            float w0, w1;
+            upk2(mul2(p, mul2(t ? pk2(f.z, f.w) : pk2(f.x, f.y), ps2)), w0, w1);
+            split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
+          }
+        }
+        if (again) break;
+        if (!mbar_wait(bar(B_VOTE), lt & 1, 4 * MBAR_LIMIT_NS)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);
+        if (vote_s[lt & 3] == 0) break;
+        // ---- move the references that were passed, and E; rescale O and l ----
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-        if (up == 0) red_s[part * H + hh] = tm;
-        if (q4 == 0 && lane == 0) smax_s[part] = smax;
+        if (up == 0) red_s[part * H + hh] = tm * qk_scale;
         group_sync();
         const float mt = fmaxf(fmaxf(red_s[hh], red_s[H + hh]), fmaxf(red_s[2 * H + hh], red_s[3 * H + hh]));
-        const float sm = fmaxf(fmaxf(smax_s[0], smax_s[1]), fmaxf(smax_s[2], smax_s[3]));
+        const float sm = fmaxf(__uint_as_float(info[stage * 2].y), __uint_as_float(info[stage * 2 + 1].y));
         float alpha = 1.f;
         if (mt > m_ref + EXCEED_LOG2) {
           alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mt);
@@ -514,7 +581,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
         l2 = mul2(l2, pk2(alpha, alpha));
         if (sm > 0.f && sm <= 3.0e38f && (!p_set || sm * p_scale >= SCALE_BOUND)) {
           int e2;
-          frexpf(sm, &e2);         // sm < 2^e2: sm 2^E in [16, 32)
+          frexpf(sm, &e2);  // sm < 2^e2: sm 2^E in [16, 32)
           const int e = min(5 - e2, 120);  // (2^E stays finite for subnormal scales)
           if (p_set) alpha *= ldexpf(1.f, e - p_exp);  // O carries 2^E
           p_exp = e;
@@ -543,26 +610,7 @@ __global__ void __launch_bounds__(NTHREADS, 1)
           tmem_wait_st();
         }
       }
-      // weights, folded with the row's scale and 2^E, as E4M3 + E5M2
-      uint32_t phi[4], plo[4];
-      const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-      const uint64_t nm2 = pk2(-m_use, -m_use), ps2 = pk2(p_scale, p_scale);
-      const float4* sf4 = reinterpret_cast<const float4*>(rowf + sb * 32 + 16 + 8 * up);
-#pragma unroll
-      for (int k4 = 0; k4 < 2; ++k4) {
-        const float4 f = sf4[k4];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int c = 4 * k4 + 2 * t;
-          float d0, d1;
-          upk2(add2(pk2(z[c], z[c + 1]), nm2), d0, d1);
-          const uint64_t p = pk2(ex2(d0), ex2(d1));
-          l2 = add2(l2, p);
-          float w0, w1;
-          upk2(mul2(p, mul2(t ? pk2(f.z, f.w) : pk2(f.x, f.y), ps2)), w0, w1);
-          split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
-        }
-      }
+      l2 = ln;
       // P buffer lt % 2 was last read by P V(lt - 2), issued before QK^T(lt): the
       // commit that completed S(lt) tracks it, so the buffer is free
       {
@@ -574,8 +622,11 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_PF + lt % NPB));
-      slot_c = slot_n, slot_n = slot_f;
-      sc_c = sc_n;
+      // Tile lt + 2's vote starts from 0: every warp has read tile lt - 2's
+      // answer here, and none sets lt + 2's before this warp reaches lt + 1's vote
+      if (st == 0) vote_s[(lt + 2) & 3] = 0;
+      if (stage == NST - 1) stage = 0, kv_phase ^= 1;
+      else ++stage;
     }
     // ---------------- epilogue ----------------
     if (ok && !wait_warp(B_FIN, 0)) ok = false;
@@ -639,9 +690,6 @@ cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, cudaStream_t
   int box = T;
   while (box >= 8 && a.page_size % box != 0) box /= 2;
   if (box < 8) box = 0;
-  int shift = -1;
-  for (int s = 0; s < 31; ++s)
-    if (a.page_size == (1 << s)) shift = s;
   ChunkMaps maps;
   const uint32_t rows = box > 0 ? box : 1;
   if (!make_kv_map(&maps.lat_box, a, DQK, 128, rows, CU_TENSOR_MAP_SWIZZLE_128B) ||
@@ -649,10 +697,18 @@ cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, cudaStream_t
       !make_kv_map(&maps.lat_row, a, DQK, 128, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_kv_map(&maps.rope_row, a, DQK, DR, 1, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(mla_chunk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (e != cudaSuccess) return e;
-  mla_chunk_kernel<<<dim3(a.num_q, a.num_splits), NTHREADS, SMEM_BYTES, stream>>>(a, q_pos, maps, box, shift);
-  return cudaGetLastError();
+  // Three TMA warps keep up with boxes of 16 rows or more (5 to 20 copies a
+  // tile; seven draw power for nothing: 1.85 against 1.80 ms on 1,024 tokens of
+  // 16,384); smaller ones need seven (page size 4: 410 against 500 us, page size 24:
+  // 2.48 against 2.62 ms).
+  auto launch = [&](auto kern, int ntma) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3(a.num_q, a.num_splits), (ntma + 1 + SM_WARPS) * 32, SMEM_BYTES, stream>>>(a, q_pos, maps, box,
+                                                                                         make_fast_div(a.page_size));
+    return cudaGetLastError();
+  };
+  return box >= 16 ? launch(mla_chunk_kernel<3>, 3) : launch(mla_chunk_kernel<7>, 7);
 }
 
 }  // namespace dsa
