@@ -138,9 +138,17 @@ def _p(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+# The current stream's handle without a Stream object (2.8 us less per call on a
+# Grace host), where this torch has the call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _check(t: torch.Tensor, name: str, dtype, ndim: int | None = None):
@@ -474,37 +482,74 @@ def sparse_mla_topk(q, kv, kv_scale, block_table, q_req, q_pos, scores, k: int, 
 
 
 # ---- the rest of a serving step --------------------------------------------------
+#
+# These calls are a few microseconds of GPU work in a decode step, so their
+# checks are written for the host's time as well: one pass over a tensor's
+# attributes, no wrapper objects, outputs cut from few allocations.
+
+_I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 
 
-def _check_all(dev: torch.device, *named):
-    """(tensor or None, name, dtype, ndim) each: as _check, and on ``dev``."""
-    for t, name, dtype, ndim in named:
-        if t is not None:
-            _check(t, name, dtype, ndim)
-            if t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, expected {dev}")
+def _need(t, name: str, dtype, ndim: int, dev: int):
+    """A contiguous CUDA tensor of this type and rank on device ``dev``."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev >= 0 and t.dim() == ndim and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _check(t, name, dtype, ndim)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
 
 
-def _check_shape(t, name: str, shape: tuple):
-    if t is not None and tuple(t.shape) != shape:
+def _need_rows(t, name: str, dtype, ndim: int, dev: int):
+    """As _need, but only the last dimension has to be contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" + (f" on cuda:{dev}, got {t.device}" if dev >= 0 else ""))
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims, got {t.dim()}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+
+
+def _need_shape(t, name: str, shape: tuple):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
-def _call_on(dev: torch.device, fn: str, stream, *args):
-    """_call with the tensors' device current (its current stream when none is given)."""
-    if dev.index == torch.cuda.current_device():
-        _call(fn, *args, _stream(stream))
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _run(dev: int, stream, fn: str, *args):
+    """Calls ``fn`` with the tensors' device current, on its current stream when
+    none is given."""
+    lib = _lib or load_library()
+    if dev == torch.cuda.current_device():
+        st = getattr(lib, fn)(*args, _stream(stream))
     else:
         with torch.cuda.device(dev):
-            _call(fn, *args, _stream(stream))
+            st = getattr(lib, fn)(*args, _stream(stream))
+    if st != 0:
+        raise DsaError(fn, st)
 
 
-def _status_arg(dev_status, dev):
-    if dev_status is not None:
-        _check_all(dev, (dev_status, "dev_status", torch.int32, None))
-        if dev_status.numel() < 1:
-            raise ValueError("dev_status needs one element")
-    return _p(dev_status)
+def _status_ptr(dev_status, dev: int):
+    if dev_status is None:
+        return None
+    _need(dev_status, "dev_status", _I32, dev_status.dim(), dev)
+    if dev_status.numel() < 1:
+        raise ValueError("dev_status needs one element")
+    return dev_status.data_ptr()
+
+
+def _device_of(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    return t.get_device()
 
 
 def _overlap(a: torch.Tensor, b: torch.Tensor) -> bool:
@@ -538,47 +583,43 @@ def batch_layout(ctx_len: torch.Tensor, new_len: torch.Tensor, pages_held: torch
     """A step's token ranges, slot map and grown block tables from the
     requests' lengths (dsa_batch_layout): ``block_table`` gets the new pages in
     place, everything else is returned.  ``out`` (a BatchLayout of
-    preallocated tensors, not the inputs) is written when given."""
-    dev = ctx_len.device
-    R = ctx_len.shape[0] if ctx_len.dim() == 1 else -1
-    _check_all(dev, (ctx_len, "ctx_len", torch.int32, 1), (new_len, "new_len", torch.int32, 1),
-               (pages_held, "pages_held", torch.int32, 1), (block_table, "block_table", torch.int32, 2),
-               (free_pages, "free_pages", torch.int32, 1), (free_used, "free_used", torch.int32, 1))
+    preallocated tensors, not the inputs) is written when given; without it
+    the returned tensors share one allocation."""
+    dev = _device_of(ctx_len, "ctx_len")
+    _need(ctx_len, "ctx_len", _I32, 1, dev)
+    _need(new_len, "new_len", _I32, 1, dev)
+    _need(pages_held, "pages_held", _I32, 1, dev)
+    _need(block_table, "block_table", _I32, 2, dev)
+    _need(free_pages, "free_pages", _I32, 1, dev)
+    _need(free_used, "free_used", _I32, 1, dev)
+    R = ctx_len.shape[0]
     if new_len.shape[0] != R or pages_held.shape[0] != R or block_table.shape[0] != R or free_used.shape[0] != 1:
         raise ValueError("inconsistent shapes")
     if capacity < 0:
         raise ValueError("capacity must not be negative")
     if out is None:
-        # one allocation: the token arrays first (each a multiple of 16 bytes apart)
-        cap = (capacity + 3) // 4 * 4
-        buf = torch.empty(3 * cap + 3 * R + 2, dtype=torch.int32, device=dev)
-        t = 3 * cap
-        out = BatchLayout(buf[t:t + R + 1], buf[:capacity], buf[cap:cap + capacity], buf[2 * cap:2 * cap + capacity],
-                          buf[t + R + 1:t + 2 * R + 1], buf[t + 2 * R + 1:t + 3 * R + 1], buf[t + 3 * R + 1:])
+        # the token arrays first, a multiple of 16 bytes apart
+        cap = (capacity + 3) & -4
+        buf = torch.empty(3 * cap + 3 * R + 2, dtype=_I32, device=ctx_len.device)
+        q_req, q_pos, slot, cu, ctx, held, used = buf.split_with_sizes((cap, cap, cap, R + 1, R, R, 1))
+        if cap != capacity:
+            q_req, q_pos, slot = q_req[:capacity], q_pos[:capacity], slot[:capacity]
+        out = BatchLayout(cu, q_req, q_pos, slot, ctx, held, used)
+        p = buf.data_ptr()
+        c = p + 12 * cap
+        ptrs = (c, p, p + 4 * cap, p + 8 * cap, c + 4 * R + 4, c + 8 * R + 4, c + 12 * R + 4)
     else:
         for x, name, n in zip(out, BatchLayout._fields, (R + 1, capacity, capacity, capacity, R, R, 1)):
-            _check_all(dev, (x, "out." + name, torch.int32, 1))
-            _check_shape(x, "out." + name, (n,))
-    _call_on(dev, "dsa_batch_layout", stream, _p(ctx_len), _p(new_len), _p(pages_held), R, _p(block_table),
-             block_table.shape[1], _p(free_pages), free_pages.shape[0], _p(free_used), page_size, num_pages, capacity,
-             _p(out.cu_q), _p(out.q_req), _p(out.q_pos), _p(out.slot), _p(out.ctx_len), _p(out.pages_held),
-             _p(out.free_used), _status_arg(dev_status, dev))
+            _need(x, "out." + name, _I32, 1, dev)
+            _need_shape(x, "out." + name, (n,))
+        ptrs = [x.data_ptr() for x in out]
+    _run(dev, stream, "dsa_batch_layout", ctx_len.data_ptr(), new_len.data_ptr(), pages_held.data_ptr(), R,
+         block_table.data_ptr(), block_table.shape[1], free_pages.data_ptr(), free_pages.shape[0], free_used.data_ptr(),
+         page_size, num_pages, capacity, *ptrs, _status_ptr(dev_status, dev))
     return out
 
 
 _ROW_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
-
-
-def _rows(x, name: str, dev, dtype, d: int):
-    """Checks rows [tokens, heads, d] whose last dimension is contiguous."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if not x.is_cuda or x.device != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-    if x.dim() != 3 or x.shape[2] != d or (d > 1 and x.stride(2) != 1):
-        raise ValueError(f"{name} must be [tokens, heads, {d}] with a contiguous last dimension")
 
 
 def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tensor | None,
@@ -595,50 +636,80 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
     None, or keys that only go into the cache, give None.  Tokens with pos =
     -1 are left as they were."""
     some = q if q is not None else k
-    if not isinstance(some, torch.Tensor) or some.dim() != 3:
-        raise ValueError("q or k must be a [tokens, heads, d] tensor")
-    dev, dtype = some.device, some.dtype
-    n, d = some.shape[0], some.shape[2]
-    if dtype not in _ROW_DTYPES:
+    if some is None:
+        raise ValueError("q or k must be given")
+    dev = _device_of(some, "q or k")
+    dtype = some.dtype
+    code = _ROW_DTYPES.get(dtype)
+    if code is None:
         raise TypeError(f"rows must be bfloat16 or float16, got {dtype}")
-    for x, name in ((q, "q"), (k, "k")):
-        if x is not None:
-            _rows(x, name, dev, dtype, d)
-            if x.shape[0] != n:
-                raise ValueError("q and k must have the same number of tokens")
+    qh = kh = qn = kn = qst = qsh = kst = ksh = slots = 0
+    qp = kp = qwp = kwp = qop = kop = None
+    if some.dim() != 3:
+        raise ValueError("rows must be [tokens, heads, d]")
+    n, _, d = some.shape
     cache = slot is not None or kv is not None or kv_scale is not None
-    if cache and (slot is None or kv is None or kv_scale is None or k is None):
-        raise ValueError("the cache write needs k, slot, kv and kv_scale")
-    _check_all(dev, (pos, "pos", torch.int32, 1), (cos_sin, "cos_sin", torch.float32, 2),
-               (q_weight, "q_weight", torch.float32, 1), (k_weight, "k_weight", torch.float32, 1),
-               (slot, "slot", torch.int32, 1), (kv, "kv", torch.uint8, 2), (kv_scale, "kv_scale", torch.float32, 1),
-               (q_out, "q_out", dtype, 3), (k_out, "k_out", dtype, 3))
+    given = q_out is not None or k_out is not None
+    if q is not None:
+        _need_rows(q, "q", dtype, 3, dev)
+        qp, qh = q.data_ptr(), q.shape[1]
+        qst, qsh, _ = q.stride()
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+        else:
+            _need(q_out, "q_out", dtype, 3, dev)
+            _need_shape(q_out, "q_out", q.shape)
+        qop = q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if k is not None:
+        _need_rows(k, "k", dtype, 3, dev)
+        if k.shape[0] != n or k.shape[2] != d:
+            raise ValueError("q and k must have the same tokens and row sizes")
+        kp, kh = k.data_ptr(), k.shape[1]
+        kst, ksh, _ = k.stride()
+        if k_out is not None:
+            _need(k_out, "k_out", dtype, 3, dev)
+            _need_shape(k_out, "k_out", k.shape)
+        elif not cache:
+            k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+        kop = None if k_out is None else k_out.data_ptr()
+    elif k_out is not None or cache:
+        raise ValueError("k_out or a cache write without k")
+    if q_weight is not None:
+        _need(q_weight, "q_weight", _F32, 1, dev)
+        qwp, qn = q_weight.data_ptr(), q_weight.shape[0]
+    if k_weight is not None:
+        _need(k_weight, "k_weight", _F32, 1, dev)
+        kwp, kn = k_weight.data_ptr(), k_weight.shape[0]
+    max_pos = 0
+    if cos_sin is not None:
+        _need(cos_sin, "cos_sin", _F32, 2, dev)
+        max_pos = cos_sin.shape[0]
+    if pos is not None:
+        _need(pos, "pos", _I32, 1, dev)
     if d_rope and (pos is None or cos_sin is None or cos_sin.shape[1] != d_rope):
         raise ValueError("a rotation needs pos and cos_sin [max_pos, d_rope]")
-    if pos is not None and pos.shape[0] != n or cache and slot.shape[0] != n:
-        raise ValueError("inconsistent shapes")
-    if cache and (kv.shape[1] != d or kv_scale.shape[0] != kv.shape[0]):
-        raise ValueError("kv must be [slots, d] and kv_scale [slots]")
-    if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=dtype, device=dev)
-    if k is not None and k_out is None and not cache:
-        k_out = torch.empty(k.shape, dtype=dtype, device=dev)
-    for o, name, own in ((q_out, "q_out", q), (k_out, "k_out", k)):
-        if o is None:
-            continue
-        if own is None:
-            raise ValueError(f"{name} without its input")
-        _check_shape(o, name, tuple(own.shape))
-        for x in (q, k):
-            if x is not None and _overlap(o, x) and not (x is own and o.data_ptr() == x.data_ptr() and x.is_contiguous()):
-                raise ValueError(f"{name} overlaps an input (in place needs its own, contiguous)")
-    qs, ks = (x.stride() if x is not None and x.numel() else (0, 0, 1) for x in (q, k))
-    _call_on(dev, "dsa_qk_norm_rope", stream, _p(q), qs[0], qs[1], 0 if q is None else q.shape[1], _p(q_weight),
-             0 if q_weight is None else q_weight.shape[0], _p(q_out), _p(k), ks[0], ks[1],
-             0 if k is None else k.shape[1], _p(k_weight), 0 if k_weight is None else k_weight.shape[0], _p(k_out), n, d,
-             d_rope, _ROW_DTYPES[dtype], _p(pos), _p(cos_sin), 0 if cos_sin is None else cos_sin.shape[0], float(eps),
-             1 if interleaved else 0, _p(slot), _p(kv), _p(kv_scale), kv.shape[0] if cache else 0,
-             _status_arg(dev_status, dev))
+    if pos is not None and pos.shape[0] != n:
+        raise ValueError("pos must have one entry per token")
+    if cache:
+        if slot is None or kv is None or kv_scale is None:
+            raise ValueError("the cache write needs slot, kv and kv_scale")
+        _need(slot, "slot", _I32, 1, dev)
+        _need(kv, "kv", _U8, 2, dev)
+        _need(kv_scale, "kv_scale", _F32, 1, dev)
+        slots = kv.shape[0]
+        if slot.shape[0] != n or kv.shape[1] != d or kv_scale.shape[0] != slots:
+            raise ValueError("slot must be [tokens], kv [slots, d] and kv_scale [slots]")
+    if given:
+        for o, own, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+            for x in (q, k):
+                if o is not None and x is not None and _overlap(o, x) and not (
+                        x is own and o.data_ptr() == x.data_ptr() and x.is_contiguous()):
+                    raise ValueError(f"{name} overlaps an input (in place needs its own, contiguous)")
+    _run(dev, stream, "dsa_qk_norm_rope", qp, qst, qsh, qh, qwp, qn, qop, kp, kst, ksh, kh, kwp, kn, kop, n, d, d_rope,
+         code, _ptr(pos), _ptr(cos_sin), max_pos, float(eps), 1 if interleaved else 0, _ptr(slot), _ptr(kv), _ptr(kv_scale),
+         slots, _status_ptr(dev_status, dev))
     return q_out, k_out
 
 
@@ -648,35 +719,47 @@ def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, 
     """Attention of each token to all positions 0..q_pos of its request
     (dsa_chunk_mla_fwd).  num_splits == 1: returns (out bf16, lse fp32).
     num_splits > 1: returns (o_part fp32 [S, ...], lse_part fp32 [S, ...])."""
-    dev = q.device
-    _check_all(dev, (q, "q", torch.bfloat16, 3), (kv, "kv", torch.uint8, 2), (kv_scale, "kv_scale", torch.float32, 1),
-               (block_table, "block_table", torch.int32, 2), (q_req, "q_req", torch.int32, 1),
-               (q_pos, "q_pos", torch.int32, 1), (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2),
-               (o_part, "o_part", torch.float32, 4), (lse_part, "lse_part", torch.float32, 3))
+    dev = _device_of(q, "q")
+    _need(q, "q", _BF16, 3, dev)
+    _need(kv, "kv", _U8, 2, dev)
+    _need(kv_scale, "kv_scale", _F32, 1, dev)
+    _need(block_table, "block_table", _I32, 2, dev)
+    _need(q_req, "q_req", _I32, 1, dev)
+    _need(q_pos, "q_pos", _I32, 1, dev)
     num_q, H, dqk = q.shape
-    if dqk != d_latent + d_rope or kv.shape[1] != dqk or page_size <= 0 or kv.shape[0] % page_size:
+    slots = kv.shape[0]
+    if dqk != d_latent + d_rope or kv.shape[1] != dqk or page_size <= 0 or slots % page_size:
         raise ValueError("q / kv row sizes do not match d_latent + d_rope, or kv is not whole pages")
-    if q_req.shape[0] != num_q or q_pos.shape[0] != num_q or kv_scale.shape[0] != kv.shape[0]:
+    if q_req.shape[0] != num_q or q_pos.shape[0] != num_q or kv_scale.shape[0] != slots:
         raise ValueError("inconsistent shapes")
+    op = lp = oo = ll = None
     if num_splits == 1:
         if out is None:
-            out = torch.empty((num_q, H, d_latent), dtype=torch.bfloat16, device=dev)
+            out = torch.empty((num_q, H, d_latent), dtype=_BF16, device=q.device)
+        else:
+            _need(out, "out", _BF16, 3, dev)
+            _need_shape(out, "out", (num_q, H, d_latent))
         if lse is None:
-            lse = torch.empty((num_q, H), dtype=torch.float32, device=dev)
-        _check_shape(out, "out", (num_q, H, d_latent))
-        _check_shape(lse, "lse", (num_q, H))
-        ptrs = (_p(out), _p(lse), None, None)
+            lse = torch.empty((num_q, H), dtype=_F32, device=q.device)
+        else:
+            _need(lse, "lse", _F32, 2, dev)
+            _need_shape(lse, "lse", (num_q, H))
+        oo, ll = out.data_ptr(), lse.data_ptr()
     else:
         if o_part is None:
-            o_part = torch.empty((num_splits, num_q, H, d_latent), dtype=torch.float32, device=dev)
+            o_part = torch.empty((num_splits, num_q, H, d_latent), dtype=_F32, device=q.device)
+        else:
+            _need(o_part, "o_part", _F32, 4, dev)
+            _need_shape(o_part, "o_part", (num_splits, num_q, H, d_latent))
         if lse_part is None:
-            lse_part = torch.empty((num_splits, num_q, H), dtype=torch.float32, device=dev)
-        _check_shape(o_part, "o_part", (num_splits, num_q, H, d_latent))
-        _check_shape(lse_part, "lse_part", (num_splits, num_q, H))
-        ptrs = (None, None, _p(o_part), _p(lse_part))
-    _call_on(dev, "dsa_chunk_mla_fwd", stream, _p(q), _p(kv), _p(kv_scale), kv.shape[0] // page_size, _p(block_table),
-             block_table.shape[0], block_table.shape[1], _p(q_req), _p(q_pos), num_q, H, d_latent, d_rope, page_size,
-             float(softmax_scale), num_splits, *ptrs, _status_arg(dev_status, dev))
+            lse_part = torch.empty((num_splits, num_q, H), dtype=_F32, device=q.device)
+        else:
+            _need(lse_part, "lse_part", _F32, 3, dev)
+            _need_shape(lse_part, "lse_part", (num_splits, num_q, H))
+        op, lp = o_part.data_ptr(), lse_part.data_ptr()
+    _run(dev, stream, "dsa_chunk_mla_fwd", q.data_ptr(), kv.data_ptr(), kv_scale.data_ptr(), slots // page_size,
+         block_table.data_ptr(), block_table.shape[0], block_table.shape[1], q_req.data_ptr(), q_pos.data_ptr(), num_q,
+         H, d_latent, d_rope, page_size, float(softmax_scale), num_splits, oo, ll, op, lp, _status_ptr(dev_status, dev))
     return (out, lse) if num_splits == 1 else (o_part, lse_part)
 
 
@@ -695,23 +778,27 @@ def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_ro
         if max_ctx is None:
             max_ctx = block_table.shape[1] * page_size
         num_splits = pick_num_splits(num_q, H, d_latent, d_rope, max(1, max_ctx))
-    r = chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
-                      page_size=page_size, softmax_scale=softmax_scale, num_splits=num_splits,
-                      out=b.get("out") if num_splits == 1 else None, lse=b.get("lse") if num_splits == 1 else None,
-                      o_part=b.get("o_part"), lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)
-    if num_splits == 1 or num_q == 0:
-        return r if num_splits == 1 else (torch.empty((0, H, d_latent), dtype=torch.bfloat16, device=q.device),
-                                          torch.empty((0, H), dtype=torch.float32, device=q.device))
     out, lse = b.get("out"), b.get("lse")
-    dev = q.device
+    if num_splits == 1 or num_q == 0:
+        return chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
+                             page_size=page_size, softmax_scale=softmax_scale, out=out, lse=lse, dev_status=dev_status,
+                             stream=stream)
+    op, lp = chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
+                           page_size=page_size, softmax_scale=softmax_scale, num_splits=num_splits,
+                           o_part=b.get("o_part"), lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)
+    dev = q.get_device()
     if out is None:
-        out = torch.empty((num_q, H, d_latent), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((num_q, H, d_latent), dtype=_BF16, device=q.device)
+    else:
+        _need(out, "out", _BF16, 3, dev)
+        _need_shape(out, "out", (num_q, H, d_latent))
     if lse is None:
-        lse = torch.empty((num_q, H), dtype=torch.float32, device=dev)
-    _check_all(dev, (out, "out", torch.bfloat16, 3), (lse, "lse", torch.float32, 2))
-    _check_shape(out, "out", (num_q, H, d_latent))
-    _check_shape(lse, "lse", (num_q, H))
-    _call_on(dev, "dsa_combine", stream, _p(r[0]), _p(r[1]), num_splits, num_q, H, d_latent, _p(out), _p(lse))
+        lse = torch.empty((num_q, H), dtype=_F32, device=q.device)
+    else:
+        _need(lse, "lse", _F32, 2, dev)
+        _need_shape(lse, "lse", (num_q, H))
+    _run(dev, stream, "dsa_combine", op.data_ptr(), lp.data_ptr(), num_splits, num_q, H, d_latent, out.data_ptr(),
+         lse.data_ptr())
     return out, lse
 
 
@@ -723,42 +810,50 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
     given random numbers (dsa_verify_draft).  Returns (tokens int32 [num_req,
     max_out], -1 padded; num_out int32 [num_req]; ctx_out = ctx_len + num_out,
     or None without ctx_len)."""
-    dev = target_probs.device
-    for t, name in ((target_probs, "target_probs"), (draft_probs, "draft_probs")):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.float32:
-            raise TypeError(f"{name} must be a float32 tensor")
-        if not t.is_cuda or t.device != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on {dev}")
-        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-            raise ValueError(f"{name} must be [rows, vocab] with contiguous rows")
+    dev = _device_of(target_probs, "target_probs")
+    _need_rows(target_probs, "target_probs", _F32, 2, dev)
     rows, vocab = target_probs.shape
-    _check_all(dev, (draft_tokens, "draft_tokens", torch.int32, 1), (cu_rows, "cu_rows", torch.int32, 1),
-               (u_accept, "u_accept", torch.float32, 1), (u_sample, "u_sample", torch.float32, 1),
-               (ctx_len, "ctx_len", torch.int32, 1), (tokens, "tokens", torch.int32, 2),
-               (num_out, "num_out", torch.int32, 1), (ctx_out, "ctx_out", torch.int32, 1))
+    ld = ldd = vocab
+    if rows > 1:
+        ld = target_probs.stride(0)
+    if draft_probs is not None:
+        _need_rows(draft_probs, "draft_probs", _F32, 2, dev)
+        _need_shape(draft_probs, "draft_probs", target_probs.shape)
+        if rows > 1:
+            ldd = draft_probs.stride(0)
+    if ld < vocab or ldd < vocab:
+        raise ValueError("rows of probabilities must not overlap")
+    _need(draft_tokens, "draft_tokens", _I32, 1, dev)
+    _need(cu_rows, "cu_rows", _I32, 1, dev)
+    _need(u_accept, "u_accept", _F32, 1, dev)
+    _need(u_sample, "u_sample", _F32, 1, dev)
     R = u_sample.shape[0]
-    if cu_rows.shape[0] != R + 1 or draft_tokens.shape[0] != rows or u_accept.shape[0] != rows or \
-            (draft_probs is not None and tuple(draft_probs.shape) != (rows, vocab)):
+    if cu_rows.shape[0] != R + 1 or draft_tokens.shape[0] != rows or u_accept.shape[0] != rows:
         raise ValueError("inconsistent shapes")
     if max_out < 1:
         raise ValueError("max_out must be positive")
     if tokens is None:
-        tokens = torch.empty((R, max_out), dtype=torch.int32, device=dev)
+        tokens = torch.empty((R, max_out), dtype=_I32, device=target_probs.device)
+    else:
+        _need(tokens, "tokens", _I32, 2, dev)
+        _need_shape(tokens, "tokens", (R, max_out))
     if num_out is None:
-        num_out = torch.empty(R, dtype=torch.int32, device=dev)
+        num_out = torch.empty(R, dtype=_I32, device=target_probs.device)
+    else:
+        _need(num_out, "num_out", _I32, 1, dev)
+        _need_shape(num_out, "num_out", (R,))
     if ctx_len is None:
         if ctx_out is not None:
             raise ValueError("ctx_out needs ctx_len")
-    elif ctx_out is None:
-        ctx_out = torch.empty(R, dtype=torch.int32, device=dev)
-    _check_shape(tokens, "tokens", (R, max_out))
-    for t, name in ((num_out, "num_out"), (ctx_len, "ctx_len"), (ctx_out, "ctx_out")):
-        _check_shape(t, name, (R,))
-    ld = target_probs.stride(0) if rows > 1 else vocab
-    ldd = draft_probs.stride(0) if draft_probs is not None and rows > 1 else vocab
-    _call_on(dev, "dsa_verify_draft", stream, _p(target_probs), ld, rows, vocab, _p(draft_probs), ldd, _p(draft_tokens),
-             _p(u_accept), _p(u_sample), _p(cu_rows), R, max_out, _p(ctx_len), _p(tokens), _p(num_out), _p(ctx_out),
-             _status_arg(dev_status, dev))
+    else:
+        _need(ctx_len, "ctx_len", _I32, 1, dev)
+        _need_shape(ctx_len, "ctx_len", (R,))
+        if ctx_out is None:
+            ctx_out = torch.empty(R, dtype=_I32, device=target_probs.device)
+        else:
+            _need(ctx_out, "ctx_out", _I32, 1, dev)
+            _need_shape(ctx_out, "ctx_out", (R,))
+    _run(dev, stream, "dsa_verify_draft", target_probs.data_ptr(), ld, rows, vocab, _ptr(draft_probs), ldd,
+         draft_tokens.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(), cu_rows.data_ptr(), R, max_out,
+         _ptr(ctx_len), tokens.data_ptr(), num_out.data_ptr(), _ptr(ctx_out), _status_ptr(dev_status, dev))
     return tokens, num_out, ctx_out

@@ -229,9 +229,10 @@ int batch_layout_max_requests() { return 8192; }
 cudaError_t launch_batch_layout(const BatchLayoutArgs& a, cudaStream_t stream) {
   // four words a request (cu and first have one more)
   const size_t smem = sizeof(int32_t) * (4 * (size_t)a.num_req + 2);
-  cudaError_t e = cudaFuncSetAttribute(batch_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)(sizeof(int32_t) * (4 * (size_t)batch_layout_max_requests() + 2)));
-  if (e != cudaSuccess) return e;
+  if (smem > 48 * 1024) {  // more than a launch may take unasked
+    const cudaError_t e = cudaFuncSetAttribute(batch_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   const int64_t groups = ((int64_t)a.capacity + BL_TOK - 1) / BL_TOK;
   const int64_t ctas = (groups + BL_THREADS - 1) / BL_THREADS;
   // one CTA per SM at most: each takes the requests' scan once

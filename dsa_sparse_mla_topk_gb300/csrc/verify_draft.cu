@@ -40,9 +40,28 @@ constexpr int VD_THREADS = 512;
 constexpr int VD_WARPS = VD_THREADS / 32;
 constexpr int VD_MAX_CLUSTER = 8;
 
-// p in [0, 1] as a multiple of 2^-60 (NaN and negative values: 0)
+// Shifts whose amounts past 31 give 0 (negative ones count as large).
+__device__ __forceinline__ uint32_t shl(uint32_t x, int n) {
+  uint32_t r;
+  asm("shl.b32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(n));
+  return r;
+}
+__device__ __forceinline__ uint32_t shr(uint32_t x, int n) {
+  uint32_t r;
+  asm("shr.u32 %0, %1, %2;" : "=r"(r) : "r"(x), "r"(n));
+  return r;
+}
+
+// p in [0, 1] as a multiple of 2^-60 (NaN and negative values: 0; above 1: 1).
+// The significand m < 2^24 of p = m 2^(e - 150) is put at 2^37 (its value for e =
+// 127) and shifted right by 127 - e: eight integer operations, where the
+// conversion of an fp32 number to 64 bits runs at a fraction of their rate.
 __device__ __forceinline__ int64_t fixed60(float p) {
-  return __float2ll_rz(fminf(fmaxf(p, 0.f), 1.f) * 0x1p60f);
+  const uint32_t x = __float_as_uint(fminf(fmaxf(p, 0.f), 1.f));
+  const uint32_t top = ((x << 5) & 0x0fffffe0u) | 0x10000000u;  // m 2^5: the upper word of m 2^37
+  const int r = 127 - (int)(x >> 23);
+  const uint32_t hi = shr(top, r), lo = shl(top, 32 - r) | shr(top, r - 32);
+  return (int64_t)(((uint64_t)hi << 32) | lo);
 }
 
 struct Row {
@@ -193,29 +212,43 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
   const uint64_t u64 = __float2ull_rz(fminf(fmaxf(u, 0.f), 0x1.fffffep-1f) * 0x1p64f);
   const int64_t t = (int64_t)__umul64hi(u64, (uint64_t)total);  // floor(u sum w): sum_{i <= j} w > t
   if (before <= t && t < before + mine) {
+    // (four turns' loads together: a run is a few round trips to L2)
+    constexpr int TURNS = 4;
     int64_t base = before;
-    for (int32_t j0 = lo; j0 < hi; j0 += 128) {
-      const int32_t j = j0 + 4 * lane;
-      int64_t w[4] = {0, 0, 0, 0};
-      if (j < hi) weights4<VEC>(row, j, w);
-      const int64_t s = (w[0] + w[1]) + (w[2] + w[3]);
-      int64_t inc = s;
+    bool found = false;
+    for (int32_t j0 = lo; j0 < hi && !found; j0 += 128 * TURNS) {
+      int64_t w[TURNS][4];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += v;
+      for (int k = 0; k < TURNS; ++k) {
+        const int32_t j = j0 + 128 * k + 4 * lane;
+        w[k][0] = w[k][1] = w[k][2] = w[k][3] = 0;
+        if (j < hi) weights4<VEC>(row, j, w[k]);
       }
-      const unsigned over = __ballot_sync(0xffffffffu, base + inc > t);
-      if (over) {
-        if (lane == __ffs(over) - 1) {
-          int64_t c = base + inc - s;
-          int e = 0;
-          while (e < 3 && c + w[e] <= t) c += w[e++];
-          out[take] = j + e;
+#pragma unroll
+      for (int k = 0; k < TURNS; ++k) {
+        if (found) break;
+        const int64_t s = (w[k][0] + w[k][1]) + (w[k][2] + w[k][3]);
+        int64_t inc = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += v;
         }
-        break;
+        const unsigned over = __ballot_sync(0xffffffffu, base + inc > t);
+        if (over) {
+          found = true;
+          if (lane == __ffs(over) - 1) {
+            int64_t c = base + inc - s;
+            int e = 0;
+            for (; e < 3; ++e) {
+              if (c + w[k][e] > t) break;
+              c += w[k][e];
+            }
+            out[take] = j0 + 128 * k + 4 * lane + e;
+          }
+        }
+        base += __shfl_sync(0xffffffffu, inc, 31);
       }
-      base += __shfl_sync(0xffffffffu, inc, 31);
     }
   }
   if (rank == 0) {
