@@ -368,6 +368,7 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_
   if (st != DSA_OK) return st;
   st = check_norm_side(k, k_tok_stride, k_head_stride, k_heads, k_weight, k_norm_dim, k_out, !cache, num_tokens, d);
   if (st != DSA_OK) return st;
+  if ((int64_t)num_tokens * (q_heads + k_heads) > INT32_MAX) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (num_tokens == 0 || q_heads + k_heads == 0) return DSA_OK;
   if (d_rope > 0 && (!pos || !cos_sin || !aligned16(cos_sin) || max_pos <= 0)) return DSA_ERR_INVALID_ARG;
   dsa::NormRopeArgs a;

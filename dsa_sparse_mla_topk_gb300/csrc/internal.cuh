@@ -149,6 +149,19 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream);
 
+// n / d for 0 <= n < 2^31: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d)
+// (< 2^32 or 2^31), floor(n m / 2^(31 + s)) is exact, as m d - 2^(31 + s) <= 2^s.
+struct FastDiv {
+  uint32_t m;
+  int32_t shift;
+  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> shift); }
+};
+inline FastDiv make_fast_div(int32_t d) {
+  int s = 0;
+  while ((1ll << s) < d) ++s;
+  return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
+}
+
 // Report a data-dependent error without trapping.
 __device__ __forceinline__ void report(int32_t* status, uint32_t bit) {
   if (status) atomicOr(reinterpret_cast<unsigned int*>(status), bit);

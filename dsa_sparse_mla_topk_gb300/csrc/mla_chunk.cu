@@ -100,19 +100,6 @@ constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;  // with alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(OFF_QR % 1024 == 0 && OFF_P % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 
-// pos / d for 0 <= pos < 2^31: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d)
-// (< 2^32 or 2^31), floor(pos m / 2^(31 + s)) is exact, as m d - 2^(31 + s) <= 2^s.
-struct FastDiv {
-  uint32_t m;
-  int32_t shift;
-  __device__ __forceinline__ int operator()(int pos) const { return (int)(((uint64_t)(uint32_t)pos * m) >> shift); }
-};
-FastDiv make_fast_div(int32_t d) {
-  int s = 0;
-  while ((1ll << s) < d) ++s;
-  return {(uint32_t)(((1ull << (31 + s)) + d - 1) / d), 31 + s};
-}
-
 struct ChunkMaps {
   CUtensorMap lat_box, rope_box;  // box_rows rows
   CUtensorMap lat_row, rope_row;  // one row, for tile::gather4

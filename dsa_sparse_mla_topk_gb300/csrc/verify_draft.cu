@@ -36,8 +36,6 @@ namespace cg = cooperative_groups;
 namespace dsa {
 namespace {
 
-constexpr int VD_THREADS = 512;
-constexpr int VD_WARPS = VD_THREADS / 32;
 constexpr int VD_MAX_CLUSTER = 8;
 
 // Shifts whose amounts past 31 give 0 (negative ones count as large).
@@ -85,6 +83,81 @@ __device__ __forceinline__ float4 load4(const float* row, int32_t j, int32_t voc
   return make_float4(v[0], v[1], v[2], v[3]);
 }
 
+// The sum of fixed60 over many values, 20 bits at a time: adding 2^3 to p in [0, 1]
+// with rounding towards 0 leaves floor(p 2^20) in the low bits of the sum, the
+// remainder is exact, and the same with 2^-17 and 2^-37 gives the next two 20
+// bits.  Seven fp32 additions at the full rate, and the three parts add up in
+// 32-bit words (2^20 a value: up to 1,024 of them before they are put together).
+struct Parts {
+  uint32_t h = 0, m = 0, l = 0;
+  __device__ __forceinline__ static void split(float p, uint32_t& h, uint32_t& m, uint32_t& l) {
+    p = __saturatef(p);  // to [0, 1], NaN to 0
+    const float a = __fadd_rz(p, 8.f), r1 = p - (a - 8.f);
+    const float b = __fadd_rz(r1, 0x1p-17f), r2 = r1 - (b - 0x1p-17f);
+    h = __float_as_uint(a), m = __float_as_uint(b), l = __float_as_uint(__fadd_rz(r2, 0x1p-37f));
+  }
+  __device__ __forceinline__ void add(float p) {
+    uint32_t x, y, z;
+    split(p, x, y, z);
+    h += x - __float_as_uint(8.f), m += y - __float_as_uint(0x1p-17f), l += z - __float_as_uint(0x1p-37f);
+  }
+  // max(p - q, 0): the parts' differences (as two's complement; the sum is what counts)
+  __device__ __forceinline__ void add_rest(float p, float q) {
+    uint32_t x, y, z, u, v, w;
+    split(p, x, y, z);
+    split(q, u, v, w);
+    if (__saturatef(p) > __saturatef(q)) h += x - u, m += y - v, l += z - w;
+  }
+  __device__ __forceinline__ int64_t total() const {
+    return ((int64_t)(int32_t)h << 40) + ((int64_t)(int32_t)m << 20) + (int64_t)(int32_t)l;
+  }
+};
+
+// A lane's part of the sum over columns [lo, hi) (without `skip`), lo a multiple
+// of 128.  The full blocks' loads are unconditional, eight turns of them in flight.
+template <bool VEC, bool Q>
+__device__ __forceinline__ int64_t run_sum(const Row& r, int32_t lo, int32_t hi) {
+  constexpr int TURNS = Q ? 4 : 8;
+  auto add4 = [](Parts& acc, const float4 p, const float4 q) {
+    if constexpr (Q) {
+      acc.add_rest(p.x, q.x);
+      acc.add_rest(p.y, q.y);
+      acc.add_rest(p.z, q.z);
+      acc.add_rest(p.w, q.w);
+    } else {
+      acc.add(p.x);
+      acc.add(p.y);
+      acc.add(p.z);
+      acc.add(p.w);
+    }
+  };
+  auto full4 = [](const float* row, int32_t j) {
+    if constexpr (VEC) return __ldg(reinterpret_cast<const float4*>(row + j));
+    else return make_float4(__ldg(row + j), __ldg(row + j + 1), __ldg(row + j + 2), __ldg(row + j + 3));
+  };
+  int64_t s = 0;
+  int32_t j0 = lo;
+  const int lane4 = 4 * (threadIdx.x & 31);
+  while (hi - j0 >= 128 * TURNS) {
+    Parts acc;
+    for (int n = 0; n < 256 / TURNS && hi - j0 >= 128 * TURNS; ++n, j0 += 128 * TURNS) {  // 1,024 values at most
+      float4 p[TURNS], q[TURNS];
+#pragma unroll
+      for (int k = 0; k < TURNS; ++k) {
+        p[k] = full4(r.p, j0 + 128 * k + lane4);
+        if constexpr (Q) q[k] = full4(r.q, j0 + 128 * k + lane4);
+      }
+#pragma unroll
+      for (int k = 0; k < TURNS; ++k) add4(acc, p[k], q[k]);
+    }
+    s += acc.total();
+  }
+  Parts acc;
+  for (int32_t j = j0 + lane4; j < hi; j += 128)
+    add4(acc, load4<VEC>(r.p, j, r.vocab), Q ? load4<VEC>(r.q, j, r.vocab) : make_float4(0.f, 0.f, 0.f, 0.f));
+  return s + acc.total();
+}
+
 template <bool VEC>
 __device__ __forceinline__ void weights4(const Row& r, int32_t j, int64_t (&w)[4]) {
   const float4 p = load4<VEC>(r.p, j, r.vocab);
@@ -101,8 +174,9 @@ __device__ __forceinline__ int64_t warp_sum(int64_t v) {
   return v;
 }
 
-template <bool VEC>
+template <int VD_THREADS, bool VEC>
 __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyArgs a) {
+  constexpr int VD_WARPS = VD_THREADS / 32;
   cg::cluster_group cluster = cg::this_cluster();
   const int C = cluster.num_blocks(), rank = cluster.block_rank();
   const int req = blockIdx.x / C;
@@ -177,11 +251,11 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
   int64_t total = 0, before = 0, mine = 0;
   for (int turn = 0; turn < 2; ++turn) {
     int64_t s = 0;
-#pragma unroll 4
-    for (int32_t j = lo + 4 * lane; j < hi; j += 128) {
-      int64_t w[4];
-      weights4<VEC>(row, j, w);
-      s += (w[0] + w[1]) + (w[2] + w[3]);
+    if (row.q) {
+      s = run_sum<VEC, true>(row, lo, hi);
+    } else {
+      s = run_sum<VEC, false>(row, lo, hi);
+      if (lane == 0 && row.skip >= lo && row.skip < hi) s -= fixed60(row.p[row.skip]);
     }
     s = warp_sum(s);
     mine = s;
@@ -267,7 +341,14 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
   const bool vec = (reinterpret_cast<uintptr_t>(a.target) & 15u) == 0 && a.ld_target % 4 == 0 &&
                    (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0 && a.ld_draft % 4 == 0));
+  // Eight CTAs a request, of 512 threads while two of them fit an SM at once
+  // (one request: 8.7 us, 256 threads 9.7 us), of 256 beyond that (128 requests, V =
+  // 131,072: 33 us; 512 threads 39 us, and with fewer CTAs a request 36 to 45 us);
+  // fewer where a request's chain of loads would repeat in too many waves.
+  const int sms = device_sm_count();
   int c = VD_MAX_CLUSTER;
+  while (c > 1 && (int64_t)a.num_req * c > 8 * sms) c /= 2;
+  const bool wide = (int64_t)a.num_req * c <= 2 * sms;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
@@ -275,12 +356,14 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.num_req * c);
-  cfg.blockDim = dim3(VD_THREADS);
+  cfg.blockDim = dim3(wide ? 512 : 256);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = vec ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<true>, a)
-                            : cudaLaunchKernelEx(&cfg, verify_draft_kernel<false>, a);
+  const cudaError_t e = wide ? (vec ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<512, true>, a)
+                                    : cudaLaunchKernelEx(&cfg, verify_draft_kernel<512, false>, a))
+                             : (vec ? cudaLaunchKernelEx(&cfg, verify_draft_kernel<256, true>, a)
+                                    : cudaLaunchKernelEx(&cfg, verify_draft_kernel<256, false>, a));
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -383,6 +383,7 @@ DSA_API dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_l
  *             most d; 0: no norm (weight may be NULL).
  *   d         a multiple of 8, at most 1024.  d_rope a multiple of 16, at most
  *             d, with d - d_rope a multiple of 8; 0: no rotation (cos_sin may be NULL).
+ *   num_tokens  times the heads of both sides below 2^31 (else UNSUPPORTED_SHAPE).
  *   pos       int32 [num_tokens] (NULL allowed when d_rope = 0); -1: a padding
  *             row, whose outputs are left as they were.
  *   cos_sin   fp32 [max_pos, d_rope], 16-byte aligned.
