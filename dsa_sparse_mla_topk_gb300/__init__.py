@@ -38,6 +38,7 @@ EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_
 
 _lock = threading.Lock()
 _lib = None
+_fast = None  # the C++ marshalling module, bound to the loaded library
 
 
 class DsaError(RuntimeError):
@@ -114,8 +115,31 @@ def load_library(path: str | None = None):
         lib.dsa_kv_tile_size.restype = i32
         lib.dsa_pick_num_splits.argtypes = [i32, i32, i32, i32, i32, i32]
         lib.dsa_pick_num_splits.restype = i32
+        global _fast
+        _fast = _load_marshal(lib)
         _lib = lib
         return lib
+
+
+# csrc/python/marshal.cpp as built for this PyTorch
+MARSHAL_PATH = os.path.join(_PKG, f"_marshal.{torch.__version__}.so")
+
+
+def _load_marshal(lib):
+    """The C++ marshalling bound to ``lib``'s entry points; None where it was not
+    built for this PyTorch, and Python marshals."""
+    if not os.path.exists(MARSHAL_PATH):
+        return None
+    from importlib.machinery import ExtensionFileLoader
+    from importlib.util import module_from_spec, spec_from_loader
+
+    loader = ExtensionFileLoader("_marshal", MARSHAL_PATH)
+    m = module_from_spec(spec_from_loader("_marshal", loader))
+    loader.exec_module(m)
+    m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+             for f in (lib.dsa_batch_layout, lib.dsa_qk_norm_rope, lib.dsa_chunk_mla_fwd, lib.dsa_combine,
+                       lib.dsa_pick_num_splits, lib.dsa_verify_draft)))
+    return m
 
 
 def status_string(status: int) -> str:
@@ -483,9 +507,10 @@ def sparse_mla_topk(q, kv, kv_scale, block_table, q_req, q_pos, scores, k: int, 
 
 # ---- the rest of a serving step --------------------------------------------------
 #
-# These calls are a few microseconds of GPU work in a decode step, so their
-# checks are written for the host's time as well: one pass over a tensor's
-# attributes, no wrapper objects, outputs cut from few allocations.
+# These calls are a few microseconds of GPU work in a decode step, so the host's
+# time matters.  An ordinary call (documented tensors, outputs allocated here, the
+# current device and stream) goes through the C++ marshalling; it takes nothing
+# else, and what it does not take is checked, explained or run by the code here.
 
 _I32, _F32, _BF16, _U8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
 
@@ -522,6 +547,13 @@ def _need_shape(t, name: str, shape: tuple):
 
 def _ptr(t):
     return None if t is None else t.data_ptr()
+
+
+def _done(fn: str, r):
+    """What the C++ marshalling returned: outputs, or a status that is an error."""
+    if type(r) is int:
+        raise DsaError(fn, r)
+    return r
 
 
 def _run(dev: int, stream, fn: str, *args):
@@ -583,8 +615,12 @@ def batch_layout(ctx_len: torch.Tensor, new_len: torch.Tensor, pages_held: torch
     """A step's token ranges, slot map and grown block tables from the
     requests' lengths (dsa_batch_layout): ``block_table`` gets the new pages in
     place, everything else is returned.  ``out`` (a BatchLayout of
-    preallocated tensors, not the inputs) is written when given; without it
-    the returned tensors share one allocation."""
+    preallocated tensors, not the inputs) is written when given."""
+    if out is None and stream is None and _fast is not None:
+        r = _fast.batch_layout(ctx_len, new_len, pages_held, block_table, free_pages, free_used, page_size, num_pages,
+                               capacity, dev_status)
+        if r is not None:
+            return BatchLayout._make(_done("dsa_batch_layout", r))
     dev = _device_of(ctx_len, "ctx_len")
     _need(ctx_len, "ctx_len", _I32, 1, dev)
     _need(new_len, "new_len", _I32, 1, dev)
@@ -636,6 +672,11 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
     None, or keys that only go into the cache, give None.  Tokens with pos =
     -1 are left as they were."""
     some = q if q is not None else k
+    if q_out is None and k_out is None and stream is None and _fast is not None:
+        r = _fast.qk_norm_rope(q, k, pos, cos_sin, d_rope, q_weight, k_weight, eps, interleaved, slot, kv, kv_scale,
+                               dev_status)
+        if r is not None:
+            return _done("dsa_qk_norm_rope", r)
     if some is None:
         raise ValueError("q or k must be given")
     dev = _device_of(some, "q or k")
@@ -773,11 +814,16 @@ def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_ro
     (optional) holds preallocated out / lse / o_part / lse_part tensors.
     Returns (out, lse)."""
     b = buffers or {}
+    if num_splits is None and max_ctx is None:
+        max_ctx = block_table.shape[1] * page_size
+    if not b and stream is None and _fast is not None and num_splits != 0:
+        r = _fast.chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, d_latent, d_rope, page_size, softmax_scale,
+                            max_ctx or 1, num_splits or 0, dev_status)
+        if r is not None:
+            return _done("dsa_chunk_mla_fwd", r)
     num_q, H, _ = q.shape
     if num_splits is None:
-        if max_ctx is None:
-            max_ctx = block_table.shape[1] * page_size
-        num_splits = pick_num_splits(num_q, H, d_latent, d_rope, max(1, max_ctx))
+        num_splits = pick_num_splits(num_q, H, d_latent, d_rope, max(1, min(max_ctx, 2**31 - 1)))
     out, lse = b.get("out"), b.get("lse")
     if num_splits == 1 or num_q == 0:
         return chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
@@ -810,6 +856,11 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
     given random numbers (dsa_verify_draft).  Returns (tokens int32 [num_req,
     max_out], -1 padded; num_out int32 [num_req]; ctx_out = ctx_len + num_out,
     or None without ctx_len)."""
+    if tokens is None and num_out is None and ctx_out is None and stream is None and _fast is not None:
+        r = _fast.verify_draft(target_probs, draft_tokens, cu_rows, u_accept, u_sample, draft_probs, ctx_len, max_out,
+                               dev_status)
+        if r is not None:
+            return _done("dsa_verify_draft", r)
     dev = _device_of(target_probs, "target_probs")
     _need_rows(target_probs, "target_probs", _F32, 2, dev)
     rows, vocab = target_probs.shape

@@ -3,6 +3,10 @@
 Each translation unit is compiled in parallel with nvcc, then linked into one
 shared library with a plain C ABI (include/dsa.h).  The library links the
 shared CUDA runtime so that it shares the process's runtime with PyTorch.
+
+csrc/python/marshal.cpp, the Python binding's argument marshalling, is compiled
+beside it with g++ against the installed PyTorch -> _marshal.<its version>.so.  It holds no
+kernels; without it (no Python or PyTorch headers) the binding marshals in Python.
 """
 from __future__ import annotations
 
@@ -19,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libdsa.so")
+MARSHAL_SRC = os.path.join(CSRC, "python", "marshal.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -49,7 +54,51 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
+def marshal_path() -> str:
+    import torch
+
+    return os.path.join(PKG, f"_marshal.{torch.__version__}.so")
+
+
+def build_marshal(force: bool = False) -> str | None:
+    """The marshalling module for the PyTorch in use; None where its headers are missing."""
+    import sysconfig
+
+    import torch
+
+    lib = marshal_path()
+    deps = (MARSHAL_SRC, os.path.join(INCLUDE, "dsa.h"), __file__)
+    if not force and os.path.exists(lib) and all(os.path.getmtime(d) <= os.path.getmtime(lib) for d in deps):
+        return lib
+    inc, cxx = sysconfig.get_paths()["include"], shutil.which("g++")
+    root = os.path.dirname(torch.__file__)
+    tinc, tlib = os.path.join(root, "include"), os.path.join(root, "lib")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    if not cxx or not all(os.path.exists(p) for p in (os.path.join(inc, "Python.h"), os.path.join(tinc, "ATen"),
+                                                      os.path.join(cuda, "cuda_runtime_api.h"))):
+        return None
+    tmp = lib + f".{os.getpid()}.tmp"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-I", tinc, "-I",
+           os.path.join(tinc, "torch", "csrc", "api", "include"), "-I", inc, "-I", cuda, MARSHAL_SRC, "-o", tmp,
+           "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stderr}")
+    os.replace(tmp, lib)
+    return lib
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:  # beside the CUDA sources
+        marshal = ex.submit(build_marshal, force)
+        lib = _build_library(force, verbose, ptxas_info)
+        marshal.result()
+    return lib
+
+
+def _build_library(force: bool, verbose: bool, ptxas_info: bool) -> str:
     if not force and up_to_date():
         return LIB
     os.makedirs(OBJ, exist_ok=True)

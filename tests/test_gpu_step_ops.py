@@ -642,6 +642,106 @@ def test_chunk_agrees_with_the_sparse_call_over_every_position():
     assert float((sl - cl).abs().max()) <= 1e-3
 
 
+# ---- the binding's two ways to marshal a call ---------------------------------------
+
+
+def _without_cpp(f):
+    fast, dsa._fast = dsa._fast, None
+    try:
+        return f()
+    finally:
+        dsa._fast = fast
+
+
+def test_cpp_marshalling_is_the_one_that_runs_and_agrees_with_python():
+    assert dsa._fast is not None
+    c, n, held, table, free, pages = _layout_case(9, 6, 100, 16, seed=11)
+    p, q, tok, cu, ua, us = _verify_case(8, 5, 777, True, seed=6, pad_cols=3)
+    ch = _cuda(_chunk_case(64, 512, 64, [300, 100], [3, 2], 64, seed=10))
+    tiny = _cuda(_chunk_case(16, 64, 16, [500, 100], [1, 1], 16, seed=10))
+    x, k, g = _qk_inputs(12, 6, 1, 576, torch.bfloat16, seed=2, pad=8)
+    pos = torch.randint(0, 50, (12,), generator=g, dtype=I32).cuda()
+    cs = torch.from_numpy(_tables(50, 64)).cuda()
+    slot = torch.randperm(20, generator=g)[:12].to(I32).cuda()
+
+    def layout():
+        t = torch.from_numpy(table.copy()).cuda()
+        return [*dsa.batch_layout(i32(c), i32(n), i32(held), t, i32(free), i32([0]), page_size=16, num_pages=pages,
+                                  capacity=70), t]
+
+    def rows():
+        kv, sc = torch.zeros((20, 576), dtype=torch.uint8, device="cuda"), torch.zeros(20, device="cuda")
+        a = dsa.qk_norm_rope(x, k, pos, cs, d_rope=64, slot=slot, kv=kv, kv_scale=sc)
+        b = dsa.qk_norm_rope(x, k, pos, cs, d_rope=64, interleaved=False)
+        assert a[1] is None
+        return [a[0], kv, sc, *b]
+
+    def attention():
+        r = []
+        for d, page, kw in ((ch, 64, dict(max_ctx=300)), (ch, 64, dict(num_splits=3)), (tiny, 16, {})):
+            r += dsa.chunk_mla(d["q"], d["kv"], d["sc"], d["table"], d["req"], d["pos"], d_latent=d["dl"],
+                               d_rope=d["dr"], page_size=page, softmax_scale=d["scale"], **kw)
+        return r
+
+    def verify():
+        a = dsa.verify_draft(p, tok, cu, ua, us, draft_probs=q, max_out=6)
+        assert a[2] is None
+        return [*a[:2], *dsa.verify_draft(p, tok, cu, ua, us, max_out=6, ctx_len=tok[:8].contiguous())]
+
+    for f in (layout, rows, attention, verify):
+        a, b = f(), _without_cpp(f)
+        torch.cuda.synchronize()
+        for s, t in zip(a, b):
+            assert s.dtype == t.dtype and s.shape == t.shape and torch.equal(s, t)
+
+
+def test_calls_the_binding_refuses_both_ways():
+    c, n, held, table, free, pages = _layout_case(9, 6, 100, 16, seed=11)
+    a = (i32(c), i32(n), i32(held), torch.from_numpy(table).cuda(), i32(free), i32([0]))
+    p, q, tok, cu, ua, us = _verify_case(8, 5, 777, True, seed=6)
+    x, k, _ = _qk_inputs(12, 6, 1, 576, torch.bfloat16, seed=2, pad=8)
+    pos, cs = i32([0] * 12), torch.from_numpy(_tables(50, 64)).cuda()
+    ch = _cuda(_chunk_case(64, 512, 64, [300, 100], [3, 2], 64, seed=10))
+    kw = dict(page_size=16, num_pages=pages, capacity=70)
+    mla = (ch["q"], ch["kv"], ch["sc"], ch["table"], ch["req"], ch["pos"])
+    mk = dict(d_latent=512, d_rope=64, page_size=64, softmax_scale=0.04)
+    bad = [
+        (ValueError, lambda: dsa.batch_layout(a[0].cpu(), *a[1:], **kw)),
+        (TypeError, lambda: dsa.batch_layout(a[0].long(), *a[1:], **kw)),
+        (ValueError, lambda: dsa.batch_layout(*a[:3], a[3].t(), *a[4:], **kw)),
+        (ValueError, lambda: dsa.batch_layout(a[0], a[1][1:], *a[2:], **kw)),
+        (ValueError, lambda: dsa.batch_layout(*a, **{**kw, "capacity": -1})),
+        (dsa.DsaError, lambda: dsa.batch_layout(*a, **{**kw, "page_size": 0})),
+        (dsa.DsaError, lambda: dsa.batch_layout(*a, **kw, out=dsa.BatchLayout(
+            *[torch.empty(m, dtype=I32, device="cuda") for m in (10, 70, 70, 70)], a[0], torch.empty_like(a[0]),
+            torch.empty_like(a[5])))),
+        (ValueError, lambda: dsa.qk_norm_rope(x, k, pos[:5], cs, d_rope=64)),
+        (ValueError, lambda: dsa.qk_norm_rope(x, k, pos, cs, d_rope=32)),
+        (ValueError, lambda: dsa.qk_norm_rope(x, k[:4], pos, cs, d_rope=64)),
+        (TypeError, lambda: dsa.qk_norm_rope(x.float(), k, pos, cs, d_rope=64)),
+        (TypeError, lambda: dsa.qk_norm_rope(x, k.half(), pos, cs, d_rope=64)),
+        (ValueError, lambda: dsa.qk_norm_rope(x.transpose(1, 2), None, pos, cs, d_rope=64)),
+        (dsa.DsaError, lambda: dsa.qk_norm_rope(x, k, pos, cs, d_rope=64, q_weight=cs[0, :12].contiguous())),
+        (dsa.DsaError, lambda: dsa.qk_norm_rope(x, k, pos, cs, d_rope=64, eps=-1.0)),
+        (ValueError, lambda: dsa.chunk_mla(*mla[:5], mla[5][:2], **mk)),
+        (ValueError, lambda: dsa.chunk_mla(*mla, **{**mk, "page_size": 7})),
+        (dsa.DsaError, lambda: dsa.chunk_mla(*mla, **mk, num_splits=65)),
+        (dsa.DsaError, lambda: dsa.chunk_mla(*mla, **mk, num_splits=0)),
+        (dsa.DsaError, lambda: dsa.chunk_mla(*mla, **{**mk, "softmax_scale": float("inf")})),
+        (TypeError, lambda: dsa.verify_draft(p.double(), tok, cu, ua, us, max_out=6)),
+        (ValueError, lambda: dsa.verify_draft(p, tok, cu, ua, us, draft_probs=q[:, :5], max_out=6)),
+        (ValueError, lambda: dsa.verify_draft(p, tok, cu, ua, us, max_out=0)),
+        (ValueError, lambda: dsa.verify_draft(p, tok, cu[:4], ua, us, max_out=6)),
+        (ValueError, lambda: dsa.verify_draft(p[:1].expand(p.shape), tok, cu, ua, us, max_out=6)),
+        (TypeError, lambda: dsa.verify_draft(p, tok, cu, ua, us, max_out=6, dev_status=cs)),
+    ]
+    for i, (kind, f) in enumerate(bad):
+        for way in (lambda f=f: f(), lambda f=f: _without_cpp(f)):
+            with pytest.raises(kind):
+                way()
+                pytest.fail(f"case {i} was taken")
+
+
 # ---- together ----------------------------------------------------------------------
 
 
