@@ -134,6 +134,7 @@ PyObject* batch_layout(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (nw->size(0) != R || held->size(0) != R || table->size(0) != R || used->size(0) != 1 || !fits32(R) ||
       !fits32(table->size(1)) || !fits32(free->size(0)))
     Py_RETURN_NONE;
+  // (seven allocations: 11.5 us a call; cutting one up with views took 13.3)
   const auto opt = ctx->options();
   const at::Tensor cu = at::empty({R + 1}, opt), req = at::empty({cap}, opt), pos = at::empty({cap}, opt),
                    slot = at::empty({cap}, opt), co = at::empty({R}, opt), ho = at::empty({R}, opt),

@@ -244,7 +244,34 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 4)
     }
   }
   const bool store = live && side.out;
-  if (store) {
+  // Halves that are both in this lane (the whole of a 128-value head): each pair
+  // once, without reading the partner chunk again.
+  bool paired = false;
+  if constexpr (!PAIRS && CH == 2) paired = rope0 == 0 && half == LPR;
+  if constexpr (!PAIRS && CH == 2) {
+    if (store && paired) {
+      Shared lo = shared_of(gl), hi;
+      hi.normed = gl + LPR < nn;
+      if (hi.normed) load8(weight + 8 * (gl + LPR), hi.w);
+      lo.rotated = hi.rotated = false;  // result(): the norm alone
+#pragma unroll
+      for (int r = 0; r < NR; ++r) {
+        if (h0 + r >= heads) break;
+        float x[8], y[8];
+        result(r, raw[r][0], gl, lo, x);
+        result(r, raw[r][1], gl + LPR, hi, y);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float a0 = x[e], b0 = y[e];
+          x[e] = a0 * lo.c[e] - b0 * lo.s[e];
+          y[e] = a0 * lo.s[e] + b0 * lo.c[e];
+        }
+        raw[r][0] = pack8<HALF>(x);
+        raw[r][1] = pack8<HALF>(y);
+      }
+    }
+  }
+  if (store && !paired) {
 #pragma unroll
     for (int u = 0; u < CH; ++u) {
       const int c = gl + LPR * u;
