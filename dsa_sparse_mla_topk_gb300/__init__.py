@@ -545,6 +545,11 @@ def _need_shape(t, name: str, shape: tuple):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
 
 
+def _strides(t):
+    """Token and head strides of rows [tokens, heads, d]; 0 where only one is there."""
+    return t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -694,7 +699,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
     if q is not None:
         _need_rows(q, "q", dtype, 3, dev)
         qp, qh = q.data_ptr(), q.shape[1]
-        qst, qsh, _ = q.stride()
+        qst, qsh = _strides(q)
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
         else:
@@ -708,7 +713,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
         if k.shape[0] != n or k.shape[2] != d:
             raise ValueError("q and k must have the same tokens and row sizes")
         kp, kh = k.data_ptr(), k.shape[1]
-        kst, ksh, _ = k.stride()
+        kst, ksh = _strides(k)
         if k_out is not None:
             _need(k_out, "k_out", dtype, 3, dev)
             _need_shape(k_out, "k_out", k.shape)

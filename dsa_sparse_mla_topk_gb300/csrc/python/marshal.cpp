@@ -97,6 +97,7 @@ template <class T>
 T* ptr(const at::Tensor* t) {
   return t ? static_cast<T*>(t->data_ptr()) : nullptr;
 }
+int64_t stride(const at::Tensor* t, int64_t dim) { return t && t->size(dim) > 1 ? t->stride(dim) : 0; }
 bool fits32(int64_t n) { return n <= INT32_MAX; }
 
 PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
@@ -191,9 +192,9 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (q) qo = at::empty(q->sizes(), x->options());
   if (k && !cache) ko = at::empty(k->sizes(), x->options());
   const dsa_status s = qk_norm_rope_fn(
-      ptr<void>(q), q ? q->stride(0) : 0, q ? q->stride(1) : 0, q ? (int32_t)q->size(1) : 0, ptr<float>(qw),
-      qw ? (int32_t)qw->size(0) : 0, q ? qo.data_ptr() : nullptr, ptr<void>(k), k ? k->stride(0) : 0,
-      k ? k->stride(1) : 0, k ? (int32_t)k->size(1) : 0, ptr<float>(kw), kw ? (int32_t)kw->size(0) : 0,
+      ptr<void>(q), stride(q, 0), stride(q, 1), q ? (int32_t)q->size(1) : 0, ptr<float>(qw),
+      qw ? (int32_t)qw->size(0) : 0, q ? qo.data_ptr() : nullptr, ptr<void>(k), stride(k, 0),
+      stride(k, 1), k ? (int32_t)k->size(1) : 0, ptr<float>(kw), kw ? (int32_t)kw->size(0) : 0,
       k && !cache ? ko.data_ptr() : nullptr, (int32_t)n, (int32_t)d, rope,
       x->scalar_type() == at::kHalf ? DSA_FP16 : DSA_BF16, ptr<int32_t>(pos), ptr<float>(cs),
       cs ? (int32_t)cs->size(0) : 0, eps, inter, ptr<int32_t>(slot), ptr<uint8_t>(kv), ptr<float>(sc),

@@ -301,6 +301,22 @@ def test_norm_rope_in_place_and_overlaps():
             dsa.qk_norm_rope(wide, None, pos, cs, q_out=wide, d_rope=rope)
 
 
+def test_norm_rope_single_tokens_and_heads_with_odd_strides():
+    """A dimension of one may have any stride; broadcast tokens may have stride 0."""
+    d = 80
+    g = torch.Generator().manual_seed(3)
+    base = torch.randn((3 * 7 * 81,), generator=g).to(torch.bfloat16).cuda()
+    one = base.as_strided((1, 2, d), (13, d, 1))          # one token: its token stride is not looked at
+    key = base.as_strided((5, 1, d), (d, 3, 1))           # one head
+    same = base.as_strided((5, 2, d), (0, d, 1))          # five times the same token
+    for x in (one, key, same):
+        for run in (lambda: dsa.qk_norm_rope(x, None, None, None, d_rope=0, q_weight=torch.ones(d, device="cuda")),
+                    lambda: _without_cpp(lambda: dsa.qk_norm_rope(x, None, None, None, d_rope=0,
+                                                                  q_weight=torch.ones(d, device="cuda")))):
+            y = run()[0]
+            _check_rows(y, ref.norm_rope(host(x.double()), np.ones(d), None, None, 0, True, 1e-6), torch.bfloat16)
+
+
 # ---- verify_draft ------------------------------------------------------------------
 
 
@@ -533,6 +549,38 @@ def test_chunk_sharp_logits_and_growing_scales(shape):
     c["sc"] = c["sc"] * torch.exp2(pos_of / 150)
     c["q"] = (c["q"].float() / 64).to(torch.bfloat16)
     for splits in (1, 4):
+        _check_chunk(*_run_chunk(c, splits)[:2], _chunk_ref(c))
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"h{s[0]}")
+@pytest.mark.parametrize("scale", [0.0, -0.05, 1e-20])
+def test_chunk_other_softmax_scales(shape, scale):
+    """No scale (every position weighs the same), a negative and a tiny one."""
+    c = _chunk_case(*shape, [700, 90], [2, 1], 16, seed=12)
+    c["scale"] = scale
+    for splits in (1, 3):
+        _check_chunk(*_run_chunk(c, splits)[:2], _chunk_ref(c))
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"h{s[0]}")
+def test_chunk_rows_of_scale_zero_and_zero_queries(shape):
+    """All-zero cache rows (scale 0) take part with logit 0; a zero query weighs every row the same."""
+    c = _chunk_case(*shape, [260, 130], [3, 2], 64, seed=13)
+    c["sc"][::3] = 0.0
+    c["sc"][int(c["table"][1, 0]) * 64:][:64] = 0.0  # the whole first tile of request 1
+    c["q"][1] = 0.0
+    for splits in (1, 2):
+        _check_chunk(*_run_chunk(c, splits)[:2], _chunk_ref(c))
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"h{s[0]}")
+def test_chunk_tokens_in_any_order_and_shared_pages(shape):
+    c = _chunk_case(*shape, [300, 300, 200], [4, 4, 4], 16, seed=14)
+    c["table"][1, :10] = c["table"][0, :10]  # a shared prefix
+    g = torch.Generator().manual_seed(1)
+    order = torch.randperm(len(c["pos"]), generator=g)
+    c["req"], c["pos"] = c["req"][order].contiguous(), c["pos"][order].contiguous()
+    for splits in (1, 2):
         _check_chunk(*_run_chunk(c, splits)[:2], _chunk_ref(c))
 
 

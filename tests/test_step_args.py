@@ -66,7 +66,7 @@ def _norm(lib, **over):
     (dict(pos=None), 1), (dict(cs=None), 1), (dict(cs=MISALIGNED), 1), (dict(mp=0), 1),
     (dict(slot=None), 1), (dict(kv=None), 1), (dict(sc=None), 1), (dict(kv=MISALIGNED), 1), (dict(ns=0), 1),
     (dict(nk=2, kh=576, kt=1152), 1), (dict(slot=None, kv=None, sc=None), 1),  # no cache and no k_out
-    (dict(T=0), 0), (dict(nq=0, nk=0, slot=None, kv=None, sc=None), 0),
+    (dict(T=1 << 30), 2), (dict(T=0), 0), (dict(nq=0, nk=0, slot=None, kv=None, sc=None), 0),
 ])
 def test_norm_rope_argument_checks(lib, over, expect):
     assert _norm(lib, **over) == expect
@@ -103,6 +103,7 @@ def _verify(lib, **over):
     (dict(rows=-1), 1), (dict(V=0), 1), (dict(R=-1), 1), (dict(mo=0), 1), (dict(ld=99), 1), (dict(ldq=99), 1),
     (dict(ctx=None), 1), (dict(co=None), 1), (dict(us=None), 1), (dict(cu=None), 1), (dict(out=None), 1),
     (dict(num=None), 1), (dict(p=None), 1), (dict(tok=None), 1), (dict(ua=None), 1), (dict(R=(1 << 24) + 1), 2),
+    (dict(V=(1 << 30) + 1, ld=1 << 31, ldq=1 << 31), 2),
     (dict(R=0), 0),
 ])
 def test_verify_argument_checks(lib, over, expect):
