@@ -100,6 +100,17 @@ T* ptr(const at::Tensor* t) {
 int64_t stride(const at::Tensor* t, int64_t dim) { return t && t->size(dim) > 1 ? t->stride(dim) : 0; }
 bool fits32(int64_t n) { return n <= INT32_MAX; }
 
+// A contiguous tensor over part of a fresh buffer's storage (`at` in elements of
+// `type`): a call's outputs share one allocation.
+at::Tensor cut(const at::Tensor& buf, int64_t at, at::IntArrayRef sizes, at::ScalarType type) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(buf.storage()), buf.key_set(),
+                                                         c10::scalarTypeToTypeMeta(type));
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
+}
+at::Tensor bytes(int64_t n, const at::Tensor& like) { return at::empty({n}, like.options().dtype(at::kByte)); }
+
 PyObject* tuple_of(std::initializer_list<const at::Tensor*> ts) {
   PyObject* r = PyTuple_New((Py_ssize_t)ts.size());
   if (!r) return nullptr;
@@ -135,11 +146,12 @@ PyObject* batch_layout(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (nw->size(0) != R || held->size(0) != R || table->size(0) != R || used->size(0) != 1 || !fits32(R) ||
       !fits32(table->size(1)) || !fits32(free->size(0)))
     Py_RETURN_NONE;
-  // (seven allocations: 11.5 us a call; cutting one up with views took 13.3)
-  const auto opt = ctx->options();
-  const at::Tensor cu = at::empty({R + 1}, opt), req = at::empty({cap}, opt), pos = at::empty({cap}, opt),
-                   slot = at::empty({cap}, opt), co = at::empty({R}, opt), ho = at::empty({R}, opt),
-                   uo = at::empty({1}, opt);
+  // the token arrays first, a multiple of 16 bytes apart
+  const int64_t c4 = ((int64_t)cap + 3) / 4 * 4;
+  const at::Tensor buf = at::empty({3 * c4 + 3 * R + 2}, ctx->options());
+  auto part = [&](int64_t at, int64_t n) { return cut(buf, at, {n}, at::kInt); };
+  const at::Tensor req = part(0, cap), pos = part(c4, cap), slot = part(2 * c4, cap), cu = part(3 * c4, R + 1),
+                   co = part(3 * c4 + R + 1, R), ho = part(3 * c4 + 2 * R + 1, R), uo = part(3 * c4 + 3 * R + 1, 1);
   const dsa_status s = batch_layout_fn(ptr<int32_t>(ctx), ptr<int32_t>(nw), ptr<int32_t>(held), (int32_t)R,
                                        ptr<int32_t>(table), (int32_t)table->size(1), ptr<int32_t>(free),
                                        (int32_t)free->size(0), ptr<int32_t>(used), page, pages, cap, ptr<int32_t>(&cu),
@@ -230,22 +242,25 @@ PyObject* chunk_mla(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (S == 0)
     S = pick_fn((int32_t)n, (int32_t)H, dl, dr, (int32_t)std::min<int64_t>(std::max<int64_t>(ctx, 1), INT32_MAX), 0);
   if (S < 1 || S > 64) Py_RETURN_NONE;
-  const at::Tensor out = at::empty({n, H, dl}, q->options());
-  const at::Tensor lse = at::empty({n, H}, sc->options());
-  at::Tensor op, lp;
+  // out, then lse; the partials of a split call in a buffer of their own
+  const int64_t ob = (2 * n * H * dl + 15) / 16 * 16;
+  const at::Tensor buf = bytes(ob + 4 * n * H, *q);
+  const at::Tensor out = cut(buf, 0, {n, H, dl}, at::kBFloat16), lse = cut(buf, ob / 4, {n, H}, at::kFloat);
+  at::Tensor parts;
+  float *op = nullptr, *lp = nullptr;
   if (S > 1) {
-    op = at::empty({S, n, H, dl}, sc->options());
-    lp = at::empty({S, n, H}, sc->options());
+    const int64_t pn = ((int64_t)S * n * H * dl + 3) / 4 * 4;
+    parts = at::empty({pn + (int64_t)S * n * H}, sc->options());
+    op = ptr<float>(&parts);
+    lp = op + pn;
   }
   void* stream = a.stream();
   dsa_status s = chunk_mla_fn(q->data_ptr(), ptr<uint8_t>(kv), ptr<float>(sc), slots / page, ptr<int32_t>(bt),
                               (int32_t)bt->size(0), (int32_t)bt->size(1), ptr<int32_t>(req), ptr<int32_t>(pos),
                               (int32_t)n, (int32_t)H, dl, dr, page, scale, S, S == 1 ? out.data_ptr() : nullptr,
-                              S == 1 ? ptr<float>(&lse) : nullptr, S > 1 ? ptr<float>(&op) : nullptr,
-                              S > 1 ? ptr<float>(&lp) : nullptr, st, stream);
+                              S == 1 ? ptr<float>(&lse) : nullptr, op, lp, st, stream);
   if (s == DSA_OK && S > 1)
-    s = combine_fn(ptr<float>(&op), ptr<float>(&lp), S, (int32_t)n, (int32_t)H, dl, out.data_ptr(), ptr<float>(&lse),
-                   stream);
+    s = combine_fn(op, lp, S, (int32_t)n, (int32_t)H, dl, out.data_ptr(), ptr<float>(&lse), stream);
   if (s != DSA_OK) return PyLong_FromLong(s);
   return tuple_of({&out, &lse});
   END_HANDLE_TH_ERRORS
@@ -277,10 +292,10 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (cu->size(0) != R + 1 || tok->size(0) != rows || ua->size(0) != rows || (q && q->sizes() != p->sizes()) ||
       (ctx && ctx->size(0) != R) || !fits32(rows) || !fits32(V) || !fits32(R))
     Py_RETURN_NONE;
-  const auto opt = cu->options();
-  const at::Tensor tokens = at::empty({R, max_out}, opt), num = at::empty({R}, opt);
+  const at::Tensor buf = at::empty({R * max_out + (ctx ? 2 : 1) * R}, cu->options());
+  const at::Tensor tokens = cut(buf, 0, {R, max_out}, at::kInt), num = cut(buf, R * max_out, {R}, at::kInt);
   at::Tensor co;
-  if (ctx) co = at::empty({R}, opt);
+  if (ctx) co = cut(buf, R * max_out + R, {R}, at::kInt);
   const dsa_status s = verify_draft_fn(ptr<float>(p), rows > 1 ? p->stride(0) : V, (int32_t)rows, (int32_t)V,
                                        ptr<float>(q), q && rows > 1 ? q->stride(0) : V, ptr<int32_t>(tok),
                                        ptr<float>(ua), ptr<float>(us), ptr<int32_t>(cu), (int32_t)R, max_out,
