@@ -19,7 +19,7 @@ __all__ = ["DsaError", "load_library", "topk_select", "sparse_mla_fwd", "combine
            "topk_sparse_mla_fwd", "two_kernel_path_supported", "sparse_mla_topk_fused", "fused_path_supported",
            "kv_write",
            "PrefixCache", "BatchLayout", "batch_layout", "qk_norm_rope", "chunk_mla_fwd", "chunk_mla", "verify_draft",
-           "kv_tile_count", "kv_tile_size", "pick_num_splits", "status_string", "EXPORTED_SYMBOLS",
+           "kv_tile_count", "kv_tile_size", "pick_num_splits", "pick_chunk_splits", "status_string", "EXPORTED_SYMBOLS",
            "DEV_BAD_QPOS", "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_TIMEOUT", "DEV_NO_PAGES"]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,7 +34,8 @@ EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_
                     "dsa_combine", "dsa_kv_write", "dsa_batch_layout", "dsa_qk_norm_rope", "dsa_chunk_mla_fwd",
                     "dsa_verify_draft", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
                     "dsa_prefix_cache_acquire", "dsa_prefix_cache_release", "dsa_prefix_cache_stats",
-                    "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits")
+                    "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits",
+                    "dsa_chunk_pick_num_splits")
 
 _lock = threading.Lock()
 _lib = None
@@ -115,6 +116,8 @@ def load_library(path: str | None = None):
         lib.dsa_kv_tile_size.restype = i32
         lib.dsa_pick_num_splits.argtypes = [i32, i32, i32, i32, i32, i32]
         lib.dsa_pick_num_splits.restype = i32
+        lib.dsa_chunk_pick_num_splits.argtypes = [i32, i32, i32, i32, i32, i32]
+        lib.dsa_chunk_pick_num_splits.restype = i32
         global _fast
         _fast = _load_marshal(lib)
         _lib = lib
@@ -138,7 +141,7 @@ def _load_marshal(lib):
     loader.exec_module(m)
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
              for f in (lib.dsa_batch_layout, lib.dsa_qk_norm_rope, lib.dsa_chunk_mla_fwd, lib.dsa_combine,
-                       lib.dsa_pick_num_splits, lib.dsa_verify_draft)))
+                       lib.dsa_chunk_pick_num_splits, lib.dsa_verify_draft)))
     return m
 
 
@@ -156,6 +159,12 @@ def kv_tile_size(heads: int, d_latent: int, d_rope: int) -> int:
 
 def pick_num_splits(num_q: int, heads: int, d_latent: int, d_rope: int, k: int, num_sms: int = 0) -> int:
     return load_library().dsa_pick_num_splits(num_q, heads, d_latent, d_rope, k, num_sms)
+
+
+def pick_chunk_splits(num_q: int, heads: int, d_latent: int, d_rope: int, max_ctx: int, num_sms: int = 0) -> int:
+    """KV splits chunk_mla takes for contexts of about max_ctx positions."""
+    return load_library().dsa_chunk_pick_num_splits(num_q, heads, d_latent, d_rope, max(1, min(max_ctx, 2**31 - 1)),
+                                                    num_sms)
 
 
 def _p(t: torch.Tensor | None):
@@ -760,11 +769,12 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
 
 
 def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_rope: int, page_size: int,
-                  softmax_scale: float, num_splits: int = 1, out=None, lse=None, o_part=None, lse_part=None,
-                  dev_status=None, stream=None):
+                  softmax_scale: float, num_splits: int = 1, merge: bool = False, out=None, lse=None, o_part=None,
+                  lse_part=None, dev_status=None, stream=None):
     """Attention of each token to all positions 0..q_pos of its request
-    (dsa_chunk_mla_fwd).  num_splits == 1: returns (out bf16, lse fp32).
-    num_splits > 1: returns (o_part fp32 [S, ...], lse_part fp32 [S, ...])."""
+    (dsa_chunk_mla_fwd).  num_splits == 1, or ``merge`` with at most 8 splits:
+    returns (out bf16, lse fp32).  Else returns (o_part fp32 [S, ...],
+    lse_part fp32 [S, ...]) for combine."""
     dev = _device_of(q, "q")
     _need(q, "q", _BF16, 3, dev)
     _need(kv, "kv", _U8, 2, dev)
@@ -779,7 +789,8 @@ def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, 
     if q_req.shape[0] != num_q or q_pos.shape[0] != num_q or kv_scale.shape[0] != slots:
         raise ValueError("inconsistent shapes")
     op = lp = oo = ll = None
-    if num_splits == 1:
+    whole = num_splits == 1 or merge
+    if whole:
         if out is None:
             out = torch.empty((num_q, H, d_latent), dtype=_BF16, device=q.device)
         else:
@@ -806,14 +817,15 @@ def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, 
     _run(dev, stream, "dsa_chunk_mla_fwd", q.data_ptr(), kv.data_ptr(), kv_scale.data_ptr(), slots // page_size,
          block_table.data_ptr(), block_table.shape[0], block_table.shape[1], q_req.data_ptr(), q_pos.data_ptr(), num_q,
          H, d_latent, d_rope, page_size, float(softmax_scale), num_splits, oo, ll, op, lp, _status_ptr(dev_status, dev))
-    return (out, lse) if num_splits == 1 else (o_part, lse_part)
+    return (out, lse) if whole else (o_part, lse_part)
 
 
 def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_rope: int, page_size: int,
               softmax_scale: float, max_ctx: int | None = None, num_splits: int | None = None,
               buffers: dict | None = None, dev_status=None, stream=None):
-    """The whole pass over every visible position: chunk_mla_fwd, then combine
-    when split.  ``max_ctx`` (default: the block table's width) is about the
+    """The whole pass over every visible position: chunk_mla_fwd, merging its
+    splits or, with more than 8 or where ``buffers`` holds partials, followed by
+    combine.  ``max_ctx`` (default: the block table's width) is about the
     longest context, from which the number of KV splits is picked when
     ``num_splits`` is None; the result is right for any value.  ``buffers``
     (optional) holds preallocated out / lse / o_part / lse_part tensors.
@@ -828,12 +840,13 @@ def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_ro
             return _done("dsa_chunk_mla_fwd", r)
     num_q, H, _ = q.shape
     if num_splits is None:
-        num_splits = pick_num_splits(num_q, H, d_latent, d_rope, max(1, min(max_ctx, 2**31 - 1)))
+        num_splits = pick_chunk_splits(num_q, H, d_latent, d_rope, max_ctx)
     out, lse = b.get("out"), b.get("lse")
-    if num_splits == 1 or num_q == 0:
+    merge = 1 < num_splits <= 8 and b.get("o_part") is None and b.get("lse_part") is None
+    if num_splits == 1 or merge or num_q == 0:
         return chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
-                             page_size=page_size, softmax_scale=softmax_scale, out=out, lse=lse, dev_status=dev_status,
-                             stream=stream)
+                             page_size=page_size, softmax_scale=softmax_scale, num_splits=num_splits if merge else 1,
+                             merge=merge, out=out, lse=lse, dev_status=dev_status, stream=stream)
     op, lp = chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, d_latent=d_latent, d_rope=d_rope,
                            page_size=page_size, softmax_scale=softmax_scale, num_splits=num_splits,
                            o_part=b.get("o_part"), lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)

@@ -85,6 +85,39 @@ int32_t dsa_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, 
   return best;
 }
 
+int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope, int32_t max_ctx,
+                                  int32_t num_sms) {
+  const int32_t tile = dsa_kv_tile_size(num_heads, d_latent, d_rope);
+  if (tile <= 0 || num_q <= 0 || max_ctx <= 0) return 1;
+  if (num_sms <= 0) num_sms = dsa::device_sm_count();
+  const bool tc = use_tensor_cores(num_heads, d_latent, d_rope);
+  // In hundredths of a tile's time (measured: 0.93 us on the tensor cores, 2.0 us
+  // of 32 rows on the CUDA cores): a CTA's start and end; the merge in a cluster;
+  // the Combine, which reads more the more splits there are.
+  const int64_t fixed = tc ? 800 : 150, merge = tc ? 500 : 50, combine = tc ? 600 : 70, combine_split = tc ? 22 : 10;
+  // clusters of S CTAs that run at once, one CTA per SM, of 152 SMs
+  // (cudaOccupancyMaxActiveClusters); the CUDA-core kernel's CTAs are small, and
+  // two to an SM still gain
+  static const int32_t clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  const int64_t ntiles = dsa_kv_tile_count(max_ctx, tile);
+  int32_t best = 1;
+  int64_t best_cost = -1;
+  for (int32_t s = 1; s <= 64 && s <= ntiles; ++s) {
+    int64_t waves;
+    if (tc && s <= 8) {
+      const int64_t cap = (int64_t)clusters[s] * num_sms / 152;
+      waves = cap > 0 ? (num_q + cap - 1) / cap : num_q;
+    } else {
+      const int64_t cap = tc ? num_sms : 2 * (int64_t)num_sms;
+      waves = ((int64_t)num_q * s + cap - 1) / cap;
+    }
+    const int64_t per = 100 * ((ntiles + s - 1) / s);
+    const int64_t cost = waves * (per + fixed) + (s == 1 ? 0 : s <= 8 ? merge : combine + s * combine_split);
+    if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
+  }
+  return best;
+}
+
 size_t dsa_sparse_mla_workspace_size(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope,
                                      int32_t k) {
   if (num_q <= 0 || k <= 0 || !use_tensor_cores(num_heads, d_latent, d_rope)) return 0;
@@ -397,15 +430,20 @@ dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_s
                              int32_t page_size, float softmax_scale, int32_t num_splits, void* out, float* lse,
                              float* o_part, float* lse_part, int32_t* dev_status, void* stream) {
   dsa::MlaArgs a;
+  // splits without partials are merged by the call itself
+  const bool merge = num_splits > 1 && !o_part && !lse_part;
+  if (merge && num_splits > dsa::chunk_max_merged()) return DSA_ERR_INVALID_ARG;
   // q_pos stands in for idx in the checks; k is unused
   const dsa_status st = check_mla_args(q, kv, kv_scale, num_pages, block_table, num_req, bt_stride, q_req, q_pos,
-                                       num_q, num_heads, d_latent, d_rope, page_size, 1, softmax_scale, num_splits,
-                                       out, lse, o_part, lse_part, 0, nullptr, 0, dev_status, &a);
+                                       num_q, num_heads, d_latent, d_rope, page_size, 1, softmax_scale,
+                                       merge ? 1 : num_splits, out, lse, o_part, lse_part, 0, nullptr, 0, dev_status,
+                                       &a);
   if (st != DSA_OK || num_q == 0) return st;
   a.idx = nullptr;
-  if (use_tensor_cores(num_heads, d_latent, d_rope))
-    return from_cuda(dsa::launch_chunk_tc(a, q_pos, static_cast<cudaStream_t>(stream)));
-  return from_cuda(dsa::launch_chunk_simt(a, q_pos, static_cast<cudaStream_t>(stream)));
+  a.num_splits = num_splits;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (use_tensor_cores(num_heads, d_latent, d_rope)) return from_cuda(dsa::launch_chunk_tc(a, q_pos, merge, s));
+  return from_cuda(dsa::launch_chunk_simt(a, q_pos, merge, s));
 }
 
 dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,

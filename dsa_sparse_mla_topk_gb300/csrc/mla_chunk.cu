@@ -38,6 +38,7 @@
 // than 2^3.8, E when a row's scale passes its bound; l is summed in fp32 from unrounded
 // p.  (Of 64 heads some reference then moves in few tiles; with 2^2 152 tokens of
 // 4,096 took 92 instead of 72 us.)  All waits are bounded.
+#include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -48,6 +49,8 @@
 #include "internal.cuh"
 #include "mla_tc_common.cuh"
 #include "sm100_ptx.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace dsa {
 namespace {
@@ -65,6 +68,7 @@ constexpr int QM = 2 * H;
 constexpr int QROPE_BYTES = QM * DR;
 constexpr int P_BYTES = H * T;  // P_hi (or P_lo) of a tile: [head][row], K-major, 64-byte swizzle
 constexpr int NPB = 2;
+constexpr int MAX_MERGED = chunk_max_merged();
 constexpr int SM_WARPS = 16, SM_THREADS = SM_WARPS * 32;
 constexpr float SCALE_BOUND = 32.0f;     // s_j 2^E < 32, and
 constexpr float EXCEED_LOG2 = 3.8f;      // p = 2^(z - m) <= 2^3.8 < 14: P' < 448, the largest E4M3 value
@@ -85,7 +89,8 @@ constexpr int OFF_RED = OFF_P + NPB * 2 * P_BYTES;    // [4 row parts][64 heads]
 constexpr int OFF_ALPHA = OFF_RED + 4 * H * 4;        // per-head factor of O, then 1 / l
 constexpr int OFF_SROW = OFF_ALPHA + H * 4;           // [NST][64] the tiles' row scales
 constexpr int OFF_INFO = OFF_SROW + NST * T * 4;      // [NST][2] valid rows (bits) and largest scale of each 32 rows
-constexpr int OFF_FLAG = OFF_INFO + NST * 2 * 8;      // O flags [4], Q exponent, vote flags [4]
+constexpr int OFF_ML = OFF_INFO + NST * 2 * 8;         // [2][64] for the cluster's merge
+constexpr int OFF_FLAG = OFF_ML + 2 * H * 4;      // O flags [4], Q exponent, vote flags [4]
 constexpr int OFF_BAR = OFF_FLAG + 128;
 constexpr int B_KVF = 0;               // [NST] the tile in stage s has landed
 constexpr int B_KVE = B_KVF + NST;     // [NST] stage s is free
@@ -102,6 +107,7 @@ static_assert(2 * STAGE_BYTES == H * DQK * 2, "bf16 Q fills two KV stages");
 constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
 constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;  // with alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(H * DL * 4 <= NST * STAGE_BYTES && MAX_MERGED * H * 4 <= NPB * 2 * P_BYTES, "the merge's O and factors");
 static_assert(OFF_QR % 1024 == 0 && OFF_P % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
 
 struct ChunkMaps {
@@ -110,7 +116,9 @@ struct ChunkMaps {
 };
 
 // NTMA TMA warps (0 .. NTMA - 1), then the MMA warp, then the softmax warps.
-template <int NTMA>
+// MERGE: a token's splits are the CTAs of a thread-block cluster and merge
+// their results over distributed shared memory (no partials, no Combine kernel).
+template <int NTMA, bool MERGE>
 __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     mla_chunk_kernel(const MlaArgs a, const int32_t* __restrict__ q_pos, const __grid_constant__ ChunkMaps maps,
                      const int box_rows, const FastDiv page_div) {
@@ -149,13 +157,17 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
   const int t_begin = (int)((int64_t)ntiles * split / S), t_end = (int)((int64_t)ntiles * (split + 1) / S);
   const int ntl = t_end - t_begin;
 
-  if (ntl == 0) {  // nothing to see: O = 0, lse = -inf
+  float* ml_s = reinterpret_cast<float*>(smem + OFF_ML);  // MERGE: [64] references, [64] l
+  // A split without tiles goes the whole way (no tile, l = 0) where the
+  // cluster's other CTAs need its answer.
+  if (MERGE ? n == 0 : ntl == 0) {  // nothing to see: O = 0, lse = -inf
+    if (MERGE && split > 0) return;
     for (int e = tid; e < H * DL; e += NTHREADS) {
-      if (S == 1) static_cast<__nv_bfloat16*>(a.out)[(int64_t)i * H * DL + e] = __float2bfloat16_rn(0.f);
+      if (MERGE || S == 1) static_cast<__nv_bfloat16*>(a.out)[(int64_t)i * H * DL + e] = __float2bfloat16_rn(0.f);
       else a.o_part[((int64_t)split * a.num_q + i) * H * DL + e] = 0.f;
     }
     for (int h = tid; h < H; h += NTHREADS) {
-      if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + h] = -INFINITY;
+      if (!MERGE && S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + h] = -INFINITY;
       else if (a.lse) a.lse[(int64_t)i * H + h] = -INFINITY;
     }
     return;
@@ -631,9 +643,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     group_sync();
     if (part == 0 && up == 0) {
       const float l = (red_s[hh] + red_s[H + hh]) + (red_s[2 * H + hh] + red_s[3 * H + hh]);
-      alpha_s[hh] = l > 0.f ? ldexpf(1.f / l, -p_exp) : 0.f;
+      alpha_s[hh] = l > 0.f ? ldexpf(MERGE ? 1.f : 1.f / l, -p_exp) : 0.f;
       const float lse = l > 0.f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
-      if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
+      if (MERGE) ml_s[hh] = ok && l > 0.f ? m_ref : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
+      else if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
       else if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
     }
     group_sync();
@@ -649,7 +662,11 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         float o[16];
         tmem_ld16(t_lane + TM_O + 64 * c + 16 * part, o);
         tmem_wait_ld();
-        if (S == 1) {
+        if (MERGE) {  // O 2^-E into the idle KV stages, [head][dim]
+          float* os = reinterpret_cast<float*>(smem + OFF_KV) + 16 * part * DL + d;
+#pragma unroll
+          for (int h = 0; h < 16; ++h) os[h * DL] = o[h] * inv[h];
+        } else if (S == 1) {
           __nv_bfloat16* ob = static_cast<__nv_bfloat16*>(a.out) + ((int64_t)i * H + 16 * part) * DL + d;
 #pragma unroll
           for (int h = 0; h < 16; ++h) ob[h * DL] = __float2bfloat16_rn(o[h] * inv[h]);
@@ -671,11 +688,55 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     tc_fence_after_sync();
     tmem_dealloc(tmem, TM_COLS);
   }
+
+  if constexpr (MERGE) {
+    // ---------------- the cluster's splits together ----------------
+    //   out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    float* fac = reinterpret_cast<float*>(smem + OFF_P);  // [S][64] factors of the splits' O (the P buffers are idle)
+    if (tid < H) {
+      float m = -INFINITY, l = 0.f;
+      for (int s = 0; s < S; ++s) m = fmaxf(m, *cluster.map_shared_rank(ml_s + tid, s));
+      for (int s = 0; s < S; ++s) {
+        const float ms = *cluster.map_shared_rank(ml_s + tid, s);
+        const float w = ms == -INFINITY ? 0.f : ex2(ms - m);
+        l = fmaf(w, *cluster.map_shared_rank(ml_s + H + tid, s), l);
+        fac[s * H + tid] = w;
+      }
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      for (int s = 0; s < S; ++s) fac[s * H + tid] *= inv;
+      if (split == 0 && a.lse) a.lse[(int64_t)i * H + tid] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+    }
+    __syncthreads();
+    // each CTA a share of the token's values, four at a time
+    const float* os = reinterpret_cast<const float*>(smem + OFF_KV);
+    for (int e = split * NTHREADS + tid; e < H * DL / 4; e += S * NTHREADS) {
+      const int h = e / (DL / 4);
+      float4 v[MAX_MERGED];
+#pragma unroll
+      for (int s = 0; s < MAX_MERGED; ++s) {
+        // (an empty split's O was never written)
+        if (s < S && fac[s * H + h] != 0.f) v[s] = reinterpret_cast<const float4*>(cluster.map_shared_rank(os, s))[e];
+        else v[s] = make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int s = 0; s < MAX_MERGED; ++s) {
+        const float f = s < S ? fac[s * H + h] : 0.f;
+        o.x = fmaf(f, v[s].x, o.x), o.y = fmaf(f, v[s].y, o.y), o.z = fmaf(f, v[s].z, o.z), o.w = fmaf(f, v[s].w, o.w);
+      }
+      __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + (int64_t)i * H * DL) + 2 * e;
+      ob[0] = __floats2bfloat162_rn(o.x, o.y);
+      ob[1] = __floats2bfloat162_rn(o.z, o.w);
+    }
+    cluster.sync();  // no CTA leaves while another reads its shared memory
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream) {
+cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, bool merge, cudaStream_t stream) {
   if (a.num_q == 0) return cudaSuccess;
   // the largest box of rows that never leaves a page (gather4 takes pages that no multiple of 8 fits)
   int box = T;
@@ -695,11 +756,23 @@ cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, cudaStream_t
   auto launch = [&](auto kern, int ntma) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(a.num_q, a.num_splits), (ntma + 1 + SM_WARPS) * 32, SMEM_BYTES, stream>>>(a, q_pos, maps, box,
-                                                                                         make_fast_div(a.page_size));
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = merge ? (unsigned)a.num_splits : 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.num_q, a.num_splits);
+    cfg.blockDim = dim3((ntma + 1 + SM_WARPS) * 32);
+    cfg.dynamicSmemBytes = SMEM_BYTES;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = merge ? 1 : 0;
+    const cudaError_t st = cudaLaunchKernelEx(&cfg, kern, a, q_pos, maps, box, make_fast_div(a.page_size));
+    return st != cudaSuccess ? st : cudaGetLastError();
   };
-  return box >= 16 ? launch(mla_chunk_kernel<3>, 3) : launch(mla_chunk_kernel<7>, 7);
+  if (merge) return box >= 16 ? launch(mla_chunk_kernel<3, true>, 3) : launch(mla_chunk_kernel<7, true>, 7);
+  return box >= 16 ? launch(mla_chunk_kernel<3, false>, 3) : launch(mla_chunk_kernel<7, false>, 7);
 }
 
 }  // namespace dsa

@@ -23,7 +23,7 @@ decltype(&dsa_batch_layout) batch_layout_fn = nullptr;
 decltype(&dsa_qk_norm_rope) qk_norm_rope_fn = nullptr;
 decltype(&dsa_chunk_mla_fwd) chunk_mla_fn = nullptr;
 decltype(&dsa_combine) combine_fn = nullptr;
-decltype(&dsa_pick_num_splits) pick_fn = nullptr;
+decltype(&dsa_chunk_pick_num_splits) pick_fn = nullptr;
 decltype(&dsa_verify_draft) verify_draft_fn = nullptr;
 
 // Reads a call's arguments; `good` is false once one is not as documented.
@@ -248,7 +248,7 @@ PyObject* chunk_mla(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   const at::Tensor out = cut(buf, 0, {n, H, dl}, at::kBFloat16), lse = cut(buf, ob / 4, {n, H}, at::kFloat);
   at::Tensor parts;
   float *op = nullptr, *lp = nullptr;
-  if (S > 1) {
+  if (S > 8) {  // (fewer are merged by the call)
     const int64_t pn = ((int64_t)S * n * H * dl + 3) / 4 * 4;
     parts = at::empty({pn + (int64_t)S * n * H}, sc->options());
     op = ptr<float>(&parts);
@@ -257,9 +257,9 @@ PyObject* chunk_mla(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   void* stream = a.stream();
   dsa_status s = chunk_mla_fn(q->data_ptr(), ptr<uint8_t>(kv), ptr<float>(sc), slots / page, ptr<int32_t>(bt),
                               (int32_t)bt->size(0), (int32_t)bt->size(1), ptr<int32_t>(req), ptr<int32_t>(pos),
-                              (int32_t)n, (int32_t)H, dl, dr, page, scale, S, S == 1 ? out.data_ptr() : nullptr,
-                              S == 1 ? ptr<float>(&lse) : nullptr, op, lp, st, stream);
-  if (s == DSA_OK && S > 1)
+                              (int32_t)n, (int32_t)H, dl, dr, page, scale, S, op ? nullptr : out.data_ptr(),
+                              op ? nullptr : ptr<float>(&lse), op, lp, st, stream);
+  if (s == DSA_OK && op)
     s = combine_fn(op, lp, S, (int32_t)n, (int32_t)H, dl, out.data_ptr(), ptr<float>(&lse), stream);
   if (s != DSA_OK) return PyLong_FromLong(s);
   return tuple_of({&out, &lse});
@@ -306,7 +306,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(batch_layout, qk_norm_rope, chunk_mla_fwd, combine, pick_num_splits, verify_draft): the entry points' addresses
+// bind(batch_layout, qk_norm_rope, chunk_mla_fwd, combine, chunk_pick_num_splits, verify_draft): the entry points' addresses
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (argc != 6) {
     PyErr_SetString(PyExc_TypeError, "bind takes 6 addresses");

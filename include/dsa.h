@@ -416,7 +416,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t
  *
  * Arguments, layouts, outputs and splits are those of dsa_sparse_mla_fwd, with
  * q_pos (int32 [num_q]) in place of idx and k, and no workspace.  A split takes
- * a contiguous share of the token's own KV tiles.  A token with q_req = -1
+ * a contiguous share of the token's own KV tiles.  With 2 to 8 splits and
+ * o_part and lse_part both NULL the call merges them itself (the splits of a
+ * token are one thread-block cluster) and writes out and lse; else the splits
+ * write o_part and lse_part for dsa_combine.  A token with q_req = -1
  * (padding) or q_pos = -1 sees nothing: out = 0 and lse = -inf.  Tokens of one
  * request next to each other share its rows in L2; any order is correct.
  * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
@@ -532,6 +535,15 @@ DSA_API int32_t dsa_kv_tile_count(int32_t width, int32_t tile);
 DSA_API int32_t dsa_kv_tile_size(int32_t num_heads, int32_t d_latent, int32_t d_rope);
 DSA_API int32_t dsa_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope, int32_t k,
                             int32_t num_sms);
+
+/*
+ * dsa_chunk_pick_num_splits: KV splits per token for dsa_chunk_mla_fwd over
+ * contexts of about max_ctx positions: the number with the least estimated
+ * time, from the tiles of a split, a CTA's fixed cost, the waves of CTAs (of clusters,
+ * for the 2 to 8 splits that the call merges) and the merge or Combine.
+ */
+DSA_API int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope,
+                                          int32_t max_ctx, int32_t num_sms);
 
 #ifdef __cplusplus
 }

@@ -527,6 +527,32 @@ def test_chunk_matches_the_oracle(shape, lens, new, page):
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"h{s[0]}")
+@pytest.mark.parametrize("page", [64, 5])
+def test_chunk_splits_merged_by_the_call_and_by_combine(shape, page):
+    """2 to 8 splits, more than some tokens have tiles, padding and empty tokens among
+    them: merged in the call, and as partials through combine."""
+    c = _chunk_case(*shape, [700, 40, 130], [2, 1, 3], page, seed=21, pad=2)
+    c["pos"][1] = -1
+    want = _chunk_ref(c)
+    g = _cuda(c)
+    args = (g["q"], g["kv"], g["sc"], g["table"], g["req"], g["pos"])
+    kw = dict(d_latent=c["dl"], d_rope=c["dr"], page_size=page, softmax_scale=c["scale"])
+    for S in range(2, 10):
+        out, lse, st = _run_chunk(c, S)
+        assert st == 0
+        _check_chunk(out, lse, want)
+        if S <= 8:
+            st = torch.zeros(1, dtype=I32, device="cuda")
+            _check_chunk(*dsa.chunk_mla_fwd(*args, num_splits=S, merge=True, dev_status=st, **kw), want)
+        _check_chunk(*dsa.combine(*dsa.chunk_mla_fwd(*args, num_splits=S, **kw)), want)
+        n, H = g["q"].shape[:2]
+        buf = dict(o_part=torch.empty((S, n, H, c["dl"]), device="cuda"), lse_part=torch.empty((S, n, H), device="cuda"))
+        _check_chunk(*dsa.chunk_mla(*args, num_splits=S, buffers=buf, **kw), want)
+    with pytest.raises(dsa.DsaError):
+        dsa.chunk_mla_fwd(*args, num_splits=9, merge=True, **kw)
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"h{s[0]}")
 def test_chunk_long_context_every_split_count(shape):
     c = _chunk_case(*shape, [5000, 2611], [1, 2], 64, seed=3)
     want = _chunk_ref(c)

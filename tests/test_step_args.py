@@ -82,7 +82,7 @@ def _chunk(lib, **over):
 @no_device_only
 @pytest.mark.parametrize("over,expect", [
     (dict(H=32), 2), (dict(dl=256), 2), (dict(dr=32), 2), (dict(P=0), 1), (dict(n=-1), 1), (dict(S=0), 1),
-    (dict(S=65), 1), (dict(q=None), 1), (dict(kv=None), 1), (dict(sc=None), 1), (dict(bt=None), 1), (dict(req=None), 1),
+    (dict(S=65), 1), (dict(S=9), 1), (dict(S=4, op=A(8)), 1), (dict(S=4, out=None), 1), (dict(q=None), 1), (dict(kv=None), 1), (dict(sc=None), 1), (dict(bt=None), 1), (dict(req=None), 1),
     (dict(pos=None), 1), (dict(out=None), 1), (dict(q=MISALIGNED), 1), (dict(kv=MISALIGNED), 1),
     (dict(out=MISALIGNED), 1), (dict(scale=float("inf")), 1), (dict(S=4, lp=A(8)), 1),
     (dict(S=4, op=MISALIGNED, lp=A(8)), 1), (dict(np=0), 1), (dict(np=1 << 26), 2), (dict(R=0), 1), (dict(n=0), 0),
@@ -108,6 +108,25 @@ def _verify(lib, **over):
 ])
 def test_verify_argument_checks(lib, over, expect):
     assert _verify(lib, **over) == expect
+
+
+def test_chunk_split_rule(lib):
+    """The rule on 152 SMs: no split once the tokens fill the GPU or the context is
+    a few tiles; clusters that run in one wave; many splits for one long context."""
+    pick = lambda n, ctx, H=64: dsa.pick_chunk_splits(n, H, 512 if H == 64 else 64, 64 if H == 64 else 16, ctx, 152)  # noqa: E731
+    assert pick(152, 16384) == pick(1024, 16384) == pick(128, 4096) == 1
+    assert pick(1, 1) == pick(1, 64) == pick(1, 256) == 1
+    assert pick(1, 65536) >= 32
+    assert pick(32, 8192) == 4 and pick(32, 1024) == 4 and pick(24, 4096) == 5 and pick(48, 4096) == 2
+    assert pick(2, 512, 16) == 8 and pick(128, 1024, 16) <= 4
+    for n in (1, 3, 15, 16, 23, 24, 36, 37, 76, 77, 200):
+        for ctx in (1, 63, 64, 65, 1000, 5000, 100000):
+            s = pick(n, ctx)
+            assert 1 <= s <= min(64, -(-ctx // 64))
+            if 2 <= s <= 8 and ctx <= 1000:
+                assert n <= {2: 76, 3: 46, 4: 36, 5: 28, 6: 23, 7: 15, 8: 15}[s]
+    assert dsa.pick_chunk_splits(4, 32, 512, 64, 2048, 152) == 1  # unsupported heads
+    assert dsa.pick_chunk_splits(0, 64, 512, 64, 2048, 152) == 1
 
 
 def test_binding_rejects_cpu_tensors_and_types(lib):
