@@ -493,37 +493,36 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
 
     // ---- the tiles ----
     float m_ref = -INFINITY;      // head hh's reference maximum (log2 domain), the same in its 8 threads
-    uint64_t l2 = pk2(0.f, 0.f);  // head hh's share of l, two running sums
+    uint64_t l2 = pk2(0.f, 0.f);  // head hh's share of l 2^E, two running sums
     int p_exp = 0;                // E, the same in every thread; set at the first row with a scale
     float p_scale = 1.f;          // 2^E
+    float shift = 0.f;            // E - m_ref (m_ref = -inf: E)
     bool p_set = false;
     const uint64_t qk2 = pk2(qk_scale, qk_scale);
     int stage = 0, kv_phase = 0;
+    const uint32_t vote_b = bar(B_VOTE);
     for (int lt = 0; lt < ntl; ++lt) {  // no early exit: every warp reaches every barrier
       const int sb = lt & 1;
-      if (ok && !wait_warp(B_KVF + stage, kv_phase)) ok = false;  // (the row scales; landed before S is computed)
-      const float4* s4 = reinterpret_cast<const float4*>(srow + stage * T + 16 * part + 8 * up);
-      const uint2 inf = info[stage * 2 + (part >> 1)];
+      if (ok && !wait_warp(B_KVF + stage, kv_phase)) ok = false;  // the tile's row scales
       if (ok && !wait_warp(B_SF + sb, (lt >> 1) & 1)) ok = false;
+      float sj[8];  // the rows' scales
+      {
+        const float4* s4 = reinterpret_cast<const float4*>(srow + stage * T + 16 * part + 8 * up);
+        const float4 lo = s4[0], hi = s4[1];
+        sj[0] = lo.x, sj[1] = lo.y, sj[2] = lo.z, sj[3] = lo.w, sj[4] = hi.x, sj[5] = hi.y, sj[6] = hi.z, sj[7] = hi.w;
+      }
+      const uint2 inf = info[stage * 2 + (part >> 1)];
       tc_fence_after_sync();
       float z[8];  // (S_hi + S_lo) s_j of head hh, rows 16 part + 8 up + c (invalid: -inf)
       {
-        float v[16];
-        tmem_ld16(t_lane + TM_S + T * sb + 16 * part, v);
+        // lanes 0-15 of the quadrant hold the heads' S_hi, lanes 16-31 their S_lo
+        float vh[8], vl[8];
+        tmem_ld8x2(t_lane + TM_S + T * sb + 16 * part, vh);
+        tmem_ld8x2(t_lane + (16u << 16) + TM_S + T * sb + 16 * part, vl);
         tmem_wait_ld();
-        float got[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) got[c] = __shfl_xor_sync(0xffffffffu, up ? v[c] : v[8 + c], 16);
-#pragma unroll
-        for (int k4 = 0; k4 < 2; ++k4) {
-          const float4 f = s4[k4];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int c = 4 * k4 + 2 * t;
-            const uint64_t mine = up ? pk2(v[8 + c], v[9 + c]) : pk2(v[c], v[c + 1]);
-            upk2(mul2(add2(mine, pk2(got[c], got[c + 1])), t ? pk2(f.z, f.w) : pk2(f.x, f.y)), z[c], z[c + 1]);
-          }
-        }
+        for (int c = 0; c < 8; c += 2)
+          upk2(mul2(add2(pk2(vh[c], vh[c + 1]), pk2(vl[c], vl[c + 1])), pk2(sj[c], sj[c + 1])), z[c], z[c + 1]);
         if (inf.x != 0xffffffffu) {  // a tile with rows past the last position, or bad pages
           const unsigned my_valid = inf.x >> (16 * (part & 1) + 8 * up);
 #pragma unroll
@@ -547,27 +546,20 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       uint32_t phi[4], plo[4];
       uint64_t ln;
       for (bool again = false;; again = true) {
-        // weights, folded with the row's scale and 2^E, as E4M3 + E5M2
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;
-        const uint64_t nm2 = pk2(-m_use, -m_use), ps2 = pk2(p_scale, p_scale);
+        // p 2^E, summed into l; folded with the row's scale, as E4M3 + E5M2
+        const uint64_t shift2 = pk2(shift, shift);
         ln = l2;
 #pragma unroll
-        for (int k4 = 0; k4 < 2; ++k4) {
-          const float4 f = s4[k4];
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const int c = 4 * k4 + 2 * t;
-            float d0, d1;
-            upk2(fma2(pk2(z[c], z[c + 1]), qk2, nm2), d0, d1);
-            const uint64_t p = pk2(ex2(d0), ex2(d1));
-            ln = add2(ln, p);
-            float w0, w1;
-            upk2(mul2(p, mul2(t ? pk2(f.z, f.w) : pk2(f.x, f.y), ps2)), w0, w1);
-            split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
-          }
+        for (int c = 0; c < 8; c += 2) {
+          float d0, d1, w0, w1;
+          upk2(fma2(pk2(z[c], z[c + 1]), qk2, shift2), d0, d1);
+          const uint64_t p = pk2(ex2(d0), ex2(d1));
+          ln = add2(ln, p);
+          upk2(mul2(p, pk2(sj[c], sj[c + 1])), w0, w1);
+          split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
         }
         if (again) break;
-        if (!mbar_wait(bar(B_VOTE), lt & 1, 4 * MBAR_LIMIT_NS)) ok = false;
+        if (!mbar_wait(vote_b, lt & 1, 4 * MBAR_LIMIT_NS)) ok = false;
         ok = __all_sync(0xffffffffu, ok);
         if (vote_s[lt & 3] == 0) break;
         // ---- move the references that were passed, and E; rescale O and l ----
@@ -581,16 +573,17 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
           alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mt);
           m_ref = mt;
         }
-        l2 = mul2(l2, pk2(alpha, alpha));
         if (sm > 0.f && sm <= 3.0e38f && (!p_set || sm * p_scale >= SCALE_BOUND)) {
           int e2;
           frexpf(sm, &e2);  // sm < 2^e2: sm 2^E in [16, 32)
-          const int e = min(5 - e2, 120);  // (2^E stays finite for subnormal scales)
-          if (p_set) alpha *= ldexpf(1.f, e - p_exp);  // O carries 2^E
+          const int e = min(5 - e2, 80);  // (sums of 2^E stay finite for subnormal scales)
+          alpha *= ldexpf(1.f, e - p_exp);  // O and l carry 2^E
           p_exp = e;
           p_set = true;
           p_scale = ldexpf(1.f, p_exp);
         }
+        l2 = mul2(l2, pk2(alpha, alpha));
+        shift = (float)p_exp - (m_ref == -INFINITY ? 0.f : m_ref);
         if (part == 0 && up == 0) alpha_s[hh] = alpha;
         const unsigned need = __ballot_sync(0xffffffffu, lt > 0 && alpha != 1.f);
         if (part == 0 && lane == 0) resc_s[q4] = need != 0u;
@@ -643,9 +636,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     group_sync();
     if (part == 0 && up == 0) {
       const float l = (red_s[hh] + red_s[H + hh]) + (red_s[2 * H + hh] + red_s[3 * H + hh]);
-      alpha_s[hh] = l > 0.f ? ldexpf(MERGE ? 1.f : 1.f / l, -p_exp) : 0.f;
-      const float lse = l > 0.f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
-      if (MERGE) ml_s[hh] = ok && l > 0.f ? m_ref : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
+      // (O and l both carry 2^E)
+      alpha_s[hh] = l > 0.f ? (MERGE ? 1.f : 1.f / l) : 0.f;
+      const float lse = l > 0.f ? (m_ref - (float)p_exp + log2f(l)) * LN2 : -INFINITY;
+      if (MERGE) ml_s[hh] = ok && l > 0.f ? m_ref - (float)p_exp : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
       else if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
       else if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
     }
@@ -662,7 +656,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         float o[16];
         tmem_ld16(t_lane + TM_O + 64 * c + 16 * part, o);
         tmem_wait_ld();
-        if (MERGE) {  // O 2^-E into the idle KV stages, [head][dim]
+        if (MERGE) {  // O into the idle KV stages, [head][dim]
           float* os = reinterpret_cast<float*>(smem + OFF_KV) + 16 * part * DL + d;
 #pragma unroll
           for (int h = 0; h < 16; ++h) os[h * DL] = o[h] * inv[h];
