@@ -29,8 +29,8 @@
 // Q = Q_hi + Q_lo is exact for bf16 (two E4M3 numbers of a token scaled by a
 // power of two).  A weight P' = p s_j 2^E is E4M3 + E5M2.  The reference weight (p =
 // 1) of the row with the largest scale is at 16 or more, so that weights down to
-// 2^-10 of it have a relative error of at most 2^-7 (0.2% root mean square,
-// like a 16-bit weight's); smaller ones an absolute one of 2^-14, and only
+// 2^-10 of it have a relative error of at most 2^-8 (0.12% root mean square,
+// a bf16 weight's is 0.08%); smaller ones an absolute one of 2^-14, and only
 // below 2^-21 nothing is left of them.  A second E4M3 number would end at 2^-14:
 // over a long context the many small weights of a flat tail are a share of
 // the result that must not be rounded away.
@@ -743,10 +743,11 @@ cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, bool merge, 
       !make_kv_map(&maps.lat_row, a, DQK, 128, 1, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_kv_map(&maps.rope_row, a, DQK, DR, 1, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
-  // Three TMA warps keep up with boxes of 16 rows or more (5 to 20 copies a
-  // tile; seven draw power for nothing: 1.85 against 1.80 ms on 1,024 tokens of
-  // 16,384); smaller ones need seven (page size 4: 410 against 500 us, page size 24:
-  // 2.48 against 2.62 ms).
+  // Three TMA warps keep up with boxes of 16 rows or more, 5 to 20 copies a tile
+  // (1,024 tokens of 16,384: 1.57 ms at page size 64, 1.69 at 16; with seven 1.68 and
+  // 1.70: more warps that look tiles up, and the power limit); smaller boxes and
+  // gathers need seven (page size 24: 1.82 against 1.97 ms; 152 tokens of 16,384
+  // at page size 4: 360 against 449 us).
   auto launch = [&](auto kern, int ntma) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;
