@@ -10,8 +10,14 @@
 //
 // One CTA = one token x one KV split (the 64 heads are the work that shares a
 // row; the tokens of a request run side by side and share its rows in L2).
-// Bound by the tensor pipe: a 64-row tile is 64 x 64 x (576 + 512) products
-// twice (below), 1,376 cycles of MMAs.  Warps:
+// A 64-row tile is 64 x 64 x (576 + 512) products twice (below), 1,376 cycles of
+// MMAs, and takes about 1,900: the P V of a tile needs its weights, and those its
+// QK^T, so the softmax's latency is hidden by two tiles only, and a long call
+// runs at the power limit.  Measured, scales and pages of 64: 1,024 tokens at the
+// end of 16,384 in 1.57 ms (1,440 TFLOP/s of the formula's bf16 products, the
+// weights' second half not counted); 128 tokens of 16 requests, 4,096 positions
+// each, 70 us; 32 x 8,192 positions 43.5 us, every request's rows read once
+// (151 MB, 3.5 TB/s).  Warps:
 //  * 3 (or 7) TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
 //    tiles in flight.  A tile whose positions are all visible comes in boxes
 //    of 64, 32, 16 or 8 rows, the largest that divides the page size (5 to
@@ -24,8 +30,9 @@
 //    Q's latent part is the A operand in tensor memory, its rope part and K
 //    are in shared memory; V^T is the same tile read MN-major.
 //  * 16 softmax warps turn S into P: lane quadrant q holds heads 16 q .. + 15,
-//    Q_hi rows in lanes 0-15 and Q_lo rows in lanes 16-31; a shuffle adds the
-//    halves, and a thread owns one head and 8 rows of the tile.
+//    Q_hi rows in lanes 0-15 and Q_lo rows in lanes 16-31.  A thread owns one
+//    head and 8 rows of the tile; two 16-lane loads, whose half-warps take
+//    different columns, bring it both halves of its logits.
 // Q = Q_hi + Q_lo is exact for bf16 (two E4M3 numbers of a token scaled by a
 // power of two).  A weight P' = p s_j 2^E is E4M3 + E5M2.  The reference weight (p =
 // 1) of the row with the largest scale is at 16 or more, so that weights down to
@@ -90,7 +97,7 @@ constexpr int OFF_ALPHA = OFF_RED + 4 * H * 4;        // per-head factor of O, t
 constexpr int OFF_SROW = OFF_ALPHA + H * 4;           // [NST][64] the tiles' row scales
 constexpr int OFF_INFO = OFF_SROW + NST * T * 4;      // [NST][2] valid rows (bits) and largest scale of each 32 rows
 constexpr int OFF_ML = OFF_INFO + NST * 2 * 8;         // [2][64] for the cluster's merge
-constexpr int OFF_FLAG = OFF_ML + 2 * H * 4;      // O flags [4], Q exponent, vote flags [4]
+constexpr int OFF_FLAG = OFF_ML + 2 * H * 4;      // O flags [4], Q exponent
 constexpr int OFF_BAR = OFF_FLAG + 128;
 constexpr int B_KVF = 0;               // [NST] the tile in stage s has landed
 constexpr int B_KVE = B_KVF + NST;     // [NST] stage s is free
@@ -100,8 +107,7 @@ constexpr int B_PVD = B_PF + NPB;      // [2] P V of the tile in P buffer b is d
 constexpr int B_FIN = B_PVD + NPB;     // every MMA is done
 constexpr int B_QREADY = B_FIN + 1;    // Q is converted (and its staging stages are free)
 constexpr int B_QLOAD = B_QREADY + 1;  // raw bf16 Q has landed in the staging stages
-constexpr int B_VOTE = B_QLOAD + 1;    // every softmax warp has looked at its logits of the tile
-constexpr int NBAR = B_VOTE + 1;
+constexpr int NBAR = B_QLOAD + 1;
 constexpr int QSTAGE = NST - 2;
 static_assert(2 * STAGE_BYTES == H * DQK * 2, "bf16 Q fills two KV stages");
 constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
@@ -130,7 +136,6 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
   float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
   int* resc_s = reinterpret_cast<int*>(smem + OFF_FLAG);
   int* qexp_s = resc_s + 4;
-  volatile int* vote_s = resc_s + 8;                     // [4] by tile: some reference or E must move
   float* srow = reinterpret_cast<float*>(smem + OFF_SROW);
   uint2* info = reinterpret_cast<uint2*>(smem + OFF_INFO);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -191,8 +196,6 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     mbar_init(bar(B_FIN), 1);
     mbar_init(bar(B_QREADY), SM_WARPS);
     mbar_init(bar(B_QLOAD), 1);
-    mbar_init(bar(B_VOTE), SM_WARPS);
-    for (int u = 0; u < 4; ++u) vote_s[u] = 0;
     fence_mbarrier_init();
     tma_prefetch_map(&maps.lat_box);
     tma_prefetch_map(&maps.rope_box);
@@ -240,9 +243,9 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     const Deal db = deal(box_rows > 0 ? box_rows : 4), dg = deal(4);
     const int past = (int)(a.num_pages * P);  // a row past the pool: reads as zeros
     auto boxed = [&](int lt) { return box_rows > 0 && (t_begin + lt + 1) * T <= n; };
-    // Everything a tile needs is loaded long before it is used, so that no
-    // round trip to L2 sits in the loop: the page ids of tile lt + 3, then, an
-    // iteration later, the scales behind them.
+    // The loop looks ahead: the page ids of tile lt + 3 are loaded, and the scales
+    // behind those of lt + 2, while tile lt's copies are issued; one round trip to
+    // L2 an iteration, in the shadow of the tiles in flight.
     // Page ids of this lane's copy of tile lt (a box: the first row's, in x).
     auto pages_of = [&](int lt) -> int4 {
       int4 v = make_int4(-1, -1, -1, -1);
@@ -500,7 +503,6 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     bool p_set = false;
     const uint64_t qk2 = pk2(qk_scale, qk_scale);
     int stage = 0, kv_phase = 0;
-    const uint32_t vote_b = bar(B_VOTE);
     for (int lt = 0; lt < ntl; ++lt) {  // no early exit: every warp reaches every barrier
       const int sb = lt & 1;
       if (ok && !wait_warp(B_KVF + stage, kv_phase)) ok = false;  // the tile's row scales
@@ -534,15 +536,11 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
 #pragma unroll
       for (int c = 1; c < 8; ++c) tm = fmaxf(tm, z[c]);
       // Does a logit pass its head's reference, or a scale E's bound?  Every
-      // warp says so and goes on as if none did; the weights are computed again
-      // in the rare tile where some warp's answer was yes.
+      // thread goes on as if none did; the vote comes after the weights, which are
+      // computed again in the rare tile where some thread's answer was yes.
       const float smax = __uint_as_float(inf.y);
       const bool grow = p_set ? smax * p_scale >= SCALE_BOUND : smax > 0.f;
-      const bool want = __any_sync(0xffffffffu, grow || fmaf(tm, qk_scale, -m_ref) > EXCEED_LOG2);
-      if (lane == 0) {
-        if (want) vote_s[lt & 3] = 1;
-        mbar_arrive(bar(B_VOTE));
-      }
+      const bool want = grow || fmaf(tm, qk_scale, -m_ref) > EXCEED_LOG2;
       uint32_t phi[4], plo[4];
       uint64_t ln;
       for (bool again = false;; again = true) {
@@ -559,9 +557,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
           split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
         }
         if (again) break;
-        if (!mbar_wait(vote_b, lt & 1, 4 * MBAR_LIMIT_NS)) ok = false;
-        ok = __all_sync(0xffffffffu, ok);
-        if (vote_s[lt & 3] == 0) break;
+        if (!named_barrier_or(3, SM_THREADS, want)) break;  // one vote of the 16 warps: uniform
         // ---- move the references that were passed, and E; rescale O and l ----
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
         if (up == 0) red_s[part * H + hh] = tm * qk_scale;
@@ -618,9 +614,6 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_PF + lt % NPB));
-      // Tile lt + 2's vote starts from 0: every warp has read tile lt - 2's
-      // answer here, and none sets lt + 2's before this warp reaches lt + 1's vote
-      if (st == 0) vote_s[(lt + 2) & 3] = 0;
       if (stage == NST - 1) stage = 0, kv_phase ^= 1;
       else ++stage;
     }
