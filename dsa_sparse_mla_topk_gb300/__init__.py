@@ -583,6 +583,15 @@ def _run(dev: int, stream, fn: str, *args):
         raise DsaError(fn, st)
 
 
+def _empty(shape, dtype, like, stream):
+    """An output on ``like``'s device, from the memory of the stream that writes it:
+    what was there before on another stream may still be in use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _status_ptr(dev_status, dev: int):
     if dev_status is None:
         return None
@@ -650,7 +659,7 @@ def batch_layout(ctx_len: torch.Tensor, new_len: torch.Tensor, pages_held: torch
     if out is None:
         # the token arrays first, a multiple of 16 bytes apart
         cap = (capacity + 3) & -4
-        buf = torch.empty(3 * cap + 3 * R + 2, dtype=_I32, device=ctx_len.device)
+        buf = _empty(3 * cap + 3 * R + 2, _I32, ctx_len, stream)
         q_req, q_pos, slot, cu, ctx, held, used = buf.split_with_sizes((cap, cap, cap, R + 1, R, R, 1))
         if cap != capacity:
             q_req, q_pos, slot = q_req[:capacity], q_pos[:capacity], slot[:capacity]
@@ -710,7 +719,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
         qp, qh = q.data_ptr(), q.shape[1]
         qst, qsh = _strides(q)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=dtype, device=q.device)
+            q_out = _empty(q.shape, dtype, q, stream)
         else:
             _need(q_out, "q_out", dtype, 3, dev)
             _need_shape(q_out, "q_out", q.shape)
@@ -727,7 +736,7 @@ def qk_norm_rope(q: torch.Tensor | None, k: torch.Tensor | None, pos: torch.Tens
             _need(k_out, "k_out", dtype, 3, dev)
             _need_shape(k_out, "k_out", k.shape)
         elif not cache:
-            k_out = torch.empty(k.shape, dtype=dtype, device=k.device)
+            k_out = _empty(k.shape, dtype, k, stream)
         kop = None if k_out is None else k_out.data_ptr()
     elif k_out is not None or cache:
         raise ValueError("k_out or a cache write without k")
@@ -792,24 +801,24 @@ def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, 
     whole = num_splits == 1 or merge
     if whole:
         if out is None:
-            out = torch.empty((num_q, H, d_latent), dtype=_BF16, device=q.device)
+            out = _empty((num_q, H, d_latent), _BF16, q, stream)
         else:
             _need(out, "out", _BF16, 3, dev)
             _need_shape(out, "out", (num_q, H, d_latent))
         if lse is None:
-            lse = torch.empty((num_q, H), dtype=_F32, device=q.device)
+            lse = _empty((num_q, H), _F32, q, stream)
         else:
             _need(lse, "lse", _F32, 2, dev)
             _need_shape(lse, "lse", (num_q, H))
         oo, ll = out.data_ptr(), lse.data_ptr()
     else:
         if o_part is None:
-            o_part = torch.empty((num_splits, num_q, H, d_latent), dtype=_F32, device=q.device)
+            o_part = _empty((num_splits, num_q, H, d_latent), _F32, q, stream)
         else:
             _need(o_part, "o_part", _F32, 4, dev)
             _need_shape(o_part, "o_part", (num_splits, num_q, H, d_latent))
         if lse_part is None:
-            lse_part = torch.empty((num_splits, num_q, H), dtype=_F32, device=q.device)
+            lse_part = _empty((num_splits, num_q, H), _F32, q, stream)
         else:
             _need(lse_part, "lse_part", _F32, 3, dev)
             _need_shape(lse_part, "lse_part", (num_splits, num_q, H))
@@ -852,12 +861,12 @@ def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_ro
                            o_part=b.get("o_part"), lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)
     dev = q.get_device()
     if out is None:
-        out = torch.empty((num_q, H, d_latent), dtype=_BF16, device=q.device)
+        out = _empty((num_q, H, d_latent), _BF16, q, stream)
     else:
         _need(out, "out", _BF16, 3, dev)
         _need_shape(out, "out", (num_q, H, d_latent))
     if lse is None:
-        lse = torch.empty((num_q, H), dtype=_F32, device=q.device)
+        lse = _empty((num_q, H), _F32, q, stream)
     else:
         _need(lse, "lse", _F32, 2, dev)
         _need_shape(lse, "lse", (num_q, H))
@@ -902,12 +911,12 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
     if max_out < 1:
         raise ValueError("max_out must be positive")
     if tokens is None:
-        tokens = torch.empty((R, max_out), dtype=_I32, device=target_probs.device)
+        tokens = _empty((R, max_out), _I32, target_probs, stream)
     else:
         _need(tokens, "tokens", _I32, 2, dev)
         _need_shape(tokens, "tokens", (R, max_out))
     if num_out is None:
-        num_out = torch.empty(R, dtype=_I32, device=target_probs.device)
+        num_out = _empty(R, _I32, target_probs, stream)
     else:
         _need(num_out, "num_out", _I32, 1, dev)
         _need_shape(num_out, "num_out", (R,))
@@ -918,7 +927,7 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
         _need(ctx_len, "ctx_len", _I32, 1, dev)
         _need_shape(ctx_len, "ctx_len", (R,))
         if ctx_out is None:
-            ctx_out = torch.empty(R, dtype=_I32, device=target_probs.device)
+            ctx_out = _empty(R, _I32, target_probs, stream)
         else:
             _need(ctx_out, "ctx_out", _I32, 1, dev)
             _need_shape(ctx_out, "ctx_out", (R,))

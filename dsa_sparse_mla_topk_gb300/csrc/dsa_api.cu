@@ -320,6 +320,11 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return a && b && na > 0 && nb > 0 && x < y + (uint64_t)nb && y < x + (uint64_t)na;
 }
 
+// Bytes from the first to the last value of 16-bit rows [tokens, heads, d].
+int64_t row_span(int64_t tokens, int64_t heads, int64_t ts, int64_t hs, int64_t d) {
+  return tokens > 0 && heads > 0 ? 2 * ((tokens - 1) * ts + (heads - 1) * hs + d) : 0;
+}
+
 // One side of dsa_qk_norm_rope.
 dsa_status check_norm_side(const void* x, int64_t ts, int64_t hs, int32_t heads, const float* w, int32_t norm_dim,
                            const void* out, bool out_needed, int32_t num_tokens, int32_t d) {
@@ -349,11 +354,11 @@ dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_len, cons
     return DSA_ERR_INVALID_ARG;
   // every CTA reads the inputs while one writes the new lengths
   const int64_t nr = 4 * (int64_t)num_req;
-  const void* in[4] = {ctx_len, new_len, pages_held, free_used};
-  const int64_t in_bytes[4] = {nr, nr, nr, 4};
+  const void* in[6] = {ctx_len, new_len, pages_held, free_used, free_pages, block_table};
+  const int64_t in_bytes[6] = {nr, nr, nr, 4, 4 * (int64_t)num_free, nr * bt_stride};
   const void* out[7] = {cu_q, ctx_out, held_out, free_used_out, q_req, q_pos, slot};
   const int64_t nt = 4 * (int64_t)capacity, out_bytes[7] = {nr + 4, nr, nr, 4, nt, nt, nt};
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 6; ++i)
     for (int o = 0; o < 7; ++o)
       if (overlap(in[i], in_bytes[i], out[o], out_bytes[o])) return DSA_ERR_INVALID_ARG;
   dsa::BatchLayoutArgs a;
@@ -404,6 +409,14 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_
   if ((int64_t)num_tokens * (q_heads + k_heads) > INT32_MAX) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (num_tokens == 0 || q_heads + k_heads == 0) return DSA_OK;
   if (d_rope > 0 && (!pos || !cos_sin || !aligned16(cos_sin) || max_pos <= 0)) return DSA_ERR_INVALID_ARG;
+  // a row may be written before another CTA has read its own: only a side in place shares memory
+  const int64_t q_in = row_span(num_tokens, q_heads, q_tok_stride, q_head_stride, d);
+  const int64_t k_in = row_span(num_tokens, k_heads, k_tok_stride, k_head_stride, d);
+  const int64_t q_to = q_heads > 0 ? 2 * (int64_t)num_tokens * q_heads * d : 0;
+  const int64_t k_to = k_heads > 0 ? 2 * (int64_t)num_tokens * k_heads * d : 0;
+  if ((q_out != q && overlap(q_out, q_to, q, q_in)) || (k_out != k && overlap(k_out, k_to, k, k_in)) ||
+      overlap(q_out, q_to, k, k_in) || overlap(k_out, k_to, q, q_in) || overlap(q_out, q_to, k_out, k_to))
+    return DSA_ERR_INVALID_ARG;
   dsa::NormRopeArgs a;
   a.q = {q, q_tok_stride, q_head_stride, q_heads, q_norm_dim, q_weight, q_heads > 0 ? q_out : nullptr};
   a.k = {k, k_tok_stride, k_head_stride, k_heads, k_norm_dim, k_weight, k_heads > 0 ? k_out : nullptr};
@@ -439,6 +452,12 @@ dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_s
                                        merge ? 1 : num_splits, out, lse, o_part, lse_part, 0, nullptr, 0, dev_status,
                                        &a);
   if (st != DSA_OK || num_q == 0) return st;
+  // a token's result may be written before another token's query is read
+  const int64_t rows = (int64_t)num_q * num_heads;
+  const bool whole = num_splits == 1 || merge;
+  if (whole ? overlap(q, 2 * rows * (d_latent + d_rope), out, 2 * rows * d_latent)
+            : overlap(q, 2 * rows * (d_latent + d_rope), o_part, 4 * rows * d_latent * num_splits))
+    return DSA_ERR_INVALID_ARG;
   a.idx = nullptr;
   a.num_splits = num_splits;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -458,6 +477,18 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
   if (num_req == 0) return DSA_OK;
   if (!u_sample || !cu_rows || !tokens || !num_out) return DSA_ERR_INVALID_ARG;
   if (num_rows > 0 && (!target_probs || !draft_tokens || !u_accept)) return DSA_ERR_INVALID_ARG;
+  // eight CTAs read a request's inputs while one writes its results
+  const int64_t nr = 4 * (int64_t)num_req, nd = 4 * (int64_t)num_rows;
+  const void* in[4] = {draft_tokens, u_accept, u_sample, cu_rows};
+  const int64_t in_bytes[4] = {nd, nd, nr, nr + 4};
+  const void* out[3] = {tokens, num_out, ctx_out};
+  const int64_t out_bytes[3] = {nr * max_out, nr, nr};
+  for (int i = 0; i < 4; ++i)
+    for (int o = 0; o < 3; ++o)
+      if (overlap(in[i], in_bytes[i], out[o], out_bytes[o])) return DSA_ERR_INVALID_ARG;
+  if (overlap(ctx_len, nr, tokens, nr * max_out) || overlap(ctx_len, nr, num_out, nr) ||
+      (ctx_out != ctx_len && overlap(ctx_len, nr, ctx_out, nr)))
+    return DSA_ERR_INVALID_ARG;
   dsa::VerifyArgs a;
   a.target = target_probs;
   a.ld_target = ld_target;

@@ -93,6 +93,17 @@ struct Args {
   void* stream() const { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream(); }
 };
 
+// Other threads run while an entry point launches (a full launch queue makes it wait).
+struct Unlocked {
+  PyThreadState* s = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(s); }
+};
+template <class F, class... A>
+dsa_status call(F fn, A... args) {
+  Unlocked u;
+  return fn(args...);
+}
+
 template <class T>
 T* ptr(const at::Tensor* t) {
   return t ? static_cast<T*>(t->data_ptr()) : nullptr;
@@ -152,7 +163,7 @@ PyObject* batch_layout(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   auto part = [&](int64_t at, int64_t n) { return cut(buf, at, {n}, at::kInt); };
   const at::Tensor req = part(0, cap), pos = part(c4, cap), slot = part(2 * c4, cap), cu = part(3 * c4, R + 1),
                    co = part(3 * c4 + R + 1, R), ho = part(3 * c4 + 2 * R + 1, R), uo = part(3 * c4 + 3 * R + 1, 1);
-  const dsa_status s = batch_layout_fn(ptr<int32_t>(ctx), ptr<int32_t>(nw), ptr<int32_t>(held), (int32_t)R,
+  const dsa_status s = call(batch_layout_fn, ptr<int32_t>(ctx), ptr<int32_t>(nw), ptr<int32_t>(held), (int32_t)R,
                                        ptr<int32_t>(table), (int32_t)table->size(1), ptr<int32_t>(free),
                                        (int32_t)free->size(0), ptr<int32_t>(used), page, pages, cap, ptr<int32_t>(&cu),
                                        ptr<int32_t>(&req), ptr<int32_t>(&pos), ptr<int32_t>(&slot), ptr<int32_t>(&co),
@@ -203,8 +214,8 @@ PyObject* qk_norm_rope(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   at::Tensor qo, ko;
   if (q) qo = at::empty(q->sizes(), x->options());
   if (k && !cache) ko = at::empty(k->sizes(), x->options());
-  const dsa_status s = qk_norm_rope_fn(
-      ptr<void>(q), stride(q, 0), stride(q, 1), q ? (int32_t)q->size(1) : 0, ptr<float>(qw),
+  const dsa_status s = call(
+      qk_norm_rope_fn, ptr<void>(q), stride(q, 0), stride(q, 1), q ? (int32_t)q->size(1) : 0, ptr<float>(qw),
       qw ? (int32_t)qw->size(0) : 0, q ? qo.data_ptr() : nullptr, ptr<void>(k), stride(k, 0),
       stride(k, 1), k ? (int32_t)k->size(1) : 0, ptr<float>(kw), kw ? (int32_t)kw->size(0) : 0,
       k && !cache ? ko.data_ptr() : nullptr, (int32_t)n, (int32_t)d, rope,
@@ -255,12 +266,12 @@ PyObject* chunk_mla(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
     lp = op + pn;
   }
   void* stream = a.stream();
-  dsa_status s = chunk_mla_fn(q->data_ptr(), ptr<uint8_t>(kv), ptr<float>(sc), slots / page, ptr<int32_t>(bt),
+  dsa_status s = call(chunk_mla_fn, q->data_ptr(), ptr<uint8_t>(kv), ptr<float>(sc), slots / page, ptr<int32_t>(bt),
                               (int32_t)bt->size(0), (int32_t)bt->size(1), ptr<int32_t>(req), ptr<int32_t>(pos),
                               (int32_t)n, (int32_t)H, dl, dr, page, scale, S, op ? nullptr : out.data_ptr(),
                               op ? nullptr : ptr<float>(&lse), op, lp, st, stream);
   if (s == DSA_OK && op)
-    s = combine_fn(op, lp, S, (int32_t)n, (int32_t)H, dl, out.data_ptr(), ptr<float>(&lse), stream);
+    s = call(combine_fn, op, lp, S, (int32_t)n, (int32_t)H, dl, out.data_ptr(), ptr<float>(&lse), stream);
   if (s != DSA_OK) return PyLong_FromLong(s);
   return tuple_of({&out, &lse});
   END_HANDLE_TH_ERRORS
@@ -296,7 +307,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   const at::Tensor tokens = cut(buf, 0, {R, max_out}, at::kInt), num = cut(buf, R * max_out, {R}, at::kInt);
   at::Tensor co;
   if (ctx) co = cut(buf, R * max_out + R, {R}, at::kInt);
-  const dsa_status s = verify_draft_fn(ptr<float>(p), rows > 1 ? p->stride(0) : V, (int32_t)rows, (int32_t)V,
+  const dsa_status s = call(verify_draft_fn, ptr<float>(p), rows > 1 ? p->stride(0) : V, (int32_t)rows, (int32_t)V,
                                        ptr<float>(q), q && rows > 1 ? q->stride(0) : V, ptr<int32_t>(tok),
                                        ptr<float>(ua), ptr<float>(us), ptr<int32_t>(cu), (int32_t)R, max_out,
                                        ptr<int32_t>(ctx), ptr<int32_t>(&tokens), ptr<int32_t>(&num),

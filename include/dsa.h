@@ -331,7 +331,7 @@ DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const
  *                  -1 in all three for every t >= cu_q[num_req].
  *   ctx_out, held_out  int32 [num_req]: ctx_len + new_len and the pages then held.
  *   free_used_out  int32 [1]: *free_used plus the pages taken.
- * ctx_out, held_out and free_used_out must not overlap the inputs (two sets
+ * The outputs must not overlap the inputs (lengths and free_used: two sets
  * used in turn): INVALID_ARG otherwise.  Only new entries of block_table are
  * written.
  *
@@ -377,8 +377,8 @@ DSA_API dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_l
  *             addressed by token and head strides in elements (multiples of 8;
  *             16-byte aligned base).  q_heads or k_heads may be 0 (the side is absent).
  *   q_out, k_out  contiguous [num_tokens, heads, d], 16-byte aligned.  Each may be
- *             its own input (then contiguous), else must not overlap q or k.  k_out
- *             may be NULL when the cache is written.
+ *             its own input (then contiguous), else must not overlap q, k or
+ *             each other (INVALID_ARG).  k_out may be NULL when the cache is written.
  *   q_weight, k_weight  fp32 [norm_dim], 16-byte aligned; norm_dim a multiple of 8, at
  *             most d; 0: no norm (weight may be NULL).
  *   d         a multiple of 8, at most 1024.  d_rope a multiple of 16, at most
@@ -419,7 +419,8 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t
  * a contiguous share of the token's own KV tiles.  With 2 to 8 splits and
  * o_part and lse_part both NULL the call merges them itself (the splits of a
  * token are one thread-block cluster) and writes out and lse; else the splits
- * write o_part and lse_part for dsa_combine.  A token with q_req = -1
+ * write o_part and lse_part for dsa_combine.  out and o_part must not overlap
+ * q (INVALID_ARG).  A token with q_req = -1
  * (padding) or q_pos = -1 sees nothing: out = 0 and lse = -inf.  Tokens of one
  * request next to each other share its rows in L2; any order is correct.
  * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
@@ -463,7 +464,8 @@ DSA_API dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const flo
  *                 drawn token, then -1.  num_out int32 [num_req] = a + 1.
  *   ctx_len, ctx_out  int32 [num_req], or both NULL: ctx_out = ctx_len + num_out,
  *                 the request's cached positions once the rejected rows are
- *                 dropped (the same buffer is allowed).
+ *                 dropped (the same buffer is allowed).  Other overlaps of outputs
+ *                 with draft_tokens, u_*, cu_rows or ctx_len: INVALID_ARG.
  * A request without rows has num_out = 0 and tokens -1.  Data errors, all
  * DSA_DEV_BAD_INDEX: cu_rows decreasing or past num_rows (as a request
  * without rows); a draft outside [0, vocab) (not taken); more rows than

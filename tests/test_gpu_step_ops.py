@@ -716,6 +716,85 @@ def test_chunk_agrees_with_the_sparse_call_over_every_position():
     assert float((sl - cl).abs().max()) <= 1e-3
 
 
+# ---- streams and graphs ----------------------------------------------------------------
+
+
+def test_two_calls_at_once_and_outputs_of_another_stream():
+    """Calls of every operator on two streams at once give what each gives alone,
+    and outputs cut for a stream are that stream's memory."""
+    c = _chunk_case(64, 512, 64, [700, 90, 1300], [5, 1, 9], 64, seed=41)
+    g = _cuda(c)
+    ckw = dict(d_latent=512, d_rope=64, page_size=64, softmax_scale=c["scale"])
+    q, k, gen = _qk_inputs(300, 64, 1, 576, torch.bfloat16, seed=42)
+    pos = torch.randint(0, 90, (300,), generator=gen, dtype=I32).cuda()
+    cs = torch.from_numpy(_tables(90, 64)).cuda()
+    w = torch.ones(576, device="cuda")
+    p, dq, tok, cu, ua, us = _verify_case(24, 6, 5003, True, seed=43)
+    lay = _layout_case(40, 9, 500, 16, seed=44)
+    li = [i32(x) for x in lay[:3]]
+    lf, pages, none_used = i32(lay[4]), lay[5], i32([0])
+
+    def calls(stream):
+        table = torch.from_numpy(lay[3].copy()).cuda()
+        r = [dsa.chunk_mla(g["q"], g["kv"], g["sc"], g["table"], g["req"], g["pos"], num_splits=S, stream=stream, **ckw)
+             for S in (1, 3, 12)]
+        r.append(dsa.qk_norm_rope(q, k, pos, cs, d_rope=64, q_weight=w, stream=stream))
+        r.append(dsa.verify_draft(p, tok, cu, ua, us, draft_probs=dq, max_out=7, stream=stream)[:2])
+        r.append(dsa.batch_layout(*li, table, lf, none_used, page_size=16, num_pages=pages, capacity=400, stream=stream))
+        return [t for x in r for t in x] + [table]
+
+    want = calls(None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        got = [calls(s) for s in streams]
+        torch.cuda.synchronize()
+        for rows in got:
+            for x, y in zip(rows, want):
+                assert torch.equal(x, y)
+        del got, rows
+
+
+def test_captured_norm_rope_and_verification_follow_their_inputs():
+    T = 70
+    q, k, gen = _qk_inputs(T, 4, 1, 576, torch.bfloat16, seed=51)
+    cs = torch.from_numpy(_tables(64, 64)).cuda()
+    w = (1 + 0.3 * torch.randn(576, generator=gen)).cuda()
+    pos = torch.randint(0, 64, (T,), generator=gen, dtype=I32).cuda()
+    slot = torch.arange(T, dtype=I32, device="cuda")
+    kv, sc = torch.zeros(T, 576, dtype=torch.uint8, device="cuda"), torch.zeros(T, device="cuda")
+    p, dq, tok, cu, ua, us = _verify_case(9, 4, 3001, True, seed=52)
+    ctx = torch.arange(9, dtype=I32, device="cuda")
+    qo = torch.empty(q.shape, dtype=q.dtype, device="cuda")
+    res = [torch.empty(9, 5, dtype=I32, device="cuda"), torch.empty(9, dtype=I32, device="cuda"),
+           torch.empty(9, dtype=I32, device="cuda")]
+    kw = dict(d_rope=64, q_weight=w, k_weight=w[:512], slot=slot)
+
+    def norm(kv_, sc_, **o):
+        return dsa.qk_norm_rope(q, k, pos, cs, kv=kv_, kv_scale=sc_, **kw, **o)[0]
+
+    def verify(**o):
+        return dsa.verify_draft(p, tok, cu, ua, us, draft_probs=dq, ctx_len=ctx, max_out=5, **o)
+
+    norm(kv, sc), verify()  # loaded before the capture
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        norm(kv, sc, q_out=qo)
+        verify(tokens=res[0], num_out=res[1], ctx_out=res[2])
+    for step in range(3):
+        pos.copy_(torch.randint(0, 64, (T,), generator=gen, dtype=I32))
+        q.normal_(), k.normal_()
+        ua.uniform_(), us.uniform_()
+        kv.zero_(), sc.zero_()
+        graph.replay()
+        kv2, sc2 = torch.zeros_like(kv), torch.zeros_like(sc)
+        assert torch.equal(norm(kv2, sc2), qo)
+        assert torch.equal(kv, kv2) and torch.equal(sc, sc2) and float(sc.min()) > 0
+        for x, y in zip(verify(), res):
+            assert torch.equal(x, y)
+
+
 # ---- the binding's two ways to marshal a call ---------------------------------------
 
 

@@ -110,6 +110,34 @@ def test_verify_argument_checks(lib, over, expect):
     assert _verify(lib, **over) == expect
 
 
+@no_device_only
+def test_outputs_over_inputs_are_refused(lib):
+    """Another CTA may still read what an output would replace."""
+    def at(base, off):
+        return VP(base.value + off)
+    # new pages are read from free_pages and old ones from block_table while tokens are written
+    assert _layout(lib, slot=A(4)) == 1
+    assert _layout(lib, pos=at(A(3), 16)) == 1
+    # rows: 4 tokens of 64 x 576, token stride twice that
+    wide = dict(qt=2 * 64 * 576)
+    last = 2 * (3 * 2 * 64 * 576 + 64 * 576)  # bytes from the first to behind the last value
+    assert _norm(lib, qo=at(A(0), last - 16), **wide) == 1
+    assert _norm(lib, qo=A(3)) == 1
+    assert _norm(lib, ko=at(A(0), 32)) == 1
+    assert _norm(lib, ko=at(A(2), 2 * 4 * 64 * 576 - 16)) == 1
+    q_bytes = 2 * 64 * 576
+    assert _chunk(lib, out=A(0)) == 1
+    assert _chunk(lib, out=at(A(0), q_bytes - 16)) == 1
+    assert _chunk(lib, S=2, op=at(A(0), -(2 * 4 * 64 * 512) + 16), lp=A(8)) == 1
+    assert _chunk(lib, S=2, out=A(0)) == 1  # merged by the call
+    for k in ("out", "num", "co"):
+        for x in (2, 3, 4, 5):
+            assert _verify(lib, **{k: A(x)}) == 1, (k, x)
+    assert _verify(lib, out=A(6)) == 1
+    assert _verify(lib, num=A(6)) == 1
+    assert _verify(lib, co=at(A(6), 4)) == 1
+
+
 def test_chunk_split_rule(lib):
     """The rule on 152 SMs: no split once the tokens fill the GPU or the context is
     a few tiles; clusters that run in one wave; many splits for one long context."""
