@@ -14,10 +14,15 @@
 // from a 16-bit copy of them).
 //
 // HBM-bound: each row is read once and written once.  A group of 8 lanes takes
-// one row as 16-byte chunks, chunk l + 8 u in lane l: a warp holds four rows,
-// so that a 576-value row has no idle lane (72 chunks, 9 a lane, all in flight
-// together) and its sums take three shuffles instead of five.  In the
-// half-split form the lane reads its partner chunk a second time (an L1 hit).
+// one row as 16-byte chunks, chunk l + 8 u in lane l, so that a 576-value row has
+// no idle lane (72 chunks, 9 a lane, all in flight together) and its sums take
+// three shuffles instead of five; 2 to 4 heads of a token share a group's loads
+// of position, rotation and weights.  Keys have CTAs of their own: no warp runs
+// both sides' code.  In the half-split form a lane reads its partner chunk a
+// second time (an L1 hit), unless both halves of its pairs are in the lane
+// already.  Measured: 8,192 tokens of 64 x 576 + a key row into the cache 190 us,
+// 95% of a copy's bandwidth; 4,099 tokens of 32 + 8 heads of 128 15.6 us, 81%;
+// 128 tokens of 64 x 576 7.2 us, latency (the floor of its bytes is 2.8).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
