@@ -26,9 +26,9 @@
 // contiguous run, 16-byte loads where the rows allow), exchange the sums over
 // distributed shared memory, and only the warp whose run holds the token
 // reads it again (from L2), 128 values a turn.  Only rows a of p and q are
-// read.  128 requests, V = 131,072, with draft probabilities: 33 us for 101 MB
-// (3.1 TB/s; the sums' arithmetic and the cluster-wide waits are what is
-// not hidden).  Few requests are one round trip after another: 4 take 5.4 us.
+// read.  128 requests, V = 131,072, with draft probabilities: 34 us for 101 MB
+// (2.9 TB/s; the sums' arithmetic and the cluster-wide waits are what is
+// not hidden).  Few requests are one round trip after another: 4 take 5.7 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -203,7 +203,10 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
     }
     return;
   }
-  cluster.barrier_arrive();  // waited for before the first write to another CTA's shared memory
+  // Waited for before the first write to another CTA's shared memory.  Nothing was
+  // written yet that it would have to order: relaxed (a releasing arrive: 4 requests
+  // 6.0 instead of 5.7 us).
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;");
   const int32_t* xs = a.draft_tokens + row0;
   int32_t n = row1 - row0 - 1;
   if (n > a.max_out - 1) {  // drafts past the output's width are not looked at
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
     s = warp_sum(s);
     mine = s;
     if (lane == 0) wsum[warp] = s;
-    if (turn == 0) cluster.barrier_wait();  // every CTA of the cluster runs
+    if (turn == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
     __syncthreads();
     if (tid < C) {
       int64_t cta = 0;
@@ -349,7 +352,7 @@ cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream) {
                    (!a.draft || ((reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0 && a.ld_draft % 4 == 0));
   // Eight CTAs a request, of 512 threads while two of them fit an SM at once
   // (one request: 8.7 us, 256 threads 9.7 us), of 256 beyond that (128 requests, V =
-  // 131,072: 33 us; 512 threads 39 us, and with fewer CTAs a request 36 to 45 us);
+  // 131,072: 34 us; 512 threads 39 us, and with fewer CTAs a request 36 to 45 us);
   // fewer where a request's chain of loads would repeat in too many waves.
   const int sms = device_sm_count();
   int c = VD_MAX_CLUSTER;
