@@ -1,4 +1,5 @@
 // C ABI of the library: argument checks, planning helpers and launches.
+#include <algorithm>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -100,19 +101,25 @@ int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_la
   // two to an SM still gain
   static const int32_t clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
   const int64_t ntiles = dsa_kv_tile_count(max_ctx, tile);
+  // The live rows are not known here: a batch of fixed capacity (a captured step,
+  // a verify block whose requests drafted less) is padded.  Tensor cores: the cost
+  // of a full batch plus that of a half full one.  128 rows of 4,096 positions: one
+  // split 66 us full and 63 with 72 live rows, two 82 and 43.
   int32_t best = 1;
   int64_t best_cost = -1;
   for (int32_t s = 1; s <= 64 && s <= ntiles; ++s) {
-    int64_t waves;
-    if (tc && s <= 8) {
-      const int64_t cap = (int64_t)clusters[s] * num_sms / 152;
-      waves = cap > 0 ? (num_q + cap - 1) / cap : num_q;
-    } else {
-      const int64_t cap = tc ? num_sms : 2 * (int64_t)num_sms;
-      waves = ((int64_t)num_q * s + cap - 1) / cap;
-    }
     const int64_t per = 100 * ((ntiles + s - 1) / s);
-    const int64_t cost = waves * (per + fixed) + (s == 1 ? 0 : s <= 8 ? merge : combine + s * combine_split);
+    const int64_t join = s == 1 ? 0 : s <= 8 ? merge : combine + s * combine_split;
+    const int64_t cap = s <= 8 ? (int64_t)clusters[s] * num_sms / 152 : num_sms / s;  // tokens that run at once
+    int64_t cost;
+    if (tc) {
+      const int64_t cta = per + (s <= 8 ? fixed + join : fixed);  // a cluster's merge is its CTAs' work
+      auto waves = [&](int64_t n) { return cap > 0 ? (n + cap - 1) / cap : (n * s + num_sms - 1) / num_sms; };
+      cost = (waves(num_q) + waves((num_q + 1) / 2)) * cta + (s <= 8 ? 0 : 2 * join);
+    } else {
+      const int64_t ctas = 2 * (int64_t)num_sms;
+      cost = ((int64_t)num_q * s + ctas - 1) / ctas * (per + fixed) + join;
+    }
     if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
   }
   return best;

@@ -542,7 +542,8 @@ DSA_API int32_t dsa_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_
  * dsa_chunk_pick_num_splits: KV splits per token for dsa_chunk_mla_fwd over
  * contexts of about max_ctx positions: the number with the least estimated
  * time, from the tiles of a split, a CTA's fixed cost, the waves of CTAs (of clusters,
- * for the 2 to 8 splits that the call merges) and the merge or Combine.
+ * for the 2 to 8 splits that the call merges) and the merge or Combine.  On the
+ * tensor cores a full batch and one whose second half is padding count the same.
  */
 DSA_API int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope,
                                           int32_t max_ctx, int32_t num_sms);
