@@ -94,8 +94,9 @@ int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_la
   const bool tc = use_tensor_cores(num_heads, d_latent, d_rope);
   // In hundredths of a tile's time (measured: 0.93 us on the tensor cores, 2.0 us
   // of 32 rows on the CUDA cores): a CTA's start and end; the merge in a cluster;
-  // the Combine, which reads more the more splits there are.
-  const int64_t fixed = tc ? 800 : 150, merge = tc ? 500 : 50, combine = tc ? 600 : 70, combine_split = tc ? 22 : 10;
+  // the Combine, whose partials grow with tokens and splits (1 x 64: 18 us, 24 x 12: 17).
+  const int64_t fixed = tc ? 800 : 150, merge = tc ? 500 : 50, combine = tc ? 500 : 70;
+  const int64_t combine_split = tc ? 15 + 4 * (int64_t)num_q : 10;
   // clusters of S CTAs that run at once, one CTA per SM, of 152 SMs
   // (cudaOccupancyMaxActiveClusters); the CUDA-core kernel's CTAs are small, and
   // two to an SM still gain
