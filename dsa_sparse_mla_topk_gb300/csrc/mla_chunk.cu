@@ -34,15 +34,16 @@
 //    head and 8 rows of the tile; two 16-lane loads, whose half-warps take
 //    different columns, bring it both halves of its logits.
 // Q = Q_hi + Q_lo is exact for bf16 (two E4M3 numbers of a token scaled by a
-// power of two).  A weight P' = p s_j 2^E is E4M3 + E5M2.  The reference weight (p =
-// 1) of the row with the largest scale is at 16 or more, so that weights down to
+// power of two).  A weight P' = p s_j F is E4M3 + E5M2.  F puts the reference weight
+// (p = 1) of the row with the largest scale at 16, an exact value (a head that looks at
+// one row gives that row), or more where scales grow, so that weights down to
 // 2^-10 of it have a relative error of at most 2^-8 (0.12% root mean square,
 // a bf16 weight's is 0.08%); smaller ones an absolute one of 2^-14, and only
 // below 2^-21 nothing is left of them.  A second E4M3 number would end at 2^-14:
 // over a long context the many small weights of a flat tail are a share of
 // the result that must not be rounded away.
 // Lazy rescaling: a head's reference maximum moves when a logit passes it by more
-// than 2^3.8, E when a row's scale passes its bound; l is summed in fp32 from unrounded
+// than 2^3.8, F when a row's scale passes its bound; l is summed in fp32 from unrounded
 // p.  (Of 64 heads some reference then moves in few tiles; with 2^2 152 tokens of
 // 4,096 took 92 instead of 72 us.)  All waits are bounded.
 #include <cooperative_groups.h>
@@ -77,7 +78,7 @@ constexpr int P_BYTES = H * T;  // P_hi (or P_lo) of a tile: [head][row], K-majo
 constexpr int NPB = 2;
 constexpr int MAX_MERGED = chunk_max_merged();
 constexpr int SM_WARPS = 16, SM_THREADS = SM_WARPS * 32;
-constexpr float SCALE_BOUND = 32.0f;     // s_j 2^E < 32, and
+constexpr float SCALE_BOUND = 32.0f;     // s_j F < 32, and
 constexpr float EXCEED_LOG2 = 3.8f;      // p = 2^(z - m) <= 2^3.8 < 14: P' < 448, the largest E4M3 value
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -496,10 +497,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
 
     // ---- the tiles ----
     float m_ref = -INFINITY;      // head hh's reference maximum (log2 domain), the same in its 8 threads
-    uint64_t l2 = pk2(0.f, 0.f);  // head hh's share of l 2^E, two running sums
-    int p_exp = 0;                // E, the same in every thread; set at the first row with a scale
-    float p_scale = 1.f;          // 2^E
-    float shift = 0.f;            // E - m_ref (m_ref = -inf: E)
+    uint64_t l2 = pk2(0.f, 0.f);  // head hh's share of l F, two running sums
+    float p_log = 0.f;            // log2 F, the same in every thread; set at the first row with a scale
+    float p_scale = 1.f;          // F
+    float shift = 0.f;            // log2 F - m_ref (m_ref = -inf: log2 F)
     bool p_set = false;
     const uint64_t qk2 = pk2(qk_scale, qk_scale);
     int stage = 0, kv_phase = 0;
@@ -535,7 +536,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       float tm = z[0];
 #pragma unroll
       for (int c = 1; c < 8; ++c) tm = fmaxf(tm, z[c]);
-      // Does a logit pass its head's reference, or a scale E's bound?  Every
+      // Does a logit pass its head's reference, or a scale F's bound?  Every
       // thread goes on as if none did; the vote comes after the weights, which are
       // computed again in the rare tile where some thread's answer was yes.
       const float smax = __uint_as_float(inf.y);
@@ -544,7 +545,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       uint32_t phi[4], plo[4];
       uint64_t ln;
       for (bool again = false;; again = true) {
-        // p 2^E, summed into l; folded with the row's scale, as E4M3 + E5M2
+        // p F, summed into l; folded with the row's scale, as E4M3 + E5M2
         const uint64_t shift2 = pk2(shift, shift);
         ln = l2;
 #pragma unroll
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         }
         if (again) break;
         if (!named_barrier_or(3, SM_THREADS, want)) break;  // one vote of the 16 warps: uniform
-        // ---- move the references that were passed, and E; rescale O and l ----
+        // ---- move the references that were passed, and F; rescale O and l ----
         tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
         if (up == 0) red_s[part * H + hh] = tm * qk_scale;
         group_sync();
@@ -570,16 +571,14 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
           m_ref = mt;
         }
         if (sm > 0.f && sm <= 3.0e38f && (!p_set || sm * p_scale >= SCALE_BOUND)) {
-          int e2;
-          frexpf(sm, &e2);  // sm < 2^e2: sm 2^E in [16, 32)
-          const int e = min(5 - e2, 80);  // (sums of 2^E stay finite for subnormal scales)
-          alpha *= ldexpf(1.f, e - p_exp);  // O and l carry 2^E
-          p_exp = e;
+          const float f = fminf(log2f(16.f / sm), 80.f);  // (sums of F stay finite for subnormal scales)
+          alpha *= ex2(f - p_log);  // O and l carry F
+          p_log = f;
           p_set = true;
-          p_scale = ldexpf(1.f, p_exp);
+          p_scale = ex2(f);
         }
         l2 = mul2(l2, pk2(alpha, alpha));
-        shift = (float)p_exp - (m_ref == -INFINITY ? 0.f : m_ref);
+        shift = p_log - (m_ref == -INFINITY ? 0.f : m_ref);
         if (part == 0 && up == 0) alpha_s[hh] = alpha;
         const unsigned need = __ballot_sync(0xffffffffu, lt > 0 && alpha != 1.f);
         if (part == 0 && lane == 0) resc_s[q4] = need != 0u;
@@ -629,10 +628,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     group_sync();
     if (part == 0 && up == 0) {
       const float l = (red_s[hh] + red_s[H + hh]) + (red_s[2 * H + hh] + red_s[3 * H + hh]);
-      // (O and l both carry 2^E)
+      // (O and l both carry F)
       alpha_s[hh] = l > 0.f ? (MERGE ? 1.f : 1.f / l) : 0.f;
-      const float lse = l > 0.f ? (m_ref - (float)p_exp + log2f(l)) * LN2 : -INFINITY;
-      if (MERGE) ml_s[hh] = ok && l > 0.f ? m_ref - (float)p_exp : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
+      const float lse = l > 0.f ? (m_ref + log2f(l * ex2(-p_log))) * LN2 : -INFINITY;
+      if (MERGE) ml_s[hh] = ok && l > 0.f ? m_ref - p_log : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
       else if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
       else if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
     }
