@@ -1,5 +1,4 @@
 // C ABI of the library: argument checks, planning helpers and launches.
-#include <algorithm>
 #include <cuda_runtime.h>
 #include <math.h>
 
@@ -91,36 +90,39 @@ int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_la
   const int32_t tile = dsa_kv_tile_size(num_heads, d_latent, d_rope);
   if (tile <= 0 || num_q <= 0 || max_ctx <= 0) return 1;
   if (num_sms <= 0) num_sms = dsa::device_sm_count();
-  const bool tc = use_tensor_cores(num_heads, d_latent, d_rope);
-  // In hundredths of a tile's time (measured: 0.93 us on the tensor cores, 2.0 us
-  // of 32 rows on the CUDA cores): a CTA's start and end; the merge in a cluster;
-  // the Combine, whose partials grow with tokens and splits (1 x 64: 18 us, 24 x 12: 17).
-  const int64_t fixed = tc ? 800 : 150, merge = tc ? 500 : 50, combine = tc ? 500 : 70;
-  const int64_t combine_split = tc ? 15 + 4 * (int64_t)num_q : 10;
-  // clusters of S CTAs that run at once, one CTA per SM, of 152 SMs
-  // (cudaOccupancyMaxActiveClusters); the CUDA-core kernel's CTAs are small, and
-  // two to an SM still gain
-  static const int32_t clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
   const int64_t ntiles = dsa_kv_tile_count(max_ctx, tile);
-  // The live rows are not known here: a batch of fixed capacity (a captured step,
-  // a verify block whose requests drafted less) is padded.  Tensor cores: the cost
-  // of a full batch plus that of a half full one.  128 rows of 4,096 positions: one
-  // split 66 us full and 63 with 72 live rows, two 82 and 43.
+  const bool tc = use_tensor_cores(num_heads, d_latent, d_rope);
+  // Clusters of S CTAs that run at once, one CTA per SM, of 152 SMs
+  // (cudaOccupancyMaxActiveClusters).
+  static const int32_t clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
+  // (64, 512, 64), in hundredths of a tile's time (measured: 0.93 us): a CTA's start
+  // and end; the merge in a cluster; the Combine, whose partials grow with tokens and
+  // splits (1 x 64: 18 us, 24 x 12: 17).  The live rows are not known here: a batch
+  // of fixed capacity (a captured step, a verify block whose requests drafted
+  // less) is padded, so the cost is that of a full batch plus that of a half full
+  // one.  128 rows of 4,096 positions: one split 66 us full and 63 with 72 live rows,
+  // two 82 and 43.
+  auto large = [&](int32_t s) {
+    const int64_t fixed = 800, merge = 500, combine = 500 + s * (15 + 4 * (int64_t)num_q);
+    const int64_t cap = s <= 8 ? (int64_t)clusters[s] * num_sms / 152 : num_sms / s;  // tokens that run at once
+    const int64_t join = s == 1 ? 0 : s <= 8 ? merge : 2 * combine;
+    // (a cluster's merge is its CTAs' work)
+    const int64_t cta = 100 * ((ntiles + s - 1) / s) + fixed + (s <= 8 ? join : 0);
+    auto waves = [&](int64_t n) { return cap > 0 ? (n + cap - 1) / cap : (n * s + num_sms - 1) / num_sms; };
+    return (waves(num_q) + waves((num_q + 1) / 2)) * cta + (s <= 8 ? 0 : join);
+  };
+  // (16, 64, 16), in hundredths of a us: a CTA's start and end, its steps of eight
+  // tiles, alone on an SM or two of them, and the merge or Combine (one token of
+  // 16,384 positions: 8 splits 14 us, 16 13, 32 15; 107 of 12,733: 1 59 us, 2 55, 5 51, 8 57).
+  auto small = [&](int32_t s) {
+    const int64_t steps = ((ntiles + s - 1) / s + 7) / 8, ctas = (int64_t)num_q * s;
+    const int64_t join = s == 1 ? 0 : s <= 8 ? 100 : 250 + 18 * s;
+    return join + (ctas <= num_sms ? 400 + 108 * steps : (ctas + 2 * num_sms - 1) / (2 * num_sms) * (400 + 200 * steps));
+  };
   int32_t best = 1;
   int64_t best_cost = -1;
   for (int32_t s = 1; s <= 64 && s <= ntiles; ++s) {
-    const int64_t per = 100 * ((ntiles + s - 1) / s);
-    const int64_t join = s == 1 ? 0 : s <= 8 ? merge : combine + s * combine_split;
-    const int64_t cap = s <= 8 ? (int64_t)clusters[s] * num_sms / 152 : num_sms / s;  // tokens that run at once
-    int64_t cost;
-    if (tc) {
-      const int64_t cta = per + (s <= 8 ? fixed + join : fixed);  // a cluster's merge is its CTAs' work
-      auto waves = [&](int64_t n) { return cap > 0 ? (n + cap - 1) / cap : (n * s + num_sms - 1) / num_sms; };
-      cost = (waves(num_q) + waves((num_q + 1) / 2)) * cta + (s <= 8 ? 0 : 2 * join);
-    } else {
-      const int64_t ctas = 2 * (int64_t)num_sms;
-      cost = ((int64_t)num_q * s + ctas - 1) / ctas * (per + fixed) + join;
-    }
+    const int64_t cost = tc ? large(s) : small(s);
     if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
   }
   return best;
@@ -470,7 +472,7 @@ dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_s
   a.num_splits = num_splits;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (use_tensor_cores(num_heads, d_latent, d_rope)) return from_cuda(dsa::launch_chunk_tc(a, q_pos, merge, s));
-  return from_cuda(dsa::launch_chunk_simt(a, q_pos, merge, s));
+  return from_cuda(dsa::launch_chunk_small(a, q_pos, merge, s));
 }
 
 dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,

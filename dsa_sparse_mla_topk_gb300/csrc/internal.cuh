@@ -131,7 +131,7 @@ cudaError_t launch_qk_norm_rope(const NormRopeArgs& a, cudaStream_t stream);
 // without idx; k is unused.  merge: num_splits <= chunk_max_merged() CTAs of a
 // cluster per token write out / lse themselves.
 constexpr int chunk_max_merged() { return 8; }
-cudaError_t launch_chunk_simt(const MlaArgs& a, const int32_t* q_pos, bool merge, cudaStream_t stream);
+cudaError_t launch_chunk_small(const MlaArgs& a, const int32_t* q_pos, bool merge, cudaStream_t stream);
 // The same on the tensor cores, for (64, 512, 64).
 cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, bool merge, cudaStream_t stream);
 

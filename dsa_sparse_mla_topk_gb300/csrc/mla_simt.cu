@@ -12,15 +12,12 @@
 // This version runs in fp32 on the CUDA cores.  It is the simple, general
 // path (both supported head shapes) that the tensor-core kernel is checked
 // and measured against.
-#include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
 #include "internal.cuh"
-
-namespace cg = cooperative_groups;
 
 namespace dsa {
 namespace {
@@ -53,12 +50,8 @@ struct SimtCfg {
                                        sizeof(float) * H * T + sizeof(float) * 3 * H + sizeof(int64_t) * T;
 };
 
-// DENSE: every position 0 .. q_pos[i] instead of the selected ones
-// (dsa_chunk_mla_fwd); a token with q_req = -1 or q_pos = -1 sees nothing.
-// MERGE: a token's splits are the CTAs of a thread-block cluster and merge
-// their results over distributed shared memory (no partials, no Combine kernel).
-template <int H, int DL, int DR, bool DENSE, bool MERGE>
-__global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a, const int32_t* __restrict__ q_pos) {
+template <int H, int DL, int DR>
+__global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a) {
   using C = SimtCfg<H, DL, DR>;
   constexpr int NT = C::NT, T = C::T, DQK = C::DQK;
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -86,16 +79,9 @@ __global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a, const
   }
   const int r = a.q_req[i];
   const bool req_ok = (r >= 0 && r < a.num_req);
-  if (!req_ok && (!DENSE || r != -1) && tid == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
+  if (!req_ok && tid == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
 
-  int32_t k = a.k;  // entries of this token
-  if constexpr (DENSE) {
-    const int32_t p = q_pos[i];
-    const bool pos_ok = p >= -1 && p <= INT32_MAX - T && p / a.page_size < a.bt_stride;
-    if (!pos_ok && req_ok && tid == 0) report(a.dev_status, DSA_DEV_BAD_QPOS);
-    k = req_ok && pos_ok ? p + 1 : 0;
-  }
-  const int ntiles = (int)(((int64_t)k + T - 1) / T);
+  const int ntiles = (a.k + T - 1) / T;
   const int t_begin = (int)((int64_t)ntiles * split / S);
   const int t_end = (int)((int64_t)ntiles * (split + 1) / S);
 
@@ -111,14 +97,14 @@ __global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a, const
 #pragma unroll
     for (int d = 0; d < C::DPT; ++d) acc[h][d] = 0.f;
 
-  const int32_t* row_idx = DENSE ? nullptr : a.idx + (int64_t)i * a.k;
+  const int32_t* row_idx = a.idx + (int64_t)i * a.k;
   for (int tile = t_begin; tile < t_end; ++tile) {
     __syncthreads();  // previous tile fully consumed
     if (tid < T) {
       const int e = tile * T + tid;
       int64_t slot = -1;
-      if (e < k && req_ok) {
-        const int32_t pos = DENSE ? e : row_idx[e];
+      if (e < a.k && req_ok) {
+        const int32_t pos = row_idx[e];
         if (pos < -1) {
           report(a.dev_status, DSA_DEV_BAD_INDEX);
         } else if (pos >= 0) {
@@ -229,83 +215,41 @@ __global__ void __launch_bounds__(kSimtThreads) mla_simt_kernel(MlaArgs a, const
     l_s[hs] = l_run;
   }
   __syncthreads();
-  if constexpr (MERGE) {
-    // out = sum_s 2^(m_s - m) O_s / sum_s 2^(m_s - m) l_s, each CTA a share of the token's values
-    static_assert(H * DL <= T * C::KSTRIDE, "a split's O fits where the KV tile was");
-    float* o_s = ks;
+  // epilogue: normalise, write bf16 output or fp32 partial
 #pragma unroll
-    for (int h = 0; h < C::HPT; ++h)
+  for (int h = 0; h < C::HPT; ++h) {
+    const int hh = hv0 + h;
+    const float l = l_s[hh];
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int64_t o_off = ((int64_t)i * H + hh) * DL + dv0;
+    if (S == 1) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + o_off;
 #pragma unroll
-      for (int d = 0; d < C::DPT; ++d) o_s[(hv0 + h) * DL + dv0 + d] = acc[h][d];
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    for (int e = split * NT + tid; e < H * DL; e += S * NT) {
-      const int h = e / DL;
-      float m = -INFINITY, l = 0.f, o = 0.f;
-      for (int s = 0; s < S; ++s) m = fmaxf(m, *cluster.map_shared_rank(m_s + h, s));
-      for (int s = 0; s < S; ++s) {
-        const float ms = *cluster.map_shared_rank(m_s + h, s);
-        const float w = ms == -INFINITY ? 0.f : __expf(ms - m);
-        l = fmaf(w, *cluster.map_shared_rank(l_s + h, s), l);
-        o = fmaf(w, *cluster.map_shared_rank(o_s + e, s), o);
-      }
-      static_cast<__nv_bfloat16*>(a.out)[(int64_t)i * H * DL + e] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
-      if (a.lse && e % DL == 0) a.lse[(int64_t)i * H + h] = l > 0.f ? m + logf(l) : -INFINITY;
+      for (int d = 0; d < C::DPT; ++d) o[d] = __float2bfloat16_rn(acc[h][d] * inv);
+    } else {
+      float* o = a.o_part + (int64_t)split * a.num_q * H * DL + o_off;
+#pragma unroll
+      for (int d = 0; d < C::DPT; ++d) o[d] = acc[h][d] * inv;
     }
-    cluster.sync();  // no CTA leaves while another reads its shared memory
-  } else {
-    // epilogue: normalise, write bf16 output or fp32 partial
-#pragma unroll
-    for (int h = 0; h < C::HPT; ++h) {
-      const int hh = hv0 + h;
-      const float l = l_s[hh];
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const int64_t o_off = ((int64_t)i * H + hh) * DL + dv0;
+    if (dv0 == 0) {
+      const float lse = l > 0.f ? m_s[hh] + logf(l) : -INFINITY;
       if (S == 1) {
-        __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) + o_off;
-#pragma unroll
-        for (int d = 0; d < C::DPT; ++d) o[d] = __float2bfloat16_rn(acc[h][d] * inv);
+        if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
       } else {
-        float* o = a.o_part + (int64_t)split * a.num_q * H * DL + o_off;
-#pragma unroll
-        for (int d = 0; d < C::DPT; ++d) o[d] = acc[h][d] * inv;
-      }
-      if (dv0 == 0) {
-        const float lse = l > 0.f ? m_s[hh] + logf(l) : -INFINITY;
-        if (S == 1) {
-          if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
-        } else {
-          a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
-        }
+        a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
       }
     }
   }
 }
 
-template <int H, int DL, int DR, bool DENSE, bool MERGE>
-cudaError_t launch_simt_shape(const MlaArgs& a, const int32_t* q_pos, cudaStream_t stream) {
+template <int H, int DL, int DR>
+cudaError_t launch_simt_shape(const MlaArgs& a, cudaStream_t stream) {
   using C = SimtCfg<H, DL, DR>;
-  auto kern = mla_simt_kernel<H, DL, DR, DENSE, MERGE>;
+  auto kern = mla_simt_kernel<H, DL, DR>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::smem_bytes);
   if (e != cudaSuccess) return e;
   dim3 grid(a.num_q, a.num_splits);
-  if constexpr (MERGE) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 1;
-    attr[0].val.clusterDim.y = (unsigned)a.num_splits;
-    attr[0].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(C::NT);
-    cfg.dynamicSmemBytes = C::smem_bytes;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, a, q_pos);
-    return e != cudaSuccess ? e : cudaGetLastError();
-  }
-  kern<<<grid, C::NT, C::smem_bytes, stream>>>(a, q_pos);
+  kern<<<grid, C::NT, C::smem_bytes, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -313,18 +257,9 @@ cudaError_t launch_simt_shape(const MlaArgs& a, const int32_t* q_pos, cudaStream
 
 cudaError_t launch_mla_simt(const MlaArgs& a, cudaStream_t stream) {
   if (a.num_q == 0) return cudaSuccess;
-  if (a.heads == 16 && a.d_latent == 64 && a.d_rope == 16)
-    return launch_simt_shape<16, 64, 16, false, false>(a, nullptr, stream);
-  if (a.heads == 64 && a.d_latent == 512 && a.d_rope == 64)
-    return launch_simt_shape<64, 512, 64, false, false>(a, nullptr, stream);
+  if (a.heads == 16 && a.d_latent == 64 && a.d_rope == 16) return launch_simt_shape<16, 64, 16>(a, stream);
+  if (a.heads == 64 && a.d_latent == 512 && a.d_rope == 64) return launch_simt_shape<64, 512, 64>(a, stream);
   return cudaErrorInvalidValue;
-}
-
-cudaError_t launch_chunk_simt(const MlaArgs& a, const int32_t* q_pos, bool merge, cudaStream_t stream) {
-  if (a.num_q == 0) return cudaSuccess;
-  if (a.heads != 16 || a.d_latent != 64 || a.d_rope != 16) return cudaErrorInvalidValue;
-  return merge ? launch_simt_shape<16, 64, 16, true, true>(a, q_pos, stream)
-               : launch_simt_shape<16, 64, 16, true, false>(a, q_pos, stream);
 }
 
 }  // namespace dsa

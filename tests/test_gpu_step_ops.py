@@ -17,7 +17,8 @@ Tolerances, each from the arithmetic:
       1 (the reference is one of the logits): row j adds at most 2^-17 |code_j| 2^-E
       <= 2^-21 s_max |code_j| to the output.  (An emulation of this rounding in numpy
       gives the kernel's largest excess over the first two terms, 0.00182809 on
-      the growing scales below, to eight digits.)
+      the growing scales below, to eight digits.)  The small head shape's weights are
+      fp16, 2^-11: within the first two terms.
 """
 import numpy as np
 import pytest

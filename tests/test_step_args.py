@@ -150,7 +150,7 @@ def test_chunk_split_rule(lib):
     assert pick(1, 1) == pick(1, 64) == pick(1, 256) == 1
     assert pick(1, 65536) >= 32
     assert pick(32, 8192) == 4 and pick(32, 1024) == 4 and pick(24, 4096) == 5
-    assert pick(2, 512, 16) == 8 and pick(128, 1024, 16) <= 4
+    assert pick(2, 512, 16) == 2 and pick(128, 1024, 16) == 1 and pick(1, 4096, 16) == 8 and pick(107, 12733, 16) == 5
     for n in (1, 3, 15, 16, 23, 24, 36, 37, 76, 77, 200):
         for ctx in (1, 63, 64, 65, 1000, 5000, 100000):
             s = pick(n, ctx)
