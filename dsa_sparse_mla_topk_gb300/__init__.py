@@ -3,7 +3,8 @@
 The three calls of the path -- ``topk_select``, ``sparse_mla_fwd`` and
 ``combine`` -- marshal torch tensors (device memory, the current CUDA stream)
 into the C ABI declared in ``include/dsa.h`` and run entirely in the
-library's CUDA kernels.  There is no CPU or PyTorch fallback: if the library
+library's CUDA kernels.  ``batch_layout``, ``qk_norm_rope``, ``chunk_mla`` and
+``verify_draft`` are the rest of a serving step around them.  There is no CPU or PyTorch fallback: if the library
 is missing, every call raises.
 """
 from __future__ import annotations
