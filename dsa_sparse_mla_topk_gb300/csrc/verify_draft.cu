@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
   // Waited for before the first write to another CTA's shared memory.  Nothing was
   // written yet that it would have to order: relaxed (a releasing arrive: 4 requests
   // 6.0 instead of 5.7 us).
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;");
+  asm volatile("barrier.cluster.arrive.relaxed;");
   const int32_t* xs = a.draft_tokens + row0;
   int32_t n = row1 - row0 - 1;
   if (n > a.max_out - 1) {  // drafts past the output's width are not looked at
@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
     s = warp_sum(s);
     mine = s;
     if (lane == 0) wsum[warp] = s;
-    if (turn == 0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
+    if (turn == 0) asm volatile("barrier.cluster.wait;" ::: "memory");  // every CTA of the cluster runs
     __syncthreads();
     if (tid < C) {
       int64_t cta = 0;
