@@ -717,6 +717,52 @@ def test_chunk_agrees_with_the_sparse_call_over_every_position():
     assert float((sl - cl).abs().max()) <= 1e-3
 
 
+# ---- offsets past 32 bits ------------------------------------------------------------
+
+
+@pytest.mark.parametrize("shape,slots", [((64, 512, 64), 8 << 20), ((16, 64, 16), 60 << 20)], ids=["h64", "h16"])
+@pytest.mark.parametrize("page", [64, 5])
+def test_cache_rows_past_4_gib(shape, slots, page):
+    """The same pages at the end of a cache of more than 2^32 bytes give the same
+    bits, and a row written there arrives there."""
+    c = _chunk_case(*shape, [300, 130], [3, 2], page, seed=61)
+    d = shape[1] + shape[2]
+    few = len(c["sc"]) // page
+    pages = slots // page
+    assert (pages - few) * page * d > 1 << 32
+    kv = torch.empty((pages * page, d), dtype=torch.uint8, device="cuda")
+    sc = torch.empty(pages * page, device="cuda")
+    kv[-few * page:].copy_(c["kv"])
+    sc[-few * page:].copy_(c["sc"])
+    for splits in (1, 3, 12):
+        want = _run_chunk(c, splits)
+        big = dict(c, kv=kv, sc=sc, table=c["table"] + (pages - few))
+        got = _run_chunk(big, splits)
+        assert got[2] == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    k = torch.randn((2, 1, d), device="cuda").to(torch.bfloat16)
+    last = i32([few * page - 1, 3])
+    kv2, sc2 = c["kv"].cuda(), c["sc"].cuda()
+    dsa.qk_norm_rope(None, k, None, None, d_rope=0, slot=last, kv=kv2, kv_scale=sc2)
+    dsa.qk_norm_rope(None, k, None, None, d_rope=0, slot=last + (pages - few) * page, kv=kv, kv_scale=sc)
+    assert torch.equal(kv[-few * page:], kv2) and torch.equal(sc[-few * page:], sc2)
+
+
+def test_verify_rows_past_32_bit_offsets():
+    rows, V, ld = 3, 1000, 1 << 30
+    g = torch.Generator().manual_seed(62)
+    p, q = (torch.softmax(3 * torch.randn((rows, V), generator=g), 1).cuda() for _ in range(2))
+    tok, cu = i32([5, 17, 0]), i32([0, rows])
+    ua, us = torch.rand(rows, generator=g).cuda(), torch.rand(1, generator=g).cuda()
+    mem = torch.empty((rows - 1) * ld + 2 * V, device="cuda")
+    far = [mem.as_strided((rows, V), (ld, 1), at) for at in (0, V)]
+    far[0].copy_(p), far[1].copy_(q)
+    for take in (0.0, 1.0):
+        u = torch.full_like(ua, take)
+        want = dsa.verify_draft(p, tok, cu, u, us, draft_probs=q, max_out=3)
+        got = dsa.verify_draft(far[0], tok, cu, u, us, draft_probs=far[1], max_out=3)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ---- streams and graphs ----------------------------------------------------------------
 
 
