@@ -682,16 +682,24 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     cluster.sync();
     float* fac = reinterpret_cast<float*>(smem + OFF_P);  // [S][64] factors of the splits' O (the P buffers are idle)
     if (tid < H) {
+      float ms[MAX_MERGED], ls[MAX_MERGED];  // (all the remote loads together)
+#pragma unroll
+      for (int s = 0; s < MAX_MERGED; ++s) {
+        ms[s] = s < S ? *cluster.map_shared_rank(ml_s + tid, s) : -INFINITY;
+        ls[s] = s < S ? *cluster.map_shared_rank(ml_s + H + tid, s) : 0.f;
+      }
       float m = -INFINITY, l = 0.f;
-      for (int s = 0; s < S; ++s) m = fmaxf(m, *cluster.map_shared_rank(ml_s + tid, s));
-      for (int s = 0; s < S; ++s) {
-        const float ms = *cluster.map_shared_rank(ml_s + tid, s);
-        const float w = ms == -INFINITY ? 0.f : ex2(ms - m);
-        l = fmaf(w, *cluster.map_shared_rank(ml_s + H + tid, s), l);
-        fac[s * H + tid] = w;
+#pragma unroll
+      for (int s = 0; s < MAX_MERGED; ++s) m = fmaxf(m, ms[s]);
+#pragma unroll
+      for (int s = 0; s < MAX_MERGED; ++s) {
+        ms[s] = ms[s] == -INFINITY ? 0.f : ex2(ms[s] - m);
+        l = fmaf(ms[s], ls[s], l);
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      for (int s = 0; s < S; ++s) fac[s * H + tid] *= inv;
+#pragma unroll
+      for (int s = 0; s < MAX_MERGED; ++s)
+        if (s < S) fac[s * H + tid] = ms[s] * inv;
       if (split == 0 && a.lse) a.lse[(int64_t)i * H + tid] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     }
     __syncthreads();

@@ -48,6 +48,7 @@ constexpr int WARPS = 8, NTHREADS = WARPS * 32;
 constexpr int T = 32;                    // rows per tile, one a lane for the lookups
 constexpr int NT = T / 8;                // MMA column blocks per tile
 constexpr int KS = DQK / 16;             // MMA steps of a logit: 4 latent, 1 rope
+constexpr int MAX_MERGED = chunk_max_merged();
 constexpr int OSTR = DL + 4;             // floats per head of a warp's O (bank spread)
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
@@ -299,13 +300,22 @@ __global__ void __launch_bounds__(NTHREADS, PER_SM)
     const int share = (NTHREADS + S - 1) / S, e = split * share + tid;
     if (tid < share && e < NTHREADS) {
       const int h = e >> 4, c = 4 * (e & 15);
+      float mk[MAX_MERGED], lk[MAX_MERGED];  // (all the remote loads together)
+      float4 vk[MAX_MERGED];
+#pragma unroll
+      for (int k = 0; k < MAX_MERGED; ++k) {
+        mk[k] = k < S ? *cluster.map_shared_rank(&mc_s[h], k) : -INFINITY;
+        lk[k] = k < S ? *cluster.map_shared_rank(&lc_s[h], k) : 0.f;
+        vk[k] = k < S ? *reinterpret_cast<const float4*>(cluster.map_shared_rank(&oc_s[h][c], k)) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
       m = -INFINITY, l = 0.f, s = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int k = 0; k < S; ++k) m = fmaxf(m, *cluster.map_shared_rank(&mc_s[h], k));
-      for (int k = 0; k < S; ++k) {
-        const float mk = *cluster.map_shared_rank(&mc_s[h], k);
-        const float w = mk == -INFINITY ? 0.f : ex2(mk - m);
-        const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(&oc_s[h][c], k));
-        l = fmaf(w, *cluster.map_shared_rank(&lc_s[h], k), l);
+#pragma unroll
+      for (int k = 0; k < MAX_MERGED; ++k) m = fmaxf(m, mk[k]);
+#pragma unroll
+      for (int k = 0; k < MAX_MERGED; ++k) {
+        const float w = mk[k] == -INFINITY ? 0.f : ex2(mk[k] - m);
+        const float4 v = vk[k];
+        l = fmaf(w, lk[k], l);
         s.x = fmaf(w, v.x, s.x), s.y = fmaf(w, v.y, s.y), s.z = fmaf(w, v.z, s.z), s.w = fmaf(w, v.w, s.w);
       }
       const float inv = l > 0.f ? 1.f / l : 0.f;
