@@ -16,8 +16,8 @@
 // runs at the power limit.  Measured, scales and pages of 64: 1,024 tokens at the
 // end of 16,384 in 1.57 ms (1,440 TFLOP/s of the formula's bf16 products, the
 // weights' second half not counted); 128 tokens of 16 requests, 4,096 positions
-// each, 70 us; 32 x 8,192 positions 42 us, every request's rows read once
-// (151 MB, 3.5 TB/s).  Warps:
+// each, 66 us in one split; 32 requests of 4,096 to 8,192 positions 42 us in
+// four (118 MB of rows, 2.8 TB/s).  Warps:
 //  * 3 (or 7) TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
 //    tiles in flight.  A tile whose positions are all visible comes in boxes
 //    of 64, 32, 16 or 8 rows, the largest that divides the page size (5 to
