@@ -20,9 +20,9 @@
 // of position, rotation and weights.  Keys have CTAs of their own: no warp runs
 // both sides' code.  In the half-split form a lane reads its partner chunk a
 // second time (an L1 hit), unless both halves of its pairs are in the lane
-// already.  Measured: 8,192 tokens of 64 x 576 + a key row into the cache 190 us,
-// 95% of a copy's bandwidth; 4,099 tokens of 32 + 8 heads of 128 15.6 us, 81%;
-// 128 tokens of 64 x 576 7.2 us, latency (the floor of its bytes is 2.8).
+// already.  Measured: 8,192 tokens of 64 x 576 + a key row into the cache 184 us,
+// 98% of a copy's bandwidth; 4,099 tokens of 32 + 8 heads of 128 15.4 us, 83%;
+// 128 tokens of 64 x 576 6.8 us, latency (the floor of its bytes is 2.8).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -34,7 +34,7 @@
 namespace dsa {
 namespace {
 
-constexpr int NR_WARPS = 4;
+constexpr int NR_WARPS = 2;  // (8,192 tokens of 64 x 576: 4 warps a CTA 190 us, 2 184; 128 tokens 1 8.8, 2 7.8)
 
 template <bool HALF>
 __device__ __forceinline__ void unpack8(const uint4 v, float (&x)[8]) {
@@ -87,7 +87,7 @@ __device__ __forceinline__ uint32_t code2(float x0, float x1) {  // two E4M3 cod
 // The first q_ctas CTAs take the queries, the rest the keys: no warp runs both
 // sides' code.
 template <bool HALF, bool PAIRS, int LPR, int CH, int NR>
-__global__ void __launch_bounds__(NR_WARPS * 32, 4)
+__global__ void __launch_bounds__(NR_WARPS * 32, 16 / NR_WARPS)
     qk_norm_rope_kernel(const NormRopeArgs a, const unsigned q_ctas, const FastDiv q_div, const FastDiv k_div) {
   constexpr int GPW = 32 / LPR;  // groups per warp
   const int lane = threadIdx.x & 31, gl = lane & (LPR - 1);
@@ -324,11 +324,20 @@ cudaError_t launch_type(const NormRopeArgs& a, cudaStream_t stream) {
   if (nch <= 16) return launch_shape<HALF, PAIRS, 8, 2, 4>(a, stream);
   if (nch <= 32) return launch_shape<HALF, PAIRS, 8, 4, 2>(a, stream);
   if (nch <= 72) {
-    // A warp a row while there are few rows: one token of 64 heads of 576 takes 3.7
-    // instead of 7.6 us, 128 tokens 7.2 instead of 8.6, 256 11.3 either way, 8,192
-    // 302 instead of 190.
-    const int64_t rows = (int64_t)a.num_tokens * (a.q.heads + a.k.heads);
-    if (rows <= 96 * (int64_t)device_sm_count()) return launch_shape<HALF, PAIRS, 32, 3, 1>(a, stream);
+    // A warp a row while there are few rows, then a warp for the rows of four heads or
+    // two (they share position, rotation and weights), and eight lanes a row once
+    // bandwidth counts.  Tokens of 64 heads of 576, us:
+    //                    1 row  4 rows  2 rows  8 lanes
+    //     1 token          3.7     4.5     4.1      7.4
+    //    64                5.3     5.4     5.1      7.8
+    //   128                7.8     6.8     8.0      9.0
+    //   320               13.4    13.6    12.5     15.2
+    //   512               19.5    18.2    17.7     17.6
+    // 8,192              302                      184
+    const int64_t rows = (int64_t)a.num_tokens * (a.q.heads + a.k.heads), sms = device_sm_count();
+    if (rows <= 32 * sms) return launch_shape<HALF, PAIRS, 32, 3, 1>(a, stream);
+    if (rows <= 72 * sms) return launch_shape<HALF, PAIRS, 32, 3, 4>(a, stream);
+    if (rows <= 200 * sms) return launch_shape<HALF, PAIRS, 32, 3, 2>(a, stream);
     return launch_shape<HALF, PAIRS, 8, 9, 2>(a, stream);
   }
   return launch_shape<HALF, PAIRS, 32, 4, 1>(a, stream);
