@@ -20,9 +20,10 @@
 // of position, rotation and weights.  Keys have CTAs of their own: no warp runs
 // both sides' code.  In the half-split form a lane reads its partner chunk a
 // second time (an L1 hit), unless both halves of its pairs are in the lane
-// already.  Measured: 8,192 tokens of 64 x 576 + a key row into the cache 184 us,
-// 98% of a copy's bandwidth; 4,099 tokens of 32 + 8 heads of 128 15.4 us, 83%;
-// 128 tokens of 64 x 576 6.8 us, latency (the floor of its bytes is 2.8).
+// already.  Measured: 8,192 tokens of 64 x 576 + a key row into the cache 181 us,
+// a copy's bandwidth; 4,099 tokens of 32 + 8 heads of 128 15.8 us, 80%, and 22 us with
+// cold caches, where a plain copy of the 43 MB takes 29; 128 tokens of 64 x 576
+// 6.5 us, 8.0 cold (the floor of its bytes is 2.8): latency.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -122,6 +123,12 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 16 / NR_WARPS)
     p = -1;
   }
   const bool live = p >= 0;  // a padding row, or a bad one, is left as it was
+  const float* cs = a.cos_sin + (int64_t)(live ? p : 0) * a.d_rope;
+  // The token's factors on their way while the rows arrive: in long calls (8,192 tokens of
+  // 32 + 8 heads of 128 36.7 -> 34.3 us with cold caches, of 64 x 576 187 -> 184); in
+  // short ones, a warp a row, the instructions cost more than they hide (128 tokens +0.1).
+  if (LPR == 8 && live)
+    for (int o = gl * 32; o < a.d_rope; o += LPR * 32) asm volatile("prefetch.global.L2 [%0];" ::"l"(cs + o));
   float inv[NR];
 #pragma unroll
   for (int r = 0; r < NR; ++r) {
@@ -143,7 +150,6 @@ __global__ void __launch_bounds__(NR_WARPS * 32, 16 / NR_WARPS)
     inv[r] = nn > 0 ? rsqrtf(ss / (float)side.norm_dim + a.eps) : 1.f;
   }
 
-  const float* cs = a.cos_sin + (int64_t)(live ? p : 0) * a.d_rope;
   auto load8 = [](const float* f, float (&v)[8]) {
     const float4 lo = *reinterpret_cast<const float4*>(f), hi = *reinterpret_cast<const float4*>(f + 4);
     v[0] = lo.x, v[1] = lo.y, v[2] = lo.z, v[3] = lo.w, v[4] = hi.x, v[5] = hi.y, v[6] = hi.z, v[7] = hi.w;
@@ -333,7 +339,7 @@ cudaError_t launch_type(const NormRopeArgs& a, cudaStream_t stream) {
     //   128                7.8     6.8     8.0      9.0
     //   320               13.4    13.6    12.5     15.2
     //   512               19.5    18.2    17.7     17.6
-    // 8,192              302                      184
+    // 8,192              302                      181
     const int64_t rows = (int64_t)a.num_tokens * (a.q.heads + a.k.heads), sms = device_sm_count();
     if (rows <= 32 * sms) return launch_shape<HALF, PAIRS, 32, 3, 1>(a, stream);
     if (rows <= 72 * sms) return launch_shape<HALF, PAIRS, 32, 3, 4>(a, stream);
