@@ -356,7 +356,8 @@ dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_len, cons
                             int32_t* held_out, int32_t* free_used_out, int32_t* dev_status, void* stream) {
   if (num_req <= 0 || bt_stride <= 0 || num_free < 0 || page_size <= 0 || num_pages <= 0 || capacity < 0)
     return DSA_ERR_INVALID_ARG;
-  if (num_req > dsa::batch_layout_max_requests() || num_pages > (int64_t)INT32_MAX / page_size)
+  // (the token loop counts four ahead, and one past the capacity, in 32 bits)
+  if (num_req > dsa::batch_layout_max_requests() || num_pages > (int64_t)INT32_MAX / page_size || capacity > (1 << 30))
     return DSA_ERR_UNSUPPORTED_SHAPE;
   if (!ctx_len || !new_len || !pages_held || !block_table || (num_free > 0 && !free_pages) || !free_used)
     return DSA_ERR_INVALID_ARG;

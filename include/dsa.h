@@ -339,7 +339,7 @@ DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const
  *   block_table    int32 [num_req, bt_stride] page ids, updated in place.
  *   free_pages     int32 [num_free] page ids; free_used int32 [1]: how many of
  *                  them earlier calls have taken.
- *   num_req        at most 8,192 (else UNSUPPORTED_SHAPE).
+ *   num_req        at most 8,192, capacity at most 2^30 (else UNSUPPORTED_SHAPE).
  * Data errors leave a request as it is (ctx_out = ctx_len, held_out =
  * pages_held, no pages taken, -1 for its tokens): a negative length sets
  * DSA_DEV_BAD_QPOS (and the request has no tokens in cu_q); a block table row

@@ -1,0 +1,18 @@
+"""CPU tests of the serving step's calls at the edges of their arguments: sizes
+whose counters would wrap, overlaps, errors left behind, the binding's loading."""
+import ctypes
+
+import pytest
+import torch
+
+import dsa_sparse_mla_topk_gb300 as dsa
+from test_step_args import A, _chunk, _layout, _norm, _verify, lib, no_device_only  # noqa: F401
+
+
+@no_device_only
+@pytest.mark.parametrize("cap,expect", [((1 << 30) + 1, 2), ((1 << 31) - 4, 2), ((1 << 31) - 1, 2)])
+def test_layout_capacity_that_its_counters_cannot_hold(lib, cap, expect):  # noqa: F811
+    """Four tokens past, or one past, a capacity near 2^31 is a negative number: the
+    last 16-byte store would go past the arrays."""
+    far = [ctypes.c_void_p(x << 36) for x in range(1, 4)]
+    assert _layout(lib, cap=cap, req=far[0], pos=far[1], slot=far[2]) == expect
