@@ -484,7 +484,9 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
   if (num_rows < 0 || vocab <= 0 || num_req < 0 || max_out <= 0 || ld_target < vocab) return DSA_ERR_INVALID_ARG;
   if (draft_probs && ld_draft < vocab) return DSA_ERR_INVALID_ARG;
   if ((ctx_len == nullptr) != (ctx_out == nullptr)) return DSA_ERR_INVALID_ARG;
-  if (num_req > (1 << 24) || vocab > (1 << 30)) return DSA_ERR_UNSUPPORTED_SHAPE;
+  // (loops over rows, columns and outputs count up to 1,024 ahead in 32 bits)
+  if (num_req > (1 << 24) || vocab > (1 << 30) || num_rows > (1 << 30) || max_out > (1 << 30))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
   if (num_req == 0) return DSA_OK;
   if (!u_sample || !cu_rows || !tokens || !num_out) return DSA_ERR_INVALID_ARG;
   if (num_rows > 0 && (!target_probs || !draft_tokens || !u_accept)) return DSA_ERR_INVALID_ARG;

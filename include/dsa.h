@@ -450,7 +450,8 @@ DSA_API dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const flo
  * target_probs[t_a].  Weights and sums are whole multiples of 2^-60: exact for
  * probabilities of 2^-37 or more, and independent of the launch.
  *
- *   num_req at most 2^24, vocab at most 2^30 (else UNSUPPORTED_SHAPE).
+ *   num_req at most 2^24; vocab, num_rows and max_out at most 2^30 (else
+ *   UNSUPPORTED_SHAPE).
  *   target_probs  fp32 [num_rows, vocab], row stride ld_target; each row in
  *                 [0, 1] with a sum below 8 (NaN and negative values count as
  *                 0, values above 1 as 1; a larger sum gives an unspecified token in range).

@@ -16,3 +16,13 @@ def test_layout_capacity_that_its_counters_cannot_hold(lib, cap, expect):  # noq
     last 16-byte store would go past the arrays."""
     far = [ctypes.c_void_p(x << 36) for x in range(1, 4)]
     assert _layout(lib, cap=cap, req=far[0], pos=far[1], slot=far[2]) == expect
+
+
+@no_device_only
+@pytest.mark.parametrize("over", [dict(mo=(1 << 30) + 1), dict(mo=(1 << 31) - 1), dict(rows=(1 << 30) + 1),
+                                  dict(rows=(1 << 31) - 1)])
+def test_verify_sizes_that_its_counters_cannot_hold(lib, over):  # noqa: F811
+    """Rows and outputs are counted 32 or a block of threads ahead: near 2^31 the count
+    would turn negative and the loop would go on."""
+    far = {k: ctypes.c_void_p(x << 44) for x, k in enumerate(("p", "q", "tok", "ua", "us", "cu", "ctx", "out", "num", "co"), 1)}
+    assert _verify(lib, **far, **over) == 2
