@@ -223,15 +223,20 @@ __global__ void __launch_bounds__(BL_THREADS) batch_layout_kernel(const BatchLay
   }
 }
 
+// four words a request (cu and first have one more)
+size_t smem_bytes(int num_req) { return sizeof(int32_t) * (4 * (size_t)num_req + 2); }
+
 }  // namespace
 
 int batch_layout_max_requests() { return 8192; }
 
 cudaError_t launch_batch_layout(const BatchLayoutArgs& a, cudaStream_t stream) {
-  // four words a request (cu and first have one more)
-  const size_t smem = sizeof(int32_t) * (4 * (size_t)a.num_req + 2);
+  const size_t smem = smem_bytes(a.num_req);
   if (smem > 48 * 1024) {  // more than a launch may take unasked
-    const cudaError_t e = cudaFuncSetAttribute(batch_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // The limit is the kernel's, for every thread of the process: always the largest
+    // batch's, so that no call lowers it between another one's two steps.
+    const cudaError_t e = cudaFuncSetAttribute(batch_layout_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)smem_bytes(batch_layout_max_requests()));
     if (e != cudaSuccess) return e;
   }
   const int64_t groups = ((int64_t)a.capacity + BL_TOK - 1) / BL_TOK;
