@@ -13,7 +13,13 @@ bool supported_shape(int32_t h, int32_t dl, int32_t dr) {
   return (h == 16 && dl == 64 && dr == 16) || (h == 64 && dl == 512 && dr == 64);
 }
 
-dsa_status from_cuda(cudaError_t e) { return e == cudaSuccess ? DSA_OK : DSA_ERR_CUDA; }
+// (an error that the status tells is taken off the runtime's record, where the
+// process's next, unrelated check would find it)
+dsa_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return DSA_OK;
+  (void)cudaGetLastError();
+  return DSA_ERR_CUDA;
+}
 
 // The 64-head shape runs on the tensor cores, the 16-head shape on the CUDA
 // cores; nothing else changes that choice.

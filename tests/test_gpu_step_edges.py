@@ -1,6 +1,7 @@
 """GPU tests of the serving step's operators at the edges of what their calls
 allow: several host threads, refused requests, bad pages, values that are not
 finite, scales that differ widely, and closer bounds on the attention's error."""
+import ctypes
 import threading
 
 import numpy as np
@@ -55,3 +56,45 @@ def test_layout_large_batches_from_several_threads():
     for t in threads:
         t.join()
     assert not errors, errors
+
+
+# ---- errors ------------------------------------------------------------------------
+
+
+def test_a_refused_launch_leaves_no_error_behind():
+    """A launch that the runtime refuses (the legacy stream while a blocking stream is
+    captured) comes back as a status, and the next, unrelated check finds nothing."""
+    rt = ctypes.CDLL("libcudart.so.13")
+    c, n, held, table, free, pages = ops._layout_case(9, 6, 100, 16, seed=11)
+    lay = (ops.i32(c), ops.i32(n), ops.i32(held), torch.from_numpy(table).cuda(), ops.i32(free), ops.i32([0]))
+    out = dsa.BatchLayout(*[torch.empty(m, dtype=I32, device="cuda") for m in (10, 70, 70, 70, 9, 9, 1)])
+    p, q, tok, cu, ua, us = ops._verify_case(3, 2, 100, True, seed=1)
+    vo = dict(tokens=torch.empty((3, 3), dtype=I32, device="cuda"), num_out=torch.empty(3, dtype=I32, device="cuda"))
+    calls = [lambda: dsa.batch_layout(*lay, page_size=16, num_pages=pages, capacity=70, out=out),
+             lambda: dsa.verify_draft(p, tok, cu, ua, us, draft_probs=q, max_out=3, **vo)]
+    for f in calls:
+        f()
+    for shape in SHAPES:
+        ch = ops._cuda(ops._chunk_case(*shape, [300, 100], [3, 2], 64, seed=10))
+        buf = dict(out=torch.empty((5, shape[0], shape[1]), dtype=torch.bfloat16, device="cuda"),
+                   lse=torch.empty((5, shape[0]), device="cuda"))
+        calls.append(lambda ch=ch, buf=buf, shape=shape: dsa.chunk_mla(
+            ch["q"], ch["kv"], ch["sc"], ch["table"], ch["req"], ch["pos"], d_latent=shape[1], d_rope=shape[2],
+            page_size=64, softmax_scale=0.04, num_splits=2, buffers=buf))
+        calls[-1]()
+    torch.cuda.synchronize()
+    assert torch.cuda.current_stream().cuda_stream == 0 and rt.cudaGetLastError() == 0
+    for i, f in enumerate(calls):
+        s, g = ctypes.c_void_p(), ctypes.c_void_p()
+        assert rt.cudaStreamCreate(ctypes.byref(s)) == 0
+        assert rt.cudaStreamBeginCapture(s, 0) == 0
+        with pytest.raises(dsa.DsaError) as e:
+            f()
+        left = rt.cudaPeekAtLastError()
+        rt.cudaStreamEndCapture(s, ctypes.byref(g))
+        rt.cudaStreamDestroy(s)
+        rt.cudaGetLastError()
+        assert e.value.status == 4 and left == 0, (i, left)
+    for f in calls:  # as before
+        f()
+    torch.cuda.synchronize()
