@@ -336,6 +336,22 @@ bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
   return a && b && na > 0 && nb > 0 && x < y + (uint64_t)nb && y < x + (uint64_t)na;
 }
 
+struct Span {
+  const void* p;
+  int64_t bytes;
+};
+// Whether a written span overlaps an input or another written one.
+template <int NO, int NI>
+bool outputs_overlap(const Span (&out)[NO], const Span (&in)[NI]) {
+  for (int o = 0; o < NO; ++o) {
+    for (int i = 0; i < NI; ++i)
+      if (overlap(out[o].p, out[o].bytes, in[i].p, in[i].bytes)) return true;
+    for (int x = 0; x < o; ++x)
+      if (overlap(out[o].p, out[o].bytes, out[x].p, out[x].bytes)) return true;
+  }
+  return false;
+}
+
 // Bytes from the first to the last value of 16-bit rows [tokens, heads, d].
 int64_t row_span(int64_t tokens, int64_t heads, int64_t ts, int64_t hs, int64_t d) {
   return tokens > 0 && heads > 0 ? 2 * ((tokens - 1) * ts + (heads - 1) * hs + d) : 0;
@@ -369,15 +385,12 @@ dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_len, cons
     return DSA_ERR_INVALID_ARG;
   if (!cu_q || (capacity > 0 && (!q_req || !q_pos || !slot)) || !ctx_out || !held_out || !free_used_out)
     return DSA_ERR_INVALID_ARG;
-  // every CTA reads the inputs while one writes the new lengths
-  const int64_t nr = 4 * (int64_t)num_req;
-  const void* in[6] = {ctx_len, new_len, pages_held, free_used, free_pages, block_table};
-  const int64_t in_bytes[6] = {nr, nr, nr, 4, 4 * (int64_t)num_free, nr * bt_stride};
-  const void* out[7] = {cu_q, ctx_out, held_out, free_used_out, q_req, q_pos, slot};
-  const int64_t nt = 4 * (int64_t)capacity, out_bytes[7] = {nr + 4, nr, nr, 4, nt, nt, nt};
-  for (int i = 0; i < 6; ++i)
-    for (int o = 0; o < 7; ++o)
-      if (overlap(in[i], in_bytes[i], out[o], out_bytes[o])) return DSA_ERR_INVALID_ARG;
+  // every CTA reads the inputs while one writes the new lengths, and others the table
+  const int64_t nr = 4 * (int64_t)num_req, nt = 4 * (int64_t)capacity;
+  const Span in[5] = {{ctx_len, nr}, {new_len, nr}, {pages_held, nr}, {free_used, 4}, {free_pages, 4 * (int64_t)num_free}};
+  const Span out[8] = {{block_table, nr * bt_stride}, {cu_q, nr + 4}, {ctx_out, nr}, {held_out, nr}, {free_used_out, 4},
+                       {q_req, nt}, {q_pos, nt}, {slot, nt}};
+  if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
   dsa::BatchLayoutArgs a;
   a.ctx_len = ctx_len;
   a.new_len = new_len;

@@ -331,9 +331,9 @@ DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const
  *                  -1 in all three for every t >= cu_q[num_req].
  *   ctx_out, held_out  int32 [num_req]: ctx_len + new_len and the pages then held.
  *   free_used_out  int32 [1]: *free_used plus the pages taken.
- * The outputs must not overlap the inputs (lengths and free_used: two sets
- * used in turn): INVALID_ARG otherwise.  Only new entries of block_table are
- * written.
+ * The outputs and block_table must not overlap the inputs (lengths and
+ * free_used: two sets used in turn) or each other: INVALID_ARG otherwise.
+ * Only new entries of block_table are written.
  *
  *   ctx_len, new_len, pages_held  int32 [num_req].
  *   block_table    int32 [num_req, bt_stride] page ids, updated in place.

@@ -26,3 +26,23 @@ def test_verify_sizes_that_its_counters_cannot_hold(lib, over):  # noqa: F811
     would turn negative and the loop would go on."""
     far = {k: ctypes.c_void_p(x << 44) for x, k in enumerate(("p", "q", "tok", "ua", "us", "cu", "ctx", "out", "num", "co"), 1)}
     assert _verify(lib, **far, **over) == 2
+
+
+def at(base, off):
+    return ctypes.c_void_p(base.value + off)
+
+
+@no_device_only
+def test_layout_table_over_its_inputs_and_outputs_over_each_other(lib):  # noqa: F811
+    """The block table is written: it may not lie over the lengths or the free list."""
+    table = 4 * 4 * 8  # its bytes
+    for x in (0, 1, 2, 4, 5):  # lengths, held pages, free_pages, free_used
+        assert _layout(lib, bt=A(x)) == 1, x
+        assert _layout(lib, bt=at(A(x), -table + 4)) == 1, x
+        assert _layout(lib, bt=at(A(x), -table)) == 4, x  # next to it (4: no device to launch on)
+    outs = dict(cu=4 * 5, req=4 * 64, pos=4 * 64, slot=4 * 64, co=16, ho=16, uo=4)
+    for a, n in outs.items():
+        for b in outs:
+            if a < b:
+                assert _layout(lib, **{a: A(20), b: at(A(20), n - 4)}) == 1, (a, b)
+                assert _layout(lib, **{a: A(20), b: at(A(20), n)}) == 4, (a, b)
