@@ -439,14 +439,17 @@ dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t q_head_
   if ((int64_t)num_tokens * (q_heads + k_heads) > INT32_MAX) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (num_tokens == 0 || q_heads + k_heads == 0) return DSA_OK;
   if (d_rope > 0 && (!pos || !cos_sin || !aligned16(cos_sin) || max_pos <= 0)) return DSA_ERR_INVALID_ARG;
-  // a row may be written before another CTA has read its own: only a side in place shares memory
-  const int64_t q_in = row_span(num_tokens, q_heads, q_tok_stride, q_head_stride, d);
-  const int64_t k_in = row_span(num_tokens, k_heads, k_tok_stride, k_head_stride, d);
-  const int64_t q_to = q_heads > 0 ? 2 * (int64_t)num_tokens * q_heads * d : 0;
-  const int64_t k_to = k_heads > 0 ? 2 * (int64_t)num_tokens * k_heads * d : 0;
-  if ((q_out != q && overlap(q_out, q_to, q, q_in)) || (k_out != k && overlap(k_out, k_to, k, k_in)) ||
-      overlap(q_out, q_to, k, k_in) || overlap(k_out, k_to, q, q_in) || overlap(q_out, q_to, k_out, k_to))
-    return DSA_ERR_INVALID_ARG;
+  // a row may be written before another CTA has read its own: only a side in place shares
+  // memory, and its input then stands for both
+  const int64_t n = num_tokens, n4 = 4 * n;
+  const int64_t q_in = row_span(n, q_heads, q_tok_stride, q_head_stride, d);
+  const int64_t k_in = row_span(n, k_heads, k_tok_stride, k_head_stride, d);
+  const bool q_own = q_heads > 0 && q_out == q, k_own = k_heads > 0 && k_out == k;
+  const Span in[7] = {{q_own ? nullptr : q, q_in}, {k_own ? nullptr : k, k_in}, {q_heads > 0 ? q_weight : nullptr, 4 * (int64_t)q_norm_dim},
+                      {k_heads > 0 ? k_weight : nullptr, 4 * (int64_t)k_norm_dim}, {pos, n4},
+                      {d_rope > 0 ? cos_sin : nullptr, 4 * (int64_t)max_pos * d_rope}, {slot, n4}};
+  const Span out[4] = {{q_out, 2 * n * q_heads * d}, {k_out, 2 * n * k_heads * d}, {kv, num_slots * d}, {kv_scale, 4 * num_slots}};
+  if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
   dsa::NormRopeArgs a;
   a.q = {q, q_tok_stride, q_head_stride, q_heads, q_norm_dim, q_weight, q_heads > 0 ? q_out : nullptr};
   a.k = {k, k_tok_stride, k_head_stride, k_heads, k_norm_dim, k_weight, k_heads > 0 ? k_out : nullptr};
@@ -482,12 +485,14 @@ dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_s
                                        merge ? 1 : num_splits, out, lse, o_part, lse_part, 0, nullptr, 0, dev_status,
                                        &a);
   if (st != DSA_OK || num_q == 0) return st;
-  // a token's result may be written before another token's query is read
-  const int64_t rows = (int64_t)num_q * num_heads;
+  // a token's result may be written before another token has read what it needs
+  const int64_t rows = (int64_t)num_q * num_heads, slots = num_pages * page_size, n4 = 4 * (int64_t)num_q;
   const bool whole = num_splits == 1 || merge;
-  if (whole ? overlap(q, 2 * rows * (d_latent + d_rope), out, 2 * rows * d_latent)
-            : overlap(q, 2 * rows * (d_latent + d_rope), o_part, 4 * rows * d_latent * num_splits))
-    return DSA_ERR_INVALID_ARG;
+  const Span in[6] = {{q, 2 * rows * (d_latent + d_rope)}, {kv, slots * (d_latent + d_rope)}, {kv_scale, 4 * slots},
+                      {block_table, 4 * (int64_t)num_req * bt_stride}, {q_req, n4}, {q_pos, n4}};
+  const Span out_whole[2] = {{out, 2 * rows * d_latent}, {lse, 4 * rows}};
+  const Span out_part[2] = {{o_part, 4 * rows * d_latent * num_splits}, {lse_part, 4 * rows * num_splits}};
+  if (outputs_overlap(whole ? out_whole : out_part, in)) return DSA_ERR_INVALID_ARG;
   a.idx = nullptr;
   a.num_splits = num_splits;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -509,18 +514,15 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
   if (num_req == 0) return DSA_OK;
   if (!u_sample || !cu_rows || !tokens || !num_out) return DSA_ERR_INVALID_ARG;
   if (num_rows > 0 && (!target_probs || !draft_tokens || !u_accept)) return DSA_ERR_INVALID_ARG;
-  // eight CTAs read a request's inputs while one writes its results
+  // eight CTAs read a request's inputs while one writes its results (only ctx_len is read
+  // by the thread that writes ctx_out over it)
   const int64_t nr = 4 * (int64_t)num_req, nd = 4 * (int64_t)num_rows;
-  const void* in[4] = {draft_tokens, u_accept, u_sample, cu_rows};
-  const int64_t in_bytes[4] = {nd, nd, nr, nr + 4};
-  const void* out[3] = {tokens, num_out, ctx_out};
-  const int64_t out_bytes[3] = {nr * max_out, nr, nr};
-  for (int i = 0; i < 4; ++i)
-    for (int o = 0; o < 3; ++o)
-      if (overlap(in[i], in_bytes[i], out[o], out_bytes[o])) return DSA_ERR_INVALID_ARG;
-  if (overlap(ctx_len, nr, tokens, nr * max_out) || overlap(ctx_len, nr, num_out, nr) ||
-      (ctx_out != ctx_len && overlap(ctx_len, nr, ctx_out, nr)))
-    return DSA_ERR_INVALID_ARG;
+  const Span in[7] = {{target_probs, num_rows > 0 ? 4 * ((num_rows - 1) * ld_target + vocab) : 0},
+                      {draft_probs, num_rows > 0 ? 4 * ((num_rows - 1) * ld_draft + vocab) : 0},
+                      {draft_tokens, nd}, {u_accept, nd}, {u_sample, nr}, {cu_rows, nr + 4},
+                      {ctx_out == ctx_len ? nullptr : ctx_len, nr}};
+  const Span out[3] = {{tokens, nr * max_out}, {num_out, nr}, {ctx_out, nr}};
+  if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
   dsa::VerifyArgs a;
   a.target = target_probs;
   a.ld_target = ld_target;

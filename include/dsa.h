@@ -377,8 +377,9 @@ DSA_API dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_l
  *             addressed by token and head strides in elements (multiples of 8;
  *             16-byte aligned base).  q_heads or k_heads may be 0 (the side is absent).
  *   q_out, k_out  contiguous [num_tokens, heads, d], 16-byte aligned.  Each may be
- *             its own input (then contiguous), else must not overlap q, k or
- *             each other (INVALID_ARG).  k_out may be NULL when the cache is written.
+ *             its own input (then contiguous); else what is written (these, kv,
+ *             kv_scale) must not overlap an input or each other (INVALID_ARG).
+ *             k_out may be NULL when the cache is written.
  *   q_weight, k_weight  fp32 [norm_dim], 16-byte aligned; norm_dim a multiple of 8, at
  *             most d; 0: no norm (weight may be NULL).
  *   d         a multiple of 8, at most 1024.  d_rope a multiple of 16, at most
@@ -419,8 +420,8 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t
  * a contiguous share of the token's own KV tiles.  With 2 to 8 splits and
  * o_part and lse_part both NULL the call merges them itself (the splits of a
  * token are one thread-block cluster) and writes out and lse; else the splits
- * write o_part and lse_part for dsa_combine.  out and o_part must not overlap
- * q (INVALID_ARG).  A token with q_req = -1
+ * write o_part and lse_part for dsa_combine.  What is written must not overlap
+ * an input or each other (INVALID_ARG).  A token with q_req = -1
  * (padding) or q_pos = -1 sees nothing: out = 0 and lse = -inf.  Tokens of one
  * request next to each other share its rows in L2; any order is correct.
  * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
@@ -466,7 +467,7 @@ DSA_API dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const flo
  *   ctx_len, ctx_out  int32 [num_req], or both NULL: ctx_out = ctx_len + num_out,
  *                 the request's cached positions once the rejected rows are
  *                 dropped (the same buffer is allowed).  Other overlaps of outputs
- *                 with draft_tokens, u_*, cu_rows or ctx_len: INVALID_ARG.
+ *                 with inputs or each other: INVALID_ARG.
  * A request without rows has num_out = 0 and tokens -1.  Data errors, all
  * DSA_DEV_BAD_INDEX: cu_rows decreasing or past num_rows (as a request
  * without rows); a draft outside [0, vocab) (not taken); more rows than

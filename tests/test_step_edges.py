@@ -46,3 +46,30 @@ def test_layout_table_over_its_inputs_and_outputs_over_each_other(lib):  # noqa:
             if a < b:
                 assert _layout(lib, **{a: A(20), b: at(A(20), n - 4)}) == 1, (a, b)
                 assert _layout(lib, **{a: A(20), b: at(A(20), n)}) == 4, (a, b)
+
+
+@no_device_only
+def test_outputs_over_any_input_or_each_other(lib):  # noqa: F811
+    """Not over the queries alone: other CTAs still read positions, tables, weights,
+    probabilities and cache rows while the first results are written."""
+    # 4 = taken, but no device to launch on
+    for x in (1, 4, 5, 6, 7):  # weights, positions, cos_sin, slots under the rows and the cache that are written
+        for k in ("qo", "kv", "sc"):
+            assert _norm(lib, **{k: A(x)}) == 1, (k, x)
+    assert _norm(lib, kv=A(0)) == 1 and _norm(lib, kv=A(3)) == 1 and _norm(lib, sc=A(3)) == 1
+    assert _norm(lib, kv=A(2)) == 1 and _norm(lib, sc=A(8)) == 1
+    assert _norm(lib, qo=A(0)) == 4 and _norm(lib, ko=A(3)) == 4 and _norm(lib) == 4  # in place; apart
+    for k in ("out", "lse"):
+        for x in range(6):
+            assert _chunk(lib, **{k: A(x)}) == 1, (k, x)
+    assert _chunk(lib, lse=at(A(6), 2 * 64 * 512 - 4)) == 1 and _chunk(lib, lse=at(A(6), 2 * 64 * 512)) == 4
+    part = dict(S=2, op=A(20), lp=A(21))
+    assert _chunk(lib, **part) == 4 and _chunk(lib, **{**part, "lp": A(1)}) == 1
+    assert _chunk(lib, **{**part, "op": A(3)}) == 1 and _chunk(lib, **{**part, "lp": A(20)}) == 1
+    assert _chunk(lib, **part, out=A(0), lse=A(0)) == 4  # not written
+    for k in ("out", "num", "co"):
+        for x in (0, 1):
+            assert _verify(lib, **{k: at(A(x), 4 * (7 * 100 + 96))}) == 1, (k, x)
+            assert _verify(lib, **{k: at(A(x), 4 * (7 * 100 + 100))}) == 4, (k, x)
+    assert _verify(lib, out=A(20), num=at(A(20), 28)) == 1 and _verify(lib, num=A(20), co=A(20)) == 1
+    assert _verify(lib, co=A(6)) == 4  # the lengths in place
