@@ -96,17 +96,16 @@ __global__ void __launch_bounds__(NTHREADS, PER_SM)
   const int t_begin = (int)((int64_t)ntiles * split / S), t_end = (int)((int64_t)ntiles * (split + 1) / S);
   const int32_t* bt = a.block_table + (int64_t)(req_ok ? r : 0) * a.bt_stride;
 
-  // a tile's rows: page ids, then slots, lane l for row l (-1: none)
-  auto page_of = [&](int tile) -> int {
-    const int pos = tile * T + lane;
-    return tile < t_end && pos < n ? __ldg(bt + page_div(pos)) : -2;
-  };
+  // a tile's rows: page ids, then slots, lane l for row l (-1: none).  Whether a row is
+  // there at all goes by its position: a page id may be any number.
+  auto has_row = [&](int tile) { return tile < t_end && tile * T + lane < n; };
+  auto page_of = [&](int tile) -> int { return has_row(tile) ? __ldg(bt + page_div(tile * T + lane)) : -1; };
   auto slot_of = [&](int tile, int page) -> int {
     if (page >= 0 && page < a.num_pages) {
       const int pos = tile * T + lane;
       return page * P + (pos - page_div(pos) * P);
     }
-    if (page != -2) report(a.dev_status, DSA_DEV_BAD_PAGE);
+    if (has_row(tile)) report(a.dev_status, DSA_DEV_BAD_PAGE);
     return -1;
   };
   struct Rows {

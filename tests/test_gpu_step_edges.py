@@ -58,6 +58,21 @@ def test_layout_large_batches_from_several_threads():
     assert not errors, errors
 
 
+# ---- chunk_mla ---------------------------------------------------------------------
+
+
+@both_shapes
+@pytest.mark.parametrize("bad", [-1, -2, -3, -2**31, 1 << 20, 2**31 - 1])
+def test_chunk_any_page_id_out_of_range_is_told(shape, bad):
+    c = ops._chunk_case(*shape, [200, 100], [2, 1], 64, seed=9)
+    c["table"][0, 1] = bad
+    want = ops._chunk_ref(dict(c, table=torch.where(c["table"] == bad, torch.tensor(1 << 20, dtype=I32), c["table"])))
+    for splits in (1, 3):
+        out, lse, st = ops._run_chunk(c, splits)
+        assert st == dsa.DEV_BAD_PAGE
+        ops._check_chunk(out, lse, want)
+
+
 # ---- errors ------------------------------------------------------------------------
 
 
