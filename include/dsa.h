@@ -303,7 +303,8 @@ DSA_API dsa_status dsa_combine(const float* o_part, const float* lse_part, int32
  * (nothing is launched); a request or page id out of range sets
  * DSA_DEV_BAD_PAGE, a position outside the block table row sets
  * DSA_DEV_BAD_INDEX, and that row is skipped.  Rows aimed at the same slot
- * leave one of them there, unspecified which.  Asynchronous on `stream`.
+ * leave an unspecified mixture of them there (scale and codes need not be of one
+ * row); other slots are as written.  Asynchronous on `stream`.
  */
 DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const int32_t* req, const int32_t* pos,
                                 const int32_t* block_table, int32_t num_req, int32_t bt_stride, int32_t page_size,
@@ -393,8 +394,10 @@ DSA_API dsa_status dsa_batch_layout(const int32_t* ctx_len, const int32_t* new_l
  *             d] 16-byte aligned, kv_scale fp32 [num_slots].
  * Data errors: pos outside [-1, max_pos) sets DSA_DEV_BAD_QPOS and the token
  * is skipped; slot outside [-1, num_slots) sets DSA_DEV_BAD_INDEX and the row
- * is not cached.  Rows aimed at the same slot leave one of them there,
- * unspecified which.  Rows with NaN or infinities give unspecified values.
+ * is not cached.  Rows aimed at the same slot leave an unspecified mixture of
+ * them there (scale and codes need not be of one row): live slots have to be
+ * different, as dsa_batch_layout's are while pages are.  Rows with NaN or
+ * infinities give unspecified values.
  */
 #define DSA_BF16 0
 #define DSA_FP16 1

@@ -58,6 +58,24 @@ def test_layout_large_batches_from_several_threads():
     assert not errors, errors
 
 
+# ---- qk_norm_rope ------------------------------------------------------------------
+
+
+def test_norm_rope_same_slot_twice_leaves_the_other_slots_right():
+    """Two rows aimed at one slot leave some mixture there, and everything else as written."""
+    T, d = 40, 576
+    q, k, g = ops._qk_inputs(T, 2, 1, d, torch.bfloat16, seed=5)
+    slot = torch.arange(T, dtype=I32) + 3
+    slot[7] = slot[30]
+    kv = torch.full((T + 6, d), 0xAA, dtype=torch.uint8, device="cuda")
+    sc = torch.full((T + 6,), -1.0, device="cuda")
+    dsa.qk_norm_rope(q, k, None, None, d_rope=0, slot=slot.cuda(), kv=kv, kv_scale=sc)
+    rows = [t for t in range(T) if t not in (7, 30)]
+    ops._check_codes(kv[slot[rows].long().cuda()], sc[slot[rows].long().cuda()], ops.host(k.double())[rows, 0])
+    for at in (0, 1, 2, 10, T + 3, T + 4, T + 5):  # no row's
+        assert (kv[at] == 0xAA).all() and sc[at] == -1.0
+
+
 # ---- chunk_mla ---------------------------------------------------------------------
 
 
