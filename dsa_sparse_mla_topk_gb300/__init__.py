@@ -33,7 +33,7 @@ EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_
                     "dsa_sparse_mla_fwd", "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_fwd_noalloc",
                     "dsa_sparse_mla_topk_fwd", "dsa_sparse_mla_topk_max_k", "dsa_topk_sparse_mla_fwd",
                     "dsa_combine", "dsa_kv_write", "dsa_batch_layout", "dsa_qk_norm_rope", "dsa_chunk_mla_fwd",
-                    "dsa_verify_draft", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
+                    "dsa_verify_draft", "dsa_verify_draft_req", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
                     "dsa_prefix_cache_acquire", "dsa_prefix_cache_release", "dsa_prefix_cache_stats",
                     "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits",
                     "dsa_chunk_pick_num_splits")
@@ -101,6 +101,9 @@ def load_library(path: str | None = None):
         lib.dsa_chunk_mla_fwd.restype = i32
         lib.dsa_verify_draft.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp, vp]
         lib.dsa_verify_draft.restype = i32
+        lib.dsa_verify_draft_req.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp,
+                                             vp]
+        lib.dsa_verify_draft_req.restype = i32
         lib.dsa_prefix_cache_create.argtypes = [i32, i32]
         lib.dsa_prefix_cache_create.restype = vp
         lib.dsa_prefix_cache_destroy.argtypes = [vp]
@@ -142,7 +145,7 @@ def _load_marshal(lib):
     loader.exec_module(m)
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
              for f in (lib.dsa_batch_layout, lib.dsa_qk_norm_rope, lib.dsa_chunk_mla_fwd, lib.dsa_combine,
-                       lib.dsa_chunk_pick_num_splits, lib.dsa_verify_draft)))
+                       lib.dsa_chunk_pick_num_splits, lib.dsa_verify_draft_req)))
     return m
 
 
@@ -878,17 +881,19 @@ def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_ro
 
 def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows: torch.Tensor,
                  u_accept: torch.Tensor, u_sample: torch.Tensor, *, draft_probs: torch.Tensor | None = None,
-                 ctx_len: torch.Tensor | None = None, max_out: int, tokens: torch.Tensor | None = None,
+                 ctx_len: torch.Tensor | None = None, q_req: torch.Tensor | None = None, max_out: int, tokens: torch.Tensor | None = None,
                  num_out: torch.Tensor | None = None, ctx_out: torch.Tensor | None = None, dev_status=None, stream=None):
     """Verification of drafted tokens against the target's probabilities from
-    given random numbers (dsa_verify_draft).  Returns (tokens int32 [num_req,
-    max_out], -1 padded; num_out int32 [num_req]; ctx_out = ctx_len + num_out,
-    or None without ctx_len)."""
+    given random numbers (dsa_verify_draft_req).  ``cu_rows`` and ``q_req`` are
+    batch_layout's: a request that it refused gets no tokens (without q_req
+    its rows would be verified like any others).  Returns (tokens int32
+    [num_req, max_out], -1 padded; num_out int32 [num_req]; ctx_out = ctx_len +
+    num_out, or None without ctx_len)."""
     if tokens is None and num_out is None and ctx_out is None and stream is None and _fast is not None:
-        r = _fast.verify_draft(target_probs, draft_tokens, cu_rows, u_accept, u_sample, draft_probs, ctx_len, max_out,
-                               dev_status)
+        r = _fast.verify_draft(target_probs, draft_tokens, cu_rows, u_accept, u_sample, draft_probs, ctx_len, q_req,
+                               max_out, dev_status)
         if r is not None:
-            return _done("dsa_verify_draft", r)
+            return _done("dsa_verify_draft_req", r)
     dev = _device_of(target_probs, "target_probs")
     _need_rows(target_probs, "target_probs", _F32, 2, dev)
     rows, vocab = target_probs.shape
@@ -911,6 +916,10 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
         raise ValueError("inconsistent shapes")
     if max_out < 1:
         raise ValueError("max_out must be positive")
+    if q_req is not None:
+        _need(q_req, "q_req", _I32, 1, dev)
+        if q_req.shape[0] < rows:
+            raise ValueError("q_req must have an entry for every row")
     if tokens is None:
         tokens = _empty((R, max_out), _I32, target_probs, stream)
     else:
@@ -932,7 +941,7 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
         else:
             _need(ctx_out, "ctx_out", _I32, 1, dev)
             _need_shape(ctx_out, "ctx_out", (R,))
-    _run(dev, stream, "dsa_verify_draft", target_probs.data_ptr(), ld, rows, vocab, _ptr(draft_probs), ldd,
-         draft_tokens.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(), cu_rows.data_ptr(), R, max_out,
-         _ptr(ctx_len), tokens.data_ptr(), num_out.data_ptr(), _ptr(ctx_out), _status_ptr(dev_status, dev))
+    _run(dev, stream, "dsa_verify_draft_req", target_probs.data_ptr(), ld, rows, vocab, _ptr(draft_probs), ldd,
+         draft_tokens.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(), cu_rows.data_ptr(), _ptr(q_req), R,
+         max_out, _ptr(ctx_len), tokens.data_ptr(), num_out.data_ptr(), _ptr(ctx_out), _status_ptr(dev_status, dev))
     return tokens, num_out, ctx_out

@@ -500,11 +500,12 @@ dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const float* kv_s
   return from_cuda(dsa::launch_chunk_small(a, q_pos, merge, s));
 }
 
-dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,
-                            const float* draft_probs, int64_t ld_draft, const int32_t* draft_tokens,
-                            const float* u_accept, const float* u_sample, const int32_t* cu_rows, int32_t num_req,
-                            int32_t max_out, const int32_t* ctx_len, int32_t* tokens, int32_t* num_out,
-                            int32_t* ctx_out, int32_t* dev_status, void* stream) {
+dsa_status dsa_verify_draft_req(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,
+                                const float* draft_probs, int64_t ld_draft, const int32_t* draft_tokens,
+                                const float* u_accept, const float* u_sample, const int32_t* cu_rows,
+                                const int32_t* q_req, int32_t num_req, int32_t max_out, const int32_t* ctx_len,
+                                int32_t* tokens, int32_t* num_out, int32_t* ctx_out, int32_t* dev_status,
+                                void* stream) {
   if (num_rows < 0 || vocab <= 0 || num_req < 0 || max_out <= 0 || ld_target < vocab) return DSA_ERR_INVALID_ARG;
   if (draft_probs && ld_draft < vocab) return DSA_ERR_INVALID_ARG;
   if ((ctx_len == nullptr) != (ctx_out == nullptr)) return DSA_ERR_INVALID_ARG;
@@ -517,9 +518,9 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
   // eight CTAs read a request's inputs while one writes its results (only ctx_len is read
   // by the thread that writes ctx_out over it)
   const int64_t nr = 4 * (int64_t)num_req, nd = 4 * (int64_t)num_rows;
-  const Span in[7] = {{target_probs, num_rows > 0 ? 4 * ((num_rows - 1) * ld_target + vocab) : 0},
+  const Span in[8] = {{target_probs, num_rows > 0 ? 4 * ((num_rows - 1) * ld_target + vocab) : 0},
                       {draft_probs, num_rows > 0 ? 4 * ((num_rows - 1) * ld_draft + vocab) : 0},
-                      {draft_tokens, nd}, {u_accept, nd}, {u_sample, nr}, {cu_rows, nr + 4},
+                      {draft_tokens, nd}, {u_accept, nd}, {u_sample, nr}, {cu_rows, nr + 4}, {q_req, nd},
                       {ctx_out == ctx_len ? nullptr : ctx_len, nr}};
   const Span out[3] = {{tokens, nr * max_out}, {num_out, nr}, {ctx_out, nr}};
   if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
@@ -532,6 +533,7 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
   a.ld_draft = ld_draft;
   a.draft_tokens = draft_tokens;
   a.cu_rows = cu_rows;
+  a.q_req = q_req;
   a.u_accept = u_accept;
   a.u_sample = u_sample;
   a.num_req = num_req;
@@ -542,4 +544,14 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
   a.ctx_out = ctx_out;
   a.dev_status = dev_status;
   return from_cuda(dsa::launch_verify_draft(a, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,
+                            const float* draft_probs, int64_t ld_draft, const int32_t* draft_tokens,
+                            const float* u_accept, const float* u_sample, const int32_t* cu_rows, int32_t num_req,
+                            int32_t max_out, const int32_t* ctx_len, int32_t* tokens, int32_t* num_out,
+                            int32_t* ctx_out, int32_t* dev_status, void* stream) {
+  return dsa_verify_draft_req(target_probs, ld_target, num_rows, vocab, draft_probs, ld_draft, draft_tokens, u_accept,
+                              u_sample, cu_rows, nullptr, num_req, max_out, ctx_len, tokens, num_out, ctx_out,
+                              dev_status, stream);
 }

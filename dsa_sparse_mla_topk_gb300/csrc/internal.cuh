@@ -143,6 +143,7 @@ struct VerifyArgs {
   const float* draft;  // [num_rows, ld_draft] or null
   int64_t ld_draft;
   const int32_t *draft_tokens, *cu_rows;
+  const int32_t* q_req;  // [num_rows] whose row it is (a request's first one counts), or null
   const float *u_accept, *u_sample;
   int32_t num_req, max_out;
   const int32_t* ctx_len;

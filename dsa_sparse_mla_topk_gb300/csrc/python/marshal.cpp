@@ -24,7 +24,7 @@ decltype(&dsa_qk_norm_rope) qk_norm_rope_fn = nullptr;
 decltype(&dsa_chunk_mla_fwd) chunk_mla_fn = nullptr;
 decltype(&dsa_combine) combine_fn = nullptr;
 decltype(&dsa_chunk_pick_num_splits) pick_fn = nullptr;
-decltype(&dsa_verify_draft) verify_draft_fn = nullptr;
+decltype(&dsa_verify_draft_req) verify_draft_fn = nullptr;
 
 // Reads a call's arguments; `good` is false once one is not as documented.
 struct Args {
@@ -277,10 +277,10 @@ PyObject* chunk_mla(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   END_HANDLE_TH_ERRORS
 }
 
-// (target_probs, draft_tokens, cu_rows, u_accept, u_sample, draft_probs, ctx_len, max_out, dev_status)
+// (target_probs, draft_tokens, cu_rows, u_accept, u_sample, draft_probs, ctx_len, q_req, max_out, dev_status)
 PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   HANDLE_TH_ERRORS
-  if (argc != 9) Py_RETURN_NONE;
+  if (argc != 10) Py_RETURN_NONE;
   Args a{argv};
   auto probs = [&a]() -> const at::Tensor* {
     const at::Tensor* t = a.any();
@@ -296,12 +296,13 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   const at::Tensor* us = a.tensor(at::kFloat, 1);
   const at::Tensor* q = probs();
   const at::Tensor* ctx = a.tensor(at::kInt, 1, true);
+  const at::Tensor* own = a.tensor(at::kInt, 1, true);
   const int32_t max_out = a.int32();
   int32_t* st = a.status();
   if (!a.good || !p || max_out < 1) Py_RETURN_NONE;
   const int64_t rows = p->size(0), V = p->size(1), R = us->size(0);
   if (cu->size(0) != R + 1 || tok->size(0) != rows || ua->size(0) != rows || (q && q->sizes() != p->sizes()) ||
-      (ctx && ctx->size(0) != R) || !fits32(rows) || !fits32(V) || !fits32(R))
+      (ctx && ctx->size(0) != R) || (own && own->size(0) < rows) || !fits32(rows) || !fits32(V) || !fits32(R))
     Py_RETURN_NONE;
   const at::Tensor buf = at::empty({R * max_out + (ctx ? 2 : 1) * R}, cu->options());
   const at::Tensor tokens = cut(buf, 0, {R, max_out}, at::kInt), num = cut(buf, R * max_out, {R}, at::kInt);
@@ -309,7 +310,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (ctx) co = cut(buf, R * max_out + R, {R}, at::kInt);
   const dsa_status s = call(verify_draft_fn, ptr<float>(p), rows > 1 ? p->stride(0) : V, (int32_t)rows, (int32_t)V,
                                        ptr<float>(q), q && rows > 1 ? q->stride(0) : V, ptr<int32_t>(tok),
-                                       ptr<float>(ua), ptr<float>(us), ptr<int32_t>(cu), (int32_t)R, max_out,
+                                       ptr<float>(ua), ptr<float>(us), ptr<int32_t>(cu), ptr<int32_t>(own), (int32_t)R, max_out,
                                        ptr<int32_t>(ctx), ptr<int32_t>(&tokens), ptr<int32_t>(&num),
                                        ctx ? ptr<int32_t>(&co) : nullptr, st, a.stream());
   if (s != DSA_OK) return PyLong_FromLong(s);
@@ -317,7 +318,7 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(batch_layout, qk_norm_rope, chunk_mla_fwd, combine, chunk_pick_num_splits, verify_draft): the entry points' addresses
+// bind(batch_layout, qk_norm_rope, chunk_mla_fwd, combine, chunk_pick_num_splits, verify_draft_req): the entry points' addresses
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   if (argc != 6) {
     PyErr_SetString(PyExc_TypeError, "bind takes 6 addresses");

@@ -191,8 +191,14 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draft_kernel(const VerifyAr
 
   const int32_t row0 = a.cu_rows[req], row1 = a.cu_rows[req + 1];
   int32_t* out = a.tokens + (int64_t)req * a.max_out;
-  const bool bad = row0 < 0 || row1 < row0 || row1 > a.num_rows;
-  if (bad || row1 == row0) {  // no rows (the same for the whole cluster)
+  bool bad = row0 < 0 || row1 < row0 || row1 > a.num_rows;
+  bool none = bad || row1 == row0;
+  if (a.q_req && !none) {  // a request that the layout refused has rows, but no positions for them
+    const int32_t owner = a.q_req[row0];
+    none = owner != req;
+    bad = none && owner != -1;
+  }
+  if (none) {  // no rows (the same for the whole cluster)
     if (rank == 0) {
       if (tid == 0) {
         if (bad) report(a.dev_status, DSA_DEV_BAD_INDEX);

@@ -342,7 +342,8 @@ DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const
  *                  them earlier calls have taken.
  *   num_req        at most 8,192, capacity at most 2^30 (else UNSUPPORTED_SHAPE).
  * Data errors leave a request as it is (ctx_out = ctx_len, held_out =
- * pages_held, no pages taken, -1 for its tokens): a negative length sets
+ * pages_held, no pages taken, -1 for its tokens, which stay in cu_q: the
+ * attention gives them 0, dsa_verify_draft_req no tokens): a negative length sets
  * DSA_DEV_BAD_QPOS (and the request has no tokens in cu_q); a block table row
  * that is too short, or a free_used outside the list, DSA_DEV_BAD_INDEX; too
  * few free pages DSA_DEV_NO_PAGES (a request's needs count against the
@@ -464,7 +465,8 @@ DSA_API dsa_status dsa_chunk_mla_fwd(const void* q, const uint8_t* kv, const flo
  *   u_accept      fp32 [num_rows], u_sample fp32 [num_req]: uniform in [0, 1).
  *                 The entries of a request's last row in draft_probs,
  *                 draft_tokens and u_accept are not read.
- *   cu_rows       int32 [num_req + 1] (dsa_batch_layout's cu_q).
+ *   cu_rows       int32 [num_req + 1] (dsa_batch_layout's cu_q; after a layout use
+ *                 dsa_verify_draft_req, which knows the requests it refused).
  *   tokens        int32 [num_req, max_out] output: the taken drafts, then the
  *                 drawn token, then -1.  num_out int32 [num_req] = a + 1.
  *   ctx_len, ctx_out  int32 [num_req], or both NULL: ctx_out = ctx_len + num_out,
@@ -481,6 +483,25 @@ DSA_API dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target
                                     const float* u_accept, const float* u_sample, const int32_t* cu_rows,
                                     int32_t num_req, int32_t max_out, const int32_t* ctx_len, int32_t* tokens,
                                     int32_t* num_out, int32_t* ctx_out, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_verify_draft_req -- dsa_verify_draft of a step whose rows dsa_batch_layout
+ * laid out.  A request that the layout refused (no pages, a block table row too
+ * short) keeps its rows in cu_q with q_req = -1: they have no positions, and
+ * nothing was attended to or cached for them.  With q_req such a request ends
+ * like one without rows, num_out = 0, tokens -1, ctx_out = ctx_len, so that its
+ * next step starts from what is cached.
+ *
+ *   q_req   int32 [num_rows] (the layout's, of a capacity of num_rows or more), or
+ *           NULL: dsa_verify_draft.  Only entries cu_rows[r] are read; one that is
+ *           neither r nor -1 sets DSA_DEV_BAD_INDEX and counts as -1.
+ */
+DSA_API dsa_status dsa_verify_draft_req(const float* target_probs, int64_t ld_target, int32_t num_rows, int32_t vocab,
+                                        const float* draft_probs, int64_t ld_draft, const int32_t* draft_tokens,
+                                        const float* u_accept, const float* u_sample, const int32_t* cu_rows,
+                                        const int32_t* q_req, int32_t num_req, int32_t max_out,
+                                        const int32_t* ctx_len, int32_t* tokens, int32_t* num_out, int32_t* ctx_out,
+                                        int32_t* dev_status, void* stream);
 
 /*
  * KV-only prefix-sharing page allocator (host side, no GPU involved).

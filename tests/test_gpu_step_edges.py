@@ -91,6 +91,87 @@ def test_chunk_any_page_id_out_of_range_is_told(shape, bad):
         ops._check_chunk(out, lse, want)
 
 
+# ---- verify_draft and whole steps ----------------------------------------------------
+
+
+@pytest.mark.parametrize("probs", [True, False])
+def test_verify_requests_that_the_layout_refused(probs):
+    p, q, tok, cu, ua, us = ops._verify_case(20, 5, 1003, probs, seed=3)
+    rows, ctx = p.shape[0], torch.arange(20, dtype=I32, device="cuda") + 7
+    cuh = ops.host(cu)
+    own = np.repeat(np.arange(20), np.diff(cuh)).astype(np.int32)
+    refused = {2, 3, 11, 19}
+    for r in refused:
+        own[cuh[r]:cuh[r + 1]] = -1
+    own[cuh[6]] = 5       # another request's: told
+    own[cuh[8] + 1:cuh[9]] = -9  # not a first row: not looked at
+    own = np.concatenate([own, [-1, -1]]).astype(np.int32)  # a longer capacity
+    want, wnum, _ = ref.verify_draft(ops.host(p), None if q is None else ops.host(q), ops.host(tok), cuh, ops.host(ua),
+                                     ops.host(us), 6)
+    gone = sorted(refused | {6})
+    want[gone], wnum[gone] = -1, 0
+    for run in (lambda f: f(), ops._without_cpp):
+        st = torch.zeros(1, dtype=I32, device="cuda")
+        t, n, c = run(lambda: dsa.verify_draft(p, tok, cu, ua, us, draft_probs=q, ctx_len=ctx, q_req=ops.i32(own), max_out=6,
+                                               dev_status=st))
+        assert np.array_equal(ops.host(t), want) and np.array_equal(ops.host(n), wnum)
+        assert np.array_equal(ops.host(c), ops.host(ctx) + wnum) and int(st) == dsa.DEV_BAD_INDEX
+        with pytest.raises(ValueError):
+            run(lambda: dsa.verify_draft(p, tok, cu, ua, us, q_req=ops.i32(own[:rows - 1]), max_out=6))
+
+
+@pytest.mark.parametrize("why", ["pages", "table"])
+def test_a_refused_request_waits_through_the_whole_step(why):
+    """Two requests of 16 positions with 3 new tokens each, and a page (or a block table
+    row) for the first alone: the second one's length stays 16, it gets no tokens, and
+    once there is room its next step attends to rows that were written."""
+    H, dl, dr, page, V = 64, 512, 64, 16, 50
+    d = dl + dr
+    g = torch.Generator().manual_seed(17)
+    kv = torch.full((6 * page, d), 0x7F, dtype=torch.uint8, device="cuda")  # NaN until written
+    sc = torch.full((6 * page,), float("nan"), device="cuda")
+    rows = torch.randn((32, 1, d), generator=g).to(torch.bfloat16).cuda()
+    dsa.qk_norm_rope(None, rows, None, None, d_rope=0, slot=torch.arange(32, dtype=I32, device="cuda"), kv=kv, kv_scale=sc)
+    cs = torch.from_numpy(ops._tables(64, dr)).cuda()
+    wide = 3 if why == "pages" else 1
+    tables = [torch.full((2, w), -1, dtype=I32, device="cuda") for w in (wide, 3)]
+    for t in tables:
+        t[:, 0] = ops.i32([0, 1])
+    ctx, held, used = ops.i32([16, 16]), ops.i32([1, 1]), ops.i32([0])
+    new = [3, 3] if why == "pages" else [0, 3]
+    for step, (table, free) in enumerate(((tables[0], [2] if why == "pages" else [2, 3, 4]), (tables[1], [2, 3, 4]))):
+        if step and why == "pages":
+            table = tables[0]
+        st = torch.zeros(1, dtype=I32, device="cuda")
+        lay = dsa.batch_layout(ctx, ops.i32(new), held, table, ops.i32(free), used, page_size=page, num_pages=6,
+                               capacity=7, dev_status=st)
+        q = torch.randn((7, H, d), generator=g).to(torch.bfloat16).cuda()
+        k = torch.randn((7, 1, d), generator=g).to(torch.bfloat16).cuda()
+        qo, _ = dsa.qk_norm_rope(q, k, lay.q_pos, cs, d_rope=dr, slot=lay.slot, kv=kv, kv_scale=sc)
+        out, lse = dsa.chunk_mla(qo, kv, sc, table, lay.q_req, lay.q_pos, d_latent=dl, d_rope=dr, page_size=page,
+                                 softmax_scale=d**-0.5)
+        p = torch.softmax(torch.randn((7, V), generator=g), 1).cuda()
+        tok = torch.zeros(7, dtype=I32, device="cuda")
+        before = ctx
+        tokens, num, ctx = dsa.verify_draft(p, tok, lay.cu_q, torch.zeros(7, device="cuda"),
+                                            torch.rand(2, generator=g).cuda(), q_req=lay.q_req, ctx_len=before, max_out=3)
+        live = ops.host(lay.q_req) >= 0
+        assert torch.isfinite(out).all() and np.isfinite(ops.host(lse)[live]).all()
+        ran = [new[0] > 0, step == 1]
+        assert int(st) == (0 if step else dsa.DEV_NO_PAGES if why == "pages" else dsa.DEV_BAD_INDEX)
+        for r in range(2):
+            # (u = 0 takes every draft: a token out for each one in)
+            assert int(num[r]) == (new[r] if ran[r] else 0) and (not ran[r]) == bool((tokens[r] == -1).all())
+            assert int(ctx[r]) == int(before[r]) + int(num[r])
+            assert int(lay.ctx_len[r]) == int(before[r]) + (new[r] if ran[r] else 0)
+        # every position that attention may read from now on lies on a page the request holds
+        assert (ops.host(lay.pages_held) * page >= ops.host(ctx)).all()
+        held, used = lay.pages_held, lay.free_used
+        new = [1, 3]
+        if step == 0:
+            assert int(ctx[1]) == 16
+
+
 # ---- errors ------------------------------------------------------------------------
 
 
