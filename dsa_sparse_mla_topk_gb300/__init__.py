@@ -11,7 +11,9 @@ from __future__ import annotations
 
 import ctypes
 import os
+import sysconfig
 import threading
+import warnings
 from typing import NamedTuple
 
 import torch
@@ -128,21 +130,28 @@ def load_library(path: str | None = None):
         return lib
 
 
-# csrc/python/marshal.cpp as built for this PyTorch
-MARSHAL_PATH = os.path.join(_PKG, f"_marshal.{torch.__version__}.so")
+# csrc/python/marshal.cpp as built for this PyTorch and this Python
+MARSHAL_PATH = os.path.join(_PKG, f"_marshal.{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _load_marshal(lib):
-    """The C++ marshalling bound to ``lib``'s entry points; None where it was not
-    built for this PyTorch, and Python marshals."""
+    """The C++ marshalling bound to ``lib``'s entry points; None where there is none
+    for this PyTorch, this Python and this library, and Python marshals."""
     if not os.path.exists(MARSHAL_PATH):
         return None
     from importlib.machinery import ExtensionFileLoader
     from importlib.util import module_from_spec, spec_from_loader
 
     loader = ExtensionFileLoader("_marshal", MARSHAL_PATH)
-    m = module_from_spec(spec_from_loader("_marshal", loader))
-    loader.exec_module(m)
+    try:
+        m = module_from_spec(spec_from_loader("_marshal", loader))
+        loader.exec_module(m)
+    except (ImportError, OSError) as e:
+        warnings.warn(f"{MARSHAL_PATH} cannot be loaded ({e}): calls are marshalled in Python")
+        return None
+    if getattr(m, "header_version", 0) != lib.dsa_version():
+        warnings.warn(f"{MARSHAL_PATH} was built for another version of the library: calls are marshalled in Python")
+        return None
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
              for f in (lib.dsa_batch_layout, lib.dsa_qk_norm_rope, lib.dsa_chunk_mla_fwd, lib.dsa_combine,
                        lib.dsa_chunk_pick_num_splits, lib.dsa_verify_draft_req)))

@@ -5,8 +5,9 @@ shared library with a plain C ABI (include/dsa.h).  The library links the
 shared CUDA runtime so that it shares the process's runtime with PyTorch.
 
 csrc/python/marshal.cpp, the Python binding's argument marshalling, is compiled
-beside it with g++ against the installed PyTorch -> _marshal.<its version>.so.  It holds no
-kernels; without it (no Python or PyTorch headers) the binding marshals in Python.
+beside it with g++ against the installed PyTorch -> _marshal.<its version>.<Python's ABI>.so.  It
+holds no kernels; without it (no Python or PyTorch headers, or they do not compile) the binding
+marshals in Python.
 """
 from __future__ import annotations
 
@@ -16,6 +17,7 @@ import os
 import shutil
 import subprocess
 import sys
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -55,13 +57,16 @@ def up_to_date() -> bool:
 
 
 def marshal_path() -> str:
+    import sysconfig
+
     import torch
 
-    return os.path.join(PKG, f"_marshal.{torch.__version__}.so")
+    return os.path.join(PKG, f"_marshal.{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def build_marshal(force: bool = False) -> str | None:
-    """The marshalling module for the PyTorch in use; None where its headers are missing."""
+    """The marshalling module for the PyTorch and the Python in use; None where it cannot be
+    built (headers missing, a compiler error, which is warned of), and no older one stays."""
     import sysconfig
 
     import torch
@@ -76,6 +81,7 @@ def build_marshal(force: bool = False) -> str | None:
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     if not cxx or not all(os.path.exists(p) for p in (os.path.join(inc, "Python.h"), os.path.join(tinc, "ATen"),
                                                       os.path.join(cuda, "cuda_runtime_api.h"))):
+        _remove(lib)
         return None
     tmp = lib + f".{os.getpid()}.tmp"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-w",
@@ -85,9 +91,17 @@ def build_marshal(force: bool = False) -> str | None:
            "-L", tlib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        raise RuntimeError(f"g++ failed for {MARSHAL_SRC}:\n{r.stderr}")
+        _remove(tmp)
+        _remove(lib)
+        warnings.warn(f"g++ failed for {MARSHAL_SRC}, calls are marshalled in Python:\n{r.stderr}")
+        return None
     os.replace(tmp, lib)
     return lib
+
+
+def _remove(path: str) -> None:
+    if os.path.exists(path):
+        os.remove(path)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

@@ -54,7 +54,7 @@ const char* dsa_status_string(int32_t status) {
   }
 }
 
-int32_t dsa_version(void) { return 200; }
+int32_t dsa_version(void) { return DSA_VERSION; }
 
 int32_t dsa_kv_tile_count(int32_t width, int32_t tile) {
   if (width < 0 || tile <= 0) return -1;

@@ -350,5 +350,8 @@ PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, method
 }  // namespace
 
 PyMODINIT_FUNC PyInit__marshal() {
-  return PyModule_Create(&module_def);
+  PyObject* m = PyModule_Create(&module_def);
+  // the signatures that the addresses given to bind() are called with
+  if (m && PyModule_AddIntConstant(m, "header_version", DSA_VERSION) != 0) Py_CLEAR(m);
+  return m;
 }

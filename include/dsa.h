@@ -86,7 +86,9 @@ typedef enum {
 /* Static description of a status code (never NULL). */
 DSA_API const char* dsa_status_string(int32_t status);
 
-/* Library ABI version: major * 10000 + minor * 100 + patch. */
+/* Library ABI version: major * 10000 + minor * 100 + patch (DSA_VERSION of the header
+ * that the library was built with). */
+#define DSA_VERSION 201
 DSA_API int32_t dsa_version(void);
 
 /*

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import dsa_sparse_mla_topk_gb300 as dsa
+from dsa_sparse_mla_topk_gb300 import build as dsa_build
 from test_step_args import A, _chunk, _layout, _norm, _verify, lib, no_device_only  # noqa: F401
 
 
@@ -73,3 +74,45 @@ def test_outputs_over_any_input_or_each_other(lib):  # noqa: F811
             assert _verify(lib, **{k: at(A(x), 4 * (7 * 100 + 100))}) == 4, (k, x)
     assert _verify(lib, out=A(20), num=at(A(20), 28)) == 1 and _verify(lib, num=A(20), co=A(20)) == 1
     assert _verify(lib, co=A(6)) == 4  # the lengths in place
+
+
+# ---- the binding's C++ marshalling ---------------------------------------------------
+
+
+def test_a_marshalling_module_that_cannot_be_loaded_is_left_alone(lib, tmp_path, monkeypatch):  # noqa: F811
+    """Another Python's module, or a broken file, is no reason for every call to raise."""
+    bad = tmp_path / "_marshal.so"
+    bad.write_bytes(b"not a library")
+    monkeypatch.setattr(dsa, "MARSHAL_PATH", str(bad))
+    with pytest.warns(UserWarning, match="marshalled in Python"):
+        assert dsa._load_marshal(lib) is None
+    monkeypatch.setattr(dsa, "MARSHAL_PATH", str(tmp_path / "none.so"))
+    assert dsa._load_marshal(lib) is None
+
+
+def test_a_marshalling_module_of_another_library_version_is_left_alone(lib):  # noqa: F811
+    class Other:
+        def __getattr__(self, name):
+            return (lambda: 1) if name == "dsa_version" else getattr(lib, name)
+    if dsa._load_marshal(lib) is None:
+        pytest.skip("not built here")
+    with pytest.warns(UserWarning, match="another version"):
+        assert dsa._load_marshal(Other()) is None
+
+
+def test_a_marshalling_source_that_does_not_compile_stops_no_build(tmp_path, monkeypatch):
+    """The build goes on without the module, and a module of other sources does not stay behind."""
+    src, out = tmp_path / "marshal.cpp", tmp_path / "_marshal.so"
+    src.write_text("this is not C++\n")
+    out.write_bytes(b"older")
+    monkeypatch.setattr(dsa_build, "MARSHAL_SRC", str(src))
+    monkeypatch.setattr(dsa_build, "marshal_path", lambda: str(out))
+    with pytest.warns(UserWarning, match="g\\+\\+ failed"):
+        assert dsa_build.build_marshal(force=True) is None
+    assert not list(tmp_path.glob("*.so*"))
+
+
+def test_the_modules_name_holds_both_versions():
+    import sysconfig
+    assert dsa.MARSHAL_PATH == dsa_build.marshal_path()
+    assert torch.__version__ in dsa.MARSHAL_PATH and sysconfig.get_config_var("SOABI") in dsa.MARSHAL_PATH
