@@ -651,7 +651,9 @@ def batch_layout(ctx_len: torch.Tensor, new_len: torch.Tensor, pages_held: torch
     """A step's token ranges, slot map and grown block tables from the
     requests' lengths (dsa_batch_layout): ``block_table`` gets the new pages in
     place, everything else is returned.  ``out`` (a BatchLayout of
-    preallocated tensors, not the inputs) is written when given."""
+    preallocated tensors, not the inputs) is written when given; else the
+    outputs share one allocation, but what the next step keeps (cu_q, lengths,
+    pages, free_used) has another one where the token arrays are over 64 KB."""
     if out is None and stream is None and _fast is not None:
         r = _fast.batch_layout(ctx_len, new_len, pages_held, block_table, free_pages, free_used, page_size, num_pages,
                                capacity, dev_status)
@@ -670,15 +672,20 @@ def batch_layout(ctx_len: torch.Tensor, new_len: torch.Tensor, pages_held: torch
     if capacity < 0:
         raise ValueError("capacity must not be negative")
     if out is None:
-        # the token arrays first, a multiple of 16 bytes apart
-        cap = (capacity + 3) & -4
-        buf = _empty(3 * cap + 3 * R + 2, _I32, ctx_len, stream)
-        q_req, q_pos, slot, cu, ctx, held, used = buf.split_with_sizes((cap, cap, cap, R + 1, R, R, 1))
+        # the token arrays first, a multiple of 16 bytes apart; the requests' state, which the
+        # next step keeps, apart from token arrays of more than 64 KB
+        cap, words = (capacity + 3) & -4, 3 * R + 2
+        if 12 * cap > 64 * 1024:
+            buf, state = _empty(3 * cap, _I32, ctx_len, stream), _empty(words, _I32, ctx_len, stream)
+        else:
+            buf = _empty(3 * cap + words, _I32, ctx_len, stream)
+            state = buf[3 * cap:]
+        q_req, q_pos, slot = buf[:cap], buf[cap:2 * cap], buf[2 * cap:3 * cap]
         if cap != capacity:
             q_req, q_pos, slot = q_req[:capacity], q_pos[:capacity], slot[:capacity]
-        out = BatchLayout(cu, q_req, q_pos, slot, ctx, held, used)
-        p = buf.data_ptr()
-        c = p + 12 * cap
+        out = BatchLayout(cu_q=state[:R + 1], q_req=q_req, q_pos=q_pos, slot=slot, ctx_len=state[R + 1:2 * R + 1],
+                          pages_held=state[2 * R + 1:3 * R + 1], free_used=state[3 * R + 1:])
+        p, c = buf.data_ptr(), state.data_ptr()
         ptrs = (c, p, p + 4 * cap, p + 8 * cap, c + 4 * R + 4, c + 8 * R + 4, c + 12 * R + 4)
     else:
         for x, name, n in zip(out, BatchLayout._fields, (R + 1, capacity, capacity, capacity, R, R, 1)):
@@ -851,7 +858,8 @@ def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_ro
     longest context, from which the number of KV splits is picked when
     ``num_splits`` is None; the result is right for any value.  ``buffers``
     (optional) holds preallocated out / lse / o_part / lse_part tensors.
-    Returns (out, lse)."""
+    Returns (out, lse), which share one allocation unless given (clone lse to
+    keep it alone)."""
     b = buffers or {}
     if num_splits is None and max_ctx is None:
         max_ctx = block_table.shape[1] * page_size
@@ -897,7 +905,8 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
     batch_layout's: a request that it refused gets no tokens (without q_req
     its rows would be verified like any others).  Returns (tokens int32
     [num_req, max_out], -1 padded; num_out int32 [num_req]; ctx_out = ctx_len +
-    num_out, or None without ctx_len)."""
+    num_out, or None without ctx_len); they share one allocation of max_out + 2
+    words a request unless given."""
     if tokens is None and num_out is None and ctx_out is None and stream is None and _fast is not None:
         r = _fast.verify_draft(target_probs, draft_tokens, cu_rows, u_accept, u_sample, draft_probs, ctx_len, q_req,
                                max_out, dev_status)

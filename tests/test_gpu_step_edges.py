@@ -58,6 +58,21 @@ def test_layout_large_batches_from_several_threads():
     assert not errors, errors
 
 
+def test_layout_state_does_not_keep_the_token_arrays():
+    """A loop keeps the lengths, pages and counts: a few words a request, and no more than 64 KB
+    of the step's tokens."""
+    c, n, held, table, free, pages = ops._layout_case(50, 60, 100, 16, seed=8)
+    a = (ops.i32(c), ops.i32(n), ops.i32(held), torch.from_numpy(table).cuda(), ops.i32(free), ops.i32([0]))
+    for run in (lambda f: f(), ops._without_cpp):
+        for cap in (3001, 5460, 5461, 100_001):  # 64 KB of token arrays: 5,461 tokens
+            lay = run(lambda: dsa.batch_layout(*a, page_size=16, num_pages=pages, capacity=cap))
+            for name in ("cu_q", "ctx_len", "pages_held", "free_used"):
+                assert getattr(lay, name).untyped_storage().nbytes() <= 64 * 1024 + 4 * (3 * 50 + 2), name
+            want, _ = ref.batch_layout(c, n, held, table, free, 0, page_size=16, num_pages=pages, capacity=cap)
+            for k, v in lay._asdict().items():
+                assert v.is_contiguous() and np.array_equal(ops.host(v), want[k]), k
+
+
 # ---- qk_norm_rope ------------------------------------------------------------------
 
 
