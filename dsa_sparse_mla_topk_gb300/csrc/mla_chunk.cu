@@ -437,9 +437,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         float m = red_s[0];
         for (int w = 1; w < SM_WARPS; ++w) m = fmaxf(m, red_s[w]);
         int e = 0;
-        const bool fin = m > 0.f && m <= 3.0e38f;
+        const bool fin = m > 0.f && m < INFINITY;
         if (fin) frexpf(m, &e);  // m < 2^e
-        *qexp_s = fin ? 8 - e : 0;
+        // (2^qexp stays finite: a query below 2^-120 is as good as zero)
+        *qexp_s = fin ? min(8 - e, 100) : 0;
       }
       group_sync();
       // (a negative softmax scale is Q's sign)

@@ -106,6 +106,26 @@ def test_chunk_any_page_id_out_of_range_is_told(shape, bad):
         ops._check_chunk(out, lse, want)
 
 
+@both_shapes
+@pytest.mark.parametrize("size", [2.0**-133, 2.0**-125, 2.0**-121, 2.0**-110])
+def test_chunk_smallest_and_largest_queries(shape, size):
+    """One element of a head's query is not zero: next to the type's smallest value the
+    result is the mean of the visible rows; next to the largest, the one row that it picks."""
+    c = ops._chunk_case(*shape, [300, 130], [2, 1], 64, seed=3)
+    c["q"][0] = 0
+    c["q"][0, :, 0] = size
+    assert float(c["q"][0, 0, 0]) != 0 and np.isfinite(float(c["q"][0, 0, 0]))
+    want = ops._chunk_ref(c)
+    for splits in (1, 3, 12):
+        out, lse, st = ops._run_chunk(c, splits)
+        assert st == 0
+        if size < 1:
+            ops._check_chunk(out, lse, want)
+        else:  # (an lse of 1e37 has no absolute bound: its own rounding and two products')
+            ops._check_chunk(out, torch.zeros_like(lse), (want[0], np.zeros_like(want[1]), *want[2:]))
+            assert (np.abs(ops.host(lse) - want[1]) <= 2.0**-20 * np.abs(want[1]) + 1e-3).all()
+
+
 # ---- verify_draft and whole steps ----------------------------------------------------
 
 
