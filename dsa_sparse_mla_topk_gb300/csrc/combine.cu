@@ -43,7 +43,9 @@ __global__ void __launch_bounds__(kCombineThreads)
     float m = -INFINITY;
     for (int s = 0; s < S; ++s) m = fmaxf(m, lse_part[((int64_t)s * num_q + i) * H + h]);
     float l = -INFINITY;
-    if (m != -INFINITY) {
+    if (m == -INFINITY) {  // every split is empty, or NaN (which loses to a number in m)
+      for (int s = 0; s < S; ++s) l += lse_part[((int64_t)s * num_q + i) * H + h];
+    } else {
       float sum = 0.f;
       for (int s = 0; s < S; ++s) sum += expf(lse_part[((int64_t)s * num_q + i) * H + h] - m);
       l = m + logf(sum);

@@ -417,11 +417,11 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     // ---- Q: bf16 -> x 2^qexp -> E4M3 hi and lo, latent part to TMEM, rope part to shared memory ----
     {
       constexpr int CH = DQK / 8;  // 16-byte chunks (8 bf16) per head
-      const uint4* qraw = reinterpret_cast<const uint4*>(smem + OFF_KV + QSTAGE * STAGE_BYTES);
+      uint4* qraw = reinterpret_cast<uint4*>(smem + OFF_KV + QSTAGE * STAGE_BYTES);
       auto bf_lo = [](uint32_t w) { return __uint_as_float(w << 16); };
       auto bf_hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
       if (!wait_warp(B_QLOAD, 0)) ok = false;
-      float mx = 0.f;
+      float mx = 0.f;  // (a NaN loses to a number)
 #pragma unroll 3
       for (int e = st; e < H * CH; e += SM_THREADS) {
         const uint4 v = qraw[e];
@@ -429,20 +429,36 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
 #pragma unroll
         for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[t])), fabsf(bf_hi(w[t]))));
       }
+      constexpr int HAS_INF = INT32_MAX;
+      auto set_exponent = [&] {
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) red_s[sw] = mx;
-      group_sync();
-      if (st == 0) {
-        float m = red_s[0];
-        for (int w = 1; w < SM_WARPS; ++w) m = fmaxf(m, red_s[w]);
-        int e = 0;
-        const bool fin = m > 0.f && m < INFINITY;
-        if (fin) frexpf(m, &e);  // m < 2^e
-        // (2^qexp stays finite: a query below 2^-120 is as good as zero)
-        *qexp_s = fin ? min(8 - e, 100) : 0;
+        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if (lane == 0) red_s[sw] = mx;
+        group_sync();
+        if (st == 0) {
+          float m = red_s[0];
+          for (int w = 1; w < SM_WARPS; ++w) m = fmaxf(m, red_s[w]);
+          int e = 0;
+          frexpf(m, &e);  // m < 2^e
+          // (2^qexp stays finite: a query below 2^-120 is as good as zero)
+          *qexp_s = m == INFINITY ? HAS_INF : m > 0.f ? min(8 - e, 100) : 0;
+        }
+        group_sync();
+      };
+      set_exponent();
+      if (*qexp_s == HAS_INF) {  // infinities become NaN (E4M3 has none), the largest finite value counts
+        mx = 0.f;
+        for (int e = st; e < H * CH * 4; e += SM_THREADS) {
+          uint32_t* q2 = reinterpret_cast<uint32_t*>(qraw) + e;
+          uint32_t w = *q2;
+          if ((w & 0x7fffu) == 0x7f80u) w |= 0x7fffu;
+          if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x7fff0000u;
+          mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w)), fabsf(bf_hi(w))));
+          *q2 = w;
+        }
+        group_sync();  // (every thread has read the mark)
+        set_exponent();
       }
-      group_sync();
       // (a negative softmax scale is Q's sign)
       const float qs = copysignf(ldexpf(1.f, *qexp_s), a.softmax_scale);
       auto split8 = [&](const uint4 v, uint2& hv, uint2& lv) {  // 8 elements as byte quadruples
@@ -629,10 +645,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     group_sync();
     if (part == 0 && up == 0) {
       const float l = (red_s[hh] + red_s[H + hh]) + (red_s[2 * H + hh] + red_s[3 * H + hh]);
-      // (O and l both carry F)
-      alpha_s[hh] = l > 0.f ? (MERGE ? 1.f : 1.f / l) : 0.f;
-      const float lse = l > 0.f ? (m_ref + log2f(l * ex2(-p_log))) * LN2 : -INFINITY;
-      if (MERGE) ml_s[hh] = ok && l > 0.f ? m_ref - p_log : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
+      // (O and l both carry F; a NaN is not an empty row)
+      alpha_s[hh] = l != 0.f ? (MERGE ? 1.f : 1.f / l) : 0.f;
+      const float lse = l != 0.f ? (m_ref + log2f(l * ex2(-p_log))) * LN2 : -INFINITY;
+      if (MERGE) ml_s[hh] = ok && l != 0.f ? m_ref - p_log : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
       else if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
       else if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
     }
@@ -697,11 +713,11 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         ms[s] = ms[s] == -INFINITY ? 0.f : ex2(ms[s] - m);
         l = fmaf(ms[s], ls[s], l);
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
       for (int s = 0; s < MAX_MERGED; ++s)
         if (s < S) fac[s * H + tid] = ms[s] * inv;
-      if (split == 0 && a.lse) a.lse[(int64_t)i * H + tid] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+      if (split == 0 && a.lse) a.lse[(int64_t)i * H + tid] = l != 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     }
     __syncthreads();
     // each CTA a share of the token's values, four at a time

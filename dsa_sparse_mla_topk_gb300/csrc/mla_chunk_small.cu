@@ -148,11 +148,24 @@ __global__ void __launch_bounds__(NTHREADS, PER_SM)
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int c = 0; c < 2 * KS; ++c) mx = max(mx, max((w[h][c] << 16) & 0x7fffffffu, w[h][c] & 0x7fff0000u));
-    const float m = __uint_as_float(__reduce_max_sync(0xffffffffu, mx));
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    if (mx >= 0x7f800000u) {  // infinities become NaN, the largest finite value counts
+      mx = 0;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int c = 0; c < 2 * KS; ++c) {
+          uint32_t& v = w[h][c];
+          if ((v & 0x7fffu) >= 0x7f80u) v |= 0x7fffu;
+          else mx = max(mx, (v << 16) & 0x7fffffffu);
+          if ((v & 0x7fff0000u) >= 0x7f800000u) v |= 0x7fff0000u;
+          else mx = max(mx, v & 0x7fff0000u);
+        }
+      mx = __reduce_max_sync(0xffffffffu, mx);
+    }
     int e = 0;
-    const bool fin = m > 0.f && m <= 3.4e38f;
-    if (fin) frexpf(m, &e);  // m < 2^e
-    const int qexp = fin ? min(14 - e, 100) : 0;
+    if (mx != 0) frexpf(__uint_as_float(mx), &e);  // the largest |q| < 2^e
+    const int qexp = mx != 0 ? min(14 - e, 100) : 0;
     const float qs = ldexpf(1.f, qexp);
 #pragma unroll
     for (int c = 0; c < KS; ++c)
@@ -317,16 +330,16 @@ __global__ void __launch_bounds__(NTHREADS, PER_SM)
         l = fmaf(w, lk[k], l);
         s.x = fmaf(w, v.x, s.x), s.y = fmaf(w, v.y, s.y), s.z = fmaf(w, v.z, s.z), s.w = fmaf(w, v.w, s.w);
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
       __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + ((int64_t)i * H + h) * DL + c);
       ob[0] = __floats2bfloat162_rn(s.x * inv, s.y * inv);
       ob[1] = __floats2bfloat162_rn(s.z * inv, s.w * inv);
-      if (a.lse && c == 0) a.lse[(int64_t)i * H + h] = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+      if (a.lse && c == 0) a.lse[(int64_t)i * H + h] = l != 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     }
     cluster.sync();  // no CTA leaves while another reads its shared memory
   } else {
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const float lse = l > 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const float lse = l != 0.f ? (m + log2f(l)) * LN2 : -INFINITY;
     if (S == 1) {
       __nv_bfloat162* ob = reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(a.out) + ((int64_t)i * H + hh) * DL + d);
       ob[0] = __floats2bfloat162_rn(s.x * inv, s.y * inv);

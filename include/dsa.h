@@ -430,6 +430,10 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t
  * an input or each other (INVALID_ARG).  A token with q_req = -1
  * (padding) or q_pos = -1 sees nothing: out = 0 and lse = -inf.  Tokens of one
  * request next to each other share its rows in L2; any order is correct.
+ * A head whose query holds a NaN or an infinity, and every head of a token that
+ * sees a NaN code or a NaN scale, has out = lse = NaN, for any number of splits;
+ * other heads and tokens are as without it.  (A visible row with an infinite
+ * scale gives NaN in out, and an unspecified lse.)
  * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
  * and the token sees nothing; q_req outside [-1, num_req) or a page id out of
  * range sets DSA_DEV_BAD_PAGE; such rows are skipped.

@@ -126,6 +126,65 @@ def test_chunk_smallest_and_largest_queries(shape, size):
             assert (np.abs(ops.host(lse) - want[1]) <= 2.0**-20 * np.abs(want[1]) + 1e-3).all()
 
 
+@both_shapes
+def test_chunk_nan_and_infinite_queries(shape):
+    """Their heads are NaN, out and lse, for every number of splits; the others exact."""
+    c = ops._chunk_case(*shape, [300, 130], [2, 2], 64, seed=3, pad=1)
+    want = ops._chunk_ref(c)
+    clean = {S: ops._run_chunk(c, S) for S in (1, 3, 8, 12)}
+    heads = {0: (3, float("nan")), 1: (2, float("inf")), 2: (0, float("-inf"))}
+    for t, (h, v) in heads.items():
+        c["q"][t, h, 5] = v
+    c["q"][1, 4, shape[1] + 1] = float("nan")  # in the rope part, beside an infinity in the token
+    bad = np.zeros(c["q"].shape[:2], dtype=bool)
+    for t, (h, _) in heads.items():
+        bad[t, h] = True
+    bad[1, 4] = True
+    for splits in clean:
+        out, lse, st = ops._run_chunk(c, splits)
+        o, n = ops.host(out.float()), ops.host(lse)
+        assert st == 0 and np.isnan(o[bad]).all() and np.isnan(n[bad]).all()
+        assert not np.isnan(o[~bad]).any() and not np.isnan(n[~bad]).any()
+        keep = ~bad
+        fixed = torch.where(torch.from_numpy(bad).cuda()[..., None], clean[splits][0], out)
+        ops._check_chunk(fixed, torch.where(torch.from_numpy(bad).cuda(), clean[splits][1], lse), want)
+        assert keep[-1].all() and (o[-1] == 0).all() and np.isneginf(n[-1]).all()
+
+
+@both_shapes
+@pytest.mark.parametrize("what", ["scale", "code"])
+@pytest.mark.parametrize("where", [0, 77, 299])
+def test_chunk_nan_in_a_visible_row(shape, what, where):
+    """Every token that sees it is NaN, out and lse, for every number of splits."""
+    c = ops._chunk_case(*shape, [300, 130], [3, 2], 64, seed=3)
+    want = ops._chunk_ref(c)
+    slot = int(c["table"][0, where // 64]) * 64 + where % 64
+    if what == "scale":
+        c["sc"][slot] = float("nan")
+    else:
+        c["kv"][slot, :] = 0x7F
+    hit = (c["req"] == 0).numpy() & (c["pos"].numpy() >= where)
+    assert hit.any() and not hit.all()
+    for splits in (1, 2, 3, 8, 12):
+        out, lse, st = ops._run_chunk(c, splits)
+        assert st == 0 and torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+        ops._check_chunk(out[~hit], lse[~hit], [x[~hit] for x in want])
+
+
+def test_combine_splits_of_nan():
+    """A head whose splits are all NaN is NaN, not empty; one NaN split is enough."""
+    o, n = torch.zeros((3, 2, 4, 8), device="cuda"), torch.zeros((3, 2, 4), device="cuda")
+    n[:, 0, 1] = float("nan")
+    n[1, 0, 2] = float("nan")
+    n[:, 1, 3] = float("-inf")
+    n[0, 1, 0], n[1:, 1, 0] = float("nan"), float("-inf")
+    out, lse = dsa.combine(o, n)
+    bad = torch.zeros((2, 4), dtype=torch.bool, device="cuda")
+    bad[0, 1] = bad[0, 2] = bad[1, 0] = True
+    assert torch.equal(torch.isnan(lse), bad) and torch.isneginf(lse[1, 3])
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(out).any(-1), bad)
+
+
 # ---- verify_draft and whole steps ----------------------------------------------------
 
 
