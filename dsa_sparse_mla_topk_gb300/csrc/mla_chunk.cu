@@ -33,8 +33,9 @@
 //    Q_hi rows in lanes 0-15 and Q_lo rows in lanes 16-31.  A thread owns one
 //    head and 8 rows of the tile; two 16-lane loads, whose half-warps take
 //    different columns, bring it both halves of its logits.
-// Q = Q_hi + Q_lo is exact for bf16 (two E4M3 numbers of a token scaled by a
-// power of two).  A weight P' = p s_j F is E4M3 + E5M2.  F puts the reference weight
+// Q = Q_hi + Q_lo: two E4M3 numbers of a head scaled by a power of two, exact for bf16
+// values down to 2^-9 of the head's largest, below that to 2^-17 of it (E4M3's
+// steps end: 0.4% of a Gaussian head).  A weight P' = p s_j F is E4M3 + E5M2.  F puts the reference weight
 // (p = 1) of the row with the largest scale at 16, an exact value (a head that looks at
 // one row gives that row), or more where scales grow, so that weights down to
 // 2^-10 of it have a relative error of at most 2^-8 (0.12% root mean square,
@@ -98,7 +99,8 @@ constexpr int OFF_ALPHA = OFF_RED + 4 * H * 4;        // per-head factor of O, t
 constexpr int OFF_SROW = OFF_ALPHA + H * 4;           // [NST][64] the tiles' row scales
 constexpr int OFF_INFO = OFF_SROW + NST * T * 4;      // [NST][2] valid rows (bits) and largest scale of each 32 rows
 constexpr int OFF_ML = OFF_INFO + NST * 2 * 8;         // [2][64] for the cluster's merge
-constexpr int OFF_FLAG = OFF_ML + 2 * H * 4;      // O flags [4], Q exponent
+constexpr int OFF_QS = OFF_ML + 2 * H * 4;             // [64] the heads' 2^e of Q, and logits' factor
+constexpr int OFF_FLAG = OFF_QS + H * 8;               // O flags [4]
 constexpr int OFF_BAR = OFF_FLAG + 128;
 constexpr int B_KVF = 0;               // [NST] the tile in stage s has landed
 constexpr int B_KVE = B_KVF + NST;     // [NST] stage s is free
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
   float* red_s = reinterpret_cast<float*>(smem + OFF_RED);
   float* alpha_s = reinterpret_cast<float*>(smem + OFF_ALPHA);
   int* resc_s = reinterpret_cast<int*>(smem + OFF_FLAG);
-  int* qexp_s = resc_s + 4;
+  float2* qs_s = reinterpret_cast<float2*>(smem + OFF_QS);
   float* srow = reinterpret_cast<float*>(smem + OFF_SROW);
   uint2* info = reinterpret_cast<uint2*>(smem + OFF_INFO);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
@@ -417,51 +419,35 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     // ---- Q: bf16 -> x 2^qexp -> E4M3 hi and lo, latent part to TMEM, rope part to shared memory ----
     {
       constexpr int CH = DQK / 8;  // 16-byte chunks (8 bf16) per head
-      uint4* qraw = reinterpret_cast<uint4*>(smem + OFF_KV + QSTAGE * STAGE_BYTES);
+      const uint4* qraw = reinterpret_cast<const uint4*>(smem + OFF_KV + QSTAGE * STAGE_BYTES);
       auto bf_lo = [](uint32_t w) { return __uint_as_float(w << 16); };
       auto bf_hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
       if (!wait_warp(B_QLOAD, 0)) ok = false;
-      float mx = 0.f;  // (a NaN loses to a number)
-#pragma unroll 3
-      for (int e = st; e < H * CH; e += SM_THREADS) {
-        const uint4 v = qraw[e];
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // Eight threads a head: its largest |q| < 2^e puts Q at 2^8 below (2^(8 - e) stays finite:
+      // a query below 2^-120 is as good as zero).
+      {
+        const int h = st >> 3;
+        float mx = 0.f;  // (a NaN loses to a number; it stays one in E4M3)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[t])), fabsf(bf_hi(w[t]))));
-      }
-      constexpr int HAS_INF = INT32_MAX;
-      auto set_exponent = [&] {
+        for (int u = 0; u < CH / 8; ++u) {
+          const uint4 v = qraw[h * CH + (st & 7) + 8 * u];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (lane == 0) red_s[sw] = mx;
-        group_sync();
-        if (st == 0) {
-          float m = red_s[0];
-          for (int w = 1; w < SM_WARPS; ++w) m = fmaxf(m, red_s[w]);
+          for (int t = 0; t < 4; ++t) mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w[t])), fabsf(bf_hi(w[t]))));
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        if ((st & 7) == 0) {
           int e = 0;
-          frexpf(m, &e);  // m < 2^e
-          // (2^qexp stays finite: a query below 2^-120 is as good as zero)
-          *qexp_s = m == INFINITY ? HAS_INF : m > 0.f ? min(8 - e, 100) : 0;
+          frexpf(mx, &e);
+          const int x = mx > 0.f && mx < INFINITY ? min(8 - e, 100) : 0;
+          // A negative softmax scale is Q's sign.  E4M3 has no infinity: the factor makes its head NaN.
+          const float qk = fmaxf(fabsf(a.softmax_scale) * LOG2E * ldexpf(1.f, -x), 1e-30f);
+          qs_s[h] = make_float2(copysignf(ldexpf(1.f, x), a.softmax_scale), mx < INFINITY ? qk : NAN);
         }
-        group_sync();
-      };
-      set_exponent();
-      if (*qexp_s == HAS_INF) {  // infinities become NaN (E4M3 has none), the largest finite value counts
-        mx = 0.f;
-        for (int e = st; e < H * CH * 4; e += SM_THREADS) {
-          uint32_t* q2 = reinterpret_cast<uint32_t*>(qraw) + e;
-          uint32_t w = *q2;
-          if ((w & 0x7fffu) == 0x7f80u) w |= 0x7fffu;
-          if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x7fff0000u;
-          mx = fmaxf(mx, fmaxf(fabsf(bf_lo(w)), fabsf(bf_hi(w))));
-          *q2 = w;
-        }
-        group_sync();  // (every thread has read the mark)
-        set_exponent();
       }
-      // (a negative softmax scale is Q's sign)
-      const float qs = copysignf(ldexpf(1.f, *qexp_s), a.softmax_scale);
-      auto split8 = [&](const uint4 v, uint2& hv, uint2& lv) {  // 8 elements as byte quadruples
+      group_sync();
+      auto split8 = [&](const uint4 v, float qs, uint2& hv, uint2& lv) {  // 8 elements as byte quadruples
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
         uint32_t hi[4], lo[4];
 #pragma unroll
@@ -473,6 +459,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         hv = make_uint2(hi[0] | (hi[1] << 16), hi[2] | (hi[3] << 16));
         lv = make_uint2(lo[0] | (lo[1] << 16), lo[2] | (lo[3] << 16));
       };
+      const float qs_own = qs_s[hh].x;
       // Lane u writes row 32 q4 + u: Q_hi (u < 16) or Q_lo of head hh.  The two
       // lanes of a head split each 32-element block's chunks and swap halves
       // (loads staggered over the banks).
@@ -483,7 +470,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           uint2 hv, lv;
-          split8((t ^ (lane & 1)) ? rb : ra, hv, lv);
+          split8((t ^ (lane & 1)) ? rb : ra, qs_own, hv, lv);
           keep[t] = up ? lv : hv;
           const uint2 send = up ? hv : lv;
           recv[t] = make_uint2(__shfl_xor_sync(0xffffffffu, send.x, 16), __shfl_xor_sync(0xffffffffu, send.y, 16));
@@ -498,7 +485,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       for (int e = st; e < H * (DR / 8); e += SM_THREADS) {
         const int h = e >> 3, c = e & 7;
         uint2 hv, lv;
-        split8(qraw[h * CH + DL / 8 + c], hv, lv);
+        split8(qraw[h * CH + DL / 8 + c], qs_s[h].x, hv, lv);
         const int cc = c >> 1, hf = c & 1, rh = q_row(h, 0), rl = q_row(h, 1);
         *reinterpret_cast<uint2*>(qr + rh * DR + ((cc ^ ((rh >> 1) & 3)) << 4) + hf * 8) = hv;
         *reinterpret_cast<uint2*>(qr + rl * DR + ((cc ^ ((rl >> 1) & 3)) << 4) + hf * 8) = lv;
@@ -510,7 +497,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       if (lane == 0) mbar_arrive(bar(B_QREADY));
     }
     // logit (log2 domain) = (S_hi + S_lo) s_j qk_scale; qk_scale > 0 keeps -inf of a masked row
-    const float qk_scale = fmaxf(fabsf(a.softmax_scale) * LOG2E * ldexpf(1.f, -*qexp_s), 1e-30f);
+    const float qk_scale = qs_s[hh].y;
 
     // ---- the tiles ----
     float m_ref = -INFINITY;      // head hh's reference maximum (log2 domain), the same in its 8 threads

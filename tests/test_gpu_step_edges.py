@@ -185,6 +185,82 @@ def test_combine_splits_of_nan():
     assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(out).any(-1), bad)
 
 
+def _split_q(q, heads):
+    """The query as the kernel multiplies it, fp64: 64 heads, two E4M3 numbers of the
+    head scaled to 2^8; 16 heads, fp16 of the token scaled to 2^14."""
+    top = q.float().abs().amax(2 if heads == 64 else (1, 2), keepdim=True)
+    e = torch.frexp(top)[1]
+    y = torch.ldexp(q.float(), (8 if heads == 64 else 14) - e).half()
+    if heads == 64:
+        hi = y.to(torch.float8_e4m3fn)
+        lo = (y - hi.half()).to(torch.float8_e4m3fn)
+        y = hi.double() + lo.double()
+    return torch.ldexp(y.double(), e - (8 if heads == 64 else 14))
+
+
+def _close_bounds(c):
+    """Oracle, and the bounds of the weights as they are stated (P' = p s F as E4M3 + E5M2
+    with the head's largest at 16 or more; 16 heads: fp16 with the largest scale at 2^11):
+      elements  2^-8 of the result (its own rounding), 2^-8 + 2^-11 + 2^-12 of A = sum_j
+                softmax_j |x_j| (the two parts; fp16 before the split; fp32 sums), and
+                2^-14 of a unit below 2^-6: 2^-18 M sum_j |code_j|, M the head's largest
+                softmax_j s_j.  16 heads: 2^-11 and 2^-12 of A, 2^-25 of a unit below
+                2^-14: 2^-36 s_max sum_j |code_j|.
+      L2        the rounding of the result, and of independent weights: 1.30e-3 (16 heads
+                2.1e-4) root mean square of the formats over their range, 1.4e-3 (2.5e-4)
+                with the smaller weights, times G = sqrt(sum_j (softmax_j x_j)^2); a tenth
+                above for the draw.  (With a bit less in a weight 1.30e-3 is 2.54e-3.)
+      lse       what the query's own split moves it by, 36 additions of partial products
+                with 2^-22 of sum_d |q_d x_d| scale each, and 2^-20 for the rest."""
+    o, l, A, _ = ops._chunk_ref(c)
+    n, H, dl = o.shape
+    big = H == 64
+    x = (c["kv"].view(torch.float8_e4m3fn).double() * c["sc"].double()[:, None]).numpy()
+    code = c["kv"].view(torch.float8_e4m3fn).double().abs().numpy()
+    qs = _split_q(c["q"], H).numpy()
+    tol = 2.0**-8 * np.abs(o) + ((2.0**-8 if big else 0) + 2.0**-11 + 2.0**-12) * A
+    G2, ltol = 0.0, np.zeros_like(l)
+    for t in range(n):
+        if c["req"][t] < 0 or c["pos"][t] < 0:
+            continue
+        p = np.arange(int(c["pos"][t]) + 1)
+        slot = c["table"].numpy()[c["req"][t], p // c["page"]].astype(np.int64) * c["page"] + p % c["page"]
+        q, v, sc = c["q"][t].double().numpy(), x[slot], np.abs(c["sc"].double().numpy()[slot])
+        w = np.exp((q @ v.T) * c["scale"] - l[t][:, None])
+        if big:
+            tol[t] += 2.0**-18 * (w * sc).max(1)[:, None] * code[slot][:, :dl].sum(0)
+        else:
+            tol[t] += 2.0**-36 * sc.max() * code[slot][:, :dl].sum(0)
+        G2 += ((w**2) @ (v[:, :dl]**2)).sum()
+        z = (qs[t] @ v.T) * c["scale"]
+        m = z.max(1)
+        near = m + np.log(np.exp(z - m[:, None]).sum(1))
+        mass = (np.abs(q) @ np.abs(v).T).max(1) * abs(c["scale"])
+        ltol[t] = np.abs(near - l[t]) + 36 * 2.0**-22 * mass + 2.0**-20 * (1 + np.abs(l[t]))
+    own = torch.from_numpy(o).to(torch.bfloat16).double().numpy() - o
+    norm = 1.1 * np.sqrt((own**2).sum() + (1.4e-3 if big else 2.5e-4)**2 * G2)
+    return o, l, tol, norm, ltol
+
+
+def _check_close(out, lse, bounds):
+    o, l, tol, norm, ltol = bounds
+    got, gl = ops.host(out.double()), ops.host(lse.double())
+    assert (np.abs(got - o) <= tol).all(), float((np.abs(got - o) - tol).max())
+    assert np.linalg.norm(got - o) <= norm, (np.linalg.norm(got - o) / np.linalg.norm(o), norm / np.linalg.norm(o))
+    seen = ~np.isneginf(l)
+    assert np.array_equal(seen, ~np.isneginf(gl)) and (np.abs(gl[seen] - l[seen]) <= ltol[seen]).all()
+
+
+@both_shapes
+def test_chunk_one_head_with_far_larger_queries(shape):
+    """A head's query 2^12 times the others' takes none of their bits."""
+    c = ops._chunk_case(*shape, [500, 90], [3, 2], 64, seed=23)
+    c["q"][:, 5] *= 2.0**12
+    bounds = _close_bounds(c)
+    for splits in (1, 3, 12):
+        _check_close(*ops._run_chunk(c, splits)[:2], bounds)
+
+
 # ---- verify_draft and whole steps ----------------------------------------------------
 
 
