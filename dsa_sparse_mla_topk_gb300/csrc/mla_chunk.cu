@@ -13,11 +13,11 @@
 // A 64-row tile is 64 x 64 x (576 + 512) products twice (below), 1,376 cycles of
 // MMAs, and takes about 1,900: the P V of a tile needs its weights, and those its
 // QK^T, so the softmax's latency is hidden by two tiles only, and a long call
-// runs at the power limit.  Measured, scales and pages of 64: 1,024 tokens at the
-// end of 16,384 in 1.57 ms (1,440 TFLOP/s of the formula's bf16 products, the
+// runs at the power limit.  Measured, pages of 64: 1,024 tokens at the end of 16,384
+// positions in 1.48 ms (1,530 TFLOP/s of the formula's bf16 products, the
 // weights' second half not counted); 128 tokens of 16 requests, 4,096 positions
-// each, 66 us in one split; 32 requests of 4,096 to 8,192 positions 42 us in
-// four (118 MB of rows, 2.8 TB/s).  Warps:
+// each, 77 us in the two splits that the rule takes; 32 requests of 4,096 to 8,192
+// positions 40.4 us in four (118 MB of rows, 2.9 TB/s).  Warps:
 //  * 3 (or 7) TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
 //    tiles in flight.  A tile whose positions are all visible comes in boxes
 //    of 64, 32, 16 or 8 rows, the largest that divides the page size (5 to
@@ -35,18 +35,21 @@
 //    different columns, bring it both halves of its logits.
 // Q = Q_hi + Q_lo: two E4M3 numbers of a head scaled by a power of two, exact for bf16
 // values down to 2^-9 of the head's largest, below that to 2^-17 of it (E4M3's
-// steps end: 0.4% of a Gaussian head).  A weight P' = p s_j F is E4M3 + E5M2.  F puts the reference weight
-// (p = 1) of the row with the largest scale at 16, an exact value (a head that looks at
-// one row gives that row), or more where scales grow, so that weights down to
-// 2^-10 of it have a relative error of at most 2^-8 (0.12% root mean square,
-// a bf16 weight's is 0.08%); smaller ones an absolute one of 2^-14, and only
-// below 2^-21 nothing is left of them.  A second E4M3 number would end at 2^-14:
-// over a long context the many small weights of a flat tail are a share of
-// the result that must not be rounded away.
-// Lazy rescaling: a head's reference maximum moves when a logit passes it by more
-// than 2^3.8, F when a row's scale passes its bound; l is summed in fp32 from unrounded
-// p.  (Of 64 heads some reference then moves in few tiles; with 2^2 152 tokens of
-// 4,096 took 92 instead of 72 us.)  All waits are bounded.
+// steps end: 0.4% of a Gaussian head).  A weight P' = p s_j F is E4M3 + E5M2.  p = 2^(z - m) with
+// a reference m for each head, and F, also the head's, puts the largest p s_j at 16:
+// what counts is how much a row adds, not its scale alone, so one row of a
+// huge scale and no weight takes no bits from the others (with one F for the largest scale
+// 2^14 times the others': 5% off, 2^22: nothing left).  16 is an exact value: a head
+// that looks at one row gives that row.  Weights down to 2^-10 of the largest have a
+// relative error of at most 2^-8 (0.13% root mean square, a bf16 weight's is 0.08%);
+// smaller ones an absolute one of 2^-14 at 16, and only below 2^-21 of the largest nothing
+// is left of them.  A second E4M3 number would end at 2^-14: over a long context the
+// many small weights of a flat tail are a share of the result that must not
+// be rounded away.
+// Lazy rescaling: m and F move when a weight nears 448, the largest E4M3 value; l is
+// summed in fp32 from unrounded p.  (Of 64 heads some weight passes a bound in few
+// tiles; with a bound 2^2 above, 152 tokens of 4,096 took 92 instead of 72 us.)  All
+// waits are bounded.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -79,8 +82,9 @@ constexpr int P_BYTES = H * T;  // P_hi (or P_lo) of a tile: [head][row], K-majo
 constexpr int NPB = 2;
 constexpr int MAX_MERGED = chunk_max_merged();
 constexpr int SM_WARPS = 16, SM_THREADS = SM_WARPS * 32;
-constexpr float SCALE_BOUND = 32.0f;     // s_j F < 32, and
-constexpr float EXCEED_LOG2 = 3.8f;      // p = 2^(z - m) <= 2^3.8 < 14: P' < 448, the largest E4M3 value
+constexpr float P_REF_LOG2 = 4.0f;    // F puts the largest weight at 2^4,
+constexpr float P_TOP_LOG2 = 8.5f;    // and moves before one reaches 448 = 2^8.8, the largest E4M3 value
+constexpr float S_MIN_LOG2 = -60.0f;  // in both a scale counts as 2^-60 at least: neither F nor p grows past all bounds
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -94,11 +98,12 @@ __device__ constexpr int q_row(int h, int lo) { return 32 * (h >> 4) + (h & 15) 
 constexpr int OFF_KV = 0;
 constexpr int OFF_QR = OFF_KV + NST * STAGE_BYTES;
 constexpr int OFF_P = OFF_QR + QROPE_BYTES;           // [buffer][hi, lo]
-constexpr int OFF_RED = OFF_P + NPB * 2 * P_BYTES;    // [4 row parts][64 heads] floats
-constexpr int OFF_ALPHA = OFF_RED + 4 * H * 4;        // per-head factor of O, then 1 / l
+constexpr int OFF_RED = OFF_P + NPB * 2 * P_BYTES;    // [2][4 row parts][64 heads] floats
+constexpr int OFF_ALPHA = OFF_RED + 8 * H * 4;        // per-head factor of O
 constexpr int OFF_SROW = OFF_ALPHA + H * 4;           // [NST][64] the tiles' row scales
-constexpr int OFF_INFO = OFF_SROW + NST * T * 4;      // [NST][2] valid rows (bits) and largest scale of each 32 rows
-constexpr int OFF_ML = OFF_INFO + NST * 2 * 8;         // [2][64] for the cluster's merge
+constexpr int OFF_SLOG = OFF_SROW + NST * T * 4;      // [NST][64] their logarithms
+constexpr int OFF_INFO = OFF_SLOG + NST * T * 4;      // [NST][2] valid rows of each 32 (bits)
+constexpr int OFF_ML = OFF_INFO + NST * 2 * 4;         // [2][64] for the cluster's merge
 constexpr int OFF_QS = OFF_ML + 2 * H * 4;             // [64] the heads' 2^e of Q, and logits' factor
 constexpr int OFF_FLAG = OFF_QS + H * 8;               // O flags [4]
 constexpr int OFF_BAR = OFF_FLAG + 128;
@@ -140,7 +145,8 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
   int* resc_s = reinterpret_cast<int*>(smem + OFF_FLAG);
   float2* qs_s = reinterpret_cast<float2*>(smem + OFF_QS);
   float* srow = reinterpret_cast<float*>(smem + OFF_SROW);
-  uint2* info = reinterpret_cast<uint2*>(smem + OFF_INFO);
+  float* slog = reinterpret_cast<float*>(smem + OFF_SLOG);
+  uint32_t* info = reinterpret_cast<uint32_t*>(smem + OFF_INFO);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
   auto bar = [&](int b) { return smem_u32(bars + b); };
@@ -235,10 +241,17 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     };
     auto deal = [&](int rows) {
       const int nc = (NLAT + 1) * (T / rows);
-      const int c0 = nc * warp / NTMA, c = c0 + lane;
+      // Warps 0 and 1 look up the scales too: of seven, they take a fifth of many copies (152
+      // tokens of 4,096 positions at page size 4: 104 us, 111 with even shares).  At most
+      // 32 each: 80 copies are 27 of three warps, 13 of seven.
+      auto first = [&](int w) {
+        if (NTMA < 7 || nc < 40) return nc * w / NTMA;
+        return w < 2 ? nc * w / 10 : nc / 5 + (nc - nc / 5) * (w - 2) / (NTMA - 2);
+      };
+      const int c0 = first(warp), c = c0 + lane;
       Deal d;
       d.g = c / (NLAT + 1), d.part = c % (NLAT + 1);
-      d.has = lane < nc * (warp + 1) / NTMA - c0;
+      d.has = lane < first(warp + 1) - c0;
       d.bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, d.has && d.part < NLAT)) * 128u * rows +
                 (uint32_t)__popc(__ballot_sync(0xffffffffu, d.has && d.part == NLAT)) * (uint32_t)DR * rows;
       return d;
@@ -280,6 +293,8 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     int rp2 = row_page(2);
     int slot0 = row_slot(0, row_page(0)), slot1 = row_slot(1, row_page(1));
     float sc0 = row_scale(slot0), sc1 = row_scale(slot1);
+    auto scale_log = [](float sc) { return fmaxf(__log2f(fabsf(sc)), S_MIN_LOG2); };
+    float lg0 = scale_log(sc0);
     for (int lt = 0; lt < ntl; ++lt) {
       const int s = lt % NST;
       const int4 pg3 = pages_of(lt + 3);
@@ -296,9 +311,9 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       }
       if (warp < 2) {
         const unsigned valid = __ballot_sync(0xffffffffu, slot0 >= 0);
-        const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(sc0)));
         srow[s * T + 32 * warp + lane] = sc0;
-        if (lane == 0) info[s * 2 + warp] = make_uint2(valid, top);
+        slog[s * T + 32 * warp + lane] = lg0;
+        if (lane == 0) info[s * 2 + warp] = valid;
         __syncwarp();
       }
       const uint32_t dst = kv_base + s * STAGE_BYTES;
@@ -327,6 +342,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       rp2 = rp3;
       slot0 = slot1, slot1 = slot2;
       sc0 = sc1, sc1 = sc2;
+      lg0 = scale_log(sc0);  // (after the copies are out)
       issued = lt + 1;
     }
     // no copy may land after the CTA is gone
@@ -442,7 +458,7 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
           frexpf(mx, &e);
           const int x = mx > 0.f && mx < INFINITY ? min(8 - e, 100) : 0;
           // A negative softmax scale is Q's sign.  E4M3 has no infinity: the factor makes its head NaN.
-          const float qk = fmaxf(fabsf(a.softmax_scale) * LOG2E * ldexpf(1.f, -x), 1e-30f);
+          const float qk = fabsf(a.softmax_scale) * LOG2E * ldexpf(1.f, -x);
           qs_s[h] = make_float2(copysignf(ldexpf(1.f, x), a.softmax_scale), mx < INFINITY ? qk : NAN);
         }
       }
@@ -496,31 +512,46 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_QREADY));
     }
-    // logit (log2 domain) = (S_hi + S_lo) s_j qk_scale; qk_scale > 0 keeps -inf of a masked row
+    // logit (log2 domain) = (S_hi + S_lo) (s_j qk_scale), rounded as a number of its own: a
+    // reference is one of the logits, and the difference to it is then exact however
+    // large they are (in one fused step a logit of 2^31 was off by 2^7: weights of infinity)
     const float qk_scale = qs_s[hh].y;
 
     // ---- the tiles ----
-    float m_ref = -INFINITY;      // head hh's reference maximum (log2 domain), the same in its 8 threads
-    uint64_t l2 = pk2(0.f, 0.f);  // head hh's share of l F, two running sums
-    float p_log = 0.f;            // log2 F, the same in every thread; set at the first row with a scale
-    float p_scale = 1.f;          // F
-    float shift = 0.f;            // log2 F - m_ref (m_ref = -inf: log2 F)
-    bool p_set = false;
+    float m_ref = -INFINITY;      // head hh's reference m (log2 domain), the same in its 8 threads
+    float f_log = 0.f, f_scale = 1.f;  // its log2 F and F
+    uint64_t l2 = pk2(0.f, 0.f);  // its share of l = sum 2^(z - m), two running sums
     const uint64_t qk2 = pk2(qk_scale, qk_scale);
     int stage = 0, kv_phase = 0;
     for (int lt = 0; lt < ntl; ++lt) {  // no early exit: every warp reaches every barrier
       const int sb = lt & 1;
       if (ok && !wait_warp(B_KVF + stage, kv_phase)) ok = false;  // the tile's row scales
-      if (ok && !wait_warp(B_SF + sb, (lt >> 1) & 1)) ok = false;
-      float sj[8];  // the rows' scales
+      // s_j qk_scale, s_j F, and log2(s_j F) - 8.5 - m: above 0 with the logit added, the
+      // row's weight is too large (m = -inf: any)
+      uint64_t sq[4], sf[4], su[4];
+      const int row0 = stage * T + 16 * part + 8 * up;
+      auto rows8 = [&](const float* of, uint64_t (&v)[4]) {
+        const float4 lo = reinterpret_cast<const float4*>(of + row0)[0], hi = reinterpret_cast<const float4*>(of + row0)[1];
+        v[0] = pk2(lo.x, lo.y), v[1] = pk2(lo.z, lo.w), v[2] = pk2(hi.x, hi.y), v[3] = pk2(hi.z, hi.w);
+      };
+      auto scaled = [&](const uint64_t (&v)[4], uint64_t f2, uint64_t (&to)[4]) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) to[c] = mul2(v[c], f2);
+      };
       {
-        const float4* s4 = reinterpret_cast<const float4*>(srow + stage * T + 16 * part + 8 * up);
-        const float4 lo = s4[0], hi = s4[1];
-        sj[0] = lo.x, sj[1] = lo.y, sj[2] = lo.z, sj[3] = lo.w, sj[4] = hi.x, sj[5] = hi.y, sj[6] = hi.z, sj[7] = hi.w;
+        uint64_t sj[4];
+        rows8(srow, sj);
+        scaled(sj, qk2, sq);
+        scaled(sj, pk2(f_scale, f_scale), sf);
+        rows8(slog, su);
+        const float above = f_log - P_TOP_LOG2 - m_ref;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) su[c] = add2(su[c], pk2(above, above));
       }
-      const uint2 inf = info[stage * 2 + (part >> 1)];
+      if (ok && !wait_warp(B_SF + sb, (lt >> 1) & 1)) ok = false;
+      const uint32_t rows = info[stage * 2 + (part >> 1)];
       tc_fence_after_sync();
-      float z[8];  // (S_hi + S_lo) s_j of head hh, rows 16 part + 8 up + c (invalid: -inf)
+      float z[8];  // the logits of head hh, rows 16 part + 8 up + c (invalid: -inf)
       {
         // lanes 0-15 of the quadrant hold the heads' S_hi, lanes 16-31 their S_lo
         float vh[8], vl[8];
@@ -529,60 +560,86 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
         tmem_wait_ld();
 #pragma unroll
         for (int c = 0; c < 8; c += 2)
-          upk2(mul2(add2(pk2(vh[c], vh[c + 1]), pk2(vl[c], vl[c + 1])), pk2(sj[c], sj[c + 1])), z[c], z[c + 1]);
-        if (inf.x != 0xffffffffu) {  // a tile with rows past the last position, or bad pages
-          const unsigned my_valid = inf.x >> (16 * (part & 1) + 8 * up);
+          upk2(mul2(add2(pk2(vh[c], vh[c + 1]), pk2(vl[c], vl[c + 1])), sq[c >> 1]), z[c], z[c + 1]);
+        if (rows != 0xffffffffu) {  // a tile with rows past the last position, or bad pages
+          const unsigned my_valid = rows >> (16 * (part & 1) + 8 * up);
 #pragma unroll
           for (int c = 0; c < 8; ++c)
             if (!((my_valid >> c) & 1u)) z[c] = -INFINITY;
         }
       }
-      float tm = z[0];
+      // Is a weight too large?  Every thread goes on as if none was; the vote comes
+      // after the weights, which are computed again in the rare tile where some
+      // thread's answer was yes.  (The answer from the weights themselves, which needs
+      // no logarithms, comes so late that 1,024 tokens of 16,384 take 2.3 ms.)
+      bool want;
+      {
+        float t[8];
 #pragma unroll
-      for (int c = 1; c < 8; ++c) tm = fmaxf(tm, z[c]);
-      // Does a logit pass its head's reference, or a scale F's bound?  Every
-      // thread goes on as if none did; the vote comes after the weights, which are
-      // computed again in the rare tile where some thread's answer was yes.
-      const float smax = __uint_as_float(inf.y);
-      const bool grow = p_set ? smax * p_scale >= SCALE_BOUND : smax > 0.f;
-      const bool want = grow || fmaf(tm, qk_scale, -m_ref) > EXCEED_LOG2;
+        for (int c = 0; c < 8; c += 2) upk2(add2(pk2(z[c], z[c + 1]), su[c >> 1]), t[c], t[c + 1]);
+        float tm = t[0];
+#pragma unroll
+        for (int c = 1; c < 8; ++c) tm = fmaxf(tm, t[c]);
+        want = tm > 0.f;
+      }
       uint32_t phi[4], plo[4];
       uint64_t ln;
       for (bool again = false;; again = true) {
-        // p F, summed into l; folded with the row's scale, as E4M3 + E5M2
+        // p = 2^(z - m), summed into l; folded with s_j F, as E4M3 + E5M2
+        const float shift = m_ref == -INFINITY ? 0.f : -m_ref;
         const uint64_t shift2 = pk2(shift, shift);
         ln = l2;
 #pragma unroll
         for (int c = 0; c < 8; c += 2) {
           float d0, d1, w0, w1;
-          upk2(fma2(pk2(z[c], z[c + 1]), qk2, shift2), d0, d1);
+          upk2(add2(pk2(z[c], z[c + 1]), shift2), d0, d1);
           const uint64_t p = pk2(ex2(d0), ex2(d1));
           ln = add2(ln, p);
-          upk2(mul2(p, pk2(sj[c], sj[c + 1])), w0, w1);
+          upk2(mul2(p, sf[c >> 1]), w0, w1);
           split_e4m3_e5m2x2(f32x2_to_f16x2(w0, w1), phi[c >> 1], plo[c >> 1]);
         }
         if (again) break;
         if (!named_barrier_or(3, SM_THREADS, want)) break;  // one vote of the 16 warps: uniform
-        // ---- move the references that were passed, and F; rescale O and l ----
-        tm = fmaxf(tm, __shfl_xor_sync(0xffffffffu, tm, 16));
-        if (up == 0) red_s[part * H + hh] = tm * qk_scale;
+        // ---- move m to the largest logit, and F where the largest weight passed it; rescale O and l ----
+        float zt = z[0], wt = -INFINITY;  // largest logit, and log2 of the largest p s_j with it as the reference
+        uint64_t sj[4], sl[4];
+        rows8(srow, sj);
+        rows8(slog, sl);
+#pragma unroll
+        for (int c = 1; c < 8; ++c) zt = fmaxf(zt, z[c]);
+#pragma unroll
+        for (int c = 0; c < 8; c += 2) {
+          float l0, l1;
+          upk2(sl[c >> 1], l0, l1);
+          wt = fmaxf(wt, fmaxf((z[c] - zt) + l0, (z[c + 1] - zt) + l1));
+        }
+        {
+          const float zo = __shfl_xor_sync(0xffffffffu, zt, 16), wo = __shfl_xor_sync(0xffffffffu, wt, 16);
+          const float zm = fmaxf(zt, zo);
+          wt = fmaxf(wt + (zt - zm), wo + (zo - zm));
+          zt = zm;
+        }
+        if (up == 0) red_s[part * H + hh] = zt, red_s[(4 + part) * H + hh] = wt;
         group_sync();
-        const float mt = fmaxf(fmaxf(red_s[hh], red_s[H + hh]), fmaxf(red_s[2 * H + hh], red_s[3 * H + hh]));
-        const float sm = fmaxf(__uint_as_float(info[stage * 2].y), __uint_as_float(info[stage * 2 + 1].y));
+        float mn = m_ref;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) mn = fmaxf(mn, red_s[c * H + hh]);
+        wt = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) wt = fmaxf(wt, red_s[(4 + c) * H + hh] + (red_s[c * H + hh] - mn));
         float alpha = 1.f;
-        if (mt > m_ref + EXCEED_LOG2) {
-          alpha = m_ref == -INFINITY ? 0.f : ex2(m_ref - mt);
-          m_ref = mt;
+        if (mn != -INFINITY) {
+          const float f_new = P_REF_LOG2 - wt;
+          const float f_old = f_log + (mn - m_ref);  // F's exponent with m moved alone (m_ref = -inf: infinite)
+          const bool move = f_old - f_new > P_TOP_LOG2 - P_REF_LOG2 - 0.5f;
+          const float al = ex2(m_ref - mn);
+          l2 = mul2(l2, pk2(al, al));
+          if (move) alpha = ex2(f_new - f_old);
+          f_log = move ? f_new : f_old;
+          f_scale = ex2(f_log);
+          m_ref = mn;
         }
-        if (sm > 0.f && sm <= 3.0e38f && (!p_set || sm * p_scale >= SCALE_BOUND)) {
-          const float f = fminf(log2f(16.f / sm), 80.f);  // (sums of F stay finite for subnormal scales)
-          alpha *= ex2(f - p_log);  // O and l carry F
-          p_log = f;
-          p_set = true;
-          p_scale = ex2(f);
-        }
-        l2 = mul2(l2, pk2(alpha, alpha));
-        shift = p_log - (m_ref == -INFINITY ? 0.f : m_ref);
+        scaled(sj, pk2(f_scale, f_scale), sf);
         if (part == 0 && up == 0) alpha_s[hh] = alpha;
         const unsigned need = __ballot_sync(0xffffffffu, lt > 0 && alpha != 1.f);
         if (part == 0 && lane == 0) resc_s[q4] = need != 0u;
@@ -632,10 +689,10 @@ __global__ void __launch_bounds__((NTMA + 1 + SM_WARPS) * 32, 1)
     group_sync();
     if (part == 0 && up == 0) {
       const float l = (red_s[hh] + red_s[H + hh]) + (red_s[2 * H + hh] + red_s[3 * H + hh]);
-      // (O and l both carry F; a NaN is not an empty row)
-      alpha_s[hh] = l != 0.f ? (MERGE ? 1.f : 1.f / l) : 0.f;
-      const float lse = l != 0.f ? (m_ref + log2f(l * ex2(-p_log))) * LN2 : -INFINITY;
-      if (MERGE) ml_s[hh] = ok && l != 0.f ? m_ref - p_log : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
+      // (O carries F; a NaN is not an empty row)
+      alpha_s[hh] = l != 0.f ? ex2(-f_log) * (MERGE ? 1.f : 1.f / l) : 0.f;
+      const float lse = l != 0.f ? (m_ref + log2f(l)) * LN2 : -INFINITY;
+      if (MERGE) ml_s[hh] = ok && l != 0.f ? m_ref : -INFINITY, ml_s[H + hh] = ok ? l : 0.f;
       else if (S > 1) a.lse_part[((int64_t)split * a.num_q + i) * H + hh] = lse;
       else if (a.lse) a.lse[(int64_t)i * H + hh] = lse;
     }

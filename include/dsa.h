@@ -434,6 +434,12 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t
  * sees a NaN code or a NaN scale, has out = lse = NaN, for any number of splits;
  * other heads and tokens are as without it.  (A visible row with an infinite
  * scale gives NaN in out, and an unspecified lse.)
+ * Precision: logits and sums are fp32.  64 heads: of bf16 queries bits below
+ * 2^-17 of the head's largest value are lost; a row's weight, softmax times
+ * kv_scale, has a relative error of at most 2^-8 (0.13% root mean square) down to
+ * 2^-10 of the head's largest weight, and one of 2^-18 of that below.
+ * Scales count in this from 2^-60 on.  16 heads: 2^-11, down to 2^-25 of the
+ * largest kv_scale that the token sees.
  * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
  * and the token sees nothing; q_req outside [-1, num_req) or a page id out of
  * range sets DSA_DEV_BAD_PAGE; such rows are skipped.

@@ -107,7 +107,7 @@ def test_chunk_any_page_id_out_of_range_is_told(shape, bad):
 
 
 @both_shapes
-@pytest.mark.parametrize("size", [2.0**-133, 2.0**-125, 2.0**-121, 2.0**-110])
+@pytest.mark.parametrize("size", [2.0**-133, 2.0**-125, 2.0**-121, 2.0**-110, 3.3e38])
 def test_chunk_smallest_and_largest_queries(shape, size):
     """One element of a head's query is not zero: next to the type's smallest value the
     result is the mean of the visible rows; next to the largest, the one row that it picks."""
@@ -258,6 +258,50 @@ def test_chunk_one_head_with_far_larger_queries(shape):
     c["q"][:, 5] *= 2.0**12
     bounds = _close_bounds(c)
     for splits in (1, 3, 12):
+        _check_close(*ops._run_chunk(c, splits)[:2], bounds)
+
+
+@both_shapes
+@pytest.mark.parametrize("log2", [10, 12, 14, 20, 22, 40])
+@pytest.mark.parametrize("at", [0, 150, 299])
+def test_chunk_a_row_of_a_huge_scale_that_weighs_nothing(shape, log2, at):
+    """One row's scale is 2^10 to 2^40 times the others', and its logit so low that it does
+    not count: the others' weights keep their bits (16 heads: up to 2^24, as documented)."""
+    if shape[0] == 16 and log2 > 24:
+        pytest.skip("past the 16-head kernel's range")
+    c = ops._chunk_case(*shape, [300, 70], [1, 2], 64, seed=4)
+    slot = int(c["table"][0, at // 64]) * 64 + at % 64
+    c["sc"][slot] = c["sc"].max() * 2.0**log2
+    c["kv"][slot] = 0
+    c["kv"][slot, -1] = 0x38  # 1
+    c["q"][:, :, -1] = -40.0
+    bounds = _close_bounds(c)
+    for splits in (1, 2, 5, 12):
+        out, lse, st = ops._run_chunk(c, splits)
+        assert st == 0
+        _check_close(out, lse, bounds)
+
+
+@both_shapes
+def test_chunk_heads_that_look_at_rows_of_different_scales(shape):
+    """Scales over 2^16 (16 heads: 2^12) along the context; each head's query picks another
+    stretch of it: every head has its own largest weight."""
+    span = 16 if shape[0] == 64 else 12
+    c = ops._chunk_case(*shape, [1024], [2], 64, seed=14)
+    pos_of = torch.zeros(len(c["sc"]))
+    for j, p in enumerate(c["table"][0].tolist()):
+        pos_of[p * 64:(p + 1) * 64] = torch.arange(64) + 64 * j
+    part = (pos_of / 128).long().clamp(max=7)  # eight stretches, each a direction of the rope part
+    scale = torch.exp2(-part.float() * span / 8)
+    c["sc"] = torch.full_like(c["sc"], 2.0**-6) * scale
+    c["kv"][:, shape[1]:] = 0
+    c["kv"][torch.arange(len(part)), shape[1] + part] = 0x78  # 256
+    c["q"] = c["q"] * 2.0**-9
+    for h in range(shape[0]):
+        c["q"][:, h, shape[1] + h % 8] = float(16 / (256 * 2.0**-6 * 2.0**(-(h % 8) * span / 8) * c["scale"]))
+    c["q"] = c["q"].to(torch.bfloat16)
+    bounds = _close_bounds(c)
+    for splits in (1, 4):
         _check_close(*ops._run_chunk(c, splits)[:2], bounds)
 
 
