@@ -252,6 +252,18 @@ def _check_close(out, lse, bounds):
 
 
 @both_shapes
+@pytest.mark.parametrize("lens,new,sharp", [([700, 130], [3, 4], 1.0), ([3000], [2], 1.0), ([900, 64], [4, 2], 3.0),
+                                            ([2000], [3], 0.1), ([1], [1], 1.0)], ids=str)
+def test_chunk_error_is_that_of_the_stated_weights(shape, lens, new, sharp):
+    c = ops._chunk_case(*shape, lens, new, 64, seed=sum(lens), sharp=sharp, pad=1)
+    bounds = _close_bounds(c)
+    for splits in (1, 3, 12):
+        out, lse, st = ops._run_chunk(c, splits)
+        assert st == 0
+        _check_close(out, lse, bounds)
+
+
+@both_shapes
 def test_chunk_one_head_with_far_larger_queries(shape):
     """A head's query 2^12 times the others' takes none of their bits."""
     c = ops._chunk_case(*shape, [500, 90], [3, 2], 64, seed=23)
