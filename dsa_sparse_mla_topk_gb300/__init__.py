@@ -38,7 +38,7 @@ EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_
                     "dsa_verify_draft", "dsa_verify_draft_req", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
                     "dsa_prefix_cache_acquire", "dsa_prefix_cache_release", "dsa_prefix_cache_stats",
                     "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits",
-                    "dsa_chunk_pick_num_splits")
+                    "dsa_chunk_pick_num_splits", "dsa_chunk_pick_num_splits_live")
 
 _lock = threading.Lock()
 _lib = None
@@ -124,6 +124,8 @@ def load_library(path: str | None = None):
         lib.dsa_pick_num_splits.restype = i32
         lib.dsa_chunk_pick_num_splits.argtypes = [i32, i32, i32, i32, i32, i32]
         lib.dsa_chunk_pick_num_splits.restype = i32
+        lib.dsa_chunk_pick_num_splits_live.argtypes = [i32, i32, i32, i32, i32, i32, i32]
+        lib.dsa_chunk_pick_num_splits_live.restype = i32
         global _fast
         _fast = _load_marshal(lib)
         _lib = lib
@@ -174,10 +176,14 @@ def pick_num_splits(num_q: int, heads: int, d_latent: int, d_rope: int, k: int, 
     return load_library().dsa_pick_num_splits(num_q, heads, d_latent, d_rope, k, num_sms)
 
 
-def pick_chunk_splits(num_q: int, heads: int, d_latent: int, d_rope: int, max_ctx: int, num_sms: int = 0) -> int:
-    """KV splits chunk_mla takes for contexts of about max_ctx positions."""
-    return load_library().dsa_chunk_pick_num_splits(num_q, heads, d_latent, d_rope, max(1, min(max_ctx, 2**31 - 1)),
-                                                    num_sms)
+def pick_chunk_splits(num_q: int, heads: int, d_latent: int, d_rope: int, max_ctx: int, num_sms: int = 0,
+                      live: int | None = None) -> int:
+    """KV splits chunk_mla takes for contexts of about max_ctx positions; ``live``:
+    about how many of the tokens are no padding (None: unknown)."""
+    lib, ctx = load_library(), max(1, min(max_ctx, 2**31 - 1))
+    if live is None:
+        return lib.dsa_chunk_pick_num_splits(num_q, heads, d_latent, d_rope, ctx, num_sms)
+    return lib.dsa_chunk_pick_num_splits_live(num_q, max(0, min(live, num_q)), heads, d_latent, d_rope, ctx, num_sms)
 
 
 def _p(t: torch.Tensor | None):
@@ -850,19 +856,22 @@ def chunk_mla_fwd(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, 
 
 
 def chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, *, d_latent: int, d_rope: int, page_size: int,
-              softmax_scale: float, max_ctx: int | None = None, num_splits: int | None = None,
+              softmax_scale: float, max_ctx: int | None = None, live: int | None = None, num_splits: int | None = None,
               buffers: dict | None = None, dev_status=None, stream=None):
     """The whole pass over every visible position: chunk_mla_fwd, merging its
     splits or, with more than 8 or where ``buffers`` holds partials, followed by
     combine.  ``max_ctx`` (default: the block table's width) is about the
-    longest context, from which the number of KV splits is picked when
-    ``num_splits`` is None; the result is right for any value.  ``buffers``
+    longest context and ``live`` (default: unknown, the batch may be half padding)
+    about how many of the tokens are live, from which the number of KV splits is
+    picked when ``num_splits`` is None; the result is right for any value.  ``buffers``
     (optional) holds preallocated out / lse / o_part / lse_part tensors.
     Returns (out, lse), which share one allocation unless given (clone lse to
     keep it alone)."""
     b = buffers or {}
     if num_splits is None and max_ctx is None:
         max_ctx = block_table.shape[1] * page_size
+    if num_splits is None and live is not None:
+        num_splits = pick_chunk_splits(q.shape[0], q.shape[1], d_latent, d_rope, max_ctx, live=live)
     if not b and stream is None and _fast is not None and num_splits != 0:
         r = _fast.chunk_mla(q, kv, kv_scale, block_table, q_req, q_pos, d_latent, d_rope, page_size, softmax_scale,
                             max_ctx or 1, num_splits or 0, dev_status)

@@ -91,8 +91,13 @@ int32_t dsa_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, 
   return best;
 }
 
-int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope, int32_t max_ctx,
-                                  int32_t num_sms) {
+}  // extern "C"
+
+namespace {
+
+// KV splits of dsa_chunk_mla_fwd; num_live < 0: not known.
+int32_t chunk_splits(int32_t num_q, int32_t num_live, int32_t num_heads, int32_t d_latent, int32_t d_rope,
+                     int32_t max_ctx, int32_t num_sms) {
   const int32_t tile = dsa_kv_tile_size(num_heads, d_latent, d_rope);
   if (tile <= 0 || num_q <= 0 || max_ctx <= 0) return 1;
   if (num_sms <= 0) num_sms = dsa::device_sm_count();
@@ -103,11 +108,11 @@ int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_la
   static const int32_t clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
   // (64, 512, 64), in hundredths of a tile's time (measured: 0.93 us): a CTA's start
   // and end; the merge in a cluster; the Combine, whose partials grow with tokens and
-  // splits (1 x 64: 18 us, 24 x 12: 17).  The live rows are not known here: a batch
-  // of fixed capacity (a captured step, a verify block whose requests drafted
-  // less) is padded, so the cost is that of a full batch plus that of a half full
-  // one.  128 rows of 4,096 positions: one split 66 us full and 63 with 72 live rows,
-  // two 82 and 43.
+  // splits (1 x 64: 18 us, 24 x 12: 17).  Where the live rows are not known (a batch of
+  // fixed capacity, as of a captured step or a verify block whose requests drafted
+  // less, is padded), the cost is that of a full batch plus that of a half full one.
+  // 128 rows of 4,096 positions: one split 61 us full and with 72 live rows, two 77
+  // and 42.
   auto large = [&](int32_t s) {
     const int64_t fixed = 800, merge = 500, combine = 500 + s * (15 + 4 * (int64_t)num_q);
     const int64_t cap = s <= 8 ? (int64_t)clusters[s] * num_sms / 152 : num_sms / s;  // tokens that run at once
@@ -115,13 +120,13 @@ int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_la
     // (a cluster's merge is its CTAs' work)
     const int64_t cta = 100 * ((ntiles + s - 1) / s) + fixed + (s <= 8 ? join : 0);
     auto waves = [&](int64_t n) { return cap > 0 ? (n + cap - 1) / cap : (n * s + num_sms - 1) / num_sms; };
-    return (waves(num_q) + waves((num_q + 1) / 2)) * cta + (s <= 8 ? 0 : join);
+    return (num_live >= 0 ? 2 * waves(num_live) : waves(num_q) + waves((num_q + 1) / 2)) * cta + (s <= 8 ? 0 : join);
   };
   // (16, 64, 16), in hundredths of a us: a CTA's start and end, its steps of eight
   // tiles, alone on an SM or two of them, and the merge or Combine (one token of
   // 16,384 positions: 8 splits 14 us, 16 13, 32 15; 107 of 12,733: 1 59 us, 2 55, 5 51, 8 57).
   auto small = [&](int32_t s) {
-    const int64_t steps = ((ntiles + s - 1) / s + 7) / 8, ctas = (int64_t)num_q * s;
+    const int64_t steps = ((ntiles + s - 1) / s + 7) / 8, ctas = (int64_t)(num_live >= 0 ? num_live : num_q) * s;
     const int64_t join = s == 1 ? 0 : s <= 8 ? 100 : 250 + 18 * s;
     return join + (ctas <= num_sms ? 400 + 108 * steps : (ctas + 2 * num_sms - 1) / (2 * num_sms) * (400 + 200 * steps));
   };
@@ -132,6 +137,21 @@ int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_la
     if (best_cost < 0 || cost < best_cost) best = s, best_cost = cost;
   }
   return best;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope, int32_t max_ctx,
+                                  int32_t num_sms) {
+  return chunk_splits(num_q, -1, num_heads, d_latent, d_rope, max_ctx, num_sms);
+}
+
+int32_t dsa_chunk_pick_num_splits_live(int32_t num_q, int32_t num_live, int32_t num_heads, int32_t d_latent,
+                                       int32_t d_rope, int32_t max_ctx, int32_t num_sms) {
+  const int32_t live = num_live < 1 ? 1 : num_live < num_q ? num_live : num_q;
+  return chunk_splits(num_q, live, num_heads, d_latent, d_rope, max_ctx, num_sms);
 }
 
 size_t dsa_sparse_mla_workspace_size(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope,

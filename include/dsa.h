@@ -581,10 +581,14 @@ DSA_API int32_t dsa_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_
  * contexts of about max_ctx positions: the number with the least estimated
  * time, from the tiles of a split, a CTA's fixed cost, the waves of CTAs (of clusters,
  * for the 2 to 8 splits that the call merges) and the merge or Combine.  On the
- * tensor cores a full batch and one whose second half is padding count the same.
+ * tensor cores a full batch and one whose second half is padding count the same;
+ * a caller that knows about how many of the num_q tokens are live (num_q in a full
+ * batch) asks dsa_chunk_pick_num_splits_live.
  */
 DSA_API int32_t dsa_chunk_pick_num_splits(int32_t num_q, int32_t num_heads, int32_t d_latent, int32_t d_rope,
                                           int32_t max_ctx, int32_t num_sms);
+DSA_API int32_t dsa_chunk_pick_num_splits_live(int32_t num_q, int32_t num_live, int32_t num_heads, int32_t d_latent,
+                                               int32_t d_rope, int32_t max_ctx, int32_t num_sms);
 
 #ifdef __cplusplus
 }

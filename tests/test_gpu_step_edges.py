@@ -317,6 +317,16 @@ def test_chunk_heads_that_look_at_rows_of_different_scales(shape):
         _check_close(*ops._run_chunk(c, splits)[:2], bounds)
 
 
+@both_shapes
+def test_chunk_live_tokens_only_choose_the_splits(shape):
+    """Any count of live tokens, right or wrong, gives the call's result."""
+    c = ops._chunk_case(*shape, [900, 130], [9, 4], 64, seed=31, pad=20)
+    want = ops._chunk_ref(c)
+    for run in (lambda f: f(), ops._without_cpp):
+        for live in (None, 0, 1, 13, 33, 99):
+            ops._check_chunk(*run(lambda: ops._run_chunk(c, None, max_ctx=900, live=live))[:2], want)
+
+
 # ---- verify_draft and whole steps ----------------------------------------------------
 
 

@@ -76,6 +76,22 @@ def test_outputs_over_any_input_or_each_other(lib):  # noqa: F811
     assert _verify(lib, co=A(6)) == 4  # the lengths in place
 
 
+def test_split_rule_of_batches_whose_live_tokens_are_known(lib):  # noqa: F811
+    """A full batch is not split for the sake of padding that it does not have, and a
+    padded one is split like the small batch that it is."""
+    pick = lambda n, live, ctx, H=64: dsa.pick_chunk_splits(  # noqa: E731
+        n, H, 512 if H == 64 else 64, 64 if H == 64 else 16, ctx, 152, live=live)
+    assert pick(128, None, 4096) == 2 and pick(128, 128, 4096) == 1 and pick(128, 72, 4096) == 2
+    assert pick(48, None, 4096) == 5 and pick(48, 48, 4096) < 5 and pick(48, 27, 4096) == 5
+    assert pick(152, 152, 16384) == 1
+    for n, live, ctx in ((128, 20, 4096), (64, 64, 8192), (1000, 18, 5000), (7, 7, 100)):
+        for H in (16, 64):
+            assert pick(n, live, ctx, H) == pick(live, live, ctx, H)  # padding costs nothing
+    # but to the Combine, which more than 8 splits need and which takes every token
+    assert pick(3, 3, 5000) > 8 >= pick(1000, 3, 5000)
+    assert pick(128, 0, 4096) == pick(128, 1, 4096) and pick(5, 99, 4096) == pick(5, 5, 4096)
+
+
 # ---- the binding's C++ marshalling ---------------------------------------------------
 
 
