@@ -358,7 +358,8 @@ __global__ void __launch_bounds__(NTHREADS, 1)
       for (int w = 1; w < nq / 32; ++w) m = fmaxf(m, red_s[w]);
       int e = 0;
       if (m > 0.f && m <= 3.0e38f) frexpf(m, &e);  // m < 2^e
-      *qexp_s = (m > 0.f && m <= 3.0e38f) ? 8 - e : 0;
+      // (2^qexp stays finite: a query below 2^-120 is as good as zero)
+      *qexp_s = (m > 0.f && m <= 3.0e38f) ? min(8 - e, 100) : 0;
     }
   };
   auto q_split_pass = [&](int qt, int nq, bool arrive) {

@@ -273,14 +273,12 @@ def test_chunk_one_head_with_far_larger_queries(shape):
         _check_close(*ops._run_chunk(c, splits)[:2], bounds)
 
 
-@both_shapes
-@pytest.mark.parametrize("log2", [10, 12, 14, 20, 22, 40])
+@pytest.mark.parametrize("shape,log2", [(s, x) for s in SHAPES for x in (10, 12, 14, 20, 22, 40) if s[0] == 64 or x <= 24],
+                         ids=lambda v: f"h{v[0]}" if isinstance(v, tuple) else str(v))
 @pytest.mark.parametrize("at", [0, 150, 299])
 def test_chunk_a_row_of_a_huge_scale_that_weighs_nothing(shape, log2, at):
     """One row's scale is 2^10 to 2^40 times the others', and its logit so low that it does
     not count: the others' weights keep their bits (16 heads: up to 2^24, as documented)."""
-    if shape[0] == 16 and log2 > 24:
-        pytest.skip("past the 16-head kernel's range")
     c = ops._chunk_case(*shape, [300, 70], [1, 2], 64, seed=4)
     slot = int(c["table"][0, at // 64]) * 64 + at % 64
     c["sc"][slot] = c["sc"].max() * 2.0**log2
@@ -325,6 +323,26 @@ def test_chunk_live_tokens_only_choose_the_splits(shape):
     for run in (lambda f: f(), ops._without_cpp):
         for live in (None, 0, 1, 13, 33, 99):
             ops._check_chunk(*run(lambda: ops._run_chunk(c, None, max_ctx=900, live=live))[:2], want)
+
+
+@both_shapes
+@pytest.mark.parametrize("size", [2.0**-133, 2.0**-125, 2.0**-121, 2.0**-110])
+def test_sparse_call_smallest_queries(shape, size):
+    """The selecting call with the same queries: the mean of the selected rows, not NaN."""
+    c = ops._chunk_case(*shape, [300, 130], [2, 1], 64, seed=3)
+    c["q"][0] = 0
+    c["q"][0, :, 0] = size
+    want = ops._chunk_ref(c)
+    g = ops._cuda(c)
+    idx = np.where(np.arange(300)[None, :] <= c["pos"].numpy()[:, None], np.arange(300)[None, :], -1).astype(np.int32)
+    for splits in (1, 2):
+        st = torch.zeros(1, dtype=I32, device="cuda")
+        r = dsa.sparse_mla_fwd(g["q"], g["kv"], g["sc"], g["table"], g["req"], torch.from_numpy(idx).cuda(),
+                               d_latent=shape[1], d_rope=shape[2], page_size=64, softmax_scale=c["scale"],
+                               num_splits=splits, dev_status=st)
+        out, lse = r if splits == 1 else dsa.combine(*r)
+        assert int(st) == 0
+        ops._check_chunk(out, lse, want)
 
 
 # ---- verify_draft and whole steps ----------------------------------------------------
