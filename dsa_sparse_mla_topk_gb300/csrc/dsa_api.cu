@@ -106,7 +106,7 @@ int32_t chunk_splits(int32_t num_q, int32_t num_live, int32_t num_heads, int32_t
   // Clusters of S CTAs that run at once, one CTA per SM, of 152 SMs
   // (cudaOccupancyMaxActiveClusters).
   static const int32_t clusters[9] = {0, 152, 76, 46, 36, 28, 23, 15, 15};
-  // (64, 512, 64), in hundredths of a tile's time (measured: 0.93 us): a CTA's start
+  // (64, 512, 64), in hundredths of a tile's time (measured: 0.87 us): a CTA's start
   // and end; the merge in a cluster; the Combine, whose partials grow with tokens and
   // splits (1 x 64: 18 us, 24 x 12: 17).  Where the live rows are not known (a batch of
   // fixed capacity, as of a captured step or a verify block whose requests drafted

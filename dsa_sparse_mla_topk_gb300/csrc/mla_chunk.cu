@@ -14,10 +14,11 @@
 // MMAs, and takes about 1,900: the P V of a tile needs its weights, and those its
 // QK^T, so the softmax's latency is hidden by two tiles only, and a long call
 // runs at the power limit.  Measured, pages of 64: 1,024 tokens at the end of 16,384
-// positions in 1.48 ms (1,530 TFLOP/s of the formula's bf16 products, the
+// positions in 1.48 ms (1,525 TFLOP/s of the formula's bf16 products, the
 // weights' second half not counted); 128 tokens of 16 requests, 4,096 positions
-// each, 77 us in the two splits that the rule takes; 32 requests of 4,096 to 8,192
-// positions 40.4 us in four (118 MB of rows, 2.9 TB/s).  Warps:
+// each, 62 us in one split and 77 in the two that the rule takes where it does not
+// know that all are live; 32 requests of 4,096 to 8,192 positions 40.4 us in four
+// (118 MB of rows, 2.9 TB/s).  Warps:
 //  * 3 (or 7) TMA warps bring KV tiles of 64 rows, FP8 as they are in the cache, five
 //    tiles in flight.  A tile whose positions are all visible comes in boxes
 //    of 64, 32, 16 or 8 rows, the largest that divides the page size (5 to
@@ -33,23 +34,23 @@
 //    Q_hi rows in lanes 0-15 and Q_lo rows in lanes 16-31.  A thread owns one
 //    head and 8 rows of the tile; two 16-lane loads, whose half-warps take
 //    different columns, bring it both halves of its logits.
-// Q = Q_hi + Q_lo: two E4M3 numbers of a head scaled by a power of two, exact for bf16
-// values down to 2^-9 of the head's largest, below that to 2^-17 of it (E4M3's
-// steps end: 0.4% of a Gaussian head).  A weight P' = p s_j F is E4M3 + E5M2.  p = 2^(z - m) with
-// a reference m for each head, and F, also the head's, puts the largest p s_j at 16:
-// what counts is how much a row adds, not its scale alone, so one row of a
-// huge scale and no weight takes no bits from the others (with one F for the largest scale
-// 2^14 times the others': 5% off, 2^22: nothing left).  16 is an exact value: a head
-// that looks at one row gives that row.  Weights down to 2^-10 of the largest have a
-// relative error of at most 2^-8 (0.13% root mean square, a bf16 weight's is 0.08%);
-// smaller ones an absolute one of 2^-14 at 16, and only below 2^-21 of the largest nothing
-// is left of them.  A second E4M3 number would end at 2^-14: over a long context the
-// many small weights of a flat tail are a share of the result that must not
-// be rounded away.
+// Q = Q_hi + Q_lo: two E4M3 numbers of a head scaled by a power of two, exact for
+// bf16 values down to 2^-9 of the head's largest, below that to 2^-17 of it (E4M3's
+// steps end: 0.4% of a Gaussian head).
+// A weight P' = p s_j F is E4M3 + E5M2.  p = 2^(z - m) with a reference m for each
+// head, and F, also the head's, puts the largest p s_j at 16: what counts is how much
+// a row adds, not its scale alone, so one row of a huge scale and no weight takes no
+// bits from the others (with one F for the largest scale, 2^14 times the others': 5%
+// off, 2^22: nothing left).  16 is an exact value: a head that looks at one row
+// gives that row.  Weights down to 2^-10 of the largest have a relative error of at
+// most 2^-8 (0.13% root mean square, a bf16 weight's is 0.08%); smaller ones an
+// absolute one of 2^-14 (of 16), and only below 2^-21 of the largest nothing is left
+// of them.  A second E4M3 number would end at 2^-14: over a long context the many
+// small weights of a flat tail are a share of the result that must not be rounded away.
 // Lazy rescaling: m and F move when a weight nears 448, the largest E4M3 value; l is
 // summed in fp32 from unrounded p.  (Of 64 heads some weight passes a bound in few
-// tiles; with a bound 2^2 above, 152 tokens of 4,096 took 92 instead of 72 us.)  All
-// waits are bounded.
+// tiles; with a bound 2^2 above 16, 152 tokens of 4,096 take 82 instead of 62 us.)
+// All waits are bounded.
 #include <cooperative_groups.h>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -805,10 +806,10 @@ cudaError_t launch_chunk_tc(const MlaArgs& a, const int32_t* q_pos, bool merge, 
       !make_kv_map(&maps.rope_row, a, DQK, DR, 1, CU_TENSOR_MAP_SWIZZLE_64B))
     return cudaErrorInvalidValue;
   // Three TMA warps keep up with boxes of 16 rows or more, 5 to 20 copies a tile
-  // (1,024 tokens of 16,384: 1.57 ms at page size 64, 1.69 at 16; with seven 1.68 and
-  // 1.70: more warps that look tiles up, and the power limit); smaller boxes and
-  // gathers need seven (page size 24: 1.82 against 1.97 ms; 152 tokens of 16,384
-  // at page size 4: 360 against 449 us).
+  // (1,024 tokens of 16,384: 1.48 ms at page size 64, 1.64 at 16; with seven 1.75 and
+  // 1.75: more warps that look tiles up, and the power limit); smaller boxes and
+  // gathers need seven (page size 24: 1.78 against 1.97 ms; 152 tokens of 16,384
+  // at page size 4: 343 against 454 us).
   auto launch = [&](auto kern, int ntma) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
     if (e != cudaSuccess) return e;

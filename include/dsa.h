@@ -161,6 +161,10 @@ DSA_API size_t dsa_topk_workspace_size(int32_t num_q, int64_t ld_scores, int32_t
  * DSA_ERR_WORKSPACE_TOO_SMALL; a pool of 2^31 or more token slots returns
  * DSA_ERR_UNSUPPORTED_SHAPE; page ids or indices out of range set
  * DSA_DEV_BAD_INDEX / DSA_DEV_BAD_PAGE and that row is skipped.
+ * Precision, 64 heads: a weight (softmax times kv_scale) carries bits down to 2^-14 of
+ * the largest kv_scale among the token's selected rows, whatever that row
+ * weighs: rows whose scales are 2^6 below it lose about 2%, 2^10 14%
+ * (dsa_chunk_mla_fwd goes by what rows weigh).  The 16-head kernel is fp32.
  */
 DSA_API dsa_status dsa_sparse_mla_fwd(const void* q, const uint8_t* kv, const float* kv_scale, int64_t num_pages,
                                       const int32_t* block_table, int32_t num_req, int32_t bt_stride,
@@ -341,7 +345,12 @@ DSA_API dsa_status dsa_kv_write(const void* rows, int32_t n, int32_t d_qk, const
  *   ctx_len, new_len, pages_held  int32 [num_req].
  *   block_table    int32 [num_req, bt_stride] page ids, updated in place.
  *   free_pages     int32 [num_free] page ids; free_used int32 [1]: how many of
- *                  them earlier calls have taken.
+ *                  them earlier calls have taken.  The pages have to be the list's
+ *                  own: none that dsa_prefix_cache_* hands out (a cache of fewer
+ *                  pages than the pool, the ids from there on in the list).  A
+ *                  finished request's n pages come back by writing them over the last
+ *                  taken entries, free_pages[*free_used - n ..], and lowering
+ *                  *free_used by n, on the same stream between two calls.
  *   num_req        at most 8,192, capacity at most 2^30 (else UNSUPPORTED_SHAPE).
  * Data errors leave a request as it is (ctx_out = ctx_len, held_out =
  * pages_held, no pages taken, -1 for its tokens, which stay in cu_q: the
@@ -438,8 +447,8 @@ DSA_API dsa_status dsa_qk_norm_rope(const void* q, int64_t q_tok_stride, int64_t
  * 2^-17 of the head's largest value are lost; a row's weight, softmax times
  * kv_scale, has a relative error of at most 2^-8 (0.13% root mean square) down to
  * 2^-10 of the head's largest weight, and one of 2^-18 of that below.
- * Scales count in this from 2^-60 on.  16 heads: 2^-11, down to 2^-25 of the
- * largest kv_scale that the token sees.
+ * Scales are from 2^-60 (smaller ones lose bits) to 2^50.  16 heads: 2^-11, down
+ * to 2^-25 of the largest kv_scale that the token sees.
  * Data errors: q_pos < -1 or past the block table row sets DSA_DEV_BAD_QPOS
  * and the token sees nothing; q_req outside [-1, num_req) or a page id out of
  * range sets DSA_DEV_BAD_PAGE; such rows are skipped.

@@ -73,6 +73,29 @@ def test_layout_state_does_not_keep_the_token_arrays():
                 assert v.is_contiguous() and np.array_equal(ops.host(v), want[k]), k
 
 
+def test_layout_pages_given_back_to_the_list():
+    """A finished request's pages, written over the last taken entries of the list, are the
+    next ones that a request gets, and no page is two requests'."""
+    page, pages = 16, 12
+    free = ops.i32([7, 3, 9, 1, 11, 5])
+    table = torch.full((3, 4), -1, dtype=I32, device="cuda")
+    zero = ops.i32([0, 0, 0])
+    kw = dict(page_size=page, num_pages=pages, capacity=100)
+    a = dsa.batch_layout(zero, ops.i32([20, 40, 0]), zero, table, free, ops.i32([0]), **kw)
+    assert table.tolist() == [[7, 3, -1, -1], [9, 1, 11, -1], [-1] * 4] and a.free_used.tolist() == [5]
+    used = a.free_used.clone()  # request 0 ends
+    free[3:5] = table[0, :2]
+    used -= 2
+    table[0] = -1
+    ctx, held = a.ctx_len.clone(), a.pages_held.clone()
+    ctx[0] = held[0] = 0
+    st = torch.zeros(1, dtype=I32, device="cuda")
+    b = dsa.batch_layout(ctx, ops.i32([0, 0, 33]), held, table, free, used, dev_status=st, **kw)
+    assert table.tolist() == [[-1] * 4, [9, 1, 11, -1], [7, 3, 5, -1]] and int(st) == 0
+    assert b.free_used.tolist() == [6] and b.pages_held.tolist() == [0, 3, 3]
+    assert b.slot.tolist()[:33] == [7 * page + x for x in range(16)] + [3 * page + x for x in range(16)] + [5 * page]
+
+
 # ---- qk_norm_rope ------------------------------------------------------------------
 
 

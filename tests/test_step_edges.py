@@ -76,6 +76,23 @@ def test_outputs_over_any_input_or_each_other(lib):  # noqa: F811
     assert _verify(lib, co=A(6)) == 4  # the lengths in place
 
 
+def _verify_req(lib, **over):  # noqa: F811
+    a = dict(p=A(0), ld=100, rows=8, V=100, q=A(1), ldq=100, tok=A(2), ua=A(3), us=A(4), cu=A(5), req=A(10), R=2, mo=4,
+             ctx=A(6), out=A(7), num=A(8), co=A(9), st=None, s=None)
+    a.update(over)
+    return lib.dsa_verify_draft_req(*a.values())
+
+
+@no_device_only
+def test_verification_with_the_requests_of_its_rows(lib):  # noqa: F811
+    """The checks of dsa_verify_draft, and the rows' requests are an input like any other."""
+    assert _verify_req(lib) == 4 and _verify_req(lib, req=None) == 4 and _verify_req(lib, R=0) == 0
+    for k in ("out", "num", "co"):
+        assert _verify_req(lib, **{k: A(10)}) == 1, k
+        assert _verify_req(lib, **{k: at(A(10), 4 * 8 - 4)}) == 1, k
+    assert _verify_req(lib, rows=-1) == 1 and _verify_req(lib, V=0) == 1 and _verify_req(lib, us=None) == 1
+
+
 def test_split_rule_of_batches_whose_live_tokens_are_known(lib):  # noqa: F811
     """A full batch is not split for the sake of padding that it does not have, and a
     padded one is split like the small batch that it is."""
