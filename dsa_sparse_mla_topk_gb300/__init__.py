@@ -4,8 +4,11 @@ The three calls of the path -- ``topk_select``, ``sparse_mla_fwd`` and
 ``combine`` -- marshal torch tensors (device memory, the current CUDA stream)
 into the C ABI declared in ``include/dsa.h`` and run entirely in the
 library's CUDA kernels.  ``batch_layout``, ``qk_norm_rope``, ``chunk_mla`` and
-``verify_draft`` are the rest of a serving step around them.  There is no CPU or PyTorch fallback: if the library
-is missing, every call raises.
+``verify_draft`` are the rest of a serving step around them; ``absorb_q`` and
+``project_out`` the products before and after attention in the cache's latent
+space, ``expand_kv`` and ``prompt_mla`` the form with every head's own keys and
+values, and ``token_logprobs`` the log probabilities of a step's tokens.  There
+is no CPU or PyTorch fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
@@ -22,6 +25,8 @@ __all__ = ["DsaError", "load_library", "topk_select", "sparse_mla_fwd", "combine
            "topk_sparse_mla_fwd", "two_kernel_path_supported", "sparse_mla_topk_fused", "fused_path_supported",
            "kv_write",
            "PrefixCache", "BatchLayout", "batch_layout", "qk_norm_rope", "chunk_mla_fwd", "chunk_mla", "verify_draft",
+           "absorb_q", "project_out", "ExpandedKV", "expand_kv", "expand_kv_workspace_size", "prompt_mla_fwd", "prompt_mla",
+           "TokenLogprobs", "token_logprobs",
            "kv_tile_count", "kv_tile_size", "pick_num_splits", "pick_chunk_splits", "status_string", "EXPORTED_SYMBOLS",
            "DEV_BAD_QPOS", "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_TIMEOUT", "DEV_NO_PAGES"]
 
@@ -35,7 +40,8 @@ EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_
                     "dsa_sparse_mla_fwd", "dsa_sparse_mla_workspace_size", "dsa_sparse_mla_fwd_noalloc",
                     "dsa_sparse_mla_topk_fwd", "dsa_sparse_mla_topk_max_k", "dsa_topk_sparse_mla_fwd",
                     "dsa_combine", "dsa_kv_write", "dsa_batch_layout", "dsa_qk_norm_rope", "dsa_chunk_mla_fwd",
-                    "dsa_verify_draft", "dsa_verify_draft_req", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
+                    "dsa_verify_draft", "dsa_verify_draft_req", "dsa_absorb_q", "dsa_project_out", "dsa_expand_kv",
+                    "dsa_expand_kv_workspace_size", "dsa_prompt_mla_fwd", "dsa_token_logprobs", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
                     "dsa_prefix_cache_acquire", "dsa_prefix_cache_release", "dsa_prefix_cache_stats",
                     "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits",
                     "dsa_chunk_pick_num_splits", "dsa_chunk_pick_num_splits_live")
@@ -106,6 +112,20 @@ def load_library(path: str | None = None):
         lib.dsa_verify_draft_req.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp,
                                              vp]
         lib.dsa_verify_draft_req.restype = i32
+        lib.dsa_absorb_q.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+        lib.dsa_absorb_q.restype = i32
+        lib.dsa_project_out.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, vp, vp]
+        lib.dsa_project_out.restype = i32
+        lib.dsa_expand_kv.argtypes = [vp, vp, i64, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp,
+                                      vp, sz, vp, vp]
+        lib.dsa_expand_kv.restype = i32
+        lib.dsa_expand_kv_workspace_size.argtypes = [i32, i32]
+        lib.dsa_expand_kv_workspace_size.restype = sz
+        lib.dsa_prompt_mla_fwd.argtypes = [vp, i64, i64, vp, i64, i64, i32, vp, i64, vp, vp, vp, i32, i32, i32, i32, i32,
+                                           i32, f32, i32, vp, vp, vp, vp, vp, vp]
+        lib.dsa_prompt_mla_fwd.restype = i32
+        lib.dsa_token_logprobs.argtypes = [vp, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
+        lib.dsa_token_logprobs.restype = i32
         lib.dsa_prefix_cache_create.argtypes = [i32, i32]
         lib.dsa_prefix_cache_create.restype = vp
         lib.dsa_prefix_cache_destroy.argtypes = [vp]
@@ -972,3 +992,220 @@ def verify_draft(target_probs: torch.Tensor, draft_tokens: torch.Tensor, cu_rows
          draft_tokens.data_ptr(), u_accept.data_ptr(), u_sample.data_ptr(), cu_rows.data_ptr(), _ptr(q_req), R,
          max_out, _ptr(ctx_len), tokens.data_ptr(), num_out.data_ptr(), _ptr(ctx_out), _status_ptr(dev_status, dev))
     return tokens, num_out, ctx_out
+
+
+# ---- latent attention's other form, and the products around both -------------------
+
+
+def _given(t, name: str, dtype, shape: tuple, like, stream):
+    """The caller's contiguous output of this type and shape, or a fresh one."""
+    if t is None:
+        return _empty(shape, dtype, like, stream)
+    _need(t, name, dtype, len(shape), like.get_device())
+    _need_shape(t, name, shape)
+    return t
+
+
+def absorb_q(q: torch.Tensor, w_kv: torch.Tensor, *, d_rope: int, q_out: torch.Tensor | None = None,
+             stream=None) -> torch.Tensor:
+    """Queries in the cache's latent space (dsa_absorb_q): q bf16 [tokens, heads,
+    d_nope + d_rope] (any token and head strides that are multiples of 8) and the
+    up-projection w_kv bf16 [heads, d_nope + d_v, d_latent] of every head's keys
+    and values give bf16 [tokens, heads, d_latent + d_rope], the queries of
+    chunk_mla and sparse_mla_topk; the rotated part stays as it is."""
+    dev = _device_of(q, "q")
+    _need_rows(q, "q", _BF16, 3, dev)
+    _need(w_kv, "w_kv", _BF16, 3, dev)
+    n, H, d = q.shape
+    if w_kv.shape[0] != H:
+        raise ValueError("q and w_kv must have the same heads")
+    _, dw, dl = w_kv.shape
+    q_out = _given(q_out, "q_out", _BF16, (n, H, dl + d_rope), q, stream)
+    ts, hs = _strides(q)
+    _run(dev, stream, "dsa_absorb_q", q.data_ptr(), ts, hs, w_kv.data_ptr(), n, H, d - d_rope, d_rope, dw - (d - d_rope),
+         dl, q_out.data_ptr())
+    return q_out
+
+
+def project_out(o: torch.Tensor, w_kv: torch.Tensor, *, d_nope: int, out: torch.Tensor | None = None,
+                stream=None) -> torch.Tensor:
+    """Attention's latent outputs o bf16 [tokens, heads, d_latent] (strides as for
+    absorb_q) to every head's values, bf16 [tokens, heads, d_v] (dsa_project_out)."""
+    dev = _device_of(o, "o")
+    _need_rows(o, "o", _BF16, 3, dev)
+    _need(w_kv, "w_kv", _BF16, 3, dev)
+    n, H, dl = o.shape
+    if w_kv.shape[0] != H or w_kv.shape[2] != dl:
+        raise ValueError("o and w_kv must have the same heads and latent width")
+    dv = w_kv.shape[1] - d_nope
+    if dv <= 0:
+        raise ValueError("d_nope leaves no values in w_kv")
+    out = _given(out, "out", _BF16, (n, H, dv), o, stream)
+    ts, hs = _strides(o)
+    _run(dev, stream, "dsa_project_out", o.data_ptr(), ts, hs, w_kv.data_ptr(), n, H, d_nope, dv, dl, out.data_ptr())
+    return out
+
+
+class ExpandedKV(NamedTuple):
+    """What expand_kv writes: every head's key and value of each row, kv bf16
+    [capacity, heads, d_nope + d_v]; the rotated part of the keys, which all heads
+    share, k_rope bf16 [capacity, d_rope]; the requests' row ranges cu_k int32
+    [num_req + 1]."""
+    kv: torch.Tensor
+    k_rope: torch.Tensor
+    cu_k: torch.Tensor
+
+
+def expand_kv_workspace_size(capacity: int, d_latent: int) -> int:
+    return int(load_library().dsa_expand_kv_workspace_size(capacity, d_latent))
+
+
+def expand_kv(kv: torch.Tensor, kv_scale: torch.Tensor, block_table: torch.Tensor, ctx_len: torch.Tensor,
+              w_kv: torch.Tensor, *, d_rope: int, page_size: int, capacity: int | None = None,
+              out: ExpandedKV | None = None, workspace: torch.Tensor | None = None, dev_status=None,
+              stream=None) -> ExpandedKV:
+    """Keys and values of every head for the cached rows of each request, packed
+    one request after another (dsa_expand_kv), from the paged FP8 cache and the
+    up-projection w_kv bf16 [heads, d_nope + d_v, d_latent].  ``capacity`` is the
+    number of rows to make room for, or ``out`` (an ExpandedKV) holds them; rows
+    behind the last request are left as they were.  ``workspace`` (uint8,
+    expand_kv_workspace_size bytes) is allocated when none is given."""
+    dev = _device_of(kv, "kv")
+    _need(kv, "kv", _U8, 2, dev)
+    _need(kv_scale, "kv_scale", _F32, 1, dev)
+    _need(block_table, "block_table", _I32, 2, dev)
+    _need(ctx_len, "ctx_len", _I32, 1, dev)
+    _need(w_kv, "w_kv", _BF16, 3, dev)
+    R, (H, dw, dl), slots = ctx_len.shape[0], w_kv.shape, kv.shape[0]
+    if page_size <= 0 or slots % page_size or kv_scale.shape[0] != slots or kv.shape[1] != dl + d_rope:
+        raise ValueError("kv must be whole pages of rows of w_kv's latent width + d_rope, kv_scale one value a row")
+    if block_table.shape[0] != R:
+        raise ValueError("block_table must have a row for every request")
+    if (capacity is None) == (out is None):
+        raise ValueError("give capacity or out")
+    if out is None:
+        if capacity < 0:
+            raise ValueError("capacity must not be negative")
+        out = ExpandedKV(_empty((capacity, H, dw), _BF16, kv, stream), _empty((capacity, d_rope), _BF16, kv, stream),
+                         _empty(R + 1, _I32, kv, stream))
+    else:
+        capacity = out.kv.shape[0]
+        for t, name, dt, shape in zip(out, ExpandedKV._fields, (_BF16, _BF16, _I32),
+                                      ((capacity, H, dw), (capacity, d_rope), (R + 1,))):
+            _given(t, "out." + name, dt, shape, kv, stream)
+    ws = expand_kv_workspace_size(capacity, dl)
+    if workspace is None:
+        workspace = _empty(ws, _U8, kv, stream)
+    else:
+        _need(workspace, "workspace", _U8, 1, dev)
+    _run(dev, stream, "dsa_expand_kv", kv.data_ptr(), kv_scale.data_ptr(), slots // page_size, block_table.data_ptr(), R,
+         block_table.shape[1], ctx_len.data_ptr(), w_kv.data_ptr(), H, dl, d_rope, dw, page_size, capacity,
+         out.kv.data_ptr(), out.k_rope.data_ptr() if d_rope else None, out.cu_k.data_ptr(), workspace.data_ptr(),
+         workspace.numel(), _status_ptr(dev_status, dev))
+    return out
+
+
+def prompt_mla_fwd(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor | None, cu_q: torch.Tensor,
+                   cu_k: torch.Tensor, q_pos: torch.Tensor, *, d_nope: int, softmax_scale: float, num_splits: int = 1,
+                   out=None, lse=None, o_part=None, lse_part=None, dev_status=None, stream=None):
+    """Attention over every head's own keys and values (dsa_prompt_mla_fwd).
+    num_splits == 1: returns (out bf16, lse fp32); else (o_part fp32 [S, ...],
+    lse_part fp32 [S, ...]) for combine."""
+    dev = _device_of(q, "q")
+    _need_rows(q, "q", _BF16, 3, dev)
+    _need_rows(kv, "kv", _BF16, 3, dev)
+    for t, name in ((cu_q, "cu_q"), (cu_k, "cu_k"), (q_pos, "q_pos")):
+        _need(t, name, _I32, 1, dev)
+    (n, H, dqk), N = q.shape, kv.shape[0]
+    dr, dv = dqk - d_nope, kv.shape[2] - d_nope
+    if kv.shape[1] != H or dr < 0 or dv <= 0:
+        raise ValueError("q and kv must have the same heads, with d_nope values of each head's key in front")
+    if dr > 0:
+        _need_rows(k_rope, "k_rope", _BF16, 2, dev)
+        _need_shape(k_rope, "k_rope", (N, dr))
+    if cu_q.shape[0] < 1 or cu_k.shape != cu_q.shape or q_pos.shape[0] != n:
+        raise ValueError("cu_q and cu_k must have one entry more than there are requests, q_pos one for each token")
+    if num_splits == 1:
+        out = _given(out, "out", _BF16, (n, H, dv), q, stream)
+        lse = _given(lse, "lse", _F32, (n, H), q, stream)
+        ptrs = (out.data_ptr(), lse.data_ptr(), None, None)
+    else:
+        o_part = _given(o_part, "o_part", _F32, (num_splits, n, H, dv), q, stream)
+        lse_part = _given(lse_part, "lse_part", _F32, (num_splits, n, H), q, stream)
+        ptrs = (None, None, o_part.data_ptr(), lse_part.data_ptr())
+    (qt, qh), (kt, kh) = _strides(q), _strides(kv)
+    _run(dev, stream, "dsa_prompt_mla_fwd", q.data_ptr(), qt, qh, kv.data_ptr(), kt, kh, N,
+         k_rope.data_ptr() if dr else None, k_rope.stride(0) if dr and N > 1 else 0, cu_q.data_ptr(), cu_k.data_ptr(),
+         q_pos.data_ptr(), cu_q.shape[0] - 1, n, H, d_nope, dr, dv, float(softmax_scale), num_splits, *ptrs,
+         _status_ptr(dev_status, dev))
+    return (out, lse) if num_splits == 1 else (o_part, lse_part)
+
+
+def prompt_mla(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor | None, cu_q: torch.Tensor, cu_k: torch.Tensor,
+               q_pos: torch.Tensor, *, d_nope: int, softmax_scale: float, num_splits: int | None = None,
+               buffers: dict | None = None, dev_status=None, stream=None):
+    """Attention of new tokens q bf16 [tokens, heads, d_nope + d_rope] over every
+    head's own keys and values, kv bf16 [rows, heads, d_nope + d_v] and the shared
+    rotated part k_rope bf16 [rows, d_rope] (expand_kv's, or a prompt's own
+    projections; any strides that are multiples of 8): token t of request r, cu_q[r] <=
+    t < cu_q[r + 1], attends to rows cu_k[r] .. cu_k[r] + q_pos[t].  ``cu_q`` and
+    ``q_pos`` are batch_layout's; padding and q_pos = -1 give 0.  ``buffers``
+    (optional) holds preallocated out / lse / o_part / lse_part tensors.  Returns
+    (out bf16 [tokens, heads, d_v], lse fp32 [tokens, heads])."""
+    b = buffers or {}
+    S = 1 if num_splits is None else num_splits
+    r = prompt_mla_fwd(q, kv, k_rope, cu_q, cu_k, q_pos, d_nope=d_nope, softmax_scale=softmax_scale, num_splits=S,
+                       out=b.get("out") if S == 1 else None, lse=b.get("lse") if S == 1 else None, o_part=b.get("o_part"),
+                       lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)
+    if S == 1:
+        return r
+    n, H, dv = r[0].shape[1:]
+    out = _given(b.get("out"), "out", _BF16, (n, H, dv), q, stream)
+    lse = _given(b.get("lse"), "lse", _F32, (n, H), q, stream)
+    if n:
+        _run(q.get_device(), stream, "dsa_combine", r[0].data_ptr(), r[1].data_ptr(), S, n, H, dv, out.data_ptr(),
+             lse.data_ptr())
+    return out, lse
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs writes: logprob and entropy fp32 [rows], rank int32
+    [rows], and the alternatives top_ids int32 and top_logprobs fp32 [rows, top]."""
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    rank: torch.Tensor
+    top_ids: torch.Tensor
+    top_logprobs: torch.Tensor
+
+
+_LOGIT_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, out: TokenLogprobs | None = None,
+                   dev_status=None, stream=None) -> TokenLogprobs:
+    """Log probabilities of ``tokens`` int32 [rows] (-1: none) under the rows of
+    ``logits`` [rows, vocab] (fp32, bf16 or fp16, any row stride; -inf: masked), with
+    the rows' entropies, the tokens' ranks and the ``top`` most probable
+    alternatives, ties to the lower id (dsa_token_logprobs).  ``out`` (a
+    TokenLogprobs of preallocated tensors) is written when given."""
+    dev = _device_of(logits, "logits")
+    code = _LOGIT_DTYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be float32, bfloat16 or float16, got {logits.dtype}")
+    _need_rows(logits, "logits", logits.dtype, 2, dev)
+    _need(tokens, "tokens", _I32, 1, dev)
+    rows, vocab = logits.shape
+    if tokens.shape[0] != rows:
+        raise ValueError("tokens must have one entry per row")
+    if top < 0:
+        raise ValueError("top must not be negative")
+    ld = logits.stride(0) if rows > 1 else vocab
+    if ld < vocab:
+        raise ValueError("rows of logits must not overlap")
+    shapes = ((rows,), (rows,), (rows,), (rows, top), (rows, top))
+    out = TokenLogprobs(*(_given(t, "out." + name, dt, shape, logits, stream) for t, name, dt, shape in
+                          zip(out or (None,) * 5, TokenLogprobs._fields, (_F32, _F32, _I32, _I32, _F32), shapes)))
+    _run(dev, stream, "dsa_token_logprobs", logits.data_ptr(), ld, rows, vocab, code, tokens.data_ptr(), top,
+         out.logprob.data_ptr(), out.entropy.data_ptr(), out.rank.data_ptr(), out.top_ids.data_ptr() if top else None,
+         out.top_logprobs.data_ptr() if top else None, _status_ptr(dev_status, dev))
+    return out

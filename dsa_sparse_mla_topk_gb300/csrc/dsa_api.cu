@@ -575,3 +575,207 @@ dsa_status dsa_verify_draft(const float* target_probs, int64_t ld_target, int32_
                               u_sample, cu_rows, nullptr, num_req, max_out, ctx_len, tokens, num_out, ctx_out,
                               dev_status, stream);
 }
+
+namespace {
+
+// The head sizes of latent attention's expanded form.
+dsa_status check_latent_dims(int32_t heads, int32_t d_nope, int32_t d_rope, int32_t d_v, int32_t d_latent) {
+  auto ok = [](int32_t d, int32_t lo, int32_t hi) { return d >= lo && d <= hi && d % 16 == 0; };
+  if (heads <= 0) return DSA_ERR_INVALID_ARG;
+  if (heads > 1024 || !ok(d_nope, 16, 128) || !ok(d_v, 16, 128) || !ok(d_rope, 0, 64) || !ok(d_latent, 16, 512))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  return DSA_OK;
+}
+
+// 16-bit rows [n, heads, d] behind strides: 16-byte loads reach every one.
+bool rows_ok(const void* x, int64_t ts, int64_t hs) {
+  return x && aligned16(x) && ts >= 0 && hs >= 0 && ts % 8 == 0 && hs % 8 == 0 && ts < ((int64_t)1 << 36) &&
+         hs < ((int64_t)1 << 36);
+}
+
+dsa_status latent_proj(const void* x, int64_t ts, int64_t hs, const void* w, int32_t n, int32_t heads, int32_t d_nope,
+                       int32_t d_rope, int32_t d_v, int32_t d_latent, void* y, bool absorb, void* stream) {
+  if (n < 0) return DSA_ERR_INVALID_ARG;
+  const dsa_status st = check_latent_dims(heads, d_nope, d_rope, d_v, d_latent);
+  if (st != DSA_OK) return st;
+  if ((int64_t)n * heads > INT32_MAX) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (n == 0) return DSA_OK;
+  if (!rows_ok(x, ts, hs) || !w || !aligned16(w) || !y || !aligned16(y)) return DSA_ERR_INVALID_ARG;
+  const int32_t d_in = absorb ? d_nope + d_rope : d_latent, d_out = absorb ? d_latent + d_rope : d_v;
+  const Span in[2] = {{x, row_span(n, heads, ts, hs, d_in)}, {w, 2 * (int64_t)heads * (d_nope + d_v) * d_latent}};
+  const Span out[1] = {{y, 2 * (int64_t)n * heads * d_out}};
+  if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
+  dsa::LatentProjArgs a;
+  a.x = x;
+  a.tok_stride = ts;
+  a.head_stride = hs;
+  a.w = w;
+  a.y = y;
+  a.num_tokens = n;
+  a.heads = heads;
+  a.d_nope = d_nope;
+  a.d_rope = d_rope;
+  a.d_v = d_v;
+  a.d_latent = d_latent;
+  return from_cuda(absorb ? dsa::launch_absorb_q(a, static_cast<cudaStream_t>(stream))
+                          : dsa::launch_project_out(a, static_cast<cudaStream_t>(stream)));
+}
+
+}  // namespace
+
+dsa_status dsa_absorb_q(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* w_kv,
+                        int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_rope, int32_t d_v,
+                        int32_t d_latent, void* q_out, void* stream) {
+  return latent_proj(q, q_tok_stride, q_head_stride, w_kv, num_tokens, num_heads, d_nope, d_rope, d_v, d_latent, q_out,
+                     true, stream);
+}
+
+dsa_status dsa_project_out(const void* o, int64_t o_tok_stride, int64_t o_head_stride, const void* w_kv,
+                           int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_v, int32_t d_latent,
+                           void* y, void* stream) {
+  return latent_proj(o, o_tok_stride, o_head_stride, w_kv, num_tokens, num_heads, d_nope, 0, d_v, d_latent, y, false,
+                     stream);
+}
+
+size_t dsa_expand_kv_workspace_size(int32_t capacity, int32_t d_latent) {
+  return capacity > 0 && d_latent > 0 ? dsa::expand_kv_workspace_bytes(capacity, d_latent) : 0;
+}
+
+dsa_status dsa_expand_kv(const uint8_t* kv, const float* kv_scale, int64_t num_pages, const int32_t* block_table,
+                         int32_t num_req, int32_t bt_stride, const int32_t* ctx_len, const void* w_kv,
+                         int32_t num_heads, int32_t d_latent, int32_t d_rope, int32_t d_kv, int32_t page_size,
+                         int32_t capacity, void* kv_out, void* k_rope, int32_t* cu_k,
+                         void* workspace, size_t workspace_bytes, int32_t* dev_status, void* stream) {
+  if (num_req <= 0 || bt_stride <= 0 || page_size <= 0 || num_pages <= 0 || capacity < 0) return DSA_ERR_INVALID_ARG;
+  const dsa_status st = check_latent_dims(num_heads, 16, d_rope, 16, d_latent);
+  if (st != DSA_OK) return st;
+  if (d_kv < 32 || d_kv > 256 || d_kv % 16 != 0) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (num_pages > (int64_t)INT32_MAX / page_size || num_req > dsa::batch_layout_max_requests() || capacity > (1 << 30))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (!kv || !aligned16(kv) || !kv_scale || !block_table || !ctx_len || !cu_k) return DSA_ERR_INVALID_ARG;
+  const size_t need = dsa_expand_kv_workspace_size(capacity, d_latent);
+  if (capacity > 0) {
+    if (!w_kv || !aligned16(w_kv) || !kv_out || !aligned16(kv_out) || !aligned16(k_rope) || (d_rope > 0 && !k_rope))
+      return DSA_ERR_INVALID_ARG;
+    if (!workspace || !aligned16(workspace)) return DSA_ERR_INVALID_ARG;
+    if (workspace_bytes < need) return DSA_ERR_WORKSPACE_TOO_SMALL;
+  }
+  const int64_t slots = num_pages * page_size;
+  const Span in[5] = {{kv, slots * (d_latent + d_rope)}, {kv_scale, 4 * slots},
+                      {block_table, 4 * (int64_t)num_req * bt_stride}, {ctx_len, 4 * (int64_t)num_req},
+                      {w_kv, 2 * (int64_t)num_heads * d_kv * d_latent}};
+  const Span out[4] = {{kv_out, 2 * (int64_t)capacity * num_heads * d_kv}, {k_rope, 2 * (int64_t)capacity * d_rope},
+                       {cu_k, 4 * ((int64_t)num_req + 1)}, {workspace, (int64_t)need}};
+  if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
+  dsa::ExpandArgs a;
+  a.kv = kv;
+  a.kv_scale = kv_scale;
+  a.num_pages = num_pages;
+  a.block_table = block_table;
+  a.num_req = num_req;
+  a.bt_stride = bt_stride;
+  a.ctx_len = ctx_len;
+  a.w = w_kv;
+  a.heads = num_heads;
+  a.d_latent = d_latent;
+  a.d_rope = d_rope;
+  a.d_kv = d_kv;
+  a.page_size = page_size;
+  a.capacity = capacity;
+  a.kv_out = kv_out;
+  a.k_rope = k_rope;
+  a.cu_k = cu_k;
+  a.workspace = workspace;
+  a.dev_status = dev_status;
+  return from_cuda(dsa::launch_expand_kv(a, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* kv,
+                              int64_t kv_tok_stride, int64_t kv_head_stride, int32_t num_rows, const void* k_rope,
+                              int64_t rope_stride, const int32_t* cu_q, const int32_t* cu_k, const int32_t* q_pos,
+                              int32_t num_req, int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_rope,
+                              int32_t d_v, float softmax_scale, int32_t num_splits, void* out, float* lse,
+                              float* o_part, float* lse_part, int32_t* dev_status, void* stream) {
+  if (num_tokens < 0 || num_rows < 0 || num_req < 0 || num_splits < 1 || num_splits > 64) return DSA_ERR_INVALID_ARG;
+  if (!isfinite(softmax_scale) || softmax_scale < 0.f) return DSA_ERR_INVALID_ARG;
+  const dsa_status st = check_latent_dims(num_heads, d_nope, d_rope, d_v, 16);
+  if (st != DSA_OK) return st;
+  if (num_req > dsa::batch_layout_max_requests() || num_tokens > (1 << 30) || num_rows > (1 << 30))
+    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (num_tokens == 0) return DSA_OK;
+  if (!rows_ok(q, q_tok_stride, q_head_stride) || !cu_q || !cu_k || !q_pos) return DSA_ERR_INVALID_ARG;
+  if (num_rows > 0) {
+    if (!rows_ok(kv, kv_tok_stride, kv_head_stride)) return DSA_ERR_INVALID_ARG;
+    if (d_rope > 0 && !rows_ok(k_rope, rope_stride, 0)) return DSA_ERR_INVALID_ARG;
+  }
+  const bool whole = num_splits == 1;
+  if (whole ? !out || !aligned16(out) : !o_part || !lse_part || !aligned16(o_part)) return DSA_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)num_tokens * num_heads;
+  const Span in[6] = {{q, row_span(num_tokens, num_heads, q_tok_stride, q_head_stride, d_nope + d_rope)},
+                      {kv, row_span(num_rows, num_heads, kv_tok_stride, kv_head_stride, d_nope + d_v)},
+                      {d_rope > 0 ? k_rope : nullptr, row_span(num_rows, 1, rope_stride, 0, d_rope)},
+                      {cu_q, 4 * ((int64_t)num_req + 1)}, {cu_k, 4 * ((int64_t)num_req + 1)},
+                      {q_pos, 4 * (int64_t)num_tokens}};
+  const Span out_whole[2] = {{out, 2 * rows * d_v}, {lse, 4 * rows}};
+  const Span out_part[2] = {{o_part, 4 * rows * d_v * num_splits}, {lse_part, 4 * rows * num_splits}};
+  if (outputs_overlap(whole ? out_whole : out_part, in)) return DSA_ERR_INVALID_ARG;
+  dsa::PromptArgs a;
+  a.q = q;
+  a.q_tok_stride = q_tok_stride;
+  a.q_head_stride = q_head_stride;
+  a.kv = kv;
+  a.kv_tok_stride = kv_tok_stride;
+  a.kv_head_stride = kv_head_stride;
+  a.k_rope = k_rope;
+  a.rope_stride = rope_stride;
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.q_pos = q_pos;
+  a.num_rows = num_rows;
+  a.num_req = num_req;
+  a.num_tokens = num_tokens;
+  a.heads = num_heads;
+  a.d_nope = d_nope;
+  a.d_rope = d_rope;
+  a.d_v = d_v;
+  a.num_splits = num_splits;
+  a.softmax_scale = softmax_scale;
+  a.out = whole ? out : nullptr;
+  a.lse = whole ? lse : nullptr;
+  a.o_part = o_part;
+  a.lse_part = lse_part;
+  a.dev_status = dev_status;
+  return from_cuda(dsa::launch_prompt_mla(a, static_cast<cudaStream_t>(stream)));
+}
+
+dsa_status dsa_token_logprobs(const void* logits, int64_t ld, int32_t num_rows, int32_t vocab, int32_t dtype,
+                              const int32_t* tokens, int32_t top, float* logprob, float* entropy, int32_t* rank,
+                              int32_t* top_ids, float* top_logprobs, int32_t* dev_status, void* stream) {
+  if (num_rows < 0 || vocab <= 0 || ld < vocab || top < 0) return DSA_ERR_INVALID_ARG;
+  if (dtype != DSA_BF16 && dtype != DSA_FP16 && dtype != DSA_FP32) return DSA_ERR_INVALID_ARG;
+  if (num_rows > (1 << 24) || vocab > (1 << 30) || top > dsa::token_logprobs_max_top()) return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (num_rows == 0) return DSA_OK;
+  if (!logits || !tokens || !logprob || !entropy || !rank) return DSA_ERR_INVALID_ARG;
+  if (top > 0 && (!top_ids || !top_logprobs)) return DSA_ERR_INVALID_ARG;
+  const int64_t size = dtype == DSA_FP32 ? 4 : 2, n4 = 4 * (int64_t)num_rows;
+  if (ld > INT64_MAX / 8 / num_rows || reinterpret_cast<uintptr_t>(logits) % size != 0) return DSA_ERR_INVALID_ARG;
+  const Span in[2] = {{logits, size * ((num_rows - 1) * ld + vocab)}, {tokens, n4}};
+  const Span out[5] = {{logprob, n4}, {entropy, n4}, {rank, n4}, {top > 0 ? top_ids : nullptr, n4 * top},
+                       {top > 0 ? top_logprobs : nullptr, n4 * top}};
+  if (outputs_overlap(out, in)) return DSA_ERR_INVALID_ARG;
+  dsa::LogprobArgs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.num_rows = num_rows;
+  a.vocab = vocab;
+  a.dtype = dtype;
+  a.tokens = tokens;
+  a.top = top;
+  a.logprob = logprob;
+  a.entropy = entropy;
+  a.rank = rank;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.dev_status = dev_status;
+  return from_cuda(dsa::launch_token_logprobs(a, static_cast<cudaStream_t>(stream)));
+}

@@ -152,6 +152,65 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify_draft(const VerifyArgs& a, cudaStream_t stream);
 
+// Latent attention's products around the cache's space (dsa_absorb_q, dsa_project_out).
+struct LatentProjArgs {
+  const void* x;  // bf16 [tokens, heads, d_nope + d_rope or d_latent] through the strides
+  int64_t tok_stride, head_stride;  // elements
+  const void* w;  // bf16 [heads, d_nope + d_v, d_latent]
+  void* y;        // bf16 [tokens, heads, d_latent + d_rope or d_v]
+  int32_t num_tokens, heads, d_nope, d_rope, d_v, d_latent;
+};
+cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream);
+cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream);
+
+// Cached latent rows to every head's keys and values (dsa_expand_kv).
+struct ExpandArgs {
+  const uint8_t* kv;
+  const float* kv_scale;
+  int64_t num_pages;
+  const int32_t* block_table;
+  const int32_t* ctx_len;
+  const void* w;
+  int32_t num_req, bt_stride, heads, d_latent, d_rope, d_kv, page_size, capacity;
+  void *kv_out, *k_rope;
+  int32_t* cu_k;
+  void* workspace;
+  int32_t* dev_status;
+};
+size_t expand_kv_workspace_bytes(int32_t capacity, int32_t d_latent);
+cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream);
+
+// Attention over every head's own keys and values (dsa_prompt_mla_fwd).
+struct PromptArgs {
+  const void* q;  // bf16 [tokens, heads, d_nope + d_rope]
+  int64_t q_tok_stride, q_head_stride;
+  const void* kv;  // bf16 [rows, heads, d_nope + d_v]
+  int64_t kv_tok_stride, kv_head_stride;
+  const void* k_rope;  // bf16 [rows, d_rope]
+  int64_t rope_stride;
+  const int32_t *cu_q, *cu_k, *q_pos;
+  int32_t num_rows, num_req, num_tokens, heads, d_nope, d_rope, d_v, num_splits;
+  float softmax_scale;
+  void* out;
+  float *lse, *o_part, *lse_part;
+  int32_t* dev_status;
+};
+cudaError_t launch_prompt_mla(const PromptArgs& a, cudaStream_t stream);
+
+// Log probabilities, entropy, rank and alternatives of tokens (dsa_token_logprobs).
+struct LogprobArgs {
+  const void* logits;
+  int64_t ld;
+  int32_t num_rows, vocab, dtype, top;
+  const int32_t* tokens;
+  float *logprob, *entropy;
+  int32_t *rank, *top_ids;
+  float* top_logprobs;
+  int32_t* dev_status;
+};
+constexpr int token_logprobs_max_top() { return 64; }
+cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream);
+
 // n / d for 0 <= n < 2^31: with s = ceil(log2 d) and m = ceil(2^(31 + s) / d)
 // (< 2^32 or 2^31), floor(n m / 2^(31 + s)) is exact, as m d - 2^(31 + s) <= 2^s.
 struct FastDiv {

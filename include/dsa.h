@@ -19,6 +19,18 @@
  *   (req, pos) --dsa_chunk_mla_fwd--> (out, lse) over every visible position
  *   probabilities --dsa_verify_draft--> tokens, the next step's lengths
  *
+ * Latent attention's two forms: dsa_chunk_mla_fwd and dsa_sparse_mla_fwd work in the
+ * latent space of the cache (the absorbed form),
+ *
+ *   q --dsa_absorb_q--> latent q --attention--> latent out --dsa_project_out--> out
+ *
+ * and for prompts, where its 3.4 times fewer products pay, the expanded form:
+ *
+ *   cached rows --dsa_expand_kv--> every head's keys and values
+ *   q --dsa_prompt_mla_fwd--> (out, lse)
+ *
+ * dsa_token_logprobs gives the log probabilities of a step's tokens.
+ *
  * Sources (page titles):
  *  [LMSYS]  "Accelerating GLM-5.3-Flash on H200: High-Throughput Disaggregated
  *           Serving": section 1 "Architecture and workloads" (an indexer picks
@@ -88,7 +100,7 @@ DSA_API const char* dsa_status_string(int32_t status);
 
 /* Library ABI version: major * 10000 + minor * 100 + patch (DSA_VERSION of the header
  * that the library was built with). */
-#define DSA_VERSION 201
+#define DSA_VERSION 202
 DSA_API int32_t dsa_version(void);
 
 /*
@@ -523,6 +535,148 @@ DSA_API dsa_status dsa_verify_draft_req(const float* target_probs, int64_t ld_ta
                                         const int32_t* q_req, int32_t num_req, int32_t max_out,
                                         const int32_t* ctx_len, int32_t* tokens, int32_t* num_out, int32_t* ctx_out,
                                         int32_t* dev_status, void* stream);
+
+/*
+ * dsa_absorb_q -- queries into the latent space of the cache: the products before
+ * the attention calls in latent attention's absorbed form.  [vLLM]
+ * "Interpretation": one latent row serves all heads; a head's key is
+ * W_k x of the latent row x, so q . (W_k x) = (W_k^T q) . x.
+ *   q_out[t, h, :d_latent] = sum_{n < d_nope} q[t, h, n] w_kv[h, n, :]
+ *   q_out[t, h, d_latent:] = q[t, h, d_nope:]               (the rotated part, as it is)
+ *
+ *   q         bf16 [num_tokens, num_heads, d_nope + d_rope], addressed by token and head
+ *             strides in elements (multiples of 8; 16-byte aligned base).
+ *   w_kv      bf16 [num_heads, d_nope + d_v, d_latent] contiguous, 16-byte aligned: a
+ *             checkpoint's up-projection of keys and values, as dsa_expand_kv takes it.
+ *   q_out     bf16 [num_tokens, num_heads, d_latent + d_rope] contiguous, 16-byte
+ *             aligned; must not overlap an input (INVALID_ARG).
+ * d_nope and d_v: multiples of 16 from 16 to 128; d_latent: of 16 from 16 to 512;
+ * d_rope: of 16 from 0 to 64; num_heads at most 1,024 (else UNSUPPORTED_SHAPE);
+ * num_tokens times num_heads below 2^31.  Sums are fp32, rounded once.  A row's
+ * result depends on that row alone (padding may hold anything, NaN too).
+ */
+DSA_API dsa_status dsa_absorb_q(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* w_kv,
+                                int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_rope, int32_t d_v,
+                                int32_t d_latent, void* q_out, void* stream);
+
+/*
+ * dsa_project_out -- the attention calls' latent outputs to the heads' values:
+ *   y[t, h, v] = sum_{l < d_latent} o[t, h, l] w_kv[h, d_nope + v, l]      (v < d_v)
+ * o bf16 [num_tokens, num_heads, d_latent] by token and head strides, y bf16
+ * [num_tokens, num_heads, d_v] contiguous; the rest as for dsa_absorb_q.
+ */
+DSA_API dsa_status dsa_project_out(const void* o, int64_t o_tok_stride, int64_t o_head_stride, const void* w_kv,
+                                   int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_v,
+                                   int32_t d_latent, void* y, void* stream);
+
+/*
+ * dsa_expand_kv -- every head's keys and values of the requests' cached rows, for
+ * dsa_prompt_mla_fwd.  With n = cu_k[r] + p for position p < ctx_len[r] of request r,
+ * its cache slot as in dsa_sparse_mla_fwd and x_d = e4m3(kv[slot, d]) * kv_scale[slot]:
+ *   kv_out[n, h, j] = sum_{l < d_latent} w_kv[h, j, l] x_l        (j < d_kv: a head's key, then its value)
+ *   k_rope[n, :]    = x[d_latent:]                              (shared by all heads)
+ *   cu_k            int32 [num_req + 1]: the running sum of ctx_len
+ * The codes enter the products exactly and the scale is applied to the fp32 sum;
+ * each result is rounded once to bf16.
+ *
+ *   kv, kv_scale, block_table, page_size  as for dsa_sparse_mla_fwd (any of the head shapes
+ *             below; a row of d_latent + d_rope bytes).
+ *   ctx_len   int32 [num_req]; num_req at most 8,192 (else UNSUPPORTED_SHAPE).
+ *   w_kv      bf16 [num_heads, d_kv, d_latent], d_kv = d_nope + d_v: a multiple of 16 from 32 to
+ *             256; the other sizes as for dsa_absorb_q.
+ *   kv_out    bf16 [capacity, num_heads, d_kv], k_rope bf16 [capacity, d_rope]
+ *             (NULL allowed when d_rope = 0), both 16-byte aligned; rows from cu_k[num_req]
+ *             on are left as they were.  capacity at most 2^30.  Nothing written
+ *             may overlap an input, the workspace or each other (INVALID_ARG).
+ *   workspace dsa_expand_kv_workspace_size() bytes, 16-byte aligned.
+ * Data errors: a negative length sets DSA_DEV_BAD_QPOS, one past the block table row
+ * DSA_DEV_BAD_INDEX; that request has no rows.  Rows past capacity set
+ * DSA_DEV_BAD_INDEX: cu_k stays at the last request that fits.  A page id out of range
+ * sets DSA_DEV_BAD_PAGE and gives rows of zeros.
+ */
+DSA_API dsa_status dsa_expand_kv(const uint8_t* kv, const float* kv_scale, int64_t num_pages,
+                                 const int32_t* block_table, int32_t num_req, int32_t bt_stride,
+                                 const int32_t* ctx_len, const void* w_kv, int32_t num_heads, int32_t d_latent,
+                                 int32_t d_rope, int32_t d_kv, int32_t page_size, int32_t capacity,
+                                 void* kv_out, void* k_rope, int32_t* cu_k, void* workspace, size_t workspace_bytes,
+                                 int32_t* dev_status, void* stream);
+DSA_API size_t dsa_expand_kv_workspace_size(int32_t capacity, int32_t d_latent);
+
+/*
+ * dsa_prompt_mla_fwd -- attention of new tokens in latent attention's expanded
+ * form: every head has keys and values of its own (dsa_expand_kv's, or a prompt's
+ * own projections).  Token t of request r (cu_q[r] <= t < cu_q[r + 1]) attends to
+ * its request's rows n = cu_k[r] + j for all j <= q_pos[t]:
+ *   z_j = softmax_scale (sum_{d < d_nope} q[t, h, d] kv[n, h, d] + sum_d q[t, h, d_nope + d] k_rope[n, d])
+ *   out[t, h, :] = sum_j softmax(z)_j kv[n, h, d_nope:],   lse[t, h] = ln sum_j exp(z_j)
+ * Any q_pos are allowed: a causal chunk's (dsa_batch_layout's), or the same last
+ * position for all tokens (no mask).
+ *
+ *   q         bf16 [num_tokens, num_heads, d_nope + d_rope] and
+ *   kv        bf16 [num_rows, num_heads, d_nope + d_v], by token and head strides in
+ *             elements (multiples of 8; 16-byte aligned base).
+ *   k_rope    bf16 [num_rows, d_rope], row stride rope_stride (a multiple of 8; 16-byte
+ *             aligned; NULL allowed when d_rope = 0).
+ *   cu_q, cu_k  int32 [num_req + 1] (num_req at most 8,192), not decreasing; dsa_batch_layout's cu_q and
+ *             dsa_expand_kv's cu_k.  cu_q[0] = 0.
+ *   q_pos     int32 [num_tokens].
+ *   num_splits 1..64.  With 1 the call writes out (bf16 [num_tokens, num_heads, d_v],
+ *             16-byte aligned) and lse (fp32 [num_tokens, num_heads], may be NULL).  With S > 1
+ *             a request's rows are cut into S runs of whole tiles and the call writes
+ *             o_part (fp32 [S, num_tokens, num_heads, d_v], 16-byte aligned) and lse_part (fp32
+ *             [S, num_tokens, num_heads]) for dsa_combine.
+ * The head sizes are those of dsa_absorb_q; num_tokens, num_rows at most 2^30.
+ * What is written must not overlap an input or each other (INVALID_ARG);
+ * softmax_scale is finite and not negative.
+ * A token with q_pos = -1, and padding (t >= cu_q[num_req]), sees nothing: out = 0 and
+ * lse = -inf.  What no token of a request sees is not looked at; a row that a token does not
+ * see does not reach its result, whatever it holds.  NaN in a query or a visible key gives
+ * NaN in out and lse of that head, NaN or an infinity in a visible value NaN or an infinity in out.
+ * Precision: logits, sums and out are fp32, a weight is rounded to bf16 (2^-9 of it).
+ * Data errors: cu_q decreasing or past num_tokens sets DSA_DEV_BAD_INDEX and such a
+ * request's tokens are left as they are; cu_k decreasing or past num_rows sets it and
+ * the request's tokens see nothing; q_pos outside [-1, cu_k[r + 1] - cu_k[r]) sets
+ * DSA_DEV_BAD_QPOS and that token sees nothing.
+ */
+DSA_API dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* kv,
+                                      int64_t kv_tok_stride, int64_t kv_head_stride, int32_t num_rows,
+                                      const void* k_rope, int64_t rope_stride, const int32_t* cu_q,
+                                      const int32_t* cu_k, const int32_t* q_pos, int32_t num_req, int32_t num_tokens,
+                                      int32_t num_heads, int32_t d_nope, int32_t d_rope, int32_t d_v,
+                                      float softmax_scale, int32_t num_splits, void* out, float* lse, float* o_part,
+                                      float* lse_part, int32_t* dev_status, void* stream);
+
+/*
+ * dsa_token_logprobs -- log probabilities of given tokens, with the entropy and the
+ * most probable alternatives.  [LMSYS] section 3: a verify step's rows of the
+ * target; what a server returns beside the tokens that dsa_verify_draft took.
+ *
+ * Row i of logits z, with lse = ln sum_j exp(z_j) and p_j = exp(z_j - lse):
+ *   logprob[i]  = z_t - lse for the token t = tokens[i]
+ *   entropy[i]  = -sum_j p_j ln p_j                     (natural logarithms)
+ *   rank[i]     = how many columns come before t by (value descending, column ascending)
+ *   top_ids[i]  = the first `top` columns in that order, top_logprobs[i] = z - lse of them
+ * A column of -inf is masked: p = 0, and never an alternative (top_ids -1 and
+ * top_logprobs -inf where fewer are left).  A row with nothing left has logprob
+ * -inf and entropy 0; a masked token's logprob is -inf.
+ *
+ *   logits    [num_rows, vocab] of `dtype` (DSA_BF16, DSA_FP16, DSA_FP32), row stride
+ *             ld >= vocab, aligned to its type.  Its values are taken as they are.
+ *   tokens    int32 [num_rows]; -1: no token (logprob -inf, rank -1).
+ *   top       0..64 (else UNSUPPORTED_SHAPE); 0: top_ids, top_logprobs may be NULL.
+ *   logprob, entropy  fp32 [num_rows]; rank int32 [num_rows]; top_ids int32 and
+ *             top_logprobs fp32 [num_rows, top].  They must not overlap an input or each
+ *             other (INVALID_ARG).
+ * num_rows at most 2^24, vocab at most 2^30 (else UNSUPPORTED_SHAPE).  Sums are fp32
+ * without the largest term, so that a sure token's small logarithm keeps its bits.
+ * Results do not depend on the launch's other rows.  A row with NaN or +inf has NaN in
+ * logprob, entropy and top_logprobs, and some rank and columns in range.  A token outside
+ * [-1, vocab) sets DSA_DEV_BAD_INDEX and counts as -1.
+ */
+#define DSA_FP32 2
+DSA_API dsa_status dsa_token_logprobs(const void* logits, int64_t ld, int32_t num_rows, int32_t vocab, int32_t dtype,
+                                      const int32_t* tokens, int32_t top, float* logprob, float* entropy, int32_t* rank,
+                                      int32_t* top_ids, float* top_logprobs, int32_t* dev_status, void* stream);
 
 /*
  * KV-only prefix-sharing page allocator (host side, no GPU involved).
