@@ -6,7 +6,17 @@
 //   project:  y[t, h, :] = x[t, h, :dl] W_v[h]^T,      W_v[h] = w[h, dn:, :]   [dv, dl]
 //   expand:   y[n, (h, j)] = s_n (code[n, :] . w[h, j, :])
 //
-// One product C = s A B per group (a head), 64 x 64 outputs a CTA on the CUDA cores.
+// All three are C = s A B with bf16 factors and fp32 sums, 128 rows of A a tile
+// (tcgen05 + TMEM + TMA), by persistent CTAs.  A unit is a head's columns (absorb: up to 512,
+// project: up to 128) or 128 of expand's; its B, at most 128 KB, stays in shared
+// memory while the CTA goes through tiles of rows, whose A comes in 64-column chunks.
+// The (unit, tile) pairs are dealt in contiguous runs, one a CTA, equal to one tile.
+// Results go through shared memory and TMA stores of 32 rows x 64 columns, while the next
+// tile's products run into the other half of TMEM.
+// absorb and project read and write more than they compute (85 and 102 flop a byte);
+// expand is bound by the tensor cores (512).  Warps: 0-3 results, 4 TMA, 5 MMA,
+// 6 the rotated part of the queries, which is copied.  All waits are bounded.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -14,77 +24,289 @@
 #include <stdint.h>
 
 #include "internal.cuh"
+#include "mla_tc_common.cuh"
+#include "sm100_ptx.cuh"
 
 namespace dsa {
 namespace {
 
+using namespace sm100;
+
+enum Mode { ABSORB, PROJECT, EXPAND };
+
+constexpr int TM = 128, CHUNK = TM * 128;  // rows of a tile; a chunk of A: 128 rows x 64 columns
+constexpr int SLOTS = 4;                   // chunks of A in flight (absorb: one less, the rotated part's place)
+constexpr int N_MMA = 256;                 // columns of one accumulator; two of them
+constexpr int THREADS = 224, WARP_TMA = 4, WARP_MMA = 5, WARP_ROPE = 6;
+constexpr int B_BYTES = 128 * 1024, STAGE = 32 * 128;  // a warp's 32 rows x 64 columns of results
+constexpr int OFF_B = 0;
+constexpr int OFF_A = OFF_B + B_BYTES;
+constexpr int OFF_OUT = OFF_A + SLOTS * CHUNK;    // [4 warps][2]
+constexpr int OFF_BAR = OFF_OUT + 4 * 2 * STAGE;
+constexpr int B_AF = 0;             // [SLOTS] a chunk of A has landed
+constexpr int B_AE = B_AF + SLOTS;  // [SLOTS] its slot is free
+constexpr int B_BF = B_AE + SLOTS;  // B of the unit has landed
+constexpr int B_BE = B_BF + 1;      // its products are done
+constexpr int B_DF = B_BE + 1;      // [2] an accumulator is complete
+constexpr int B_DE = B_DF + 2;      // [2] it has been read
+constexpr int B_RF = B_DE + 2;      // the rotated part has landed
+constexpr int NBAR = B_RF + 1;
+constexpr int OFF_TMEM = OFF_BAR + NBAR * 8;
+constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;  // with alignment slack
+static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+
+struct ProductMaps {
+  CUtensorMap a, b, c, c_rope;
+};
 struct Product {
-  const __nv_bfloat16* a;  // [m, k]: row stride lda, group stride ga
-  int64_t lda, ga;
-  const __nv_bfloat16* b;  // b_k_major: [n, k], else [k, n]; row stride ldb, group stride gb
-  int64_t ldb, gb;
-  __nv_bfloat16* c;  // [m, n]
-  int64_t ldc, gc;
-  const float* scale;  // [m], or null
-  const int32_t* rows;  // where m stands on the device, or null
-  int32_t m, n, k;
+  int m, n, k;             // rows; columns of a head (expand: of all); the sum's length
+  int n_unit, per_group;   // columns of a unit, units of a head (expand: of all)
+  int units;
+  int b_row0, b_group;     // B's first row, and rows from head to head
+  int rope_x;              // absorb: the rotated part's column in A, -1: none
+  const int32_t* rows;     // expand: the rows there are, on the device
+  const float* scale;      // expand: [m]
+  __nv_bfloat16* out;      // expand: [m, n]
+  int32_t* dev_status;
 };
 
-template <bool B_K_MAJOR>
-__global__ void __launch_bounds__(256) product_kernel(const Product p) {
-  constexpr int TM = 64, TN = 64, TK = 16;
-  __shared__ float as[TK][TM + 4], bs[TK][TN + 4];
-  const int m_all = p.rows ? min(*p.rows, p.m) : p.m;
-  const int m0 = blockIdx.x * TM, n0 = blockIdx.y * TN;
-  if (m0 >= m_all) return;
-  const __nv_bfloat16* a = p.a + blockIdx.z * p.ga;
-  const __nv_bfloat16* b = p.b + blockIdx.z * p.gb;
-  const int tid = threadIdx.x, tm = tid / 16 * 4, tn = tid % 16 * 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < p.k; k0 += TK) {
-    for (int e = tid; e < TM * TK; e += 256) {
-      const int m = e / TK, k = e % TK;
-      as[k][m] = m0 + m < m_all ? __bfloat162float(a[(m0 + m) * p.lda + k0 + k]) : 0.f;
-    }
-    for (int e = tid; e < TN * TK; e += 256) {
-      const int n = B_K_MAJOR ? e / TK : e % TN, k = B_K_MAJOR ? e % TK : e / TN;
-      bs[k][n] = n0 + n < p.n ? __bfloat162float(b[B_K_MAJOR ? (n0 + n) * p.ldb + k0 + k : (k0 + k) * p.ldb + n0 + n]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < TK; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] += as[k][tm + i] * bs[k][tn + j];
-    __syncthreads();
+template <Mode MODE>
+__global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, const __grid_constant__ ProductMaps maps) {
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
+  auto bar = [&](int b) { return smem_u32(bars + b); };
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  constexpr int NSLOT = MODE == ABSORB ? SLOTS - 1 : SLOTS;
+
+  if (warp == WARP_MMA) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
   }
-  for (int i = 0; i < 4; ++i) {
-    const int m = m0 + tm + i;
-    if (m >= m_all) break;
-    const float s = p.scale ? p.scale[m] : 1.f;
-    for (int j = 0; j < 4; ++j)
-      if (n0 + tn + j < p.n) p.c[blockIdx.z * p.gc + m * p.ldc + n0 + tn + j] = __float2bfloat16_rn(acc[i][j] * s);
+  if (tid == WARP_TMA * 32) {
+    for (int b = 0; b < NBAR; ++b) mbar_init(bar(b), b >= B_DE && b < B_DE + 2 ? 4u : 1u);
+    fence_mbarrier_init();
+    tma_prefetch_map(&maps.a);
+    tma_prefetch_map(&maps.b);
+    tma_prefetch_map(&maps.c);
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  int m_all = p.m;
+  if constexpr (MODE == EXPAND) m_all = min(max(__ldg(p.rows), 0), p.m);
+  const int mt = (m_all + TM - 1) / TM;
+  const int64_t tiles = (int64_t)p.units * mt;
+  const int t0 = (int)(tiles * blockIdx.x / gridDim.x), t1 = (int)(tiles * (blockIdx.x + 1) / gridDim.x);
+  const int nkc = (p.k + 63) / 64;
+  // unit u: head (expand: 0) and the first of its columns there
+  auto group_of = [&](int u) { return MODE == EXPAND ? 0 : u / p.per_group; };
+  auto col_of = [&](int u) { return (u % p.per_group) * p.n_unit; };
+  auto cols_of = [&](int u) { return min(p.n_unit, p.n - col_of(u)); };
+  bool ok = true;
+
+  if (warp == WARP_TMA) {
+    if (lane == 0) {
+      int slot = 0, phase = 0, unit = -1, loads = 0;
+      for (int t = t0; t < t1 && ok; ++t) {
+        const int u = t / mt, m0 = (t - u * mt) * TM, g = group_of(u);
+        if (u != unit) {
+          if (unit >= 0 && !mbar_wait(bar(B_BE), (loads - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          unit = u;
+          const int n0 = col_of(u), nb = cols_of(u);
+          const uint32_t b = smem_u32(smem + OFF_B);
+          if (MODE == ABSORB) {  // slices of 64 columns, k rows each
+            const int slices = (nb + 63) / 64;
+            mbar_arrive_expect_tx(bar(B_BF), slices * p.k * 128);
+            for (int s = 0; s < slices; ++s)
+              tma_load_3d(b + s * p.k * 128, &maps.b, n0 + 64 * s, 0, p.b_row0 + g * p.b_group, bar(B_BF));
+          } else {  // 64 columns of k at a time, n_unit rows each
+            mbar_arrive_expect_tx(bar(B_BF), nkc * p.n_unit * 128);
+            for (int c = 0; c < nkc; ++c)
+              tma_load_3d(b + c * p.n_unit * 128, &maps.b, 64 * c, 0, p.b_row0 + g * p.b_group + n0, bar(B_BF));
+          }
+          ++loads;
+        }
+        for (int c = 0; c < nkc; ++c) {
+          if (!mbar_wait(bar(B_AE + slot), phase ^ 1)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(bar(B_AF + slot), CHUNK);
+          tma_load_3d(smem_u32(smem + OFF_A + slot * CHUNK), &maps.a, 64 * c, g, m0, bar(B_AF + slot));
+          if (++slot == NSLOT) slot = 0, phase ^= 1;
+        }
+      }
+      if (!ok) {  // no copy may land after the CTA is gone
+        if (loads) mbar_wait(bar(B_BF), (loads - 1) & 1);
+        for (int s = 0; s < NSLOT; ++s) mbar_wait(bar(B_AF + s), s < slot ? phase : phase ^ 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == WARP_MMA) {
+    auto wait_u = [&](int b, uint32_t parity) { return __reduce_min_sync(0xffffffffu, (uint32_t)mbar_wait(bar(b), parity)); };
+    const uint64_t a_desc = smem_desc(smem_u32(smem + OFF_A), 16, 1024, SWIZZLE_128B);
+    // absorb's B has its columns contiguous: from one 64-column slice to the next k rows of 128 bytes
+    const uint64_t b_desc = smem_desc(smem_u32(smem + OFF_B), MODE == ABSORB ? p.k * 128 : 16, 1024, SWIZZLE_128B);
+    uint32_t good = __reduce_min_sync(0xffffffffu, (uint32_t)(tmem == 0));
+    const int ut0 = __reduce_min_sync(0xffffffffu, (uint32_t)t0), ut1 = __reduce_min_sync(0xffffffffu, (uint32_t)t1);
+    int slot = 0, phase = 0, unit = -1, loads = 0, d = 0;  // d: accumulators filled so far
+    for (int t = ut0; t < ut1 && good; ++t) {
+      const int u = t / mt, nb = cols_of(u);
+      if (u != unit) {
+        if (unit >= 0) mma_commit_warp(bar(B_BE));
+        unit = u;
+        good = wait_u(B_BF, loads & 1);
+        ++loads;
+      }
+      const int subs = MODE == ABSORB ? (nb + N_MMA - 1) / N_MMA : 1;
+      int s = slot, ph = phase;
+      for (int j = 0; j < subs && good; ++j, ++d) {
+        good = wait_u(B_DE + (d & 1), ((d >> 1) & 1) ^ 1);
+        tc_fence_after_sync();
+        const uint32_t idesc = idesc_f16_f32(TM, min(N_MMA, nb - j * N_MMA), 0, MODE == ABSORB ? 1 : 0, 1);
+        s = slot, ph = phase;
+        for (int c = 0; c < nkc && good; ++c) {
+          if (j == 0) {
+            good = wait_u(B_AF + s, ph);
+            tc_fence_after_sync();
+          }
+          const uint64_t ad = a_desc + (uint32_t)(s * (CHUNK >> 4));
+          // 16 of k: 32 bytes along a row, or 16 rows of 128 bytes
+          const uint64_t bd = MODE == ABSORB ? b_desc + (uint32_t)(j * (N_MMA / 64) * p.k * 8 + c * 64 * 8)
+                                             : b_desc + (uint32_t)(c * p.n_unit * 8);
+          const int steps = min(4, (p.k - 64 * c) / 16);
+          if (good) {
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < steps)
+                mma_f16_ss_warp(N_MMA * (d & 1), ad + 2 * kk, bd + (MODE == ABSORB ? 128 : 2) * kk, idesc, c | kk ? 1u : 0u);
+            if (j == subs - 1) mma_commit_warp(bar(B_AE + s));
+          }
+          if (++s == NSLOT) s = 0, ph ^= 1;
+        }
+        if (good) mma_commit_warp(bar(B_DF + (d & 1)));
+      }
+      slot = s, phase = ph;
+    }
+    if (!good) ok = false;
+  } else if (warp == WARP_ROPE) {
+    if (MODE == ABSORB && p.rope_x >= 0 && lane == 0) {
+      const uint32_t buf = smem_u32(smem + OFF_A + NSLOT * CHUNK);
+      int done = 0;
+      for (int t = t0; t < t1; ++t) {
+        const int u = t / mt, m0 = (t - u * mt) * TM, g = group_of(u);
+        if (col_of(u) != 0) continue;  // one of the head's units does it
+        mbar_arrive_expect_tx(bar(B_RF), CHUNK);
+        tma_load_3d(buf, &maps.a, p.rope_x, g, m0, bar(B_RF));
+        if (!mbar_wait(bar(B_RF), done & 1)) {
+          ok = false;
+          break;
+        }
+        ++done;
+        for (int i = 0; i < 4 && m0 + 32 * i < m_all; ++i) tma_store_3d(&maps.c_rope, buf + i * STAGE, 0, g, m0 + 32 * i);
+        tma_store_commit();
+        tma_store_wait_read<0>();
+      }
+      tma_store_wait_all();
+    }
+    __syncwarp();
+  } else {
+    // ---------------- results: warp w has rows 32 w .. + 31 of a tile, one a lane ----------------
+    const uint32_t buf = smem_u32(smem + OFF_OUT + warp * 2 * STAGE);
+    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+    int d = 0, out = 0;
+    for (int t = t0; t < t1 && ok; ++t) {
+      const int u = t / mt, m0 = (t - u * mt) * TM + 32 * warp, g = group_of(u), n0 = col_of(u), nb = cols_of(u);
+      float scale = 1.f;
+      if constexpr (MODE == EXPAND) scale = m0 + lane < m_all ? __ldg(p.scale + m0 + lane) : 0.f;
+      for (int j = 0; j < nb; j += N_MMA, ++d) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_DF + (d & 1)), (d >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const int width = min(N_MMA, nb - j);
+        for (int c = 0; c < width; c += 64) {
+          float x[64];
+          tmem_ld32(N_MMA * (d & 1) + c + lanes, *reinterpret_cast<float(*)[32]>(x));
+          if (c + 32 < width) tmem_ld32(N_MMA * (d & 1) + c + 32 + lanes, *reinterpret_cast<float(*)[32]>(x + 32));
+          tmem_wait_ld();
+          if (c + 64 >= width) {  // the accumulator has been read
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_DE + (d & 1)));
+          }
+          __align__(16) uint32_t y[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const __nv_bfloat162 v = MODE == EXPAND ? __floats2bfloat162_rn(x[2 * e] * scale, x[2 * e + 1] * scale)
+                                                    : __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
+            y[e] = *reinterpret_cast<const uint32_t*>(&v);
+          }
+          if (MODE == EXPAND && m0 + 32 > m_all) {
+            // rows behind the last one stay as they were: no box of 32 rows
+            if (m0 + lane < m_all) {
+              __nv_bfloat16* dst = p.out + (int64_t)(m0 + lane) * p.n + n0 + j + c;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (n0 + j + c + 8 * e < p.n && c + 8 * e < width)
+                  *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+            }
+            continue;
+          }
+          if (m0 >= m_all) continue;
+          const uint32_t to = buf + (out & 1) * STAGE;
+          if (lane == 0) tma_store_wait_read<1>();  // the store before the last has left this buffer
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + lane * 128 + ((e ^ (lane & 7)) << 4)),
+                         "r"(y[4 * e]), "r"(y[4 * e + 1]), "r"(y[4 * e + 2]), "r"(y[4 * e + 3])
+                         : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&maps.c, to, n0 + j + c, g, m0);
+            tma_store_commit();
+          }
+          ++out;
+        }
+      }
+    }
+    if (lane == 0) tma_store_wait_all();
+    __syncwarp();
+  }
+  if (!ok && lane == 0) report(p.dev_status, DSA_DEV_TIMEOUT);
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == WARP_MMA) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
   }
 }
 
-// The rotated part of the queries, as it is: 16 bytes a thread.
-__global__ void __launch_bounds__(256) copy_rope_kernel(const LatentProjArgs a) {
-  const int per = a.d_rope / 8;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x, row = e / per;
-  if (row >= (int64_t)a.num_tokens * a.heads) return;
-  const int64_t t = row / a.heads, h = row % a.heads;
-  const int c = (int)(e % per) * 8;
-  const uint4 v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.x) + t * a.tok_stride +
-                                                  h * a.head_stride + a.d_nope + c);
-  *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + row * (a.d_latent + a.d_rope) + a.d_latent + c) = v;
-}
-
-cudaError_t launch_product(const Product& p, bool b_k_major, int groups, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.m + 63) / 64), (unsigned)((p.n + 63) / 64), (unsigned)groups);
-  if (b_k_major) product_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else product_kernel<false><<<grid, 256, 0, stream>>>(p);
+template <Mode MODE>
+cudaError_t launch_product(const Product& p, const ProductMaps& maps, cudaStream_t stream) {
+  auto kernel = product_kernel<MODE>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.units * ((p.m + TM - 1) / TM), sms = device_sm_count();
+  kernel<<<(unsigned)(tiles < sms ? tiles : sms), THREADS, SMEM_BYTES, stream>>>(p, maps);
   return cudaGetLastError();
+}
+
+// Columns of a unit: the whole head's, halved while twice as many units still find SMs.
+int columns_of_unit(int n, int most, int64_t groups_tiles) {
+  int unit = (n + 63) / 64 * 64;
+  unit = unit < most ? unit : most;
+  while (unit > 64 && groups_tiles * ((n + unit - 1) / unit) * 2 <= device_sm_count()) unit = (unit / 2 + 63) / 64 * 64;
+  return unit;
 }
 
 // ---- cached rows: codes as bf16 numbers (exact), scales and rotated parts ----
@@ -179,25 +401,43 @@ __global__ void __launch_bounds__(EX_THREADS) expand_rows_kernel(const ExpandArg
 }  // namespace
 
 cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream) {
-  const int64_t d_out = a.d_latent + a.d_rope, d_w = a.d_nope + a.d_v;
-  Product p = {static_cast<const __nv_bfloat16*>(a.x), a.tok_stride, a.head_stride,
-               static_cast<const __nv_bfloat16*>(a.w), a.d_latent, d_w * a.d_latent,
-               static_cast<__nv_bfloat16*>(a.y), a.heads * d_out, d_out, nullptr, nullptr,
-               a.num_tokens, a.d_latent, a.d_nope};
-  const cudaError_t e = launch_product(p, false, a.heads, stream);
-  if (e != cudaSuccess || a.d_rope == 0) return e;
-  const int64_t n = (int64_t)a.num_tokens * a.heads * (a.d_rope / 8);
-  copy_rope_kernel<<<(unsigned)((n + 255) / 256), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int d_w = a.d_nope + a.d_v, d_out = a.d_latent + a.d_rope;
+  const int64_t mt = (a.num_tokens + TM - 1) / TM;
+  Product p = {};
+  p.m = a.num_tokens, p.n = a.d_latent, p.k = a.d_nope;
+  p.n_unit = columns_of_unit(p.n, 512, a.heads * mt);
+  p.per_group = (p.n + p.n_unit - 1) / p.n_unit;
+  p.units = a.heads * p.per_group;
+  p.b_row0 = 0, p.b_group = d_w;
+  p.rope_x = a.d_rope > 0 ? a.d_nope : -1;
+  ProductMaps maps;
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
+  if (!make_rows_map(&maps.a, a.x, a.num_tokens, a.heads, a.d_nope + a.d_rope, a.tok_stride, a.head_stride, TM) ||
+      !make_rows_map(&maps.b, a.w, (int64_t)a.heads * d_w, 1, a.d_latent, a.d_latent, 0, (uint32_t)a.d_nope) ||
+      !make_rows_map(&maps.c, y, a.num_tokens, a.heads, a.d_latent, (int64_t)a.heads * d_out, d_out, 32) ||
+      !make_rows_map(&maps.c_rope, y + (a.d_rope > 0 ? a.d_latent : 0), a.num_tokens, a.heads,
+                     a.d_rope > 0 ? a.d_rope : a.d_latent, (int64_t)a.heads * d_out, d_out, 32))
+    return cudaErrorInvalidValue;
+  return launch_product<ABSORB>(p, maps, stream);
 }
 
 cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream) {
-  const int64_t d_w = a.d_nope + a.d_v;
-  Product p = {static_cast<const __nv_bfloat16*>(a.x), a.tok_stride, a.head_stride,
-               static_cast<const __nv_bfloat16*>(a.w) + (int64_t)a.d_nope * a.d_latent, a.d_latent, d_w * a.d_latent,
-               static_cast<__nv_bfloat16*>(a.y), (int64_t)a.heads * a.d_v, a.d_v, nullptr, nullptr,
-               a.num_tokens, a.d_v, a.d_latent};
-  return launch_product(p, true, a.heads, stream);
+  const int d_w = a.d_nope + a.d_v;
+  const int64_t mt = (a.num_tokens + TM - 1) / TM;
+  Product p = {};
+  p.m = a.num_tokens, p.n = a.d_v, p.k = a.d_latent;
+  p.n_unit = columns_of_unit(p.n, 128, a.heads * mt);
+  p.per_group = (p.n + p.n_unit - 1) / p.n_unit;
+  p.units = a.heads * p.per_group;
+  p.b_row0 = a.d_nope, p.b_group = d_w;
+  p.rope_x = -1;
+  ProductMaps maps;
+  if (!make_rows_map(&maps.a, a.x, a.num_tokens, a.heads, a.d_latent, a.tok_stride, a.head_stride, TM) ||
+      !make_rows_map(&maps.b, a.w, (int64_t)a.heads * d_w, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit) ||
+      !make_rows_map(&maps.c, a.y, a.num_tokens, a.heads, a.d_v, (int64_t)a.heads * a.d_v, a.d_v, 32))
+    return cudaErrorInvalidValue;
+  maps.c_rope = maps.c;
+  return launch_product<PROJECT>(p, maps, stream);
 }
 
 // codes as bf16 [capacity, d_latent], then a scale a row
@@ -212,10 +452,22 @@ cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream) {
   expand_rows_kernel<<<grid, EX_THREADS, 4 * (a.num_req + 1), stream>>>(a, x, scale);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.capacity == 0) return e;
-  const int d_w = a.heads * a.d_kv;
-  Product p = {x, a.d_latent, 0, static_cast<const __nv_bfloat16*>(a.w), a.d_latent, 0,
-               static_cast<__nv_bfloat16*>(a.kv_out), d_w, 0, scale, a.cu_k + a.num_req, a.capacity, d_w, a.d_latent};
-  return launch_product(p, true, 1, stream);
+  Product p = {};
+  p.m = a.capacity, p.n = a.heads * a.d_kv, p.k = a.d_latent;
+  p.n_unit = 128;
+  p.per_group = p.units = (p.n + p.n_unit - 1) / p.n_unit;
+  p.rope_x = -1;
+  p.rows = a.cu_k + a.num_req;
+  p.scale = scale;
+  p.out = static_cast<__nv_bfloat16*>(a.kv_out);
+  p.dev_status = a.dev_status;
+  ProductMaps maps;
+  if (!make_rows_map(&maps.a, x, a.capacity, 1, a.d_latent, a.d_latent, 0, TM) ||
+      !make_rows_map(&maps.b, a.w, p.n, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit) ||
+      !make_rows_map(&maps.c, a.kv_out, a.capacity, 1, p.n, p.n, 0, 32))
+    return cudaErrorInvalidValue;
+  maps.c_rope = maps.c;
+  return launch_product<EXPAND>(p, maps, stream);
 }
 
 }  // namespace dsa

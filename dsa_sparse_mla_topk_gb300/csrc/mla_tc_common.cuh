@@ -103,4 +103,20 @@ inline bool make_kv_map(CUtensorMap* map, const MlaArgs& a, uint32_t row_bytes, 
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// bf16 rows [n, groups, d] behind strides (in elements), in boxes of 64 columns, one
+// group and box_rows rows, 128-byte swizzle; what a box takes from outside is zero.
+inline bool make_rows_map(CUtensorMap* map, const void* p, int64_t n, int64_t groups, int64_t d, int64_t row_stride,
+                          int64_t group_stride, uint32_t box_rows) {
+  EncodeTiledFn enc = encode_tiled();
+  if (!enc) return false;
+  // (a stride that is never taken is any valid one)
+  const cuuint64_t any = (cuuint64_t)((d * 2 + 15) / 16 * 16);
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)groups, (cuuint64_t)n};
+  const cuuint64_t strides[2] = {groups > 1 ? (cuuint64_t)group_stride * 2 : any, n > 1 ? (cuuint64_t)row_stride * 2 : any};
+  const cuuint32_t box[3] = {64, 1, box_rows}, elem[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, elem,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace dsa

@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
             mbar_arrive_expect_tx(bar(B_KF + slot), CHUNK);
             const uint32_t dst = smem_u32(smem + OFF_K + slot * CHUNK);
             if (c < nn) tma_load_3d(dst, &maps.kv, 64 * c, h, n0, bar(B_KF + slot));
-            else tma_load_2d(dst, &maps.rope, 0, n0, bar(B_KF + slot));
+            else tma_load_3d(dst, &maps.rope, 0, 0, n0, bar(B_KF + slot));
             if (++slot == KSLOTS) slot = 0, phase ^= 1;
           }
           if (lt == 0 && cnt1 > 0) query(1);
@@ -499,30 +499,6 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
   }
 }
 
-// 16-bit rows [n, heads, d] behind strides, in boxes of 64 columns, one head, 128 rows.
-bool make_map3(CUtensorMap* map, const void* p, int64_t n, int64_t heads, int64_t d, int64_t ts, int64_t hs) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  // (a stride that is never taken is any valid one)
-  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)n};
-  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? hs * 2 : (d * 2 + 15) / 16 * 16),
-                                 (cuuint64_t)(n > 1 ? ts * 2 : (d * 2 + 15) / 16 * 16)};
-  const cuuint32_t box[3] = {64, 1, 128}, elem[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool make_map2(CUtensorMap* map, const void* p, int64_t n, int64_t d, int64_t ts) {
-  EncodeTiledFn enc = encode_tiled();
-  if (!enc) return false;
-  const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)n};
-  const cuuint64_t strides[1] = {(cuuint64_t)(n > 1 ? ts * 2 : (d * 2 + 15) / 16 * 16)};
-  const cuuint32_t box[2] = {64, 128}, elem[2] = {1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, box, elem,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <bool STD>
 cudaError_t launch(const PromptArgs& a, const PromptMaps& maps, cudaStream_t stream) {
   auto kernel = prompt_mla_kernel<STD>;
@@ -538,15 +514,13 @@ cudaError_t launch(const PromptArgs& a, const PromptMaps& maps, cudaStream_t str
 
 cudaError_t launch_prompt_mla(const PromptArgs& a, cudaStream_t stream) {
   PromptMaps maps;
-  if (!make_map3(&maps.q, a.q, a.num_tokens, a.heads, a.d_nope + a.d_rope, a.q_tok_stride, a.q_head_stride))
+  if (!make_rows_map(&maps.q, a.q, a.num_tokens, a.heads, a.d_nope + a.d_rope, a.q_tok_stride, a.q_head_stride, 128))
     return cudaErrorInvalidValue;
   // (without rows no token sees anything, and no copy is made)
-  const bool rows = a.num_rows > 0;
-  if (!make_map3(&maps.kv, rows ? a.kv : a.q, rows ? a.num_rows : 1, rows ? a.heads : 1, rows ? a.d_nope + a.d_v : 16,
-                 a.kv_tok_stride, a.kv_head_stride))
-    return cudaErrorInvalidValue;
-  const bool rope = rows && a.d_rope > 0;
-  if (!make_map2(&maps.rope, rope ? a.k_rope : a.q, rope ? a.num_rows : 1, rope ? a.d_rope : 16, a.rope_stride))
+  const bool rows = a.num_rows > 0, rope = rows && a.d_rope > 0;
+  if (!make_rows_map(&maps.kv, rows ? a.kv : a.q, rows ? a.num_rows : 1, rows ? a.heads : 1, rows ? a.d_nope + a.d_v : 16,
+                     a.kv_tok_stride, a.kv_head_stride, 128) ||
+      !make_rows_map(&maps.rope, rope ? a.k_rope : a.q, rope ? a.num_rows : 1, 1, rope ? a.d_rope : 16, a.rope_stride, 0, 128))
     return cudaErrorInvalidValue;
   const bool std = a.d_nope == 128 && a.d_rope == 64 && a.d_v == 128;
   return std ? launch<true>(a, maps, stream) : launch<false>(a, maps, stream);
