@@ -26,6 +26,7 @@ __all__ = ["DsaError", "load_library", "topk_select", "sparse_mla_fwd", "combine
            "kv_write",
            "PrefixCache", "BatchLayout", "batch_layout", "qk_norm_rope", "chunk_mla_fwd", "chunk_mla", "verify_draft",
            "absorb_q", "project_out", "ExpandedKV", "expand_kv", "expand_kv_workspace_size", "prompt_mla_fwd", "prompt_mla",
+           "pick_prompt_splits",
            "TokenLogprobs", "token_logprobs",
            "kv_tile_count", "kv_tile_size", "pick_num_splits", "pick_chunk_splits", "status_string", "EXPORTED_SYMBOLS",
            "DEV_BAD_QPOS", "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_TIMEOUT", "DEV_NO_PAGES"]
@@ -41,7 +42,7 @@ EXPORTED_SYMBOLS = ("dsa_status_string", "dsa_version", "dsa_topk_select", "dsa_
                     "dsa_sparse_mla_topk_fwd", "dsa_sparse_mla_topk_max_k", "dsa_topk_sparse_mla_fwd",
                     "dsa_combine", "dsa_kv_write", "dsa_batch_layout", "dsa_qk_norm_rope", "dsa_chunk_mla_fwd",
                     "dsa_verify_draft", "dsa_verify_draft_req", "dsa_absorb_q", "dsa_project_out", "dsa_expand_kv",
-                    "dsa_expand_kv_workspace_size", "dsa_prompt_mla_fwd", "dsa_token_logprobs", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
+                    "dsa_expand_kv_workspace_size", "dsa_prompt_mla_fwd", "dsa_prompt_pick_num_splits", "dsa_token_logprobs", "dsa_prefix_cache_create", "dsa_prefix_cache_destroy",
                     "dsa_prefix_cache_acquire", "dsa_prefix_cache_release", "dsa_prefix_cache_stats",
                     "dsa_kv_tile_count", "dsa_kv_tile_size", "dsa_pick_num_splits",
                     "dsa_chunk_pick_num_splits", "dsa_chunk_pick_num_splits_live")
@@ -124,6 +125,8 @@ def load_library(path: str | None = None):
         lib.dsa_prompt_mla_fwd.argtypes = [vp, i64, i64, vp, i64, i64, i32, vp, i64, vp, vp, vp, i32, i32, i32, i32, i32,
                                            i32, f32, i32, vp, vp, vp, vp, vp, vp]
         lib.dsa_prompt_mla_fwd.restype = i32
+        lib.dsa_prompt_pick_num_splits.argtypes = [i32, i32, i32, i32, i32]
+        lib.dsa_prompt_pick_num_splits.restype = i32
         lib.dsa_token_logprobs.argtypes = [vp, i64, i32, i32, i32, vp, i32, vp, vp, vp, vp, vp, vp, vp]
         lib.dsa_token_logprobs.restype = i32
         lib.dsa_prefix_cache_create.argtypes = [i32, i32]
@@ -176,7 +179,9 @@ def _load_marshal(lib):
         return None
     m.bind(*(ctypes.cast(f, ctypes.c_void_p).value
              for f in (lib.dsa_batch_layout, lib.dsa_qk_norm_rope, lib.dsa_chunk_mla_fwd, lib.dsa_combine,
-                       lib.dsa_chunk_pick_num_splits, lib.dsa_verify_draft_req)))
+                       lib.dsa_chunk_pick_num_splits, lib.dsa_verify_draft_req, lib.dsa_absorb_q, lib.dsa_project_out,
+                       lib.dsa_expand_kv, lib.dsa_expand_kv_workspace_size, lib.dsa_prompt_mla_fwd,
+                       lib.dsa_prompt_pick_num_splits, lib.dsa_token_logprobs)))
     return m
 
 
@@ -1013,6 +1018,10 @@ def absorb_q(q: torch.Tensor, w_kv: torch.Tensor, *, d_rope: int, q_out: torch.T
     up-projection w_kv bf16 [heads, d_nope + d_v, d_latent] of every head's keys
     and values give bf16 [tokens, heads, d_latent + d_rope], the queries of
     chunk_mla and sparse_mla_topk; the rotated part stays as it is."""
+    if q_out is None and stream is None and _fast is not None:
+        r = _fast.absorb_q(q, w_kv, d_rope)
+        if r is not None:
+            return _done("dsa_absorb_q", r)
     dev = _device_of(q, "q")
     _need_rows(q, "q", _BF16, 3, dev)
     _need(w_kv, "w_kv", _BF16, 3, dev)
@@ -1031,6 +1040,10 @@ def project_out(o: torch.Tensor, w_kv: torch.Tensor, *, d_nope: int, out: torch.
                 stream=None) -> torch.Tensor:
     """Attention's latent outputs o bf16 [tokens, heads, d_latent] (strides as for
     absorb_q) to every head's values, bf16 [tokens, heads, d_v] (dsa_project_out)."""
+    if out is None and stream is None and _fast is not None:
+        r = _fast.project_out(o, w_kv, d_nope)
+        if r is not None:
+            return _done("dsa_project_out", r)
     dev = _device_of(o, "o")
     _need_rows(o, "o", _BF16, 3, dev)
     _need(w_kv, "w_kv", _BF16, 3, dev)
@@ -1070,6 +1083,12 @@ def expand_kv(kv: torch.Tensor, kv_scale: torch.Tensor, block_table: torch.Tenso
     number of rows to make room for, or ``out`` (an ExpandedKV) holds them; rows
     behind the last request are left as they were.  ``workspace`` (uint8,
     expand_kv_workspace_size bytes) is allocated when none is given."""
+    if out is not None and capacity is None and workspace is None and stream is None and _fast is not None:
+        r = _fast.expand_kv(kv, kv_scale, block_table, ctx_len, w_kv, d_rope, page_size, *out, dev_status)
+        if r is not None:
+            if r:
+                raise DsaError("dsa_expand_kv", r)
+            return out
     dev = _device_of(kv, "kv")
     _need(kv, "kv", _U8, 2, dev)
     _need(kv_scale, "kv_scale", _F32, 1, dev)
@@ -1141,19 +1160,36 @@ def prompt_mla_fwd(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor | Non
     return (out, lse) if num_splits == 1 else (o_part, lse_part)
 
 
+def pick_prompt_splits(num_tokens: int, num_req: int, heads: int, max_ctx: int, num_sms: int = 0) -> int:
+    """Shares of the rows that prompt_mla takes for contexts of about max_ctx positions."""
+    return load_library().dsa_prompt_pick_num_splits(num_tokens, num_req, heads, max(1, min(max_ctx, 2**31 - 1)), num_sms)
+
+
 def prompt_mla(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor | None, cu_q: torch.Tensor, cu_k: torch.Tensor,
-               q_pos: torch.Tensor, *, d_nope: int, softmax_scale: float, num_splits: int | None = None,
-               buffers: dict | None = None, dev_status=None, stream=None):
+               q_pos: torch.Tensor, *, d_nope: int, softmax_scale: float, max_ctx: int | None = None,
+               num_splits: int | None = None, buffers: dict | None = None, dev_status=None, stream=None):
     """Attention of new tokens q bf16 [tokens, heads, d_nope + d_rope] over every
     head's own keys and values, kv bf16 [rows, heads, d_nope + d_v] and the shared
     rotated part k_rope bf16 [rows, d_rope] (expand_kv's, or a prompt's own
     projections; any strides that are multiples of 8): token t of request r, cu_q[r] <=
     t < cu_q[r + 1], attends to rows cu_k[r] .. cu_k[r] + q_pos[t].  ``cu_q`` and
-    ``q_pos`` are batch_layout's; padding and q_pos = -1 give 0.  ``buffers``
-    (optional) holds preallocated out / lse / o_part / lse_part tensors.  Returns
-    (out bf16 [tokens, heads, d_v], lse fp32 [tokens, heads])."""
+    ``q_pos`` are batch_layout's; padding and q_pos = -1 give 0.  ``max_ctx``
+    (default: the rows a request on average) is about the longest context, from which
+    the number of shares of the rows is picked when ``num_splits`` is None; the
+    result is right for any value.  ``buffers`` (optional) holds preallocated out / lse /
+    o_part / lse_part tensors.  Returns (out bf16 [tokens, heads, d_v], lse fp32 [tokens,
+    heads]), which share one allocation unless given (clone lse to keep it alone)."""
     b = buffers or {}
-    S = 1 if num_splits is None else num_splits
+    if not b and stream is None and _fast is not None and num_splits != 0:
+        r = _fast.prompt_mla(q, kv, k_rope, cu_q, cu_k, q_pos, d_nope, softmax_scale, max_ctx or 0, num_splits or 0,
+                             dev_status)
+        if r is not None:
+            return _done("dsa_prompt_mla_fwd", r)
+    _need_rows(q, "q", _BF16, 3, _device_of(q, "q"))
+    S = num_splits
+    if S is None:
+        R = max(1, cu_q.shape[0] - 1)
+        S = pick_prompt_splits(q.shape[0], R, q.shape[1], kv.shape[0] // R if max_ctx is None else max_ctx)
     r = prompt_mla_fwd(q, kv, k_rope, cu_q, cu_k, q_pos, d_nope=d_nope, softmax_scale=softmax_scale, num_splits=S,
                        out=b.get("out") if S == 1 else None, lse=b.get("lse") if S == 1 else None, o_part=b.get("o_part"),
                        lse_part=b.get("lse_part"), dev_status=dev_status, stream=stream)
@@ -1187,7 +1223,12 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, *, top: int = 0, 
     ``logits`` [rows, vocab] (fp32, bf16 or fp16, any row stride; -inf: masked), with
     the rows' entropies, the tokens' ranks and the ``top`` most probable
     alternatives, ties to the lower id (dsa_token_logprobs).  ``out`` (a
-    TokenLogprobs of preallocated tensors) is written when given."""
+    TokenLogprobs of preallocated tensors) is written when given; else the outputs
+    share one allocation."""
+    if out is None and stream is None and _fast is not None:
+        r = _fast.token_logprobs(logits, tokens, top, dev_status)
+        if r is not None:
+            return TokenLogprobs._make(_done("dsa_token_logprobs", r))
     dev = _device_of(logits, "logits")
     code = _LOGIT_DTYPES.get(logits.dtype)
     if code is None:

@@ -690,6 +690,19 @@ dsa_status dsa_expand_kv(const uint8_t* kv, const float* kv_scale, int64_t num_p
   return from_cuda(dsa::launch_expand_kv(a, static_cast<cudaStream_t>(stream)));
 }
 
+int32_t dsa_prompt_pick_num_splits(int32_t num_tokens, int32_t num_req, int32_t num_heads, int32_t max_ctx,
+                                   int32_t num_sms) {
+  if (num_tokens <= 0 || num_req <= 0 || num_heads <= 0 || max_ctx <= 0) return 1;
+  const int64_t sms = num_sms > 0 ? num_sms : dsa::device_sm_count();
+  // CTAs of a share, about: a request's last tile is half full
+  const int64_t ctas = num_heads * (num_tokens / 256 + (int64_t)(num_req + 1) / 2);
+  // a share of 4 tiles of 128 rows (4 x 0.6 us) outweighs its part of the Combine
+  const int64_t most = max_ctx / (4 * 128) < 16 ? max_ctx / (4 * 128) : 16;
+  int64_t s = sms / ctas;
+  if (s > most) s = most;
+  return s < 1 ? 1 : (int32_t)s;
+}
+
 dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* kv,
                               int64_t kv_tok_stride, int64_t kv_head_stride, int32_t num_rows, const void* k_rope,
                               int64_t rope_stride, const int32_t* cu_q, const int32_t* cu_k, const int32_t* q_pos,

@@ -25,6 +25,13 @@ decltype(&dsa_chunk_mla_fwd) chunk_mla_fn = nullptr;
 decltype(&dsa_combine) combine_fn = nullptr;
 decltype(&dsa_chunk_pick_num_splits) pick_fn = nullptr;
 decltype(&dsa_verify_draft_req) verify_draft_fn = nullptr;
+decltype(&dsa_absorb_q) absorb_q_fn = nullptr;
+decltype(&dsa_project_out) project_out_fn = nullptr;
+decltype(&dsa_expand_kv) expand_kv_fn = nullptr;
+decltype(&dsa_expand_kv_workspace_size) expand_size_fn = nullptr;
+decltype(&dsa_prompt_mla_fwd) prompt_mla_fn = nullptr;
+decltype(&dsa_prompt_pick_num_splits) prompt_pick_fn = nullptr;
+decltype(&dsa_token_logprobs) token_logprobs_fn = nullptr;
 
 // Reads a call's arguments; `good` is false once one is not as documented.
 struct Args {
@@ -61,6 +68,12 @@ struct Args {
       return nullptr;
     }
     if (t->scalar_type() != type || !placed(*t, dim) || !t->is_contiguous()) good = false;
+    return t;
+  }
+  // of this type and rank with a contiguous last dimension, on the same device
+  const at::Tensor* rows(at::ScalarType type, int64_t dim) {
+    const at::Tensor* t = any();
+    if (!t || t->scalar_type() != type || !placed(*t, dim) || (t->size(dim - 1) > 1 && t->stride(dim - 1) != 1)) good = false;
     return t;
   }
   int64_t integer() {
@@ -324,23 +337,174 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   END_HANDLE_TH_ERRORS
 }
 
-// bind(batch_layout, qk_norm_rope, chunk_mla_fwd, combine, chunk_pick_num_splits, verify_draft_req): the entry points' addresses
+// (x, w_kv, d_rope of absorb_q or d_nope of project_out)
+template <bool ABSORB>
+PyObject* latent_proj(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  HANDLE_TH_ERRORS
+  if (argc != 3) Py_RETURN_NONE;
+  Args a{argv};
+  const at::Tensor* x = a.rows(at::kBFloat16, 3);
+  const at::Tensor* w = a.tensor(at::kBFloat16, 3);
+  const int32_t given = a.int32();
+  if (!a.good) Py_RETURN_NONE;
+  const int64_t n = x->size(0), H = x->size(1), d = x->size(2), dw = w->size(1), dl = w->size(2);
+  const int64_t dn = ABSORB ? d - given : given;
+  if (w->size(0) != H || !fits32(n) || !fits32(H) || dn <= 0 || given < 0 || dw <= dn || dw > 256 || dl > 512 ||
+      (!ABSORB && d != dl))
+    Py_RETURN_NONE;
+  const at::Tensor y = at::empty({n, H, ABSORB ? dl + given : dw - dn}, x->options());
+  dsa_status s;
+  if constexpr (ABSORB)
+    s = call(absorb_q_fn, x->data_ptr(), stride(x, 0), stride(x, 1), w->data_ptr(), (int32_t)n, (int32_t)H, (int32_t)dn,
+             given, (int32_t)(dw - dn), (int32_t)dl, y.data_ptr(), a.stream());
+  else
+    s = call(project_out_fn, x->data_ptr(), stride(x, 0), stride(x, 1), w->data_ptr(), (int32_t)n, (int32_t)H, given,
+             (int32_t)(dw - dn), (int32_t)dl, y.data_ptr(), a.stream());
+  if (s != DSA_OK) return PyLong_FromLong(s);
+  return THPVariable_Wrap(y);
+  END_HANDLE_TH_ERRORS
+}
+
+// (kv, kv_scale, block_table, ctx_len, w_kv, d_rope, page_size, out.kv, out.k_rope, out.cu_k, dev_status)
+PyObject* expand_kv(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  HANDLE_TH_ERRORS
+  if (argc != 11) Py_RETURN_NONE;
+  Args a{argv};
+  const at::Tensor* kv = a.tensor(at::kByte, 2);
+  const at::Tensor* sc = a.tensor(at::kFloat, 1);
+  const at::Tensor* bt = a.tensor(at::kInt, 2);
+  const at::Tensor* ctx = a.tensor(at::kInt, 1);
+  const at::Tensor* w = a.tensor(at::kBFloat16, 3);
+  const int32_t dr = a.int32(), page = a.int32();
+  const at::Tensor* out = a.tensor(at::kBFloat16, 3);
+  const at::Tensor* rope = a.tensor(at::kBFloat16, 2);
+  const at::Tensor* cu = a.tensor(at::kInt, 1);
+  int32_t* st = a.status();
+  if (!a.good || page <= 0) Py_RETURN_NONE;
+  const int64_t R = ctx->size(0), slots = kv->size(0), cap = out->size(0), H = w->size(0), dw = w->size(1), dl = w->size(2);
+  if (slots % page != 0 || sc->size(0) != slots || kv->size(1) != dl + dr || bt->size(0) != R || !fits32(R) || !fits32(H) ||
+      !fits32(bt->size(1)) || !fits32(cap) || dw > 256 || dl > 512 || out->size(1) != H || out->size(2) != dw ||
+      rope->size(0) != cap || rope->size(1) != dr || cu->size(0) != R + 1)
+    Py_RETURN_NONE;
+  const int64_t size = (int64_t)expand_size_fn((int32_t)cap, (int32_t)dl);
+  const at::Tensor ws = bytes(size, *kv);
+  const dsa_status s = call(expand_kv_fn, ptr<uint8_t>(kv), ptr<float>(sc), slots / page, ptr<int32_t>(bt), (int32_t)R,
+                            (int32_t)bt->size(1), ptr<int32_t>(ctx), w->data_ptr(), (int32_t)H, (int32_t)dl, dr,
+                            (int32_t)dw, page, (int32_t)cap, out->data_ptr(), dr ? rope->data_ptr() : nullptr,
+                            ptr<int32_t>(cu), ws.data_ptr(), (size_t)size, st, a.stream());
+  return PyLong_FromLong(s);
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, kv, k_rope, cu_q, cu_k, q_pos, d_nope, softmax_scale, max_ctx (0: the rows a request on average), num_splits (0: by
+// the rule), dev_status)
+PyObject* prompt_mla(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  HANDLE_TH_ERRORS
+  if (argc != 11) Py_RETURN_NONE;
+  Args a{argv};
+  const at::Tensor* q = a.rows(at::kBFloat16, 3);
+  const at::Tensor* kv = a.rows(at::kBFloat16, 3);
+  const at::Tensor* rope = argv[a.i] == Py_None ? a.any() : a.rows(at::kBFloat16, 2);
+  const at::Tensor* cuq = a.tensor(at::kInt, 1);
+  const at::Tensor* cuk = a.tensor(at::kInt, 1);
+  const at::Tensor* pos = a.tensor(at::kInt, 1);
+  const int32_t dn = a.int32();
+  const float scale = a.number();
+  int64_t ctx = a.integer();
+  int32_t S = a.int32();
+  int32_t* st = a.status();
+  if (!a.good) Py_RETURN_NONE;
+  const int64_t n = q->size(0), H = q->size(1), N = kv->size(0), dr = q->size(2) - dn, dv = kv->size(2) - dn,
+                R = cuq->size(0) - 1;
+  if (kv->size(1) != H || dn <= 0 || dr < 0 || dr > 64 || dv <= 0 || dv > 128 || R < 0 || cuk->size(0) != R + 1 ||
+      pos->size(0) != n || n == 0 || !fits32(n) || !fits32(N) || !fits32(H) || !fits32(R) ||
+      (dr > 0 && (!rope || rope->size(0) != N || rope->size(1) != dr)))
+    Py_RETURN_NONE;
+  if (ctx <= 0) ctx = N / std::max<int64_t>(R, 1);
+  if (S == 0)
+    S = prompt_pick_fn((int32_t)n, (int32_t)R, (int32_t)H, (int32_t)std::min<int64_t>(std::max<int64_t>(ctx, 1), INT32_MAX), 0);
+  if (S < 1 || S > 64) Py_RETURN_NONE;
+  // out, then lse; the partials of a split call in a buffer of their own
+  const int64_t ob = (2 * n * H * dv + 15) / 16 * 16;
+  const at::Tensor buf = bytes(ob + 4 * n * H, *q);
+  const at::Tensor out = cut(buf, 0, {n, H, dv}, at::kBFloat16), lse = cut(buf, ob / 4, {n, H}, at::kFloat);
+  at::Tensor parts;
+  float *op = nullptr, *lp = nullptr;
+  if (S > 1) {
+    const int64_t pn = (int64_t)S * n * H * dv;
+    parts = at::empty({pn + (int64_t)S * n * H}, lse.options());
+    op = ptr<float>(&parts);
+    lp = op + pn;
+  }
+  void* stream = a.stream();
+  dsa_status s = call(prompt_mla_fn, q->data_ptr(), ::stride(q, 0), ::stride(q, 1), kv->data_ptr(), ::stride(kv, 0),
+                      ::stride(kv, 1), (int32_t)N, dr ? rope->data_ptr() : nullptr, dr ? ::stride(rope, 0) : (int64_t)0,
+                      ptr<int32_t>(cuq), ptr<int32_t>(cuk), ptr<int32_t>(pos), (int32_t)R, (int32_t)n, (int32_t)H, dn,
+                      (int32_t)dr, (int32_t)dv, scale, S, op ? nullptr : out.data_ptr(), op ? nullptr : ptr<float>(&lse), op,
+                      lp, st, stream);
+  if (s == DSA_OK && op)
+    s = call(combine_fn, op, lp, S, (int32_t)n, (int32_t)H, (int32_t)dv, out.data_ptr(), ptr<float>(&lse), stream);
+  if (s != DSA_OK) return PyLong_FromLong(s);
+  return tuple_of({&out, &lse});
+  END_HANDLE_TH_ERRORS
+}
+
+// (logits, tokens, top, dev_status)
+PyObject* token_logprobs(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
+  HANDLE_TH_ERRORS
+  if (argc != 4) Py_RETURN_NONE;
+  Args a{argv};
+  const at::Tensor* z = a.any();
+  if (!z) Py_RETURN_NONE;
+  const at::ScalarType type = z->scalar_type();
+  if ((type != at::kFloat && type != at::kBFloat16 && type != at::kHalf) || !a.placed(*z, 2) ||
+      (z->size(1) > 1 && z->stride(1) != 1) || (z->size(0) > 1 && z->stride(0) < z->size(1)))
+    Py_RETURN_NONE;
+  const at::Tensor* tok = a.tensor(at::kInt, 1);
+  const int32_t top = a.int32();
+  int32_t* st = a.status();
+  const int64_t rows = z->size(0), V = z->size(1);
+  if (!a.good || tok->size(0) != rows || rows == 0 || top < 0 || top > 64 || !fits32(rows) || !fits32(V)) Py_RETURN_NONE;
+  const at::Tensor buf = at::empty({rows * (3 + 2 * (int64_t)top)}, tok->options());
+  const at::Tensor lp = cut(buf, 0, {rows}, at::kFloat), ent = cut(buf, rows, {rows}, at::kFloat),
+                   rank = cut(buf, 2 * rows, {rows}, at::kInt), ids = cut(buf, 3 * rows, {rows, top}, at::kInt),
+                   tlp = cut(buf, rows * (3 + (int64_t)top), {rows, top}, at::kFloat);
+  const dsa_status s = call(token_logprobs_fn, z->data_ptr(), rows > 1 ? z->stride(0) : V, (int32_t)rows, (int32_t)V,
+                            type == at::kFloat ? DSA_FP32 : type == at::kHalf ? DSA_FP16 : DSA_BF16, ptr<int32_t>(tok), top,
+                            ptr<float>(&lp), ptr<float>(&ent), ptr<int32_t>(&rank), top ? ptr<int32_t>(&ids) : nullptr,
+                            top ? ptr<float>(&tlp) : nullptr, st, a.stream());
+  if (s != DSA_OK) return PyLong_FromLong(s);
+  return tuple_of({&lp, &ent, &rank, &ids, &tlp});
+  END_HANDLE_TH_ERRORS
+}
+
+// bind(addresses of the entry points, in this order)
 PyObject* bind(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
-  if (argc != 6) {
-    PyErr_SetString(PyExc_TypeError, "bind takes 6 addresses");
+  constexpr Py_ssize_t N = 13;
+  if (argc != N) {
+    PyErr_SetString(PyExc_TypeError, "bind takes 13 addresses");
     return nullptr;
   }
-  void* p[6];
-  for (int i = 0; i < 6; ++i) {
+  void* p[N];
+  for (Py_ssize_t i = 0; i < N; ++i) {
     p[i] = PyLong_AsVoidPtr(argv[i]);
     if (PyErr_Occurred()) return nullptr;
   }
-  batch_layout_fn = reinterpret_cast<decltype(batch_layout_fn)>(p[0]);
-  qk_norm_rope_fn = reinterpret_cast<decltype(qk_norm_rope_fn)>(p[1]);
-  chunk_mla_fn = reinterpret_cast<decltype(chunk_mla_fn)>(p[2]);
-  combine_fn = reinterpret_cast<decltype(combine_fn)>(p[3]);
-  pick_fn = reinterpret_cast<decltype(pick_fn)>(p[4]);
-  verify_draft_fn = reinterpret_cast<decltype(verify_draft_fn)>(p[5]);
+  int i = 0;
+  auto take = [&](auto& fn) { fn = reinterpret_cast<std::remove_reference_t<decltype(fn)>>(p[i++]); };
+  take(batch_layout_fn);
+  take(qk_norm_rope_fn);
+  take(chunk_mla_fn);
+  take(combine_fn);
+  take(pick_fn);
+  take(verify_draft_fn);
+  take(absorb_q_fn);
+  take(project_out_fn);
+  take(expand_kv_fn);
+  take(expand_size_fn);
+  take(prompt_mla_fn);
+  take(prompt_pick_fn);
+  take(token_logprobs_fn);
   Py_RETURN_NONE;
 }
 
@@ -350,6 +514,9 @@ PyMethodDef method(const char* name) {
 }
 PyMethodDef methods[] = {method<batch_layout>("batch_layout"), method<qk_norm_rope>("qk_norm_rope"),
                          method<chunk_mla>("chunk_mla"),       method<verify_draft>("verify_draft"),
+                         method<latent_proj<true>>("absorb_q"), method<latent_proj<false>>("project_out"),
+                         method<expand_kv>("expand_kv"),       method<prompt_mla>("prompt_mla"),
+                         method<token_logprobs>("token_logprobs"),
                          method<bind>("bind"),                 {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module_def = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
