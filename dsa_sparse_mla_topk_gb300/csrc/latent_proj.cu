@@ -6,16 +6,20 @@
 //   project:  y[t, h, :] = x[t, h, :dl] W_v[h]^T,      W_v[h] = w[h, dn:, :]   [dv, dl]
 //   expand:   y[n, (h, j)] = s_n (code[n, :] . w[h, j, :])
 //
-// All three are C = s A B with bf16 factors and fp32 sums, 128 rows of A a tile
+// All three are C = s A B with bf16 factors and fp32 sums, 128 rows of A a CTA and tile
 // (tcgen05 + TMEM + TMA), by persistent CTAs.  A unit is a head's columns (absorb: up to 512,
-// project: up to 128) or 128 of expand's; its B, at most 128 KB, stays in shared
+// project: up to 128) or 256 of expand's; its B, at most 128 KB a CTA, stays in shared
 // memory while the CTA goes through tiles of rows, whose A comes in 64-column chunks.
-// The (unit, tile) pairs are dealt in contiguous runs, one a CTA, equal to one tile.
+// The (unit, tile) pairs are dealt in contiguous runs, one a CTA, equal to one tile; B of the
+// next unit follows chunk by chunk behind the last tile of the one before.
 // Results go through shared memory and TMA stores of 32 rows x 64 columns, while the next
 // tile's products run into the other half of TMEM.
-// absorb and project read and write more than they compute (85 and 102 flop a byte);
-// expand is bound by the tensor cores (512).  Warps: 0-3 results, 4 TMA, 5 MMA,
-// 6 the rotated part of the queries, which is copied.  All waits are bounded.
+// absorb and project read and write more than they compute (85 and 102 flop a byte).
+// expand is bound by the tensor cores (512): pairs of CTAs (cta_group::2) take 256 x 256
+// outputs a tile, each holding half of the columns' weights, so that A is half
+// as many bytes a product (with single CTAs of 128 columns, 50 GB/s of A an SM: 16,384
+// rows 283 us).  Warps: 0-3 results, 4 TMA, 5 MMA, 6 the rotated part of the queries, which
+// is copied.  All waits are bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -45,9 +49,10 @@ constexpr int OFF_OUT = OFF_A + SLOTS * CHUNK;    // [4 warps][2]
 constexpr int OFF_BAR = OFF_OUT + 4 * 2 * STAGE;
 constexpr int B_AF = 0;             // [SLOTS] a chunk of A has landed
 constexpr int B_AE = B_AF + SLOTS;  // [SLOTS] its slot is free
-constexpr int B_BF = B_AE + SLOTS;  // B of the unit has landed
-constexpr int B_BE = B_BF + 1;      // its products are done
-constexpr int B_DF = B_BE + 1;      // [2] an accumulator is complete
+constexpr int MAX_KC = 8;           // chunks of k
+constexpr int B_BF = B_AE + SLOTS;  // [MAX_KC] chunk of B of the unit has landed (absorb: [0], all of it)
+constexpr int B_BE = B_BF + MAX_KC; // [MAX_KC] its products are done
+constexpr int B_DF = B_BE + MAX_KC; // [2] an accumulator is complete
 constexpr int B_DE = B_DF + 2;      // [2] it has been read
 constexpr int B_RF = B_DE + 2;      // the rotated part has landed
 constexpr int NBAR = B_RF + 1;
@@ -78,14 +83,22 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
   auto bar = [&](int b) { return smem_u32(bars + b); };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  constexpr bool PAIR = MODE == EXPAND;
   constexpr int NSLOT = MODE == ABSORB ? SLOTS - 1 : SLOTS;
+  constexpr int CTAS = PAIR ? 2 : 1, TROWS = CTAS * TM;  // rows of a tile
+  const int rank = PAIR ? (int)cluster_rank() : 0;
 
   if (warp == WARP_MMA) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
+    if constexpr (PAIR) {
+      tmem_alloc_pair(smem_u32(tmem_slot), 512);
+      tmem_relinquish_pair();
+    } else {
+      tmem_alloc(smem_u32(tmem_slot), 512);
+      tmem_relinquish();
+    }
   }
   if (tid == WARP_TMA * 32) {
-    for (int b = 0; b < NBAR; ++b) mbar_init(bar(b), b >= B_DE && b < B_DE + 2 ? 4u : 1u);
+    for (int b = 0; b < NBAR; ++b) mbar_init(bar(b), b >= B_DE && b < B_DE + 2 ? 4u * CTAS : 1u);
     fence_mbarrier_init();
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b);
@@ -93,14 +106,20 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
   }
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) {  // the other CTA's barriers and tensor memory are there, too
+    cluster_arrive();
+    cluster_wait();
+  }
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   int m_all = p.m;
   if constexpr (MODE == EXPAND) m_all = min(max(__ldg(p.rows), 0), p.m);
-  const int mt = (m_all + TM - 1) / TM;
+  const int mt = (m_all + TROWS - 1) / TROWS;
   const int64_t tiles = (int64_t)p.units * mt;
-  const int t0 = (int)(tiles * blockIdx.x / gridDim.x), t1 = (int)(tiles * (blockIdx.x + 1) / gridDim.x);
+  const int workers = gridDim.x / CTAS, worker = blockIdx.x / CTAS;
+  const int t0 = (int)(tiles * worker / workers), t1 = (int)(tiles * (worker + 1) / workers);
   const int nkc = (p.k + 63) / 64;
+  const int b_rows = p.n_unit / CTAS;  // columns of a unit whose weights this CTA holds
   // unit u: head (expand: 0) and the first of its columns there
   auto group_of = [&](int u) { return MODE == EXPAND ? 0 : u / p.per_group; };
   auto col_of = [&](int u) { return (u % p.per_group) * p.n_unit; };
@@ -109,92 +128,110 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
 
   if (warp == WARP_TMA) {
     if (lane == 0) {
+      // A barrier's bytes are those of both CTAs, counted on the first one's
+      auto load = [&](int b, int off, const CUtensorMap* map, int x, int y, int z) {
+        if constexpr (PAIR) tma_load_3d_pair(smem_u32(smem + off), map, x, y, z, cluster_addr(bar(b), 0));
+        else tma_load_3d(smem_u32(smem + off), map, x, y, z, bar(b));
+      };
+      auto expect = [&](int b, uint32_t bytes) {
+        if (rank == 0) mbar_arrive_expect_tx(bar(b), bytes * CTAS);
+      };
       int slot = 0, phase = 0, unit = -1, loads = 0;
       for (int t = t0; t < t1 && ok; ++t) {
-        const int u = t / mt, m0 = (t - u * mt) * TM, g = group_of(u);
-        if (u != unit) {
-          if (unit >= 0 && !mbar_wait(bar(B_BE), (loads - 1) & 1)) {
+        const int u = t / mt, m0 = (t - u * mt) * TROWS + rank * TM, g = group_of(u), n0 = col_of(u) + rank * b_rows;
+        const bool fresh = u != unit;
+        if (fresh) unit = u, ++loads;
+        if (MODE == ABSORB && fresh) {  // slices of 64 columns, k rows each
+          if (!mbar_wait(bar(B_BE), (loads & 1))) {
             ok = false;
             break;
           }
-          unit = u;
-          const int n0 = col_of(u), nb = cols_of(u);
-          const uint32_t b = smem_u32(smem + OFF_B);
-          if (MODE == ABSORB) {  // slices of 64 columns, k rows each
-            const int slices = (nb + 63) / 64;
-            mbar_arrive_expect_tx(bar(B_BF), slices * p.k * 128);
-            for (int s = 0; s < slices; ++s)
-              tma_load_3d(b + s * p.k * 128, &maps.b, n0 + 64 * s, 0, p.b_row0 + g * p.b_group, bar(B_BF));
-          } else {  // 64 columns of k at a time, n_unit rows each
-            mbar_arrive_expect_tx(bar(B_BF), nkc * p.n_unit * 128);
-            for (int c = 0; c < nkc; ++c)
-              tma_load_3d(b + c * p.n_unit * 128, &maps.b, 64 * c, 0, p.b_row0 + g * p.b_group + n0, bar(B_BF));
-          }
-          ++loads;
+          const int slices = (cols_of(u) + 63) / 64;
+          expect(B_BF, slices * p.k * 128);
+          for (int s = 0; s < slices; ++s) load(B_BF, OFF_B + s * p.k * 128, &maps.b, n0 + 64 * s, 0, p.b_row0 + g * p.b_group);
         }
         for (int c = 0; c < nkc; ++c) {
+          if (MODE != ABSORB && fresh) {  // 64 columns of k, b_rows rows
+            if (!mbar_wait(bar(B_BE + c), (loads & 1))) {
+              ok = false;
+              break;
+            }
+            expect(B_BF + c, b_rows * 128);
+            load(B_BF + c, OFF_B + c * b_rows * 128, &maps.b, 64 * c, 0, p.b_row0 + g * p.b_group + n0);
+          }
           if (!mbar_wait(bar(B_AE + slot), phase ^ 1)) {
             ok = false;
             break;
           }
-          mbar_arrive_expect_tx(bar(B_AF + slot), CHUNK);
-          tma_load_3d(smem_u32(smem + OFF_A + slot * CHUNK), &maps.a, 64 * c, g, m0, bar(B_AF + slot));
+          expect(B_AF + slot, CHUNK);
+          load(B_AF + slot, OFF_A + slot * CHUNK, &maps.a, 64 * c, g, m0);
           if (++slot == NSLOT) slot = 0, phase ^= 1;
         }
       }
-      if (!ok) {  // no copy may land after the CTA is gone
-        if (loads) mbar_wait(bar(B_BF), (loads - 1) & 1);
+      if (!ok && rank == 0) {  // no copy may land after the CTA is gone
+        for (int c = 0; c < (MODE == ABSORB ? 1 : nkc) && loads; ++c) mbar_wait(bar(B_BF + c), (loads - 1) & 1);
         for (int s = 0; s < NSLOT; ++s) mbar_wait(bar(B_AF + s), s < slot ? phase : phase ^ 1);
       }
     }
     __syncwarp();
   } else if (warp == WARP_MMA) {
-    auto wait_u = [&](int b, uint32_t parity) { return __reduce_min_sync(0xffffffffu, (uint32_t)mbar_wait(bar(b), parity)); };
-    const uint64_t a_desc = smem_desc(smem_u32(smem + OFF_A), 16, 1024, SWIZZLE_128B);
-    // absorb's B has its columns contiguous: from one 64-column slice to the next k rows of 128 bytes
-    const uint64_t b_desc = smem_desc(smem_u32(smem + OFF_B), MODE == ABSORB ? p.k * 128 : 16, 1024, SWIZZLE_128B);
-    uint32_t good = __reduce_min_sync(0xffffffffu, (uint32_t)(tmem == 0));
-    const int ut0 = __reduce_min_sync(0xffffffffu, (uint32_t)t0), ut1 = __reduce_min_sync(0xffffffffu, (uint32_t)t1);
-    int slot = 0, phase = 0, unit = -1, loads = 0, d = 0;  // d: accumulators filled so far
-    for (int t = ut0; t < ut1 && good; ++t) {
-      const int u = t / mt, nb = cols_of(u);
-      if (u != unit) {
-        if (unit >= 0) mma_commit_warp(bar(B_BE));
-        unit = u;
-        good = wait_u(B_BF, loads & 1);
-        ++loads;
-      }
-      const int subs = MODE == ABSORB ? (nb + N_MMA - 1) / N_MMA : 1;
-      int s = slot, ph = phase;
-      for (int j = 0; j < subs && good; ++j, ++d) {
-        good = wait_u(B_DE + (d & 1), ((d >> 1) & 1) ^ 1);
-        tc_fence_after_sync();
-        const uint32_t idesc = idesc_f16_f32(TM, min(N_MMA, nb - j * N_MMA), 0, MODE == ABSORB ? 1 : 0, 1);
-        s = slot, ph = phase;
-        for (int c = 0; c < nkc && good; ++c) {
-          if (j == 0) {
-            good = wait_u(B_AF + s, ph);
+    if (rank == 0) {
+      auto wait_u = [&](int b, uint32_t parity) {
+        return __reduce_min_sync(0xffffffffu, (uint32_t)mbar_wait(bar(b), parity));
+      };
+      auto commit = [&](int b) {
+        if constexpr (PAIR) mma_commit_pair_warp(bar(b));
+        else mma_commit_warp(bar(b));
+      };
+      const uint64_t a_desc = smem_desc(smem_u32(smem + OFF_A), 16, 1024, SWIZZLE_128B);
+      // absorb's B has its columns contiguous: from one 64-column slice to the next k rows of 128 bytes
+      const uint64_t b_desc = smem_desc(smem_u32(smem + OFF_B), MODE == ABSORB ? p.k * 128 : 16, 1024, SWIZZLE_128B);
+      uint32_t good = __reduce_min_sync(0xffffffffu, (uint32_t)(tmem == 0));
+      const int ut0 = __reduce_min_sync(0xffffffffu, (uint32_t)t0), ut1 = __reduce_min_sync(0xffffffffu, (uint32_t)t1);
+      int slot = 0, phase = 0, unit = -1, loads = 0, d = 0;  // d: accumulators filled so far
+      for (int t = ut0; t < ut1 && good; ++t) {
+        const int u = t / mt, nb = MODE == EXPAND ? p.n_unit : cols_of(u);
+        const bool fresh = u != unit, last = t + 1 == ut1 || (t + 1) / mt != u;  // of the unit's tiles here
+        if (fresh) unit = u, ++loads;
+        if (MODE == ABSORB && fresh) good = wait_u(B_BF, (loads - 1) & 1);
+        const int subs = MODE == ABSORB ? (nb + N_MMA - 1) / N_MMA : 1;
+        int s = slot, ph = phase;
+        for (int j = 0; j < subs && good; ++j, ++d) {
+          good = wait_u(B_DE + (d & 1), ((d >> 1) & 1) ^ 1);
+          tc_fence_after_sync();
+          const uint32_t idesc = idesc_f16_f32(TROWS, min(N_MMA, nb - j * N_MMA), 0, MODE == ABSORB ? 1 : 0, 1);
+          s = slot, ph = phase;
+          for (int c = 0; c < nkc && good; ++c) {
+            if (MODE != ABSORB && fresh) good = wait_u(B_BF + c, (loads - 1) & 1);
+            if (j == 0 && good) good = wait_u(B_AF + s, ph);
             tc_fence_after_sync();
-          }
-          const uint64_t ad = a_desc + (uint32_t)(s * (CHUNK >> 4));
-          // 16 of k: 32 bytes along a row, or 16 rows of 128 bytes
-          const uint64_t bd = MODE == ABSORB ? b_desc + (uint32_t)(j * (N_MMA / 64) * p.k * 8 + c * 64 * 8)
-                                             : b_desc + (uint32_t)(c * p.n_unit * 8);
-          const int steps = min(4, (p.k - 64 * c) / 16);
-          if (good) {
+            const uint64_t ad = a_desc + (uint32_t)(s * (CHUNK >> 4));
+            // 16 of k: 32 bytes along a row, or 16 rows of 128 bytes
+            const uint64_t bd = MODE == ABSORB ? b_desc + (uint32_t)(j * (N_MMA / 64) * p.k * 8 + c * 64 * 8)
+                                               : b_desc + (uint32_t)(c * b_rows * 8);
+            const int steps = min(4, (p.k - 64 * c) / 16);
+            if (good) {
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              if (kk < steps)
-                mma_f16_ss_warp(N_MMA * (d & 1), ad + 2 * kk, bd + (MODE == ABSORB ? 128 : 2) * kk, idesc, c | kk ? 1u : 0u);
-            if (j == subs - 1) mma_commit_warp(bar(B_AE + s));
+              for (int kk = 0; kk < 4; ++kk)
+                if (kk < steps) {
+                  if constexpr (PAIR)
+                    mma_f16_ss_pair_warp(N_MMA * (d & 1), ad + 2 * kk, bd + 2 * kk, idesc, c | kk ? 1u : 0u);
+                  else
+                    mma_f16_ss_warp(N_MMA * (d & 1), ad + 2 * kk, bd + (MODE == ABSORB ? 128 : 2) * kk, idesc,
+                                    c | kk ? 1u : 0u);
+                }
+              if (j == subs - 1) commit(B_AE + s);
+              if (MODE != ABSORB && last) commit(B_BE + c);
+            }
+            if (++s == NSLOT) s = 0, ph ^= 1;
           }
-          if (++s == NSLOT) s = 0, ph ^= 1;
+          if (good) commit(B_DF + (d & 1));
         }
-        if (good) mma_commit_warp(bar(B_DF + (d & 1)));
+        if (MODE == ABSORB && last && good) commit(B_BE);
+        slot = s, phase = ph;
       }
-      slot = s, phase = ph;
+      if (!good) ok = false;
     }
-    if (!good) ok = false;
   } else if (warp == WARP_ROPE) {
     if (MODE == ABSORB && p.rope_x >= 0 && lane == 0) {
       const uint32_t buf = smem_u32(smem + OFF_A + NSLOT * CHUNK);
@@ -222,7 +259,8 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
     const uint32_t lanes = (uint32_t)(32 * warp) << 16;
     int d = 0, out = 0;
     for (int t = t0; t < t1 && ok; ++t) {
-      const int u = t / mt, m0 = (t - u * mt) * TM + 32 * warp, g = group_of(u), n0 = col_of(u), nb = cols_of(u);
+      const int u = t / mt, m0 = (t - u * mt) * TROWS + rank * TM + 32 * warp, g = group_of(u), n0 = col_of(u);
+      const int nb = MODE == EXPAND ? p.n_unit : cols_of(u);
       float scale = 1.f;
       if constexpr (MODE == EXPAND) scale = m0 + lane < m_all ? __ldg(p.scale + m0 + lane) : 0.f;
       for (int j = 0; j < nb; j += N_MMA, ++d) {
@@ -240,8 +278,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
           if (c + 64 >= width) {  // the accumulator has been read
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_DE + (d & 1)));
+            if (lane == 0) {
+              if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(bar(B_DE + (d & 1)), 0));
+              else mbar_arrive(bar(B_DE + (d & 1)));
+            }
           }
+          if (m0 >= m_all || n0 + j + c >= p.n) continue;
           __align__(16) uint32_t y[32];
 #pragma unroll
           for (int e = 0; e < 32; ++e) {
@@ -255,12 +297,11 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
               __nv_bfloat16* dst = p.out + (int64_t)(m0 + lane) * p.n + n0 + j + c;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (n0 + j + c + 8 * e < p.n && c + 8 * e < width)
+                if (n0 + j + c + 8 * e < p.n)
                   *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
             }
             continue;
           }
-          if (m0 >= m_all) continue;
           const uint32_t to = buf + (out & 1) * STAGE;
           if (lane == 0) tma_store_wait_read<1>();  // the store before the last has left this buffer
           __syncwarp();
@@ -285,9 +326,14 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
   if (!ok && lane == 0) report(p.dev_status, DSA_DEV_TIMEOUT);
   tc_fence_before_sync();
   __syncthreads();
+  if constexpr (PAIR) {  // neither CTA leaves while the other's products read its shared memory
+    cluster_arrive();
+    cluster_wait();
+  }
   if (warp == WARP_MMA) {
     tc_fence_after_sync();
-    tmem_dealloc(tmem, 512);
+    if constexpr (PAIR) tmem_dealloc_pair(tmem, 512);
+    else tmem_dealloc(tmem, 512);
   }
 }
 
@@ -296,9 +342,22 @@ cudaError_t launch_product(const Product& p, const ProductMaps& maps, cudaStream
   auto kernel = product_kernel<MODE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)p.units * ((p.m + TM - 1) / TM), sms = device_sm_count();
-  kernel<<<(unsigned)(tiles < sms ? tiles : sms), THREADS, SMEM_BYTES, stream>>>(p, maps);
-  return cudaGetLastError();
+  constexpr int CTAS = MODE == EXPAND ? 2 : 1;
+  const int64_t tiles = (int64_t)p.units * ((p.m + CTAS * TM - 1) / (CTAS * TM)), workers = device_sm_count() / CTAS;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = CTAS;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(CTAS * (tiles < workers ? tiles : workers)));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  const cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, p, maps);
+  return r != cudaSuccess ? r : cudaGetLastError();
 }
 
 // Columns of a unit: the whole head's, halved while twice as many units still find SMs.
@@ -454,7 +513,7 @@ cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream) {
   if (e != cudaSuccess || a.capacity == 0) return e;
   Product p = {};
   p.m = a.capacity, p.n = a.heads * a.d_kv, p.k = a.d_latent;
-  p.n_unit = 128;
+  p.n_unit = 256;
   p.per_group = p.units = (p.n + p.n_unit - 1) / p.n_unit;
   p.rope_x = -1;
   p.rows = a.cu_k + a.num_req;
@@ -463,7 +522,7 @@ cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream) {
   p.dev_status = a.dev_status;
   ProductMaps maps;
   if (!make_rows_map(&maps.a, x, a.capacity, 1, a.d_latent, a.d_latent, 0, TM) ||
-      !make_rows_map(&maps.b, a.w, p.n, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit) ||
+      !make_rows_map(&maps.b, a.w, p.n, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit / 2) ||
       !make_rows_map(&maps.c, a.kv_out, a.capacity, 1, p.n, p.n, 0, 32))
     return cudaErrorInvalidValue;
   maps.c_rope = maps.c;
