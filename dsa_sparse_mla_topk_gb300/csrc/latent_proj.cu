@@ -18,7 +18,7 @@
 // expand is bound by the tensor cores (512): pairs of CTAs (cta_group::2) take 256 x 256
 // outputs a tile, each holding half of the columns' weights, so that A is half
 // as many bytes a product (with single CTAs of 128 columns, 50 GB/s of A an SM: 16,384
-// rows 283 us).  Warps: 0-3 results, 4 TMA, 5 MMA, 6 the rotated part of the queries, which
+// rows 283 us).  Warps: 0-7 results, 8 TMA, 9 MMA, 10 the rotated part of the queries, which
 // is copied.  All waits are bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -41,16 +41,16 @@ enum Mode { ABSORB, PROJECT, EXPAND };
 constexpr int TM = 128, CHUNK = TM * 128;  // rows of a tile; a chunk of A: 128 rows x 64 columns
 constexpr int SLOTS = 4;                   // chunks of A in flight (absorb: one less, the rotated part's place)
 constexpr int N_MMA = 256;                 // columns of one accumulator; two of them
-constexpr int THREADS = 224, WARP_TMA = 4, WARP_MMA = 5, WARP_ROPE = 6;
+constexpr int OUT_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_ROPE = 10, THREADS = 352;
 constexpr int B_BYTES = 128 * 1024, STAGE = 32 * 128;  // a warp's 32 rows x 64 columns of results
 constexpr int OFF_B = 0;
 constexpr int OFF_A = OFF_B + B_BYTES;
-constexpr int OFF_OUT = OFF_A + SLOTS * CHUNK;    // [4 warps][2]
-constexpr int OFF_BAR = OFF_OUT + 4 * 2 * STAGE;
-constexpr int B_AF = 0;             // [SLOTS] a chunk of A has landed
-constexpr int B_AE = B_AF + SLOTS;  // [SLOTS] its slot is free
+constexpr int OFF_OUT = OFF_A + SLOTS * CHUNK;  // [OUT_WARPS]
+constexpr int OFF_BAR = OFF_OUT + OUT_WARPS * STAGE;
+constexpr int B_AF = 0;             // [SLOTS + 2] a chunk of A has landed
+constexpr int B_AE = B_AF + SLOTS + 2;  // [SLOTS + 2] its slot is free
 constexpr int MAX_KC = 8;           // chunks of k
-constexpr int B_BF = B_AE + SLOTS;  // [MAX_KC] chunk of B of the unit has landed (absorb: [0], all of it)
+constexpr int B_BF = B_AE + SLOTS + 2;  // [MAX_KC] chunk of B of the unit has landed (absorb: [0], all of it)
 constexpr int B_BE = B_BF + MAX_KC; // [MAX_KC] its products are done
 constexpr int B_DF = B_BE + MAX_KC; // [2] an accumulator is complete
 constexpr int B_DE = B_DF + 2;      // [2] it has been read
@@ -72,6 +72,7 @@ struct Product {
   const int32_t* rows;     // expand: the rows there are, on the device
   const float* scale;      // expand: [m]
   __nv_bfloat16* out;      // expand: [m, n]
+  bool wide;               // it is 32-byte aligned
   int32_t* dev_status;
 };
 
@@ -84,7 +85,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
   auto bar = [&](int b) { return smem_u32(bars + b); };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr bool PAIR = MODE == EXPAND;
-  constexpr int NSLOT = MODE == ABSORB ? SLOTS - 1 : SLOTS;
+  constexpr int NSLOT = MODE == ABSORB ? SLOTS - 1 : MODE == EXPAND ? SLOTS + 2 : SLOTS;
   constexpr int CTAS = PAIR ? 2 : 1, TROWS = CTAS * TM;  // rows of a tile
   const int rank = PAIR ? (int)cluster_rank() : 0;
 
@@ -98,7 +99,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
     }
   }
   if (tid == WARP_TMA * 32) {
-    for (int b = 0; b < NBAR; ++b) mbar_init(bar(b), b >= B_DE && b < B_DE + 2 ? 4u * CTAS : 1u);
+    for (int b = 0; b < NBAR; ++b) mbar_init(bar(b), b >= B_DE && b < B_DE + 2 ? (uint32_t)(OUT_WARPS * CTAS) : 1u);
     fence_mbarrier_init();
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b);
@@ -112,33 +113,44 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
   }
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  int m_all = p.m;
-  if constexpr (MODE == EXPAND) m_all = min(max(__ldg(p.rows), 0), p.m);
-  const int mt = (m_all + TROWS - 1) / TROWS;
-  const int64_t tiles = (int64_t)p.units * mt;
   const int workers = gridDim.x / CTAS, worker = blockIdx.x / CTAS;
-  const int t0 = (int)(tiles * worker / workers), t1 = (int)(tiles * (worker + 1) / workers);
   const int nkc = (p.k + 63) / 64;
   const int b_rows = p.n_unit / CTAS;  // columns of a unit whose weights this CTA holds
   // unit u: head (expand: 0) and the first of its columns there
   auto group_of = [&](int u) { return MODE == EXPAND ? 0 : u / p.per_group; };
   auto col_of = [&](int u) { return (u % p.per_group) * p.n_unit; };
   auto cols_of = [&](int u) { return min(p.n_unit, p.n - col_of(u)); };
+  // A barrier's bytes are those of both CTAs, counted on the first one's
+  auto load = [&](int b, int off, const CUtensorMap* map, int x, int y, int z) {
+    if constexpr (PAIR) tma_load_3d_pair(smem_u32(smem + off), map, x, y, z, cluster_addr(bar(b), 0));
+    else tma_load_3d(smem_u32(smem + off), map, x, y, z, bar(b));
+  };
+  auto expect = [&](int b, uint32_t bytes) {
+    if (rank == 0) mbar_arrive_expect_tx(bar(b), bytes * CTAS);
+  };
+  // chunk c of B of unit u: 64 columns of k, b_rows rows (not absorb)
+  auto load_b = [&](int u, int c) {
+    expect(B_BF + c, b_rows * 128);
+    load(B_BF + c, OFF_B + c * b_rows * 128, &maps.b, 64 * c, 0, p.b_row0 + group_of(u) * p.b_group + col_of(u) + rank * b_rows);
+  };
+  int m_all = p.m;
+  if constexpr (MODE == EXPAND) {
+    // the first unit's weights do not depend on the rows (floor(floor(x mt) / mt) = floor(x))
+    if (warp == WARP_TMA && lane == 0)
+      for (int c = 0; c < nkc; ++c) load_b((int)((int64_t)p.units * worker / workers), c);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    m_all = min(max(*reinterpret_cast<const volatile int32_t*>(p.rows), 0), p.m);
+  }
+  const int mt = (m_all + TROWS - 1) / TROWS;
+  const int64_t tiles = (int64_t)p.units * mt;
+  const int t0 = (int)(tiles * worker / workers), t1 = (int)(tiles * (worker + 1) / workers);
   bool ok = true;
 
   if (warp == WARP_TMA) {
     if (lane == 0) {
-      // A barrier's bytes are those of both CTAs, counted on the first one's
-      auto load = [&](int b, int off, const CUtensorMap* map, int x, int y, int z) {
-        if constexpr (PAIR) tma_load_3d_pair(smem_u32(smem + off), map, x, y, z, cluster_addr(bar(b), 0));
-        else tma_load_3d(smem_u32(smem + off), map, x, y, z, bar(b));
-      };
-      auto expect = [&](int b, uint32_t bytes) {
-        if (rank == 0) mbar_arrive_expect_tx(bar(b), bytes * CTAS);
-      };
       int slot = 0, phase = 0, unit = -1, loads = 0;
       for (int t = t0; t < t1 && ok; ++t) {
-        const int u = t / mt, m0 = (t - u * mt) * TROWS + rank * TM, g = group_of(u), n0 = col_of(u) + rank * b_rows;
+        const int u = t / mt, m0 = (t - u * mt) * TROWS + rank * TM, g = group_of(u), n0 = col_of(u);
         const bool fresh = u != unit;
         if (fresh) unit = u, ++loads;
         if (MODE == ABSORB && fresh) {  // slices of 64 columns, k rows each
@@ -151,13 +163,12 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
           for (int s = 0; s < slices; ++s) load(B_BF, OFF_B + s * p.k * 128, &maps.b, n0 + 64 * s, 0, p.b_row0 + g * p.b_group);
         }
         for (int c = 0; c < nkc; ++c) {
-          if (MODE != ABSORB && fresh) {  // 64 columns of k, b_rows rows
+          if (MODE != ABSORB && fresh && !(MODE == EXPAND && loads == 1)) {
             if (!mbar_wait(bar(B_BE + c), (loads & 1))) {
               ok = false;
               break;
             }
-            expect(B_BF + c, b_rows * 128);
-            load(B_BF + c, OFF_B + c * b_rows * 128, &maps.b, 64 * c, 0, p.b_row0 + g * p.b_group + n0);
+            load_b(u, c);
           }
           if (!mbar_wait(bar(B_AE + slot), phase ^ 1)) {
             ok = false;
@@ -168,9 +179,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
           if (++slot == NSLOT) slot = 0, phase ^= 1;
         }
       }
-      if (!ok && rank == 0) {  // no copy may land after the CTA is gone
+      if (MODE == EXPAND && t0 >= t1) loads = 1;
+      if ((!ok || t0 >= t1) && rank == 0) {  // no copy may land after the CTA is gone
         for (int c = 0; c < (MODE == ABSORB ? 1 : nkc) && loads; ++c) mbar_wait(bar(B_BF + c), (loads - 1) & 1);
-        for (int s = 0; s < NSLOT; ++s) mbar_wait(bar(B_AF + s), s < slot ? phase : phase ^ 1);
+        for (int s = 0; s < NSLOT && !ok; ++s) mbar_wait(bar(B_AF + s), s < slot ? phase : phase ^ 1);
       }
     }
     __syncwarp();
@@ -254,15 +266,16 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
     }
     __syncwarp();
   } else {
-    // ---------------- results: warp w has rows 32 w .. + 31 of a tile, one a lane ----------------
-    const uint32_t buf = smem_u32(smem + OFF_OUT + warp * 2 * STAGE);
-    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-    int d = 0, out = 0;
+    // ---- results: warp w has rows 32 (w % 4) .. + 31 of a tile, one a lane, and every other 64 columns ----
+    const uint32_t buf = smem_u32(smem + OFF_OUT + warp * STAGE);
+    const int quad = warp & 3, half = warp >> 2;
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16;
+    int d = 0;
     for (int t = t0; t < t1 && ok; ++t) {
-      const int u = t / mt, m0 = (t - u * mt) * TROWS + rank * TM + 32 * warp, g = group_of(u), n0 = col_of(u);
+      const int u = t / mt, m0 = (t - u * mt) * TROWS + rank * TM + 32 * quad, g = group_of(u), n0 = col_of(u);
       const int nb = MODE == EXPAND ? p.n_unit : cols_of(u);
       float scale = 1.f;
-      if constexpr (MODE == EXPAND) scale = m0 + lane < m_all ? __ldg(p.scale + m0 + lane) : 0.f;
+      if constexpr (MODE == EXPAND) scale = m0 + lane < m_all ? *const_cast<const volatile float*>(p.scale + m0 + lane) : 0.f;
       for (int j = 0; j < nb; j += N_MMA, ++d) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar(B_DF + (d & 1)), (d >> 1) & 1))) {
           ok = false;
@@ -270,19 +283,21 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
         }
         tc_fence_after_sync();
         const int width = min(N_MMA, nb - j);
-        for (int c = 0; c < width; c += 64) {
+        auto read = [&] {  // this warp's share of the accumulator
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) {
+            if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(bar(B_DE + (d & 1)), 0));
+            else mbar_arrive(bar(B_DE + (d & 1)));
+          }
+        };
+        if (64 * half >= width) read();
+        for (int c = 64 * half; c < width; c += 128) {
           float x[64];
           tmem_ld32(N_MMA * (d & 1) + c + lanes, *reinterpret_cast<float(*)[32]>(x));
           if (c + 32 < width) tmem_ld32(N_MMA * (d & 1) + c + 32 + lanes, *reinterpret_cast<float(*)[32]>(x + 32));
           tmem_wait_ld();
-          if (c + 64 >= width) {  // the accumulator has been read
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) {
-              if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(bar(B_DE + (d & 1)), 0));
-              else mbar_arrive(bar(B_DE + (d & 1)));
-            }
-          }
+          if (c + 128 >= width) read();
           if (m0 >= m_all || n0 + j + c >= p.n) continue;
           __align__(16) uint32_t y[32];
 #pragma unroll
@@ -291,32 +306,36 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
                                                     : __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
             y[e] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          if (MODE == EXPAND && m0 + 32 > m_all) {
-            // rows behind the last one stay as they were: no box of 32 rows
+          if (MODE == EXPAND) {
+            // straight to memory, a row's 128 bytes a lane
             if (m0 + lane < m_all) {
               __nv_bfloat16* dst = p.out + (int64_t)(m0 + lane) * p.n + n0 + j + c;
 #pragma unroll
-              for (int e = 0; e < 8; ++e)
-                if (n0 + j + c + 8 * e < p.n)
-                  *reinterpret_cast<uint4*>(dst + 8 * e) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+              for (int e = 0; e < 4; ++e)
+                if (n0 + j + c + 16 * e < p.n) {
+                  if (p.wide) {
+                    store32(dst + 16 * e, y + 8 * e);
+                  } else {
+                    *reinterpret_cast<uint4*>(dst + 16 * e) = make_uint4(y[8 * e], y[8 * e + 1], y[8 * e + 2], y[8 * e + 3]);
+                    *reinterpret_cast<uint4*>(dst + 16 * e + 8) = make_uint4(y[8 * e + 4], y[8 * e + 5], y[8 * e + 6], y[8 * e + 7]);
+                  }
+                }
             }
             continue;
           }
-          const uint32_t to = buf + (out & 1) * STAGE;
-          if (lane == 0) tma_store_wait_read<1>();  // the store before the last has left this buffer
+          if (lane == 0) tma_store_wait_read<0>();  // the store before has left the buffer
           __syncwarp();
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + lane * 128 + ((e ^ (lane & 7)) << 4)),
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((e ^ (lane & 7)) << 4)),
                          "r"(y[4 * e]), "r"(y[4 * e + 1]), "r"(y[4 * e + 2]), "r"(y[4 * e + 3])
                          : "memory");
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(&maps.c, to, n0 + j + c, g, m0);
+            tma_store_3d(&maps.c, buf, n0 + j + c, g, m0);
             tma_store_commit();
           }
-          ++out;
         }
       }
     }
@@ -344,18 +363,20 @@ cudaError_t launch_product(const Product& p, const ProductMaps& maps, cudaStream
   if (e != cudaSuccess) return e;
   constexpr int CTAS = MODE == EXPAND ? 2 : 1;
   const int64_t tiles = (int64_t)p.units * ((p.m + CTAS * TM - 1) / (CTAS * TM)), workers = device_sm_count() / CTAS;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CTAS;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // after the rows' kernel
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(CTAS * (tiles < workers ? tiles : workers)));
   cfg.blockDim = dim3(THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = stream;
   cfg.attrs = attr;
-  cfg.numAttrs = CTAS > 1 ? 1 : 0;
+  cfg.numAttrs = MODE == EXPAND ? 2 : 0;
   const cudaError_t r = cudaLaunchKernelEx(&cfg, kernel, p, maps);
   return r != cudaSuccess ? r : cudaGetLastError();
 }
@@ -372,9 +393,10 @@ int columns_of_unit(int n, int most, int64_t groups_tiles) {
 
 constexpr int EX_THREADS = 256, EX_WARPS = EX_THREADS / 32, EX_ROWS = 32;  // rows a CTA
 
-// Every CTA takes the running sum of the lengths for itself; then a warp a row.
+// Every CTA takes the running sum of the lengths for itself.
 __global__ void __launch_bounds__(EX_THREADS) expand_rows_kernel(const ExpandArgs a, __nv_bfloat16* x, float* scale) {
   extern __shared__ int32_t cu[];  // [num_req + 1]
+  asm volatile("griddepcontrol.launch_dependents;");  // the products' CTAs may get ready meanwhile
   __shared__ int64_t wsum[EX_WARPS];
   __shared__ int64_t fit[EX_WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, R = a.num_req;
@@ -420,40 +442,48 @@ __global__ void __launch_bounds__(EX_THREADS) expand_rows_kernel(const ExpandArg
   if (blockIdx.x == 0)
     for (int r = tid; r <= R; r += EX_THREADS) a.cu_k[r] = min(cu[r], total);
 
-  const int dl = a.d_latent, row_bytes = dl + a.d_rope, chunks = row_bytes / 16;
-  for (int i = warp; i < EX_ROWS; i += EX_WARPS) {
-    const int n = blockIdx.x * EX_ROWS + i;
-    if (n >= total) break;
+  // ---- where the CTA's rows are, a thread a row; then 16 bytes a thread ----
+  __shared__ int32_t s_slot[EX_ROWS];
+  __shared__ float s_scale[EX_ROWS];
+  const int n0 = blockIdx.x * EX_ROWS;
+  if (tid < EX_ROWS && n0 + tid < total) {
+    const int n = n0 + tid;
     int lo = 0, hi = R - 1;  // the request with cu[r] <= n < cu[r + 1]
     while (lo < hi) {
       const int mid = (lo + hi) / 2;
       if (cu[mid + 1] > n) hi = mid;
       else lo = mid + 1;
     }
-    const int pos = n - cu[lo];
-    const int page = a.block_table[(int64_t)lo * a.bt_stride + pos / a.page_size];
+    const int pos = n - cu[lo], page = a.block_table[(int64_t)lo * a.bt_stride + pos / a.page_size];
     const bool good = page >= 0 && page < a.num_pages;
-    if (!good && lane == 0) report(a.dev_status, DSA_DEV_BAD_PAGE);
-    const int64_t slot = (int64_t)page * a.page_size + pos % a.page_size;
-    const float s = good ? a.kv_scale[slot] : 0.f;
-    if (lane == 0) scale[n] = s;
-    for (int c = lane; c < chunks; c += 32) {
-      const uint4 v = good ? *reinterpret_cast<const uint4*>(a.kv + slot * row_bytes + 16 * c) : make_uint4(0, 0, 0, 0);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      const bool rope = 16 * c >= dl;
-      __align__(16) __nv_bfloat162 y[8];
+    if (!good) report(a.dev_status, DSA_DEV_BAD_PAGE);
+    const int slot = good ? page * a.page_size + pos % a.page_size : -1;  // (num_pages page_size < 2^31)
+    const float sc = good ? a.kv_scale[slot] : 0.f;
+    s_slot[tid] = slot;
+    s_scale[tid] = sc;
+    scale[n] = sc;
+  }
+  __syncthreads();
+  const int dl = a.d_latent, row_bytes = dl + a.d_rope, chunks = row_bytes / 16;
+  const int rows = min(EX_ROWS, total - n0);
+  for (int e = tid; e < rows * chunks; e += EX_THREADS) {
+    const int i = e / chunks, c = e - i * chunks, slot = s_slot[i], n = n0 + i;
+    const float sc = s_scale[i];
+    const uint4 v = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.kv + (int64_t)slot * row_bytes) + c) : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const bool rope = 16 * c >= dl;
+    __align__(16) __nv_bfloat162 y[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[e / 2] >> (16 * (e & 1))), __NV_E4M3));
-        float2 f = __half22float2(h);
-        if (rope) f.x *= s, f.y *= s;
-        y[e] = __floats2bfloat162_rn(f.x, f.y);  // (a code is exact in bf16)
-      }
-      __nv_bfloat16* dst = rope ? static_cast<__nv_bfloat16*>(a.k_rope) + (int64_t)n * a.d_rope + (16 * c - dl)
-                                : x + (int64_t)n * dl + 16 * c;
-      *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(y);
-      *reinterpret_cast<uint4*>(dst + 8) = *reinterpret_cast<uint4*>(y + 4);
+    for (int q = 0; q < 8; ++q) {
+      const __half2 h = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[q / 2] >> (16 * (q & 1))), __NV_E4M3));
+      float2 f = __half22float2(h);
+      if (rope) f.x *= sc, f.y *= sc;
+      y[q] = __floats2bfloat162_rn(f.x, f.y);  // (a code is exact in bf16)
     }
+    __nv_bfloat16* dst = rope ? static_cast<__nv_bfloat16*>(a.k_rope) + (int64_t)n * a.d_rope + (16 * c - dl)
+                              : x + (int64_t)n * dl + 16 * c;
+    *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(y);
+    *reinterpret_cast<uint4*>(dst + 8) = *reinterpret_cast<uint4*>(y + 4);
   }
 }
 
@@ -519,6 +549,7 @@ cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream) {
   p.rows = a.cu_k + a.num_req;
   p.scale = scale;
   p.out = static_cast<__nv_bfloat16*>(a.kv_out);
+  p.wide = reinterpret_cast<uintptr_t>(a.kv_out) % 32 == 0;
   p.dev_status = a.dev_status;
   ProductMaps maps;
   if (!make_rows_map(&maps.a, x, a.capacity, 1, a.d_latent, a.d_latent, 0, TM) ||
