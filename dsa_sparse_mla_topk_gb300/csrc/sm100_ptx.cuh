@@ -100,9 +100,10 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
 }
 // A box of shared memory (swizzled as the tensor map says) to a 3-D tensor; what
 // lies outside the tensor is not written.  The coordinates are not negative.
-__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap), "r"(src),
-               "r"(x), "r"(y), "r"(z)
+__device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int x, int y, int z, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
+                   tmap),
+               "r"(src), "r"(x), "r"(y), "r"(z), "l"(policy)
                : "memory");
 }
 // The thread's stores so far as one group; at most N groups that still read shared
@@ -170,10 +171,17 @@ __device__ __forceinline__ void reg_less() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// How L2 treats what is written with it: kept like anything, or the first to go.
+__device__ __forceinline__ uint64_t l2_policy(bool first_to_go) {
+  uint64_t p;
+  if (first_to_go) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+  return p;
+}
 // 32 bytes to global memory (32-byte aligned).
-__device__ __forceinline__ void store32(void* p, const uint32_t* v) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, uint64_t policy) {
+  asm volatile("st.global.L2::cache_hint.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8}, %9;" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "l"(policy)
                : "memory");
 }
 
