@@ -71,7 +71,8 @@ struct Product {
   int rope_x;              // absorb: the rotated part's column in A, -1: none
   const int32_t* rows;     // expand: the rows there are, on the device
   const float* scale;      // expand: [m]
-  __nv_bfloat16* out;      // expand: [m, n]
+  __nv_bfloat16* out;      // not absorb: rows of ldc values, a head after the other
+  int64_t ldc;
   bool wide;               // it is 32-byte aligned
   int32_t* dev_status;
 };
@@ -85,7 +86,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
   auto bar = [&](int b) { return smem_u32(bars + b); };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr bool PAIR = MODE == EXPAND;
-  constexpr int NSLOT = MODE == ABSORB ? SLOTS - 1 : MODE == EXPAND ? SLOTS + 2 : SLOTS;
+  constexpr int NSLOT = MODE == ABSORB ? SLOTS - 1 : SLOTS + 2;
   constexpr int CTAS = PAIR ? 2 : 1, TROWS = CTAS * TM;  // rows of a tile
   const int rank = PAIR ? (int)cluster_rank() : 0;
 
@@ -309,10 +310,10 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
                                                     : __floats2bfloat162_rn(x[2 * e], x[2 * e + 1]);
             y[e] = *reinterpret_cast<const uint32_t*>(&v);
           }
-          if (MODE == EXPAND) {
+          if (MODE != ABSORB) {
             // straight to memory, a row's 128 bytes a lane
             if (m0 + lane < m_all) {
-              __nv_bfloat16* dst = p.out + (int64_t)(m0 + lane) * p.n + n0 + j + c;
+              __nv_bfloat16* dst = p.out + (int64_t)(m0 + lane) * p.ldc + (int64_t)g * p.n + n0 + j + c;
 #pragma unroll
               for (int e = 0; e < 4; ++e)
                 if (n0 + j + c + 16 * e < p.n) {
@@ -522,6 +523,8 @@ cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream) {
   p.per_group = (p.n + p.n_unit - 1) / p.n_unit;
   p.units = a.heads * p.per_group;
   p.b_row0 = a.d_nope, p.b_group = d_w;
+  p.out = static_cast<__nv_bfloat16*>(a.y), p.ldc = (int64_t)a.heads * a.d_v;
+  p.wide = reinterpret_cast<uintptr_t>(a.y) % 32 == 0;
   p.rope_x = -1;
   ProductMaps maps;
   if (!make_rows_map(&maps.a, a.x, a.num_tokens, a.heads, a.d_latent, a.tok_stride, a.head_stride, TM) ||
@@ -551,7 +554,7 @@ cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream) {
   p.rope_x = -1;
   p.rows = a.cu_k + a.num_req;
   p.scale = scale;
-  p.out = static_cast<__nv_bfloat16*>(a.kv_out);
+  p.out = static_cast<__nv_bfloat16*>(a.kv_out), p.ldc = p.n;
   p.wide = reinterpret_cast<uintptr_t>(a.kv_out) % 32 == 0;
   p.dev_status = a.dev_status;
   ProductMaps maps;
