@@ -8,9 +8,11 @@
 // reference m for each query row, p = 2^(c (s - m)), c = scale log2 e, l = sum p, O =
 // sum p v; when m moves by d, l and O take the factor 2^(-c d).
 //
-// One CTA = one head, 256 tokens of one request (two tiles of 128 query rows) and one
-// share of its rows, 128 rows a tile.  TMEM: S of both query tiles (2 x 128 columns;
-// the weights P, bf16, take their place) and O (2 x 128).  Warps:
+// One item of work = one head, 256 tokens of one request (two tiles of 128 query rows)
+// and one share of its rows, 128 rows a tile; one CTA each in the grid, but a CTA that is done
+// takes over one that has not started (cluster launch control), whose queries and
+// first keys arrive while it finishes its own.  TMEM: S of both query tiles (2 x 128
+// columns; the weights P, bf16, take their place) and O (2 x 128).  Warps:
 //  * 0-3 and 4-7: softmax of query tile 0 and 1, one query row a thread.  S comes into
 //    registers once; a row's O is rescaled only when its maximum has risen by more
 //    than 2^8 (weights stay below 2^8, sums far inside fp32).
@@ -19,14 +21,16 @@
 //    two value tiles in flight.
 //  * 9: MMA.  P V of one query tile, then its next Q K^T, then the other's: one tile's
 //    softmax runs under the other's products.
-//  * 10, 11: values that are NaN or infinite are taken out of tiles that some query row
+//  * 10: values that are NaN or infinite are taken out of tiles that some query row
 //    sees only in part (a weight of 0 would turn them into NaN); the few rows that do
 //    see them look them up again at the end.
+//  * 11: the next item.
 // All waits are bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "internal.cuh"
@@ -42,7 +46,7 @@ constexpr int TQ = 128, QT = 2 * TQ;  // query rows of a tile, of a CTA
 constexpr int TK = 128;               // rows of a key tile
 constexpr int CHUNK = 128 * 128;      // 128 rows x 64 columns of bf16, 128-byte swizzle
 constexpr int KSLOTS = 4, VST = 2;    // key chunks and value tiles in flight
-constexpr int THREADS = 384, SM_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_FIX = 10;
+constexpr int THREADS = 384, SM_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_FIX = 10, WARP_NEXT = 11;
 // 384 threads at 168 registers: 2 x 128 x 200 + 128 x 104 = 384 x 168
 constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 104;
 static_assert(128 * (2 * REGS_SOFTMAX + REGS_OTHER) <= THREADS * 168, "no more registers than at launch");
@@ -56,7 +60,8 @@ constexpr int OFF_K = OFF_Q + 2 * 3 * CHUNK;
 constexpr int OFF_V = OFF_K + KSLOTS * CHUNK;
 constexpr int OFF_BAR = OFF_V + VST * 2 * CHUNK;
 constexpr int B_QF = 0;              // [2] query tile g has landed
-constexpr int B_KF = B_QF + 2;       // [KSLOTS] key chunk has landed
+constexpr int B_QE = B_QF + 2;       // [2] its products are done
+constexpr int B_KF = B_QE + 2;       // [KSLOTS] key chunk has landed
 constexpr int B_KE = B_KF + KSLOTS;  // [KSLOTS] its slot is free
 constexpr int B_VF = B_KE + KSLOTS;  // [VST]
 constexpr int B_VE = B_VF + VST;     // [VST]
@@ -65,66 +70,109 @@ constexpr int B_GO = B_VX + VST;     // [VST] a value tile to look through is on
 constexpr int B_SF = B_GO + VST;     // [2] S of query tile g is complete
 constexpr int B_PF = B_SF + 2;       // [2] P is written (and O rescaled)
 constexpr int B_PVD = B_PF + 2;      // [2] P V is done
-constexpr int NBAR = B_PVD + 2;
-constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
+constexpr int B_IF = B_PVD + 2;      // [2] an item is described
+constexpr int B_IE = B_IF + 2;       // [2] all warps are done with it
+constexpr int B_CLC = B_IE + 2;      // the answer about the next CTA
+constexpr int NBAR = B_CLC + 1;
+constexpr int IE_COUNT = SM_WARPS + 3;  // softmax, TMA, MMA and value warps
+constexpr int NCHUNK = 128;             // requests' tiles are summed in so many parts
+struct Item {
+  int32_t req, q0, rows, h, split;  // req -1: padding rows, -2: no more
+  int32_t k0, kv_len, t_begin, t_end;
+  int32_t cnt[2], whole[2];  // tiles of the share that query tile g sees, that all its rows see whole
+  int32_t fix0;              // from this tile on some row may see a tile in part
+  int32_t any_bad;           // a value that is not finite was taken out
+};
+constexpr int OFF_ANSWER = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;
+constexpr int OFF_MISC = OFF_ANSWER + 16;
 struct Misc {
-  int32_t req, q0, rows, any_bad;
-  int32_t wsum[12], wmax[SM_WARPS], wmin[SM_WARPS];
+  Item item[2];
+  alignas(16) int32_t upto[NCHUNK];  // tiles of the requests up to the end of each part (read four at a time)
+  int32_t wsum[4];
   uint32_t tmem;
 };
 constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;  // with alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+static_assert(OFF_ANSWER % 16 == 0 && OFF_MISC % 16 == 0 && offsetof(Misc, upto) % 16 == 0, "16-byte accesses");
 
 struct PromptMaps {
   CUtensorMap q, kv, rope;  // boxes of 64 columns, one head, 128 rows
 };
 
-// The tile that this CTA takes: the requests' tiles of QT tokens one after another, then
-// the padding's (req -1), in `index` order; req -2: none.
-__device__ __forceinline__ void find_tile(const PromptArgs& a, int index, bool tell, Misc* misc) {
+// Tokens of request r from q0 on (0 where its range is none), in tiles of QT.
+__device__ __forceinline__ int tiles_of(const PromptArgs& a, int r, int& q0, int& n) {
+  q0 = __ldg(a.cu_q + r);
+  const int q1 = __ldg(a.cu_q + r + 1);
+  n = q0 >= 0 && q1 >= q0 && q1 <= a.num_tokens ? q1 - q0 : -1;
+  return (n + QT - 1) / QT;
+}
+
+// misc->upto, by the CTA's first NCHUNK threads (a barrier follows).
+__device__ __forceinline__ void sum_tiles(const PromptArgs& a, bool tell, Misc* misc) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (a.num_req + THREADS - 1) / THREADS, r0 = min(tid * per, a.num_req), r1 = min(r0 + per, a.num_req);
-  auto tiles_of = [&](int r, int& q0, int& n) {
-    q0 = __ldg(a.cu_q + r);
-    const int q1 = __ldg(a.cu_q + r + 1);
-    const bool good = q0 >= 0 && q1 >= q0 && q1 <= a.num_tokens;
-    n = good ? q1 - q0 : 0;
-    if (!good && tell) report(a.dev_status, DSA_DEV_BAD_INDEX);
-    return (n + QT - 1) / QT;
-  };
-  int mine = 0, q0, n;
-  for (int r = r0; r < r1; ++r) mine += tiles_of(r, q0, n);
-  mine = min(mine, (int)gridDim.x);  // (ranges that overlap, an error, could add up past 32 bits)
-  int inc = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
-  }
-  if (lane == 31) misc->wsum[warp] = inc;
-  if (tid == 0) misc->req = -2, misc->any_bad = 0;
-  __syncthreads();
-  int all = 0, first = inc - mine;
-  for (int w = 0; w < THREADS / 32; ++w) {
-    if (w < warp) first += misc->wsum[w];
-    all += misc->wsum[w];
-  }
-  if (index >= first && index < first + mine) {
-    int left = index - first;
+  int inc = 0;
+  if (tid < NCHUNK) {
+    const int per = (a.num_req + NCHUNK - 1) / NCHUNK, r0 = min(tid * per, a.num_req), r1 = min(r0 + per, a.num_req);
     for (int r = r0; r < r1; ++r) {
-      const int t = tiles_of(r, q0, n);
-      if (left < t) {
-        misc->req = r, misc->q0 = q0 + left * QT, misc->rows = min(QT, n - left * QT);
-        break;
-      }
-      left -= t;
+      int q0, n;
+      inc += tiles_of(a, r, q0, n);
+      if (n < 0 && tell) report(a.dev_status, DSA_DEV_BAD_INDEX);
     }
-  } else if (index >= all && tid == 0) {
+    inc = min(inc, (int)gridDim.x);  // (ranges that overlap, an error, could add up past 32 bits)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    if (lane == 31) misc->wsum[warp] = inc;
+  }
+  __syncthreads();
+  if (tid < NCHUNK) {
+    for (int w = 0; w < warp; ++w) inc += misc->wsum[w];
+    misc->upto[tid] = inc;
+  }
+}
+
+// Tile `index` of the requests' tiles one after another, then the padding's (req -1);
+// req -2: none.  One warp.
+__device__ __forceinline__ void find_tile(const PromptArgs& a, int index, const Misc* misc, int& req, int& q0, int& rows) {
+  const int lane = threadIdx.x & 31;
+  req = -2, q0 = 0, rows = 0;
+  const int4 u = reinterpret_cast<const int4*>(misc->upto)[lane];  // parts 4 lane .. + 3
+  const int all = __shfl_sync(0xffffffffu, u.w, 31);
+  if (index >= all) {
     const int pad0 = a.num_req > 0 ? min(max(__ldg(a.cu_q + a.num_req), 0), a.num_tokens) : 0;
     const int64_t at = pad0 + (int64_t)(index - all) * QT;
-    if (at < a.num_tokens) misc->req = -1, misc->q0 = (int)at, misc->rows = (int)min((int64_t)QT, a.num_tokens - at);
+    if (at < a.num_tokens) req = -1, q0 = (int)at, rows = (int)min((int64_t)QT, a.num_tokens - at);
+    return;
   }
-  __syncthreads();
+  const int who = __ffs(__ballot_sync(0xffffffffu, u.w > index)) - 1;
+  const int part = u.x > index ? 0 : u.y > index ? 1 : u.z > index ? 2 : 3;
+  const int before = part == 0 ? 0 : part == 1 ? u.x : part == 2 ? u.y : u.z;
+  const int prev = __shfl_up_sync(0xffffffffu, u.w, 1);
+  const int j = 4 * who + __shfl_sync(0xffffffffu, part, who);
+  int left = index - __shfl_sync(0xffffffffu, part == 0 ? (lane == 0 ? 0 : prev) : before, who);
+  const int per = (a.num_req + NCHUNK - 1) / NCHUNK, r1 = min((j + 1) * per, a.num_req);
+  for (int r0 = j * per; r0 < r1; r0 += 32) {
+    int s = 0, n = 0, t = 0;
+    if (r0 + lane < r1) t = tiles_of(a, r0 + lane, s, n);
+    int inc = t;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += v;
+    }
+    const unsigned over = __ballot_sync(0xffffffffu, inc > left);
+    if (over) {
+      const int l = __ffs(over) - 1;
+      const int i = left - __shfl_sync(0xffffffffu, inc - t, l);
+      req = r0 + l;
+      q0 = __shfl_sync(0xffffffffu, s, l) + i * QT;
+      rows = min(QT, __shfl_sync(0xffffffffu, n, l) - i * QT);
+      return;
+    }
+    left -= __shfl_sync(0xffffffffu, inc, 31);
+  }
 }
 
 // Results of a row that sees nothing in this share.
@@ -140,6 +188,36 @@ __device__ __forceinline__ void write_nothing(const PromptArgs& a, int64_t row, 
   }
 }
 
+// Columns d0 .. d0 + n - 1 (16 or 32) of a row's result.
+__device__ __forceinline__ void finish(const PromptArgs& a, const volatile Item& it, float (&o)[32], int d0, int n, int bad0, int bad1,
+                                       bool live, int64_t row, int64_t part, int dn, int dv, int S) {
+  for (int j = bad0; j <= bad1; ++j) {
+    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.kv) + (it.k0 + (int64_t)j) * a.kv_tok_stride +
+                             it.h * a.kv_head_stride + dn + d0;
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < n && !isfinite(__bfloat162float(v[e]))) o[e] = NAN;
+  }
+  if (!live) return;
+  if (S == 1) {
+    uint32_t y[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+      y[e] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * dv + d0);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (8 * e < n) dst[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+  } else {
+    float4* dst = reinterpret_cast<float4*>(a.o_part + part * dv + d0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (4 * e < n) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+  }
+}
+
 // STD: head widths 128 + 64 (rotated) and values of 128, known to the compiler.
 template <bool STD>
 __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps) {
@@ -150,128 +228,196 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
   auto bar = [&](int b) { return smem_u32(bars + b); };
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int dn = STD ? 128 : a.d_nope, dr = STD ? 64 : a.d_rope, dv = STD ? 128 : a.d_v;
-  const int h = blockIdx.y, split = blockIdx.z, S = a.num_splits;
+  const int S = a.num_splits;
 
   if (warp == WARP_MMA) {
     tmem_alloc(smem_u32(&misc->tmem), TM_COLS);
     tmem_relinquish();
   }
   if (tid == WARP_TMA * 32) {
-    for (int b = 0; b < NBAR; ++b) mbar_init(bar(b), b >= B_PF && b < B_PF + 2 ? 4u : b >= B_VX && b < B_VX + VST ? 2u : 1u);
+    for (int b = 0; b < NBAR; ++b)
+      mbar_init(bar(b), b >= B_PF && b < B_PF + 2 ? 4u : b >= B_IE && b < B_IE + 2 ? (uint32_t)IE_COUNT : 1u);
     fence_mbarrier_init();
     tma_prefetch_map(&maps.q);
     tma_prefetch_map(&maps.kv);
     tma_prefetch_map(&maps.rope);
   }
-  // the last tiles first: in causal prompts they see the most
-  const int index = (int)gridDim.x - 1 - (int)blockIdx.x;
-  find_tile(a, index, blockIdx.x == 0 && h == 0 && split == 0, misc);
+  sum_tiles(a, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0, misc);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const int req = misc->req, q0 = misc->q0, rows = misc->rows;
   const uint32_t tmem = misc->tmem;
-
-  // ---- what each row sees ----
-  int k0 = 0, kv_len = 0;
-  if (req >= 0) {
-    k0 = __ldg(a.cu_k + req);
-    const int k1 = __ldg(a.cu_k + req + 1);
-    if (k0 >= 0 && k1 >= k0 && k1 <= a.num_rows) kv_len = k1 - k0;
-    else if (tid == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
-  }
-  int last = -1;  // this thread's query row (softmax warps: row tid)
-  if (tid < QT) {
-    if (req >= 0 && tid < rows) {
-      last = __ldg(a.q_pos + q0 + tid);
-      if (last < -1 || last >= kv_len) {
-        report(a.dev_status, DSA_DEV_BAD_QPOS);
-        last = -1;
-      }
-    }
-    const int mx = __reduce_max_sync(0xffffffffu, last), mn = __reduce_min_sync(0xffffffffu, tid < rows ? last : INT32_MAX);
-    if (lane == 0) misc->wmax[warp] = mx, misc->wmin[warp] = mn;
-  }
-  __syncthreads();
-  int n_g[2], full_g[2];  // tiles that some row of query tile g sees, that all see whole
-#pragma unroll
-  for (int g = 0; g < 2; ++g) {
-    int mx = -1, mn = INT32_MAX;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mx = max(mx, misc->wmax[4 * g + w]), mn = min(mn, misc->wmin[4 * g + w]);
-    n_g[g] = (mx + TK) / TK;  // ceil((mx + 1) / TK)
-    full_g[g] = mn == INT32_MAX ? 0 : (mn + 1) / TK;
-  }
-  const int ntiles = max(n_g[0], n_g[1]);
-  const int t_begin = (int)((int64_t)ntiles * split / S), t_end = (int)((int64_t)ntiles * (split + 1) / S);
-  const int cnt0 = max(0, min(t_end, n_g[0]) - t_begin), cnt1 = max(0, min(t_end, n_g[1]) - t_begin);
-  const int cnt = __reduce_max_sync(0xffffffffu, max(cnt0, cnt1));
-  // local tiles from here on may be seen in part by some row
-  const int fix0 = max(0, min(cnt0 > 0 ? full_g[0] : INT32_MAX, cnt1 > 0 ? full_g[1] : INT32_MAX) - t_begin);
   const int nn = (dn + 63) / 64, nk = nn + (dr > 0 ? 1 : 0), nv = (dv + 63) / 64;
   bool ok = true;
+  // waits for item n's description; false: no more
+  auto next_item = [&](int n) -> bool {
+    if (!__all_sync(0xffffffffu, mbar_wait(bar(B_IF + (n & 1)), (n >> 1) & 1))) {
+      ok = false;
+      return false;
+    }
+    return misc->item[n & 1].req != -2;
+  };
+  auto item_done = [&](int n) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(B_IE + (n & 1)));
+  };
 
-  if (cnt == 0) {
-    if (req != -2)
-      for (int i = warp; i < rows; i += THREADS / 32) write_nothing(a, (int64_t)(q0 + i) * a.heads + h, split, lane, 32);
-  } else if (warp >= SM_WARPS) {
+  if (warp >= SM_WARPS) {
     reg_less<REGS_OTHER>();
-    if (warp == WARP_TMA) {
+    if (warp == WARP_NEXT) {
+      // ---------------- the items ----------------
+      int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z, n = 0, asked = 0;
+      bool room = true;  // item n's place is free
+      for (;;) {
+        int req, q0, rows;
+        // the last tiles first: in causal prompts they see the most
+        find_tile(a, (int)gridDim.x - 1 - x, misc, req, q0, rows);
+        if (req != -2) {
+          int k0 = 0, kv_len = 0;
+          if (req >= 0) {
+            k0 = __ldg(a.cu_k + req);
+            const int k1 = __ldg(a.cu_k + req + 1);
+            if (k0 >= 0 && k1 >= k0 && k1 <= a.num_rows) kv_len = k1 - k0;
+            else if (lane == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
+          }
+          int n_g[2] = {0, 0}, full_g[2] = {0, 0};  // tiles that some row of query tile g sees, that all see whole
+          if (req >= 0) {
+            int mx[2] = {-1, -1}, mn[2] = {INT32_MAX, INT32_MAX}, pos[QT / 32];
+#pragma unroll
+            for (int i = 0; i < QT / 32; ++i) pos[i] = 32 * i + lane < rows ? __ldg(a.q_pos + q0 + 32 * i + lane) : -2;
+#pragma unroll
+            for (int i = 0; i < QT / 32; ++i)
+              if (32 * i + lane < rows) {
+                const int p = pos[i] < -1 || pos[i] >= kv_len ? -1 : pos[i];  // (reported by the softmax threads)
+                mx[i / 4] = max(mx[i / 4], p), mn[i / 4] = min(mn[i / 4], p);
+              }
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              const int top = __reduce_max_sync(0xffffffffu, mx[g]), low = __reduce_min_sync(0xffffffffu, mn[g]);
+              n_g[g] = (top + TK) / TK;  // ceil((top + 1) / TK)
+              full_g[g] = low == INT32_MAX ? 0 : (low + 1) / TK;
+            }
+          }
+          const int ntiles = max(n_g[0], n_g[1]);
+          const int t_begin = (int)((int64_t)ntiles * z / S), t_end = (int)((int64_t)ntiles * (z + 1) / S);
+          if (lane == 0) {
+            Item& it = misc->item[n & 1];
+            it.req = req, it.q0 = q0, it.rows = rows, it.h = y, it.split = z;
+            it.k0 = k0, it.kv_len = kv_len, it.t_begin = t_begin, it.t_end = t_end, it.any_bad = 0;
+            int fix0 = INT32_MAX;
+#pragma unroll
+            for (int g = 0; g < 2; ++g) {
+              it.cnt[g] = max(0, min(t_end, n_g[g]) - t_begin);
+              it.whole[g] = max(0, full_g[g] - t_begin);
+              if (it.cnt[g] > 0) fix0 = min(fix0, it.whole[g]);
+            }
+            it.fix0 = fix0;
+            mbar_arrive(bar(B_IF + (n & 1)));
+          }
+          __syncwarp();
+          ++n;
+          room = false;
+        }
+        // (one item ahead, no more: the last ones are shared out evenly)
+        if (!room && !__all_sync(0xffffffffu, mbar_wait(bar(B_IE + (n & 1)), ((n >> 1) & 1) ^ 1))) {
+          ok = false;
+          break;
+        }
+        room = true;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(B_CLC), 16);
+          clc_try_cancel(smem_u32(smem + OFF_ANSWER), bar(B_CLC));
+        }
+        __syncwarp();
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_CLC), asked & 1))) {
+          ok = false;
+          break;
+        }
+        ++asked;
+        const bool more = clc_answer(smem_u32(smem + OFF_ANSWER), x, y, z);
+        fence_proxy_async_smem();  // (the next answer is written behind this read)
+        __syncwarp();
+        if (!__any_sync(0xffffffffu, more)) break;
+      }
+      if (ok && lane == 0) {
+        misc->item[n & 1].req = -2;
+        mbar_arrive(bar(B_IF + (n & 1)));
+      }
+    } else if (warp == WARP_TMA) {
       // ---------------- TMA warp ----------------
-      if (lane == 0) {
-        auto query = [&](int g) {
-          mbar_arrive_expect_tx(bar(B_QF + g), nk * CHUNK);
-          for (int c = 0; c < nk; ++c)
-            tma_load_3d(smem_u32(smem + OFF_Q + (3 * g + c) * CHUNK), &maps.q, c < nn ? 64 * c : dn, h, q0 + TQ * g,
-                        bar(B_QF + g));
-        };
-        int slot = 0, phase = 0;  // of the next key chunk
-        for (int lt = 0; lt < cnt && ok; ++lt) {
-          if (lt == 0 && cnt0 > 0) query(0);
-          const int n0 = k0 + (t_begin + lt) * TK;
-          for (int c = 0; c < nk; ++c) {
-            if (!mbar_wait(bar(B_KE + slot), phase ^ 1)) {
+      int slot = 0, phase = 0, vt = 0, qn0 = 0, qn1 = 0;  // of the next key chunk; value tiles and queries loaded so far
+      for (int n = 0; next_item(n); ++n) {
+        const Item it = misc->item[n & 1];
+        const int cnt = max(it.cnt[0], it.cnt[1]);
+        if (lane == 0) {
+          auto query = [&](int g) {
+            if (!ok || !mbar_wait(bar(B_QE + g), ((g ? qn1 : qn0) & 1) ^ 1)) {
+              ok = false;
+              return;
+            }
+            if (g) ++qn1;
+            else ++qn0;
+            mbar_arrive_expect_tx(bar(B_QF + g), nk * CHUNK);
+            for (int c = 0; c < nk; ++c)
+              tma_load_3d(smem_u32(smem + OFF_Q + (3 * g + c) * CHUNK), &maps.q, c < nn ? 64 * c : dn, it.h, it.q0 + TQ * g,
+                          bar(B_QF + g));
+          };
+          for (int lt = 0; lt < cnt && ok; ++lt) {
+            if (lt == 0 && it.cnt[0] > 0) query(0);
+            const int n0 = it.k0 + (it.t_begin + lt) * TK;
+            for (int c = 0; c < nk && ok; ++c) {
+              if (!mbar_wait(bar(B_KE + slot), phase ^ 1)) {
+                ok = false;
+                break;
+              }
+              mbar_arrive_expect_tx(bar(B_KF + slot), CHUNK);
+              const uint32_t dst = smem_u32(smem + OFF_K + slot * CHUNK);
+              if (c < nn) tma_load_3d(dst, &maps.kv, 64 * c, it.h, n0, bar(B_KF + slot));
+              else tma_load_3d(dst, &maps.rope, 0, 0, n0, bar(B_KF + slot));
+              if (++slot == KSLOTS) slot = 0, phase ^= 1;
+            }
+            if (lt == 0 && it.cnt[1] > 0) query(1);
+            const int s = vt % VST;
+            if (!ok || !mbar_wait(bar(B_VE + s), ((vt / VST) & 1) ^ 1)) {
               ok = false;
               break;
             }
-            mbar_arrive_expect_tx(bar(B_KF + slot), CHUNK);
-            const uint32_t dst = smem_u32(smem + OFF_K + slot * CHUNK);
-            if (c < nn) tma_load_3d(dst, &maps.kv, 64 * c, h, n0, bar(B_KF + slot));
-            else tma_load_3d(dst, &maps.rope, 0, 0, n0, bar(B_KF + slot));
-            if (++slot == KSLOTS) slot = 0, phase ^= 1;
+            if (lt >= it.fix0) mbar_arrive(bar(B_GO + s));
+            mbar_arrive_expect_tx(bar(B_VF + s), nv * CHUNK);
+            for (int c = 0; c < nv; ++c)
+              tma_load_3d(smem_u32(smem + OFF_V + (2 * s + c) * CHUNK), &maps.kv, dn + 64 * c, it.h, n0, bar(B_VF + s));
+            ++vt;
           }
-          if (lt == 0 && cnt1 > 0) query(1);
-          const int s = lt % VST;
-          if (!ok || !mbar_wait(bar(B_VE + s), ((lt / VST) & 1) ^ 1)) {
-            ok = false;
-            break;
-          }
-          if (lt >= fix0) mbar_arrive(bar(B_GO + s));
-          mbar_arrive_expect_tx(bar(B_VF + s), nv * CHUNK);
-          for (int c = 0; c < nv; ++c)
-            tma_load_3d(smem_u32(smem + OFF_V + (2 * s + c) * CHUNK), &maps.kv, dn + 64 * c, h, n0, bar(B_VF + s));
         }
-        if (!ok) {  // no copy may land after the CTA is gone
-          for (int g = 0; g < 2; ++g)
-            if (g ? cnt1 > 0 : cnt0 > 0) mbar_wait(bar(B_QF + g), 0);
-          for (int s = 0; s < KSLOTS; ++s) mbar_wait(bar(B_KF + s), s < slot ? phase : phase ^ 1);
+        if (!__all_sync(0xffffffffu, ok)) {
+          ok = false;
+          break;
         }
+        item_done(n);
+      }
+      if (!ok && lane == 0) {  // no copy may land after the CTA is gone
+        if (qn0 > 0) mbar_wait(bar(B_QF), (qn0 - 1) & 1);
+        if (qn1 > 0) mbar_wait(bar(B_QF + 1), (qn1 - 1) & 1);
+        for (int s = 0; s < KSLOTS; ++s) mbar_wait(bar(B_KF + s), s < slot ? phase : phase ^ 1);
+        for (int v = max(0, vt - VST); v < vt; ++v) mbar_wait(bar(B_VF + v % VST), (v / VST) & 1);
       }
       __syncwarp();
     } else if (warp == WARP_MMA) {
       // ---------------- MMA warp ----------------
       const uint32_t ID_QK = idesc_f16_f32(TQ, TK, 0, 0, 1);
       const uint32_t ID_PV = STD ? idesc_f16_f32(TQ, 128, 0, 1, 1) : idesc_f16_f32(TQ, dv, 0, 1, 1);
+      // (reductions over the warp: their results are in uniform registers)
       auto wait_u = [&](int b, uint32_t parity) { return __reduce_min_sync(0xffffffffu, (uint32_t)mbar_wait(bar(b), parity)); };
+      auto uniform = [&](int v) { return (int)__reduce_max_sync(0xffffffffu, (uint32_t)v); };
       const uint64_t q_desc = smem_desc(smem_u32(smem + OFF_Q), 16, 1024, SWIZZLE_128B);
       const uint64_t k_desc = smem_desc(smem_u32(smem + OFF_K), 16, 1024, SWIZZLE_128B);
       const uint64_t v_desc = smem_desc(smem_u32(smem + OFF_V), CHUNK, 1024, SWIZZLE_128B);
-      const int c0 = __reduce_max_sync(0xffffffffu, cnt0), c1 = __reduce_max_sync(0xffffffffu, cnt1);
-      const int fix = __reduce_max_sync(0xffffffffu, fix0);
       uint32_t good = __reduce_min_sync(0xffffffffu, (uint32_t)(tmem == 0));
-      int slot = 0, phase = 0;  // of the first key chunk of the tile to come
+      int slot = 0, phase = 0;           // of the first key chunk of the tile to come
+      int vs = 0, vphase = 0, vx = 0;    // value stage, its phase, and the phases of B_VX (a bit each)
+      int pn0 = 0, pn1 = 0, qn0 = 0, qn1 = 0;  // phases of B_PF and B_QF
       // S_g = Q_g K^T; the last of the tile's users frees its chunks
-      auto issue_qk = [&](int g, bool first_user, bool last_user) {
+      auto issue_qk = [&](int g, bool first_user, bool last_user, bool last_tile) {
         int s = slot, ph = phase;
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
@@ -291,203 +437,244 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
             if (++s == KSLOTS) s = 0, ph ^= 1;
           }
         }
-        if (good) mma_commit_warp(bar(B_SF + g));
+        if (good) {
+          mma_commit_warp(bar(B_SF + g));
+          if (last_tile) mma_commit_warp(bar(B_QE + g));
+        }
         if (last_user) slot = s, phase = ph;
       };
-      auto issue_pv = [&](int g, int lt, bool last_user) {
-        const uint64_t vb = v_desc + (uint32_t)((lt % VST) * (2 * CHUNK >> 4));
+      auto issue_pv = [&](int g, uint32_t acc, bool last_user) {
+        const uint64_t vb = v_desc + (uint32_t)(vs * (2 * CHUNK >> 4));
 #pragma unroll
         for (int kk = 0; kk < TK / 16; ++kk)
-          mma_f16_ts_warp(TM_O + 128 * g, TM_S + 128 * g + 8 * kk, vb + 128 * kk, ID_PV, lt > 0 || kk > 0 ? 1u : 0u);
+          mma_f16_ts_warp(TM_O + 128 * g, TM_S + 128 * g + 8 * kk, vb + 128 * kk, ID_PV, kk > 0 ? 1u : acc);
         mma_commit_warp(bar(B_PVD + g));
-        if (last_user) mma_commit_warp(bar(B_VE + lt % VST));
+        if (last_user) mma_commit_warp(bar(B_VE + vs));
       };
-      if (c0 > 0 && good) {
-        good = wait_u(B_QF, 0);
-        issue_qk(0, true, c1 == 0);
-      }
-      if (c1 > 0 && good) {
-        good = wait_u(B_QF + 1, 0);
-        tc_fence_after_sync();
-        issue_qk(1, c0 == 0, true);
-      }
-      for (int lt = 0; lt < cnt && good; ++lt) {
-        good = wait_u(B_VF + lt % VST, (lt / VST) & 1);
-        if (lt >= fix && good) good = wait_u(B_VX + lt % VST, ((lt - fix) / VST) & 1);
+      for (int n = 0; good; ++n) {
+        // (every branch here hangs on a reduction's result: what a load or a vote decides would take the
+        // loop's values out of the uniform registers, and an MMA's issue would cost twice as much)
+        good = wait_u(B_IF + (n & 1), (n >> 1) & 1);
+        const Item* it = &misc->item[n & 1];
+        if (!good || uniform(it->req) == -2) break;
+        const int c0 = uniform(it->cnt[0]), c1 = uniform(it->cnt[1]), fix = uniform(it->fix0), cnt = max(c0, c1);
+        slot = uniform(slot), phase = uniform(phase), vs = uniform(vs), vphase = uniform(vphase), vx = uniform(vx);
+        pn0 = uniform(pn0), pn1 = uniform(pn1);
+        if (c0 > 0) {
+          good = wait_u(B_QF, qn0);
+          qn0 ^= 1;
+          tc_fence_after_sync();
+          issue_qk(0, true, c1 == 0, c0 == 1);
+        }
+        if (c1 > 0 && good) {
+          good = wait_u(B_QF + 1, qn1);
+          qn1 ^= 1;
+          tc_fence_after_sync();
+          issue_qk(1, c0 == 0, true, c1 == 1);
+        }
+        for (int lt = 0; lt < cnt && good; ++lt) {
+          good = wait_u(B_VF + vs, vphase);
+          if (lt >= fix && good) {
+            good = wait_u(B_VX + vs, (vx >> vs) & 1);
+            vx ^= 1 << vs;
+          }
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const int mine = g ? c1 : c0, other = g ? c0 : c1;
-          if (lt < mine && good) {
-            good = wait_u(B_PF + g, lt & 1);
-            tc_fence_after_sync();
-            if (good) {
-              issue_pv(g, lt, g == 1 || lt >= other);
-              if (lt + 1 < mine) issue_qk(g, g == 0 || lt + 1 >= other, g == 1 || lt + 1 >= other);
+          for (int g = 0; g < 2; ++g) {
+            const int mine = g ? c1 : c0, other = g ? c0 : c1;
+            if (lt < mine && good) {
+              good = wait_u(B_PF + g, g ? pn1 : pn0);
+              if (g) pn1 ^= 1;
+              else pn0 ^= 1;
+              tc_fence_after_sync();
+              if (good) {
+                issue_pv(g, lt > 0 ? 1u : 0u, g == 1 || lt >= other);
+                if (lt + 1 < mine)
+                  issue_qk(g, g == 0 || lt + 1 >= other, g == 1 || lt + 1 >= other, lt + 2 == mine);
+              }
             }
           }
+          if (++vs == VST) vs = 0, vphase ^= 1;
         }
+        item_done(n);
       }
       if (!good) ok = false;
-    } else {
+    } else if (warp == WARP_FIX) {
       // ---------------- values that are not finite ----------------
-      const int t = tid - WARP_FIX * 32;  // rows t and t + 64 of a tile
-      for (int lt = fix0; lt < cnt; ++lt) {
-        const int s = lt % VST;
-        // (B_VF alone would not do: a wait on a barrier whose phase before the one that is meant
-        // has not ended returns at once)
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_GO + s), ((lt - fix0) / VST) & 1) &&
-                                         mbar_wait(bar(B_VF + s), (lt / VST) & 1))) {
-          ok = false;
-          break;
-        }
-        for (int half = 0; half < 2; ++half) {
-          unsigned char* row = smem + OFF_V + 2 * s * CHUNK + (t + 64 * half) * 128;
-          uint32_t odd = 0;
-          for (int c = 0; c < nv; ++c)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {  // (every lane at another bank; the order does not matter)
-              const uint4 v = *reinterpret_cast<const uint4*>(row + c * CHUNK + 16 * ((e + lane) & 7));
-              // an exponent of ones carries into the sign's place
-              auto look = [&](uint32_t w) { odd |= (w & 0x7f807f80u) + 0x00800080u; };
-              look(v.x), look(v.y), look(v.z), look(v.w);
-            }
-          if (odd & 0x80008000u) {
-            for (int c = 0; c < nv; ++c)
-              for (int e = 0; e < 64; ++e) {
-                uint16_t* v = reinterpret_cast<uint16_t*>(row + c * CHUNK) + e;
-                if ((*v & 0x7f80u) == 0x7f80u) *v = 0;
-              }
-            misc->any_bad = 1;
+      int vt = 0, go = 0;  // value tiles so far, phases of B_GO (a bit each)
+      for (int n = 0; ok && next_item(n); ++n) {
+        const Item* it = &misc->item[n & 1];
+        const int cnt = max(it->cnt[0], it->cnt[1]);
+        for (int lt = min(it->fix0, cnt); lt < cnt; ++lt) {
+          const int v = vt + lt, s = v % VST;
+          // (B_VF alone would not do: a wait on a barrier whose phase before the one that is meant
+          // has not ended returns at once)
+          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_GO + s), (go >> s) & 1) && mbar_wait(bar(B_VF + s), (v / VST) & 1))) {
+            ok = false;
+            break;
           }
+          go ^= 1 << s;
+          for (int r = lane; r < TK; r += 32) {
+            unsigned char* row = smem + OFF_V + 2 * s * CHUNK + r * 128;
+            uint32_t odd = 0;
+            for (int c = 0; c < nv; ++c)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {  // (every lane at another bank; the order does not matter)
+                const uint4 w = *reinterpret_cast<const uint4*>(row + c * CHUNK + 16 * ((e + lane) & 7));
+                // an exponent of ones carries into the sign's place
+                auto look = [&](uint32_t u) { odd |= (u & 0x7f807f80u) + 0x00800080u; };
+                look(w.x), look(w.y), look(w.z), look(w.w);
+              }
+            if (odd & 0x80008000u) {
+              for (int c = 0; c < nv; ++c)
+                for (int e = 0; e < 64; ++e) {
+                  uint16_t* u = reinterpret_cast<uint16_t*>(row + c * CHUNK) + e;
+                  if ((*u & 0x7f80u) == 0x7f80u) *u = 0;
+                }
+              misc->item[n & 1].any_bad = 1;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(B_VX + s));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(B_VX + s));
+        vt += cnt;
+        item_done(n);
       }
     }
   } else {
     // ---------------- softmax warps ----------------
     reg_more<REGS_SOFTMAX>();
-    const int g = warp >> 2, mine = g ? cnt1 : cnt0;
-    const int whole = max(0, (g ? full_g[1] : full_g[0]) - t_begin);  // local tiles that all rows see whole
+    const int g = warp >> 2;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, ts = TM_S + 128 * g + lanes, to = TM_O + 128 * g + lanes;
     const float c = fmaxf(a.softmax_scale * LOG2E, 0x1p-120f);  // (0 would make NaN of masked logits)
-    float m = -INFINITY;
-    uint64_t l2 = 0;
-    for (int lt = 0; lt < mine; ++lt) {
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SF + g), lt & 1))) {
+    int sn = 0;  // tiles so far
+    for (int n = 0; ok && next_item(n); ++n) {
+      const volatile Item& it = misc->item[n & 1];  // (read again where it is needed: the loop needs the registers)
+      const int mine = it.cnt[g], whole = it.whole[g], tile0 = it.t_begin;
+      if (max(it.cnt[0], it.cnt[1]) == 0) {
+        for (int i = warp; i < it.rows; i += SM_WARPS)
+          write_nothing(a, (int64_t)(it.q0 + i) * a.heads + it.h, it.split, lane, 32);
+      }
+      int last = -1;  // this thread's query row
+      if (it.req >= 0 && tid < it.rows) {
+        last = __ldg(a.q_pos + it.q0 + tid);
+        if (last < -1 || last >= it.kv_len) {
+          report(a.dev_status, DSA_DEV_BAD_QPOS);
+          last = -1;
+        }
+      }
+      float m = -INFINITY;
+      uint64_t l2 = 0;
+      for (int lt = 0; lt < mine; ++lt, ++sn) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SF + g), sn & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        float s[TK];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, *reinterpret_cast<float(*)[32]>(s + 32 * b));
+        tmem_wait_ld();
+        if (lt >= whole) {
+          const int seen = last - (tile0 + lt) * TK;
+#pragma unroll
+          for (int j = 0; j < TK; ++j) s[j] = j <= seen ? s[j] : -INFINITY;
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < TK; j += 4)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
+        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);  // (not NaN)
+        const bool move = (top - m) * c > RISE;
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? ex2((m - top) * c) : 1.f;
+          if (move) m = top;
+          l2 = mul2(l2, pk2(f, f));
+          if (lt > 0) {
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            for (int b = 0; b < dv / 16; ++b) {
+              float o[16];
+              tmem_ld16(to + 16 * b, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tmem_st16(to + 16 * b, o);
+            }
+          }
+        }
+        const float ref = m == -INFINITY ? 0.f : m;
+        const uint64_t ref2 = pk2(-ref, -ref), c2 = pk2(c, c);
+        uint64_t sum[2] = {0, 0};
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          uint32_t p[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            // (s - m first: it is exact where it matters, however large both are)
+            const uint64_t x = mul2(add2(pk2(s[64 * b + 2 * j], s[64 * b + 2 * j + 1]), ref2), c2);
+            float x0, x1;
+            upk2(x, x0, x1);
+            x0 = ex2(x0), x1 = ex2(x1);
+            sum[j & 1] = add2(sum[j & 1], pk2(x0, x1));
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
+            p[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          tmem_st32(ts + 32 * b, p);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PF + g));
+        l2 = add2(l2, add2(sum[0], sum[1]));
+      }
+      if (!ok) break;
+      if (mine > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) {
         ok = false;
         break;
       }
       tc_fence_after_sync();
-      float s[TK];
+      float la, lb;
+      upk2(l2, la, lb);
+      const float l = la + lb;
+      const int64_t row = (int64_t)(it.q0 + tid) * a.heads + it.h, part = (int64_t)it.split * a.num_tokens * a.heads + row;
+      const bool live = tid < it.rows;
+      if (mine == 0) {
+        if (live && it.cnt[g ^ 1] > 0) write_nothing(a, row, it.split, 0, 1);
+      } else {
+        const bool any = !(l == 0.f);  // (NaN counts)
+        const float inv = any ? 1.f / l : 0.f;
+        // values that were taken out, and that this row sees
+        const bool look = it.any_bad != 0;
+        const int bad0 = look ? (it.t_begin + it.fix0) * TK : INT32_MAX, bad1 = min(last, it.t_end * TK - 1);
+        for (int b = 0; b < dv / 32; ++b) {
+          float o[32];
+          tmem_ld32(to + 32 * b, o);
+          tmem_wait_ld();
 #pragma unroll
-      for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, *reinterpret_cast<float(*)[32]>(s + 32 * b));
-      tmem_wait_ld();
-      if (lt >= whole) {
-        const int seen = last - (t_begin + lt) * TK;
-#pragma unroll
-        for (int j = 0; j < TK; ++j) s[j] = j <= seen ? s[j] : -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int j = 4; j < TK; j += 4)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
-      const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);  // (not NaN)
-      const bool move = (top - m) * c > RISE;
-      if (__any_sync(0xffffffffu, move)) {
-        const float f = move ? ex2((m - top) * c) : 1.f;
-        if (move) m = top;
-        l2 = mul2(l2, pk2(f, f));
-        if (lt > 0) {
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (lt - 1) & 1))) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          for (int b = 0; b < dv / 16; ++b) {
-            float o[16];
-            tmem_ld16(to + 16 * b, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= f;
-            tmem_st16(to + 16 * b, o);
-          }
+          for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * inv : 0.f;
+          finish(a, it, o, 32 * b, 32, bad0, bad1, live, row, part, dn, dv, S);
         }
-      }
-      const float ref = m == -INFINITY ? 0.f : m;
-      const uint64_t ref2 = pk2(-ref, -ref), c2 = pk2(c, c);
-      uint64_t sum[2] = {0, 0};
+        if (dv % 32) {
+          float o[32];
+          tmem_ld16(to + dv - 16, *reinterpret_cast<float(*)[16]>(o));
+          tmem_wait_ld();
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t p[32];
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          // (s - m first: it is exact where it matters, however large both are)
-          const uint64_t x = mul2(add2(pk2(s[64 * b + 2 * j], s[64 * b + 2 * j + 1]), ref2), c2);
-          float x0, x1;
-          upk2(x, x0, x1);
-          x0 = ex2(x0), x1 = ex2(x1);
-          sum[j & 1] = add2(sum[j & 1], pk2(x0, x1));
-          const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
-          p[j] = *reinterpret_cast<const uint32_t*>(&y);
-        }
-        tmem_st32(ts + 32 * b, p);
-      }
-      tmem_wait_st();
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_PF + g));
-      l2 = add2(l2, add2(sum[0], sum[1]));
-    }
-    if (mine > 0 && ok && !__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (mine - 1) & 1))) ok = false;
-    tc_fence_after_sync();
-    float la, lb;
-    upk2(l2, la, lb);
-    const float l = la + lb;
-    const int64_t row = (int64_t)(q0 + tid) * a.heads + h, part = (int64_t)split * a.num_tokens * a.heads + row;
-    const bool live = tid < rows && ok;
-    if (mine == 0) {
-      if (live) write_nothing(a, row, split, 0, 1);
-    } else {
-      const bool any = !(l == 0.f);  // (NaN counts)
-      const float inv = any ? 1.f / l : 0.f;
-      // values that were taken out, and that this row sees
-      const int bad0 = misc->any_bad ? (t_begin + fix0) * TK : INT32_MAX, bad1 = min(last, t_end * TK - 1);
-      for (int b = 0; b < dv / 16; ++b) {
-        float o[16];
-        tmem_ld16(to + 16 * b, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] = any ? o[e] * inv : 0.f;
-        for (int j = bad0; j <= bad1; ++j) {
-          const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(a.kv) + (k0 + (int64_t)j) * a.kv_tok_stride +
-                                   h * a.kv_head_stride + dn + 16 * b;
-#pragma unroll
-          for (int e = 0; e < 16; ++e)
-            if (!isfinite(__bfloat162float(v[e]))) o[e] = NAN;
+          for (int e = 0; e < 16; ++e) o[e] = any ? o[e] * inv : 0.f;
+          finish(a, it, o, dv - 16, 16, bad0, bad1, live, row, part, dn, dv, S);
         }
         if (live) {
-          if (S == 1) {
-            __align__(16) __nv_bfloat162 y[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * dv + 16 * b);
-            dst[0] = reinterpret_cast<uint4*>(y)[0];
-            dst[1] = reinterpret_cast<uint4*>(y)[1];
-          } else {
-            float4* dst = reinterpret_cast<float4*>(a.o_part + part * dv + 16 * b);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-          }
+          const float z = any ? m * a.softmax_scale + __logf(l) : -INFINITY;
+          if (S > 1) a.lse_part[part] = z;
+          else if (a.lse) a.lse[row] = z;
         }
       }
-      if (live) {
-        const float z = any ? m * a.softmax_scale + __logf(l) : -INFINITY;
-        if (S > 1) a.lse_part[part] = z;
-        else if (a.lse) a.lse[row] = z;
-      }
+      tc_fence_before_sync();
+      item_done(n);
     }
     tc_fence_before_sync();
   }

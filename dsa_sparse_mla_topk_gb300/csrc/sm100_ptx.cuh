@@ -416,5 +416,30 @@ __device__ __forceinline__ void mma_commit_pair_warp(uint32_t bar) {
       : "memory");
 }
 
+// ---- work from the grid (cluster launch control) --------------------------------------
+
+// Takes over a CTA of this grid that has not started; the answer (16 bytes, 16-byte
+// aligned) completes its bytes on `bar`.  Not asked again after a refusal.
+__device__ __forceinline__ void clc_try_cancel(uint32_t answer, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   answer),
+               "r"(bar)
+               : "memory");
+}
+// Whether there was one, and which.
+__device__ __forceinline__ bool clc_answer(uint32_t answer, int& x, int& y, int& z) {
+  uint32_t ok, cx = 0, cy = 0, cz = 0;
+  asm volatile(
+      "{\n\t.reg .b128 r;\n\t.reg .pred p;\n\tld.shared.b128 r, [%4];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\tselp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, %2, %3, _}, r;\n\t}"
+      : "=r"(ok), "=r"(cx), "=r"(cy), "=r"(cz)
+      : "r"(answer)
+      : "memory");
+  x = (int)cx, y = (int)cy, z = (int)cz;
+  return ok != 0;
+}
+
 }  // namespace sm100
 }  // namespace dsa
