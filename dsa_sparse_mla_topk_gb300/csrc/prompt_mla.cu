@@ -13,18 +13,20 @@
 // takes over one that has not started (cluster launch control), whose queries and
 // first keys arrive while it finishes its own.  TMEM: S of both query tiles (2 x 128
 // columns; the weights P, bf16, take their place) and O (2 x 128).  Warps:
-//  * 0-3 and 4-7: softmax of query tile 0 and 1, one query row a thread.  S comes into
-//    registers once; a row's O is rescaled only when its maximum has risen by more
-//    than 2^8 (weights stay below 2^8, sums far inside fp32).
-//  * 8: TMA.  A tile's key is two 64-column chunks of the head's own and one of the
+//  * 0-7 and 8-15: softmax of query tile 0 and 1, two threads a query row, 64 keys each, who
+//    exchange their maxima: what lies between a tile's S and its P must be less
+//    than the other tile's products take (1,280 cycles; with a thread a row, about
+//    1,600).  S comes into registers once; a row's O is rescaled only when its maximum
+//    has risen by more than 2^8 (weights stay below 2^8, sums far inside fp32).
+//  * 16: TMA.  A tile's key is two 64-column chunks of the head's own and one of the
 //    shared rotated part (never copied to the heads), its value two; four key chunks and
 //    two value tiles in flight.
-//  * 9: MMA.  P V of one query tile, then its next Q K^T, then the other's: one tile's
+//  * 17: MMA.  P V of one query tile, then its next Q K^T, then the other's: one tile's
 //    softmax runs under the other's products.
-//  * 10: values that are NaN or infinite are taken out of tiles that some query row
+//  * 18: values that are NaN or infinite are taken out of tiles that some query row
 //    sees only in part (a weight of 0 would turn them into NaN); the few rows that do
 //    see them look them up again at the end.
-//  * 11: the next item.
+//  * 19: the next item.
 // All waits are bounded.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -46,12 +48,14 @@ constexpr int TQ = 128, QT = 2 * TQ;  // query rows of a tile, of a CTA
 constexpr int TK = 128;               // rows of a key tile
 constexpr int CHUNK = 128 * 128;      // 128 rows x 64 columns of bf16, 128-byte swizzle
 constexpr int KSLOTS = 4, VST = 2;    // key chunks and value tiles in flight
-constexpr int THREADS = 384, SM_WARPS = 8, WARP_TMA = 8, WARP_MMA = 9, WARP_FIX = 10, WARP_NEXT = 11;
-// 384 threads at 168 registers: 2 x 128 x 200 + 128 x 104 = 384 x 168
-constexpr int REGS_SOFTMAX = 200, REGS_OTHER = 104;
-static_assert(128 * (2 * REGS_SOFTMAX + REGS_OTHER) <= THREADS * 168, "no more registers than at launch");
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float RISE = 8.f;  // a reference moves when a weight would pass 2^RISE
+constexpr int THREADS = 640, SM_WARPS = 16, WARP_TMA = 16, WARP_MMA = 17, WARP_FIX = 18, WARP_NEXT = 19;
+constexpr int HALF = TK / 2;          // keys of a softmax thread
+// 640 threads at 96 registers: 4 x 128 x 104 + 128 x 64 = 640 x 96
+constexpr int REGS_SOFTMAX = 104, REGS_OTHER = 64;
+static_assert(128 * (4 * REGS_SOFTMAX + REGS_OTHER) <= THREADS * 96, "no more registers than at launch");
+constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float RISE = 8.f;         // a reference moves when a weight would pass 2^RISE
+constexpr float HUGE_X = 0x1p28f;   // logits (to base 2) from here on take a step more
 
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // query tile g at + 128 g
 
@@ -90,8 +94,10 @@ struct Misc {
   alignas(16) int32_t upto[NCHUNK];  // tiles of the requests up to the end of each part (read four at a time)
   int32_t wsum[4];
   uint32_t tmem;
+  float pair[2][2][TQ];  // what the two threads of a query row exchange: [query tile][half]
 };
-constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc) + 1024;  // with alignment slack
+// (no room for alignment slack: a kernel without static shared memory gets it from a 1,024-byte boundary on)
+constexpr int SMEM_BYTES = OFF_MISC + (int)sizeof(Misc);
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 static_assert(OFF_ANSWER % 16 == 0 && OFF_MISC % 16 == 0 && offsetof(Misc, upto) % 16 == 0, "16-byte accesses");
 
@@ -188,6 +194,12 @@ __device__ __forceinline__ void write_nothing(const PromptArgs& a, int64_t row, 
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // Columns d0 .. d0 + n - 1 (16 or 32) of a row's result.
 __device__ __forceinline__ void finish(const PromptArgs& a, const volatile Item& it, float (&o)[32], int d0, int n, int bad0, int bad1,
                                        bool live, int64_t row, int64_t part, int dn, int dv, int S) {
@@ -200,16 +212,24 @@ __device__ __forceinline__ void finish(const PromptArgs& a, const volatile Item&
   }
   if (!live) return;
   if (S == 1) {
+    const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     uint32_t y[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
       y[e] = *reinterpret_cast<const uint32_t*>(&v);
     }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + row * dv + d0);
+    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) + row * dv + d0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (8 * e < n) dst[e] = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    for (int e = 0; e < 2; ++e)
+      if (16 * e < n) {
+        if (wide) {
+          store32(dst + 16 * e, y + 8 * e, l2_policy(false));
+        } else {
+          reinterpret_cast<uint4*>(dst)[2 * e] = make_uint4(y[8 * e], y[8 * e + 1], y[8 * e + 2], y[8 * e + 3]);
+          reinterpret_cast<uint4*>(dst)[2 * e + 1] = make_uint4(y[8 * e + 4], y[8 * e + 5], y[8 * e + 6], y[8 * e + 7]);
+        }
+      }
   } else {
     float4* dst = reinterpret_cast<float4*>(a.o_part + part * dv + d0);
 #pragma unroll
@@ -221,8 +241,11 @@ __device__ __forceinline__ void finish(const PromptArgs& a, const volatile Item&
 // STD: head widths 128 + 64 (rotated) and values of 128, known to the compiler.
 template <bool STD>
 __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs a, const __grid_constant__ PromptMaps maps) {
-  extern __shared__ unsigned char smem_raw[];
-  unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if (smem_u32(smem) % 1024 != 0) {  // (the swizzle's atoms would not be where the copies put them)
+    if (threadIdx.x == 0) report(a.dev_status, DSA_DEV_TIMEOUT);
+    return;
+  }
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + OFF_BAR);
   Misc* misc = reinterpret_cast<Misc*>(smem + OFF_MISC);
   auto bar = [&](int b) { return smem_u32(bars + b); };
@@ -236,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
   }
   if (tid == WARP_TMA * 32) {
     for (int b = 0; b < NBAR; ++b)
-      mbar_init(bar(b), b >= B_PF && b < B_PF + 2 ? 4u : b >= B_IE && b < B_IE + 2 ? (uint32_t)IE_COUNT : 1u);
+      mbar_init(bar(b), b >= B_PF && b < B_PF + 2 ? 8u : b >= B_IE && b < B_IE + 2 ? (uint32_t)IE_COUNT : 1u);
     fence_mbarrier_init();
     tma_prefetch_map(&maps.q);
     tma_prefetch_map(&maps.kv);
@@ -416,35 +439,37 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
       int slot = 0, phase = 0;           // of the first key chunk of the tile to come
       int vs = 0, vphase = 0, vx = 0;    // value stage, its phase, and the phases of B_VX (a bit each)
       int pn0 = 0, pn1 = 0, qn0 = 0, qn1 = 0;  // phases of B_PF and B_QF
+      // Waits inside an item only note that they gave up: one reduction a tile (30 cycles or more in
+      // which no MMA is issued) instead of one a wait; what is issued until then stays in bounds.
+      uint32_t fine = 1;
+      auto wait = [&](int b, uint32_t parity) { fine &= (uint32_t)mbar_wait(bar(b), parity, good ? MBAR_LIMIT_NS : 0); };
       // S_g = Q_g K^T; the last of the tile's users frees its chunks
       auto issue_qk = [&](int g, bool first_user, bool last_user, bool last_tile) {
         int s = slot, ph = phase;
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          if (c < nk && good) {
+          if (c < nk) {
             if (first_user) {
-              good = wait_u(B_KF + s, ph);
+              wait(B_KF + s, ph);
               tc_fence_after_sync();
             }
             const uint64_t qa = q_desc + (uint32_t)((3 * g + c) * (CHUNK >> 4)), kb = k_desc + (uint32_t)(s * (CHUNK >> 4));
             const int steps = STD ? 4 : (c < nn ? min(4, (dn - 64 * c) / 16) : dr / 16);
-            if (good) {
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                if (STD || kk < steps) mma_f16_ss_warp(TM_S + 128 * g, qa + 2 * kk, kb + 2 * kk, ID_QK, c | kk ? 1u : 0u);
-              if (last_user) mma_commit_warp(bar(B_KE + s));
-            }
+            for (int kk = 0; kk < 4; ++kk)
+              if (STD || kk < steps) mma_f16_ss_warp(TM_S + 128 * g, qa + 2 * kk, kb + 2 * kk, ID_QK, c | kk ? 1u : 0u);
+            if (last_user) mma_commit_warp(bar(B_KE + s));
             if (++s == KSLOTS) s = 0, ph ^= 1;
           }
         }
-        if (good) {
-          mma_commit_warp(bar(B_SF + g));
-          if (last_tile) mma_commit_warp(bar(B_QE + g));
-        }
+        mma_commit_warp(bar(B_SF + g));
+        if (last_tile) mma_commit_warp(bar(B_QE + g));
         if (last_user) slot = s, phase = ph;
       };
-      auto issue_pv = [&](int g, uint32_t acc, bool last_user) {
+      auto issue_pv = [&](int g, uint32_t acc, uint32_t parity, bool last_user) {
         const uint64_t vb = v_desc + (uint32_t)(vs * (2 * CHUNK >> 4));
+        wait(B_PF + g, parity);
+        tc_fence_after_sync();
 #pragma unroll
         for (int kk = 0; kk < TK / 16; ++kk)
           mma_f16_ts_warp(TM_O + 128 * g, TM_S + 128 * g + 8 * kk, vb + 128 * kk, ID_PV, kk > 0 ? 1u : acc);
@@ -461,39 +486,35 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
         slot = uniform(slot), phase = uniform(phase), vs = uniform(vs), vphase = uniform(vphase), vx = uniform(vx);
         pn0 = uniform(pn0), pn1 = uniform(pn1);
         if (c0 > 0) {
-          good = wait_u(B_QF, qn0);
+          wait(B_QF, qn0);
           qn0 ^= 1;
           tc_fence_after_sync();
           issue_qk(0, true, c1 == 0, c0 == 1);
         }
-        if (c1 > 0 && good) {
-          good = wait_u(B_QF + 1, qn1);
+        if (c1 > 0) {
+          wait(B_QF + 1, qn1);
           qn1 ^= 1;
           tc_fence_after_sync();
           issue_qk(1, c0 == 0, true, c1 == 1);
         }
         for (int lt = 0; lt < cnt && good; ++lt) {
-          good = wait_u(B_VF + vs, vphase);
-          if (lt >= fix && good) {
-            good = wait_u(B_VX + vs, (vx >> vs) & 1);
+          wait(B_VF + vs, vphase);
+          if (lt >= fix) {
+            wait(B_VX + vs, (vx >> vs) & 1);
             vx ^= 1 << vs;
           }
 #pragma unroll
           for (int g = 0; g < 2; ++g) {
             const int mine = g ? c1 : c0, other = g ? c0 : c1;
-            if (lt < mine && good) {
-              good = wait_u(B_PF + g, g ? pn1 : pn0);
+            if (lt < mine) {
+              issue_pv(g, lt > 0 ? 1u : 0u, g ? pn1 : pn0, g == 1 || lt >= other);
               if (g) pn1 ^= 1;
               else pn0 ^= 1;
-              tc_fence_after_sync();
-              if (good) {
-                issue_pv(g, lt > 0 ? 1u : 0u, g == 1 || lt >= other);
-                if (lt + 1 < mine)
-                  issue_qk(g, g == 0 || lt + 1 >= other, g == 1 || lt + 1 >= other, lt + 2 == mine);
-              }
+              if (lt + 1 < mine) issue_qk(g, g == 0 || lt + 1 >= other, g == 1 || lt + 1 >= other, lt + 2 == mine);
             }
           }
           if (++vs == VST) vs = 0, vphase ^= 1;
+          good = __reduce_min_sync(0xffffffffu, fine);
         }
         item_done(n);
       }
@@ -515,16 +536,15 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           go ^= 1 << s;
           for (int r = lane; r < TK; r += 32) {
             unsigned char* row = smem + OFF_V + 2 * s * CHUNK + r * 128;
-            uint32_t odd = 0;
+            __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);  // the largest magnitudes, NaN if there is one
             for (int c = 0; c < nv; ++c)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {  // (every lane at another bank; the order does not matter)
                 const uint4 w = *reinterpret_cast<const uint4*>(row + c * CHUNK + 16 * ((e + lane) & 7));
-                // an exponent of ones carries into the sign's place
-                auto look = [&](uint32_t u) { odd |= (u & 0x7f807f80u) + 0x00800080u; };
+                auto look = [&](uint32_t u) { top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u))); };
                 look(w.x), look(w.y), look(w.z), look(w.w);
               }
-            if (odd & 0x80008000u) {
+            if (!isfinite(__low2float(top)) || !isfinite(__high2float(top))) {
               for (int c = 0; c < nv; ++c)
                 for (int e = 0; e < 64; ++e) {
                   uint16_t* u = reinterpret_cast<uint16_t*>(row + c * CHUNK) + e;
@@ -544,60 +564,77 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
   } else {
     // ---------------- softmax warps ----------------
     reg_more<REGS_SOFTMAX>();
-    const int g = warp >> 2;
-    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, ts = TM_S + 128 * g + lanes, to = TM_O + 128 * g + lanes;
+    const int g = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+    const int qrow = TQ * g + 32 * quad + lane;  // this thread's query row of the CTA's QT
+    const uint32_t lanes = (uint32_t)(32 * quad) << 16, ts = TM_S + 128 * g + lanes, to = TM_O + 128 * g + lanes;
+    float* const mine_p = &misc->pair[g][half][32 * quad + lane];
+    const float* const other_p = &misc->pair[g][half ^ 1][32 * quad + lane];
+    const int pair_bar = 1 + 4 * g + quad;  // the two warps of these 32 rows
     const float c = fmaxf(a.softmax_scale * LOG2E, 0x1p-120f);  // (0 would make NaN of masked logits)
     int sn = 0;  // tiles so far
-    for (int n = 0; ok && next_item(n); ++n) {
+    // The two warps of a pair share a barrier, which has no limit: they leave their loops only by what it
+    // tells both, whether a wait of either gave up.
+    for (int n = 0;; ++n) {
+      const bool more = next_item(n);
+      if (named_barrier_or(pair_bar, 64, !more || !ok)) break;
       const volatile Item& it = misc->item[n & 1];  // (read again where it is needed: the loop needs the registers)
       const int mine = it.cnt[g], whole = it.whole[g], tile0 = it.t_begin;
       if (max(it.cnt[0], it.cnt[1]) == 0) {
         for (int i = warp; i < it.rows; i += SM_WARPS)
           write_nothing(a, (int64_t)(it.q0 + i) * a.heads + it.h, it.split, lane, 32);
       }
-      int last = -1;  // this thread's query row
-      if (it.req >= 0 && tid < it.rows) {
-        last = __ldg(a.q_pos + it.q0 + tid);
+      int last = -1;
+      if (it.req >= 0 && qrow < it.rows) {
+        last = __ldg(a.q_pos + it.q0 + qrow);
         if (last < -1 || last >= it.kv_len) {
-          report(a.dev_status, DSA_DEV_BAD_QPOS);
+          if (half == 0) report(a.dev_status, DSA_DEV_BAD_QPOS);
           last = -1;
         }
       }
-      float m = -INFINITY;
+      float m = -INFINITY, r = 0.f;  // the reference, and in units of x
       uint64_t l2 = 0;
       for (int lt = 0; lt < mine; ++lt, ++sn) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SF + g), sn & 1))) {
+        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SF + g), sn & 1))) ok = false;
+        tc_fence_after_sync();
+        float s[HALF];
+#pragma unroll
+        for (int b = 0; b < 2; ++b) tmem_ld32(ts + HALF * half + 32 * b, *reinterpret_cast<float(*)[32]>(s + 32 * b));
+        tmem_wait_ld();
+        if (lt >= whole) {
+          const int seen = last - (tile0 + lt) * TK - HALF * half;
+#pragma unroll
+          for (int j = 0; j < HALF; ++j) s[j] = j <= seen ? s[j] : -INFINITY;
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (a NaN is no maximum)
+#pragma unroll
+        for (int j = 0; j < HALF; j += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[j + 2 * e], s[j + 2 * e + 1]);
+        float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+        // The other thread's; after the barrier S has been read by both, and P may take its place.  (The one
+        // behind that keeps a value here until it is read: both pass B_SF's next phase only after P is whole.)
+        *mine_p = top;
+        tc_fence_before_sync();
+        if (named_barrier_or(pair_bar, 64, !ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        float s[TK];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) tmem_ld32(ts + 32 * b, *reinterpret_cast<float(*)[32]>(s + 32 * b));
-        tmem_wait_ld();
-        if (lt >= whole) {
-          const int seen = last - (tile0 + lt) * TK;
-#pragma unroll
-          for (int j = 0; j < TK; ++j) s[j] = j <= seen ? s[j] : -INFINITY;
-        }
-        float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-        for (int j = 4; j < TK; j += 4)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) mx[e] = fmaxf(mx[e], s[j + e]);
-        const float top = fmaxf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), -INFINITY);  // (not NaN)
+        top = fmaxf(top, *other_p);
         const bool move = (top - m) * c > RISE;
         if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? ex2((m - top) * c) : 1.f;
-          if (move) m = top;
+          float f = 1.f;
+          if (move) {
+            const float to_r = top * c;
+            f = fabsf(top) * c < HUGE_X ? ex2(r - to_r) : ex2((m - top) * c);  // (from -inf: 0)
+            if (m == -INFINITY) f = 0.f;
+            m = top, r = to_r;
+          }
           l2 = mul2(l2, pk2(f, f));
-          if (lt > 0) {
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) {
-              ok = false;
-              break;
-            }
+          if (lt > 0) {  // each thread half of the columns (a multiple of 16)
+            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) ok = false;
             tc_fence_after_sync();
-            for (int b = 0; b < dv / 16; ++b) {
+            for (int b = half; b < dv / 16; b += 2) {
               float o[16];
               tmem_ld16(to + 16 * b, o);
               tmem_wait_ld();
@@ -607,51 +644,60 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
             }
           }
         }
-        const float ref = m == -INFINITY ? 0.f : m;
-        const uint64_t ref2 = pk2(-ref, -ref), c2 = pk2(c, c);
-        uint64_t sum[2] = {0, 0};
+        // x = c s - r, r = c m rounded: the reference is any number, so r's rounding changes no weight's share.
+        // Past 2^28 it would (r's steps reach 2^4 and more): x = c (s - m) there, where s - m is exact.
+        const bool huge = !(fabsf(m) * c < HUGE_X) && m > -INFINITY;
+        if (__any_sync(0xffffffffu, huge)) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          uint32_t p[32];
+          for (int j = 0; j < HALF; ++j) s[j] = huge ? (s[j] - m) * c : fmaf(s[j], c, -r);
+        } else {
+          const uint64_t r2 = pk2(-r, -r), c2 = pk2(c, c);
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            // (s - m first: it is exact where it matters, however large both are)
-            const uint64_t x = mul2(add2(pk2(s[64 * b + 2 * j], s[64 * b + 2 * j + 1]), ref2), c2);
-            float x0, x1;
-            upk2(x, x0, x1);
-            x0 = ex2(x0), x1 = ex2(x1);
-            sum[j & 1] = add2(sum[j & 1], pk2(x0, x1));
-            const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
-            p[j] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          tmem_st32(ts + 32 * b, p);
+          for (int j = 0; j < HALF; j += 2) upk2(fma2(pk2(s[j], s[j + 1]), c2, r2), s[j], s[j + 1]);
         }
+        uint32_t p[32];
+        uint64_t sum = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          const float x0 = ex2(s[2 * j]), x1 = ex2(s[2 * j + 1]);
+          if (j & 1) sum = add2(sum, pk2(x0, x1));
+          else l2 = add2(l2, pk2(x0, x1));
+          const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
+          p[j] = *reinterpret_cast<const uint32_t*>(&y);
+        }
+        tmem_st32(ts + 32 * half, p);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_PF + g));
-        l2 = add2(l2, add2(sum[0], sum[1]));
+        l2 = add2(l2, sum);
       }
-      if (!ok) break;
-      if (mine > 0 && !__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) {
-        ok = false;
-        break;
+      if (mine > 0) {
+        if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) ok = false;
+        if (named_barrier_or(pair_bar, 64, !ok)) {  // (and the maxima have been read)
+          ok = false;
+          break;
+        }
       }
       tc_fence_after_sync();
-      float la, lb;
-      upk2(l2, la, lb);
-      const float l = la + lb;
-      const int64_t row = (int64_t)(it.q0 + tid) * a.heads + it.h, part = (int64_t)it.split * a.num_tokens * a.heads + row;
-      const bool live = tid < it.rows;
+      float l, lb;
+      upk2(l2, l, lb);
+      l += lb;
+      const int64_t row = (int64_t)(it.q0 + qrow) * a.heads + it.h, part = (int64_t)it.split * a.num_tokens * a.heads + row;
+      const bool live = qrow < it.rows;
       if (mine == 0) {
-        if (live && it.cnt[g ^ 1] > 0) write_nothing(a, row, it.split, 0, 1);
+        if (live && it.cnt[g ^ 1] > 0) write_nothing(a, row, it.split, half, 2);
       } else {
+        *mine_p = l;
+        named_barrier_sync(pair_bar, 64);
+        l = half ? *other_p + l : l + *other_p;  // (the same sum in both)
+        named_barrier_sync(pair_bar, 64);
         const bool any = !(l == 0.f);  // (NaN counts)
         const float inv = any ? 1.f / l : 0.f;
         // values that were taken out, and that this row sees
         const bool look = it.any_bad != 0;
         const int bad0 = look ? (it.t_begin + it.fix0) * TK : INT32_MAX, bad1 = min(last, it.t_end * TK - 1);
-        for (int b = 0; b < dv / 32; ++b) {
+        for (int b = half; b < dv / 32; b += 2) {
           float o[32];
           tmem_ld32(to + 32 * b, o);
           tmem_wait_ld();
@@ -659,7 +705,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * inv : 0.f;
           finish(a, it, o, 32 * b, 32, bad0, bad1, live, row, part, dn, dv, S);
         }
-        if (dv % 32) {
+        if (dv % 32 && half == 1) {
           float o[32];
           tmem_ld16(to + dv - 16, *reinterpret_cast<float(*)[16]>(o));
           tmem_wait_ld();
@@ -667,8 +713,8 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           for (int e = 0; e < 16; ++e) o[e] = any ? o[e] * inv : 0.f;
           finish(a, it, o, dv - 16, 16, bad0, bad1, live, row, part, dn, dv, S);
         }
-        if (live) {
-          const float z = any ? m * a.softmax_scale + __logf(l) : -INFINITY;
+        if (live && half == 0) {
+          const float z = !any ? -INFINITY : fabsf(m) * c < HUGE_X ? r * LN2 + __logf(l) : m * a.softmax_scale + __logf(l);
           if (S > 1) a.lse_part[part] = z;
           else if (a.lse) a.lse[row] = z;
         }
