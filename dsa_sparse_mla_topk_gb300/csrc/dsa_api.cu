@@ -694,13 +694,22 @@ int32_t dsa_prompt_pick_num_splits(int32_t num_tokens, int32_t num_req, int32_t 
                                    int32_t num_sms) {
   if (num_tokens <= 0 || num_req <= 0 || num_heads <= 0 || max_ctx <= 0) return 1;
   const int64_t sms = num_sms > 0 ? num_sms : dsa::device_sm_count();
-  // CTAs of a share, about: a request's last tile is half full
-  const int64_t ctas = num_heads * (num_tokens / 256 + (int64_t)(num_req + 1) / 2);
-  // a share of 4 tiles of 128 rows (4 x 0.6 us) outweighs its part of the Combine
-  const int64_t most = max_ctx / (4 * 128) < 16 ? max_ctx / (4 * 128) : 16;
-  int64_t s = sms / ctas;
-  if (s > most) s = most;
-  return s < 1 ? 1 : (int32_t)s;
+  // The least estimated time over 1 to 8 shares: waves of CTAs, 1.5 us for 128 rows and 5 us beside them,
+  // then the Combine (3.5 us, and the partials written and read at 5 TB/s).  Measured, 64 heads: one token
+  // of 16,384 positions 189 us in one share and 103 in two, of 1,024 17.9 and 16.0, of 512 12.2 and 13.0; three
+  // tokens of 8,192 194, and 141 in three; 1,024 tokens of 16,384 407, and 454 in four.  16 heads: one
+  // token of 16,384 154 us, and 29 in eight (32 in sixteen).
+  const int64_t least = num_req < num_tokens ? num_req : num_tokens;  // tiles of 256 tokens, about: every request's last
+  const int64_t full = ((int64_t)num_tokens + 255) / 256 + (num_req - 1) / 2;  // one is half full
+  const int64_t ctas = num_heads * (full > least ? full : least), n = ((int64_t)max_ctx + 127) / 128;
+  int64_t best = 0;
+  int32_t pick = 1;
+  for (int64_t k = 1; k <= 8 && k <= n; ++k) {
+    const int64_t parts = k * num_tokens * num_heads * 128 * 8;  // bytes
+    const int64_t ns = (ctas * k + sms - 1) / sms * ((n + k - 1) / k * 1500 + 5000) + (k > 1 ? 3500 + parts / 5000 : 0);
+    if (k == 1 || ns < best) best = ns, pick = (int32_t)k;
+  }
+  return pick;
 }
 
 dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* kv,

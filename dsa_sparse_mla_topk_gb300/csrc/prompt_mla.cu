@@ -655,17 +655,21 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
 #pragma unroll
           for (int j = 0; j < HALF; j += 2) upk2(fma2(pk2(s[j], s[j + 1]), c2, r2), s[j], s[j + 1]);
         }
-        uint32_t p[32];
+        // (few weights at a time: with all of them in registers beside the logits, some of both spill)
         uint64_t sum = 0;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const float x0 = ex2(s[2 * j]), x1 = ex2(s[2 * j + 1]);
-          if (j & 1) sum = add2(sum, pk2(x0, x1));
-          else l2 = add2(l2, pk2(x0, x1));
-          const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
-          p[j] = *reinterpret_cast<const uint32_t*>(&y);
+        for (int b = 0; b < 4; ++b) {
+          uint32_t p[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float x0 = ex2(s[16 * b + 2 * j]), x1 = ex2(s[16 * b + 2 * j + 1]);
+            if (j & 1) sum = add2(sum, pk2(x0, x1));
+            else l2 = add2(l2, pk2(x0, x1));
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
+            p[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          tmem_st8(ts + 32 * half + 8 * b, p);
         }
-        tmem_st32(ts + 32 * half, p);
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();

@@ -755,8 +755,8 @@ DSA_API int32_t dsa_chunk_pick_num_splits_live(int32_t num_q, int32_t num_live, 
 
 /*
  * dsa_prompt_pick_num_splits: shares of the rows for dsa_prompt_mla_fwd over contexts of
- * about max_ctx positions: more than one (then dsa_combine) only while the tiles of 256
- * tokens leave SMs idle and the shares stay long enough to pay for the Combine.
+ * about max_ctx positions (1 to 8): the number with the least estimated time, from the
+ * waves of CTAs, the tiles of a share and the Combine.
  */
 DSA_API int32_t dsa_prompt_pick_num_splits(int32_t num_tokens, int32_t num_req, int32_t num_heads, int32_t max_ctx,
                                            int32_t num_sms);

@@ -152,3 +152,16 @@ def test_binding_rejects_what_is_not_documented(lib):
         dsa.token_logprobs(torch.zeros(1, 4, dtype=torch.float64), i(1))
     with pytest.raises(ValueError, match="CUDA"):
         dsa.token_logprobs(torch.zeros(1, 4), i(1))
+
+
+def test_prompt_split_rule(lib):
+    """The rule on 152 SMs: shares while the tiles leave SMs idle and a share outweighs its part of the Combine."""
+    pick = lambda n, R, H, ctx: dsa.pick_prompt_splits(n, R, H, ctx, num_sms=152)  # noqa: E731
+    assert pick(1, 1, 64, 512) == 1 and pick(1, 1, 64, 1024) == 2 and pick(1, 1, 64, 16384) == 2
+    assert pick(256, 1, 64, 16384) == 2 and pick(300, 1, 64, 16384) == 1 and pick(128, 2, 64, 8192) == 1
+    assert pick(3, 3, 64, 8192) == 3 and pick(1024, 1, 64, 16384) == 1 and pick(16384, 8, 64, 3048) == 1
+    assert pick(1, 1, 16, 16384) == 8 and pick(0, 1, 64, 100) == pick(1, 0, 64, 100) == 1
+    for n in (1, 5, 300, 1 << 30):
+        for R in (1, 7, 8192):
+            for ctx in (1, 127, 129, 5000, 1 << 20, 2**31 - 1):
+                assert 1 <= pick(n, R, 64, ctx) <= min(8, -(-ctx // 128))
