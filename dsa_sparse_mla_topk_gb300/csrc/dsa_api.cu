@@ -702,12 +702,12 @@ int32_t dsa_prompt_pick_num_splits(int32_t num_tokens, int32_t num_req, int32_t 
   const int64_t least = num_req < num_tokens ? num_req : num_tokens;  // tiles of 256 tokens, about: every request's last
   const int64_t full = ((int64_t)num_tokens + 255) / 256 + (num_req - 1) / 2;  // one is half full
   const int64_t ctas = num_heads * (full > least ? full : least), n = ((int64_t)max_ctx + 127) / 128;
-  int64_t best = 0;
+  double best = 0;
   int32_t pick = 1;
   for (int64_t k = 1; k <= 8 && k <= n; ++k) {
-    const int64_t parts = k * num_tokens * num_heads * 128 * 8;  // bytes
-    const int64_t ns = (ctas * k + sms - 1) / sms * ((n + k - 1) / k * 1500 + 5000) + (k > 1 ? 3500 + parts / 5000 : 0);
-    if (k == 1 || ns < best) best = ns, pick = (int32_t)k;
+    const double parts = (double)k * num_tokens * num_heads * 128 * 8;  // bytes
+    const double us = (double)((ctas * k + sms - 1) / sms) * (1.5 * ((n + k - 1) / k) + 5) + (k > 1 ? 3.5 + parts / 5e6 : 0);
+    if (k == 1 || us < 0.97 * best) best = us, pick = (int32_t)k;  // (more shares for a gain that shows)
   }
   return pick;
 }
