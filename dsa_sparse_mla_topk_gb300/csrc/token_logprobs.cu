@@ -72,9 +72,11 @@ struct Pack<float> {
     }
     __device__ __forceinline__ float value() const { return v; }
   };
+  typedef float Bound;  // a value to compare with
+  __device__ __forceinline__ static Bound bound(float x) { return x; }
   struct Count {
     int n = 0;
-    __device__ __forceinline__ void take(const uint4& w, float thr) {
+    __device__ __forceinline__ void take(const uint4& w, Bound thr) {
       n += __uint_as_float(w.x) > thr;
       n += __uint_as_float(w.y) > thr;
       n += __uint_as_float(w.z) > thr;
@@ -110,12 +112,15 @@ struct Pack16 {
     }
     __device__ __forceinline__ float value() const { return fmaxf((float)v.x, (float)v.y); }
   };
+  typedef uint32_t Bound;  // a value to compare with, twice
+  __device__ __forceinline__ static Bound bound(float x) {
+    const T t = (T)x;
+    return 0x10001u * *reinterpret_cast<const uint16_t*>(&t);
+  }
   struct Count {  // as numbers of the type: exact up to 256 a half, 32 loads
     T2 v = as_pair<T2>(0u);
-    __device__ __forceinline__ void take(const uint4& w, float thr) {
-      const T t = (T)thr;
-      T2 t2;
-      t2.x = t, t2.y = t;
+    __device__ __forceinline__ void take(const uint4& w, Bound thr) {
+      const T2 t2 = as_pair<T2>(thr);
       v = __hadd2(v, __hadd2(__hadd2(__hgt2(as_pair<T2>(w.x), t2), __hgt2(as_pair<T2>(w.y), t2)),
                              __hadd2(__hgt2(as_pair<T2>(w.z), t2), __hgt2(as_pair<T2>(w.w), t2))));
     }
@@ -197,18 +202,12 @@ struct Shared {
 
 // Sums and order over the share [v0, v1) of a row's loads by this CTA.
 template <class T>
-__device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, int t, float zt, int top, Shared* sh,
-                                             Part* part, float* lz, int* lc) {
+__device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, const int32_t* token, int& t, float& zt,
+                                             bool& bad, int top, Shared* sh, Part* part, float* lz, int* lc) {
   constexpr int N = Pack<T>::N;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int vt = t >= 0 ? (t + row.shift) / N : 0;  // the token's load
-  // before it equal values count, from it on they do not
-  const float thr_hi = t >= 0 ? zt : INFINITY, thr_lo = t >= 0 ? Pack<T>::below(zt) : INFINITY;
-  float m = -INFINITY;
-  uint64_t s2 = 0, e2 = 0;
-  int count = 0;
-  for (int vb = v0; vb < v1; vb += THREADS * TURNS) {
-    uint4 w[TURNS];
+  // a turn's loads are on their way while the one before is worked on, the first while the token is looked up
+  auto fetch = [&](int vb, uint4 (&w)[TURNS]) {
     const bool whole = vb + THREADS * TURNS <= v1 && row.inside(vb) && row.inside(vb + THREADS * TURNS - 1);
 #pragma unroll
     for (int k = 0; k < TURNS; ++k) {
@@ -217,6 +216,25 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
       else if (v < v1) w[k] = row.load(v);
       else w[k] = make_uint4(Pack<T>::minus_inf(), Pack<T>::minus_inf(), Pack<T>::minus_inf(), Pack<T>::minus_inf());
     }
+  };
+  uint4 next[TURNS];
+  fetch(v0, next);
+  t = __ldg(token);
+  bad = t < -1 || t >= row.vocab;
+  if (bad) t = -1;
+  zt = t >= 0 ? (float)row.p[t] : 0.f;
+  const int vt = t >= 0 ? (t + row.shift) / N : 0;  // the token's load
+  // before it equal values count, from it on they do not
+  const typename Pack<T>::Bound thr_hi = Pack<T>::bound(t >= 0 ? zt : INFINITY);
+  const typename Pack<T>::Bound thr_lo = Pack<T>::bound(t >= 0 ? Pack<T>::below(zt) : INFINITY);
+  float m = -INFINITY;
+  uint64_t s2 = 0, e2 = 0;
+  int count = 0;
+  for (int vb = v0; vb < v1; vb += THREADS * TURNS) {
+    uint4 w[TURNS];
+#pragma unroll
+    for (int k = 0; k < TURNS; ++k) w[k] = next[k];
+    if (vb + THREADS * TURNS < v1) fetch(vb + THREADS * TURNS, next);
     typename Pack<T>::Most most;
     typename Pack<T>::Count n;
 #pragma unroll
@@ -280,27 +298,26 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
   if (lane == 0) sh->wf[0][warp] = s, sh->wf[1][warp] = e, sh->wi[warp] = count;
 
   // ---- tau: at least `top` threads reach it, few more if the values allow ----
+  // (by the whole block: one warp over all 512 values takes 0.5 us longer)
   uint32_t tau = 0;
-  bool mine = false;
   if (top > 0) {
     const uint32_t none = order_of(-INFINITY);
     // reached by at least `top` threads (or all that hold values); by none
-    uint32_t lo = max(least, none + 1), hi_key = most + 1;
+    uint32_t lo = max(least, none + 1), up = most + 1;
     if (most > none && (least > none || __syncthreads_count(key >= lo) > top)) {
-      while (hi_key - lo > 1) {
-        const uint32_t mid = lo + (hi_key - lo) / 2;
+      while (up - lo > 1) {
+        const uint32_t mid = lo + (up - lo) / 2;
         const int c = __syncthreads_count(key >= mid);
         if (c >= top) {
           lo = mid;
           if (c <= top + top / 4 + 4) break;
         } else {
-          hi_key = mid;
+          up = mid;
         }
       }
     }
     tau = lo;
-    mine = key >= tau;
-    if (mine) sh->list[atomicAdd(&sh->flagged, 1)] = tid;
+    if (key >= tau) sh->list[atomicAdd(&sh->flagged, 1)] = tid;
   }
   __syncthreads();
   // ---- columns read again, a warp a thread's: the owner's for the sum, the others' for tau ----
@@ -406,17 +423,14 @@ __global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs 
   const int64_t i = blockIdx.x / C;
   const T* p = static_cast<const T*>(a.logits) + i * a.ld;
   const Row<T> row(p, a.vocab);
-  int t = __ldg(a.tokens + i);
-  if (t < -1 || t >= a.vocab) {
-    if (tid == 0 && rank == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
-    t = -1;
-  }
-  const float zt = t >= 0 ? (float)p[t] : 0.f;
   // waited for before the first write to another CTA's shared memory
   if (C > 1) asm volatile("barrier.cluster.arrive.relaxed;");
   const int each = (row.loads + C - 1) / C, v0 = min(rank * each, row.loads), v1 = min(v0 + each, row.loads);
-  // (a masked token: every column with a value is before it, and the masked ones of lower columns)
-  share_of_row(row, v0, v1, t, zt, a.top, &sh, &sh.part[rank], sh.lz[rank], sh.lc[rank]);
+  int t;
+  float zt;
+  bool bad;
+  share_of_row(row, v0, v1, a.tokens + i, t, zt, bad, a.top, &sh, &sh.part[rank], sh.lz[rank], sh.lc[rank]);
+  if (bad && tid == 0 && rank == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
   __syncthreads();
   if (C > 1) {
     asm volatile("barrier.cluster.wait;" ::: "memory");
@@ -498,10 +512,12 @@ __global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs 
 
 template <class T>
 cudaError_t launch(const LogprobArgs& a, cudaStream_t stream) {
-  // CTAs a row: few rows share the GPU, as long as a thread has a load
+  // CTAs a row: few rows share the GPU, as long as a thread has a load and all CTAs run at once, two an
+  // SM (64 x 50,000 values 10 us in 256 CTAs, 20 in 512; 128 x 131,072 fp32 19 us in 256, 31 in 512).  Rows
+  // past that go a CTA each (sharing out the last wave's among clusters: 1,024 rows 66 -> 72 us).
   const int64_t loads = ((int64_t)a.vocab + Pack<T>::N - 1) / Pack<T>::N;
   int c = 1;
-  while (c < MAX_CLUSTER && (int64_t)a.num_rows * c * 2 <= 4 * device_sm_count() && loads > (int64_t)THREADS * c) c *= 2;
+  while (c < MAX_CLUSTER && (int64_t)a.num_rows * c * 2 <= 2 * device_sm_count() && loads > (int64_t)THREADS * c) c *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = c;
