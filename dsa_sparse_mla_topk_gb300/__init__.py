@@ -113,9 +113,9 @@ def load_library(path: str | None = None):
         lib.dsa_verify_draft_req.argtypes = [vp, i64, i32, i32, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp,
                                              vp]
         lib.dsa_verify_draft_req.restype = i32
-        lib.dsa_absorb_q.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, i32, vp, vp]
+        lib.dsa_absorb_q.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp]
         lib.dsa_absorb_q.restype = i32
-        lib.dsa_project_out.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, vp, vp]
+        lib.dsa_project_out.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]
         lib.dsa_project_out.restype = i32
         lib.dsa_expand_kv.argtypes = [vp, vp, i64, vp, i32, i32, vp, vp, i32, i32, i32, i32, i32, i32, vp, vp, vp,
                                       vp, sz, vp, vp]
@@ -1012,14 +1012,14 @@ def _given(t, name: str, dtype, shape: tuple, like, stream):
 
 
 def absorb_q(q: torch.Tensor, w_kv: torch.Tensor, *, d_rope: int, q_out: torch.Tensor | None = None,
-             stream=None) -> torch.Tensor:
+             dev_status=None, stream=None) -> torch.Tensor:
     """Queries in the cache's latent space (dsa_absorb_q): q bf16 [tokens, heads,
     d_nope + d_rope] (any token and head strides that are multiples of 8) and the
     up-projection w_kv bf16 [heads, d_nope + d_v, d_latent] of every head's keys
     and values give bf16 [tokens, heads, d_latent + d_rope], the queries of
     chunk_mla and sparse_mla_topk; the rotated part stays as it is."""
     if q_out is None and stream is None and _fast is not None:
-        r = _fast.absorb_q(q, w_kv, d_rope)
+        r = _fast.absorb_q(q, w_kv, d_rope, dev_status)
         if r is not None:
             return _done("dsa_absorb_q", r)
     dev = _device_of(q, "q")
@@ -1032,16 +1032,16 @@ def absorb_q(q: torch.Tensor, w_kv: torch.Tensor, *, d_rope: int, q_out: torch.T
     q_out = _given(q_out, "q_out", _BF16, (n, H, dl + d_rope), q, stream)
     ts, hs = _strides(q)
     _run(dev, stream, "dsa_absorb_q", q.data_ptr(), ts, hs, w_kv.data_ptr(), n, H, d - d_rope, d_rope, dw - (d - d_rope),
-         dl, q_out.data_ptr())
+         dl, q_out.data_ptr(), _status_ptr(dev_status, dev))
     return q_out
 
 
 def project_out(o: torch.Tensor, w_kv: torch.Tensor, *, d_nope: int, out: torch.Tensor | None = None,
-                stream=None) -> torch.Tensor:
+                dev_status=None, stream=None) -> torch.Tensor:
     """Attention's latent outputs o bf16 [tokens, heads, d_latent] (strides as for
     absorb_q) to every head's values, bf16 [tokens, heads, d_v] (dsa_project_out)."""
     if out is None and stream is None and _fast is not None:
-        r = _fast.project_out(o, w_kv, d_nope)
+        r = _fast.project_out(o, w_kv, d_nope, dev_status)
         if r is not None:
             return _done("dsa_project_out", r)
     dev = _device_of(o, "o")
@@ -1055,7 +1055,8 @@ def project_out(o: torch.Tensor, w_kv: torch.Tensor, *, d_nope: int, out: torch.
         raise ValueError("d_nope leaves no values in w_kv")
     out = _given(out, "out", _BF16, (n, H, dv), o, stream)
     ts, hs = _strides(o)
-    _run(dev, stream, "dsa_project_out", o.data_ptr(), ts, hs, w_kv.data_ptr(), n, H, d_nope, dv, dl, out.data_ptr())
+    _run(dev, stream, "dsa_project_out", o.data_ptr(), ts, hs, w_kv.data_ptr(), n, H, d_nope, dv, dl, out.data_ptr(),
+         _status_ptr(dev_status, dev))
     return out
 
 

@@ -587,20 +587,20 @@ dsa_status check_latent_dims(int32_t heads, int32_t d_nope, int32_t d_rope, int3
   return DSA_OK;
 }
 
-// 16-bit rows [n, heads, d] behind strides: 16-byte loads reach every one.
-bool rows_ok(const void* x, int64_t ts, int64_t hs) {
+// 16-bit rows [n, heads, d] behind strides: 16-byte loads reach every one, and a span of 64 bits holds them.
+bool rows_ok(const void* x, int64_t n, int64_t heads, int64_t ts, int64_t hs) {
   return x && aligned16(x) && ts >= 0 && hs >= 0 && ts % 8 == 0 && hs % 8 == 0 && ts < ((int64_t)1 << 36) &&
-         hs < ((int64_t)1 << 36);
+         hs < ((int64_t)1 << 36) && ts <= ((int64_t)1 << 60) / n && hs <= ((int64_t)1 << 60) / heads;
 }
 
 dsa_status latent_proj(const void* x, int64_t ts, int64_t hs, const void* w, int32_t n, int32_t heads, int32_t d_nope,
-                       int32_t d_rope, int32_t d_v, int32_t d_latent, void* y, bool absorb, void* stream) {
+                       int32_t d_rope, int32_t d_v, int32_t d_latent, void* y, bool absorb, int32_t* dev_status, void* stream) {
   if (n < 0) return DSA_ERR_INVALID_ARG;
   const dsa_status st = check_latent_dims(heads, d_nope, d_rope, d_v, d_latent);
   if (st != DSA_OK) return st;
   if ((int64_t)n * heads > INT32_MAX) return DSA_ERR_UNSUPPORTED_SHAPE;
   if (n == 0) return DSA_OK;
-  if (!rows_ok(x, ts, hs) || !w || !aligned16(w) || !y || !aligned16(y)) return DSA_ERR_INVALID_ARG;
+  if (!rows_ok(x, n, heads, ts, hs) || !w || !aligned16(w) || !y || !aligned16(y)) return DSA_ERR_INVALID_ARG;
   const int32_t d_in = absorb ? d_nope + d_rope : d_latent, d_out = absorb ? d_latent + d_rope : d_v;
   const Span in[2] = {{x, row_span(n, heads, ts, hs, d_in)}, {w, 2 * (int64_t)heads * (d_nope + d_v) * d_latent}};
   const Span out[1] = {{y, 2 * (int64_t)n * heads * d_out}};
@@ -617,6 +617,7 @@ dsa_status latent_proj(const void* x, int64_t ts, int64_t hs, const void* w, int
   a.d_rope = d_rope;
   a.d_v = d_v;
   a.d_latent = d_latent;
+  a.dev_status = dev_status;
   return from_cuda(absorb ? dsa::launch_absorb_q(a, static_cast<cudaStream_t>(stream))
                           : dsa::launch_project_out(a, static_cast<cudaStream_t>(stream)));
 }
@@ -625,16 +626,16 @@ dsa_status latent_proj(const void* x, int64_t ts, int64_t hs, const void* w, int
 
 dsa_status dsa_absorb_q(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* w_kv,
                         int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_rope, int32_t d_v,
-                        int32_t d_latent, void* q_out, void* stream) {
+                        int32_t d_latent, void* q_out, int32_t* dev_status, void* stream) {
   return latent_proj(q, q_tok_stride, q_head_stride, w_kv, num_tokens, num_heads, d_nope, d_rope, d_v, d_latent, q_out,
-                     true, stream);
+                     true, dev_status, stream);
 }
 
 dsa_status dsa_project_out(const void* o, int64_t o_tok_stride, int64_t o_head_stride, const void* w_kv,
                            int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_v, int32_t d_latent,
-                           void* y, void* stream) {
+                           void* y, int32_t* dev_status, void* stream) {
   return latent_proj(o, o_tok_stride, o_head_stride, w_kv, num_tokens, num_heads, d_nope, 0, d_v, d_latent, y, false,
-                     stream);
+                     dev_status, stream);
 }
 
 size_t dsa_expand_kv_workspace_size(int32_t capacity, int32_t d_latent) {
@@ -722,13 +723,13 @@ dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_hea
   if (!isfinite(softmax_scale) || softmax_scale < 0.f) return DSA_ERR_INVALID_ARG;
   const dsa_status st = check_latent_dims(num_heads, d_nope, d_rope, d_v, 16);
   if (st != DSA_OK) return st;
-  if (num_req > dsa::batch_layout_max_requests() || num_tokens > (1 << 30) || num_rows > (1 << 30))
-    return DSA_ERR_UNSUPPORTED_SHAPE;
+  if (num_req > dsa::batch_layout_max_requests() || num_tokens > (1 << 30) || num_rows > (1 << 26))
+    return DSA_ERR_UNSUPPORTED_SHAPE;  // (a wait for a CTA's work of 2^26 rows, 0.8 s, stays below its limit)
   if (num_tokens == 0) return DSA_OK;
-  if (!rows_ok(q, q_tok_stride, q_head_stride) || !cu_q || !cu_k || !q_pos) return DSA_ERR_INVALID_ARG;
+  if (!rows_ok(q, num_tokens, num_heads, q_tok_stride, q_head_stride) || !cu_q || !cu_k || !q_pos) return DSA_ERR_INVALID_ARG;
   if (num_rows > 0) {
-    if (!rows_ok(kv, kv_tok_stride, kv_head_stride)) return DSA_ERR_INVALID_ARG;
-    if (d_rope > 0 && !rows_ok(k_rope, rope_stride, 0)) return DSA_ERR_INVALID_ARG;
+    if (!rows_ok(kv, num_rows, num_heads, kv_tok_stride, kv_head_stride)) return DSA_ERR_INVALID_ARG;
+    if (d_rope > 0 && !rows_ok(k_rope, num_rows, 1, rope_stride, 0)) return DSA_ERR_INVALID_ARG;
   }
   const bool whole = num_splits == 1;
   if (whole ? !out || !aligned16(out) : !o_part || !lse_part || !aligned16(o_part)) return DSA_ERR_INVALID_ARG;

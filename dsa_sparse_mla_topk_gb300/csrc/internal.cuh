@@ -159,6 +159,7 @@ struct LatentProjArgs {
   const void* w;  // bf16 [heads, d_nope + d_v, d_latent]
   void* y;        // bf16 [tokens, heads, d_latent + d_rope or d_v]
   int32_t num_tokens, heads, d_nope, d_rope, d_v, d_latent;
+  int32_t* dev_status;
 };
 cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream);
 cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream);

@@ -503,6 +503,7 @@ cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream) {
   p.units = a.heads * p.per_group;
   p.b_row0 = 0, p.b_group = d_w;
   p.rope_x = a.d_rope > 0 ? a.d_nope : -1;
+  p.dev_status = a.dev_status;
   ProductMaps maps;
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
   if (!make_rows_map(&maps.a, a.x, a.num_tokens, a.heads, a.d_nope + a.d_rope, a.tok_stride, a.head_stride, TM) ||
@@ -523,6 +524,7 @@ cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream) {
   p.per_group = (p.n + p.n_unit - 1) / p.n_unit;
   p.units = a.heads * p.per_group;
   p.b_row0 = a.d_nope, p.b_group = d_w;
+  p.dev_status = a.dev_status;
   p.out = static_cast<__nv_bfloat16*>(a.y), p.ldc = (int64_t)a.heads * a.d_v;
   p.wide = reinterpret_cast<uintptr_t>(a.y) % 32 == 0;
   p.rope_x = -1;

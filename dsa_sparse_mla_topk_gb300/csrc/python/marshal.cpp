@@ -337,15 +337,16 @@ PyObject* verify_draft(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   END_HANDLE_TH_ERRORS
 }
 
-// (x, w_kv, d_rope of absorb_q or d_nope of project_out)
+// (x, w_kv, d_rope of absorb_q or d_nope of project_out, dev_status)
 template <bool ABSORB>
 PyObject* latent_proj(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   HANDLE_TH_ERRORS
-  if (argc != 3) Py_RETURN_NONE;
+  if (argc != 4) Py_RETURN_NONE;
   Args a{argv};
   const at::Tensor* x = a.rows(at::kBFloat16, 3);
   const at::Tensor* w = a.tensor(at::kBFloat16, 3);
   const int32_t given = a.int32();
+  int32_t* st = a.status();
   if (!a.good) Py_RETURN_NONE;
   const int64_t n = x->size(0), H = x->size(1), d = x->size(2), dw = w->size(1), dl = w->size(2);
   const int64_t dn = ABSORB ? d - given : given;
@@ -356,10 +357,10 @@ PyObject* latent_proj(PyObject*, PyObject* const* argv, Py_ssize_t argc) {
   dsa_status s;
   if constexpr (ABSORB)
     s = call(absorb_q_fn, x->data_ptr(), stride(x, 0), stride(x, 1), w->data_ptr(), (int32_t)n, (int32_t)H, (int32_t)dn,
-             given, (int32_t)(dw - dn), (int32_t)dl, y.data_ptr(), a.stream());
+             given, (int32_t)(dw - dn), (int32_t)dl, y.data_ptr(), st, a.stream());
   else
     s = call(project_out_fn, x->data_ptr(), stride(x, 0), stride(x, 1), w->data_ptr(), (int32_t)n, (int32_t)H, given,
-             (int32_t)(dw - dn), (int32_t)dl, y.data_ptr(), a.stream());
+             (int32_t)(dw - dn), (int32_t)dl, y.data_ptr(), st, a.stream());
   if (s != DSA_OK) return PyLong_FromLong(s);
   return THPVariable_Wrap(y);
   END_HANDLE_TH_ERRORS

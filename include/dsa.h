@@ -557,7 +557,7 @@ DSA_API dsa_status dsa_verify_draft_req(const float* target_probs, int64_t ld_ta
  */
 DSA_API dsa_status dsa_absorb_q(const void* q, int64_t q_tok_stride, int64_t q_head_stride, const void* w_kv,
                                 int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_rope, int32_t d_v,
-                                int32_t d_latent, void* q_out, void* stream);
+                                int32_t d_latent, void* q_out, int32_t* dev_status, void* stream);
 
 /*
  * dsa_project_out -- the attention calls' latent outputs to the heads' values:
@@ -567,7 +567,7 @@ DSA_API dsa_status dsa_absorb_q(const void* q, int64_t q_tok_stride, int64_t q_h
  */
 DSA_API dsa_status dsa_project_out(const void* o, int64_t o_tok_stride, int64_t o_head_stride, const void* w_kv,
                                    int32_t num_tokens, int32_t num_heads, int32_t d_nope, int32_t d_v,
-                                   int32_t d_latent, void* y, void* stream);
+                                   int32_t d_latent, void* y, int32_t* dev_status, void* stream);
 
 /*
  * dsa_expand_kv -- every head's keys and values of the requests' cached rows, for
@@ -625,7 +625,7 @@ DSA_API size_t dsa_expand_kv_workspace_size(int32_t capacity, int32_t d_latent);
  *             a request's rows are cut into S runs of whole tiles and the call writes
  *             o_part (fp32 [S, num_tokens, num_heads, d_v], 16-byte aligned) and lse_part (fp32
  *             [S, num_tokens, num_heads]) for dsa_combine.
- * The head sizes are those of dsa_absorb_q; num_tokens, num_rows at most 2^30.
+ * The head sizes are those of dsa_absorb_q; num_tokens at most 2^30, num_rows 2^26.
  * What is written must not overlap an input or each other (INVALID_ARG);
  * softmax_scale is finite and not negative.
  * A token with q_pos = -1, and padding (t >= cu_q[num_req]), sees nothing: out = 0 and

@@ -30,13 +30,13 @@ def M(i, by=4):  # the same, not aligned
 
 
 def _absorb(lib, **over):
-    a = dict(q=A(0), ts=64 * 192, hs=192, w=A(1), n=4, H=64, dn=128, dr=64, dv=128, dl=512, y=A(2), s=None)
+    a = dict(q=A(0), ts=64 * 192, hs=192, w=A(1), n=4, H=64, dn=128, dr=64, dv=128, dl=512, y=A(2), st=None, s=None)
     a.update(over)
     return lib.dsa_absorb_q(*a.values())
 
 
 def _project(lib, **over):
-    a = dict(o=A(0), ts=64 * 512, hs=512, w=A(1), n=4, H=64, dn=128, dv=128, dl=512, y=A(2), s=None)
+    a = dict(o=A(0), ts=64 * 512, hs=512, w=A(1), n=4, H=64, dn=128, dv=128, dl=512, y=A(2), st=None, s=None)
     a.update(over)
     return lib.dsa_project_out(*a.values())
 
@@ -99,7 +99,7 @@ def _prompt(lib, **over):
 @no_device_only
 @pytest.mark.parametrize("over,expect", [
     (dict(n=-1), 1), (dict(n=0), 0), (dict(N=-1), 1), (dict(R=-1), 1), (dict(R=8193), 2), (dict(n=(1 << 30) + 1), 2),
-    (dict(N=(1 << 30) + 1), 2), (dict(S=0), 1), (dict(S=65), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
+    (dict(N=(1 << 26) + 1), 2), (dict(N=1 << 26, kt=(1 << 36) - 8), 1), (dict(S=0), 1), (dict(S=65), 1), (dict(scale=float("nan")), 1), (dict(scale=float("inf")), 1),
     (dict(scale=-0.1), 1), (dict(H=0), 1), (dict(H=1025), 2), (dict(dn=8), 2), (dict(dn=144), 2), (dict(dr=72), 2),
     (dict(dv=8), 2), (dict(dv=256), 2), (dict(q=None), 1), (dict(q=M(0)), 1), (dict(qt=4), 1), (dict(qh=-8), 1),
     (dict(kv=None), 1), (dict(kv=M(1)), 1), (dict(kt=4), 1), (dict(kh=12), 1), (dict(rope=None), 1), (dict(rope=M(2)), 1),
