@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
           tc_fence_before_sync();
           __syncwarp();
           if (lane == 0) {
-            if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(bar(B_DE + (d & 1)), 0));
+            if constexpr (PAIR) mbar_arrive_cluster_relaxed(cluster_addr(bar(B_DE + (d & 1)), 0));
             else mbar_arrive(bar(B_DE + (d & 1)));
           }
         };
