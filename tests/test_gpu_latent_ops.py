@@ -604,3 +604,68 @@ def test_a_prompt_in_both_forms():
         assert rel <= 2.25e-3 * math.sqrt(1 + 1 + 1 + 16), rel
         assert float(a[n:].abs().max()) == 0 and float(b[n:].max()) == -math.inf
         assert float((b[:n].double() - want_lse[:n]).abs().max()) <= 0.05
+
+
+def test_calls_of_several_threads_and_graphs_at_once():
+    """Host threads on streams of their own, and two captured steps replayed side by side: the same bits as alone."""
+    import threading
+
+    c, g = LARGE, gen(30)
+    w = weight(c, g)
+    q, o = rows((70, 64, 192), g), rows((70, 64, 512), g)
+    kv, scale, table = cache(c, 2, 300, 64, g)
+    lens = i32([300, 211])
+    pq, _, _, cu_q, cu_k, pos = batch(c, [(40, 300), (30, 211)], g)
+    tq, tp = i32(cu_q), i32(pos)
+
+    def step():
+        x = dsa.expand_kv(kv, scale, table, lens, w, d_rope=64, page_size=64, capacity=511)
+        return (dsa.absorb_q(q, w, d_rope=64), dsa.project_out(o, w, d_nope=128), x.kv,
+                *dsa.prompt_mla(pq, x.kv, x.k_rope, tq, x.cu_k, tp, d_nope=128, softmax_scale=0.07),
+                *dsa.prompt_mla(pq, x.kv, x.k_rope, tq, x.cu_k, tp, d_nope=128, softmax_scale=0.07, num_splits=2))
+
+    want = step()
+    torch.cuda.synchronize()
+    got, errors = {}, []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got[i] = step()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # pragma: no cover
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for r in got.values():
+        assert all(torch.equal(a, b) for a, b in zip(r, want))
+    graphs = []
+    for _ in range(2):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            out = step()
+        graphs.append((graph, out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for graph, _, s in graphs:
+            with torch.cuda.stream(s):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, out, _ in graphs:
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_prompt_requests_of_every_length():
+    """Queries from 1 to 300 behind contexts that end anywhere in a tile: one call, each request checked."""
+    c, g = SMALL, gen(31)
+    lens = [(n, n + (37 * n) % 290) for n in range(1, 301, 7)]
+    x = batch(c, lens, g, extra=5)
+    check_prompt(c, *x, 48**-0.5, run_prompt(c, *x))
+    check_prompt(c, *x, 48**-0.5, run_prompt(c, *x, num_splits=5))
