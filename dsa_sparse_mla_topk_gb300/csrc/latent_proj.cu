@@ -448,7 +448,6 @@ __global__ void __launch_bounds__(EX_THREADS) expand_rows_kernel(const ExpandArg
 
   // ---- where the CTA's rows are, a thread a row; then 16 bytes a thread ----
   __shared__ int32_t s_slot[EX_ROWS];
-  __shared__ float s_scale[EX_ROWS];
   const int n0 = blockIdx.x * EX_ROWS;
   if (tid < EX_ROWS && n0 + tid < total) {
     const int n = n0 + tid;
@@ -462,17 +461,16 @@ __global__ void __launch_bounds__(EX_THREADS) expand_rows_kernel(const ExpandArg
     const bool good = page >= 0 && page < a.num_pages;
     if (!good) report(a.dev_status, DSA_DEV_BAD_PAGE);
     const int slot = good ? page * a.page_size + pos % a.page_size : -1;  // (num_pages page_size < 2^31)
-    const float sc = good ? a.kv_scale[slot] : 0.f;
     s_slot[tid] = slot;
-    s_scale[tid] = sc;
-    scale[n] = sc;
   }
   __syncthreads();
   const int dl = a.d_latent, row_bytes = dl + a.d_rope, chunks = row_bytes / 16;
   const int rows = min(EX_ROWS, total - n0);
   for (int e = tid; e < rows * chunks; e += EX_THREADS) {
     const int i = e / chunks, c = e - i * chunks, slot = s_slot[i], n = n0 + i;
-    const float sc = s_scale[i];
+    // (the row's scale beside its bytes, where it is needed)
+    const float sc = slot >= 0 && 16 * (c + 1) >= dl ? __ldg(a.kv_scale + slot) : 0.f;
+    if (16 * (c + 1) == dl) scale[n] = sc;
     const uint4 v = slot >= 0 ? __ldg(reinterpret_cast<const uint4*>(a.kv + (int64_t)slot * row_bytes) + c) : make_uint4(0, 0, 0, 0);
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     const bool rope = 16 * c >= dl;

@@ -296,18 +296,16 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
         // the last tiles first: in causal prompts they see the most
         find_tile(a, (int)gridDim.x - 1 - x, misc, req, q0, rows);
         if (req != -2) {
-          int k0 = 0, kv_len = 0;
-          if (req >= 0) {
-            k0 = __ldg(a.cu_k + req);
-            const int k1 = __ldg(a.cu_k + req + 1);
-            if (k0 >= 0 && k1 >= k0 && k1 <= a.num_rows) kv_len = k1 - k0;
-            else if (lane == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
-          }
+          // (all loads before the first use of one)
+          int k0 = 0, k1 = 0, kv_len = 0, pos[QT / 32];
+          if (req >= 0) k0 = __ldg(a.cu_k + req), k1 = __ldg(a.cu_k + req + 1);
+#pragma unroll
+          for (int i = 0; i < QT / 32; ++i) pos[i] = req >= 0 && 32 * i + lane < rows ? __ldg(a.q_pos + q0 + 32 * i + lane) : -2;
+          if (k0 >= 0 && k1 >= k0 && k1 <= a.num_rows) kv_len = k1 - k0;
+          else if (lane == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
           int n_g[2] = {0, 0}, full_g[2] = {0, 0};  // tiles that some row of query tile g sees, that all see whole
           if (req >= 0) {
-            int mx[2] = {-1, -1}, mn[2] = {INT32_MAX, INT32_MAX}, pos[QT / 32];
-#pragma unroll
-            for (int i = 0; i < QT / 32; ++i) pos[i] = 32 * i + lane < rows ? __ldg(a.q_pos + q0 + 32 * i + lane) : -2;
+            int mx[2] = {-1, -1}, mn[2] = {INT32_MAX, INT32_MAX};
 #pragma unroll
             for (int i = 0; i < QT / 32; ++i)
               if (32 * i + lane < rows) {
