@@ -632,7 +632,7 @@ DSA_API size_t dsa_expand_kv_workspace_size(int32_t capacity, int32_t d_latent);
  * lse = -inf.  What no token of a request sees is not looked at; a row that a token does not
  * see does not reach its result, whatever it holds.  NaN in a query or a visible key gives
  * NaN in out and lse of that head, NaN or an infinity in a visible value NaN or an infinity in out.
- * Precision: logits, sums and out are fp32, a weight is rounded to bf16 (2^-9 of it).
+ * Precision: logits, sums and out are fp32, a weight is rounded to bf16 (2^-8 of it at most).
  * Data errors: cu_q decreasing or past num_tokens sets DSA_DEV_BAD_INDEX and such a
  * request's tokens are left as they are; cu_k decreasing or past num_rows sets it and
  * the request's tokens see nothing; q_pos outside [-1, cu_k[r + 1] - cu_k[r]) sets
