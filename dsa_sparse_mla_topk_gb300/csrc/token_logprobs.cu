@@ -23,6 +23,8 @@
 //    for the next one.
 // A row of 16-bit values costs 6.5 instructions a value (of 10.9 that the SMs have in the time
 // that HBM takes): two-wide fp32 arithmetic, maxima and counts two-wide in the type.
+// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 66 us (4.1 TB/s; the loads alone 47, with the sums
+// 54), 128 such rows fp32 19 us, 4 rows of 32,003 fp32 9.4 us (launch and the chain of steps).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
