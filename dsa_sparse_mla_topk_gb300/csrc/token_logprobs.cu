@@ -12,19 +12,18 @@
 // thread keeps its own largest value m_t and the sums of 2^x and 2^x x relative to it, and
 // counts the columns before the token.  Then
 //  * the sums are put together relative to the largest m_t.  Only the thread that holds it
-//    has the term 1 among its terms: one warp reads that thread's columns again and sums
-//    them without it.
-//  * of the k-th largest m_t, tau, it is known that k columns at least reach it: all
-//    alternatives are among the columns >= tau, which only the few threads with m_t >= tau
-//    hold.  Their columns are read again (from L2) by a warp each; the columns
-//    found, usually little more than k, are put in order by counting.  tau comes from
-//    a bisection on the values' bits that ends as soon as not many more than k threads
-//    reach it.  Too many columns >= tau (equal logits all over): k rounds of a search
-//    for the next one.
+//    has the term 1 among its terms: its columns are read again and summed without it.
+//  * of the k-th largest of 128 groups of threads' maxima, tau, it is known that k columns
+//    at least reach it: all alternatives are among the columns >= tau, which only a few threads
+//    hold (about as many as k).  Their columns are read again (from L2) too; those that reach
+//    tau, usually little more than k, are put in order by counting.  Too many of them (equal
+//    logits all over): k rounds of a search for the next one.
 // A row of 16-bit values costs 6.5 instructions a value (of 10.9 that the SMs have in the time
 // that HBM takes): two-wide fp32 arithmetic, maxima and counts two-wide in the type.
-// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 66 us (4.1 TB/s; the loads alone 47, with the sums
-// 54), 128 such rows fp32 19 us, 4 rows of 32,003 fp32 9.4 us (launch and the chain of steps).
+// What follows a row is a chain of ten thousand cycles that mostly waits; a row a CTA of 256 threads,
+// four an SM, lets other rows' loads run under it.
+// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 64 us (4.2 TB/s), 4,096 rows of 32,000 90 us, 128
+// rows of 131,072 fp32 19 us, 4 rows of 32,003 fp32 8.8 us (launch and the chain of steps).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -40,9 +39,11 @@ namespace cg = cooperative_groups;
 namespace dsa {
 namespace {
 
-constexpr int THREADS = 512, WARPS = THREADS / 32, MAX_CLUSTER = 8, MAX_TOP = token_logprobs_max_top();
+constexpr int MAX_CLUSTER = 8, MAX_TOP = token_logprobs_max_top();
+constexpr int SLOTS = 512;  // parts of a share, each with its largest value: a thread's, cut in time where there are fewer threads
 constexpr int TURNS = 4;    // loads of a thread in flight
 constexpr int CAND = 1024;  // columns >= tau that are put in order
+constexpr int GROUPS = 128;  // of slots, slot mod GROUPS: as many hold values as loads do, at most all
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float X_MIN = -200.f;  // 2^x is 0 from -150 on; x of a masked column (-inf) times 0 would be NaN
 
@@ -57,6 +58,8 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
+
+__device__ __forceinline__ float value_of(uint32_t o) { return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o); }
 
 // Whether (x, i) comes before (y, j): larger, or equal and of a lower column.
 __device__ __forceinline__ bool before(float x, int i, float y, int j) { return x > y || (x == y && i < j); }
@@ -188,25 +191,25 @@ struct Part {
   int count, n;          // columns before the token; alternatives listed
 };
 struct Shared {
-  float wf[2][WARPS];
-  int wi[WARPS];
-  uint32_t wk[2][WARPS];
-  float m_t[THREADS];
+  float wf[2][16];
+  int wi[2][16], wt[16];
+  uint32_t wk[2][16];
+  float m_s[SLOTS];
+  __align__(16) float gm[GROUPS];
   Part part[MAX_CLUSTER];
   float lz[MAX_CLUSTER][MAX_TOP];
   int lc[MAX_CLUSTER][MAX_TOP];
   float cz[CAND];
   int cc[CAND];
-  int list[THREADS];
-  int owner, flagged, cands;
-  float own_rest, own_ent;
+  int list[SLOTS + 4];
+  int listed, cands;
 };
 
 // Sums and order over the share [v0, v1) of a row's loads by this CTA.
-template <class T>
+template <class T, int THREADS>
 __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, const int32_t* token, int& t, float& zt,
                                              bool& bad, int top, Shared* sh, Part* part, float* lz, int* lc) {
-  constexpr int N = Pack<T>::N;
+  constexpr int N = Pack<T>::N, WARPS = THREADS / 32, SEG = SLOTS / THREADS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // a turn's loads are on their way while the one before is worked on, the first while the token is looked up
   auto fetch = [&](int vb, uint4 (&w)[TURNS]) {
@@ -232,6 +235,15 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
   float m = -INFINITY;
   uint64_t s2 = 0, e2 = 0;
   int count = 0;
+  // a thread's slots: `per` turns each
+  const int per = ((v1 - v0 + THREADS * TURNS - 1) / (THREADS * TURNS) + SEG - 1) / SEG;
+  float m_seg = -INFINITY;
+  int seg = 0, left = per;
+  if (tid == 0 && v0 == 0 && t >= 0) {  // equal values of lower columns in the token's own load
+    const uint4 w = row.load(vt);
+#pragma unroll
+    for (int c = 0; c < N; ++c) count += Pack<T>::get(w, c) == zt && vt * N - row.shift + c < t;
+  }
   for (int vb = v0; vb < v1; vb += THREADS * TURNS) {
     uint4 w[TURNS];
 #pragma unroll
@@ -245,7 +257,11 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
       n.take(w[k], vb + THREADS * k + tid < vt ? thr_lo : thr_hi);
     }
     count += n.value();
-    const float up = fmaxf(m, most.value());
+    const float now = most.value(), up = fmaxf(m, now);
+    if (SEG > 1) {
+      m_seg = fmaxf(m_seg, now);
+      if (--left == 0) sh->m_s[seg * THREADS + tid] = m_seg, m_seg = -INFINITY, ++seg, left = per;
+    }
     if (up > m) {  // the sums relative to the new largest value: 2^(x + d) (x + d)
       const float d = fmaxf((m - up) * LOG2E, X_MIN), f = ex2(d);
       const uint64_t d2 = pk2(d, d), f2 = pk2(f, f);
@@ -274,113 +290,153 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
   e += hi;
 
   // ---- the largest value, and one thread that holds it ----
-  if (tid == 0) sh->owner = THREADS, sh->flagged = 0, sh->cands = 0;
-  sh->m_t[tid] = m;
-  const uint32_t key = order_of(m), wmost = __reduce_max_sync(0xffffffffu, key), wleast = __reduce_min_sync(0xffffffffu, key);
-  if (lane == 0) sh->wk[0][warp] = wmost, sh->wk[1][warp] = wleast;
+  if (tid == 0) sh->listed = SEG, sh->cands = 0;  // the owner's first
+  if (SEG == 1) sh->m_s[tid] = m;
+  else
+    for (; seg < SEG; ++seg) sh->m_s[seg * THREADS + tid] = m_seg, m_seg = -INFINITY;
+  const uint32_t key = order_of(m), wmost = __reduce_max_sync(0xffffffffu, key);
+  const int wfirst = __ffs(__ballot_sync(0xffffffffu, key == wmost)) - 1;
+  if (lane == 0) sh->wk[0][warp] = wmost, sh->wt[warp] = warp * 32 + wfirst;
   __syncthreads();
-  uint32_t most = 0, least = UINT32_MAX;
+  const uint32_t kw = sh->wk[0][lane % WARPS], most = __reduce_max_sync(0xffffffffu, kw);
+  const int owner = sh->wt[__ffs(__ballot_sync(0xffffffffu, kw == most)) - 1];
+  const float M = value_of(most);
+
+  // ---- tau: the top-th largest of the groups' maxima ----
+  uint32_t tau = UINT32_MAX;
+  if (top > 0) {
+    if (tid < GROUPS) {
+      float g = sh->m_s[tid];
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) most = max(most, sh->wk[0][w]), least = min(least, sh->wk[1][w]);
-  if (key == most) atomicMin(&sh->owner, tid);
-  __syncthreads();
-  const int owner = sh->owner;
-  const float M = sh->m_t[owner];
+      for (int k = GROUPS; k < SLOTS; k += GROUPS) g = fmaxf(g, sh->m_s[tid + k]);
+      sh->gm[tid] = g;
+    }
+    __syncthreads();
+    // a group's threads count the groups that reach it
+    constexpr int EACH = THREADS / GROUPS;
+    const float x = sh->gm[tid / EACH];
+    int c = 0;
+#pragma unroll
+    for (int j = tid % EACH; j < GROUPS / 4; j += EACH) {
+      const float4 y = reinterpret_cast<const float4*>(sh->gm)[j];
+      c += y.x >= x;
+      c += y.y >= x;
+      c += y.z >= x;
+      c += y.w >= x;
+    }
+#pragma unroll
+    for (int o = EACH / 2; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    const uint32_t reached = __reduce_max_sync(0xffffffffu, c >= top ? order_of(x) : 0u);
+    if (lane == 0) sh->wk[1][warp] = reached;
+    __syncthreads();
+    // (fewer groups that hold values: every value)
+    tau = max(__reduce_max_sync(0xffffffffu, sh->wk[1][lane % WARPS]), order_of(-INFINITY) + 1);
+#pragma unroll
+    for (int g = 0; g < SEG; ++g) {
+      const uint32_t flags = __ballot_sync(0xffffffffu, order_of(sh->m_s[g * THREADS + tid]) >= tau && tid != owner);
+      if (flags) {
+        int at = 0;
+        if (lane == 0) at = atomicAdd(&sh->listed, __popc(flags));
+        at = __shfl_sync(0xffffffffu, at, 0);
+        if (flags >> lane & 1) sh->list[at + __popc(flags & ((1u << lane) - 1))] = g * THREADS + tid;
+      }
+    }
+    __syncthreads();
+  }
+
+  // ---- columns read again: the owner's for the sum, the listed threads' for tau ----
   const float d = fmaxf((m - M) * LOG2E, X_MIN), f = m == -INFINITY ? 0.f : ex2(d);
   // (a thread without values: s is 0, or NaN where there was one)
   e = fmaf(s, m == -INFINITY ? 0.f : d, e) * f;
   s = m == -INFINITY ? s : s * f;
   if (tid == owner && M > -INFINITY) s = 0.f, e = 0.f;
+  int same = 0;
+  const int listed = sh->listed, loads = SEG > 1 ? per * TURNS : (v1 - v0 + THREADS - 1) / THREADS;  // of a slot
+  const int lg = loads > 1 ? 32 - __clz(loads - 1) : 0;
+  constexpr int AT_ONCE = 1024 / THREADS;  // the listed slots' loads in a round or two
+  for (int q0 = tid; q0 < listed << lg; q0 += THREADS * AT_ONCE) {
+    uint4 w[AT_ONCE];
+    int who[AT_ONCE], v[AT_ONCE];
+#pragma unroll
+    for (int h = 0; h < AT_ONCE; ++h) {
+      const int q = q0 + THREADS * h, k = q >> lg, j = q & ((1 << lg) - 1);
+      const int slot = k < SEG ? k * THREADS + owner : k < listed ? sh->list[k] : 0;
+      who[h] = slot % THREADS;
+      v[h] = v0 + who[h] + THREADS * (slot / THREADS * loads + j);
+      if (k >= listed || j >= loads || v[h] >= v1) who[h] = -1;
+      else w[h] = row.load(v[h]);
+    }
+#pragma unroll
+    for (int h = 0; h < AT_ONCE; ++h) {
+      if (who[h] < 0) continue;
+      int hits = 0;
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        const float z = Pack<T>::get(w[h], c);
+        hits += z > -INFINITY && order_of(z) >= tau;
+      }
+      if (hits > 0) {
+        int at = atomicAdd(&sh->cands, hits);
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float z = Pack<T>::get(w[h], c);
+          if (z > -INFINITY && order_of(z) >= tau) {
+            if (at < CAND) sh->cz[at] = z, sh->cc[at] = v[h] * N - row.shift + c;
+            ++at;
+          }
+        }
+      }
+      if (who[h] == owner && M > -INFINITY) {
+#pragma unroll
+        for (int c = 0; c < N; ++c) {
+          const float z = Pack<T>::get(w[h], c);
+          if (z == M) {
+            ++same;
+          } else {
+            const float x = max_nan((z - M) * LOG2E, X_MIN), p = ex2(x);
+            s += p;
+            e = fmaf(p, x, e);
+          }
+        }
+      }
+    }
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     s += __shfl_xor_sync(0xffffffffu, s, o);
     e += __shfl_xor_sync(0xffffffffu, e, o);
   }
   count = (int)__reduce_add_sync(0xffffffffu, (uint32_t)count);
-  if (lane == 0) sh->wf[0][warp] = s, sh->wf[1][warp] = e, sh->wi[warp] = count;
-
-  // ---- tau: at least `top` threads reach it, few more if the values allow ----
-  // (by the whole block: one warp over all 512 values takes 0.5 us longer)
-  uint32_t tau = 0;
-  if (top > 0) {
-    const uint32_t none = order_of(-INFINITY);
-    // reached by at least `top` threads (or all that hold values); by none
-    uint32_t lo = max(least, none + 1), up = most + 1;
-    if (most > none && (least > none || __syncthreads_count(key >= lo) > top)) {
-      while (up - lo > 1) {
-        const uint32_t mid = lo + (up - lo) / 2;
-        const int c = __syncthreads_count(key >= mid);
-        if (c >= top) {
-          lo = mid;
-          if (c <= top + top / 4 + 4) break;
-        } else {
-          up = mid;
-        }
-      }
-    }
-    tau = lo;
-    if (key >= tau) sh->list[atomicAdd(&sh->flagged, 1)] = tid;
-  }
-  __syncthreads();
-  // ---- columns read again, a warp a thread's: the owner's for the sum, the others' for tau ----
-  const int flagged = sh->flagged;
-  auto turn = [&](int who, int i) { return v0 + who + THREADS * i; };
-  if (warp == 0 && M > -INFINITY) {
-    float rs = 0.f, re = 0.f;
-    int same = 0;
-    for (int i = lane; turn(owner, i) < v1; i += 32) {
-      const uint4 w = row.load(turn(owner, i));
-#pragma unroll
-      for (int q = 0; q < N; ++q) {
-        const float z = Pack<T>::get(w, q);
-        if (z == M) {
-          ++same;
-        } else {
-          const float x = max_nan((z - M) * LOG2E, X_MIN), p = ex2(x);
-          rs += p;
-          re = fmaf(p, x, re);
-        }
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      rs += __shfl_xor_sync(0xffffffffu, rs, o);
-      re += __shfl_xor_sync(0xffffffffu, re, o);
-    }
-    same = (int)__reduce_add_sync(0xffffffffu, (uint32_t)same);
-    if (lane == 0) sh->own_rest = rs + (float)(same - 1), sh->own_ent = re;
-  }
-  for (int q = WARPS - 1 - warp; q < flagged; q += WARPS) {
-    const int who = sh->list[q];
-    for (int i = lane; turn(who, i) < v1; i += 32) {
-      const int v = turn(who, i);
-      const uint4 w = row.load(v);
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
-        const float z = Pack<T>::get(w, c);
-        if (z > -INFINITY && order_of(z) >= tau) {
-          const int at = atomicAdd(&sh->cands, 1);
-          if (at < CAND) sh->cz[at] = z, sh->cc[at] = v * N - row.shift + c;
-        }
-      }
-    }
-  }
+  same = (int)__reduce_add_sync(0xffffffffu, (uint32_t)same);
+  if (lane == 0) sh->wf[0][warp] = s, sh->wf[1][warp] = e, sh->wi[0][warp] = count, sh->wi[1][warp] = same;
   __syncthreads();
   const int cands = sh->cands;
-  if (tid == 0) {
-    float rs = M > -INFINITY ? sh->own_rest : 0.f, re = M > -INFINITY ? sh->own_ent : 0.f;
-    int c = 0;
-    for (int w = 0; w < WARPS; ++w) rs += sh->wf[0][w], re += sh->wf[1][w], c += sh->wi[w];
-    part->top = M, part->rest = rs, part->ent = re, part->count = c;
-    part->n = cands <= CAND ? min(top, cands) : top;
+  if (warp == 0) {
+    s = lane < WARPS ? sh->wf[0][lane] : 0.f, e = lane < WARPS ? sh->wf[1][lane] : 0.f;
+#pragma unroll
+    for (int o = WARPS / 2; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
+    count = (int)__reduce_add_sync(0xffffffffu, lane < WARPS ? sh->wi[0][lane] : 0);
+    same = (int)__reduce_add_sync(0xffffffffu, lane < WARPS ? sh->wi[1][lane] : 0);
+    if (lane == 0) {
+      part->top = M, part->rest = M > -INFINITY ? s + (float)(same - 1) : s, part->ent = e, part->count = count;
+      part->n = cands <= CAND ? min(top, cands) : top;
+    }
   }
   if (cands <= CAND) {
-    for (int i = tid; i < cands; i += THREADS) {
-      const float z = sh->cz[i];
-      const int c = sh->cc[i];
+    // eight threads a column
+    for (int q0 = 0; q0 < cands; q0 += THREADS / 8) {
+      const int q = q0 + tid / 8;
+      const float z = q < cands ? sh->cz[q] : 0.f;
+      const int c = q < cands ? sh->cc[q] : 0;
       int r = 0;
-      for (int j = 0; j < cands; ++j) r += before(sh->cz[j], sh->cc[j], z, c);
-      if (r < top) lz[r] = z, lc[r] = c;
+      if (q < cands)
+        for (int j = tid % 8; j < cands; j += 8) r += before(sh->cz[j], sh->cc[j], z, c);
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+      if (q < cands && tid % 8 == 0 && r < top) lz[r] = z, lc[r] = c;
     }
   } else {
     // more than CAND columns reach tau (and so at least `top`): the next one, `top` times
@@ -416,8 +472,8 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs a, const int C) {
+template <class T, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) logprobs_kernel(const LogprobArgs a, const int C) {
   __shared__ Shared sh;
   const int tid = threadIdx.x;
   cg::cluster_group cluster = cg::this_cluster();
@@ -431,7 +487,7 @@ __global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs 
   int t;
   float zt;
   bool bad;
-  share_of_row(row, v0, v1, a.tokens + i, t, zt, bad, a.top, &sh, &sh.part[rank], sh.lz[rank], sh.lc[rank]);
+  share_of_row<T, THREADS>(row, v0, v1, a.tokens + i, t, zt, bad, a.top, &sh, &sh.part[rank], sh.lz[rank], sh.lc[rank]);
   if (bad && tid == 0 && rank == 0) report(a.dev_status, DSA_DEV_BAD_INDEX);
   __syncthreads();
   if (C > 1) {
@@ -468,9 +524,6 @@ __global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs 
   if (tid == 0) {
     a.logprob[i] = odd ? NAN : t < 0 || none ? -INFINITY : (zt - M) - log_total;
     a.entropy[i] = odd ? NAN : none ? 0.f : log_total - LN2 * ent / (1.f + rest);
-    // equal values of lower columns in the token's own load
-    if (t >= 0 && zt > -INFINITY)
-      for (int j = max(0, t - (t + row.shift) % Row<T>::N); j < t; ++j) count += (float)p[j] == zt;
     if (!(t >= 0 && zt == -INFINITY)) a.rank[i] = t < 0 ? -1 : min(count, a.vocab - 1);
   }
   if (t >= 0 && zt == -INFINITY) {  // a masked token: counted on its own
@@ -481,11 +534,11 @@ __global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs 
     }
     n = (int)__reduce_add_sync(0xffffffffu, (uint32_t)n);
     __syncthreads();
-    if ((tid & 31) == 0) sh.wi[tid >> 5] = n;
+    if ((tid & 31) == 0) sh.wi[0][tid >> 5] = n;
     __syncthreads();
     if (tid == 0) {
       n = 0;
-      for (int w = 0; w < WARPS; ++w) n += sh.wi[w];
+      for (int w = 0; w < THREADS / 32; ++w) n += sh.wi[0][w];
       a.rank[i] = min(n, a.vocab - 1);
     }
   }
@@ -512,11 +565,11 @@ __global__ void __launch_bounds__(THREADS, 2) logprobs_kernel(const LogprobArgs 
   }
 }
 
-template <class T>
+template <class T, int THREADS>
 cudaError_t launch(const LogprobArgs& a, cudaStream_t stream) {
   // CTAs a row: few rows share the GPU, as long as a thread has a load and all CTAs run at once, two an
   // SM (64 x 50,000 values 10 us in 256 CTAs, 20 in 512; 128 x 131,072 fp32 19 us in 256, 31 in 512).  Rows
-  // past that go a CTA each (sharing out the last wave's among clusters: 1,024 rows 66 -> 72 us).
+  // past that go a CTA each (sharing out the last wave's among clusters costs 1,024 rows 6 us more).
   const int64_t loads = ((int64_t)a.vocab + Pack<T>::N - 1) / Pack<T>::N;
   int c = 1;
   while (c < MAX_CLUSTER && (int64_t)a.num_rows * c * 2 <= 2 * device_sm_count() && loads > (int64_t)THREADS * c) c *= 2;
@@ -531,16 +584,19 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t stream) {
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, a, c);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, logprobs_kernel<T, THREADS>, a, c);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
-  if (a.dtype == DSA_BF16) return launch<__nv_bfloat16>(a, stream);
-  if (a.dtype == DSA_FP16) return launch<__half>(a, stream);
-  return launch<float>(a, stream);
+  // Many rows: CTAs of half the threads, whose chains behind a row overlap.  4,096 x 8,000 bf16 93 -> 56 us, 4,096
+  // x 32,000 117 -> 90, 1,024 x 131,072 67 -> 64, fp32 105 -> 108 (a quarter of the threads: 48, 85, 74, 108).
+  const bool many = a.num_rows > 2 * device_sm_count();
+  if (a.dtype == DSA_BF16) return many ? launch<__nv_bfloat16, 256>(a, stream) : launch<__nv_bfloat16, 512>(a, stream);
+  if (a.dtype == DSA_FP16) return many ? launch<__half, 256>(a, stream) : launch<__half, 512>(a, stream);
+  return many ? launch<float, 256>(a, stream) : launch<float, 512>(a, stream);
 }
 
 }  // namespace dsa

@@ -113,6 +113,17 @@ def test_logprobs_many_rows(R):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,top", [(1, 3), (9, 20), (515, 64), (2049, 64), (8200, 1), (32003, 20), (70001, 0)])
+def test_logprobs_more_rows_than_run_at_once(dtype, V, top):
+    R = 1400
+    z, tok = logits((R, V), dtype, V), some(R, V)
+    z[5], z[-1, V // 2:] = 1.5, -math.inf
+    z[7] = -math.inf
+    tok[::9] = V - 1
+    check(z, tok, top, run(z, tok, top))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["fp32", "bf16", "fp16"])
 @pytest.mark.parametrize("V", [300, 8200, 140003])
 def test_logprobs_shapes_of_rows(dtype, V):
     """Ties everywhere, all equal, ascending, descending, blocks of large ones, a sure token, masks, signed zeros."""
