@@ -18,12 +18,14 @@
 //    hold (about as many as k).  Their columns are read again (from L2) too; those that reach
 //    tau, usually little more than k, are put in order by counting.  Too many of them (equal
 //    logits all over): k rounds of a search for the next one.
-// A row of 16-bit values costs 6.5 instructions a value (of 10.9 that the SMs have in the time
-// that HBM takes): two-wide fp32 arithmetic, maxima and counts two-wide in the type.
+// A row of 16-bit values costs 10 instructions a value, as many as the SMs have in the time that HBM takes:
+// 6.6 are arithmetic (fp32 two-wide, maxima and counts two-wide in the type), the rest a turn's; nothing is
+// checked in turns that lie in the row as a whole (with checks at each load 11.2).
 // What follows a row is a chain of ten thousand cycles that mostly waits; a row a CTA of 256 threads,
 // four an SM, lets other rows' loads run under it.
-// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 64 us (4.2 TB/s), 4,096 rows of 32,000 90 us, 128
-// rows of 131,072 fp32 19 us, 4 rows of 32,003 fp32 8.8 us (launch and the chain of steps).
+// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 59 us (4.6 TB/s), 4,096 rows of 131,072 203 us (5.3 TB/s),
+// 4,096 of 32,000 83 us, 128 of 131,072 fp32 19 us, 4 of 32,003 fp32 8.8 us (launch and the chain of steps).
+// Rows that do not start at 16 bytes pay for their ends, two waits and a turn more: 1,024 x 131,071 75 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -122,14 +124,18 @@ struct Pack16 {
     const T t = (T)x;
     return 0x10001u * *reinterpret_cast<const uint16_t*>(&t);
   }
-  struct Count {  // as numbers of the type: exact up to 256 a half, 32 loads
-    T2 v = as_pair<T2>(0u);
+  struct Count {
+    // of masks of ones (at most 2^15 a half): a lower and b upper halves sum to 2^16 (a - b) - a mod 2^32
+    uint32_t v = 0;
     __device__ __forceinline__ void take(const uint4& w, Bound thr) {
       const T2 t2 = as_pair<T2>(thr);
-      v = __hadd2(v, __hadd2(__hadd2(__hgt2(as_pair<T2>(w.x), t2), __hgt2(as_pair<T2>(w.y), t2)),
-                             __hadd2(__hgt2(as_pair<T2>(w.z), t2), __hgt2(as_pair<T2>(w.w), t2))));
+      v += __hgt2_mask(as_pair<T2>(w.x), t2) + __hgt2_mask(as_pair<T2>(w.y), t2);
+      v += __hgt2_mask(as_pair<T2>(w.z), t2) + __hgt2_mask(as_pair<T2>(w.w), t2);
     }
-    __device__ __forceinline__ int value() const { return (int)(float)v.x + (int)(float)v.y; }
+    __device__ __forceinline__ int value() const {
+      const int a = (int)(0u - v & 0xffffu);
+      return 2 * a - ((int)(v + (uint32_t)a) >> 16);
+    }
   };
   __device__ __forceinline__ static float get(const uint4& w, int e) {
     const uint32_t u = e < 2 ? w.x : e < 4 ? w.y : e < 6 ? w.z : w.w;
@@ -172,9 +178,8 @@ struct Row {
     loads = (V + shift + N - 1) / N;
   }
   __device__ __forceinline__ bool inside(int v) const { return v * N >= shift && v * N - shift + N <= vocab; }
-  __device__ __forceinline__ uint4 full(int v) const { return __ldg(reinterpret_cast<const uint4*>(p - shift) + v); }
   __device__ __forceinline__ uint4 load(int v) const {
-    if (inside(v)) return full(v);
+    if (inside(v)) return __ldg(reinterpret_cast<const uint4*>(p - shift) + v);
     __align__(16) T e[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -211,16 +216,31 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
                                              bool& bad, int top, Shared* sh, Part* part, float* lz, int* lc) {
   constexpr int N = Pack<T>::N, WARPS = THREADS / 32, SEG = SLOTS / THREADS;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // a turn's loads are on their way while the one before is worked on, the first while the token is looked up
+  // A turn's loads are on their way while the one before is worked on, the first while the token is looked up.
+  // Loads that lie in the row as a whole, in0 .. in1 - 1 of the share, wait for nothing; the row's ends are patched in.
+  constexpr int TURN = THREADS * TURNS;
+  const int in0 = max(v0, row.inside(0) ? 0 : 1), in1 = min(v1, row.inside(row.loads - 1) ? row.loads : row.loads - 1);
+  const uint4* from = reinterpret_cast<const uint4*>(row.p - row.shift) + v0 + tid;
   auto fetch = [&](int vb, uint4 (&w)[TURNS]) {
-    const bool whole = vb + THREADS * TURNS <= v1 && row.inside(vb) && row.inside(vb + THREADS * TURNS - 1);
+    if (vb >= in0 && vb + TURN <= in1) {
 #pragma unroll
-    for (int k = 0; k < TURNS; ++k) {
-      const int v = vb + THREADS * k + tid;
-      if (whole) w[k] = row.full(v);
-      else if (v < v1) w[k] = row.load(v);
-      else w[k] = make_uint4(Pack<T>::minus_inf(), Pack<T>::minus_inf(), Pack<T>::minus_inf(), Pack<T>::minus_inf());
+      for (int k = 0; k < TURNS; ++k) w[k] = __ldg(from + THREADS * k);
+    } else {
+#pragma unroll
+      for (int k = 0; k < TURNS; ++k) {
+        const int v = vb + THREADS * k + tid;
+        w[k] = make_uint4(Pack<T>::minus_inf(), Pack<T>::minus_inf(), Pack<T>::minus_inf(), Pack<T>::minus_inf());
+        if (v >= in0 && v < in1) w[k] = __ldg(from + THREADS * k);
+      }
+      if ((vb < in0 && v0 < v1) || (in1 < v1 && vb + TURN > in1)) {
+#pragma unroll
+        for (int k = 0; k < TURNS; ++k) {
+          const int v = vb + THREADS * k + tid;
+          if (v < v1 && (v < in0 || v >= in1)) w[k] = row.load(v);
+        }
+      }
     }
+    from += TURN;
   };
   uint4 next[TURNS];
   fetch(v0, next);
@@ -236,7 +256,7 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
   uint64_t s2 = 0, e2 = 0;
   int count = 0;
   // a thread's slots: `per` turns each
-  const int per = ((v1 - v0 + THREADS * TURNS - 1) / (THREADS * TURNS) + SEG - 1) / SEG;
+  const int per = ((v1 - v0 + TURN - 1) / TURN + SEG - 1) / SEG;
   float m_seg = -INFINITY;
   int seg = 0, left = per;
   if (tid == 0 && v0 == 0 && t >= 0) {  // equal values of lower columns in the token's own load
@@ -244,19 +264,22 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
 #pragma unroll
     for (int c = 0; c < N; ++c) count += Pack<T>::get(w, c) == zt && vt * N - row.shift + c < t;
   }
-  for (int vb = v0; vb < v1; vb += THREADS * TURNS) {
+  int room = 512;
+  typename Pack<T>::Count n;
+#pragma unroll 1
+  for (int vb = v0; vb < v1; vb += TURN) {
     uint4 w[TURNS];
 #pragma unroll
     for (int k = 0; k < TURNS; ++k) w[k] = next[k];
-    if (vb + THREADS * TURNS < v1) fetch(vb + THREADS * TURNS, next);
+    if (vb + TURN < v1) fetch(vb + TURN, next);
     typename Pack<T>::Most most;
-    typename Pack<T>::Count n;
+    const int before_t = vt - tid - vb;
 #pragma unroll
     for (int k = 0; k < TURNS; ++k) {
       most.take(w[k]);
-      n.take(w[k], vb + THREADS * k + tid < vt ? thr_lo : thr_hi);
+      n.take(w[k], THREADS * k < before_t ? thr_lo : thr_hi);
     }
-    count += n.value();
+    if (--room == 0) count += n.value(), n = {}, room = 512;
     const float now = most.value(), up = fmaxf(m, now);
     if (SEG > 1) {
       m_seg = fmaxf(m_seg, now);
@@ -283,6 +306,7 @@ __device__ __forceinline__ void share_of_row(const Row<T>& row, int v0, int v1, 
         e2 = fma2(p, pk2(x0, x1), e2);
       }
   }
+  count += n.value();
   float s, e, hi;
   upk2(s2, s, hi);
   s += hi;
@@ -592,7 +616,8 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
   // Many rows: CTAs of half the threads, whose chains behind a row overlap.  4,096 x 8,000 bf16 93 -> 56 us, 4,096
-  // x 32,000 117 -> 90, 1,024 x 131,072 67 -> 64, fp32 105 -> 108 (a quarter of the threads: 48, 85, 74, 108).
+  // x 32,000 117 -> 90, 1,024 x 131,072 67 -> 64, fp32 105 -> 108 (a quarter of the threads: 48, 85, 74, 108);
+  // measured before the loads' checks went.
   const bool many = a.num_rows > 2 * device_sm_count();
   if (a.dtype == DSA_BF16) return many ? launch<__nv_bfloat16, 256>(a, stream) : launch<__nv_bfloat16, 512>(a, stream);
   if (a.dtype == DSA_FP16) return many ? launch<__half, 256>(a, stream) : launch<__half, 512>(a, stream);
