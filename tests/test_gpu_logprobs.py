@@ -222,6 +222,15 @@ def test_logprobs_outputs_streams_and_graphs(both_ways):
     assert empty.logprob.shape == (0,) and empty.top_ids.shape == (0, 3)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16], ids=["fp32", "bf16", "fp16"])
+def test_logprobs_of_a_very_long_row(dtype):
+    """Thousands of turns a thread: counts of the columns before the token are carried over in between."""
+    V = 70_000_003
+    z = logits((2, V), dtype, 7)
+    at = [int(torch.sort(r.float()).indices[k]) for r, k in zip(z, (10, V // 2))]  # a token almost all come before, one in the middle
+    check(z, i32(at), 20, run(z, i32(at), 20))
+
+
 def test_logprobs_rows_past_32_bit_offsets():
     big = torch.empty((2, 2**31 + 8), dtype=torch.bfloat16, device="cuda")
     z = big[:, :5000]
