@@ -323,8 +323,9 @@ DSA_API dsa_status dsa_test_sparse_mla_fwd_cuda_cores(const void* q, const uint8
 
 dsa_status dsa_combine(const float* o_part, const float* lse_part, int32_t num_splits, int32_t num_q,
                        int32_t num_heads, int32_t d_v, void* out, float* lse, void* stream) {
-  if (num_q < 0 || num_splits < 1 || num_splits > 64 || num_heads < 1 || num_heads > 64 || d_v <= 0 ||
-      d_v % 4 != 0)
+  // (what the attention calls write: up to 64 heads in the latent space, 1,024 of at most 128 values)
+  if (num_q < 0 || num_splits < 1 || num_splits > 64 || num_heads < 1 || num_heads > (d_v <= 128 ? 1024 : 64) ||
+      d_v <= 0 || d_v % 4 != 0)
     return DSA_ERR_INVALID_ARG;
   if (num_q == 0) return DSA_OK;
   if (!o_part || !lse_part || !out || !aligned16(o_part) || !aligned16(out)) return DSA_ERR_INVALID_ARG;

@@ -291,7 +291,8 @@ DSA_API dsa_status dsa_topk_sparse_mla_fwd(const float* scores, int64_t ld_score
  * Splits with lse_part = -inf are empty and ignored; if all are, out = 0 and
  * lse = -inf.  o_part fp32 [S, num_q, heads, d_v]; lse_part fp32 [S, num_q,
  * heads]; out bf16 [num_q, heads, d_v]; lse fp32 [num_q, heads] (may be NULL).
- * d_v must be a multiple of 4 and o_part 16-byte aligned.
+ * d_v must be a multiple of 4, and o_part and out 16-byte aligned.  heads at most 64, or
+ * 1,024 where d_v is at most 128 (dsa_prompt_mla_fwd's), num_splits 1..64 (else INVALID_ARG).
  */
 DSA_API dsa_status dsa_combine(const float* o_part, const float* lse_part, int32_t num_splits, int32_t num_q,
                        int32_t num_heads, int32_t d_v, void* out, float* lse, void* stream);

@@ -1,0 +1,75 @@
+"""GPU tests of latent attention's other form and the products around it at the
+edges of what their calls allow."""
+import math
+
+import pytest
+import torch
+
+import dsa_sparse_mla_topk_gb300 as dsa
+import test_gpu_latent_ops as ops
+from test_gpu_latent_ops import BF16, LARGE, SMALL, both_ways, gen, i32, rows, weight  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from dsa_sparse_mla_topk_gb300 import build
+    build.build()
+    dsa.load_library()
+
+
+def shape(heads, dn=32, dr=16, dv=32, dl=64):
+    return dict(heads=heads, dn=dn, dr=dr, dv=dv, dl=dl)
+
+
+# ---- more than 64 heads ----------------------------------------------------------------
+
+
+@pytest.mark.parametrize("c", [shape(65), shape(96, 128, 64, 128), shape(128, 128, 64, 128), shape(200, 48, 0, 80),
+                               shape(1024, 16, 16, 16)], ids=lambda c: f"{c['heads']}x{c['dn']}")
+@pytest.mark.parametrize("splits", [1, 2, 5, None])
+def test_prompt_many_heads(c, splits, both_ways):  # noqa: F811
+    """Heads past 64, in one share, in several, and in as many as the rule takes."""
+    x = ops.batch(c, [(3, 700), (20, 150), (1, 1)], gen(c["heads"]), extra=2)
+    scale = (c["dn"] + c["dr"])**-0.5
+    ops.check_prompt(c, *x, scale, ops.run_prompt(c, *x, num_splits=splits))
+
+
+def test_prompt_many_heads_shares_by_the_rule(both_ways):  # noqa: F811
+    """A chunk whose number of shares the rule picks from a long context: 96 heads take more than one."""
+    c, new, ctx = shape(96, 16, 0, 16), 256, 16_384
+    assert dsa.pick_prompt_splits(new, 1, 96, ctx, num_sms=152) > 1
+    x = ops.batch(c, [(new, ctx)], gen(3))
+    ops.check_prompt(c, *x, 0.25, ops.run_prompt(c, *x))
+
+
+@pytest.mark.parametrize("heads", [65, 128, 300])
+def test_products_and_expansion_many_heads(heads):
+    c, g, n = shape(heads, 48, 16, 80, 208), gen(heads), 150
+    w = weight(c, g)
+    q, o = rows((n, heads, 64), g), rows((n, heads, 208), g)
+    ops.check_absorb(c, q, w, dsa.absorb_q(q, w, d_rope=16))
+    ops.check_project(c, o, w, dsa.project_out(o, w, d_nope=48))
+    kv, scale, table = ops.cache(c, 3, 200, 48, g)
+    lens = [200, 0, 131]
+    ops.check_expand(c, kv, scale, table, lens, w, 48, ops.run_expand(c, kv, scale, table, lens, w, 48, 340))
+
+
+@pytest.mark.parametrize("heads,d_v", [(64, 512), (65, 128), (96, 80), (1024, 16), (1024, 128), (1000, 4)])
+@pytest.mark.parametrize("splits", [1, 3, 64])
+def test_combine_many_heads(heads, d_v, splits):
+    """out = sum_s exp(lse_s - lse) o_s.  exp's argument is rounded by 2^-24 of |lse_s - lse| (below 40) and its
+    own error is 2^-22; lse by 2^-22 of its value (below 30) and the splits' additions: a weight is off by (40 +
+    120 + 4 + splits) 2^-24 of itself, the sum by the splits' additions more, and a rounding to bf16."""
+    n, g = 3, gen(heads + splits)
+    o = torch.randn((splits, n, heads, d_v), generator=g, device="cuda")
+    l = torch.randn((splits, n, heads), generator=g, device="cuda") * 3
+    l[splits // 2, 1, ::3] = -math.inf
+    out, lse = dsa.combine(o, l)
+    want = torch.logsumexp(l.double(), 0)
+    w = torch.where(torch.isfinite(l), (l.double() - want).exp(), 0.0)
+    off = (164 + splits) * 2.0**-24
+    res = (w[..., None] * o.double()).sum(0)
+    ops.near(out, res, 2.0**-8 * res.abs() + (off + (splits + 1) * 2.0**-24) * (w[..., None] * o.double().abs()).sum(0))
+    ops.near(lse, want, 2.0**-22 * want.abs() + off)
