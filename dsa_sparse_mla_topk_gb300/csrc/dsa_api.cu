@@ -725,7 +725,7 @@ dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_hea
   const dsa_status st = check_latent_dims(num_heads, d_nope, d_rope, d_v, 16);
   if (st != DSA_OK) return st;
   if (num_req > dsa::batch_layout_max_requests() || num_tokens > (1 << 30) || num_rows > (1 << 26))
-    return DSA_ERR_UNSUPPORTED_SHAPE;  // (a wait for a CTA's work of 2^26 rows, 0.8 s, stays below its limit)
+    return DSA_ERR_UNSUPPORTED_SHAPE;  // (a wait for an item's work of 2^26 rows, 2.8 s at most, stays below its limit)
   if (num_tokens == 0) return DSA_OK;
   if (!rows_ok(q, num_tokens, num_heads, q_tok_stride, q_head_stride) || !cu_q || !cu_k || !q_pos) return DSA_ERR_INVALID_ARG;
   if (num_rows > 0) {

@@ -24,8 +24,9 @@
 //  * 17: MMA.  P V of one query tile, then its next Q K^T, then the other's: one tile's
 //    softmax runs under the other's products.
 //  * 18: values that are NaN or infinite are taken out of tiles that some query row
-//    sees only in part (a weight of 0 would turn them into NaN); the few rows that do
-//    see them look them up again at the end.
+//    sees only in part (a weight of 0 would turn them into NaN), and of each column the first
+//    position of one is kept: a row sees a run of positions from the start, so it sees
+//    a column's if and only if it sees that one.
 //  * 19: the next item.
 // All waits are bounded.
 //
@@ -61,6 +62,10 @@ constexpr int REGS_SOFTMAX = 104, REGS_OTHER = 64;
 static_assert(128 * (4 * REGS_SOFTMAX + REGS_OTHER) <= THREADS * 96, "no more registers than at launch");
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
 constexpr float RISE = 8.f;         // a reference moves when a weight would pass 2^RISE
+// Waits end after this long.  Some last for an item's whole work (one query tile's warps wait out the other's): for
+// 2^26 rows, the most that a call takes, 0.9 s (1.7 us a tile where all are looked through for values that are not
+// finite), and 2.8 s (5.4 us) where every tile holds some.
+constexpr uint64_t WAIT_NS = 6000000000ull;
 constexpr float HUGE_X = 0x1p28f;   // logits (to base 2) from here on take a step more
 
 constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;  // query tile g at + 128 g
@@ -91,13 +96,17 @@ struct Item {
   int32_t k0, kv_len, t_begin, t_end;
   int32_t cnt[2], whole[2];  // tiles of the share that query tile g sees, that all its rows see whole
   int32_t fix0;              // from this tile on some row may see a tile in part
-  int32_t any_bad;           // a value that is not finite was taken out
+  int32_t any_bad;           // a value that is not finite was taken out, and first_bad holds this item's
 };
 constexpr int OFF_ANSWER = OFF_BAR + (NBAR * 8 + 15) / 16 * 16;
 constexpr int OFF_MISC = OFF_ANSWER + 16;
 struct Misc {
   Item item[2];
-  alignas(16) int32_t upto[NCHUNK];  // tiles of the requests up to the end of each part (read four at a time)
+  union {
+    alignas(16) int32_t upto[NCHUNK];  // tiles of the requests up to the end of each part; the item warp takes them into
+                                       // registers before the first item
+    alignas(16) int32_t first_bad[128];  // of each column of an item's values
+  };
   int32_t wsum[4];
   uint32_t tmem;
   float pair[2][2][TQ];  // what the two threads of a query row exchange: [query tile][half]
@@ -146,11 +155,10 @@ __device__ __forceinline__ void sum_tiles(const PromptArgs& a, bool tell, Misc* 
 }
 
 // Tile `index` of the requests' tiles one after another, then the padding's (req -1);
-// req -2: none.  One warp.
-__device__ __forceinline__ void find_tile(const PromptArgs& a, int index, const Misc* misc, int& req, int& q0, int& rows) {
+// req -2: none.  One warp; u: parts 4 lane .. + 3 of the sums.
+__device__ __forceinline__ void find_tile(const PromptArgs& a, int index, const int4& u, int& req, int& q0, int& rows) {
   const int lane = threadIdx.x & 31;
   req = -2, q0 = 0, rows = 0;
-  const int4 u = reinterpret_cast<const int4*>(misc->upto)[lane];  // parts 4 lane .. + 3
   const int all = __shfl_sync(0xffffffffu, u.w, 31);
   if (index >= all) {
     const int pad0 = a.num_req > 0 ? min(max(__ldg(a.cu_q + a.num_req), 0), a.num_tokens) : 0;
@@ -207,21 +215,17 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Columns d0 .. d0 + n - 1 (16 or 32) of a row's result.
-__device__ __forceinline__ void finish(const PromptArgs& a, const volatile Item& it, float (&o)[32], int d0, int n, int bad0, int bad1,
-                                       bool live, int64_t row, int64_t part, int dn, int dv, int S) {
-  for (int j = bad0; j <= bad1; ++j) {
-    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kv) +
-                                                    (it.k0 + (int64_t)j) * a.kv_tok_stride + it.h * a.kv_head_stride + dn + d0);
+__device__ __forceinline__ void finish(const PromptArgs& a, const int32_t* first_bad, float (&o)[32], int d0, int n, int last,
+                                       bool look, bool live, int64_t row, int64_t part, int dv, int S) {
+  if (look) {  // values that were taken out, and that this row sees
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (8 * e < n) {
-        const uint4 w4 = __ldg(v + e);
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // (an exponent of ones)
-          if ((w[q] & 0x7f80u) == 0x7f80u) o[8 * e + 2 * q] = NAN;
-          if ((w[q] & 0x7f800000u) == 0x7f800000u) o[8 * e + 2 * q + 1] = NAN;
-        }
+    for (int e = 0; e < 8; ++e)
+      if (4 * e < n) {
+        const int4 f = reinterpret_cast<const int4*>(first_bad + d0)[e];
+        if (f.x <= last) o[4 * e] = NAN;
+        if (f.y <= last) o[4 * e + 1] = NAN;
+        if (f.z <= last) o[4 * e + 2] = NAN;
+        if (f.w <= last) o[4 * e + 3] = NAN;
       }
   }
   if (!live) return;
@@ -250,6 +254,15 @@ __device__ __forceinline__ void finish(const PromptArgs& a, const volatile Item&
     for (int e = 0; e < 8; ++e)
       if (4 * e < n) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
   }
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, float x) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(addr), "f"(x) : "memory");
+}
+__device__ __forceinline__ float ld_shared(uint32_t addr) {
+  float x;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(addr) : "memory");
+  return x;
 }
 
 // STD: head widths 128 + 64 (rotated) and values of 128, known to the compiler.
@@ -286,9 +299,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
   const uint32_t tmem = misc->tmem;
   const int nn = (dn + 63) / 64, nk = nn + (dr > 0 ? 1 : 0), nv = (dv + 63) / 64;
   bool ok = true;
+  auto wait_for = [](uint32_t b, uint32_t parity) { return mbar_wait(b, parity, WAIT_NS); };
   // waits for item n's description; false: no more
   auto next_item = [&](int n) -> bool {
-    if (!__all_sync(0xffffffffu, mbar_wait(bar(B_IF + (n & 1)), (n >> 1) & 1))) {
+    if (!__all_sync(0xffffffffu, wait_for(bar(B_IF + (n & 1)), (n >> 1) & 1))) {
       ok = false;
       return false;
     }
@@ -304,11 +318,13 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
     if (warp == WARP_NEXT) {
       // ---------------- the items ----------------
       int x = blockIdx.x, y = blockIdx.y, z = blockIdx.z, n = 0, asked = 0;
+      const int4 upto = reinterpret_cast<const int4*>(misc->upto)[lane];
+      __syncwarp();
       bool room = true;  // item n's place is free
       for (;;) {
         int req, q0, rows;
         // the last tiles first: in causal prompts they see the most
-        find_tile(a, (int)gridDim.x - 1 - x, misc, req, q0, rows);
+        find_tile(a, (int)gridDim.x - 1 - x, upto, req, q0, rows);
         if (req != -2) {
           // (all loads before the first use of one)
           int k0 = 0, k1 = 0, kv_len = 0, pos[QT / 32];
@@ -354,7 +370,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           room = false;
         }
         // (one item ahead, no more: the last ones are shared out evenly)
-        if (!room && !__all_sync(0xffffffffu, mbar_wait(bar(B_IE + (n & 1)), ((n >> 1) & 1) ^ 1))) {
+        if (!room && !__all_sync(0xffffffffu, wait_for(bar(B_IE + (n & 1)), ((n >> 1) & 1) ^ 1))) {
           ok = false;
           break;
         }
@@ -364,7 +380,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           clc_try_cancel(smem_u32(smem + OFF_ANSWER), bar(B_CLC));
         }
         __syncwarp();
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_CLC), asked & 1))) {
+        if (!__all_sync(0xffffffffu, wait_for(bar(B_CLC), asked & 1))) {
           ok = false;
           break;
         }
@@ -386,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
         const int cnt = max(it.cnt[0], it.cnt[1]);
         if (lane == 0) {
           auto query = [&](int g) {
-            if (!ok || !mbar_wait(bar(B_QE + g), ((g ? qn1 : qn0) & 1) ^ 1)) {
+            if (!ok || !wait_for(bar(B_QE + g), ((g ? qn1 : qn0) & 1) ^ 1)) {
               ok = false;
               return;
             }
@@ -401,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
             if (lt == 0 && it.cnt[0] > 0) query(0);
             const int n0 = it.k0 + (it.t_begin + lt) * TK;
             for (int c = 0; c < nk && ok; ++c) {
-              if (!mbar_wait(bar(B_KE + slot), phase ^ 1)) {
+              if (!wait_for(bar(B_KE + slot), phase ^ 1)) {
                 ok = false;
                 break;
               }
@@ -413,7 +429,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
             }
             if (lt == 0 && it.cnt[1] > 0) query(1);
             const int s = vt % VST;
-            if (!ok || !mbar_wait(bar(B_VE + s), ((vt / VST) & 1) ^ 1)) {
+            if (!ok || !wait_for(bar(B_VE + s), ((vt / VST) & 1) ^ 1)) {
               ok = false;
               break;
             }
@@ -431,10 +447,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
         item_done(n);
       }
       if (!ok && lane == 0) {  // no copy may land after the CTA is gone
-        if (qn0 > 0) mbar_wait(bar(B_QF), (qn0 - 1) & 1);
-        if (qn1 > 0) mbar_wait(bar(B_QF + 1), (qn1 - 1) & 1);
-        for (int s = 0; s < KSLOTS; ++s) mbar_wait(bar(B_KF + s), s < slot ? phase : phase ^ 1);
-        for (int v = max(0, vt - VST); v < vt; ++v) mbar_wait(bar(B_VF + v % VST), (v / VST) & 1);
+        if (qn0 > 0) wait_for(bar(B_QF), (qn0 - 1) & 1);
+        if (qn1 > 0) wait_for(bar(B_QF + 1), (qn1 - 1) & 1);
+        for (int s = 0; s < KSLOTS; ++s) wait_for(bar(B_KF + s), s < slot ? phase : phase ^ 1);
+        for (int v = max(0, vt - VST); v < vt; ++v) wait_for(bar(B_VF + v % VST), (v / VST) & 1);
       }
       __syncwarp();
     } else if (warp == WARP_MMA) {
@@ -442,7 +458,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
       const uint32_t ID_QK = idesc_f16_f32(TQ, TK, 0, 0, 1);
       const uint32_t ID_PV = STD ? idesc_f16_f32(TQ, 128, 0, 1, 1) : idesc_f16_f32(TQ, dv, 0, 1, 1);
       // (reductions over the warp: their results are in uniform registers)
-      auto wait_u = [&](int b, uint32_t parity) { return __reduce_min_sync(0xffffffffu, (uint32_t)mbar_wait(bar(b), parity)); };
+      auto wait_u = [&](int b, uint32_t parity) { return __reduce_min_sync(0xffffffffu, (uint32_t)wait_for(bar(b), parity)); };
       auto uniform = [&](int v) { return (int)__reduce_max_sync(0xffffffffu, (uint32_t)v); };
       const uint64_t q_desc = smem_desc(smem_u32(smem + OFF_Q), 16, 1024, SWIZZLE_128B);
       const uint64_t k_desc = smem_desc(smem_u32(smem + OFF_K), 16, 1024, SWIZZLE_128B);
@@ -454,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
       // Waits inside an item only note that they gave up: one reduction a tile (30 cycles or more in
       // which no MMA is issued) instead of one a wait; what is issued until then stays in bounds.
       uint32_t fine = 1;
-      auto wait = [&](int b, uint32_t parity) { fine &= (uint32_t)mbar_wait(bar(b), parity, good ? MBAR_LIMIT_NS : 0); };
+      auto wait = [&](int b, uint32_t parity) { fine &= (uint32_t)mbar_wait(bar(b), parity, good ? WAIT_NS : 0); };
       // S_g = Q_g K^T; the last of the tile's users frees its chunks
       auto issue_qk = [&](int g, bool first_user, bool last_user, bool last_tile) {
         int s = slot, ph = phase;
@@ -541,14 +557,14 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           const int v = vt + lt, s = v % VST;
           // (B_VF alone would not do: a wait on a barrier whose phase before the one that is meant
           // has not ended returns at once)
-          if (!__all_sync(0xffffffffu, mbar_wait(bar(B_GO + s), (go >> s) & 1) && mbar_wait(bar(B_VF + s), (v / VST) & 1))) {
+          if (!__all_sync(0xffffffffu, wait_for(bar(B_GO + s), (go >> s) & 1) && wait_for(bar(B_VF + s), (v / VST) & 1))) {
             ok = false;
             break;
           }
           go ^= 1 << s;
+          __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);  // the largest magnitudes, NaN if there is one
           for (int r = lane; r < TK; r += 32) {
-            unsigned char* row = smem + OFF_V + 2 * s * CHUNK + r * 128;
-            __nv_bfloat162 top = __floats2bfloat162_rn(0.f, 0.f);  // the largest magnitudes, NaN if there is one
+            const unsigned char* row = smem + OFF_V + 2 * s * CHUNK + r * 128;
             for (int c = 0; c < nv; ++c)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {  // (every lane at another bank; the order does not matter)
@@ -556,14 +572,55 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
                 auto look = [&](uint32_t u) { top = __hmax2_nan(top, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&u))); };
                 look(w.x), look(w.y), look(w.z), look(w.w);
               }
-            if (!isfinite(__low2float(top)) || !isfinite(__high2float(top))) {
-              for (int c = 0; c < nv; ++c)
-                for (int e = 0; e < 64; ++e) {
-                  uint16_t* u = reinterpret_cast<uint16_t*>(row + c * CHUNK) + e;
-                  if ((*u & 0x7f80u) == 0x7f80u) *u = 0;
-                }
-              misc->item[n & 1].any_bad = 1;
+          }
+          const bool odd = !isfinite(__low2float(top)) || !isfinite(__high2float(top));
+          if (__any_sync(0xffffffffu, odd)) {
+            // (what is kept from tile to tile is in shared memory: the search above needs the registers)
+            volatile Item* const item = &misc->item[n & 1];
+            int4* const kept = reinterpret_cast<int4*>(misc->first_bad) + lane;  // of columns 4 lane .. + 3
+            int first[4] = {INT32_MAX, INT32_MAX, INT32_MAX, INT32_MAX};
+            if (item->any_bad) {
+              const int4 f = *kept;
+              first[0] = f.x, first[1] = f.y, first[2] = f.z, first[3] = f.w;
+            } else if (n > 0 && !__all_sync(0xffffffffu, wait_for(bar(B_IE + ((n - 1) & 1)), ((n - 1) >> 1) & 1))) {
+              ok = false;  // (the places are the item's before until all are done with that)
+              break;
             }
+            __syncwarp();
+            // Four columns a lane, four rows at a time: what is not finite becomes 0.
+            const int at = (item->t_begin + lt) * TK;
+            const __nv_bfloat162 inf = __floats2bfloat162_rn(INFINITY, INFINITY);
+            uint32_t open[2] = {0, 0};  // columns without a first one
+#pragma unroll
+            for (int e = 0; e < 4; ++e) open[e / 2] |= first[e] == INT32_MAX ? 0xffffu << (16 * (e & 1)) : 0u;
+            unsigned char* col = smem + OFF_V + (2 * s + (lane >> 4)) * CHUNK + 8 * (lane & 1);
+            if (lane >> 4 < nv)
+#pragma unroll 1
+              for (int r0 = 0; r0 < TK; r0 += 4) {
+                uint32_t w[4][2];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  const uint2 v = *reinterpret_cast<const uint2*>(col + (r0 + r) * 128 + 16 * (((lane & 15) >> 1) ^ (r0 & 4) ^ r));
+                  w[r][0] = v.x, w[r][1] = v.y;
+                }
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+#pragma unroll
+                  for (int e = 0; e < 2; ++e) {
+                    const uint32_t fine = __hlt2_mask(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[r][e])), inf);
+                    const uint32_t fresh = open[e] & ~fine;
+                    if (fresh) {
+                      if (fresh & 0xffffu) first[2 * e] = at + r0 + r;
+                      if (fresh >> 16) first[2 * e + 1] = at + r0 + r;
+                      open[e] &= fine;
+                    }
+                    w[r][e] &= fine;
+                  }
+                  *reinterpret_cast<uint2*>(col + (r0 + r) * 128 + 16 * (((lane & 15) >> 1) ^ (r0 & 4) ^ r)) = make_uint2(w[r][0], w[r][1]);
+                }
+              }
+            *kept = make_int4(first[0], first[1], first[2], first[3]);
+            item->any_bad = 1;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -579,8 +636,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
     const int g = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
     const int qrow = TQ * g + 32 * quad + lane;  // this thread's query row of the CTA's QT
     const uint32_t lanes = (uint32_t)(32 * quad) << 16, ts = TM_S + 128 * g + lanes, to = TM_O + 128 * g + lanes;
-    float* const mine_p = &misc->pair[g][half][32 * quad + lane];
-    const float* const other_p = &misc->pair[g][half ^ 1][32 * quad + lane];
+    const uint32_t mine_p = smem_u32(&misc->pair[g][half][32 * quad + lane]), other_p = mine_p + (half ? -4 * TQ : 4 * TQ);
     const int pair_bar = 1 + 4 * g + quad;  // the two warps of these 32 rows
     const float c = fmaxf(a.softmax_scale * LOG2E, 0x1p-120f);  // (0 would make NaN of masked logits)
     int sn = 0;  // tiles so far
@@ -606,7 +662,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
       float m = -INFINITY, r = 0.f;  // the reference, and in units of x
       uint64_t l2 = 0;
       for (int lt = 0; lt < mine; ++lt, ++sn) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar(B_SF + g), sn & 1))) ok = false;
+        if (!__all_sync(0xffffffffu, wait_for(bar(B_SF + g), sn & 1))) ok = false;
         tc_fence_after_sync();
         float s[HALF];
 #pragma unroll
@@ -625,14 +681,14 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
         float top = max3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
         // The other thread's; after the barrier S has been read by both, and P may take its place.  (The one
         // behind that keeps a value here until it is read: both pass B_SF's next phase only after P is whole.)
-        *mine_p = top;
+        st_shared(mine_p, top);
         tc_fence_before_sync();
         if (named_barrier_or(pair_bar, 64, !ok)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        top = fmaxf(top, *other_p);
+        top = fmaxf(top, ld_shared(other_p));
         const bool move = (top - m) * c > RISE;
         if (__any_sync(0xffffffffu, move)) {
           float f = 1.f;
@@ -644,7 +700,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           }
           l2 = mul2(l2, pk2(f, f));
           if (lt > 0) {  // each thread half of the columns (a multiple of 16)
-            if (!__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) ok = false;
+            if (!__all_sync(0xffffffffu, wait_for(bar(B_PVD + g), (sn - 1) & 1))) ok = false;
             tc_fence_after_sync();
             for (int b = half; b < dv / 16; b += 2) {
               float o[16];
@@ -689,7 +745,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
         l2 = add2(l2, sum);
       }
       if (mine > 0) {
-        if (ok && !__all_sync(0xffffffffu, mbar_wait(bar(B_PVD + g), (sn - 1) & 1))) ok = false;
+        if (ok && !__all_sync(0xffffffffu, wait_for(bar(B_PVD + g), (sn - 1) & 1))) ok = false;
         if (named_barrier_or(pair_bar, 64, !ok)) {  // (and the maxima have been read)
           ok = false;
           break;
@@ -704,22 +760,20 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
       if (mine == 0) {
         if (live && it.cnt[g ^ 1] > 0) write_nothing(a, row, it.split, half, 2);
       } else {
-        *mine_p = l;
+        st_shared(mine_p, l);
         named_barrier_sync(pair_bar, 64);
-        l = half ? *other_p + l : l + *other_p;  // (the same sum in both)
+        l = half ? ld_shared(other_p) + l : l + ld_shared(other_p);  // (the same sum in both)
         named_barrier_sync(pair_bar, 64);
         const bool any = !(l == 0.f);  // (NaN counts)
         const float inv = any ? 1.f / l : 0.f;
-        // values that were taken out, and that this row sees
         const bool look = it.any_bad != 0;
-        const int bad0 = look ? (it.t_begin + it.fix0) * TK : INT32_MAX, bad1 = min(last, it.t_end * TK - 1);
         for (int b = half; b < dv / 32; b += 2) {
           float o[32];
           tmem_ld32(to + 32 * b, o);
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = any ? o[e] * inv : 0.f;
-          finish(a, it, o, 32 * b, 32, bad0, bad1, live, row, part, dn, dv, S);
+          finish(a, misc->first_bad, o, 32 * b, 32, last, look, live, row, part, dv, S);
         }
         if (dv % 32 && half == 1) {
           float o[32];
@@ -727,7 +781,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           tmem_wait_ld();
 #pragma unroll
           for (int e = 0; e < 16; ++e) o[e] = any ? o[e] * inv : 0.f;
-          finish(a, it, o, dv - 16, 16, bad0, bad1, live, row, part, dn, dv, S);
+          finish(a, misc->first_bad, o, dv - 16, 16, last, look, live, row, part, dv, S);
         }
         if (live && half == 0) {
           const float z = !any ? -INFINITY : fabsf(m) * c < HUGE_X ? r * LN2 + __logf(l) : m * a.softmax_scale + __logf(l);

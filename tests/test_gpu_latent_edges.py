@@ -73,3 +73,43 @@ def test_combine_many_heads(heads, d_v, splits):
     res = (w[..., None] * o.double()).sum(0)
     ops.near(out, res, 2.0**-8 * res.abs() + (off + (splits + 1) * 2.0**-24) * (w[..., None] * o.double().abs()).sum(0))
     ops.near(lse, want, 2.0**-22 * want.abs() + off)
+
+
+# ---- values that are not finite ----------------------------------------------------------
+
+
+@pytest.mark.parametrize("c", [LARGE, shape(5, 48, 16, 80), shape(3, 16, 0, 16), shape(2, 128, 64, 64)],
+                         ids=lambda c: f"{c['heads']}x{c['dv']}")
+@pytest.mark.parametrize("splits", [1, 3])
+def test_prompt_bad_values_among_any_last_positions(c, splits):
+    """A token that sees nothing makes every tile of its query tile one that is seen in part; bad values stand
+    in some tiles, columns and heads, next to each other and far apart, and others read past them."""
+    g = gen(c["heads"] + splits)
+    q, kv, k_rope, cu_q, cu_k, pos = ops.batch(c, [(300, 1500), (130, 700), (5, 260)], g)
+    r = torch.Generator().manual_seed(5)
+    pos = [int(torch.randint(-1, n, (1,), generator=r)) for m, n in ((300, 1500), (130, 700), (5, 260)) for _ in range(m)]
+    for t in (0, 140, 299, 300, 429, 434):
+        pos[t] = -1
+    pos[1], pos[141], pos[431] = 1499, 1499, 259
+    H, dn, dv = c["heads"], c["dn"], c["dv"]
+    for at, h, d, what in ((0, 0, 0, math.nan), (127, 1, dv - 1, math.inf), (128, 1, 3, -math.inf), (640, 0, 5, math.nan),
+                           (641, 0, 5, math.nan), (300, 0, 5, math.inf), (1499, H - 1, dv // 2, math.nan),
+                           (1500 + 699, 0, 8, math.inf), (1500 + 3, 1, 9, -math.nan), (2200 + 130, H - 1, 15, math.nan)):
+        kv[at, h, dn + d] = what
+    kv[900, H - 1, dn:] = math.nan
+    ops.check_prompt(c, q, kv, k_rope, cu_q, cu_k, pos, 0.1, ops.run_prompt(c, q, kv, k_rope, cu_q, cu_k, pos, scale=0.1,
+                                                                            num_splits=splits))
+
+
+@pytest.mark.parametrize("every", [False, True], ids=["two bad values", "bad values in every tile"])
+def test_prompt_bad_values_in_a_context_of_millions_of_rows(every):
+    """The work beside a tile's products is bounded for every tile, so that no wait of the call's runs out."""
+    c, n, g = shape(1, 16, 0, 16), 1 << 24, gen(9)
+    kv, q = rows((n, 1, 32), g), rows((4, 1, 16), g)
+    kv[1000, 0, 16 + 3], kv[n - 3, 0, 16 + 7] = math.nan, math.inf
+    if every:
+        kv[1000:, 0, 16 + 3] = math.inf
+        kv[5000::50, 0, 16 + 5] = math.nan
+    pos = [-1, 999, n // 2, n - 1]
+    ops.check_prompt(c, q, kv, None, [0, 4], [0, n], pos, 0.25,
+                     ops.run_prompt(c, q, kv, None, [0, 4], [0, n], pos, scale=0.25, num_splits=1), rms=False)
