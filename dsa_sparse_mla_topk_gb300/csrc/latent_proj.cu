@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
     asm volatile("griddepcontrol.wait;" ::: "memory");
     m_all = min(max(*reinterpret_cast<const volatile int32_t*>(p.rows), 0), p.m);
   }
-  const int mt = (m_all + TROWS - 1) / TROWS;
+  const int mt = m_all / TROWS + (m_all % TROWS != 0);  // (up to 2^31 - 1 rows)
   const int64_t tiles = (int64_t)p.units * mt;
   const int t0 = (int)(tiles * worker / workers), t1 = (int)(tiles * (worker + 1) / workers);
   bool ok = true;
@@ -372,7 +372,7 @@ cudaError_t launch_product(const Product& p, const ProductMaps& maps, cudaStream
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   constexpr int CTAS = MODE == EXPAND ? 2 : 1;
-  const int64_t tiles = (int64_t)p.units * ((p.m + CTAS * TM - 1) / (CTAS * TM)), workers = device_sm_count() / CTAS;
+  const int64_t tiles = (int64_t)p.units * (((int64_t)p.m + CTAS * TM - 1) / (CTAS * TM)), workers = device_sm_count() / CTAS;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = CTAS;
@@ -499,7 +499,7 @@ __global__ void __launch_bounds__(EX_THREADS) expand_rows_kernel(const ExpandArg
 
 cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream) {
   const int d_w = a.d_nope + a.d_v, d_out = a.d_latent + a.d_rope;
-  const int64_t mt = (a.num_tokens + TM - 1) / TM;
+  const int64_t mt = ((int64_t)a.num_tokens + TM - 1) / TM;
   Product p = {};
   p.m = a.num_tokens, p.n = a.d_latent, p.k = a.d_nope;
   p.n_unit = columns_of_unit(p.n, 512, a.heads * mt);
@@ -521,7 +521,7 @@ cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream) {
   const int d_w = a.d_nope + a.d_v;
-  const int64_t mt = (a.num_tokens + TM - 1) / TM;
+  const int64_t mt = ((int64_t)a.num_tokens + TM - 1) / TM;
   Product p = {};
   p.m = a.num_tokens, p.n = a.d_v, p.k = a.d_latent;
   p.n_unit = columns_of_unit(p.n, 128, a.heads * mt);

@@ -113,3 +113,33 @@ def test_prompt_bad_values_in_a_context_of_millions_of_rows(every):
     pos = [-1, 999, n // 2, n - 1]
     ops.check_prompt(c, q, kv, None, [0, 4], [0, n], pos, 0.25,
                      ops.run_prompt(c, q, kv, None, [0, 4], [0, n], pos, scale=0.25, num_splits=1), rms=False)
+
+
+# ---- the largest sizes ---------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("op", ["absorb", "project"])
+@pytest.mark.parametrize("n", [2**31 - 1, 2**31 - 128, 2**31 - 255])
+def test_products_of_the_most_tokens(op, n):
+    """One head of 16 values and as many tokens as there may be: overlapping rows (a token stride of 8) of 32 GiB,
+    outputs of 64 GiB.  All written; the first, the last and some between against 64 bits."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 110 << 30:
+        pytest.skip("needs 110 GiB of free memory")
+    g = gen(3)
+    x = torch.empty(8 * n + 8, dtype=BF16, device="cuda").normal_(generator=g).as_strided((n, 1, 16), (8, 16, 1))
+    w = weight(shape(1, 16, 0, 16, 16), g)
+    y = torch.full((n, 1, 16), math.nan, dtype=BF16, device="cuda")
+    st = i32([0])
+    if op == "absorb":
+        dsa.absorb_q(x, w, d_rope=0, q_out=y, dev_status=st)
+    else:
+        dsa.project_out(x, w, d_nope=16, out=y, dev_status=st)
+    assert int(st) == 0
+    b = w[0, :16].double() if op == "absorb" else w[0, 16:].double().t()
+    for at in (0, 2**30 - 500, 2**31 - 2**20 - 77, n - 1000):
+        ops.near_product(y[at:at + 1000, 0], x[at:at + 1000, 0].double(), b, 16)
+    for at in range(0, n, 2**27):
+        assert not bool(torch.isnan(y[at:at + 2**27]).any()), at
+    del x, y
+    torch.cuda.empty_cache()
