@@ -128,17 +128,20 @@ __device__ __forceinline__ int tiles_of(const PromptArgs& a, int r, int& q0, int
   return (n + QT - 1) / QT;
 }
 
-// misc->upto, by the CTA's first NCHUNK threads (a barrier follows).
-__device__ __forceinline__ void sum_tiles(const PromptArgs& a, bool tell, Misc* misc) {
+// misc->upto, by the CTA's first NCHUNK threads (a barrier follows).  Every CTA that runs tells of ranges that are
+// none: which ones start, and which are taken over before they do, nothing guarantees.
+__device__ __forceinline__ void sum_tiles(const PromptArgs& a, Misc* misc) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int inc = 0;
   if (tid < NCHUNK) {
     const int per = (a.num_req + NCHUNK - 1) / NCHUNK, r0 = min(tid * per, a.num_req), r1 = min(r0 + per, a.num_req);
+    bool none = false;
     for (int r = r0; r < r1; ++r) {
       int q0, n;
       inc += tiles_of(a, r, q0, n);
-      if (n < 0 && tell) report(a.dev_status, DSA_DEV_BAD_INDEX);
+      none |= n < 0;
     }
+    if (none) report(a.dev_status, DSA_DEV_BAD_INDEX);
     inc = min(inc, (int)gridDim.x);  // (ranges that overlap, an error, could add up past 32 bits)
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
     tma_prefetch_map(&maps.kv);
     tma_prefetch_map(&maps.rope);
   }
-  sum_tiles(a, blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0, misc);
+  sum_tiles(a, misc);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();

@@ -115,6 +115,40 @@ def test_prompt_bad_values_in_a_context_of_millions_of_rows(every):
                      ops.run_prompt(c, q, kv, None, [0, 4], [0, n], pos, scale=0.25, num_splits=1), rms=False)
 
 
+# ---- data errors ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("bad", [0, 1, 37, 199])
+@pytest.mark.parametrize("busy", [False, True], ids=["alone", "beside others"])
+def test_prompt_ranges_that_are_none_are_told(bad, busy):
+    """A request whose token range goes down or past the tokens, wherever it stands and whichever CTAs run first:
+    told, its tokens left alone, the others' results as without it."""
+    c, R, g = SMALL, 200, gen(7)
+    q, kv, k_rope, cu_q, cu_k, pos = ops.batch(c, [(300, 330)] * R, g)
+    want = ops.run_prompt(c, q, kv, k_rope, cu_q, cu_k, pos)
+    cut = list(cu_q)
+    cut[bad + 1] = len(pos) + 1 if bad == R - 1 else 300 * (bad + 2) + 5  # too high here, and so down at the next
+    other = torch.cuda.Stream()
+    for _ in range(5):
+        out, lse = torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0)
+        torch.cuda.synchronize()
+        if busy:
+            with torch.cuda.stream(other):
+                for _ in range(3):
+                    dsa.prompt_mla(q, kv, k_rope, i32(cu_q), i32(cu_k), i32(pos), d_nope=32, softmax_scale=0.1)
+        st = i32([0])
+        dsa.prompt_mla(q, kv, k_rope, i32(cut), i32(cu_k), i32(pos), d_nope=32, softmax_scale=48**-0.5, dev_status=st,
+                       buffers=dict(out=out, lse=lse))
+        torch.cuda.synchronize()
+        # (the request before the one that goes down takes tokens that are the next one's: past their contexts)
+        assert int(st) & dsa.DEV_BAD_INDEX
+        good = torch.ones(len(pos), dtype=torch.bool, device="cuda")
+        good[300 * bad:300 * (bad + 2) + 5] = False
+        assert torch.equal(out[good], want[0][good]) and torch.equal(lse[good], want[1][good])
+        if bad == R - 1:
+            assert bool((out[300 * bad:] == 7).all()) and bool((lse[300 * bad:] == 7).all())
+
+
 # ---- the largest sizes ---------------------------------------------------------------------
 
 
