@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
     const uint32_t lanes = (uint32_t)(32 * quad) << 16, ts = TM_S + 128 * g + lanes, to = TM_O + 128 * g + lanes;
     const uint32_t mine_p = smem_u32(&misc->pair[g][half][32 * quad + lane]), other_p = mine_p + (half ? -4 * TQ : 4 * TQ);
     const int pair_bar = 1 + 4 * g + quad;  // the two warps of these 32 rows
-    const float c = fmaxf(a.softmax_scale * LOG2E, 0x1p-120f);  // (0 would make NaN of masked logits)
+    const float c = fmaxf(a.softmax_scale * LOG2E, 0x1p-149f);  // (0 would make NaN of masked logits; of none it makes 2^-21)
     int sn = 0;  // tiles so far
     // The two warps of a pair share a barrier, which has no limit: they leave their loops only by what it
     // tells both, whether a wait of either gave up.

@@ -115,6 +115,22 @@ def test_prompt_bad_values_in_a_context_of_millions_of_rows(every):
                      ops.run_prompt(c, q, kv, None, [0, 4], [0, n], pos, scale=0.25, num_splits=1), rms=False)
 
 
+# ---- scales --------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("c", [LARGE, SMALL], ids=["64", "16"])
+@pytest.mark.parametrize("scale", [0.0, 2.0**-140, 2.0**-126, 2.0**-124, 3e-37, 2.0**-118])
+@pytest.mark.parametrize("splits", [1, 3])
+def test_prompt_small_scales_of_large_logits(c, scale, splits):
+    """Sums up to 2^126 under scales down to 0: the logits are what their product is."""
+    q, kv, k_rope, cu_q, cu_k, pos = ops.batch(c, [(140, 400), (30, 30)], gen(21))
+    one = torch.zeros_like(q)
+    one[..., 0] = q[..., 0].clamp(-1, 1) * 2.0**63
+    kv[..., 0] = kv[..., 0].clamp(-1, 1) * 2.0**63
+    ops.check_prompt(c, one, kv, k_rope, cu_q, cu_k, pos, scale, ops.run_prompt(c, one, kv, k_rope, cu_q, cu_k, pos, scale=scale,
+                                                                                num_splits=splits))
+
+
 # ---- data errors ---------------------------------------------------------------------------
 
 
