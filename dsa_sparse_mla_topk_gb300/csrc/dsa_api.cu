@@ -721,7 +721,7 @@ dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64_t q_hea
                               int32_t d_v, float softmax_scale, int32_t num_splits, void* out, float* lse,
                               float* o_part, float* lse_part, int32_t* dev_status, void* stream) {
   if (num_tokens < 0 || num_rows < 0 || num_req < 0 || num_splits < 1 || num_splits > 64) return DSA_ERR_INVALID_ARG;
-  if (!isfinite(softmax_scale) || softmax_scale < 0.f) return DSA_ERR_INVALID_ARG;
+  if (!(softmax_scale >= 0.f && softmax_scale <= 0x1p127f)) return DSA_ERR_INVALID_ARG;  // (log2 e times it is finite)
   const dsa_status st = check_latent_dims(num_heads, d_nope, d_rope, d_v, 16);
   if (st != DSA_OK) return st;
   if (num_req > dsa::batch_layout_max_requests() || num_tokens > (1 << 30) || num_rows > (1 << 26))

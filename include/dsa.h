@@ -628,7 +628,7 @@ DSA_API size_t dsa_expand_kv_workspace_size(int32_t capacity, int32_t d_latent);
  *             [S, num_tokens, num_heads]) for dsa_combine.
  * The head sizes are those of dsa_absorb_q; num_tokens at most 2^30, num_rows 2^26.
  * What is written must not overlap an input or each other (INVALID_ARG);
- * softmax_scale is finite and not negative.
+ * softmax_scale is not negative and at most 2^127.
  * A token with q_pos = -1, and padding (t >= cu_q[num_req]), sees nothing: out = 0 and
  * lse = -inf.  What no token of a request sees is not looked at; a row that a token does not
  * see does not reach its result, whatever it holds.  NaN in a query or a visible key gives

@@ -5,7 +5,7 @@ import ctypes
 import pytest
 
 import dsa_sparse_mla_topk_gb300 as dsa
-from test_latent_args import A, lib, no_device_only  # noqa: F401
+from test_latent_args import A, _prompt, lib, no_device_only  # noqa: F401
 
 
 @no_device_only
@@ -30,3 +30,14 @@ def test_combine_keeps_its_limit_for_wider_values(lib):  # noqa: F811
     assert lib.dsa_combine(A(0), A(1), 2, 0, 64, 512, A(2), A(3), None) == 0
     assert lib.dsa_combine(A(0), A(1), 2, 0, 65, 132, A(2), A(3), None) == 1
     assert lib.dsa_combine(A(0), A(1), 2, 0, 0, 128, A(2), A(3), None) == 1
+
+
+@no_device_only
+@pytest.mark.parametrize("scale,expect", [(2.0**127, 0), (2.0**127 * (1 + 2.0**-23), 1), (3e38, 1), (float("inf"), 1), (0.0, 0),
+                                          (-0.0, 0), (-1e-45, 1)])
+def test_prompt_scales_whose_logits_to_base_2_are_finite(lib, scale, expect):  # noqa: F811
+    """Past 2^127 log2 e times the scale is infinite, and a sum of 0 times that no number."""
+    if expect == 0:  # (nothing is launched without tokens, but the scale is looked at first)
+        assert _prompt(lib, scale=scale, n=0) == 0
+    else:
+        assert _prompt(lib, scale=scale, n=0) == _prompt(lib, scale=scale) == expect
