@@ -670,7 +670,9 @@ DSA_API dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64
  *             other (INVALID_ARG).
  * num_rows at most 2^24, vocab at most 2^30 (else UNSUPPORTED_SHAPE).  Sums are fp32
  * without the largest term, so that a sure token's small logarithm keeps its bits.
- * Results do not depend on the launch's other rows.  A row with NaN or +inf has NaN in
+ * rank and top_ids depend on the row alone, and no result on what other rows hold.  The last
+ * bits of logprob, entropy and top_logprobs also depend on num_rows, which decides
+ * in how many parts a row is summed.  A row with NaN or +inf has NaN in
  * logprob, entropy and top_logprobs, and some rank and columns in range.  A token outside
  * [-1, vocab) sets DSA_DEV_BAD_INDEX and counts as -1.
  */
