@@ -37,3 +37,31 @@ def test_logprobs_depend_on_the_row_and_on_how_many_there_are(dtype, V):
         other[n - 1] = math.nan
         again = run(other, tok[:n], 7)
         assert all(torch.equal(a[0], b[0]) for a, b in zip(got, again)), n
+
+
+@DTYPES
+@pytest.mark.parametrize("R,V,parts", [(2, 70_000_003, 8192), (160, 2_000_003, 1024), (310, 1_000_003, 512)],
+                         ids=["clusters", "512 threads", "256 threads"])
+def test_logprobs_sums_of_very_long_rows(dtype, R, V, parts):
+    """logprob and entropy within the bounds of test_gpu_logprobs' head, with the sums' additions as the call makes them:
+    a row's values go to `parts` sums in turn (two a thread: eight CTAs of 512 threads a row for few
+    rows, one of 512 up to 304 rows, one of 256 past that), so that one has V / parts terms."""
+    z, tok = logits((R, V), dtype, R), some(R, V)
+    got = run(z, tok, 0)
+    adds = (V / parts + 64) * U
+    for r in range(0, R, 16 if R > 2 else 1):
+        x = z[r].double()
+        at = int(x.argmax())
+        d = x - x[at]
+        e = d.exp()
+        entropy_terms = (e * d.abs()).sum()
+        entropy_off = (e * d.abs() * (4 * U * d.abs() + 2.0**-22 + adds + U)).sum()
+        e[at] = 0
+        rest = e.sum()
+        S = 1 + rest
+        E = (e * (3 * U * d.abs() + 2.0**-22 + adds)).sum() / S + 2.0**-22 * rest.log1p()
+        dt = d[int(tok[r])]
+        lp = dt - rest.log1p()
+        assert abs(float(got.logprob[r]) - float(lp)) <= float(E + 2 * U * dt.abs() + U * lp.abs())
+        ent = rest.log1p() + entropy_terms / S
+        assert abs(float(got.entropy[r]) - float(ent)) <= float(E + entropy_off / S + ent * (E + 2.0**-22))
