@@ -67,7 +67,7 @@ constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;  // with alignment slack
 static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 
 struct ProductMaps {
-  CUtensorMap a, b, c, c_rope;
+  CUtensorMap a, b, c, c_rope;  // (results by TMA: absorb's)
 };
 struct Product {
   int m, n, k;             // rows; columns of a head (expand: of all); the sum's length
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(THREADS, 1) product_kernel(const Product p, co
     fence_mbarrier_init();
     tma_prefetch_map(&maps.a);
     tma_prefetch_map(&maps.b);
-    tma_prefetch_map(&maps.c);
+    if (MODE == ABSORB) tma_prefetch_map(&maps.c);
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -508,7 +508,7 @@ cudaError_t launch_absorb_q(const LatentProjArgs& a, cudaStream_t stream) {
   p.b_row0 = 0, p.b_group = d_w;
   p.rope_x = a.d_rope > 0 ? a.d_nope : -1;
   p.dev_status = a.dev_status;
-  ProductMaps maps;
+  ProductMaps maps = {};
   __nv_bfloat16* y = static_cast<__nv_bfloat16*>(a.y);
   if (!make_rows_map(&maps.a, a.x, a.num_tokens, a.heads, a.d_nope + a.d_rope, a.tok_stride, a.head_stride, TM) ||
       !make_rows_map(&maps.b, a.w, (int64_t)a.heads * d_w, 1, a.d_latent, a.d_latent, 0, (uint32_t)a.d_nope) ||
@@ -532,12 +532,10 @@ cudaError_t launch_project_out(const LatentProjArgs& a, cudaStream_t stream) {
   p.out = static_cast<__nv_bfloat16*>(a.y), p.ldc = (int64_t)a.heads * a.d_v;
   p.wide = reinterpret_cast<uintptr_t>(a.y) % 32 == 0;
   p.rope_x = -1;
-  ProductMaps maps;
+  ProductMaps maps = {};
   if (!make_rows_map(&maps.a, a.x, a.num_tokens, a.heads, a.d_latent, a.tok_stride, a.head_stride, TM) ||
-      !make_rows_map(&maps.b, a.w, (int64_t)a.heads * d_w, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit) ||
-      !make_rows_map(&maps.c, a.y, a.num_tokens, a.heads, a.d_v, (int64_t)a.heads * a.d_v, a.d_v, 32))
+      !make_rows_map(&maps.b, a.w, (int64_t)a.heads * d_w, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit))
     return cudaErrorInvalidValue;
-  maps.c_rope = maps.c;
   return launch_product<PROJECT>(p, maps, stream);
 }
 
@@ -563,12 +561,10 @@ cudaError_t launch_expand_kv(const ExpandArgs& a, cudaStream_t stream) {
   p.out = static_cast<__nv_bfloat16*>(a.kv_out), p.ldc = p.n;
   p.wide = reinterpret_cast<uintptr_t>(a.kv_out) % 32 == 0;
   p.dev_status = a.dev_status;
-  ProductMaps maps;
+  ProductMaps maps = {};
   if (!make_rows_map(&maps.a, x, a.capacity, 1, a.d_latent, a.d_latent, 0, TM) ||
-      !make_rows_map(&maps.b, a.w, p.n, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit / 2) ||
-      !make_rows_map(&maps.c, a.kv_out, a.capacity, 1, p.n, p.n, 0, 32))
+      !make_rows_map(&maps.b, a.w, p.n, 1, a.d_latent, a.d_latent, 0, (uint32_t)p.n_unit / 2))
     return cudaErrorInvalidValue;
-  maps.c_rope = maps.c;
   return launch_product<EXPAND>(p, maps, stream);
 }
 

@@ -93,7 +93,7 @@ constexpr int IE_COUNT = SM_WARPS + 3;  // softmax, TMA, MMA and value warps
 constexpr int NCHUNK = 128;             // requests' tiles are summed in so many parts
 struct Item {
   int32_t req, q0, rows, h, split;  // req -1: padding rows, -2: no more
-  int32_t k0, kv_len, t_begin, t_end;
+  int32_t k0, kv_len, t_begin;
   int32_t cnt[2], whole[2];  // tiles of the share that query tile g sees, that all its rows see whole
   int32_t fix0;              // from this tile on some row may see a tile in part
   int32_t any_bad;           // a value that is not finite was taken out, and first_bad holds this item's
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
           if (lane == 0) {
             Item& it = misc->item[n & 1];
             it.req = req, it.q0 = q0, it.rows = rows, it.h = y, it.split = z;
-            it.k0 = k0, it.kv_len = kv_len, it.t_begin = t_begin, it.t_end = t_end, it.any_bad = 0;
+            it.k0 = k0, it.kv_len = kv_len, it.t_begin = t_begin, it.any_bad = 0;
             int fix0 = INT32_MAX;
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
