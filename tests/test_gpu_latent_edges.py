@@ -44,13 +44,15 @@ def test_prompt_many_heads_shares_by_the_rule(both_ways):  # noqa: F811
     ops.check_prompt(c, *x, 0.25, ops.run_prompt(c, *x))
 
 
-@pytest.mark.parametrize("heads", [65, 128, 300])
-def test_products_and_expansion_many_heads(heads):
-    c, g, n = shape(heads, 48, 16, 80, 208), gen(heads), 150
+@pytest.mark.parametrize("c", [shape(65, 48, 16, 80, 208), shape(128, 48, 16, 80, 208), shape(300, 48, 16, 80, 208),
+                               shape(1, 16, 0, 16, 16), shape(1, 16, 64, 16, 512), shape(1, 128, 16, 112, 48)],
+                         ids=lambda c: f"{c['heads']}x{c['dn']}x{c['dl']}")
+def test_products_and_expansion_one_and_many_heads(c):
+    g, n = gen(c["heads"]), 150
     w = weight(c, g)
-    q, o = rows((n, heads, 64), g), rows((n, heads, 208), g)
-    ops.check_absorb(c, q, w, dsa.absorb_q(q, w, d_rope=16))
-    ops.check_project(c, o, w, dsa.project_out(o, w, d_nope=48))
+    q, o = rows((n, c["heads"], c["dn"] + c["dr"]), g), rows((n, c["heads"], c["dl"]), g)
+    ops.check_absorb(c, q, w, dsa.absorb_q(q, w, d_rope=c["dr"]))
+    ops.check_project(c, o, w, dsa.project_out(o, w, d_nope=c["dn"]))
     kv, scale, table = ops.cache(c, 3, 200, 48, g)
     lens = [200, 0, 131]
     ops.check_expand(c, kv, scale, table, lens, w, 48, ops.run_expand(c, kv, scale, table, lens, w, 48, 340))
@@ -193,3 +195,60 @@ def test_products_of_the_most_tokens(op, n):
         assert not bool(torch.isnan(y[at:at + 2**27]).any()), at
     del x, y
     torch.cuda.empty_cache()
+
+
+def test_products_results_past_32_bit_offsets():
+    """Results of more than 2^31 values: the first rows, those around 2^31 values, the last."""
+    c, g = LARGE, gen(40)
+    w = weight(c, g)
+    n = 2**31 // (64 * 576) + 300
+    q = rows((n, 64, 192), g)
+    y = dsa.absorb_q(q, w, d_rope=64)
+    assert y.numel() > 2**31
+    for at in (0, n - 400, n - 150):
+        ops.check_absorb(c, q[at:at + 150], w, y[at:at + 150])
+    del q, y
+    n = 2**31 // (64 * 128) + 300
+    o = rows((n, 64, 512), g)
+    y = dsa.project_out(o, w, d_nope=128)
+    assert y.numel() > 2**31
+    for at in (0, n - 400, n - 150):
+        ops.check_project(c, o[at:at + 150], w, y[at:at + 150])
+    del o, y
+    torch.cuda.empty_cache()
+
+
+def test_expand_results_past_32_bit_offsets():
+    c, g, P = LARGE, gen(41), 64
+    n = 2**31 // (64 * 256) + 300
+    kv, scale, table = ops.cache(c, 2, n, P, g)
+    w = weight(c, g)
+    x = ops.run_expand(c, kv, scale, table, [n, 77], w, P, n + 100)
+    assert x.cu_k.tolist() == [0, n, n + 77] and x.kv[:n].numel() > 2**31
+    for r, at, m in ((0, 0, 150), (0, n - 400, 400), (1, 0, 77)):
+        p = torch.arange(at, at + m, device="cuda")
+        slot = table[r].long()[p // P] * P + p % P
+        a = kv[slot].view(torch.float8_e4m3fn).double() * scale[slot].double()[:, None]
+        out = slice(n * r + at, n * r + at + m)
+        ops.near_product(x.kv[out].flatten(1), a[:, :512], w.double().flatten(0, 1).t(), 512)
+        assert torch.equal(x.k_rope[out], a[:, 512:].float().to(BF16))
+    del x
+    torch.cuda.empty_cache()
+
+
+# ---- workspaces ------------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("c", ops.SHAPES, ids=lambda c: f"{c['heads']}x{c['dn']}")
+def test_expand_whatever_the_workspace_holds(c, both_ways):  # noqa: F811
+    """What a tile's rows past the last one read of the workspace (NaN here, and infinite scales) reaches nothing."""
+    g, lens = gen(42), [100, 0, 133]
+    kv, scale, table = ops.cache(c, 3, 140, 48, g)
+    w = weight(c, g)
+    want = ops.run_expand(c, kv, scale, table, lens, w, 48, 700)
+    for fill in (0xff, 0x7f):  # NaN in both types; 0x7f7f, the largest finite values
+        ws = torch.full((dsa.expand_kv_workspace_size(700, c["dl"]),), fill, dtype=torch.uint8, device="cuda")
+        out = dsa.ExpandedKV(torch.full_like(want.kv, 7.0), torch.full_like(want.k_rope, 7.0), i32([0] * 4))
+        x = dsa.expand_kv(kv, scale, table, i32(lens), w, d_rope=c["dr"], page_size=48, out=out, workspace=ws)
+        assert all(torch.equal(a, b) for a, b in zip(x, want))
+    ops.check_expand(c, kv, scale, table, lens, w, 48, want)
