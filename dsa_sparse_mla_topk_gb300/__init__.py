@@ -1177,7 +1177,8 @@ def prompt_mla(q: torch.Tensor, kv: torch.Tensor, k_rope: torch.Tensor | None, c
     ``q_pos`` are batch_layout's; padding and q_pos = -1 give 0.  ``max_ctx``
     (default: the rows a request on average) is about the longest context, from which
     the number of shares of the rows is picked when ``num_splits`` is None; the
-    result is right for any value.  ``buffers`` (optional) holds preallocated out / lse /
+    result is right for any value.  Give it where ``kv`` has room for more rows than
+    the requests have: rows that no request has count in the default.  ``buffers`` (optional) holds preallocated out / lse /
     o_part / lse_part tensors.  Returns (out bf16 [tokens, heads, d_v], lse fp32 [tokens,
     heads]), which share one allocation unless given (clone lse to keep it alone)."""
     b = buffers or {}

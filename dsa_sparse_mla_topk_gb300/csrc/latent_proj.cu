@@ -16,14 +16,14 @@
 // absorb's, whose heads' rows are 1,152 bytes apart from the rotated part, through shared memory
 // and TMA stores of 32 rows x 64 columns; the others' straight from registers, 32 bytes a
 // store, which leaves room for two more chunks of A (project, 8,192 tokens: 112 -> 108 us).
-// absorb and project read and write more than they compute (85 and 102 flop a byte).  Measured, 64
-// heads of 128 + 64, latent 512: absorb 4,099 tokens 76.6 us (5.4 TB/s, most of it stores), 8 tokens 4.7;
-// project 8,192 tokens 106 us (6.4 TB/s, 95% of a copy), 128 tokens 6.3.
+// absorb and project read and write more than they compute (85 and 102 flop a byte).  Measured, device time
+// back to back, 64 heads of 128 + 64, latent 512: absorb 4,099 tokens 76 us (5.4 TB/s, most of it stores), 8
+// tokens 4.7; project 8,192 tokens 107.6 us (6.3 TB/s, 93% of a copy), 128 tokens 6.3.
 // expand is bound by the tensor cores (512): pairs of CTAs (cta_group::2) take 256 x 256
 // outputs a tile, each holding half of the columns' weights, so that A is half
 // as many bytes a product (with single CTAs of 128 columns 16,384 rows take 283 us, in pairs 211 at
-// that step and 169 now: 1,629 TFLOP/s, with L2 between A's reads and the results).  Five
-// requests of 167 to 333 rows: 28 us, two launches and 4 to 5 tiles a pair.
+// that step and 168 now: 1,637 TFLOP/s, with L2 between A's reads and the results).  Five
+// requests of 167 to 333 rows: 27 us, two launches and 4 to 5 tiles a pair.
 // Warps: 0-7 results, 8 TMA, 9 MMA, 10 the rotated part of the queries, which is copied.
 // All waits are bounded.
 #include <cuda.h>

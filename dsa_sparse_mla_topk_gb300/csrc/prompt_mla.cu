@@ -31,10 +31,10 @@
 // All waits are bounded.
 //
 // Bound by the tensor cores, and by what keeps them waiting: 640 flop a pair and head; a tile of
-// both query tiles is 2,560 cycles of MMAs and takes about 3,050.  Measured, 64 heads of 128 + 64 and 128: one
-// prompt of 8,192 tokens 836 us (1,643 TFLOP/s), 1,024 tokens of 16,384 positions 412 us (256 items
-// on 152 SMs), 8 prompts of 1,024 to 2,048 tokens on up to 1,000 positions 566 us (an item
-// costs 4 us beside its tiles); 16 heads of 32 + 16, two prompts of 200: 10 us.
+// both query tiles is 2,560 cycles of MMAs and takes about 3,050.  Measured, device time back to back, 64 heads of
+// 128 + 64 and 128: one prompt of 8,192 tokens 830 us (1,656 TFLOP/s), 1,024 tokens of 16,384 positions
+// 408 us (256 items on 152 SMs), 8 prompts of 1,024 to 2,048 tokens on up to 1,000 positions 560 us (an
+// item costs 4 us beside its tiles); 16 heads of 32 + 16, two prompts of 200: 9.7 us.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -736,6 +736,9 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
             const float x0 = ex2(s[16 * b + 2 * j]), x1 = ex2(s[16 * b + 2 * j + 1]);
             if (j & 1) sum = add2(sum, pk2(x0, x1));
             else l2 = add2(l2, pk2(x0, x1));
+            // A weight enters the products as bf16, the type of the values (both factors of an MMA have the same),
+            // 2^-8 of it off at most: out's error against 64 bits is 1.9 to 2.3e-3 with it, out's own rounding alone
+            // 1.6 to 1.7e-3.  A second bf16 for the rest would be two fifths more products.  The sum takes it unrounded.
             const __nv_bfloat162 y = __floats2bfloat162_rn(x0, x1);
             p[j] = *reinterpret_cast<const uint32_t*>(&y);
           }

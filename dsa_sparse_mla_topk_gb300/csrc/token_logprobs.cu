@@ -23,8 +23,8 @@
 // checked in turns that lie in the row as a whole (with checks at each load 11.2).
 // What follows a row is a chain of ten thousand cycles that mostly waits; a row a CTA of 256 threads,
 // four an SM, lets other rows' loads run under it.
-// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 59 us (4.6 TB/s), 4,096 rows of 131,072 203 us (5.3 TB/s),
-// 4,096 of 32,000 83 us, 128 of 131,072 fp32 19 us, 4 of 32,003 fp32 8.8 us (launch and the chain of steps).
+// Measured: 1,024 rows of 131,072 bf16, 20 alternatives, 59 us (4.6 TB/s), fp32 103 us (5.2 TB/s), 4,096 rows bf16 203 us (5.3 TB/s),
+// 4,096 of 32,000 83 us, 128 of 131,072 fp32 19 us, 4 of 32,003 fp32 9.1 us (launch and the chain of steps).
 // Rows that do not start at 16 bytes pay for their ends, two waits and a turn more: 1,024 x 131,071 75 us.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -615,9 +615,9 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, cudaStream_t stream) {
-  // Many rows: CTAs of half the threads, whose chains behind a row overlap.  4,096 x 8,000 bf16 93 -> 56 us, 4,096
-  // x 32,000 117 -> 90, 1,024 x 131,072 67 -> 64, fp32 105 -> 108 (a quarter of the threads: 48, 85, 74, 108);
-  // measured before the loads' checks went.
+  // Many rows: CTAs of half the threads, whose chains behind a row overlap.  512, 256, 128 threads, us: 400 x 8,000
+  // bf16 13.0, 8.7, 9.8; 4,096 x 8,000 93, 54, 55; 4,096 x 32,000 114, 83, 94; 1,024 x 131,072 63, 59, 77; fp32
+  // 4,096 x 8,000 84, 56, 54; 4,096 x 32,000 128, 110, 123; 1,024 x 131,072 107, 103, 112; fp16 as bf16.
   const bool many = a.num_rows > 2 * device_sm_count();
   if (a.dtype == DSA_BF16) return many ? launch<__nv_bfloat16, 256>(a, stream) : launch<__nv_bfloat16, 512>(a, stream);
   if (a.dtype == DSA_FP16) return many ? launch<__half, 256>(a, stream) : launch<__half, 512>(a, stream);

@@ -669,7 +669,8 @@ DSA_API dsa_status dsa_prompt_mla_fwd(const void* q, int64_t q_tok_stride, int64
  *             top_logprobs fp32 [num_rows, top].  They must not overlap an input or each
  *             other (INVALID_ARG).
  * num_rows at most 2^24, vocab at most 2^30 (else UNSUPPORTED_SHAPE).  Sums are fp32
- * without the largest term, so that a sure token's small logarithm keeps its bits.
+ * without the largest term, so that a sure token's small logarithm keeps its bits (down to
+ * 2^-126; a term of the sum below that counts as 0).
  * rank and top_ids depend on the row alone, and no result on what other rows hold.  The last
  * bits of logprob, entropy and top_logprobs also depend on num_rows, which decides
  * in how many parts a row is summed.  A row with NaN or +inf has NaN in
