@@ -623,7 +623,10 @@ __global__ void __launch_bounds__(THREADS, 1) prompt_mla_kernel(const PromptArgs
                 }
               }
             *kept = make_int4(first[0], first[1], first[2], first[3]);
-            item->any_bad = 1;
+            // (a query tile that is done before this one is looked through may read both now)
+            __threadfence_block();
+            __syncwarp();
+            if (lane == 0) item->any_bad = 1;
           }
           fence_proxy_async_smem();
           __syncwarp();

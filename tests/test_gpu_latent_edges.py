@@ -103,6 +103,29 @@ def test_prompt_bad_values_among_any_last_positions(c, splits):
                                                                             num_splits=splits))
 
 
+@pytest.mark.parametrize("dv", [32, 128])
+@pytest.mark.parametrize("at", [256, 384, 511, 640])
+def test_prompt_bad_values_behind_what_half_the_tokens_see(dv, at):
+    """The first 128 tokens end before a bad value that the next 128 see, in heads that take turns with heads whose first
+    value is bad in every column: each token's results by what it sees alone."""
+    c, g = shape(608, 32, 16, dv), gen(at + dv)
+    q, kv, k_rope, cu_q, cu_k, pos = ops.batch(c, [(256, 700)], g)
+    pos = [(7 * t) % 256 if t < 128 else 699 - t % 3 for t in range(256)]
+    pos[9] = pos[140] = -1
+    clean = ops.run_prompt(c, q, kv, k_rope, cu_q, cu_k, pos, num_splits=1)
+    kv[0, ::2, 32:] = math.nan
+    kv[at, 1::2, 32 + dv - 3] = math.inf
+    dead = torch.tensor(pos, device="cuda") < 0
+    for _ in range(20):
+        out, lse = ops.run_prompt(c, q, kv, k_rope, cu_q, cu_k, pos, num_splits=1)
+        assert torch.equal(lse, clean[1])
+        assert bool(torch.isnan(out[~dead][:, ::2]).all()) and torch.equal(out[dead], clean[0][dead])
+        assert torch.equal(out[:128, 1::2], clean[0][:128, 1::2])
+        col = torch.arange(dv, device="cuda") != dv - 3
+        assert torch.equal(out[128:, 1::2][..., col], clean[0][128:, 1::2][..., col])
+        assert bool(torch.isnan(out[128:, 1::2, dv - 3][~dead[128:]]).all())
+
+
 @pytest.mark.parametrize("every", [False, True], ids=["two bad values", "bad values in every tile"])
 def test_prompt_bad_values_in_a_context_of_millions_of_rows(every):
     """The work beside a tile's products is bounded for every tile, so that no wait of the call's runs out."""
